@@ -349,6 +349,84 @@ TF_API tf_status tf_ulysses_gather_out(const char *tag, const void *const *attn,
                                        void *stream, tf_targets *out);
 
 /*
+ * Attention over the head groups: the step between the scatter and the gather.
+ * Every group g holds H/P query heads and Hkv/P key and value heads (shared by
+ * H/Hkv query heads each, consecutive ones) of the whole sequence.  For query i
+ * and key j of one batch row and head,
+ *
+ *   x = scale * q_i . k_j
+ *   y = softcap * tanh(x / softcap)                   (y = x where softcap == 0)
+ *   z = y - slopes[h] * |i + Sk - Sq - j|             (h counts heads over all groups)
+ *
+ * Query i stands at position i + Sk - Sq, so the last query sits on the last key.
+ * Key j is visible to query i when both of these hold:
+ *   - causal == 0, or j <= i + Sk - Sq, or j < prefix[b];
+ *   - there are no documents, or q_docs[b][i] == k_docs[b][j] >= 0.
+ * A negative document number marks padding: it sees nothing and is seen by nothing.
+ *
+ *   lse_i = log sum_j e^z       out_i = sum_j e^(z - lse_i) v_j
+ *
+ * over the visible keys; a row without one gets out = 0 and lse = -infinity.
+ * Scores, softmax and sums are fp32; the weights are rounded to the I/O type
+ * for the product with V, and the result once more.
+ */
+typedef struct tf_attention {
+    int P, B;              /* head groups (1..8), batch rows */
+    int Sq, Sk;            /* query and key tokens of each batch row (0 is valid) */
+    int H, Hkv, D;         /* heads over all groups: Hkv % P == 0, H % Hkv == 0; D is 64 or 128 */
+    tf_dtype dtype;        /* TF_BF16 or TF_FP16 */
+    float scale;           /* finite; 1/sqrt(D) as a rule */
+    float softcap;         /* >= 0, finite; 0: scores are not capped */
+    int causal;            /* 0 or 1 */
+    const float *slopes;   /* device [H] (H over all groups), or NULL: no bias.  Finite, read-only */
+    const int32_t *prefix; /* device [B], or NULL; needs causal */
+    const int32_t *q_docs; /* device [B][Sq] and [B][Sk], contiguous; */
+    const int32_t *k_docs; /*   both or neither */
+} tf_attention;
+
+/*
+ * tf_ulysses_attention -- the forward pass.
+ *  q, k, v      host arrays of P device pointers: group g's views [B, Sq, H/P, D]
+ *               and [B, Sk, Hkv/P, D], e.g. the scatter's targets or views into
+ *               its fused payloads.
+ *  strides      host array of 3 tf_strides: q, k, v.
+ *  out          host array of P device pointers, [B, Sq, H/P, D] through
+ *               out_strides (NULL = contiguous); must not overlap the inputs.
+ *  lse          host array of P device pointers to contiguous fp32 [B, H/P, Sq], or NULL.
+ *  workspace    device memory of at least tf_ulysses_attention_workspace(a, 0)
+ *               bytes, 16-byte aligned (NULL where that is 0); its contents need
+ *               not be kept, and calls that may run at the same time (replays of
+ *               graphs among them) need one each.
+ * Nothing is allocated and nothing is kept between calls; the call may be captured.
+ */
+TF_API tf_status tf_ulysses_attention(const tf_attention *a, const void *const *q, const void *const *k,
+                                      const void *const *v, const tf_strides *strides, void *const *out,
+                                      const tf_strides *out_strides, float *const *lse, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/*
+ * tf_ulysses_attention_backward -- the gradients of Q, K and V.
+ *  dout         host array of P device pointers, the gradient of out.
+ *  q, k, v, out, lse   the forward pass's inputs and results (lse is required).
+ *  strides      host array of 5 tf_strides: dout, q, k, v, out.
+ *  dq, dk, dv   host arrays of P device pointers, [B, Sq, H/P, D] and twice
+ *               [B, Sk, Hkv/P, D]; every element is written.  A shared key head's
+ *               gradients are summed over its query heads.
+ *  grad_strides host array of 3 tf_strides: dq, dk, dv (NULL = contiguous).
+ *  workspace    as above, tf_ulysses_attention_workspace(a, 1) bytes.
+ * There is no gradient of the slopes.  The same inputs give the same bits.
+ */
+TF_API tf_status tf_ulysses_attention_backward(const tf_attention *a, const void *const *dout, const void *const *q,
+                                               const void *const *k, const void *const *v, const void *const *out,
+                                               const float *const *lse, const tf_strides *strides, void *const *dq,
+                                               void *const *dk, void *const *dv, const tf_strides *grad_strides,
+                                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the two calls above for `a` (its device pointers are only
+ * tested against NULL); backward != 0: of the second. */
+TF_API tf_status tf_ulysses_attention_workspace(const tf_attention *a, int backward, size_t *bytes);
+
+/*
  * tf_ulysses_rope_table -- the resident fp32 cos/sin table [S][D/2][2] for
  * (theta, S, D) on the current device, built on `stream` on first use and kept
  * (up to 4 tables; least recently used evicted).  *table receives its device

@@ -1,0 +1,81 @@
+"""Refusals of the attention entry points, before any CUDA call (no GPU needed)."""
+import ctypes
+import math
+
+import pytest
+
+FAKE = 0x10000
+
+
+@pytest.fixture(scope="module")
+def tf():
+    from ulysses_sequence_attention_tf_gb300 import binding, build
+    build.build()
+    return binding
+
+
+def describe(tf, **kw):
+    a = dict(P=2, B=1, Sq=8, Sk=8, H=4, Hkv=2, D=64, dtype=1, scale=0.125, softcap=0.0, causal=0, slopes=None, prefix=None,
+             q_docs=None, k_docs=None)
+    a.update(kw)
+    return tf.Attention(*[a[n] for n, _ in tf.Attention._fields_])
+
+
+def forward(tf, a, q=FAKE, k=FAKE, v=FAKE, out=FAKE, strides=None, out_strides=None, lse=None):
+    ptrs = [(ctypes.c_void_p * 8)(*([p] * 8)) if p is not None else None for p in (q, k, v, out)]
+    st = (tf.Strides * 3)(*(strides or [tf.Strides(8 * 2 * 64, 2 * 64, 64)] * 3))
+    return tf.lib().tf_ulysses_attention(ctypes.byref(a), *ptrs[:3], st, ptrs[3],
+                                         ctypes.byref(out_strides) if out_strides else None, lse, None, 0, None)
+
+
+def backward(tf, a, workspace=None, nbytes=0, lse=FAKE, dk=FAKE):
+    arr = (ctypes.c_void_p * 8)(*([FAKE] * 8))
+    st = (tf.Strides * 5)(*([tf.Strides(8 * 2 * 64, 2 * 64, 64)] * 5))
+    return tf.lib().tf_ulysses_attention_backward(
+        ctypes.byref(a), arr, arr, arr, arr, arr, (ctypes.c_void_p * 8)(*([lse] * 8)) if lse else None, st, arr,
+        (ctypes.c_void_p * 8)(*([dk] * 8)) if dk else None, arr, None, workspace, nbytes, None)
+
+
+REFUSED = [
+    (dict(P=0), 1), (dict(P=9), 1), (dict(B=-1), 1), (dict(Sq=-1), 1), (dict(Sk=-1), 1), (dict(H=0), 1), (dict(Hkv=0), 1),
+    (dict(P=4), 2), (dict(H=3), 2), (dict(dtype=2), 4), (dict(dtype=3), 4), (dict(dtype=9), 4), (dict(D=32), 4),
+    (dict(D=96), 4), (dict(D=256), 4), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1), (dict(softcap=-1.0), 1),
+    (dict(softcap=math.nan), 1), (dict(softcap=math.inf), 1), (dict(causal=2), 1), (dict(prefix=FAKE), 1),
+    (dict(q_docs=FAKE), 1), (dict(k_docs=FAKE), 1), (dict(Sq=2 ** 30, Sk=2 ** 30), 4),
+]
+
+
+@pytest.mark.parametrize("kw,status", REFUSED)
+def test_descriptions_refused(tf, kw, status):
+    a = describe(tf, **kw)
+    n = ctypes.c_size_t()
+    assert forward(tf, a) == status and tf.lib().tf_ulysses_last_error()
+    assert backward(tf, a) == status
+    assert tf.lib().tf_ulysses_attention_workspace(ctypes.byref(a), 0, ctypes.byref(n)) == status
+
+
+def test_pointers_and_strides_refused(tf):
+    a = describe(tf)
+    for name in ("q", "k", "v", "out"):
+        assert forward(tf, a, **{name: None}) == 1
+        assert forward(tf, a, **{name: 0}) == 1
+        assert forward(tf, a, **{name: FAKE + 8}) == 3
+    good = tf.Strides(8 * 2 * 64, 2 * 64, 64)
+    assert forward(tf, a, strides=[good, tf.Strides(8 * 2 * 64, 2 * 64 + 4, 64), good]) == 3
+    assert forward(tf, a, strides=[good, good, tf.Strides(8 * 2 * 64, -128, 64)]) == 4
+    assert forward(tf, a, out_strides=tf.Strides(8 * 2 * 64, 0, 64)) == 1
+    assert forward(tf, a, lse=(ctypes.c_void_p * 8)(FAKE, 0)) == 1
+    assert tf.lib().tf_ulysses_attention(None, None, None, None, None, None, None, None, None, 0, None) == 1
+
+
+def test_gradient_needs_its_statistics_and_workspace(tf):
+    a = describe(tf)
+    n = ctypes.c_size_t()
+    assert tf.lib().tf_ulysses_attention_workspace(ctypes.byref(a), 1, ctypes.byref(n)) == 0 and n.value > 0
+    assert tf.lib().tf_ulysses_attention_workspace(ctypes.byref(a), 1, None) == 1
+    assert backward(tf, a, None, n.value) == 1
+    assert backward(tf, a, FAKE, n.value - 1) == 1
+    assert backward(tf, a, FAKE + 4, n.value) == 3
+    assert backward(tf, a, FAKE, n.value, lse=None) == 1
+    assert backward(tf, a, FAKE, n.value, lse=0) == 1
+    assert backward(tf, a, FAKE, n.value, dk=0) == 1

@@ -1,0 +1,239 @@
+"""Attention over the head groups and its gradient against 64 bits (bounds derived in attention_util)."""
+import math
+
+import pytest
+import torch
+
+from attention_util import Reference
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def tf():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from ulysses_sequence_attention_tf_gb300 import binding, build
+    build.build()
+    binding.lib()
+    yield binding
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+
+
+def make(P, B, Sq, Sk, Hl, Hkl, D, dtype, seed, fused=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    if fused:
+        pay = [r(B, Sq, Hl, 3 * D) for _ in range(P)]
+        q, k, v = ([x[..., i * D:(i + 1) * D] for x in pay] for i in range(3))
+    else:
+        q = [r(B, Sq, Hl, D) for _ in range(P)]
+        k = [r(B, Sk, Hkl, D) for _ in range(P)]
+        v = [r(B, Sk, Hkl, D) for _ in range(P)]
+    return q, k, v, [r(B, Sq, Hl, D) for _ in range(P)]
+
+
+def both(tf, q, k, v, dout, **kw):
+    out, lse = tf.attention(q, k, v, **kw)
+    dq, dk, dv = tf.attention_backward(dout, q, k, v, out, lse, **kw)
+    ref = Reference(q, k, v, dout, **kw)
+    for name, got in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        ref.check(name, got)
+    return out, lse, dq, dk, dv
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq,Sk", [(1, 1), (1, 300), (300, 1), (127, 129), (128, 128), (256, 384), (257, 255), (700, 513)])
+def test_sizes(tf, Sq, Sk, D, dtype):
+    both(tf, *make(1, 1, Sq, Sk, 2, 2, D, dtype, Sq + Sk))
+
+
+@pytest.mark.parametrize("P,B,Hl,Hkl", [(1, 1, 1, 1), (2, 3, 4, 1), (4, 1, 6, 2), (8, 2, 1, 1), (3, 2, 5, 5)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_groups_and_shared_heads(tf, P, B, Hl, Hkl, causal):
+    both(tf, *make(P, B, 200, 200, Hl, Hkl, 64, BF16, P + B), causal=causal)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq,Sk", [(1, 1), (130, 130), (300, 300), (100, 400), (400, 100), (513, 770)])
+def test_causal_with_and_without_prefix(tf, Sq, Sk, D):
+    x = make(2, 2, Sq, Sk, 2, 1, D, FP16, 3)
+    both(tf, *x, causal=True)  # Sq > Sk: the first rows see nothing
+    for pre in ([0, 1], [Sk // 2, Sk + 50], [Sk, 129]):
+        both(tf, *x, causal=True, prefix=torch.tensor(pre, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("cap", [0.5, 5.0, 50.0])
+def test_capped_scores(tf, cap, dtype):
+    q, k, v, dout = make(1, 2, 200, 333, 2, 2, 128, dtype, 7)
+    both(tf, [4 * t for t in q], k, v, dout, softcap=cap)
+    both(tf, q, k, v, dout, softcap=cap, scale=0.01)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_distance_bias(tf, cap, causal):
+    x = make(2, 1, 300, 450, 2, 2, 64, BF16, 9)
+    slopes = torch.tensor([0.5, 0.01, 0.0, 2.0], device="cuda")
+    both(tf, *x, slopes=slopes, softcap=cap, causal=causal)
+
+
+DOCS = {
+    "packed": lambda S: [i * 5 // S for i in range(S)],
+    "tail": lambda S: [0] * (S // 3) + [1] * (S // 5) + [-1] * (S - S // 3 - S // 5),
+    "scattered": lambda S: [(i * 7) % 3 - (i % 11 == 0) * 9 for i in range(S)],
+    "all padding": lambda S: [-3] * S,
+    "singles": lambda S: list(range(S)),
+    "large numbers": lambda S: [2 ** 31 - 1 - i // 100 for i in range(S)],
+}
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("S", [1, 257, 640])
+@pytest.mark.parametrize("kind", sorted(DOCS))
+def test_documents(tf, kind, S, causal):
+    x = make(2, 2, S, S, 2, 1, 64, BF16, 11)
+    docs = torch.tensor([DOCS[kind](S), DOCS["packed"](S)], dtype=torch.int32, device="cuda")
+    both(tf, *x, q_docs=docs, k_docs=docs, causal=causal)
+
+
+def test_documents_of_unequal_sides_behind_a_prefix(tf):
+    q, k, v, dout = make(1, 2, 150, 400, 2, 2, 128, FP16, 13)
+    qd = torch.tensor([[i * 3 // 150 for i in range(150)]] * 2, dtype=torch.int32, device="cuda")
+    kd = torch.tensor([[i * 4 // 400 for i in range(400)]] * 2, dtype=torch.int32, device="cuda")
+    both(tf, q, k, v, dout, q_docs=qd, k_docs=kd, causal=True, prefix=torch.tensor([200, 7], dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_padding_may_hold_anything(tf, D):
+    S = 300
+    q, k, v, dout = make(1, 2, S, S, 2, 1, D, BF16, 17)
+    docs = torch.tensor([[0] * 200 + [-1] * 100, [-1] * 33 + [1] * 100 + [-5] * 40 + [2] * 127], dtype=torch.int32, device="cuda")
+    pad = docs < 0
+    for ts in (q, k, v, dout):
+        ts[0][pad] = math.nan
+        ts[0][:, -1] = torch.where(pad[:, -1, None, None], torch.tensor(math.inf, device="cuda", dtype=BF16), ts[0][:, -1])
+    kw = dict(q_docs=docs, k_docs=docs)
+    out, lse = tf.attention(q, k, v, **kw)
+    dq, dk, dv = tf.attention_backward(dout, q, k, v, out, lse, **kw)
+    ref = Reference(q, k, v, dout, clean=True, **kw)
+    for name, got in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        ref.check(name, got)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_views_into_fused_payloads_and_strided_results(tf, D):
+    q, k, v, dout = make(2, 2, 260, 260, 3, 3, D, BF16, 19, fused=True)
+    dout = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in dout]  # heads outside tokens
+    ref = Reference(q, k, v, dout)
+    big = [torch.full((2, 260, 3, 3 * D), 7.0, dtype=BF16, device="cuda") for _ in q]
+    out = [t[..., D:2 * D] for t in big]
+    out, lse = tf.attention(q, k, v, out)
+    ref.check("out", out)
+    grads = [torch.full((2, 260, 3, 3 * D), 7.0, dtype=BF16, device="cuda") for _ in q]
+    dq, dk, dv = tf.attention_backward(dout, q, k, v, out, lse, *([t[..., i * D:(i + 1) * D] for t in grads] for i in range(3)))
+    for name, got in (("dq", dq), ("dk", dk), ("dv", dv)):
+        ref.check(name, got)
+    for t in big:  # nothing beside the view was written
+        assert bool((t[..., :D] == 7).all()) and bool((t[..., 2 * D:] == 7).all())
+
+
+def test_large_scores_and_equal_keys(tf):
+    q, k, v, dout = make(1, 1, 140, 300, 2, 2, 64, BF16, 23)
+    both(tf, [30 * t for t in q], k, v, dout)          # one weight takes nearly all
+    both(tf, q, [torch.ones_like(t) for t in k], v, dout)  # all weights equal
+    both(tf, q, k, v, dout, scale=0.0)
+    both(tf, q, k, v, dout, scale=-0.3)
+
+
+def test_nothing_to_do(tf):
+    empty = lambda *s: [torch.empty(s, dtype=BF16, device="cuda")]  # noqa: E731
+    out, lse = tf.attention(empty(1, 0, 2, 64), empty(1, 5, 2, 64), empty(1, 5, 2, 64))
+    assert out[0].shape == (1, 0, 2, 64) and lse[0].shape == (1, 2, 0)
+    q, _, _, dout = make(1, 2, 5, 5, 2, 2, 64, BF16, 0)
+    out, lse = tf.attention(q, empty(2, 0, 2, 64), empty(2, 0, 2, 64))
+    assert bool((out[0] == 0).all()) and bool((lse[0] == -math.inf).all())
+    dq, dk, dv = tf.attention_backward(dout, q, empty(2, 0, 2, 64), empty(2, 0, 2, 64), out, lse)
+    assert bool((dq[0] == 0).all()) and dk[0].numel() == 0
+    k = [torch.ones((2, 5, 2, 64), dtype=BF16, device="cuda")]
+    none = empty(2, 0, 2, 64)
+    dq, dk, dv = tf.attention_backward(none, none, k, k, none, [torch.empty((2, 2, 0), device="cuda")],
+                                       dk=[torch.ones_like(k[0])], dv=[torch.ones_like(k[0])])
+    assert bool((dk[0] == 0).all()) and bool((dv[0] == 0).all())
+
+
+def test_gradient_against_differences(tf):
+    q, k, v, dout = make(1, 1, 70, 90, 2, 1, 64, FP16, 29)
+    kw = dict(softcap=5.0, causal=True, slopes=torch.tensor([0.1, 0.02], device="cuda"))
+    out, lse = tf.attention(q, k, v, **kw)
+    grads = tf.attention_backward(dout, q, k, v, out, lse, **kw)
+    loss = lambda *x: float((Reference(*x, **kw).out * dout[0].double().transpose(1, 2)).sum())  # noqa: E731
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    for n in range(3):  # the derivative along a random direction, central differences of the 64-bit forward pass
+        step = torch.randn((q, k, v)[n][0].shape, generator=gen, device="cuda").double()
+        moved = lambda e: [[x[0].double() + e * step] if m == n else x for m, x in enumerate((q, k, v))]  # noqa: E731
+        h = 1e-4
+        want = (loss(*moved(h)) - loss(*moved(-h))) / (2 * h)
+        ref = Reference(q, k, v, dout, **kw)
+        tol = float((getattr(ref, ("dq_tol", "dk_tol", "dv_tol")[n]) * step.transpose(1, 2).abs()).sum())
+        got = float((grads[n][0].double() * step).sum())
+        assert abs(got - want) <= tol + 1e-6 * abs(want), (n, got, want, tol)
+
+
+def test_the_same_inputs_give_the_same_bits(tf):
+    x = make(2, 2, 300, 300, 4, 2, 128, BF16, 37)
+    kw = dict(causal=True, softcap=30.0)
+    a, b = both(tf, *x, **kw), both(tf, *x, **kw)
+    for s, t in zip(a, b):
+        assert all(torch.equal(m, n) for m, n in zip(s, t))
+
+
+def test_another_stream(tf):
+    x = make(2, 1, 400, 400, 2, 2, 64, BF16, 41)
+    want = both(tf, *x)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream()):
+        out, lse = tf.attention(*x[:3], stream=stream)
+        got = (out, lse, *tf.attention_backward(x[3], *x[:3], out, lse, stream=stream.cuda_stream))
+        stream.synchronize()
+        assert all(torch.equal(m, n) for s, t in zip(want, got) for m, n in zip(s, t))
+
+
+def test_captured_and_replayed_with_new_inputs(tf):
+    x = make(2, 1, 300, 300, 2, 2, 64, BF16, 43)
+    docs = torch.tensor([DOCS["packed"](300)], dtype=torch.int32, device="cuda")
+    kw = dict(q_docs=docs, k_docs=docs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = tf.attention(*x[:3], **kw)
+        grads = tf.attention_backward(x[3], *x[:3], out, lse, **kw)
+    for seed in (44, 45):
+        for ts, new in zip(x, make(2, 1, 300, 300, 2, 2, 64, BF16, seed)):
+            for t, n in zip(ts, new):
+                t.copy_(n)
+        docs.copy_(torch.tensor([DOCS["tail" if seed == 44 else "scattered"](300)], dtype=torch.int32))
+        graph.replay()
+        ref = Reference(*x, **kw)
+        for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+            ref.check(name, got)
+
+
+def test_between_scatter_and_gather(tf):
+    """The path of one layer: scatter with norm and rotation, attention, gather; each step as its own test checks it."""
+    from ulysses_sequence_attention_tf_gb300 import synth
+    P, B, S, H, D = 4, 1, 512, 8, 64
+    d = synth.move(synth.qkv_shards(P, B, S // P, H, D, BF16, seed=3, layout="fused"), "cuda:0")
+    wq, wk = (w.cuda() for w in synth.norm_weights(D, BF16, seed=3))
+    q, k, v, _ = tf.scatter_qkv("layer", d["q"], d["k"], d["v"], norm_rope=True, q_weight=wq, k_weight=wk, layout="fused")
+    out, lse = tf.attention(q, k, v, softcap=20.0)
+    Reference(q, k, v, softcap=20.0).check("out", out)
+    back, _ = tf.gather_out("layer", out)
+    whole = torch.cat(out, 2)
+    for r in range(P):
+        assert torch.equal(back[r], whole[:, r * (S // P):(r + 1) * (S // P)])
+    tf.cache_clear()

@@ -10,6 +10,7 @@ Names follow the C ABI: ``scatter_qkv`` / ``scatter_qkv_into`` / ``gather_out``
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -56,6 +57,12 @@ class Targets(ctypes.Structure):
                 ("v", ctypes.c_void_p * MAX_SHARDS), ("done", ctypes.c_void_p)]
 
 
+class Attention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("P", "B", "Sq", "Sk", "H", "Hkv", "D", "dtype")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("causal", ctypes.c_int)] + \
+               [(n, ctypes.c_void_p) for n in ("slopes", "prefix", "q_docs", "k_docs")]
+
+
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 FREE_FN = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 
@@ -80,7 +87,12 @@ def _declare(lib):
     lib.tf_ulysses_gather_out.argtypes = [ctypes.c_char_p, PP, ctypes.POINTER(Strides), i32, i32, i32, i32, i32,
                                           i32, PP, ctypes.POINTER(Strides), vp, ctypes.POINTER(Targets)]
     lib.tf_ulysses_rope_table.argtypes = [ctypes.c_float, i32, i32, vp, ctypes.POINTER(ctypes.c_void_p)]
-    for name in ("tf_ulysses_scatter_qkv_heads_into", "tf_ulysses_exchange_chunks", "tf_ulysses_project_qkv_into",
+    AP, SP, size_t = ctypes.POINTER(Attention), ctypes.POINTER(Strides), ctypes.c_size_t
+    lib.tf_ulysses_attention.argtypes = [AP, PP, PP, PP, SP, PP, SP, PP, vp, size_t, vp]
+    lib.tf_ulysses_attention_backward.argtypes = [AP, PP, PP, PP, PP, PP, PP, SP, PP, PP, PP, SP, vp, size_t, vp]
+    lib.tf_ulysses_attention_workspace.argtypes = [AP, i32, ctypes.POINTER(size_t)]
+    for name in ("tf_ulysses_attention", "tf_ulysses_attention_backward", "tf_ulysses_attention_workspace",
+                 "tf_ulysses_scatter_qkv_heads_into", "tf_ulysses_exchange_chunks", "tf_ulysses_project_qkv_into",
                  "tf_ulysses_scatter_qkv", "tf_ulysses_scatter_qkv_into", "tf_ulysses_scatter_qkv_noalloc",
                  "tf_ulysses_gather_out",
                  "tf_ulysses_rope_table", "tf_ulysses_cache_clear"):
@@ -400,6 +412,140 @@ def gather_out(tag, attn, out=None, *, stream=None):
     if out is not None:
         return list(out), res.done
     return [_wrap(res.q[r], (B, Sl, H, D), attn[0].dtype, attn[0].device) for r in range(P)], res.done
+
+
+# ---------------------------------------------------------------- attention
+def _allocating_on(stream):
+    """Context in which torch allocates for ``stream``: memory that the call's kernels
+    use on that stream returns to the allocator in that stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _on_current_device(*tensors):
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (t.device.type != "cuda" or t.device.index != device):
+            raise ValueError(f"every tensor must be on the current device cuda:{device}, not {t.device}")
+
+
+def _plain_array(name, t, dtype, shape):
+    """Data pointer of a contiguous tensor of this type and shape, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _groups(name, ts, shape, dtype):
+    """Strides of P views of this shape and type."""
+    if tuple(ts[0].shape) != tuple(shape) or ts[0].dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} views of shape {tuple(shape)}, not {ts[0].dtype} {tuple(ts[0].shape)}")
+    return _strides_of(ts)
+
+
+def _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs):
+    P = len(q)
+    if not 1 <= P <= MAX_SHARDS or len(k) != P or len(v) != P:
+        raise ValueError(f"q, k and v must be lists of the same P in [1, {MAX_SHARDS}] head groups")
+    if q[0].dim() != 4 or k[0].dim() != 4:
+        raise ValueError("expected 4-d views [B, tokens, heads, D]")
+    B, Sq, Hl, D = q[0].shape
+    Sk, Hkl = k[0].shape[1:3]
+    dtype = q[0].dtype
+    _on_current_device(*q, *k, *v, slopes, prefix, q_docs, k_docs)
+    a = Attention(P, B, Sq, Sk, P * Hl, P * Hkl, D, _dtype_code(dtype), D ** -0.5 if scale is None else float(scale),
+                  float(softcap), 1 if causal else 0, _plain_array("slopes", slopes, torch.float32, (P * Hl,)),
+                  _plain_array("prefix", prefix, torch.int32, (B,)), _plain_array("q_docs", q_docs, torch.int32, (B, Sq)),
+                  _plain_array("k_docs", k_docs, torch.int32, (B, Sk)))
+    strides = (_groups("q", q, q[0].shape, dtype), _groups("k", k, (B, Sk, Hkl, D), dtype),
+               _groups("v", v, (B, Sk, Hkl, D), dtype))
+    return a, strides
+
+
+def _workspace(a, backward):
+    n = ctypes.c_size_t()
+    _check(lib().tf_ulysses_attention_workspace(ctypes.byref(a), backward, ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device="cuda") if n.value else None
+
+
+def _lse_arrays(lse, P, shape):
+    if lse is None:
+        return None
+    if len(lse) != P:
+        raise ValueError(f"lse must be a list of {P} tensors")
+    _on_current_device(*lse)
+    return (ctypes.c_void_p * P)(*[_plain_array("lse", t, torch.float32, shape) for t in lse])
+
+
+def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=None, causal=False, prefix=None,
+              q_docs=None, k_docs=None, stream=None):
+    """Attention over P head groups: ``q`` P views ``[B, Sq, H/P, D]``, ``k`` and ``v`` P views
+    ``[B, Sk, Hkv/P, D]`` (bf16 or fp16, D 64 or 128; H/Hkv query heads share a key head).
+
+    Scores are ``scale * q.k`` (default 1/sqrt(D)), capped to ``softcap * tanh(x / softcap)``
+    where softcap > 0, plus ``-slopes[h] * |i + Sk - Sq - j|`` (``slopes``: fp32 ``[H]``).
+    ``causal``: key j is visible up to position i + Sk - Sq, and below ``prefix[b]`` (int32
+    ``[B]``) always.  ``q_docs`` / ``k_docs`` (int32 ``[B, Sq]``, ``[B, Sk]``): only equal
+    document numbers see one another; negative ones are padding.  Returns ``(out, lse)``:
+    P tensors ``[B, Sq, H/P, D]`` and fp32 ``[B, H/P, Sq]``, 0 and -inf for rows that see
+    nothing; both are made here unless given.
+    """
+    a, strides = _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs)
+    shape, rows = q[0].shape, (a.B, a.H // a.P, a.Sq)
+    with _allocating_on(stream):
+        if out is None:
+            out = [torch.empty(shape, dtype=q[0].dtype, device=q[0].device) for _ in q]
+        if lse is None:
+            lse = [torch.empty(rows, dtype=torch.float32, device=q[0].device) for _ in q]
+        if len(out) != a.P:
+            raise ValueError(f"out must be a list of {a.P} tensors")
+        _on_current_device(*out)
+        o_str = _groups("out", out, shape, q[0].dtype)
+        ws = _workspace(a, 0)
+        _check(lib().tf_ulysses_attention(
+            ctypes.byref(a), _ptr_array(q), _ptr_array(k), _ptr_array(v), (Strides * 3)(*strides), _ptr_array(out),
+            ctypes.byref(o_str), _lse_arrays(lse, a.P, rows), ws.data_ptr() if ws is not None else None,
+            ws.numel() if ws is not None else 0, _stream_handle(stream)))
+    return out, lse
+
+
+def attention_backward(dout, q, k, v, out, lse, dq=None, dk=None, dv=None, *, scale=None, softcap=0.0, slopes=None,
+                       causal=False, prefix=None, q_docs=None, k_docs=None, stream=None):
+    """Gradients ``(dq, dk, dv)`` of ``attention`` for the gradient ``dout`` of its output, from
+    the same inputs and options and its results ``out`` and ``lse``: lists of P tensors
+    shaped like q, k and v, made here unless given.  Shared key heads get the sum over
+    their query heads.  The same inputs give the same bits."""
+    a, (q_str, k_str, v_str) = _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs)
+    dtype, P = q[0].dtype, a.P
+    if len(dout) != P or len(out) != P or lse is None:
+        raise ValueError(f"dout, out and lse must be lists of {P} tensors")
+    _on_current_device(*dout, *out)
+    strides = (Strides * 5)(_groups("dout", dout, q[0].shape, dtype), q_str, k_str, v_str,
+                            _groups("out", out, q[0].shape, dtype))
+    with _allocating_on(stream):
+        made = []
+        for grads, like in ((dq, q), (dk, k), (dv, v)):
+            if grads is None:
+                grads = [torch.empty(like[0].shape, dtype=dtype, device=like[0].device) for _ in like]
+            if len(grads) != P:
+                raise ValueError(f"dq, dk and dv must be lists of {P} tensors")
+            _on_current_device(*grads)
+            made.append(grads)
+        dq, dk, dv = made
+        g_strides = (Strides * 3)(_groups("dq", dq, q[0].shape, dtype), _groups("dk", dk, k[0].shape, dtype),
+                                  _groups("dv", dv, v[0].shape, dtype))
+        ws = _workspace(a, 1)
+        _check(lib().tf_ulysses_attention_backward(
+            ctypes.byref(a), _ptr_array(dout), _ptr_array(q), _ptr_array(k), _ptr_array(v), _ptr_array(out),
+            _lse_arrays(lse, P, (a.B, a.H // P, a.Sq)), strides, _ptr_array(dq), _ptr_array(dk), _ptr_array(dv),
+            g_strides, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+            _stream_handle(stream)))
+    return dq, dk, dv
 
 
 def rope_table(theta, S, D, *, stream=None, device=None):

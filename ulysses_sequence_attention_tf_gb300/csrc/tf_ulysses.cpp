@@ -20,36 +20,21 @@
 #include <vector>
 
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include "gemm.h"
+#include "host.h"
 #include "noalloc.h"
 #include "relayout.h"
 #include "tf_ulysses.h"
 #include "tma_plan.h"
 
+namespace tfu {
+namespace host {
+
 namespace {
-
-// A named NVTX range around each C-ABI call, so that a profiler's timeline shows
-// which library call issued which launches (header-only NVTX; a few nanoseconds
-// when no profiler is attached).
-struct CallRange {
-    explicit CallRange(const char* name) { nvtxRangePushA(name); }
-    ~CallRange() { nvtxRangePop(); }
-    CallRange(const CallRange&) = delete;
-    CallRange& operator=(const CallRange&) = delete;
-};
-
-using tfu::RelayoutParams;
-
 thread_local std::string g_last_error;
 std::atomic<uint64_t> g_launches{0};
-std::atomic<uint64_t> g_allocs{0};  // device allocations made (cache entries, tables)
-std::mutex g_mu;  // guards the cache, the tables and the allocator
-// The relayout launchers fill per-kernel launch facts (occupancy, the shared-memory
-// opt-in) into function-local statics on first use; calls that launch without
-// g_mu serialise on this one, which is never held while taking g_mu.
-std::mutex g_launch_mu;
+}  // namespace
 
 tf_status fail(tf_status s, const char* fmt, ...) {
     char buf[512];
@@ -65,13 +50,6 @@ tf_status cuda_fail(cudaError_t e, const char* what) {
     return fail(TF_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-// ---------------------------------------------------------------- stream capture
-// CUDA-graph capture protocol (flashinfer PR #6332 commit message, "Description",
-// "CUDA graphs": a prepared call allocates nothing; a size first seen inside a
-// capture fails rather than allocate; captured calls interleave with eager
-// ones).  Inside a capture the library allocates and frees nothing, records its
-// events as external event nodes (so every replay records them) and waits on
-// events recorded outside the capture as external waits.
 tf_status capture_state(cudaStream_t s, bool* capturing) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(s, &st);
@@ -80,6 +58,72 @@ tf_status capture_state(cudaStream_t s, bool* capturing) {
     return TF_OK;
 }
 
+tf_status current_device(int* dev) {
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    return TF_OK;
+}
+
+int elem_size(tf_dtype d) {
+    switch (d) {
+        case TF_FP16: return 2;
+        case TF_BF16: return 2;
+        case TF_FP32: return 4;
+        case TF_BYTE: return 1;
+    }
+    return 0;
+}
+
+tf_status check_ptrs(const char* what, const void* const* a, int P) {
+    for (int i = 0; i < P; ++i) {
+        if (!a[i]) return fail(TF_ERR_INVALID, "%s[%d] is NULL", what, i);
+        if (!aligned16(a[i])) return fail(TF_ERR_ALIGNMENT, "%s[%d] is not 16-byte aligned", what, i);
+    }
+    return TF_OK;
+}
+
+tf_status check_strides(const char* what, const tf_strides& s, int esize, int64_t nb, int64_t nt, int64_t nh) {
+    const int64_t v[3] = {s.b, s.t, s.h};
+    const int64_t n[3] = {nb, nt, nh};
+    const char* name[3] = {"b", "t", "h"};
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        if (v[i] < 0) return fail(TF_ERR_UNSUPPORTED, "%s stride %s=%lld is negative", what, name[i], (long long)v[i]);
+        if ((v[i] * esize) % 16 != 0)
+            return fail(TF_ERR_ALIGNMENT, "%s stride %s=%lld elements is not a multiple of 16 bytes", what, name[i],
+                        (long long)v[i]);
+    }
+    return TF_OK;
+}
+
+void count_launches(int n) { g_launches.fetch_add(uint64_t(n)); }
+
+uint64_t launch_count() { return g_launches.load(); }
+
+const char* last_error() { return g_last_error.c_str(); }
+
+}  // namespace host
+}  // namespace tfu
+
+namespace {
+
+using namespace tfu::host;
+using tfu::RelayoutParams;
+
+std::atomic<uint64_t> g_allocs{0};  // device allocations made (cache entries, tables)
+std::mutex g_mu;  // guards the cache, the tables and the allocator
+// The relayout launchers fill per-kernel launch facts (occupancy, the shared-memory
+// opt-in) into function-local statics on first use; calls that launch without
+// g_mu serialise on this one, which is never held while taking g_mu.
+std::mutex g_launch_mu;
+
+// ---------------------------------------------------------------- stream capture
+// CUDA-graph capture protocol (flashinfer PR #6332 commit message, "Description",
+// "CUDA graphs": a prepared call allocates nothing; a size first seen inside a
+// capture fails rather than allocate; captured calls interleave with eager
+// ones).  Inside a capture the library allocates and frees nothing, records its
+// events as external event nodes (so every replay records them) and waits on
+// events recorded outside the capture as external waits.
 cudaError_t record_event(cudaEvent_t ev, cudaStream_t s, bool capturing) {
     return capturing ? cudaEventRecordWithFlags(ev, s, cudaEventRecordExternal) : cudaEventRecord(ev, s);
 }
@@ -121,18 +165,6 @@ void dev_release(const Allocator& a, void* ptr, size_t bytes, cudaEvent_t last_u
 }
 
 // ---------------------------------------------------------------- validation
-int elem_size(tf_dtype d) {
-    switch (d) {
-        case TF_FP16: return 2;
-        case TF_BF16: return 2;
-        case TF_FP32: return 4;
-        case TF_BYTE: return 1;
-    }
-    return 0;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 struct Shape {
     int P, B, Sl, H, D, Hl, esize;
     tf_dtype dtype;
@@ -153,28 +185,7 @@ tf_status check_shape(int P, int B, int Sl, int H, int D, tf_dtype dtype, Shape*
     return TF_OK;
 }
 
-tf_status check_ptrs(const char* what, const void* const* a, int P) {
-    for (int i = 0; i < P; ++i) {
-        if (!a[i]) return fail(TF_ERR_INVALID, "%s[%d] is NULL", what, i);
-        if (!aligned16(a[i])) return fail(TF_ERR_ALIGNMENT, "%s[%d] is not 16-byte aligned", what, i);
-    }
-    return TF_OK;
-}
 
-// strides of a [nb, nt, nh, D] view; a stride of an extent-1 dimension is never used
-tf_status check_strides(const char* what, const tf_strides& s, int esize, int64_t nb, int64_t nt, int64_t nh) {
-    const int64_t v[3] = {s.b, s.t, s.h};
-    const int64_t n[3] = {nb, nt, nh};
-    const char* name[3] = {"b", "t", "h"};
-    for (int i = 0; i < 3; ++i) {
-        if (n[i] <= 1) continue;
-        if (v[i] < 0) return fail(TF_ERR_UNSUPPORTED, "%s stride %s=%lld is negative", what, name[i], (long long)v[i]);
-        if ((v[i] * esize) % 16 != 0)
-            return fail(TF_ERR_ALIGNMENT, "%s stride %s=%lld elements is not a multiple of 16 bytes", what, name[i],
-                        (long long)v[i]);
-    }
-    return TF_OK;
-}
 
 // 32-byte vectors when every address the kernel forms is 32-byte aligned
 // (bases, strides of dimensions longer than 1, weights, the head row), else 16.
@@ -344,7 +355,7 @@ tf_status launch_planned(RelayoutParams& p, const Shape& sh, tfu::Dir dir, tfu::
         e = tfu::launch_relayout(p, dir, stream);
     }
     if (e != cudaSuccess) return cuda_fail(e, "launching the relayout kernel");
-    g_launches.fetch_add(1);
+    count_launches(1);
     return TF_OK;
 }
 
@@ -405,7 +416,7 @@ tf_status get_table(float theta, int S, int D, int device, cudaStream_t stream, 
     std::vector<double> inv_freq(size_t(D / 2));
     for (int i = 0; i < D / 2; ++i) inv_freq[size_t(i)] = std::pow(double(theta), -2.0 * i / D);
     e = tfu::launch_rope_table(t.ptr, inv_freq.data(), S, D, stream);
-    if (e == cudaSuccess && S > 0) g_launches.fetch_add(1);
+    if (e == cudaSuccess && S > 0) count_launches(1);
     if (e == cudaSuccess) e = cudaEventRecord(t.last_use, stream);
     if (e != cudaSuccess) {
         dev_release(t.alloc, t.ptr, t.bytes, nullptr, stream);
@@ -654,11 +665,6 @@ tf_status launch_scatter(ScatterPlan& pl, const tf_norm_rope* nr, int device, cu
     return TF_OK;
 }
 
-tf_status current_device(int* dev) {
-    cudaError_t e = cudaGetDevice(dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    return TF_OK;
-}
 
 tf_status check_tag(const char* tag, std::string* out) {
     if (!tag) tag = "";
@@ -669,6 +675,21 @@ tf_status check_tag(const char* tag, std::string* out) {
 }
 
 }  // namespace
+
+tf_status tfu::host::with_rope_table(float theta, int S, int D, cudaStream_t stream,
+                                     const std::function<cudaError_t(const float*)>& launch) {
+    int device = 0;
+    tf_status s = current_device(&device);
+    if (s != TF_OK) return s;
+    bool cap = false;
+    if ((s = capture_state(stream, &cap)) != TF_OK) return s;
+    std::lock_guard<std::mutex> lock(g_mu);
+    Table* t = nullptr;
+    if ((s = get_table(theta, S, D, device, stream, cap, &t)) != TF_OK) return s;
+    cudaError_t e = launch(t->ptr);
+    if (e == cudaSuccess) e = record_event(t->last_use, stream, cap);
+    return e == cudaSuccess ? TF_OK : cuda_fail(e, "launching a kernel that reads the RoPE table");
+}
 
 extern "C" {
 
@@ -783,7 +804,7 @@ TF_API tf_status tf_ulysses_scatter_qkv_noalloc(const void* const* q, const void
         bool built = false;
         cudaError_t e = tfu::noalloc_table(nr->theta, P * S_local, D, st, cap, &table, &built);
         if (e != cudaSuccess) return cuda_fail(e, "preparing the cos/sin table in the fixed scratch");
-        if (built) g_launches.fetch_add(1);
+        if (built) count_launches(1);
         pl.p.table = table;
     }
     return launch_planned(pl.p, pl.sh, tfu::Dir::kScatter, pl.fused, pl.sh.Sl, int64_t(P) * S_local, st);
@@ -991,7 +1012,7 @@ TF_API tf_status tf_ulysses_project_qkv_into(const void* const* x, int64_t x_row
     }
     cudaError_t e = tfu::launch_qkv_gemm(p, fused, neox, st);
     if (e != cudaSuccess) return cuda_fail(e, "launching the projection kernel");
-    g_launches.fetch_add(1);
+    count_launches(1);
     if (used) record_event(used->last_use, st, cap);
     return TF_OK;
 }
@@ -1147,13 +1168,13 @@ TF_API tf_status tf_ulysses_selftest_wait(unsigned long long cycles, void* strea
         return fail(TF_ERR_INVALID, "cycles=%llu outside [1, 1e9]", (unsigned long long)cycles);
     cudaError_t e = tfu::launch_wait_selftest((long long)cycles, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "launching the bounded-wait self-test");
-    g_launches.fetch_add(1);
+    count_launches(1);
     return TF_OK;
 }
 
-TF_API const char* tf_ulysses_last_error(void) { return g_last_error.c_str(); }
+TF_API const char* tf_ulysses_last_error(void) { return tfu::host::last_error(); }
 
-TF_API uint64_t tf_ulysses_launch_count(void) { return g_launches.load(); }
+TF_API uint64_t tf_ulysses_launch_count(void) { return tfu::host::launch_count(); }
 
 TF_API int tf_ulysses_abi_version(void) { return TF_ULYSSES_ABI_VERSION; }
 
