@@ -427,6 +427,104 @@ TF_API tf_status tf_ulysses_attention_backward(const tf_attention *a, const void
 TF_API tf_status tf_ulysses_attention_workspace(const tf_attention *a, int backward, size_t *bytes);
 
 /*
+ * A paged key-value cache of N sequences: what streaming and token-by-token
+ * generation keep of earlier chunks.  A page holds page_size consecutive tokens
+ * of one sequence for every key head, as e4m3 codes with one fp32 scale for each
+ * page and head: K = k code * k_scale, V = v code * v_scale.  Token j of sequence
+ * n is slot j % page_size of page page_table[n][j / page_size].  Heads count over
+ * all P groups (group g holds heads [g*Hkv/P, (g+1)*Hkv/P)).
+ *
+ * A call handles the newest tokens of each sequence: rows [starts[n], starts[n+1])
+ * of its row tensors are the last starts[n+1] - starts[n] tokens of sequence n,
+ * whose length with them is lens[n]; rows in front of starts[0] and behind
+ * starts[N] belong to no sequence and are neither read nor written.  Table, lengths
+ * and starts are read on the device, so a captured call follows their contents.  A
+ * sequence whose length is out of range (starts[n+1] - starts[n] <= lens[n] <=
+ * max_pages * page_size) is left out, a page number outside [0, num_pages) leaves out
+ * that page's tokens, and both set bit 3 of tf_ulysses_device_status.  So do starts
+ * that do not ascend within [0, T]; any sequence of such a call may be left out.
+ */
+typedef struct tf_kv_cache {
+    void *k, *v;                /* device, e4m3 [num_pages][Hkv][page_size][D] contiguous, 16-byte aligned */
+    float *k_scale, *v_scale;   /* device, [num_pages][Hkv] */
+    int num_pages, Hkv;
+    int page_size, D;           /* 16, 32, 64 or 128 tokens; 64 or 128 */
+    int N, max_pages;           /* sequences, entries of a table row in use */
+    const int32_t *page_table;  /* device, [N][max_pages], rows table_stride entries apart */
+    int64_t table_stride;       /* >= max_pages */
+    const int32_t *lens;        /* device, [N] */
+    const int32_t *starts;      /* device, [N + 1] */
+} tf_kv_cache;
+
+typedef enum tf_rope {
+    TF_ROPE_NONE = 0,
+    TF_ROPE_INTERLEAVED = 1, /* pairs (2i, 2i + 1) */
+    TF_ROPE_HALF_SPLIT = 2   /* pairs (i, i + D/2) */
+} tf_rope;
+
+/*
+ * tf_ulysses_kv_append -- write the new rows of K and V into the cache, and
+ * normalise and rotate the queries of the same tokens, in one launch.
+ *  c            the cache; its codes and scales are written.
+ *  P, T, H      head groups (1..8), rows, query heads over all groups (H % P == 0;
+ *               ignored without q).
+ *  dtype        TF_BF16 or TF_FP16: type of k, v, q and q_out.
+ *  k, v, q      host arrays of P device pointers to row views [T, heads/P, D]; q may
+ *               be NULL.  strides: host array of 3 tf_strides for k, v, q (t and h used).
+ *  q_out        host array of P device pointers [T, H/P, D] through q_out_strides
+ *               (NULL = contiguous); NULL without q.  May be q itself.
+ *  nr           q_weight, k_weight: RMSNorm weights, or NULL where that tensor is not
+ *               normalised; eps; cos_sin: fp32 [table_rows][D/2][2], or NULL for the
+ *               resident table of theta and max_pages * page_size rows.  nr may be NULL
+ *               where rope is TF_ROPE_NONE and nothing is normalised.
+ *  rope         rotation of K and Q by the token's position in its sequence.  A sequence
+ *               longer than a given table is out of range.
+ * Arithmetic: fp32 throughout -- x * (1 / sqrt(mean(x^2) + eps)) * w, then the rotation
+ * -- with one rounding at the end, to e4m3 or to the queries' type (the scatter, which
+ * reproduces the 16-bit steps of a separate norm, rounds between them).
+ * Scales: a page's scale is the smallest power of two s (at least 2^-100) with
+ * |x| <= 448 s for its new values, or the page's scale so far if that is larger and
+ * the page already holds tokens of the sequence; when the scale grows, the older codes
+ * are rounded again to the new one.  Infinities are stored as the largest code and
+ * NaN as NaN; neither moves the scale.  Two sequences may share a page only if
+ * neither gets new rows in it.
+ */
+TF_API tf_status tf_ulysses_kv_append(const tf_kv_cache *c, int P, int T, int H, tf_dtype dtype,
+                                      const void *const *k, const void *const *v, const void *const *q,
+                                      const tf_strides *strides, void *const *q_out,
+                                      const tf_strides *q_out_strides, const tf_norm_rope *nr, tf_rope rope,
+                                      int table_rows, void *stream);
+
+/* The call of tf_ulysses_kv_attend: everything but the tensors. */
+typedef struct tf_kv_attention {
+    int P, T, H;          /* head groups, rows, query heads over all groups (H % Hkv == 0, Hkv % P == 0) */
+    tf_dtype dtype;       /* TF_BF16 or TF_FP16 */
+    int max_tokens;       /* bound of the tokens of one sequence in this call, 1..T */
+    int max_len;          /* bound of lens[n], 1..max_pages * page_size */
+    float scale, softcap; /* as tf_attention */
+    int causal;           /* 1: a token sees keys up to its own; 0: all lens[n] keys */
+    const float *slopes;  /* device [H], or NULL */
+} tf_kv_attention;
+
+/*
+ * tf_ulysses_kv_attend -- attention of the newest tokens of each sequence over
+ * its cached keys and values (their own among them, appended before).  Scores,
+ * bias and softmax are those of tf_attention with the token's position in its
+ * sequence; a sequence of length 0 or without new tokens has nothing to write.
+ * A sequence above max_tokens or max_len is out of range.
+ *  q            host array of P device pointers to row views [T, H/P, D], q_strides (t, h).
+ *  out          the same through out_strides (NULL = contiguous).
+ *  lse          host array of P device pointers to fp32 [H/P, T], or NULL.
+ *  workspace    device memory of tf_ulysses_kv_attend_workspace bytes, 16-byte aligned,
+ *               one for each call that may run at the same time.
+ */
+TF_API tf_status tf_ulysses_kv_attend(const tf_kv_cache *c, const tf_kv_attention *a, const void *const *q,
+                                      const tf_strides *q_strides, void *const *out, const tf_strides *out_strides,
+                                      float *const *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+TF_API tf_status tf_ulysses_kv_attend_workspace(const tf_kv_cache *c, const tf_kv_attention *a, size_t *bytes);
+
+/*
  * tf_ulysses_rope_table -- the resident fp32 cos/sin table [S][D/2][2] for
  * (theta, S, D) on the current device, built on `stream` on first use and kept
  * (up to 4 tables; least recently used evicted).  *table receives its device
@@ -459,7 +557,9 @@ TF_API void tf_ulysses_set_allocator(tf_alloc_fn alloc, tf_free_fn release, void
  * (bulk-copy) kernel gave up, bit 1 when one of the projection kernel did --
  * that kernel then stopped early and its outputs are incomplete.  Bit 2 exists
  * in checked builds of the library (compiled with TFU_CHECKED=1) only: a block
- * kernel access fell outside the buffer the plan allows and was skipped.
+ * kernel access fell outside the buffer the plan allows and was skipped.  Bit 3:
+ * a key-value cache call left out a sequence or a page whose length, starts or
+ * page number (device data) were out of range.
  * Synchronises with the device.  clear != 0 resets the words after reading them.
  */
 TF_API tf_status tf_ulysses_device_status(int clear, unsigned *status);

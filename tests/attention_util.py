@@ -65,10 +65,12 @@ class Reference:
         score = 2.0 ** -19 * size + 2.0 ** -21 * (softcap + far)
         self.score = torch.where(self.see, score, 0.0)
         worst = self.score.amax(-1) if Sk else torch.zeros_like(self.lse)
-        # the sum's own error: fp32 terms and sums, the exponential to 2 units: 2^-20
-        self.lse_tol = worst + 2.0 ** -20 + 2.0 ** -23 * base.abs()
+        # the row's sum: n fp32 terms in any order are off by at most (n - 1) 2^-24 of the sum of their sizes, each
+        # term by the exponential's 2 units and its argument's rounding: 32 * 2^-24
+        sums = (max(Sq, Sk) + 64) * 2.0 ** -24
+        self.lse_tol = worst + sums + 2.0 ** -23 * base.abs()
         # a weight: rounded to the I/O type once; its score's and its row sum's errors
-        dw = w * (u + 2 * worst[..., None] + 2.0 ** -18) + tiny
+        dw = w * (u + 2 * worst[..., None] + sums) + tiny
         self.out_tol = u * self.out.abs() + dw @ vv.abs() + tiny
         if dout is None:
             return
@@ -83,7 +85,7 @@ class Reference:
         self.dq, self.dk, self.dv = self.scale * dx @ kk, join(self.scale * dx.transpose(-1, -2) @ q), join(w.transpose(-1, -2) @ g)
         # dP - delta: the product's error as a score's; delta from the rounded output; bend: 2^-20 absolute
         inner = 2.0 ** -19 * (g.abs() @ vv.abs().transpose(-1, -2)) + (g.abs() * (self.out_tol + 2.0 ** -19 * self.out.abs())).sum(-1, keepdim=True)
-        ddx = dx.abs() * (u + 2 * worst[..., None] + 2.0 ** -18) + w * inner * bend + w * (dp - delta).abs() * 2.0 ** -20 + tiny * (1 + (dp - delta).abs())
+        ddx = dx.abs() * (u + 2 * worst[..., None] + 2 * sums + 2.0 ** -18) + w * inner * bend + w * (dp - delta).abs() * 2.0 ** -20 + tiny * (1 + (dp - delta).abs())
         ddx = torch.where(self.see, ddx, 0.0)
         dw = torch.where(self.see, dw, 0.0)
         s = abs(self.scale)

@@ -14,6 +14,7 @@ import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -63,6 +64,26 @@ class Attention(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("slopes", "prefix", "q_docs", "k_docs")]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(n, ctypes.c_int) for n in ("num_pages", "Hkv", "page_size", "D", "N", "max_pages")] + \
+               [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p)]
+
+
+class KvAttention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("P", "T", "H", "dtype", "max_tokens", "max_len")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("causal", ctypes.c_int), ("slopes", ctypes.c_void_p)]
+
+
+class PagedCache(NamedTuple):
+    """A paged key-value cache: e4m3 codes ``[pages, Hkv, page_size, D]`` and their fp32 scales ``[pages, Hkv]``."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 FREE_FN = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 
@@ -91,7 +112,13 @@ def _declare(lib):
     lib.tf_ulysses_attention.argtypes = [AP, PP, PP, PP, SP, PP, SP, PP, vp, size_t, vp]
     lib.tf_ulysses_attention_backward.argtypes = [AP, PP, PP, PP, PP, PP, PP, SP, PP, PP, PP, SP, vp, size_t, vp]
     lib.tf_ulysses_attention_workspace.argtypes = [AP, i32, ctypes.POINTER(size_t)]
-    for name in ("tf_ulysses_attention", "tf_ulysses_attention_backward", "tf_ulysses_attention_workspace",
+    CP, KP = ctypes.POINTER(KvCache), ctypes.POINTER(KvAttention)
+    lib.tf_ulysses_kv_append.argtypes = [CP, i32, i32, i32, i32, PP, PP, PP, SP, PP, SP, ctypes.POINTER(NormRope), i32,
+                                         i32, vp]
+    lib.tf_ulysses_kv_attend.argtypes = [CP, KP, PP, SP, PP, SP, PP, vp, size_t, vp]
+    lib.tf_ulysses_kv_attend_workspace.argtypes = [CP, KP, ctypes.POINTER(size_t)]
+    for name in ("tf_ulysses_kv_append", "tf_ulysses_kv_attend", "tf_ulysses_kv_attend_workspace",
+                 "tf_ulysses_attention", "tf_ulysses_attention_backward", "tf_ulysses_attention_workspace",
                  "tf_ulysses_scatter_qkv_heads_into", "tf_ulysses_exchange_chunks", "tf_ulysses_project_qkv_into",
                  "tf_ulysses_scatter_qkv", "tf_ulysses_scatter_qkv_into", "tf_ulysses_scatter_qkv_noalloc",
                  "tf_ulysses_gather_out",
@@ -546,6 +573,122 @@ def attention_backward(dout, q, k, v, out, lse, dq=None, dk=None, dv=None, *, sc
             g_strides, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
             _stream_handle(stream)))
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- key-value cache
+_ROPE = {None: 0, "interleaved": 1, "neox": 2}
+
+
+def kv_cache(num_pages, Hkv, page_size, D, *, device="cuda"):
+    """A paged cache of ``num_pages`` pages of ``page_size`` (16, 32, 64 or 128) tokens for ``Hkv`` key heads
+    (over all head groups) of D 64 or 128.  Pages need no clearing: the first append to a page sets it up."""
+    codes = lambda: torch.zeros((num_pages, Hkv, page_size, D), dtype=torch.float8_e4m3fn, device=device)  # noqa: E731
+    scales = lambda: torch.ones((num_pages, Hkv), dtype=torch.float32, device=device)  # noqa: E731
+    return PagedCache(codes(), codes(), scales(), scales())
+
+
+def _kv_cache(cache, page_table, lens, starts):
+    k, v, k_scale, v_scale = cache
+    if k.dim() != 4:
+        raise ValueError("the cache's codes must be [pages, Hkv, page_size, D]")
+    pages, Hkv, page, D = k.shape
+    _on_current_device(k, v, k_scale, v_scale, page_table, lens, starts)
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be int32 [N, max_pages] with unit stride along a row")
+    N, most = page_table.shape
+    return KvCache(_plain_array("k", k, torch.float8_e4m3fn, (pages, Hkv, page, D)),
+                   _plain_array("v", v, torch.float8_e4m3fn, (pages, Hkv, page, D)),
+                   _plain_array("k_scale", k_scale, torch.float32, (pages, Hkv)),
+                   _plain_array("v_scale", v_scale, torch.float32, (pages, Hkv)), pages, Hkv, page, D, N, most,
+                   page_table.data_ptr(), page_table.stride(0) if N > 1 else most,
+                   _plain_array("lens", lens, torch.int32, (N,)), _plain_array("starts", starts, torch.int32, (N + 1,)))
+
+
+def _rows(name, ts, P, shape, dtype):
+    """Strides of P row views [T, heads, D]."""
+    if len(ts) != P:
+        raise ValueError(f"{name} must be a list of {P} head groups")
+    s = ts[0].stride()
+    for t in ts:
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.stride() != s:
+            raise ValueError(f"{name} must be {dtype} views of shape {tuple(shape)} with the same strides")
+    if shape[2] > 1 and s[2] != 1:
+        raise ValueError("the D dimension must have stride 1")
+    _on_current_device(*ts)
+    return Strides(0, s[0], s[1])
+
+
+def kv_append(cache, page_table, lens, starts, k, v, q=None, q_out=None, *, q_weight=None, k_weight=None, eps=1e-6,
+              theta=10000.0, cos_sin=None, rope="interleaved", stream=None):
+    """Append new rows to a paged cache (``kv_cache``): ``k`` and ``v`` are P row views ``[T, Hkv/P, D]`` whose rows
+    ``[starts[n], starts[n + 1])`` are the newest tokens of sequence n, of length ``lens[n]`` with them, in the pages
+    of row n of ``page_table`` (int32 ``[N, max_pages]``; ``lens`` int32 ``[N]``, ``starts`` int32 ``[N + 1]``).
+
+    K is normalised (``k_weight`` given) and rotated at its token's position (``rope`` "interleaved", "neox" or None;
+    the table ``cos_sin`` fp32 ``[rows, D/2, 2]`` or the resident one of theta) before it is stored; the queries
+    ``q`` ``[T, H/P, D]`` of the same tokens likewise into ``q_out`` (made here unless given; ``q`` itself is fine).
+    Returns ``q_out``, or None without q.
+    """
+    c = _kv_cache(cache, page_table, lens, starts)
+    P, T, dtype = len(k), k[0].shape[0], k[0].dtype
+    if not 1 <= P <= MAX_SHARDS or c.Hkv % P:
+        raise ValueError(f"k must be a list of P in [1, {MAX_SHARDS}] head groups, P dividing Hkv={c.Hkv}")
+    if rope not in _ROPE:
+        raise ValueError(f"rope must be 'interleaved', 'neox' or None, not {rope!r}")
+    strides = (Strides * 3)(_rows("k", k, P, (T, c.Hkv // P, c.D), dtype), _rows("v", v, P, (T, c.Hkv // P, c.D), dtype))
+    weights = [_plain_array(n, w, dtype, (c.D,)) for n, w in (("q_weight", q_weight), ("k_weight", k_weight))]
+    _on_current_device(q_weight, k_weight, cos_sin)
+    rows = 0
+    if cos_sin is not None:
+        rows = cos_sin.shape[0]
+        _plain_array("cos_sin", cos_sin, torch.float32, (rows, c.D // 2, 2))
+    nr = NormRope(*weights, float(eps), float(theta), cos_sin.data_ptr() if cos_sin is not None else None)
+    H, o_str = 0, None
+    with _allocating_on(stream):
+        if q is not None:
+            H = P * q[0].shape[1]
+            strides[2] = _rows("q", q, P, (T, H // P, c.D), dtype)
+            if q_out is None:
+                q_out = [torch.empty((T, H // P, c.D), dtype=dtype, device=t.device) for t in q]
+            o_str = _rows("q_out", q_out, P, (T, H // P, c.D), dtype)
+        _check(lib().tf_ulysses_kv_append(
+            ctypes.byref(c), P, T, H, _dtype_code(dtype), _ptr_array(k), _ptr_array(v), _ptr_array(q), strides,
+            _ptr_array(q_out), ctypes.byref(o_str) if o_str is not None else None, ctypes.byref(nr), _ROPE[rope], rows,
+            _stream_handle(stream)))
+    return q_out
+
+
+def kv_attend(cache, page_table, lens, starts, q, out=None, lse=None, *, max_tokens=None, max_len=None, scale=None,
+              softcap=0.0, slopes=None, causal=True, stream=None):
+    """Attention of each sequence's newest tokens over its cached keys and values (their own appended before):
+    ``q`` P row views ``[T, H/P, D]``, rows as in ``kv_append``.  Score options are those of ``attention``, positions
+    those in the sequence; ``causal=False`` lets a token see all ``lens[n]`` keys.  ``max_tokens`` and ``max_len`` bound
+    the new tokens and the length of one sequence (default: T and the table's width); tight ones spare work.
+    Returns ``(out, lse)``: P tensors ``[T, H/P, D]`` and fp32 ``[H/P, T]``, made here unless given (rows of no sequence
+    are then undefined; given tensors keep them).
+    """
+    c = _kv_cache(cache, page_table, lens, starts)
+    P, (T, Hl, D), dtype = len(q), q[0].shape, q[0].dtype
+    if not 1 <= P <= MAX_SHARDS or D != c.D:
+        raise ValueError(f"q must be a list of P in [1, {MAX_SHARDS}] views [T, heads, {c.D}]")
+    _on_current_device(slopes)
+    a = KvAttention(P, T, P * Hl, _dtype_code(dtype), T if max_tokens is None else int(max_tokens),
+                    c.max_pages * c.page_size if max_len is None else int(max_len), D ** -0.5 if scale is None else float(scale),
+                    float(softcap), 1 if causal else 0, _plain_array("slopes", slopes, torch.float32, (P * Hl,)))
+    q_str = _rows("q", q, P, (T, Hl, D), dtype)
+    with _allocating_on(stream):
+        if out is None:
+            out = [torch.empty((T, Hl, D), dtype=dtype, device=t.device) for t in q]
+        if lse is None:
+            lse = [torch.empty((Hl, T), dtype=torch.float32, device=t.device) for t in q]
+        o_str = _rows("out", out, P, (T, Hl, D), dtype)
+        n = ctypes.c_size_t()
+        _check(lib().tf_ulysses_kv_attend_workspace(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)))
+        ws = torch.empty(n.value, dtype=torch.uint8, device="cuda") if n.value else None
+        _check(lib().tf_ulysses_kv_attend(
+            ctypes.byref(c), ctypes.byref(a), _ptr_array(q), ctypes.byref(q_str), _ptr_array(out), ctypes.byref(o_str),
+            _lse_arrays(lse, P, (Hl, T)), ws.data_ptr() if ws is not None else None, n.value, _stream_handle(stream)))
+    return out, lse
 
 
 def rope_table(theta, S, D, *, stream=None, device=None):
