@@ -559,7 +559,8 @@ TF_API void tf_ulysses_set_allocator(tf_alloc_fn alloc, tf_free_fn release, void
  * in checked builds of the library (compiled with TFU_CHECKED=1) only: a block
  * kernel access fell outside the buffer the plan allows and was skipped.  Bit 3:
  * a key-value cache call left out a sequence or a page whose length, starts or
- * page number (device data) were out of range.
+ * page number (device data) were out of range.  Bit 4: a bounded wait of an
+ * attention kernel gave up; its outputs are incomplete.
  * Synchronises with the device.  clear != 0 resets the words after reading them.
  */
 TF_API tf_status tf_ulysses_device_status(int clear, unsigned *status);

@@ -5,11 +5,15 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "relayout.h"
 
 namespace tfu {
+
+constexpr uint32_t kAttnRows = 128;   // rows of a tile: TMEM lanes
+constexpr uint32_t kAttnPair = 256;   // query rows of a forward CTA: two tiles
 
 // A [B, tokens, heads, D] view of every head group: base addresses and byte strides.
 struct GroupView {
@@ -22,6 +26,7 @@ struct AttentionParams {
     GroupView dout, dq, dk, dv;  // backward only
     float* lse[kMaxShards];      // [B][Hl][Sq] per group, or null
     float* delta;                // backward: workspace [P][B][Hl][Sq], sum_d dO * O of each row
+    uint32_t* plan;              // with documents: the visible tiles (TilePlan)
     const float* slopes;         // [P * Hl] or null
     const int32_t* prefix;       // [B] or null
     const int32_t* q_docs;       // [B][Sq] or null
@@ -33,8 +38,39 @@ struct AttentionParams {
     uint32_t causal;
 };
 
-cudaError_t launch_attention(const AttentionParams& p, bool bf16, cudaStream_t stream);
+// Tensor maps of the head groups' views: 4-D (D, heads, tokens, B), boxes of 64
+// elements x 128 tokens of one head with the 128-byte swizzle.
+struct GroupMaps {
+    CUtensorMap m[kMaxShards];
+};
+
+struct ForwardParams {
+    GroupMaps q, k, v;
+    AttentionParams a;
+    uint32_t q_tiles;  // of kAttnPair rows
+};
+
+// With documents, a kernel in front of the attention writes for every row tile
+// of a batch row one bit per tile of the other side, twice: [0] some pair may be
+// visible, [1] every pair is.
+struct TilePlan {
+    uint32_t row_tiles, words;  // words of one bit set
+    __host__ __device__ size_t bytes(uint32_t B) const { return size_t(B) * row_tiles * words * 2 * sizeof(uint32_t); }
+};
+inline TilePlan tile_plan(uint32_t rows, uint32_t rows_per_tile, uint32_t cols) {
+    const uint32_t col_tiles = (cols + kAttnRows - 1) / kAttnRows;
+    return {(rows + rows_per_tile - 1) / rows_per_tile, (col_tiles + 31) / 32};
+}
+
+// Encode the maps of P groups ([B, tokens, heads, D] 16-bit views); false if the driver refuses.
+bool encode_group_maps(GroupMaps* maps, const GroupView& v, uint32_t P, uint32_t B, uint32_t tokens, uint32_t heads,
+                       uint32_t D, bool bf16);
+
 // *launches: kernels launched
+cudaError_t launch_attention(const ForwardParams& p, bool bf16, cudaStream_t stream, int* launches);
 cudaError_t launch_attention_backward(const AttentionParams& p, bool bf16, cudaStream_t stream, int* launches);
+
+// Status word of the attention kernels: 0, or 1 when a bounded wait gave up.
+cudaError_t read_attention_status(unsigned* out, bool clear);
 
 }  // namespace tfu

@@ -1,107 +1,435 @@
-// attention_forward.cu -- attention over the head groups, forward.
+// attention_forward.cu -- attention over the head groups, forward, on the
+// 5th-generation tensor cores.
 //
-// One pass over the keys with the running maximum m and sum l of each row's
+// One pass over the keys with the running reference m and sum l of each row's
 // softmax (Milakov & Gimelshein, "Online normalizer calculation for softmax",
-// 2018): for each block of keys, m' = max(m, max z), l = l e^(m - m') + sum e^(z - m'),
-// o = o e^(m - m') + sum e^(z - m') v.  Everything in fp32; the output is rounded once.
+// 2018), z in units of log2: o = sum 2^(z - m) v, l = sum 2^(z - m).  m follows the
+// row's maximum only when that outgrows it by more than 2^8: what is scaled by
+// 2^(m_old - m) then is rare, the weights stay below 2^8 and all sums are fp32.
+//
+// A CTA of 384 threads takes two tiles of 128 queries of one head and walks the
+// tiles of 128 keys that some query can see:
+//  * warp 8, one lane: TMA producer.  Q once, then K and V tiles through a ring of
+//    stages in the order K0 V0 K1 V1 ...
+//  * warp 9, one lane: issues S_t = Q_t K^T (both operands from shared memory) and
+//    O_t += P_t V (P_t from TMEM, V read MN-major) for t = 0, 1.  The matrix pipe
+//    completes in order, so S_t of the next keys may overwrite P_t behind the
+//    product that reads it, and a finished S_t says that O_t stands still.
+//  * warps 0-3 and 4-7: one thread a query row of tile 0 or 1.  Reads the row's 128
+//    scores from TMEM, masks, takes maximum, weights and sum, writes the 16-bit
+//    weights back over the scores, and at the end divides and stores the row.
+// While one tile's softmax runs, the matrix pipe works on the other tile.
+// Registers move from the last warpgroup (two idle warps among it) to the rows' threads.
+// TMEM: S0 S1 (128 columns each, P on top of S), O0 O1 (D columns each).
 #include "attention_common.cuh"
+#include "attention_plan.h"
 
 namespace tfu {
+
+__device__ unsigned g_attention_status;
 
 namespace {
 
 using namespace dev;
 
-constexpr int kRowThreads = 128;
-constexpr int kKeys = 32;  // keys of a block
+constexpr int kThreadsA = 384;
+constexpr uint32_t kHalfTile = kAttnRows * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
+constexpr float kSlack = 8.0f;                           // growth of the maximum that m lets pass, in powers of two
 
-// kLanes = D / 32 lanes share a query row, 32 dims each.
-template <Fused kF, int kD>
-__global__ void __launch_bounds__(kRowThreads) attention_kernel(const __grid_constant__ AttentionParams p) {
-    constexpr int kLanes = kD / 32, kRows = kRowThreads / kLanes;
-    __shared__ float ks[kKeys][kD], vs[kKeys][kD];
-    __shared__ int32_t kdoc[kKeys];
-    const uint32_t part = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
-    const uint32_t h = blockIdx.y % p.Hl, b = blockIdx.y / p.Hl % p.B, g = blockIdx.y / p.Hl / p.B;
-    const uint32_t kh = h / p.shared;
-    const int64_t i = int64_t(blockIdx.x) * kRows + row;
-    const bool valid = i < int64_t(p.Sq);
-    float q[32], o[32];
-    const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.q.base[g] + b * p.q.b + (valid ? i : 0) * p.q.t + h * p.q.h);
+// Scores beyond scale * q.k: none, the cap, or cap (if any) and bias and any scale.
+enum class Score { kPlain, kCap, kAny };
+
+template <int kD>
+struct Shape {
+    static constexpr uint32_t kTile = kHalfTile * (kD / 64);
+    static constexpr int kStages = kD == 128 ? 5 : 8;
+    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kTile + 512 + 1024;  // tiles, barriers, alignment
+};
+
+// z of one row's 128 scores, times log2 e, in place (kCap, kAny).
+template <Score kScore>
+__device__ __forceinline__ void finish_scores(float (&s)[128], float scale, float cap, float slope, float far) {
+    if (kScore == Score::kCap || cap != 0.f) {
+        const float to_x = scale / cap, to_z = cap * kLog2e;
+        float most = 0.f;
 #pragma unroll
-    for (int d = 0; d < 32; ++d) {
-        q[d] = valid ? to_float<kF>(qp[part * 32 + d]) : 0.f;
-        o[d] = 0.f;
+        for (int i = 0; i < 128; i += 2) most = fmaxf(fmaxf(fabsf(s[i]), fabsf(s[i + 1])), most);
+        if (__all_sync(0xffffffffu, most * fabsf(to_x) <= kTanhNear)) {
+            const uint64_t x2 = f2_pack(to_x, to_x), z2 = f2_pack(to_z, to_z);
+#pragma unroll
+            for (int i = 0; i < 128; i += 2) {
+                const uint64_t x = f2_mul(f2_pack(s[i], s[i + 1]), x2);
+                f2_unpack(f2_mul(f2_mul(x, z2), tanh_over_x(f2_mul(x, x))), s[i], s[i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) s[i] = to_z * tanh_wide(s[i] * to_x);
+        }
+    } else {
+        const float c = scale * kLog2e;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i] *= c;
     }
-    const int bound = valid ? key_bound(p, b, i) : 0;
-    const int32_t doc = valid && p.q_docs ? p.q_docs[int64_t(b) * p.Sq + i] : -1;
-    const float slope = p.slopes ? p.slopes[g * p.Hl + h] : 0.f;
-    const int64_t pos = i + int64_t(p.Sk) - int64_t(p.Sq);
-    float m = -INFINITY, l = 0.f;
-    const uint8_t* kb = p.k.base[g] + b * p.k.b + kh * p.k.h;
-    const uint8_t* vb = p.v.base[g] + b * p.v.b + kh * p.v.h;
-    for (int j0 = 0; j0 < int(p.Sk); j0 += kKeys) {
-        if (!__syncthreads_or(j0 < bound)) break;
-        for (int x = threadIdx.x; x < kKeys * kD; x += kRowThreads) {
-            const int j = x / kD, d = x % kD;
-            const bool in = j0 + j < int(p.Sk);
-            ks[j][d] = in ? to_float<kF>(reinterpret_cast<const uint16_t*>(kb + int64_t(j0 + j) * p.k.t)[d]) : 0.f;
-            vs[j][d] = in ? to_float<kF>(reinterpret_cast<const uint16_t*>(vb + int64_t(j0 + j) * p.v.t)[d]) : 0.f;
-        }
-        if (p.k_docs && threadIdx.x < kKeys)
-            kdoc[threadIdx.x] = j0 + int(threadIdx.x) < int(p.Sk) ? p.k_docs[int64_t(b) * p.Sk + j0 + threadIdx.x] : -1;
-        __syncthreads();
-        float z[kKeys], top = m;
+    if (kScore == Score::kAny) {
+        const float m = slope * kLog2e;
 #pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-            float s = 0.f;
-#pragma unroll
-            for (int d = 0; d < 32; ++d) s = fmaf(q[d], ks[j][part * 32 + d], s);
-#pragma unroll
-            for (int w = 1; w < kLanes; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-            s *= p.scale;
-            if (p.cap != 0.f) s = p.cap * tanhf(s / p.cap);
-            s -= slope * fabsf(float(pos - (j0 + j)));
-            const bool see = j0 + j < bound && (!p.k_docs || (doc >= 0 && kdoc[j] == doc));
-            z[j] = see ? s : -INFINITY;
-            top = fmaxf(top, z[j]);
-        }
-        const float base = top == -INFINITY ? 0.f : top;
-        const float shrink = expf(m - base);
-        l *= shrink;
-#pragma unroll
-        for (int d = 0; d < 32; ++d) o[d] *= shrink;
-#pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-            if (z[j] == -INFINITY) continue;
-            const float e = expf(z[j] - base);
-            l += e;
-#pragma unroll
-            for (int d = 0; d < 32; ++d) o[d] = fmaf(e, vs[j][part * 32 + d], o[d]);
-        }
-        m = top;
-        __syncthreads();
+        for (int i = 0; i < 128; ++i) s[i] = fmaf(-m, fabsf(far - float(i)), s[i]);
     }
-    if (!valid) return;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    uint16_t* op = reinterpret_cast<uint16_t*>(p.out.base[g] + b * p.out.b + i * p.out.t + h * p.out.h);
+}
+
+template <Fused kF, int kD, Score kScore>
+__global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_constant__ ForwardParams fp) {
+    using S = Shape<kD>;
+    constexpr uint32_t kTile = S::kTile;
+    constexpr int kStages = S::kStages;
+    const AttentionParams& p = fp.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kStages) * size_t(kTile));
+    const uint32_t q_smem = smem_u32(smem), ring = q_smem + 2 * kTile;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
+    const uint32_t s_full0 = q_full + 8, p_full0 = s_full0 + 16, o_full = p_full0 + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 6);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    uint32_t u = blockIdx.x;
+    uint32_t qt = u % fp.q_tiles;
+    u /= fp.q_tiles;
+    if (p.causal) qt = fp.q_tiles - 1 - qt;  // the rows that see most first
+    const uint32_t h = u % p.Hl, b = u / p.Hl % p.B, g = u / p.Hl / p.B;
+    const int row0 = int(qt * kAttnPair);
+    const int tiles = row0 + int(kAttnRows) < int(p.Sq) ? 2 : 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(q_full, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full0 + 8 * t, 1);
+            mbar_init(p_full0 + 8 * t, kAttnRows);
+        }
+        mbar_init(o_full, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dependency_wait();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t o_tmem = tmem + 2 * kAttnRows;
+
+    // the keys in reach of the last row, in tiles; with documents the plan picks among them
+    const int last = min(row0 + int(kAttnPair), int(p.Sq)) - 1;
+    const int n_tiles = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
+    const uint32_t words = (((p.Sk + kAttnRows - 1) / kAttnRows) + 31) / 32;
+    const uint32_t* plan = p.plan ? p.plan + (size_t(b) * fp.q_tiles + qt) * 2 * words : nullptr;
+    TileIter it(plan, n_tiles);
+
+    // 384 * 168 registers at launch = 256 * 216 + 128 * 72
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8 && lane == 0) {
+        // ---------------- TMA producer
+        const CUtensorMap* maps[2] = {&fp.k.m[g], &fp.v.m[g]};
+        const int kh = int(h / p.shared);
+        uint32_t n = 0;  // tiles loaded into the ring
+        bool ok = true;
+        int j = it.next();
+        if (j >= 0) {
+            mbar_expect_tx(q_full, uint32_t(tiles) * kTile);
+            for (int t = 0; t < tiles; ++t)
+                for (int x = 0; x < kD / 64; ++x)
+                    tma_load_4d(q_smem + t * kTile + x * kHalfTile, &fp.q.m[g], x * 64, int(h), row0 + t * int(kAttnRows),
+                                int(b), q_full);
+        }
+        for (; ok && j >= 0; j = it.next()) {
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+                const uint32_t s = n % kStages, use = n / kStages;
+                if (use > 0 && !bounded_wait(empty0 + 8 * s, (use - 1) & 1u, abort_flag, &g_attention_status)) {
+                    ok = false;
+                    break;
+                }
+                mbar_expect_tx(full0 + 8 * s, kTile);
+                for (int x = 0; x < kD / 64; ++x)
+                    tma_load_4d(ring + s * kTile + x * kHalfTile, maps[kv], x * 64, kh, j * int(kAttnRows), int(b),
+                                full0 + 8 * s);
+            }
+        }
+        // every load has landed before the CTA exits
+        if (n > 0) drain_phase(q_full, 0);
+        for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
+            drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
+    } else if (warp == 9 && lane == 0) {
+        // ---------------- MMA issuer
+        constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
+        constexpr uint32_t kIdescO = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
+        auto scores = [&](int t, uint32_t k_smem) {
 #pragma unroll
-    for (int d = 0; d < 32; ++d) op[part * 32 + d] = to_half<kF>(o[d] * inv);
-    if (p.lse[g] && part == 0) p.lse[g][(int64_t(b) * p.Hl + h) * p.Sq + i] = m + logf(l);
+            for (uint32_t kk = 0; kk < kD / 16; ++kk) {
+                const uint32_t off = kk / 4 * kHalfTile + kk % 4 * 32;
+                tc_mma(tmem + t * kAttnRows, sw128_desc(q_smem + t * kTile + off), sw128_desc(k_smem + off), kIdescS, kk != 0);
+            }
+            tc_commit(s_full0 + 8 * t);
+        };
+        uint32_t n = 0;  // ring tiles consumed
+        int i = 0;       // key tiles finished
+        auto landed = [&](uint32_t k) {
+            return bounded_wait(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag, &g_attention_status);
+        };
+        auto stage = [&](uint32_t k) { return ring + (k % kStages) * kTile; };
+        int j = it.next();
+        bool ok = j < 0 || (bounded_wait(q_full, 0, abort_flag, &g_attention_status) && landed(0));
+        if (ok && j >= 0) {
+            tc_fence_after();
+            for (int t = 0; t < tiles; ++t) scores(t, stage(0));
+            tc_commit(empty0);
+            n = 1;
+        }
+        for (; ok && j >= 0; ++i) {
+            j = it.next();
+            const uint32_t v = n, k = n + 1;
+            n += j >= 0 ? 2 : 1;
+            if (!(ok = landed(v))) break;
+            for (int t = 0; t < tiles; ++t) {
+                if (!(ok = bounded_wait(p_full0 + 8 * t, i & 1u, abort_flag, &g_attention_status))) break;
+                tc_fence_after();
+#pragma unroll
+                for (uint32_t kk = 0; kk < kAttnRows / 16; ++kk)
+                    tc_mma_ts(o_tmem + t * kD, tmem + t * kAttnRows + kk * 8, sw128_desc(stage(v) + kk * 2048, kHalfTile),
+                              kIdescO, (uint32_t(i) | kk) != 0);
+                if (j >= 0) {
+                    if (t == 0 && !(ok = landed(k))) break;
+                    tc_fence_after();
+                    scores(t, stage(k));
+                }
+            }
+            if (!ok) break;
+            tc_commit(empty0 + 8 * (v % kStages));
+            if (j >= 0) tc_commit(empty0 + 8 * (k % kStages));
+        }
+        tc_commit(o_full);
+        drain_phase(o_full, 0);  // every MMA of this CTA has completed
+    }
+    } else {
+        // ---------------- softmax and epilogue: a thread per query row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const uint32_t t = warp / 4, quarter = warp % 4;
+        const int i = row0 + int(t * kAttnRows + quarter * 32 + lane);
+        const bool valid = i < int(p.Sq);
+        const uint32_t lane_base = (quarter * 32u) << 16;
+        const uint32_t s_tmem = tmem + t * kAttnRows + lane_base, o_row = o_tmem + t * kD + lane_base;
+        int bound = valid ? key_bound(p, b, i) : 0;
+        int32_t doc = -1;
+        if (p.plan) {
+            doc = valid ? p.q_docs[int64_t(b) * p.Sq + i] : -1;
+            if (doc < 0) bound = 0;
+        }
+        const float slope = kScore == Score::kAny && p.slopes ? p.slopes[g * p.Hl + h] : 0.f;
+        const float c = kScore == Score::kPlain ? p.scale * kLog2e : 1.0f;
+        float m = -INFINITY, l = 0.f;
+        int n = 0;  // key tiles done
+        bool ok = true;
+        for (int j = int(t) < tiles ? it.next() : -1; j >= 0; j = it.next(), ++n) {
+            ok = bounded_wait(s_full0 + 8 * t, n & 1u, abort_flag, &g_attention_status);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float s[128];
+            {
+                uint32_t r[4][32];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tc_ld32(s_tmem + x * 32, r[x]);
+                tc_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    tc_landed(r[x]);
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) s[x * 32 + y] = __uint_as_float(r[x][y]);
+                }
+            }
+            const int j0 = j * int(kAttnRows);
+            if (kScore != Score::kPlain)
+                finish_scores<kScore>(s, p.scale, p.cap, slope, float(i + (int(p.Sk) - int(p.Sq)) - j0));
+            const bool whole = plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + int(kAttnRows) <= bound;
+            if (!__all_sync(0xffffffffu, whole)) {
+                if (plan) {
+                    // the tile's documents, four keys a lane; a warp of tile 0 also clears the
+                    // V rows of padding, whose contents may be anything
+                    int32_t kd[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int key = j0 + x * 32 + int(lane);
+                        kd[x] = key < int(p.Sk) ? __ldg(p.k_docs + int64_t(b) * p.Sk + key) : -1;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 128; ++x)
+                        s[x] = __shfl_sync(0xffffffffu, kd[x / 32], x % 32) == doc && j0 + x < bound ? s[x] : -INFINITY;
+                    if (t == 0) {
+                        const uint32_t vn = 2 * uint32_t(n) + 1;
+                        ok = bounded_wait(full0 + 8 * (vn % kStages), (vn / kStages) & 1u, abort_flag, &g_attention_status);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        int32_t own = kd[0];
+#pragma unroll
+                        for (int x = 1; x < 4; ++x) own = quarter == uint32_t(x) ? kd[x] : own;
+                        if (own < 0) {
+                            uint4* v = reinterpret_cast<uint4*>(smem + (2 + vn % kStages) * size_t(kTile) +
+                                                                (quarter * 32 + lane) * kSwizzleRow);
+                            for (int x = 0; x < kD / 64; ++x)
+                                for (int y = 0; y < 8; ++y) v[x * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_shared();
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 128; ++x) s[x] = j0 + x < bound ? s[x] : -INFINITY;
+                }
+            }
+            float top[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                top[x] = fmaxf(s[x], s[x + 4]);
+#pragma unroll
+                for (int y = x + 8; y < 128; y += 8) top[x] = fmaxf(top[x], fmaxf(s[y], s[y + 4]));
+            }
+            const float most = c * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            const bool grow = most > m + kSlack;  // from -inf: on any visible key
+            if (__any_sync(0xffffffffu, grow)) {
+                const float to = grow ? most : m;
+                const float shrink = grow ? ex2(m - to) : 1.0f;
+                l *= shrink;
+                m = to;
+                if (n > 0) {
+#pragma unroll 1
+                    for (int x = 0; x < kD; x += 32) {
+                        uint32_t r[32];
+                        tc_ld32(o_row + x, r);
+                        tc_wait_ld();
+                        tc_landed(r);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * shrink);
+                        tc_st32(o_row + x, r);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t w[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    const int e = x * 32 + 2 * y;
+                    float lo, hi;
+                    f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, b2), lo, hi);
+                    lo = ex2(lo);
+                    hi = ex2(hi);
+                    sum[y & 1] = f2_add(sum[y & 1], f2_pack(lo, hi));
+                    w[y] = pack2<kF>(lo, hi);
+                }
+                tc_st16(s_tmem + x * 16, w);
+            }
+            float a0, a1;
+            f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
+            l += a0 + a1;
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full0 + 8 * t);
+        }
+        if (int(t) < tiles && ok) {
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            uint8_t* dst = p.out.base[g] + int64_t(b) * p.out.b + int64_t(valid ? i : 0) * p.out.t + int64_t(h) * p.out.h;
+            if (n > 0) ok = bounded_wait(o_full, 0, abort_flag, &g_attention_status);
+            if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < kD; x += 32) {
+                    uint32_t r[32];
+                    if (n > 0) {
+                        tc_ld32(o_row + x, r);
+                        tc_wait_ld();
+                        tc_landed(r);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) r[y] = 0;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8) {
+                        uint4 w;
+                        uint32_t* o = &w.x;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            o[z] = l == 0.f ? 0u
+                                            : pack2<kF>(__uint_as_float(r[y + 2 * z]) * inv, __uint_as_float(r[y + 2 * z + 1]) * inv);
+                        if (valid) *reinterpret_cast<uint4*>(dst + (x + y) * 2) = w;
+                    }
+                }
+                if (valid && p.lse[g])
+                    p.lse[g][(int64_t(b) * p.Hl + h) * p.Sq + i] = (m == -INFINITY ? 0.f : m * kLn2) + logf(l);
+            }
+        }
+    }
+    // teardown: every MMA has completed (warp 9 drained o_full) and every TMEM access
+    // has finished before the columns are freed
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <Fused kF, int kD, Score kScore>
+cudaError_t launch(const ForwardParams& p, cudaStream_t stream) {
+    const size_t smem = Shape<kD>::kSmem;
+    auto kernel = attention_kernel<kF, kD, kScore>;
+    // setting it twice is harmless; the cost is a fraction of a microsecond
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kernel, p.q_tiles * p.a.P * p.a.B * p.a.Hl, kThreadsA, smem, stream, p);
 }
 
 template <Fused kF, int kD>
-cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
-    constexpr uint32_t kRows = kRowThreads / (kD / 32);
-    attention_kernel<kF, kD><<<dim3((p.Sq + kRows - 1) / kRows, p.B * p.P * p.Hl), kRowThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_scored(const ForwardParams& p, cudaStream_t stream) {
+    if (p.a.slopes || !(p.a.scale > 0.f)) return launch<kF, kD, Score::kAny>(p, stream);
+    return p.a.cap != 0.f ? launch<kF, kD, Score::kCap>(p, stream) : launch<kF, kD, Score::kPlain>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attention(const AttentionParams& p, bool bf16, cudaStream_t stream) {
-    if (p.D == 64) return bf16 ? launch<Fused::kBF16, 64>(p, stream) : launch<Fused::kFP16, 64>(p, stream);
-    return bf16 ? launch<Fused::kBF16, 128>(p, stream) : launch<Fused::kFP16, 128>(p, stream);
+cudaError_t launch_attention(const ForwardParams& p, bool bf16, cudaStream_t stream, int* launches) {
+    *launches = 0;
+    if (p.a.plan) {
+        const cudaError_t e = launch_plan(p.a, p.a.plan, false, kAttnPair, stream);
+        if (e != cudaSuccess) return e;
+        *launches = 1;
+    }
+    const cudaError_t e = p.a.D == 64 ? (bf16 ? launch_scored<Fused::kBF16, 64>(p, stream) : launch_scored<Fused::kFP16, 64>(p, stream))
+                                      : (bf16 ? launch_scored<Fused::kBF16, 128>(p, stream) : launch_scored<Fused::kFP16, 128>(p, stream));
+    if (e == cudaSuccess) *launches += 1;
+    return e;
+}
+
+cudaError_t read_attention_status(unsigned* out, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_attention_status, sizeof(unsigned));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attention_status, &zero, sizeof(unsigned));
 }
 
 }  // namespace tfu

@@ -40,8 +40,10 @@
 
 #include <cudaTypedefs.h>
 
+#include "attention.h"
 #include "device_common.cuh"
 #include "gemm.h"
+#include "tcgen05.cuh"
 
 namespace tfu {
 
@@ -59,151 +61,15 @@ constexpr uint32_t kStageBytesG = kABytes + kBBytes;
 constexpr int kThreadsG = 192;
 constexpr uint32_t kTmemCols = 256;
 constexpr size_t kSmemG = size_t(kStagesG) * kStageBytesG + 256 + 1024;  // stages, barriers, alignment slack
-constexpr long long kWaitCyclesG = 4000000000LL;                           // ~2 s at 2 GHz
-constexpr unsigned kStatusWait = 1u;
 
-// Instruction descriptor of tcgen05.mma kind::f16: D fp32 (bits 4-5 = 1), A and
-// B bf16 (bits 7-9, 10-12 = 1), both K-major (bits 15, 16 = 0), N >> 3 at bits
-// 17-22, M >> 4 at bits 24-28.
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kGemmBN >> 3) << 17) |
-                            (uint32_t(kGemmBM >> 4) << 24);
+constexpr uint32_t kIdesc = f16_idesc(true, kGemmBM, kGemmBN, false);
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// ---------------------------------------------------------------- mbarriers
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-// kCS: acquire at cluster scope (arrivals and copies of the other CTA of a pair).
-template <bool kCS = false>
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    if constexpr (kCS) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    } else {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    }
-    return ok != 0;
-}
-__device__ __forceinline__ void fence_barrier_init() {
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-
-// Wait for the phase of `bar` with parity `parity`; false if the abort flag is
-// raised or the budget runs out (then records the status and raises the flag,
-// and also the flag at shared::cluster address `peer_flag` of the other CTA of a
-// pair when it is not 0).
+// Wait for a phase of `bar` (bounded_wait with this kernel's status word).
 template <bool kCS = false>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           long long budget = kWaitCyclesG, uint32_t peer_flag = 0) {
-    if (mbar_try_wait<kCS>(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait<kCS>(bar, parity)) return true;
-        if ((i & 63u) == 0) {
-            if (*abort_flag) return false;
-            if (clock64() - t0 > budget) {
-                atomicOr(&g_gemm_status, kStatusWait);
-                *abort_flag = 1;
-                if (peer_flag) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_flag), "r"(1u) : "memory");
-                return false;
-            }
-        }
-    }
+                                           long long budget = kWaitCycles, uint32_t peer_flag = 0) {
+    return bounded_wait<kCS>(bar, parity, abort_flag, &g_gemm_status, budget, peer_flag);
 }
-
-// The same without the abort flag (draining after an abort): bounded only.
-template <bool kCS = false>
-__device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity) {
-    const long long t0 = clock64();
-    while (!mbar_try_wait<kCS>(bar, parity)) {
-        if (clock64() - t0 > kWaitCyclesG) return;
-    }
-}
-
-// ---------------------------------------------------------------- TMA
-__device__ __forceinline__ void tma_load_2d(uint32_t smem_dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-// ---------------------------------------------------------------- tcgen05
-__device__ __forceinline__ void tmem_alloc(uint32_t smem_result, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_result), "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// D[tmem] (+)= A[smem] * B[smem]^T, one M=128 x N=256 x K=16 step.
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(kIdesc), "r"(accumulate)
-        : "memory");
-}
-
-// Arrive once on `bar` when every tcgen05 operation this thread issued so far completed.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-// Shared-memory matrix descriptor of a K-major operand tile whose rows are
-// 128 bytes with the 128-byte swizzle, 8-row groups 1024 bytes apart: start
-// address >> 4 (bits 0-13), leading byte offset (unused by this layout, 1) at
-// bits 16-29, stride byte offset at bits 32-45, descriptor version 1 at bits
-// 46-47, base offset 0 (tiles are aligned to the swizzle pattern), swizzle mode
-// 2 (128-byte) at bits 61-63.  A K step of 16 elements advances the start by 32
-// bytes.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t smem_addr) {
-    constexpr uint64_t kMode = 2;
-    return uint64_t((smem_addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t((8 * kRowBytesG) >> 4) << 32) |
-           (uint64_t(1) << 46) | (kMode << 61);
-}
-
-// 32 consecutive fp32 accumulator columns of this thread's TMEM lane (warp-collective:
-// the warp is reconverged first).
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    __syncwarp();
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- epilogue
 // 16 packed bf16 pairs of 32 accumulator columns: the projection's output rounding.
@@ -357,10 +223,6 @@ __device__ __forceinline__ Tile decode_tile(const GemmParams& p, uint32_t t, uin
     return gemm_tile<kCluster>(p.P, p.m_tiles, p.n_tiles, p.n_group, t, rank);
 }
 
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -454,7 +316,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) qkv_gemm_kernel(const __grid_con
                 const uint32_t sa = smem_u32(smem + size_t(s) * kStageBytesG);
 #pragma unroll
                 for (uint32_t kk = 0; kk < kGemmBK / 16; ++kk)
-                    tc_mma(d, sw128_desc(sa + kk * 32), sw128_desc(sa + kABytes + kk * 32), (kb | kk) != 0);
+                    tc_mma(d, sw128_desc(sa + kk * 32), sw128_desc(sa + kABytes + kk * 32), kIdesc,
+                           (kb | kk) != 0);
                 tc_commit(empty0 + 8 * s);  // the stage is free once these MMAs have read it
             }
             tc_commit(acc_full0 + 8 * a);  // the tile's accumulator is complete (or abandoned)
@@ -528,9 +391,8 @@ constexpr uint32_t kBHalfBytes = kBBytes / 2;
 constexpr uint32_t kStageBytesP = kABytes + kBHalfBytes;
 constexpr size_t kSmemP = size_t(kStagesP) * kStageBytesP + 256 + 1024;
 static_assert(kSmemP <= 232448, "the pair stage ring exceeds 227 KiB of shared memory");
-// M = 256 (two CTAs of 128 rows), N = 256, otherwise as kIdesc.
-constexpr uint32_t kIdescPair = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kGemmBN >> 3) << 17) |
-                                (uint32_t((2 * kGemmBM) >> 4) << 24);
+// M = 256 (two CTAs of 128 rows), N = 256
+constexpr uint32_t kIdescPair = f16_idesc(true, 2 * kGemmBM, kGemmBN, false);
 
 // shared::cluster address of the object at this CTA's shared address `local` in CTA `rank`.
 __device__ __forceinline__ uint32_t map_rank(uint32_t local, uint32_t rank) {
@@ -650,7 +512,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) qkv_gemm_pair_kernel(const __gri
             const CUtensorMap* mx = &p.tmap_x[tl.r];
             for (uint32_t kb = 0; kb < KB; ++kb, ++q) {
                 const uint32_t s = q % kStagesP, use = q / kStagesP;
-                if (use > 0 && !wait_phase<true>(empty0 + 8 * s, (use - 1) & 1u, abort_flag, kWaitCyclesG, peer_flag)) {
+                if (use > 0 && !wait_phase<true>(empty0 + 8 * s, (use - 1) & 1u, abort_flag, kWaitCycles, peer_flag)) {
                     ok = false;
                     break;
                 }
@@ -676,13 +538,13 @@ __global__ void __launch_bounds__(kThreadsG, 1) qkv_gemm_pair_kernel(const __gri
             bool ok = true;
             for (uint32_t t = cid; ok && t < units; t += clusters, ++i) {
                 const uint32_t a = i % kAccBufs, u = i / kAccBufs;
-                if (u > 0 && !wait_phase<true>(acc_empty0 + 8 * a, (u - 1) & 1u, abort_flag, kWaitCyclesG, peer_flag))
+                if (u > 0 && !wait_phase<true>(acc_empty0 + 8 * a, (u - 1) & 1u, abort_flag, kWaitCycles, peer_flag))
                     break;  // both epilogues drained it
                 tc_fence_after();
                 const uint32_t d = tmem + a * kTmemCols;
                 for (uint32_t kb = 0; kb < KB; ++kb, ++q) {
                     const uint32_t s = q % kStagesP, use = q / kStagesP;
-                    if (!wait_phase<true>(full0 + 8 * s, use & 1u, abort_flag, kWaitCyclesG, peer_flag)) {
+                    if (!wait_phase<true>(full0 + 8 * s, use & 1u, abort_flag, kWaitCycles, peer_flag)) {
                         ok = false;
                         break;
                     }
@@ -705,7 +567,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) qkv_gemm_pair_kernel(const __gri
         uint32_t i = 0;
         for (uint32_t t = cid; t < units; t += clusters, ++i) {
             const uint32_t a = i % kAccBufs, u = i / kAccBufs;
-            const bool ok = wait_phase<true>(acc_full0 + 8 * a, u & 1u, abort_flag, kWaitCyclesG, peer_flag);
+            const bool ok = wait_phase<true>(acc_full0 + 8 * a, u & 1u, abort_flag, kWaitCycles, peer_flag);
             tc_fence_after();
             if (!__all_sync(0xffffffffu, ok && !*abort_flag)) break;  // warp-uniform: TMEM loads are collective
             const Tile tl = decode_tile<2>(p, t, rank);
@@ -862,6 +724,24 @@ bool encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uin
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_group_maps(GroupMaps* maps, const GroupView& v, uint32_t P, uint32_t B, uint32_t tokens, uint32_t heads,
+                       uint32_t D, bool bf16) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    // a stride of an extent-1 dimension is never used; give the driver a valid one
+    const cuuint64_t gdim[4] = {D, heads, tokens, B};
+    const cuuint64_t gstride[3] = {heads > 1 ? cuuint64_t(v.h) : D * 2, tokens > 1 ? cuuint64_t(v.t) : D * 2,
+                                   B > 1 ? cuuint64_t(v.b) : D * 2};
+    const cuuint32_t box[4] = {64, 1, kAttnRows, 1};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    for (uint32_t g = 0; g < P; ++g)
+        if (enc(&maps->m[g], bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, v.base[g],
+                gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
 }
 
 cudaError_t launch_qkv_gemm(const GemmParams& p, bool fused, bool neox, cudaStream_t stream) {

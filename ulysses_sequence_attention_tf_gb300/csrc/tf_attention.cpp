@@ -41,6 +41,8 @@ tf_status view(const char* name, const void* const* base, const tf_strides* give
     if (!empty && (s = check_ptrs(name, base, a.P)) != TF_OK) return s;
     const tf_strides st = given ? *given : tf_strides{tokens * hl * a.D, hl * a.D, a.D};
     if ((s = check_strides(name, st, 2, a.B, tokens, hl)) != TF_OK) return s;
+    if (!written && ((a.B > 1 && st.b == 0) || (tokens > 1 && st.t == 0) || (hl > 1 && st.h == 0)))
+        return fail(TF_ERR_UNSUPPORTED, "%s has a stride of 0 (key heads are shared through Hkv)", name);
     if (written && ((a.B > 1 && st.b == 0) || (tokens > 1 && st.t == 0) || (hl > 1 && st.h == 0)))
         return fail(TF_ERR_INVALID, "%s is written and has a stride of 0", name);
     for (int g = 0; g < a.P; ++g) out->base[g] = static_cast<uint8_t*>(const_cast<void*>(base[g]));
@@ -69,7 +71,8 @@ void describe(const tf_attention& a, tfu::AttentionParams* p) {
 }
 
 size_t workspace_bytes_of(const tf_attention& a, bool backward) {
-    return backward ? size_t(a.B) * size_t(a.H) * size_t(a.Sq) * sizeof(float) : 0;
+    if (backward) return size_t(a.B) * size_t(a.H) * size_t(a.Sq) * sizeof(float);
+    return a.q_docs ? tfu::tile_plan(uint32_t(a.Sq), tfu::kAttnPair, uint32_t(a.Sk)).bytes(uint32_t(a.B)) : 0;
 }
 
 tf_status check_workspace(const tf_attention& a, bool backward, const void* workspace, size_t bytes) {
@@ -101,7 +104,9 @@ TF_API tf_status tf_ulysses_attention(const tf_attention* a, const void* const* 
     tf_status s = check_attention(a);
     if (s != TF_OK) return s;
     if (!strides) return fail(TF_ERR_INVALID, "strides is NULL");
-    tfu::AttentionParams p{};
+    tfu::ForwardParams fp;  // tensor maps of absent groups stay unset
+    fp.a = tfu::AttentionParams{};
+    tfu::AttentionParams& p = fp.a;
     if ((s = view("q", q, &strides[0], *a, a->Sq, a->H, false, &p.q)) != TF_OK) return s;
     if ((s = view("k", k, &strides[1], *a, a->Sk, a->Hkv, false, &p.k)) != TF_OK) return s;
     if ((s = view("v", v, &strides[2], *a, a->Sk, a->Hkv, false, &p.v)) != TF_OK) return s;
@@ -116,9 +121,17 @@ TF_API tf_status tf_ulysses_attention(const tf_attention* a, const void* const* 
     if ((s = current_device(&device)) != TF_OK) return s;
     if (empty) return TF_OK;
     describe(*a, &p);
-    const cudaError_t e = tfu::launch_attention(p, a->dtype == TF_BF16, static_cast<cudaStream_t>(stream));
+    const bool bf16 = a->dtype == TF_BF16;
+    if (!tfu::encode_group_maps(&fp.q, p.q, p.P, p.B, p.Sq, p.Hl, p.D, bf16) ||
+        (a->Sk > 0 && (!tfu::encode_group_maps(&fp.k, p.k, p.P, p.B, p.Sk, p.Hkl, p.D, bf16) ||
+                       !tfu::encode_group_maps(&fp.v, p.v, p.P, p.B, p.Sk, p.Hkl, p.D, bf16))))
+        return fail(TF_ERR_UNSUPPORTED, "the driver refused a tensor map of q, k or v");
+    p.plan = a->q_docs && a->Sk > 0 ? static_cast<uint32_t*>(workspace) : nullptr;
+    fp.q_tiles = (p.Sq + tfu::kAttnPair - 1) / tfu::kAttnPair;
+    int launches = 0;
+    const cudaError_t e = tfu::launch_attention(fp, bf16, static_cast<cudaStream_t>(stream), &launches);
+    count_launches(launches);
     if (e != cudaSuccess) return cuda_fail(e, "launching the attention kernel");
-    count_launches(1);
     return TF_OK;
 }
 

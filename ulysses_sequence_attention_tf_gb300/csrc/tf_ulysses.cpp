@@ -21,6 +21,7 @@
 
 #include <cuda_runtime.h>
 
+#include "attention.h"
 #include "gemm.h"
 #include "host.h"
 #include "kv_cache.h"
@@ -1154,15 +1155,17 @@ TF_API void tf_ulysses_set_allocator(tf_alloc_fn alloc, tf_free_fn release, void
 
 TF_API tf_status tf_ulysses_device_status(int clear, unsigned* status) {
     if (!status) return fail(TF_ERR_INVALID, "status is NULL");
-    unsigned staged = 0, gemm = 0, block = 0, block16 = 0, append = 0, attend = 0;
+    unsigned staged = 0, gemm = 0, block = 0, block16 = 0, append = 0, attend = 0, attention = 0;
     cudaError_t e = tfu::read_staged_status(&staged, clear != 0);
     if (e == cudaSuccess) e = tfu::read_gemm_status(&gemm, clear != 0);
     if (e == cudaSuccess) e = tfu::read_block_status(&block, clear != 0);
     if (e == cudaSuccess) e = tfu::read_block_status_v16(&block16, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_append_status(&append, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_attend_status(&attend, clear != 0);
+    if (e == cudaSuccess) e = tfu::read_attention_status(&attention, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device status words");
-    *status = (staged ? 1u : 0u) | (gemm ? 2u : 0u) | ((block | block16) ? 4u : 0u) | ((append | attend) ? 8u : 0u);
+    *status = (staged ? 1u : 0u) | (gemm ? 2u : 0u) | ((block | block16) ? 4u : 0u) | ((append | attend) ? 8u : 0u) |
+              (attention ? 16u : 0u);
     return TF_OK;
 }
 
