@@ -39,7 +39,7 @@ struct AttentionParams {
 };
 
 // Tensor maps of the head groups' views: 4-D (D, heads, tokens, B), boxes of 64
-// elements x 128 tokens of one head with the 128-byte swizzle.
+// elements x 128 or 64 tokens of one head with the 128-byte swizzle.
 struct GroupMaps {
     CUtensorMap m[kMaxShards];
 };
@@ -48,6 +48,14 @@ struct ForwardParams {
     GroupMaps q, k, v;
     AttentionParams a;
     uint32_t q_tiles;  // of kAttnPair rows
+};
+
+struct BackwardParams {
+    GroupMaps q, k, v, dout;      // boxes of 128 tokens
+    GroupMaps q_half, dout_half;  // boxes of 64
+    AttentionParams a;
+    uint32_t* key_plan;           // with documents: row tiles of keys (a.plan: of 128 queries)
+    uint32_t q_tiles, k_tiles;    // of kAttnRows rows
 };
 
 // With documents, a kernel in front of the attention writes for every row tile
@@ -62,15 +70,17 @@ inline TilePlan tile_plan(uint32_t rows, uint32_t rows_per_tile, uint32_t cols) 
     return {(rows + rows_per_tile - 1) / rows_per_tile, (col_tiles + 31) / 32};
 }
 
-// Encode the maps of P groups ([B, tokens, heads, D] 16-bit views); false if the driver refuses.
+// Encode the maps of P groups ([B, tokens, heads, D] 16-bit views, boxes of box_tokens);
+// false if the driver refuses.
 bool encode_group_maps(GroupMaps* maps, const GroupView& v, uint32_t P, uint32_t B, uint32_t tokens, uint32_t heads,
-                       uint32_t D, bool bf16);
+                       uint32_t D, uint32_t box_tokens, bool bf16);
 
 // *launches: kernels launched
 cudaError_t launch_attention(const ForwardParams& p, bool bf16, cudaStream_t stream, int* launches);
-cudaError_t launch_attention_backward(const AttentionParams& p, bool bf16, cudaStream_t stream, int* launches);
+cudaError_t launch_attention_backward(const BackwardParams& p, bool bf16, cudaStream_t stream, int* launches);
 
-// Status word of the attention kernels: 0, or 1 when a bounded wait gave up.
+// Status words of the attention kernels: 0, or 1 when a bounded wait gave up.
 cudaError_t read_attention_status(unsigned* out, bool clear);
+cudaError_t read_attention_backward_status(unsigned* out, bool clear);
 
 }  // namespace tfu

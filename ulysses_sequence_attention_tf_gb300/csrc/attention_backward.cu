@@ -1,228 +1,795 @@
-// attention_backward.cu -- the gradient of the attention over the head groups.
+// attention_backward.cu -- the gradient of the attention over the head groups, on the
+// 5th-generation tensor cores.
 //
 // With the weights P_ij = e^(z_ij - lse_i) recomputed from Q, K and the saved
-// log-sum-exp, and delta_i = sum_d dO_id O_id:
-//   dV_j = sum_i P_ij dO_i
-//   dx_ij = P_ij (dO_i . V_j - delta_i) (1 - tanh^2(x_ij / cap))    (the last factor where scores are capped)
-//   dQ_i = scale * sum_j dx_ij K_j        dK_j = scale * sum_i dx_ij Q_i
-// dQ is summed by the rows that own it in one kernel, dK and dV by the keys that
-// own them in another (over all query heads that share the key head): no atomics,
-// so the same inputs give the same bits.
+// log-sum-exp, and delta_i = sum_j P_ij dP_ij (= sum_d dO_id O_id):
+//   dP_ij = dO_i . V_j                          dV_j = sum_i P_ij dO_i
+//   dx_ij = P_ij (dP_ij - delta_i) (1 - tanh^2(x_ij / cap))    (the last factor where scores are capped)
+//   dQ_i  = scale * sum_j dx_ij K_j             dK_j = scale * sum_i dx_ij Q_i
+//
+// Two kernels: dq_kernel owns query rows and sums over the keys, dkv_kernel owns
+// key rows and sums over the queries of every head that shares the key head.  S and
+// dP are computed in both (7 products instead of 5), which spares the read-modify-
+// write of dQ in memory: no atomics, so the same inputs give the same bits.
+//
+// delta_i: the output O holds a rounding of 2^-9 (bf16), and where a row sees few keys
+// dP - delta cancels, so that dO . O is not enough (a row of three keys: dQ off by 2 %).
+// A row tile that visits at most kExactTiles key tiles therefore sums P dP over its keys
+// first and uses that; the others take dO . O.
 #include "attention_common.cuh"
+#include "attention_plan.h"
 
 namespace tfu {
+
+__device__ unsigned g_attention_backward_status;
 
 namespace {
 
 using namespace dev;
 
-constexpr int kRowThreads = 128;
-constexpr int kOther = 16;  // rows of the other side in a block
+constexpr int kThreadsB = 384;
+constexpr uint32_t kHalfTile = kAttnRows * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
+constexpr int kExactTiles = 4;
 
-// delta_i = sum_d dO_id O_id: a warp per row.
-template <Fused kF>
-__global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ AttentionParams p) {
-    const uint64_t rows = uint64_t(p.P) * p.B * p.Hl * p.Sq;
-    const uint64_t r = uint64_t(blockIdx.x) * 8 + threadIdx.x / 32;
-    const uint32_t lane = threadIdx.x % 32;
-    if (r >= rows) return;
-    const uint32_t i = r % p.Sq, h = r / p.Sq % p.Hl, b = r / p.Sq / p.Hl % p.B, g = r / p.Sq / p.Hl / p.B;
-    const uint16_t* o = reinterpret_cast<const uint16_t*>(p.out.base[g] + b * p.out.b + int64_t(i) * p.out.t + h * p.out.h);
-    const uint16_t* d = reinterpret_cast<const uint16_t*>(p.dout.base[g] + b * p.dout.b + int64_t(i) * p.dout.t + h * p.dout.h);
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return bounded_wait(bar, parity, abort_flag, &g_attention_backward_status);
+}
+
+// Weights w = 2^(z log2 e - lse2) of kN scores in place, and (capped) the factor
+// bend = 1 - tanh^2 of each.  far0: pos - key of element 0, one less (kStep = -1, a row
+// of keys) or one more (kStep = 1, a row of queries) for each next element.
+template <bool kCap, bool kBias, int kN, int kStep>
+__device__ __forceinline__ void to_scores(float (&s)[kN], float (&bend)[kCap ? kN : 2], float scale, float cap, float slope,
+                                          float far0) {
+    if constexpr (kCap) {
+        const float to_x = scale / cap, to_z = cap * kLog2e;
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < kN; i += 2) most = fmaxf(fmaxf(fabsf(s[i]), fabsf(s[i + 1])), most);
+        if (__all_sync(0xffffffffu, most * fabsf(to_x) <= kTanhNear)) {
+            const uint64_t x2 = f2_pack(to_x, to_x), z2 = f2_pack(to_z, to_z), one = f2_pack(1.f, 1.f);
+#pragma unroll
+            for (int i = 0; i < kN; i += 2) {
+                const uint64_t x = f2_mul(f2_pack(s[i], s[i + 1]), x2);
+                const uint64_t t = f2_mul(x, tanh_over_x(f2_mul(x, x)));
+                f2_unpack(f2_mul(t, z2), s[i], s[i + 1]);
+                f2_unpack(f2_sub(one, f2_mul(t, t)), bend[i], bend[i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const float t = tanh_wide(s[i] * to_x);
+                s[i] = to_z * t;
+                bend[i] = fmaf(-t, t, 1.0f);
+            }
+        }
+    } else {
+        const uint64_t c2 = f2_pack(scale * kLog2e, scale * kLog2e);
+#pragma unroll
+        for (int i = 0; i < kN; i += 2) f2_unpack(f2_mul(f2_pack(s[i], s[i + 1]), c2), s[i], s[i + 1]);
+    }
+    if constexpr (kBias) {
+        const float m = slope * kLog2e;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) s[i] = fmaf(-m, fabsf(far0 + float(kStep * i)), s[i]);
+    }
+}
+
+template <int kN>
+__device__ __forceinline__ void load_row(uint32_t taddr, float (&v)[kN]) {
+    uint32_t r[kN / 32][32];
+#pragma unroll
+    for (int x = 0; x < kN / 32; ++x) tc_ld32(taddr + x * 32, r[x]);
+    tc_wait_ld();
+#pragma unroll
+    for (int x = 0; x < kN / 32; ++x) {
+        tc_landed(r[x]);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) v[x * 32 + y] = __uint_as_float(r[x][y]);
+    }
+}
+
+// 16-bit pairs of kN values over TMEM columns from taddr
+template <Fused kF, int kN>
+__device__ __forceinline__ void store_row16(uint32_t taddr, const float (&v)[kN]) {
+#pragma unroll
+    for (int x = 0; x < kN / 32; ++x) {
+        uint32_t w[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y) w[y] = pack2<kF>(v[x * 32 + 2 * y], v[x * 32 + 2 * y + 1]);
+        tc_st16(taddr + x * 16, w);
+    }
+}
+
+// kD accumulator columns times `factor` to a row of 16-bit values
+template <Fused kF, int kD>
+__device__ __forceinline__ void write_row(uint32_t taddr, bool any, bool valid, float factor, uint8_t* dst) {
+#pragma unroll 1
+    for (int x = 0; x < kD; x += 32) {
+        uint32_t r[32];
+        if (any) {
+            tc_ld32(taddr + x, r);
+            tc_wait_ld();
+            tc_landed(r);
+        } else {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) r[y] = 0;
+        }
+#pragma unroll
+        for (int y = 0; y < 32; y += 8) {
+            uint4 w;
+            uint32_t* o = &w.x;
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                o[z] = pack2<kF>(__uint_as_float(r[y + 2 * z]) * factor, __uint_as_float(r[y + 2 * z + 1]) * factor);
+            if (valid) *reinterpret_cast<uint4*>(dst + (x + y) * 2) = w;
+        }
+    }
+}
+
+// sum_d a_d b_d of two 16-bit rows
+template <Fused kF, int kD>
+__device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b) {
     float s = 0.f;
-    for (uint32_t x = lane; x < p.D; x += 32) s = fmaf(to_float<kF>(o[x]), to_float<kF>(d[x]), s);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    if (lane == 0) p.delta[r] = s;
-}
-
-// x -> weight P and the slope of the cap; both 0 where the pair is masked.
-__device__ __forceinline__ void weight_of(const AttentionParams& p, float dot, float slope, int64_t far, float lse, bool see,
-                                          float& w, float& bend) {
-    float s = dot * p.scale;
-    bend = 1.f;
-    if (p.cap != 0.f) {
-        const float t = tanhf(s / p.cap);
-        s = p.cap * t;
-        bend = 1.f - t * t;
-    }
-    s -= slope * fabsf(float(far));
-    w = see ? expf(s - lse) : 0.f;
-}
-
-template <Fused kF, int kD>
-__global__ void __launch_bounds__(kRowThreads) dq_kernel(const __grid_constant__ AttentionParams p) {
-    constexpr int kLanes = kD / 32, kRows = kRowThreads / kLanes;
-    __shared__ float ks[kOther][kD], vs[kOther][kD];
-    __shared__ int32_t kdoc[kOther];
-    const uint32_t part = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
-    const uint32_t h = blockIdx.y % p.Hl, b = blockIdx.y / p.Hl % p.B, g = blockIdx.y / p.Hl / p.B;
-    const uint32_t kh = h / p.shared;
-    const int64_t i = int64_t(blockIdx.x) * kRows + row;
-    const bool valid = i < int64_t(p.Sq);
-    float q[32], dy[32], acc[32];
-    const int64_t at = valid ? i : 0;
-    const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.q.base[g] + b * p.q.b + at * p.q.t + h * p.q.h);
-    const uint16_t* dp = reinterpret_cast<const uint16_t*>(p.dout.base[g] + b * p.dout.b + at * p.dout.t + h * p.dout.h);
-#pragma unroll
-    for (int d = 0; d < 32; ++d) {
-        q[d] = valid ? to_float<kF>(qp[part * 32 + d]) : 0.f;
-        dy[d] = valid ? to_float<kF>(dp[part * 32 + d]) : 0.f;
-        acc[d] = 0.f;
-    }
-    const int bound = valid ? key_bound(p, b, i) : 0;
-    const int32_t doc = valid && p.q_docs ? p.q_docs[int64_t(b) * p.Sq + i] : -1;
-    const float slope = p.slopes ? p.slopes[g * p.Hl + h] : 0.f;
-    const int64_t pos = i + int64_t(p.Sk) - int64_t(p.Sq);
-    const int64_t stat = (int64_t(b) * p.Hl + h) * p.Sq + at;
-    const float lse = p.lse[g][stat];
-    const float delta = p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat];
-    const uint8_t* kb = p.k.base[g] + b * p.k.b + kh * p.k.h;
-    const uint8_t* vb = p.v.base[g] + b * p.v.b + kh * p.v.h;
-    for (int j0 = 0; j0 < int(p.Sk); j0 += kOther) {
-        if (!__syncthreads_or(j0 < bound)) break;
-        for (int x = threadIdx.x; x < kOther * kD; x += kRowThreads) {
-            const int j = x / kD, d = x % kD;
-            const bool in = j0 + j < int(p.Sk);
-            ks[j][d] = in ? to_float<kF>(reinterpret_cast<const uint16_t*>(kb + int64_t(j0 + j) * p.k.t)[d]) : 0.f;
-            vs[j][d] = in ? to_float<kF>(reinterpret_cast<const uint16_t*>(vb + int64_t(j0 + j) * p.v.t)[d]) : 0.f;
-        }
-        if (p.k_docs && threadIdx.x < kOther)
-            kdoc[threadIdx.x] = j0 + int(threadIdx.x) < int(p.Sk) ? p.k_docs[int64_t(b) * p.Sk + j0 + threadIdx.x] : -1;
-        __syncthreads();
 #pragma unroll 4
-        for (int j = 0; j < kOther; ++j) {
-            float s = 0.f, t = 0.f;
+    for (int x = 0; x < kD / 8; ++x) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(a) + x), v = __ldg(reinterpret_cast<const uint4*>(b) + x);
+        const uint32_t* uw = &u.x;
+        const uint32_t* vw = &v.x;
 #pragma unroll
-            for (int d = 0; d < 32; ++d) {
-                s = fmaf(q[d], ks[j][part * 32 + d], s);
-                t = fmaf(dy[d], vs[j][part * 32 + d], t);
-            }
-#pragma unroll
-            for (int w = 1; w < kLanes; w <<= 1) {
-                s += __shfl_xor_sync(0xffffffffu, s, w);
-                t += __shfl_xor_sync(0xffffffffu, t, w);
-            }
-            const bool see = j0 + j < bound && (!p.k_docs || (doc >= 0 && kdoc[j] == doc));
-            if (!see) continue;
-            float w, bend;
-            weight_of(p, s, slope, pos - (j0 + j), lse, see, w, bend);
-            const float dx = w * (t - delta) * bend * p.scale;
-#pragma unroll
-            for (int d = 0; d < 32; ++d) acc[d] = fmaf(dx, ks[j][part * 32 + d], acc[d]);
-        }
-        __syncthreads();
-    }
-    if (!valid) return;
-    uint16_t* op = reinterpret_cast<uint16_t*>(p.dq.base[g] + b * p.dq.b + i * p.dq.t + h * p.dq.h);
-#pragma unroll
-    for (int d = 0; d < 32; ++d) op[part * 32 + d] = to_half<kF>(acc[d]);
-}
-
-template <Fused kF, int kD>
-__global__ void __launch_bounds__(kRowThreads) dkv_kernel(const __grid_constant__ AttentionParams p) {
-    constexpr int kLanes = kD / 32, kRows = kRowThreads / kLanes;
-    __shared__ float qs[kOther][kD], ds[kOther][kD];
-    __shared__ float lses[kOther], deltas[kOther];
-    __shared__ int32_t qdoc[kOther];
-    __shared__ int bounds[kOther];
-    const uint32_t part = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
-    const uint32_t kh = blockIdx.y % p.Hkl, b = blockIdx.y / p.Hkl % p.B, g = blockIdx.y / p.Hkl / p.B;
-    const int64_t j = int64_t(blockIdx.x) * kRows + row;
-    const bool valid = j < int64_t(p.Sk);
-    float k[32], v[32], dk[32], dv[32];
-    const int64_t at = valid ? j : 0;
-    const uint16_t* kp = reinterpret_cast<const uint16_t*>(p.k.base[g] + b * p.k.b + at * p.k.t + kh * p.k.h);
-    const uint16_t* vp = reinterpret_cast<const uint16_t*>(p.v.base[g] + b * p.v.b + at * p.v.t + kh * p.v.h);
-#pragma unroll
-    for (int d = 0; d < 32; ++d) {
-        k[d] = valid ? to_float<kF>(kp[part * 32 + d]) : 0.f;
-        v[d] = valid ? to_float<kF>(vp[part * 32 + d]) : 0.f;
-        dk[d] = dv[d] = 0.f;
-    }
-    const int32_t doc = valid && p.k_docs ? p.k_docs[int64_t(b) * p.Sk + j] : -1;
-    const int64_t ahead = int64_t(p.Sk) - int64_t(p.Sq);
-    for (uint32_t h = kh * p.shared; h < (kh + 1) * p.shared; ++h) {
-        const float slope = p.slopes ? p.slopes[g * p.Hl + h] : 0.f;
-        const uint8_t* qb = p.q.base[g] + b * p.q.b + h * p.q.h;
-        const uint8_t* db = p.dout.base[g] + b * p.dout.b + h * p.dout.h;
-        const int64_t stat = (int64_t(b) * p.Hl + h) * p.Sq;
-        for (int64_t i0 = 0; i0 < int64_t(p.Sq); i0 += kOther) {
-            __syncthreads();
-            for (int x = threadIdx.x; x < kOther * kD; x += kRowThreads) {
-                const int i = x / kD, d = x % kD;
-                const bool in = i0 + i < int64_t(p.Sq);
-                qs[i][d] = in ? to_float<kF>(reinterpret_cast<const uint16_t*>(qb + (i0 + i) * p.q.t)[d]) : 0.f;
-                ds[i][d] = in ? to_float<kF>(reinterpret_cast<const uint16_t*>(db + (i0 + i) * p.dout.t)[d]) : 0.f;
-            }
-            if (threadIdx.x < kOther) {
-                const int64_t i = i0 + threadIdx.x;
-                const bool in = i < int64_t(p.Sq);
-                lses[threadIdx.x] = in ? p.lse[g][stat + i] : 0.f;
-                deltas[threadIdx.x] = in ? p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat + i] : 0.f;
-                qdoc[threadIdx.x] = in && p.q_docs ? p.q_docs[int64_t(b) * p.Sq + i] : -1;
-                bounds[threadIdx.x] = in ? key_bound(p, b, i) : 0;
-            }
-            __syncthreads();
-#pragma unroll 4
-            for (int i = 0; i < kOther; ++i) {
-                float s = 0.f, t = 0.f;
-#pragma unroll
-                for (int d = 0; d < 32; ++d) {
-                    s = fmaf(k[d], qs[i][part * 32 + d], s);
-                    t = fmaf(v[d], ds[i][part * 32 + d], t);
-                }
-#pragma unroll
-                for (int w = 1; w < kLanes; w <<= 1) {
-                    s += __shfl_xor_sync(0xffffffffu, s, w);
-                    t += __shfl_xor_sync(0xffffffffu, t, w);
-                }
-                const bool see = valid && j < bounds[i] && (!p.k_docs || (doc >= 0 && qdoc[i] == doc));
-                if (!see) continue;
-                float w, bend;
-                weight_of(p, s, slope, i0 + i + ahead - j, lses[i], see, w, bend);
-                const float dx = w * (t - deltas[i]) * bend * p.scale;
-#pragma unroll
-                for (int d = 0; d < 32; ++d) {
-                    dv[d] = fmaf(w, ds[i][part * 32 + d], dv[d]);
-                    dk[d] = fmaf(dx, qs[i][part * 32 + d], dk[d]);
-                }
-            }
+        for (int y = 0; y < 4; ++y) {
+            float a0, a1, b0, b1;
+            unpack2<kF>(uw[y], a0, a1);
+            unpack2<kF>(vw[y], b0, b1);
+            s = fmaf(a0, b0, s);
+            s = fmaf(a1, b1, s);
         }
     }
-    if (!valid) return;
-    uint16_t* ok = reinterpret_cast<uint16_t*>(p.dk.base[g] + b * p.dk.b + j * p.dk.t + kh * p.dk.h);
-    uint16_t* ov = reinterpret_cast<uint16_t*>(p.dv.base[g] + b * p.dv.b + j * p.dv.t + kh * p.dv.h);
+    return s;
+}
+
+// ---------------------------------------------------------------- dQ
+// One CTA: 128 query rows of one head, tiles of 128 keys.
+//  * warp 8, one lane: TMA.  Q and dO once, K and V through a ring K0 V0 K1 V1 ...
+//  * warp 9, one lane: S(j+1) = Q K^T into the other S buffer, dP(j+1) = dO V^T once
+//    dP(j) has been read, dQ += dx(j) K (dx from TMEM, K read MN-major).
+//  * warps 0-3 and 4-7: a thread per row and half of the tile's keys; dx in 16 bits goes
+//    over the scores it came from.
+// TMEM: S0 S1 dP (128 columns each), dQ (D columns).
+template <int kD>
+struct DqShape {
+    static constexpr uint32_t kTile = kHalfTile * (kD / 64);
+    static constexpr int kStages = kD == 128 ? 4 : 8;
+    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kTile + 1024 + 512 + 1024;  // + the rows' sums, barriers, alignment
+};
+
+template <Fused kF, int kD, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant__ BackwardParams bp) {
+    using S = DqShape<kD>;
+    constexpr uint32_t kTile = S::kTile;
+    constexpr int kStages = S::kStages;
+    const AttentionParams& p = bp.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* sums = reinterpret_cast<float*>(smem + (2 + kStages) * size_t(kTile));  // [2][128]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sums + 2 * kAttnRows);
+    const uint32_t q_smem = smem_u32(smem), do_smem = q_smem + kTile, ring = q_smem + 2 * kTile;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
+    const uint32_t s_full0 = q_full + 8, dp_full = s_full0 + 16, dp_free = dp_full + 8, dx_full = dp_free + 8;
+    const uint32_t sums_full = dx_full + 8, done = sums_full + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 8);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    uint32_t u = blockIdx.x;
+    uint32_t qt = u % bp.q_tiles;
+    u /= bp.q_tiles;
+    if (p.causal) qt = bp.q_tiles - 1 - qt;
+    const uint32_t h = u % p.Hl, b = u / p.Hl % p.B, g = u / p.Hl / p.B;
+    const int row0 = int(qt * kAttnRows);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(s_full0, 1);
+        mbar_init(s_full0 + 8, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(dp_free, 2 * kAttnRows);
+        mbar_init(dx_full, 2 * kAttnRows);
+        mbar_init(sums_full, 2 * kAttnRows);
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dependency_wait();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t dp_tmem = tmem + 2 * kAttnRows, dq_tmem = tmem + 3 * kAttnRows;
+
+    const int last = min(row0 + int(kAttnRows), int(p.Sq)) - 1;
+    const int n_tiles = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
+    const uint32_t words = (((p.Sk + kAttnRows - 1) / kAttnRows) + 31) / 32;
+    const uint32_t* plan = p.plan ? p.plan + (size_t(b) * bp.q_tiles + qt) * 2 * words : nullptr;
+    int visits = n_tiles;
+    if (plan) {
+        visits = 0;
+        for (uint32_t w = 0; w < words; ++w) visits += __popc(__ldg(plan + w));
+    }
+    const bool exact = visits <= kExactTiles;  // two phases: delta from P dP, then dQ
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8 && lane == 0) {
+        const CUtensorMap* maps[2] = {&bp.k.m[g], &bp.v.m[g]};
+        const int kh = int(h / p.shared);
+        uint32_t n = 0;
+        bool ok = true;
+        if (visits > 0) {
+            mbar_expect_tx(q_full, 2 * kTile);
+            for (int x = 0; x < kD / 64; ++x) {
+                tma_load_4d(q_smem + x * kHalfTile, &bp.q.m[g], x * 64, int(h), row0, int(b), q_full);
+                tma_load_4d(do_smem + x * kHalfTile, &bp.dout.m[g], x * 64, int(h), row0, int(b), q_full);
+            }
+        }
+        for (int phase = exact ? 0 : 1; phase < 2; ++phase) {
+            TileIter it(plan, n_tiles);
+            for (int j = it.next(); ok && j >= 0; j = it.next()) {
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const uint32_t s = n % kStages, use = n / kStages;
+                    if (use > 0 && !wait_for(empty0 + 8 * s, (use - 1) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(full0 + 8 * s, kTile);
+                    for (int x = 0; x < kD / 64; ++x)
+                        tma_load_4d(ring + s * kTile + x * kHalfTile, maps[kv], x * 64, kh, j * int(kAttnRows), int(b),
+                                    full0 + 8 * s);
+                }
+            }
+        }
+        if (visits > 0) drain_phase(q_full, 0);
+        for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
+            drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
+    } else if (warp == 9 && lane == 0) {
+        constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
+        constexpr uint32_t kIdescQ = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
+        const int steps = exact ? 2 * visits : visits;
+        auto landed = [&](uint32_t k) { return wait_for(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag); };
+        auto stage = [&](uint32_t k) { return ring + (k % kStages) * kTile; };
+        auto product = [&](uint32_t d, uint32_t a_smem, uint32_t b_smem) {
 #pragma unroll
-    for (int d = 0; d < 32; ++d) {
-        ok[part * 32 + d] = to_half<kF>(dk[d]);
-        ov[part * 32 + d] = to_half<kF>(dv[d]);
+            for (uint32_t kk = 0; kk < kD / 16; ++kk) {
+                const uint32_t off = kk / 4 * kHalfTile + kk % 4 * 32;
+                tc_mma(d, sw128_desc(a_smem + off), sw128_desc(b_smem + off), kIdescS, kk != 0);
+            }
+        };
+        bool ok = steps == 0 || wait_for(q_full, 0, abort_flag);
+        // step i: K at ring tile 2i, V at 2i + 1
+        auto scores = [&](int i) {
+            if (!landed(2 * i)) return false;
+            tc_fence_after();
+            product(tmem + (i & 1) * kAttnRows, q_smem, stage(2 * i));
+            tc_commit(s_full0 + 8 * (i & 1));
+            return true;
+        };
+        auto dp = [&](int i) {
+            if (!landed(2 * i + 1)) return false;
+            tc_fence_after();
+            product(dp_tmem, do_smem, stage(2 * i + 1));
+            tc_commit(dp_full);
+            tc_commit(empty0 + 8 * ((2 * i + 1) % kStages));
+            return true;
+        };
+        if (ok && steps > 0) ok = scores(0) && dp(0);
+        for (int i = 0; ok && i < steps; ++i) {
+            const bool sums_only = exact && i < visits;
+            if (i + 1 < steps) {
+                // the other S buffer: its dx was read by the dQ product issued before
+                if (!(ok = scores(i + 1))) break;
+                if (!(ok = wait_for(dp_free, i & 1u, abort_flag))) break;
+                if (!(ok = dp(i + 1))) break;
+            }
+            if (!(ok = wait_for(dx_full, i & 1u, abort_flag))) break;
+            tc_fence_after();
+            if (!sums_only) {
+                const uint32_t a = tmem + (i & 1) * kAttnRows;
+                const bool first = i == (exact ? visits : 0);
+#pragma unroll
+                for (uint32_t kk = 0; kk < kAttnRows / 16; ++kk)
+                    tc_mma_ts(dq_tmem, a + kk / 4 * 64 + kk % 4 * 8, sw128_desc(stage(2 * i) + kk * 2048, kHalfTile), kIdescQ,
+                              !first || kk != 0);
+            }
+            tc_commit(empty0 + 8 * (2 * i % kStages));
+        }
+        tc_commit(done);
+        drain_phase(done, 0);
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const uint32_t half = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+        const int i = row0 + int(r);
+        const bool valid = i < int(p.Sq);
+        const uint32_t lane_base = (quarter * 32u) << 16;
+        int bound = valid ? key_bound(p, b, i) : 0;
+        int32_t doc = -1;
+        if (plan) {
+            doc = valid ? p.q_docs[int64_t(b) * p.Sq + i] : -1;
+            if (doc < 0) bound = 0;
+        }
+        const float slope = kBias && p.slopes ? p.slopes[g * p.Hl + h] : 0.f;
+        const int64_t stat = (int64_t(b) * p.Hl + h) * p.Sq + (valid ? i : 0);
+        float* delta_at = p.delta + int64_t(g) * p.B * p.Hl * p.Sq + stat;
+        const float lse2 = valid ? p.lse[g][stat] * kLog2e : 0.f;
+        const int64_t at = valid ? i : 0;
+        float delta = 0.f;
+        if (!exact && valid) {
+            delta = row_dot<kF, kD>(p.dout.base[g] + b * p.dout.b + at * p.dout.t + h * p.dout.h,
+                                    p.out.base[g] + b * p.out.b + at * p.out.t + h * p.out.h);
+            if (half == 0) *delta_at = delta;
+        }
+        bool ok = true;
+        int n = 0;
+        for (int phase = exact ? 0 : 1; ok && phase < 2; ++phase) {
+            TileIter it(plan, n_tiles);
+            float sum = 0.f;
+            for (int j = it.next(); j >= 0; j = it.next(), ++n) {
+                const uint32_t s_row = tmem + (n & 1) * kAttnRows + half * 64 + lane_base;
+                ok = wait_for(s_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int j0 = j * int(kAttnRows) + int(half) * 64;
+                float s[64], bend[kCap ? 64 : 2];
+                load_row<64>(s_row, s);
+                to_scores<kCap, kBias, 64, -1>(s, bend, p.scale, p.cap, slope, float(i + (int(p.Sk) - int(p.Sq)) - j0));
+#pragma unroll
+                for (int x = 0; x < 64; ++x) s[x] = ex2(s[x] - lse2);
+                const bool whole = plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + 64 <= bound;
+                if (!__all_sync(0xffffffffu, whole)) {
+                    if (plan) {
+                        int32_t kd[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int key = j0 + x * 32 + int(lane);
+                            kd[x] = key < int(p.Sk) ? __ldg(p.k_docs + int64_t(b) * p.Sk + key) : -1;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 64; ++x)
+                            s[x] = __shfl_sync(0xffffffffu, kd[x / 32], x % 32) == doc && j0 + x < bound ? s[x] : 0.f;
+                        // padding's K rows may hold anything: clear them for the product with dx
+                        if (quarter < 2 && (quarter == 0 ? kd[0] : kd[1]) < 0) {
+                            uint4* k = reinterpret_cast<uint4*>(smem + (2 + 2 * n % kStages) * size_t(kTile) +
+                                                                (half * 64 + quarter * 32 + lane) * kSwizzleRow);
+                            for (int x = 0; x < kD / 64; ++x)
+                                for (int y = 0; y < 8; ++y) k[x * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_shared();
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 64; ++x) s[x] = j0 + x < bound ? s[x] : 0.f;
+                    }
+                }
+                ok = wait_for(dp_full, n & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float d[64];
+                load_row<64>(dp_tmem + half * 64 + lane_base, d);
+                tc_fence_before();
+                mbar_arrive(dp_free);
+                if (phase == 0) {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) sum += s[x] == 0.f ? 0.f : s[x] * d[x];
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) {
+                        float dx = s[x] == 0.f ? 0.f : s[x] * (d[x] - delta);
+                        if constexpr (kCap) dx *= bend[x];
+                        d[x] = dx;
+                    }
+                    store_row16<kF, 64>(s_row, d);
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(dx_full);
+            }
+            if (phase == 0 && ok) {  // the two halves of the row
+                sums[half * kAttnRows + r] = sum;
+                mbar_arrive(sums_full);
+                ok = wait_for(sums_full, 0, abort_flag);
+                delta = sums[r] + sums[kAttnRows + r];
+                if (half == 0 && valid) *delta_at = delta;
+                ok = __all_sync(0xffffffffu, ok);
+            }
+        }
+        if (ok && half == 0) {
+            ok = wait_for(done, 0, abort_flag);
+            if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
+                tc_fence_after();
+                write_row<kF, kD>(dq_tmem + lane_base, visits > 0, valid, p.scale,
+                                  p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
-template <Fused kF, int kD>
-cudaError_t launch(const AttentionParams& p, cudaStream_t stream, int* launches) {
-    constexpr uint32_t kRows = kRowThreads / (kD / 32);
-    const uint64_t rows = uint64_t(p.P) * p.B * p.Hl * p.Sq;
-    if (rows > 0) {
-        delta_kernel<kF><<<unsigned((rows + 7) / 8), 256, 0, stream>>>(p);
-        dq_kernel<kF, kD><<<dim3((p.Sq + kRows - 1) / kRows, p.P * p.B * p.Hl), kRowThreads, 0, stream>>>(p);
-        *launches += 2;
+// ---------------------------------------------------------------- dK and dV
+// One CTA: 128 key rows of one key head, blocks of 64 queries of every query head that
+// shares it.  Scores are taken transposed, keys on the TMEM lanes, so that P and dx
+// are operands as they stand:
+//  * warp 8, one lane: TMA.  K and V once, Q and dO blocks through a ring.
+//  * warp 9, one lane: S(n+1) = K Q^T and dP(n+1) = V dO^T into the other pair of
+//    buffers, then dV += P(n) dO, dK += dx(n) Q (P, dx from TMEM, dO, Q MN-major).
+//  * warp 10: the queries' log-sum-exp, delta, bounds and documents into shared memory.
+//  * warps 0-3 take the even blocks, warps 4-7 the odd ones: a thread per key row.
+// P goes over S, dx over dP, both in 16 bits.  fp16: P is kept times 2^8, away from
+// fp16's subnormals (weights of a long row are about 1 / Sk).
+// TMEM: S0 dP0 S1 dP1 (64 columns each), dK, dV (D columns each).
+constexpr uint32_t kQueries = 64;
+constexpr int kStatSlots = 4;
+
+struct QueryStat {
+    float lse2, delta;
+    int bound, doc;
+};
+
+template <int kD>
+struct DkvShape {
+    static constexpr uint32_t kTile = kHalfTile * (kD / 64);
+    static constexpr uint32_t kBlock = kTile / 2;         // 64 queries
+    static constexpr uint32_t kHalfBlock = kHalfTile / 2;
+    static constexpr int kStages = 8;
+    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kBlock + kStatSlots * kQueries * sizeof(QueryStat) + 512 + 1024;
+};
+
+// The blocks of a key tile, in order: query heads outer, tiles of 128 queries that can see
+// the keys, two blocks each.
+struct BlockIter {
+    TileIter it;
+    const uint32_t* words;
+    int n, first, Sq, tile, part;
+    uint32_t head, heads;
+    __device__ BlockIter(const uint32_t* w, int first_tile, int tiles, int sq, uint32_t shared)
+        : it(w, tiles), words(w), n(tiles), first(first_tile), Sq(sq), tile(-1), part(1), head(0), heads(shared) {
+        if (!w) it.pos = first_tile;
     }
-    if (p.Sk > 0) {
-        dkv_kernel<kF, kD><<<dim3((p.Sk + kRows - 1) / kRows, p.P * p.B * p.Hkl), kRowThreads, 0, stream>>>(p);
+    // first query of the next block, or -1
+    __device__ __forceinline__ int next() {
+        if (part == 0 && tile * int(kAttnRows) + int(kQueries) < Sq) {
+            part = 1;
+            return tile * int(kAttnRows) + int(kQueries);
+        }
+        while (true) {
+            tile = it.next();
+            if (tile >= 0) break;
+            if (++head >= heads) return -1;
+            it = TileIter(words, n);
+            if (!words) it.pos = first;
+        }
+        part = 0;
+        return tile * int(kAttnRows);
+    }
+};
+
+template <Fused kF, int kD, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant__ BackwardParams bp) {
+    using S = DkvShape<kD>;
+    constexpr uint32_t kTile = S::kTile, kBlock = S::kBlock, kHalfBlock = S::kHalfBlock;
+    constexpr int kStages = S::kStages;
+    constexpr float kUp = kF == Fused::kFP16 ? 8.0f : 0.0f, kDown = kF == Fused::kFP16 ? 0x1p-8f : 1.0f;
+    const AttentionParams& p = bp.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    QueryStat* stats = reinterpret_cast<QueryStat*>(smem + 2 * size_t(kTile) + kStages * size_t(kBlock));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(stats + kStatSlots * kQueries);
+    const uint32_t k_smem = smem_u32(smem), v_smem = k_smem + kTile, ring = k_smem + 2 * kTile;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, kv_full = empty0 + 8 * kStages;
+    const uint32_t s_full0 = kv_full + 8, dx_full0 = s_full0 + 16, stat_full0 = dx_full0 + 16;
+    const uint32_t stat_free0 = stat_full0 + 8 * kStatSlots, done = stat_free0 + 8 * kStatSlots;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 6 + 2 * kStatSlots);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    uint32_t u = blockIdx.x;
+    const uint32_t kt = u % bp.k_tiles;  // causal: the first keys are seen by most queries
+    u /= bp.k_tiles;
+    const uint32_t kh = u % p.Hkl, b = u / p.Hkl % p.B, g = u / p.Hkl / p.B;
+    const int row0 = int(kt * kAttnRows);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(kv_full, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full0 + 8 * t, 1);
+            mbar_init(dx_full0 + 8 * t, kAttnRows);
+        }
+        for (int t = 0; t < kStatSlots; ++t) {
+            mbar_init(stat_full0 + 8 * t, 32);
+            mbar_init(stat_free0 + 8 * t, kAttnRows);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dependency_wait();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t dk_tmem = tmem + 256, dv_tmem = dk_tmem + kD;
+
+    const int ahead = int(p.Sk) - int(p.Sq);
+    const int q_tiles = int((p.Sq + kAttnRows - 1) / kAttnRows);
+    int first = 0;  // the first query tile in reach of the keys
+    if (p.causal && !(p.prefix && row0 < p.prefix[b])) first = min(q_tiles, max(0, row0 - ahead) / int(kAttnRows));
+    const uint32_t words = (uint32_t(q_tiles) + 31) / 32;
+    const uint32_t* plan = p.plan ? p.plan + (size_t(b) * bp.k_tiles + kt) * 2 * words : nullptr;
+    BlockIter it(plan, first, q_tiles, int(p.Sq), p.shared);
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8 && lane == 0) {
+        uint32_t n = 0;
+        bool ok = true;
+        int i0 = it.next();
+        if (i0 >= 0) {
+            mbar_expect_tx(kv_full, 2 * kTile);
+            for (int x = 0; x < kD / 64; ++x) {
+                tma_load_4d(k_smem + x * kHalfTile, &bp.k.m[g], x * 64, int(kh), row0, int(b), kv_full);
+                tma_load_4d(v_smem + x * kHalfTile, &bp.v.m[g], x * 64, int(kh), row0, int(b), kv_full);
+            }
+        }
+        const bool any = i0 >= 0;
+        for (; ok && i0 >= 0; i0 = it.next()) {
+            const int h = int(kh * p.shared + it.head);
+            for (int qd = 0; qd < 2; ++qd, ++n) {
+                const uint32_t s = n % kStages, use = n / kStages;
+                if (use > 0 && !wait_for(empty0 + 8 * s, (use - 1) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                mbar_expect_tx(full0 + 8 * s, kBlock);
+                for (int x = 0; x < kD / 64; ++x)
+                    tma_load_4d(ring + s * kBlock + x * kHalfBlock, qd == 0 ? &bp.q_half.m[g] : &bp.dout_half.m[g], x * 64, h, i0,
+                                int(b), full0 + 8 * s);
+            }
+        }
+        if (any) drain_phase(kv_full, 0);
+        for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
+            drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
+    } else if (warp == 9 && lane == 0) {
+        constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kQueries, false);
+        constexpr uint32_t kIdescD = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
+        auto landed = [&](uint32_t k) { return wait_for(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag); };
+        auto stage = [&](uint32_t k) { return ring + (k % kStages) * kBlock; };
+        auto transposed = [&](int n) {  // S and dP of block n
+            if (!landed(2 * n) || !landed(2 * n + 1)) return false;
+            tc_fence_after();
+            const uint32_t d = tmem + (n & 1) * 2 * kQueries;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (uint32_t kk = 0; kk < kD / 16; ++kk)
+                    tc_mma(d + x * kQueries, sw128_desc((x ? v_smem : k_smem) + kk / 4 * kHalfTile + kk % 4 * 32),
+                           sw128_desc(stage(2 * n + x) + kk / 4 * kHalfBlock + kk % 4 * 32), kIdescS, kk != 0);
+            }
+            tc_commit(s_full0 + 8 * (n & 1));
+            return true;
+        };
+        bool more = it.next() >= 0;
+        bool ok = !more || (wait_for(kv_full, 0, abort_flag) && transposed(0));
+        for (int n = 0; ok && more; ++n) {
+            more = it.next() >= 0;
+            if (more && !(ok = transposed(n + 1))) break;
+            if (!(ok = wait_for(dx_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t a = tmem + (n & 1) * 2 * kQueries;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // dV += P dO, dK += dx Q
+#pragma unroll
+                for (uint32_t kk = 0; kk < kQueries / 16; ++kk)
+                    tc_mma_ts(x ? dk_tmem : dv_tmem, a + x * kQueries + kk * 8,
+                              sw128_desc(stage(2 * n + 1 - x) + kk * 2048, kHalfBlock), kIdescD, (uint32_t(n) | kk) != 0);
+            }
+            tc_commit(empty0 + 8 * (2 * n % kStages));
+            tc_commit(empty0 + 8 * ((2 * n + 1) % kStages));
+        }
+        tc_commit(done);
+        drain_phase(done, 0);
+    } else if (warp == 10) {
+        uint32_t n = 0;
+        for (int i0 = it.next(); i0 >= 0; i0 = it.next(), ++n) {
+            if (n >= uint32_t(kStatSlots)) {  // block n - kStatSlots has been computed
+                const bool ok = wait_for(stat_free0 + 8 * (n % kStatSlots), (n / kStatSlots - 1) & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
+            const int64_t stat = (int64_t(b) * p.Hl + kh * p.shared + it.head) * p.Sq;
+            for (int x = int(lane); x < int(kQueries); x += 32) {
+                const int i = i0 + x;
+                QueryStat q{INFINITY, 0.f, 0, -1};  // no such query: weight 0
+                if (i < int(p.Sq)) {
+                    const float lse = p.lse[g][stat + i];
+                    q.lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e - kUp;
+                    q.delta = p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat + i];
+                    q.bound = key_bound(p, b, i);
+                    if (plan) {
+                        q.doc = p.q_docs[int64_t(b) * p.Sq + i];
+                        if (q.doc < 0) q.bound = 0;
+                    }
+                }
+                stats[n % kStatSlots * kQueries + x] = q;
+            }
+            mbar_arrive(stat_full0 + 8 * (n % kStatSlots));
+        }
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const uint32_t t = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+        const int j = row0 + int(r);
+        const bool valid = j < int(p.Sk);
+        const uint32_t lane_base = (quarter * 32u) << 16;
+        const int32_t doc = plan && valid ? p.k_docs[int64_t(b) * p.Sk + j] : -1;
+        const uint32_t s_row = tmem + t * 2 * kQueries + lane_base, dp_row = s_row + kQueries;
+        bool ok = true;
+        uint32_t n = 0;
+        for (int i0 = it.next(); i0 >= 0; i0 = it.next(), ++n) {
+            if ((n & 1u) != t) continue;
+            const uint32_t slot = n % kStatSlots;
+            ok = wait_for(stat_full0 + 8 * slot, (n / kStatSlots) & 1u, abort_flag) &&
+                 wait_for(s_full0 + 8 * t, (n >> 1) & 1u, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const QueryStat* st = stats + slot * kQueries;
+            const float slope = kBias && p.slopes ? p.slopes[g * p.Hl + kh * p.shared + it.head] : 0.f;
+            float s[64], bend[kCap ? 64 : 2];
+            load_row<64>(s_row, s);
+            to_scores<kCap, kBias, 64, 1>(s, bend, p.scale, p.cap, slope, float(i0 + ahead - j));
+#pragma unroll
+            for (int x = 0; x < 64; ++x) s[x] = ex2(s[x] - st[x].lse2);
+            const int qt = i0 / int(kAttnRows);
+            const bool whole = plan ? (__ldg(plan + words + (qt >> 5)) >> (qt & 31)) & 1u
+                                    : i0 + int(kQueries) <= int(p.Sq) && row0 + int(kAttnRows) <= st[0].bound;
+            if (!whole) {  // the same for every thread
+                if (plan) {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) s[x] = st[x].doc == doc && j < st[x].bound ? s[x] : 0.f;
+                    // padding's Q and dO rows may hold anything: clear them for the products with dx and P
+                    if (r < kQueries && st[r].doc < 0) {
+                        for (int qd = 0; qd < 2; ++qd) {
+                            uint4* row = reinterpret_cast<uint4*>(smem + 2 * size_t(kTile) +
+                                                                  ((2 * n + qd) % kStages) * size_t(kBlock) + r * kSwizzleRow);
+                            for (int x = 0; x < kD / 64; ++x)
+                                for (int y = 0; y < 8; ++y) row[x * (kHalfBlock / 16) + y] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_async_shared();
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) s[x] = j < st[x].bound ? s[x] : 0.f;
+                }
+            }
+            float d[64];
+            load_row<64>(dp_row, d);
+            store_row16<kF, 64>(s_row, s);
+#pragma unroll
+            for (int x = 0; x < 64; ++x) {
+                float dx = s[x] == 0.f ? 0.f : s[x] * ((d[x] - st[x].delta) * kDown);
+                if constexpr (kCap) dx *= bend[x];
+                d[x] = dx;
+            }
+            store_row16<kF, 64>(dp_row, d);
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(dx_full0 + 8 * t);
+            mbar_arrive(stat_free0 + 8 * slot);
+        }
+        // n counts every block, of both halves of the warps
+        if (ok) ok = wait_for(done, 0, abort_flag);
+        if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
+            tc_fence_after();
+            const int64_t at = valid ? j : 0;
+            if (t == 0)
+                write_row<kF, kD>(dv_tmem + lane_base, n > 0, valid, kDown,
+                                  p.dv.base[g] + b * p.dv.b + at * p.dv.t + kh * p.dv.h);
+            else
+                write_row<kF, kD>(dk_tmem + lane_base, n > 0, valid, p.scale,
+                                  p.dk.base[g] + b * p.dk.b + at * p.dk.t + kh * p.dk.h);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <Fused kF, int kD, bool kCap, bool kBias>
+cudaError_t launch(const BackwardParams& p, cudaStream_t stream, int* launches) {
+    cudaError_t e;
+    BackwardParams q = p;
+    if (p.a.Sq > 0) {
+        if (p.a.plan) {
+            if ((e = launch_plan(p.a, p.a.plan, false, kAttnRows, stream)) != cudaSuccess) return e;
+            *launches += 1;
+        }
+        auto kernel = dq_kernel<kF, kD, kCap, kBias>;
+        constexpr size_t smem = DqShape<kD>::kSmem;
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) != cudaSuccess) return e;
+        e = launch_overlapped(kernel, p.q_tiles * p.a.P * p.a.B * p.a.Hl, kThreadsB, smem, stream, p);
+        if (e != cudaSuccess) return e;
         *launches += 1;
     }
-    return cudaGetLastError();
+    if (p.a.Sk > 0) {
+        if (p.a.plan) {
+            q.a.plan = p.key_plan;
+            if ((e = launch_plan(q.a, q.a.plan, true, kAttnRows, stream)) != cudaSuccess) return e;
+            *launches += 1;
+        }
+        auto kernel = dkv_kernel<kF, kD, kCap, kBias>;
+        constexpr size_t smem = DkvShape<kD>::kSmem;
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) != cudaSuccess) return e;
+        e = launch_overlapped(kernel, p.k_tiles * p.a.P * p.a.B * p.a.Hkl, kThreadsB, smem, stream, q);
+        if (e != cudaSuccess) return e;
+        *launches += 1;
+    }
+    return cudaSuccess;
+}
+
+template <Fused kF, int kD>
+cudaError_t launch_scored(const BackwardParams& p, cudaStream_t stream, int* launches) {
+    if (p.a.cap != 0.f)
+        return p.a.slopes ? launch<kF, kD, true, true>(p, stream, launches) : launch<kF, kD, true, false>(p, stream, launches);
+    return p.a.slopes ? launch<kF, kD, false, true>(p, stream, launches) : launch<kF, kD, false, false>(p, stream, launches);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_backward(const AttentionParams& p, bool bf16, cudaStream_t stream, int* launches) {
+cudaError_t launch_attention_backward(const BackwardParams& p, bool bf16, cudaStream_t stream, int* launches) {
     *launches = 0;
-    if (p.D == 64)
-        return bf16 ? launch<Fused::kBF16, 64>(p, stream, launches) : launch<Fused::kFP16, 64>(p, stream, launches);
-    return bf16 ? launch<Fused::kBF16, 128>(p, stream, launches) : launch<Fused::kFP16, 128>(p, stream, launches);
+    if (p.a.D == 64)
+        return bf16 ? launch_scored<Fused::kBF16, 64>(p, stream, launches) : launch_scored<Fused::kFP16, 64>(p, stream, launches);
+    return bf16 ? launch_scored<Fused::kBF16, 128>(p, stream, launches) : launch_scored<Fused::kFP16, 128>(p, stream, launches);
+}
+
+cudaError_t read_attention_backward_status(unsigned* out, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_attention_backward_status, sizeof(unsigned));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attention_backward_status, &zero, sizeof(unsigned));
 }
 
 }  // namespace tfu

@@ -727,14 +727,14 @@ bool encode_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t cols, uin
 }
 
 bool encode_group_maps(GroupMaps* maps, const GroupView& v, uint32_t P, uint32_t B, uint32_t tokens, uint32_t heads,
-                       uint32_t D, bool bf16) {
+                       uint32_t D, uint32_t box_tokens, bool bf16) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     // a stride of an extent-1 dimension is never used; give the driver a valid one
     const cuuint64_t gdim[4] = {D, heads, tokens, B};
     const cuuint64_t gstride[3] = {heads > 1 ? cuuint64_t(v.h) : D * 2, tokens > 1 ? cuuint64_t(v.t) : D * 2,
                                    B > 1 ? cuuint64_t(v.b) : D * 2};
-    const cuuint32_t box[4] = {64, 1, kAttnRows, 1};
+    const cuuint32_t box[4] = {64, 1, box_tokens, 1};
     const cuuint32_t estride[4] = {1, 1, 1, 1};
     for (uint32_t g = 0; g < P; ++g)
         if (enc(&maps->m[g], bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, v.base[g],

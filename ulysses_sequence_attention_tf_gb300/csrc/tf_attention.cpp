@@ -70,10 +70,21 @@ void describe(const tf_attention& a, tfu::AttentionParams* p) {
     p->causal = uint32_t(a.causal);
 }
 
-size_t workspace_bytes_of(const tf_attention& a, bool backward) {
-    if (backward) return size_t(a.B) * size_t(a.H) * size_t(a.Sq) * sizeof(float);
-    return a.q_docs ? tfu::tile_plan(uint32_t(a.Sq), tfu::kAttnPair, uint32_t(a.Sk)).bytes(uint32_t(a.B)) : 0;
-}
+// Parts of the workspace, in order, each a multiple of 16 bytes.
+struct Workspace {
+    size_t delta = 0, plan = 0, key_plan = 0;  // bytes
+    Workspace(const tf_attention& a, bool backward) {
+        auto up = [](size_t n) { return (n + 15) / 16 * 16; };
+        const uint32_t B = uint32_t(a.B), Sq = uint32_t(a.Sq), Sk = uint32_t(a.Sk);
+        const bool docs = a.q_docs && Sq > 0 && Sk > 0;
+        if (backward) delta = up(size_t(B) * size_t(a.H) * Sq * sizeof(float));
+        if (docs) plan = up(tfu::tile_plan(Sq, backward ? tfu::kAttnRows : tfu::kAttnPair, Sk).bytes(B));
+        if (docs && backward) key_plan = up(tfu::tile_plan(Sk, tfu::kAttnRows, Sq).bytes(B));
+    }
+    size_t bytes() const { return delta + plan + key_plan; }
+};
+
+size_t workspace_bytes_of(const tf_attention& a, bool backward) { return Workspace(a, backward).bytes(); }
 
 tf_status check_workspace(const tf_attention& a, bool backward, const void* workspace, size_t bytes) {
     const size_t need = workspace_bytes_of(a, backward);
@@ -122,11 +133,11 @@ TF_API tf_status tf_ulysses_attention(const tf_attention* a, const void* const* 
     if (empty) return TF_OK;
     describe(*a, &p);
     const bool bf16 = a->dtype == TF_BF16;
-    if (!tfu::encode_group_maps(&fp.q, p.q, p.P, p.B, p.Sq, p.Hl, p.D, bf16) ||
-        (a->Sk > 0 && (!tfu::encode_group_maps(&fp.k, p.k, p.P, p.B, p.Sk, p.Hkl, p.D, bf16) ||
-                       !tfu::encode_group_maps(&fp.v, p.v, p.P, p.B, p.Sk, p.Hkl, p.D, bf16))))
+    if (!tfu::encode_group_maps(&fp.q, p.q, p.P, p.B, p.Sq, p.Hl, p.D, tfu::kAttnRows, bf16) ||
+        (a->Sk > 0 && (!tfu::encode_group_maps(&fp.k, p.k, p.P, p.B, p.Sk, p.Hkl, p.D, tfu::kAttnRows, bf16) ||
+                       !tfu::encode_group_maps(&fp.v, p.v, p.P, p.B, p.Sk, p.Hkl, p.D, tfu::kAttnRows, bf16))))
         return fail(TF_ERR_UNSUPPORTED, "the driver refused a tensor map of q, k or v");
-    p.plan = a->q_docs && a->Sk > 0 ? static_cast<uint32_t*>(workspace) : nullptr;
+    p.plan = Workspace(*a, false).plan > 0 ? static_cast<uint32_t*>(workspace) : nullptr;
     fp.q_tiles = (p.Sq + tfu::kAttnPair - 1) / tfu::kAttnPair;
     int launches = 0;
     const cudaError_t e = tfu::launch_attention(fp, bf16, static_cast<cudaStream_t>(stream), &launches);
@@ -144,7 +155,9 @@ TF_API tf_status tf_ulysses_attention_backward(const tf_attention* a, const void
     tf_status s = check_attention(a);
     if (s != TF_OK) return s;
     if (!strides) return fail(TF_ERR_INVALID, "strides is NULL");
-    tfu::AttentionParams p{};
+    tfu::BackwardParams bp;  // tensor maps of absent groups stay unset
+    bp.a = tfu::AttentionParams{};
+    tfu::AttentionParams& p = bp.a;
     if ((s = view("dout", dout, &strides[0], *a, a->Sq, a->H, false, &p.dout)) != TF_OK) return s;
     if ((s = view("q", q, &strides[1], *a, a->Sq, a->H, false, &p.q)) != TF_OK) return s;
     if ((s = view("k", k, &strides[2], *a, a->Sk, a->Hkv, false, &p.k)) != TF_OK) return s;
@@ -164,9 +177,26 @@ TF_API tf_status tf_ulysses_attention_backward(const tf_attention* a, const void
     if ((s = current_device(&device)) != TF_OK) return s;
     if (a->B == 0 || (a->Sq == 0 && a->Sk == 0)) return TF_OK;
     describe(*a, &p);
-    p.delta = static_cast<float*>(workspace);
+    const bool bf16 = a->dtype == TF_BF16;
+    auto query_maps = [&](tfu::GroupMaps* m, const tfu::GroupView& v, uint32_t box) {
+        return a->Sq == 0 || tfu::encode_group_maps(m, v, p.P, p.B, p.Sq, p.Hl, p.D, box, bf16);
+    };
+    auto key_maps = [&](tfu::GroupMaps* m, const tfu::GroupView& v) {
+        return a->Sk == 0 || tfu::encode_group_maps(m, v, p.P, p.B, p.Sk, p.Hkl, p.D, tfu::kAttnRows, bf16);
+    };
+    if (!query_maps(&bp.q, p.q, tfu::kAttnRows) || !query_maps(&bp.dout, p.dout, tfu::kAttnRows) ||
+        !query_maps(&bp.q_half, p.q, tfu::kAttnRows / 2) || !query_maps(&bp.dout_half, p.dout, tfu::kAttnRows / 2) ||
+        !key_maps(&bp.k, p.k) || !key_maps(&bp.v, p.v))
+        return fail(TF_ERR_UNSUPPORTED, "the driver refused a tensor map of dout, q, k or v");
+    const Workspace ws(*a, true);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    p.delta = reinterpret_cast<float*>(at);
+    p.plan = ws.plan > 0 ? reinterpret_cast<uint32_t*>(at + ws.delta) : nullptr;
+    bp.key_plan = ws.plan > 0 ? reinterpret_cast<uint32_t*>(at + ws.delta + ws.plan) : nullptr;
+    bp.q_tiles = (p.Sq + tfu::kAttnRows - 1) / tfu::kAttnRows;
+    bp.k_tiles = (p.Sk + tfu::kAttnRows - 1) / tfu::kAttnRows;
     int launches = 0;
-    const cudaError_t e = tfu::launch_attention_backward(p, a->dtype == TF_BF16, static_cast<cudaStream_t>(stream), &launches);
+    const cudaError_t e = tfu::launch_attention_backward(bp, bf16, static_cast<cudaStream_t>(stream), &launches);
     count_launches(launches);
     if (e != cudaSuccess) return cuda_fail(e, "launching the attention's gradient kernels");
     return TF_OK;

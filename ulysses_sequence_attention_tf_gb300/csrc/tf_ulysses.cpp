@@ -1162,10 +1162,12 @@ TF_API tf_status tf_ulysses_device_status(int clear, unsigned* status) {
     if (e == cudaSuccess) e = tfu::read_block_status_v16(&block16, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_append_status(&append, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_attend_status(&attend, clear != 0);
+    unsigned gradient = 0;
     if (e == cudaSuccess) e = tfu::read_attention_status(&attention, clear != 0);
+    if (e == cudaSuccess) e = tfu::read_attention_backward_status(&gradient, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device status words");
     *status = (staged ? 1u : 0u) | (gemm ? 2u : 0u) | ((block | block16) ? 4u : 0u) | ((append | attend) ? 8u : 0u) |
-              (attention ? 16u : 0u);
+              ((attention | gradient) ? 16u : 0u);
     return TF_OK;
 }
 
