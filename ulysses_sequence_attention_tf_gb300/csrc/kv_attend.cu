@@ -1,11 +1,24 @@
 // kv_attend.cu -- attention of each sequence's newest tokens over the paged 8-bit cache.
 //
-// The scores and the softmax are those of attention_forward.cu with K = code * scale
-// and V = code * scale of the page's head; key j of a sequence is in page j / page_size of
-// its table row.
+// The scores and the softmax are those of attention_common.cuh with K = code * scale and
+// V = code * scale of the page's head; key j of a sequence is in page j / page_size of its
+// table row.  Few rows (tokens times shared heads) for each key: the bound is
+// reading the codes once, 2 D bytes a key and head.
+//
+// kv_decode_kernel: a CTA of 4 warps takes 16 rows of one key head and a chunk of the
+// keys; each warp walks its own part in steps of 16 keys and the warps join at the end.
+// Codes go from memory straight into registers in the layout of mma.m16n8k16 -- the order
+// of the summed dimensions is free, so lane (g, t) takes 16 consecutive bytes of key g for
+// Q K^T, and of keys 2t, 2t+1, 2t+8, 2t+9 for P V, where bytes of two keys are paired by a
+// permute -- and become fp16 exactly (e4m3 fits); no shared memory is passed.
+//  * Q in fp16 times a power of two for each row that puts its largest value at 2^14: exact
+//    but for values 2^28 below it; the factor goes into the score's scale.
+//  * P in fp16 times the page's V scale relative to the largest one so far (O is rescaled
+//    when that grows), so O sums codes times weights of at most 2^8.
+//  * The reference m of a row follows its maximum when that outgrows it by 2^8.
 #include <cuda_fp8.h>
 
-#include "device_common.cuh"
+#include "attention_common.cuh"
 #include "kv_cache.h"
 
 namespace tfu {
@@ -16,119 +29,417 @@ namespace {
 
 using namespace dev;
 
-constexpr int kRowThreads = 128;
-constexpr int kKeys = 16;  // keys of a block: a page is a whole number of blocks
+constexpr int kWarps = 4;
+constexpr int kStep = 16;      // keys of a warp's step; a page is a whole number of steps
+constexpr float kSlack = 8.0f; // growth of the maximum that m lets pass, in powers of two
 
-__device__ __forceinline__ float from_e4m3(uint8_t v) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(v)));
-    return __half2float(__ushort_as_half(uint16_t(h)));
-}
-
-template <Fused kF>
-__device__ __forceinline__ float to_float(uint16_t v) {
-    float lo, hi;
-    unpack2<kF>(uint32_t(v), lo, hi);
-    return lo;
-}
-
-// A row is a (token, query head) pair of one sequence and key head; kLanes = D / 32 lanes share it.
-template <Fused kF, int kD>
-__global__ void __launch_bounds__(kRowThreads) kv_attend_kernel(const __grid_constant__ KvAttendParams p) {
-    constexpr int kLanes = kD / 32, kRows = kRowThreads / kLanes;
-    __shared__ float ks[kKeys][kD], vs[kKeys][kD];
+// What a CTA needs of its sequence; ok = false: nothing to do (flagged if out of range).
+struct Sequence {
+    int64_t s0;
+    int tokens, len, chunks;
+    bool ok;
+};
+__device__ __forceinline__ Sequence sequence_of(const KvAttendParams& p, uint32_t n) {
     const KvCache& c = p.c;
-    const uint32_t part = threadIdx.x % kLanes;
-    const uint32_t kh = blockIdx.y, n = blockIdx.z;
-    const int64_t s0 = c.starts[n], s1 = c.starts[n + 1], len = c.lens[n];
-    const int64_t tokens = s1 - s0;
+    const int64_t s0 = c.starts[n], s1 = c.starts[n + 1], len = c.lens[n], tokens = s1 - s0;
+    Sequence s{s0, int(tokens), int(len), 0, false};
     if (s0 < 0 || tokens < 0 || s1 > int64_t(p.T) || len < tokens || len > int64_t(p.max_len) || tokens > int64_t(p.max_tokens)) {
         if (threadIdx.x == 0) atomicOr(&g_kv_attend_status, 1u);
-        return;
+        return s;
     }
-    const int64_t r = int64_t(blockIdx.x) * kRows + threadIdx.x / kLanes;
-    if (int64_t(blockIdx.x) * kRows >= tokens * p.shared) return;
-    const bool valid = r < tokens * p.shared;
-    const int64_t token = valid ? r / p.shared : 0;
-    const uint32_t head = kh * p.shared + uint32_t(valid ? r % p.shared : 0);  // over all groups
-    const uint32_t g = head / p.Hl, h = head % p.Hl;
-    float q[32], o[32];
-    const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.q.base[g] + (s0 + token) * p.q.t + h * p.q.h);
+    s.ok = tokens > 0;
+    s.chunks = int((uint32_t(len) + p.chunk - 1) / p.chunk);
+    return s;
+}
+
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t e4m3_pair) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(e4m3_pair)));
+    return h;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+// The codes of one step in flight.
+template <int kD>
+struct Codes {
+    uint32_t k[2][kD / 16];  // keys g and g + 8: kD / 64 pieces of 16 bytes
+    uint32_t v[4][kD / 32];  // keys 2t, 2t + 1, 2t + 8, 2t + 9: kD / 8 bytes from dim g * kD / 8
+    float ks, vs;
+    int keys;                // visible ones of the step
+};
+
+template <Fused kF, int kD>
+__global__ void __launch_bounds__(kWarps * 32, 2) kv_decode_kernel(const __grid_constant__ KvAttendParams p) {
+    constexpr int kSteps = kD / 16;   // k-steps of Q K^T
+    constexpr int kTilesO = kD / 8;   // column tiles of O
+    __shared__ float o_all[kWarps][kDecodeRows][kD + 4];
+    __shared__ float m_all[kWarps][kDecodeRows], l_all[kWarps][kDecodeRows];
+    grid_dependency_wait();
+    const KvCache& c = p.c;
+    const uint32_t n = blockIdx.z, row_tiles = gridDim.y / c.Hkv, kh = blockIdx.y / row_tiles;
+    const uint32_t row0 = blockIdx.y % row_tiles * kDecodeRows;
+    const Sequence seq = sequence_of(p, n);
+    if (!seq.ok || int(blockIdx.x) >= seq.chunks) return;
+    const uint32_t rows = uint32_t(seq.tokens) * p.shared;
+    if (row0 >= rows) return;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+
+    // this lane's rows g and g + 8: Q in fragments, bounds, factors
+    uint32_t qf[kSteps][4];
+    float factor[2], slope[2];
+    int bound[2], pos[2];
 #pragma unroll
-    for (int d = 0; d < 32; ++d) {
-        q[d] = valid ? to_float<kF>(qp[part * 32 + d]) : 0.f;
-        o[d] = 0.f;
+    for (int x = 0; x < 2; ++x) {
+        const uint32_t r = row0 + g + 8 * x;
+        const bool in = r < rows;
+        const uint32_t token = in ? r / p.shared : 0, head = kh * p.shared + (in ? r % p.shared : 0);
+        pos[x] = seq.len - seq.tokens + int(token);
+        bound[x] = !in ? 0 : p.causal ? pos[x] + 1 : seq.len;
+        slope[x] = p.slopes ? p.slopes[head] * kLog2e : 0.f;
+        const uint8_t* src = p.q.base[head / p.Hl] + (seq.s0 + token) * p.q.t + int64_t(head % p.Hl) * p.q.h;
+        float f[kSteps][4], most = 0.f;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const uint2 w = in ? *reinterpret_cast<const uint2*>(src + 2 * (s / 4 * 64 + t * 16 + s % 4 * 4)) : make_uint2(0, 0);
+            unpack2<kF>(w.x, f[s][0], f[s][1]);
+            unpack2<kF>(w.y, f[s][2], f[s][3]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) most = fmaxf(most, fabsf(f[s][y]));
+        }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        int e = 14 - (int(__float_as_uint(most) >> 23) - 127);  // most * 2^e in [2^14, 2^15)
+        e = most == 0.f || !(most <= kFltMax) ? 0 : min(e, 100);
+        const float up = __uint_as_float(uint32_t(e + 127) << 23);
+        factor[x] = p.scale / up;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            qf[s][x] = pack2<Fused::kFP16>(f[s][0] * up, f[s][1] * up);
+            qf[s][2 + x] = pack2<Fused::kFP16>(f[s][2] * up, f[s][3] * up);
+        }
     }
-    const int64_t pos = len - tokens + token;
-    const int64_t bound = !valid ? 0 : p.causal ? pos + 1 : len;
-    const float slope = p.slopes ? p.slopes[head] : 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int64_t j0 = 0; j0 < len; j0 += kKeys) {
-        if (!__syncthreads_or(j0 < bound)) break;
-        const int64_t id = c.table[n * c.table_stride + j0 / c.page];
-        const bool bad = id < 0 || id >= int64_t(c.pages);
-        if (bad) {
-            if (threadIdx.x == 0) atomicOr(&g_kv_attend_status, 1u);
+
+    const int lo = int(blockIdx.x * p.chunk), hi = min(seq.len, lo + int(p.chunk));
+    const int steps = (hi - lo + kStep - 1) / kStep, per = (steps + kWarps - 1) / kWarps;
+    const int first = lo + int(warp) * per * kStep, last = min(hi, first + per * kStep);
+
+    float o[kTilesO][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, v_ref = 0x1p-126f;
+#pragma unroll
+    for (int s = 0; s < kTilesO; ++s)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[s][y] = 0.f;
+
+    // the pages of 32 steps at a time, one a lane
+    int id_of = 0;
+    float ks_of = 0.f, vs_of = 0.f;
+    auto pages = [&](int j) {
+        const int key = j + int(lane) * kStep;
+        id_of = -1;
+        ks_of = vs_of = 0.f;
+        if (key < last) {
+            const int id = c.table[int64_t(n) * c.table_stride + uint32_t(key) / c.page];
+            if (id >= 0 && uint32_t(id) < c.pages) {
+                id_of = id;
+                ks_of = c.scales[0][int64_t(id) * c.Hkv + kh];
+                vs_of = c.scales[1][int64_t(id) * c.Hkv + kh];
+            } else {
+                atomicOr(&g_kv_attend_status, 1u);
+            }
+        }
+    };
+    auto load = [&](Codes<kD>& d, int j) {  // j - first is a multiple of kStep
+        const int w = (j - first) / kStep % 32;
+        if (w == 0) pages(j);
+        const int id = __shfl_sync(0xffffffffu, id_of, w);
+        d.ks = __shfl_sync(0xffffffffu, ks_of, w);
+        d.vs = __shfl_sync(0xffffffffu, vs_of, w);
+        d.keys = id < 0 ? 0 : min(kStep, last - j);
+        if (id < 0) return;
+        const int64_t at = (int64_t(id) * c.Hkv + kh) * c.page + uint32_t(j) % c.page;
+        const uint8_t* k = c.codes[0] + at * kD;
+        const uint8_t* v = c.codes[1] + at * kD;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < kD / 64; ++y)
+                *reinterpret_cast<uint4*>(&d.k[x][4 * y]) = ld_codes16(k + (g + 8 * x) * kD + y * 64 + t * 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const uint8_t* row = v + (2 * t + x % 2 + x / 2 * 8) * kD + g * (kD / 8);
+            if constexpr (kD == 128)
+                *reinterpret_cast<uint4*>(&d.v[x][0]) = ld_codes16(row);
+            else
+                *reinterpret_cast<uint2*>(&d.v[x][0]) = ld_codes8(row);
+        }
+    };
+    auto step = [&](Codes<kD>& d, int j) {
+        if (d.keys == 0) return;
+        float s[2][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+#pragma unroll
+            for (int y = 0; y < kSteps; ++y) mma_f16(s[x], qf[y], to_f16x2(d.k[x][y]), to_f16x2(d.k[x][y] >> 16));
+        }
+        // s[x][2 * row + e]: key j + 8x + 2t + e
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float f = factor[r] * d.ks;
+            if (p.cap != 0.f) {
+                const float to_x = f / p.cap, to_z = p.cap * kLog2e;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float a = s[x][2 * r] * to_x, b = s[x][2 * r + 1] * to_x;
+                    if (__all_sync(0xffffffffu, fmaxf(fabsf(a), fabsf(b)) <= kTanhNear)) {
+                        const uint64_t y = f2_pack(a, b);
+                        f2_unpack(f2_mul(f2_mul(y, f2_pack(to_z, to_z)), tanh_over_x(f2_mul(y, y))), s[x][2 * r], s[x][2 * r + 1]);
+                    } else {
+                        s[x][2 * r] = to_z * tanh_wide(a);
+                        s[x][2 * r + 1] = to_z * tanh_wide(b);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[x][2 * r + e] *= f * kLog2e;
+            }
+            if (p.slopes) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        s[x][2 * r + e] = fmaf(-slope[r], fabsf(float(pos[r] - (j + 8 * x + 2 * int(t) + e))), s[x][2 * r + e]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int key = j + 8 * x + 2 * int(t) + e;
+                    if (key >= bound[r]) s[x][2 * r + e] = -INFINITY;
+                    top[r] = fmaxf(top[r], s[x][2 * r + e]);
+                }
+        }
+        float shrink[2] = {1.f, 1.f};
+        bool move = d.vs > v_ref;
+        if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                if (top[r] > m[r] + kSlack) {
+                    shrink[r] = ex2(m[r] - top[r]);
+                    m[r] = top[r];
+                    l[r] *= shrink[r];
+                }
+            }
+            move = true;
+        }
+        if (move) {  // the same for the whole warp
+            const float v_new = fmaxf(v_ref, d.vs), down = v_ref / v_new;
+            v_ref = v_new;
+#pragma unroll
+            for (int y = 0; y < kTilesO; ++y) {
+                o[y][0] *= shrink[0] * down, o[y][1] *= shrink[0] * down;
+                o[y][2] *= shrink[1] * down, o[y][3] *= shrink[1] * down;
+            }
+        }
+        const float fv = d.vs / v_ref;
+        uint32_t a[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float e0 = ex2(s[x][2 * r] - base), e1 = ex2(s[x][2 * r + 1] - base);
+                l[r] += e0 + e1;
+                a[2 * x + r] = pack2<Fused::kFP16>(e0 * fv, e1 * fv);
+            }
+        }
+        if (d.keys < kStep) {  // what lies behind the sequence may be anything
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (2 * int(t) + x % 2 + x / 2 * 8 >= d.keys) {
+#pragma unroll
+                    for (int y = 0; y < kD / 32; ++y) d.v[x][y] = 0;
+                }
+        }
+#pragma unroll
+        for (int y = 0; y < kD / 32; ++y) {
+            const uint32_t lo0 = __byte_perm(d.v[0][y], d.v[1][y], 0x5140), hi0 = __byte_perm(d.v[0][y], d.v[1][y], 0x7362);
+            const uint32_t lo1 = __byte_perm(d.v[2][y], d.v[3][y], 0x5140), hi1 = __byte_perm(d.v[2][y], d.v[3][y], 0x7362);
+            mma_f16(o[4 * y], a, to_f16x2(lo0), to_f16x2(lo1));
+            mma_f16(o[4 * y + 1], a, to_f16x2(lo0 >> 16), to_f16x2(lo1 >> 16));
+            mma_f16(o[4 * y + 2], a, to_f16x2(hi0), to_f16x2(hi1));
+            mma_f16(o[4 * y + 3], a, to_f16x2(hi0 >> 16), to_f16x2(hi1 >> 16));
+        }
+    };
+
+    // two steps in flight behind the one that is computed
+    if (first < last) {
+        Codes<kD> d[2];
+        load(d[0], first);
+        for (int j = first; j < last; j += 2 * kStep) {
+            if (j + kStep < last) load(d[1], j + kStep);
+            step(d[0], j);
+            if (j + kStep < last) {
+                if (j + 2 * kStep < last) load(d[0], j + 2 * kStep);
+                step(d[1], j + kStep);
+            }
+        }
+    }
+
+    // join the warps: column 2t + e of O's tile s is dimension (2t + e) * kD / 8 + s
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        const uint32_t row = g + 8 * r;
+        if (t == 0) {
+            m_all[warp][row] = m[r];
+            l_all[warp][row] = l[r];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int s = 0; s < kTilesO; ++s) o_all[warp][row][(2 * t + e) * (kD / 8) + s] = o[s][2 * r + e] * v_ref;
+    }
+    __syncthreads();
+    for (uint32_t x = threadIdx.x; x < kDecodeRows * (kD / 8); x += kWarps * 32) {
+        const uint32_t row = x / (kD / 8), d = x % (kD / 8) * 8, r = row0 + row;
+        if (r >= rows) break;
+        float top = -INFINITY, sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_all[w][row]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            // nothing visible: 0, or the NaN of a row whose scores are
+            const float f = m_all[w][row] == -INFINITY ? 0.f * l_all[w][row] : ex2(m_all[w][row] - top);
+            if (f == 0.f) continue;
+            sum = fmaf(f, l_all[w][row], sum);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) acc[y] = fmaf(f, o_all[w][row][d + y], acc[y]);
+        }
+        if (seq.chunks > 1) {
+            const int64_t at = ((int64_t(n) * c.Hkv + kh) * p.row_cap + r) * p.chunks + blockIdx.x;
+            float4* dst = reinterpret_cast<float4*>(p.part + at * kD + d);
+            dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            if (d == 0) p.part_stat[at] = make_float2(top, sum);
             continue;
         }
-        const int64_t at = (id * c.Hkv + kh) * int64_t(c.page) + j0 % c.page;
-        const float sk = c.scales[0][id * c.Hkv + kh], sv = c.scales[1][id * c.Hkv + kh];
-        for (int x = threadIdx.x; x < kKeys * kD; x += kRowThreads) {
-            const int j = x / kD, d = x % kD;
-            const bool in = j0 + j < len;
-            ks[j][d] = in ? from_e4m3(c.codes[0][(at + j) * kD + d]) * sk : 0.f;
-            vs[j][d] = in ? from_e4m3(c.codes[1][(at + j) * kD + d]) * sv : 0.f;
-        }
-        __syncthreads();
-        float z[kKeys], top = m;
-#pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-            float s = 0.f;
-#pragma unroll
-            for (int d = 0; d < 32; ++d) s = fmaf(q[d], ks[j][part * 32 + d], s);
-#pragma unroll
-            for (int w = 1; w < kLanes; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-            s *= p.scale;
-            if (p.cap != 0.f) s = p.cap * tanhf(s / p.cap);
-            s -= slope * fabsf(float(pos - (j0 + j)));
-            z[j] = j0 + j < bound ? s : -INFINITY;
-            top = fmaxf(top, z[j]);
-        }
-        const float base = top == -INFINITY ? 0.f : top;
-        const float shrink = expf(m - base);
-        l *= shrink;
-#pragma unroll
-        for (int d = 0; d < 32; ++d) o[d] *= shrink;
-#pragma unroll
-        for (int j = 0; j < kKeys; ++j) {
-            if (z[j] == -INFINITY) continue;
-            const float e = expf(z[j] - base);
-            l += e;
-#pragma unroll
-            for (int d = 0; d < 32; ++d) o[d] = fmaf(e, vs[j][part * 32 + d], o[d]);
-        }
-        m = top;
+        const uint32_t token = r / p.shared, head = kh * p.shared + r % p.shared;
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+        uint8_t* dst = p.out.base[head / p.Hl] + (seq.s0 + token) * p.out.t + int64_t(head % p.Hl) * p.out.h + d * 2;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<kF>(acc[0] * inv, acc[1] * inv), pack2<kF>(acc[2] * inv, acc[3] * inv),
+                                                    pack2<kF>(acc[4] * inv, acc[5] * inv), pack2<kF>(acc[6] * inv, acc[7] * inv));
+        float* lse = p.lse[head / p.Hl];
+        if (lse && d == 0) lse[int64_t(head % p.Hl) * p.T + seq.s0 + token] = (top == -INFINITY ? 0.f : top * kLn2) + logf(sum);
     }
-    if (!valid) return;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    uint16_t* op = reinterpret_cast<uint16_t*>(p.out.base[g] + (s0 + token) * p.out.t + h * p.out.h);
+}
+
+// Joins the chunks of a row: a warp a row.
+template <Fused kF, int kD>
+__global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ KvAttendParams p) {
+    grid_dependency_wait();
+    const KvCache& c = p.c;
+    const uint32_t n = blockIdx.z, kh = blockIdx.y, lane = threadIdx.x % 32;
+    const Sequence seq = sequence_of(p, n);
+    const uint32_t r = blockIdx.x * 8 + threadIdx.x / 32;
+    if (!seq.ok || seq.chunks <= 1 || r >= uint32_t(seq.tokens) * p.shared) return;
+    const int64_t at = ((int64_t(n) * c.Hkv + kh) * p.row_cap + r) * p.chunks;
+    float top = -INFINITY;
+    for (int x = int(lane); x < seq.chunks; x += 32) top = fmaxf(top, p.part_stat[at + x].x);
 #pragma unroll
-    for (int d = 0; d < 32; ++d) op[part * 32 + d] = uint16_t(pack2<kF>(o[d] * inv, 0.f) & 0xffffu);
-    if (p.lse[g] && part == 0) p.lse[g][int64_t(h) * p.T + s0 + token] = m + logf(l);
+    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    constexpr int kPer = kD / 32;
+    float sum = 0.f, acc[kPer];
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) acc[y] = 0.f;
+#pragma unroll 4
+    for (int x = 0; x < seq.chunks; ++x) {
+        const float2 s = p.part_stat[at + x];
+        const float f = s.x == -INFINITY ? 0.f * s.y : ex2(s.x - top);
+        const float* src = p.part + (at + x) * kD + lane * kPer;
+        float v[kPer];
+        if constexpr (kPer == 4)
+            *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+        else
+            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+        if (f == 0.f) continue;
+        sum = fmaf(f, s.y, sum);
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) acc[y] = fmaf(f, v[y], acc[y]);
+    }
+    const uint32_t token = r / p.shared, head = kh * p.shared + r % p.shared;
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    uint8_t* dst = p.out.base[head / p.Hl] + (seq.s0 + token) * p.out.t + int64_t(head % p.Hl) * p.out.h + lane * kPer * 2;
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int y = 0; y < kPer / 2; ++y) w[y] = pack2<kF>(acc[2 * y] * inv, acc[2 * y + 1] * inv);
+    if constexpr (kPer == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t*>(dst) = w[0];
+    float* lse = p.lse[head / p.Hl];
+    if (lse && lane == 0) lse[int64_t(head % p.Hl) * p.T + seq.s0 + token] = (top == -INFINITY ? 0.f : top * kLn2) + logf(sum);
+}
+
+template <typename... Args>
+cudaError_t launch_grid(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <Fused kF, int kD>
-cudaError_t launch(const KvAttendParams& p, cudaStream_t stream) {
-    constexpr uint32_t kRows = kRowThreads / (kD / 32);
-    kv_attend_kernel<kF, kD><<<dim3((p.max_tokens * p.shared + kRows - 1) / kRows, p.c.Hkv, p.c.N), kRowThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t launch(const KvAttendParams& p, cudaStream_t stream, int* launches) {
+    const uint32_t rows = p.max_tokens * p.shared;
+    cudaError_t e = launch_grid(kv_decode_kernel<kF, kD>, dim3(p.chunks, p.c.Hkv * (p.row_cap / kDecodeRows), p.c.N), kWarps * 32,
+                                stream, p);
+    if (e != cudaSuccess) return e;
+    *launches += 1;
+    if (p.chunks > 1) {
+        e = launch_grid(kv_join_kernel<kF, kD>, dim3((rows + 7) / 8, p.c.Hkv, p.c.N), 256, stream, p);
+        if (e != cudaSuccess) return e;
+        *launches += 1;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attend(const KvAttendParams& p, bool bf16, cudaStream_t stream) {
-    if (p.c.D == 64) return bf16 ? launch<Fused::kBF16, 64>(p, stream) : launch<Fused::kFP16, 64>(p, stream);
-    return bf16 ? launch<Fused::kBF16, 128>(p, stream) : launch<Fused::kFP16, 128>(p, stream);
+cudaError_t launch_kv_attend(const KvAttendParams& p, bool bf16, cudaStream_t stream, int* launches) {
+    *launches = 0;
+    if (p.c.D == 64)
+        return bf16 ? launch<Fused::kBF16, 64>(p, stream, launches) : launch<Fused::kFP16, 64>(p, stream, launches);
+    return bf16 ? launch<Fused::kBF16, 128>(p, stream, launches) : launch<Fused::kFP16, 128>(p, stream, launches);
 }
 
 cudaError_t read_kv_attend_status(unsigned* out, bool clear) {

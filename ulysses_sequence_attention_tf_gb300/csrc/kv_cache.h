@@ -42,9 +42,17 @@ struct KvAppendParams {
     uint32_t units;        // upper bound of the (sequence, page) pairs that get rows
 };
 
+// Attention over long caches is split along the keys: chunk c of a sequence is keys
+// [c * chunk, (c + 1) * chunk).  A sequence of one chunk is written at once; the
+// others leave sums relative to their own reference, and a second kernel joins them:
+// per (sequence, key head, row, chunk) D unnormalised fp32 values, reference and sum.
 struct KvAttendParams {
     KvCache c;
     RowView q, out;
+    float* part;             // [N][Hkv][row_cap][chunks][D], or null for one chunk
+    float2* part_stat;       // [N][Hkv][row_cap][chunks] (reference in log2 units, sum)
+    uint32_t chunk, chunks;  // keys of a chunk, chunks of the longest sequence
+    uint32_t row_cap;        // rows (token, query head) of a key head, rounded up to row tiles
     float* lse[kMaxShards];  // [Hl][T] per group, or null
     const float* slopes;     // [P * Hl] or null
     float scale, cap;
@@ -53,8 +61,10 @@ struct KvAttendParams {
     uint32_t causal;
 };
 
+constexpr uint32_t kDecodeRows = 16;  // rows of a CTA of the decode kernel
+
 cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, cudaStream_t stream);
-cudaError_t launch_kv_attend(const KvAttendParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_kv_attend(const KvAttendParams& p, bool bf16, cudaStream_t stream, int* launches);
 
 // Status word of the cache kernels: 0, or 1 when a length, a start or a page number
 // of some sequence was out of range and the sequence (or the page) was left out.

@@ -67,6 +67,23 @@ tf_status rows_of(const char* name, const void* const* base, const tf_strides* g
     return TF_OK;
 }
 
+// Split the keys so that about kTargetCtas CTAs have work when every sequence is as
+// long as the longest may be, in chunks of at least kLeastChunk keys (below it the
+// join costs more than the parallel chunks give) and at most kMostChunk (so that one
+// long sequence among many is spread).
+constexpr uint32_t kTargetCtas = 2432, kLeastChunk = 512, kMostChunk = 8192;
+
+void plan_chunks(tfu::KvAttendParams* p) {
+    const uint32_t rows = p->max_tokens * p->shared;
+    p->row_cap = (rows + tfu::kDecodeRows - 1) / tfu::kDecodeRows * tfu::kDecodeRows;
+    const uint64_t ctas = uint64_t(p->c.N) * p->c.Hkv * (p->row_cap / tfu::kDecodeRows);
+    const uint64_t want = ctas ? (kTargetCtas + ctas - 1) / ctas : 1;
+    uint64_t chunk = (p->max_len + want - 1) / want;
+    chunk = chunk < kLeastChunk ? kLeastChunk : chunk > kMostChunk ? kMostChunk : chunk;
+    p->chunk = uint32_t((chunk + 63) / 64 * 64);
+    p->chunks = (p->max_len + p->chunk - 1) / p->chunk;
+}
+
 tf_status check_kv_attention(const tf_kv_cache* c, const tf_kv_attention* a, tfu::KvAttendParams* p) {
     if (!a) return fail(TF_ERR_INVALID, "the attention's description is NULL");
     tf_status s = check_cache(c, a->P, a->T, a->dtype, &p->c);
@@ -93,8 +110,17 @@ tf_status check_kv_attention(const tf_kv_cache* c, const tf_kv_attention* a, tfu
     p->max_tokens = uint32_t(a->max_tokens);
     p->max_len = uint32_t(a->max_len);
     p->causal = uint32_t(a->causal);
+    plan_chunks(p);
+    if (int64_t(c->Hkv) * (p->row_cap / tfu::kDecodeRows) > 65535)
+        return fail(TF_ERR_UNSUPPORTED, "too many rows of one sequence");
     return TF_OK;
 }
+
+// Bytes of the chunks' sums, then of their statistics.
+size_t part_bytes(const tfu::KvAttendParams& p) {
+    return p.chunks > 1 ? size_t(p.c.N) * p.c.Hkv * p.row_cap * p.chunks * p.c.D * sizeof(float) : 0;
+}
+size_t stat_bytes(const tfu::KvAttendParams& p) { return part_bytes(p) / (p.c.D * sizeof(float)) * sizeof(float2); }
 
 }  // namespace
 
@@ -175,7 +201,7 @@ TF_API tf_status tf_ulysses_kv_attend_workspace(const tf_kv_cache* c, const tf_k
     tfu::KvAttendParams p{};
     tf_status s = check_kv_attention(c, a, &p);
     if (s != TF_OK) return s;
-    *bytes = 0;
+    *bytes = part_bytes(p) + stat_bytes(p);
     return TF_OK;
 }
 
@@ -193,12 +219,21 @@ TF_API tf_status tf_ulysses_kv_attend(const tf_kv_cache* c, const tf_kv_attentio
         if (a->T > 0 && !lse[g]) return fail(TF_ERR_INVALID, "lse[%d] is NULL", g);
         p.lse[g] = lse[g];
     }
+    const size_t need = part_bytes(p) + stat_bytes(p);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(TF_ERR_INVALID, "the workspace holds %zu bytes of the %zu needed", workspace ? workspace_bytes : size_t(0), need);
+    if (need > 0 && !aligned16(workspace)) return fail(TF_ERR_ALIGNMENT, "the workspace is not 16-byte aligned");
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;
     if (a->T == 0 || c->N == 0) return TF_OK;
-    const cudaError_t e = tfu::launch_kv_attend(p, a->dtype == TF_BF16, static_cast<cudaStream_t>(stream));
+    if (p.chunks > 1) {
+        p.part = static_cast<float*>(workspace);
+        p.part_stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + part_bytes(p));
+    }
+    int launches = 0;
+    const cudaError_t e = tfu::launch_kv_attend(p, a->dtype == TF_BF16, static_cast<cudaStream_t>(stream), &launches);
+    count_launches(launches);
     if (e != cudaSuccess) return cuda_fail(e, "launching the cache attention");
-    count_launches(1);
     return TF_OK;
 }
 
