@@ -429,8 +429,8 @@ TF_API tf_status tf_ulysses_attention_workspace(const tf_attention *a, int backw
 /*
  * A paged key-value cache of N sequences: what streaming and token-by-token
  * generation keep of earlier chunks.  A page holds page_size consecutive tokens
- * of one sequence for every key head, as e4m3 codes with one fp32 scale for each
- * page and head: K = k code * k_scale, V = v code * v_scale.  Token j of sequence
+ * of one sequence for every key head, as e4m3 codes with one scale for each page and
+ * head, a power of two in fp32: K = k code * k_scale, V = v code * v_scale.  Token j of sequence
  * n is slot j % page_size of page page_table[n][j / page_size].  Heads count over
  * all P groups (group g holds heads [g*Hkv/P, (g+1)*Hkv/P)).
  *

@@ -75,20 +75,6 @@ __device__ __forceinline__ void to_scores(float (&s)[kN], float (&bend)[kCap ? k
     }
 }
 
-template <int kN>
-__device__ __forceinline__ void load_row(uint32_t taddr, float (&v)[kN]) {
-    uint32_t r[kN / 32][32];
-#pragma unroll
-    for (int x = 0; x < kN / 32; ++x) tc_ld32(taddr + x * 32, r[x]);
-    tc_wait_ld();
-#pragma unroll
-    for (int x = 0; x < kN / 32; ++x) {
-        tc_landed(r[x]);
-#pragma unroll
-        for (int y = 0; y < 32; ++y) v[x * 32 + y] = __uint_as_float(r[x][y]);
-    }
-}
-
 // 16-bit pairs of kN values over TMEM columns from taddr
 template <Fused kF, int kN>
 __device__ __forceinline__ void store_row16(uint32_t taddr, const float (&v)[kN]) {

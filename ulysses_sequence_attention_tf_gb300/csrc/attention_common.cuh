@@ -96,5 +96,114 @@ __device__ __forceinline__ void tc_landed(uint32_t (&r)[32]) {
     asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
+// kN columns of this thread's TMEM lane from taddr, as floats
+template <int kN>
+__device__ __forceinline__ void load_row(uint32_t taddr, float (&v)[kN]) {
+    uint32_t r[kN / 32][32];
+#pragma unroll
+    for (int x = 0; x < kN / 32; ++x) tc_ld32(taddr + x * 32, r[x]);
+    tc_wait_ld();
+#pragma unroll
+    for (int x = 0; x < kN / 32; ++x) {
+        tc_landed(r[x]);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) v[x * 32 + y] = __uint_as_float(r[x][y]);
+    }
+}
+
+// Scores beyond scale * q.k: none, the cap, or cap (if any) and bias and any scale.
+enum class Score { kPlain, kCap, kAny };
+
+// z of one row's 128 scores, times log2 e, in place (kCap, kAny).
+template <Score kScore>
+__device__ __forceinline__ void finish_scores(float (&s)[128], float scale, float cap, float slope, float far) {
+    if (kScore == Score::kCap || cap != 0.f) {
+        const float to_x = scale / cap, to_z = cap * kLog2e;
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) most = fmaxf(fmaxf(fabsf(s[i]), fabsf(s[i + 1])), most);
+        if (__all_sync(0xffffffffu, most * fabsf(to_x) <= kTanhNear)) {
+            const uint64_t x2 = f2_pack(to_x, to_x), z2 = f2_pack(to_z, to_z);
+#pragma unroll
+            for (int i = 0; i < 128; i += 2) {
+                const uint64_t x = f2_mul(f2_pack(s[i], s[i + 1]), x2);
+                f2_unpack(f2_mul(f2_mul(x, z2), tanh_over_x(f2_mul(x, x))), s[i], s[i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) s[i] = to_z * tanh_wide(s[i] * to_x);
+        }
+    } else {
+        const float c = scale * kLog2e;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i] *= c;
+    }
+    if (kScore == Score::kAny) {
+        const float m = slope * kLog2e;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i] = fmaf(-m, fabsf(far - float(i)), s[i]);
+    }
+}
+
+constexpr float kSlack = 8.0f;  // growth of a row's maximum that its reference lets pass, in powers of two
+
+// One tile of keys into a row's softmax: s holds 128 scores (z = c * s, -inf where masked),
+// m the reference, l the sum, s_tmem the row's score columns, which take the weights in 16
+// bits, o_row its output columns (they hold something when `started`), which are
+// scaled by `down` and by 2^(m_old - m) when the reference moves.
+template <Fused kF, int kD>
+__device__ __forceinline__ void fold_tile(float (&s)[128], float c, float down, bool started, float& m, float& l,
+                                          uint32_t s_tmem, uint32_t o_row) {
+    float top[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        top[x] = fmaxf(s[x], s[x + 4]);
+#pragma unroll
+        for (int y = x + 8; y < 128; y += 8) top[x] = fmaxf(top[x], fmaxf(s[y], s[y + 4]));
+    }
+    const float most = c * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    const bool grow = most > m + kSlack;  // from -inf: on any visible key
+    if (__any_sync(0xffffffffu, grow || down != 1.0f)) {
+        const float to = grow ? most : m;
+        const float shrink = grow ? ex2(m - to) : 1.0f;
+        l *= shrink;
+        m = to;
+        if (started) {
+            const float f = shrink * down;
+#pragma unroll 1
+            for (int x = 0; x < kD; x += 32) {
+                uint32_t r[32];
+                tc_ld32(o_row + x, r);
+                tc_wait_ld();
+                tc_landed(r);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * f);
+                tc_st32(o_row + x, r);
+            }
+        }
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+    const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        uint32_t w[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+            const int e = x * 32 + 2 * y;
+            float lo, hi;
+            f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, b2), lo, hi);
+            lo = ex2(lo);
+            hi = ex2(hi);
+            sum[y & 1] = f2_add(sum[y & 1], f2_pack(lo, hi));
+            w[y] = pack2<kF>(lo, hi);
+        }
+        tc_st16(s_tmem + x * 16, w);
+    }
+    float a0, a1;
+    f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
+    l += a0 + a1;
+}
+
 }  // namespace dev
 }  // namespace tfu

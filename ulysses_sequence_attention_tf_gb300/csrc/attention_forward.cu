@@ -34,10 +34,6 @@ using namespace dev;
 
 constexpr int kThreadsA = 384;
 constexpr uint32_t kHalfTile = kAttnRows * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
-constexpr float kSlack = 8.0f;                           // growth of the maximum that m lets pass, in powers of two
-
-// Scores beyond scale * q.k: none, the cap, or cap (if any) and bias and any scale.
-enum class Score { kPlain, kCap, kAny };
 
 template <int kD>
 struct Shape {
@@ -45,37 +41,6 @@ struct Shape {
     static constexpr int kStages = kD == 128 ? 5 : 8;
     static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kTile + 512 + 1024;  // tiles, barriers, alignment
 };
-
-// z of one row's 128 scores, times log2 e, in place (kCap, kAny).
-template <Score kScore>
-__device__ __forceinline__ void finish_scores(float (&s)[128], float scale, float cap, float slope, float far) {
-    if (kScore == Score::kCap || cap != 0.f) {
-        const float to_x = scale / cap, to_z = cap * kLog2e;
-        float most = 0.f;
-#pragma unroll
-        for (int i = 0; i < 128; i += 2) most = fmaxf(fmaxf(fabsf(s[i]), fabsf(s[i + 1])), most);
-        if (__all_sync(0xffffffffu, most * fabsf(to_x) <= kTanhNear)) {
-            const uint64_t x2 = f2_pack(to_x, to_x), z2 = f2_pack(to_z, to_z);
-#pragma unroll
-            for (int i = 0; i < 128; i += 2) {
-                const uint64_t x = f2_mul(f2_pack(s[i], s[i + 1]), x2);
-                f2_unpack(f2_mul(f2_mul(x, z2), tanh_over_x(f2_mul(x, x))), s[i], s[i + 1]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = to_z * tanh_wide(s[i] * to_x);
-        }
-    } else {
-        const float c = scale * kLog2e;
-#pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] *= c;
-    }
-    if (kScore == Score::kAny) {
-        const float m = slope * kLog2e;
-#pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] = fmaf(-m, fabsf(far - float(i)), s[i]);
-    }
-}
 
 template <Fused kF, int kD, Score kScore>
 __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_constant__ ForwardParams fp) {
@@ -246,18 +211,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
             }
             tc_fence_after();
             float s[128];
-            {
-                uint32_t r[4][32];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) tc_ld32(s_tmem + x * 32, r[x]);
-                tc_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    tc_landed(r[x]);
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) s[x * 32 + y] = __uint_as_float(r[x][y]);
-                }
-            }
+            load_row<128>(s_tmem, s);
             const int j0 = j * int(kAttnRows);
             if (kScore != Score::kPlain)
                 finish_scores<kScore>(s, p.scale, p.cap, slope, float(i + (int(p.Sk) - int(p.Sq)) - j0));
@@ -298,54 +252,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
                     for (int x = 0; x < 128; ++x) s[x] = j0 + x < bound ? s[x] : -INFINITY;
                 }
             }
-            float top[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                top[x] = fmaxf(s[x], s[x + 4]);
-#pragma unroll
-                for (int y = x + 8; y < 128; y += 8) top[x] = fmaxf(top[x], fmaxf(s[y], s[y + 4]));
-            }
-            const float most = c * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            const bool grow = most > m + kSlack;  // from -inf: on any visible key
-            if (__any_sync(0xffffffffu, grow)) {
-                const float to = grow ? most : m;
-                const float shrink = grow ? ex2(m - to) : 1.0f;
-                l *= shrink;
-                m = to;
-                if (n > 0) {
-#pragma unroll 1
-                    for (int x = 0; x < kD; x += 32) {
-                        uint32_t r[32];
-                        tc_ld32(o_row + x, r);
-                        tc_wait_ld();
-                        tc_landed(r);
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * shrink);
-                        tc_st32(o_row + x, r);
-                    }
-                }
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t w[16];
-#pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    const int e = x * 32 + 2 * y;
-                    float lo, hi;
-                    f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, b2), lo, hi);
-                    lo = ex2(lo);
-                    hi = ex2(hi);
-                    sum[y & 1] = f2_add(sum[y & 1], f2_pack(lo, hi));
-                    w[y] = pack2<kF>(lo, hi);
-                }
-                tc_st16(s_tmem + x * 16, w);
-            }
-            float a0, a1;
-            f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
-            l += a0 + a1;
+            fold_tile<kF, kD>(s, c, 1.0f, n > 0, m, l, s_tmem, o_row);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(p_full0 + 8 * t);
@@ -406,7 +313,7 @@ cudaError_t launch(const ForwardParams& p, cudaStream_t stream) {
 
 template <Fused kF, int kD>
 cudaError_t launch_scored(const ForwardParams& p, cudaStream_t stream) {
-    if (p.a.slopes || !(p.a.scale > 0.f)) return launch<kF, kD, Score::kAny>(p, stream);
+    if (p.a.slopes || !(p.a.scale >= 0x1p-120f)) return launch<kF, kD, Score::kAny>(p, stream);
     return p.a.cap != 0.f ? launch<kF, kD, Score::kCap>(p, stream) : launch<kF, kD, Score::kPlain>(p, stream);
 }
 

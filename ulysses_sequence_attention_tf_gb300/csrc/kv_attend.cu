@@ -16,10 +16,7 @@
 //  * P in fp16 times the page's V scale relative to the largest one so far (O is rescaled
 //    when that grows), so O sums codes times weights of at most 2^8.
 //  * The reference m of a row follows its maximum when that outgrows it by 2^8.
-#include <cuda_fp8.h>
-
-#include "attention_common.cuh"
-#include "kv_cache.h"
+#include "kv_common.cuh"
 
 namespace tfu {
 
@@ -31,32 +28,6 @@ using namespace dev;
 
 constexpr int kWarps = 4;
 constexpr int kStep = 16;      // keys of a warp's step; a page is a whole number of steps
-constexpr float kSlack = 8.0f; // growth of the maximum that m lets pass, in powers of two
-
-// What a CTA needs of its sequence; ok = false: nothing to do (flagged if out of range).
-struct Sequence {
-    int64_t s0;
-    int tokens, len, chunks;
-    bool ok;
-};
-__device__ __forceinline__ Sequence sequence_of(const KvAttendParams& p, uint32_t n) {
-    const KvCache& c = p.c;
-    const int64_t s0 = c.starts[n], s1 = c.starts[n + 1], len = c.lens[n], tokens = s1 - s0;
-    Sequence s{s0, int(tokens), int(len), 0, false};
-    if (s0 < 0 || tokens < 0 || s1 > int64_t(p.T) || len < tokens || len > int64_t(p.max_len) || tokens > int64_t(p.max_tokens)) {
-        if (threadIdx.x == 0) atomicOr(&g_kv_attend_status, 1u);
-        return s;
-    }
-    s.ok = tokens > 0;
-    s.chunks = int((uint32_t(len) + p.chunk - 1) / p.chunk);
-    return s;
-}
-
-__device__ __forceinline__ uint32_t to_f16x2(uint32_t e4m3_pair) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(e4m3_pair)));
-    return h;
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -64,13 +35,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 __device__ __forceinline__ uint2 ld_codes8(const uint8_t* p) {
     uint2 v;
     asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
@@ -96,7 +60,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_decode_kernel(const __grid_
     const KvCache& c = p.c;
     const uint32_t n = blockIdx.z, row_tiles = gridDim.y / c.Hkv, kh = blockIdx.y / row_tiles;
     const uint32_t row0 = blockIdx.y % row_tiles * kDecodeRows;
-    const Sequence seq = sequence_of(p, n);
+    const Sequence seq = sequence_of(p, n, &g_kv_attend_status);
     if (!seq.ok || int(blockIdx.x) >= seq.chunks) return;
     const uint32_t rows = uint32_t(seq.tokens) * p.shared;
     if (row0 >= rows) return;
@@ -126,9 +90,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_decode_kernel(const __grid_
         }
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        int e = 14 - (int(__float_as_uint(most) >> 23) - 127);  // most * 2^e in [2^14, 2^15)
-        e = most == 0.f || !(most <= kFltMax) ? 0 : min(e, 100);
-        const float up = __uint_as_float(uint32_t(e + 127) << 23);
+        const float up = f16_factor(most);
         factor[x] = p.scale / up;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
@@ -363,7 +325,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
     grid_dependency_wait();
     const KvCache& c = p.c;
     const uint32_t n = blockIdx.z, kh = blockIdx.y, lane = threadIdx.x % 32;
-    const Sequence seq = sequence_of(p, n);
+    const Sequence seq = sequence_of(p, n, &g_kv_attend_status);
     const uint32_t r = blockIdx.x * 8 + threadIdx.x / 32;
     if (!seq.ok || seq.chunks <= 1 || r >= uint32_t(seq.tokens) * p.shared) return;
     const int64_t at = ((int64_t(n) * c.Hkv + kh) * p.row_cap + r) * p.chunks;
@@ -421,7 +383,8 @@ cudaError_t launch_grid(void (*kernel)(Args...), dim3 grid, int threads, cudaStr
 template <Fused kF, int kD>
 cudaError_t launch(const KvAttendParams& p, cudaStream_t stream, int* launches) {
     const uint32_t rows = p.max_tokens * p.shared;
-    cudaError_t e = launch_grid(kv_decode_kernel<kF, kD>, dim3(p.chunks, p.c.Hkv * (p.row_cap / kDecodeRows), p.c.N), kWarps * 32,
+    cudaError_t e = p.tiles ? launch_kv_tiles(p, kF == Fused::kBF16, stream)
+                            : launch_grid(kv_decode_kernel<kF, kD>, dim3(p.chunks, p.c.Hkv * (p.row_cap / kDecodeRows), p.c.N), kWarps * 32,
                                 stream, p);
     if (e != cudaSuccess) return e;
     *launches += 1;

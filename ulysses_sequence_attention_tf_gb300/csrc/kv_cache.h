@@ -53,6 +53,7 @@ struct KvAttendParams {
     float2* part_stat;       // [N][Hkv][row_cap][chunks] (reference in log2 units, sum)
     uint32_t chunk, chunks;  // keys of a chunk, chunks of the longest sequence
     uint32_t row_cap;        // rows (token, query head) of a key head, rounded up to row tiles
+    bool tiles;              // many rows: kv_attend_tiles.cu
     float* lse[kMaxShards];  // [Hl][T] per group, or null
     const float* slopes;     // [P * Hl] or null
     float scale, cap;
@@ -62,13 +63,18 @@ struct KvAttendParams {
 };
 
 constexpr uint32_t kDecodeRows = 16;  // rows of a CTA of the decode kernel
+constexpr uint32_t kTileRows = 256;   // of the tile kernel
 
 cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_kv_attend(const KvAttendParams& p, bool bf16, cudaStream_t stream, int* launches);
+
+// the tile kernel alone (kv_attend_tiles.cu)
+cudaError_t launch_kv_tiles(const KvAttendParams& p, bool bf16, cudaStream_t stream);
 
 // Status word of the cache kernels: 0, or 1 when a length, a start or a page number
 // of some sequence was out of range and the sequence (or the page) was left out.
 cudaError_t read_kv_append_status(unsigned* out, bool clear);
 cudaError_t read_kv_attend_status(unsigned* out, bool clear);
+cudaError_t read_kv_tiles_status(unsigned* out, unsigned* waits, bool clear);  // *waits: 1 when a bounded wait gave up
 
 }  // namespace tfu

@@ -67,20 +67,42 @@ tf_status rows_of(const char* name, const void* const* base, const tf_strides* g
     return TF_OK;
 }
 
-// Split the keys so that about kTargetCtas CTAs have work when every sequence is as
-// long as the longest may be, in chunks of at least kLeastChunk keys (below it the
-// join costs more than the parallel chunks give) and at most kMostChunk (so that one
-// long sequence among many is spread).
-constexpr uint32_t kTargetCtas = 2432, kLeastChunk = 512, kMostChunk = 8192;
+// Up to this many rows (new tokens times query heads) of a key head take the decode kernel,
+// which reads each code once for 16 rows; more take the tile kernel, whose cost hardly depends
+// on the rows below 256.
+constexpr uint32_t kDecodeMost = 64;
+constexpr uint32_t kSms = 152;
+
+// How the keys are split.  Decode: about kTargetCtas CTAs when every sequence is as long
+// as the longest may be, in chunks of at least kLeastChunk keys (below it the join costs
+// more than the parallel chunks give) and at most kMostChunk (so that one long sequence
+// among many is spread).  Tiles: one CTA an SM, so the number of chunks that makes the
+// rounds of CTAs fullest, a chunk's fixed cost counted as kChunkCost keys.
+constexpr uint32_t kTargetCtas = 2432, kLeastChunk = 512, kMostChunk = 8192, kChunkCost = 512;
 
 void plan_chunks(tfu::KvAttendParams* p) {
     const uint32_t rows = p->max_tokens * p->shared;
-    p->row_cap = (rows + tfu::kDecodeRows - 1) / tfu::kDecodeRows * tfu::kDecodeRows;
-    const uint64_t ctas = uint64_t(p->c.N) * p->c.Hkv * (p->row_cap / tfu::kDecodeRows);
-    const uint64_t want = ctas ? (kTargetCtas + ctas - 1) / ctas : 1;
-    uint64_t chunk = (p->max_len + want - 1) / want;
-    chunk = chunk < kLeastChunk ? kLeastChunk : chunk > kMostChunk ? kMostChunk : chunk;
-    p->chunk = uint32_t((chunk + 63) / 64 * 64);
+    p->tiles = rows > kDecodeMost;
+    const uint32_t unit = p->tiles ? tfu::kTileRows : tfu::kDecodeRows;
+    p->row_cap = (rows + unit - 1) / unit * unit;
+    const uint64_t ctas = uint64_t(p->c.N) * p->c.Hkv * (p->row_cap / unit);
+    uint64_t chunk;
+    if (p->tiles) {
+        uint64_t best = 1, least = UINT64_MAX;
+        for (uint64_t c = 1; c <= 16 && p->max_len / c >= kLeastChunk; ++c) {
+            const uint64_t cost = (ctas * c + kSms - 1) / kSms * (p->max_len / c + kChunkCost);
+            if (cost < least) {
+                least = cost;
+                best = c;
+            }
+        }
+        chunk = (p->max_len + best - 1) / best;
+    } else {
+        const uint64_t want = ctas ? (kTargetCtas + ctas - 1) / ctas : 1;
+        chunk = (p->max_len + want - 1) / want;
+        chunk = chunk < kLeastChunk ? kLeastChunk : chunk > kMostChunk ? kMostChunk : chunk;
+    }
+    p->chunk = uint32_t((chunk + 127) / 128 * 128);
     p->chunks = (p->max_len + p->chunk - 1) / p->chunk;
 }
 
@@ -97,8 +119,8 @@ tf_status check_kv_attention(const tf_kv_cache* c, const tf_kv_attention* a, tfu
         return fail(TF_ERR_INVALID, "max_tokens=%d outside [1, T=%d]", a->max_tokens, a->T);
     if (a->max_len < 1 || int64_t(a->max_len) > int64_t(c->max_pages) * c->page_size)
         return fail(TF_ERR_INVALID, "max_len=%d outside [1, max_pages * page_size]", a->max_len);
-    if (c->N > 65535 || c->Hkv > 65535 || int64_t(a->max_tokens) * (a->H / c->Hkv) > (int64_t(1) << 30))
-        return fail(TF_ERR_UNSUPPORTED, "more than 65535 sequences or key heads, or 2^30 rows of one key head");
+    if (c->N > 65535 || c->Hkv > 16383 || int64_t(a->max_tokens) * (a->H / c->Hkv) > (int64_t(1) << 30))
+        return fail(TF_ERR_UNSUPPORTED, "more than 65535 sequences or 16383 key heads, or 2^30 rows of one key head");
     p->slopes = a->slopes;
     p->scale = a->scale;
     p->cap = a->softcap;
@@ -111,8 +133,8 @@ tf_status check_kv_attention(const tf_kv_cache* c, const tf_kv_attention* a, tfu
     p->max_len = uint32_t(a->max_len);
     p->causal = uint32_t(a->causal);
     plan_chunks(p);
-    if (int64_t(c->Hkv) * (p->row_cap / tfu::kDecodeRows) > 65535)
-        return fail(TF_ERR_UNSUPPORTED, "too many rows of one sequence");
+    if (uint64_t(c->N) * c->Hkv * (p->row_cap / tfu::kDecodeRows) * p->chunks >= (uint64_t(1) << 31))
+        return fail(TF_ERR_UNSUPPORTED, "problem exceeds 2^31 work units");
     return TF_OK;
 }
 

@@ -1162,12 +1162,13 @@ TF_API tf_status tf_ulysses_device_status(int clear, unsigned* status) {
     if (e == cudaSuccess) e = tfu::read_block_status_v16(&block16, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_append_status(&append, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_attend_status(&attend, clear != 0);
-    unsigned gradient = 0;
+    unsigned gradient = 0, tiles = 0, tile_waits = 0;
+    if (e == cudaSuccess) e = tfu::read_kv_tiles_status(&tiles, &tile_waits, clear != 0);
     if (e == cudaSuccess) e = tfu::read_attention_status(&attention, clear != 0);
     if (e == cudaSuccess) e = tfu::read_attention_backward_status(&gradient, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device status words");
-    *status = (staged ? 1u : 0u) | (gemm ? 2u : 0u) | ((block | block16) ? 4u : 0u) | ((append | attend) ? 8u : 0u) |
-              ((attention | gradient) ? 16u : 0u);
+    *status = (staged ? 1u : 0u) | (gemm ? 2u : 0u) | ((block | block16) ? 4u : 0u) | ((append | attend | tiles) ? 8u : 0u) |
+              ((attention | gradient | tile_waits) ? 16u : 0u);
     return TF_OK;
 }
 
