@@ -10,7 +10,6 @@ Names follow the C ABI: ``scatter_qkv`` / ``scatter_qkv_into`` / ``gather_out``
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -441,72 +440,101 @@ def gather_out(tag, attn, out=None, *, stream=None):
     return [_wrap(res.q[r], (B, Sl, H, D), attn[0].dtype, attn[0].device) for r in range(P)], res.done
 
 
-# ---------------------------------------------------------------- attention
-def _allocating_on(stream):
-    """Context in which torch allocates for ``stream``: memory that the call's kernels
-    use on that stream returns to the allocator in that stream's order."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+# ---------------------------------------------------------------- attention and key-value cache
+# These calls are short on the GPU, so their checks take one pass over the tensors.
+class _OnStream:
+    """The stream of a call: torch allocates for it inside the context, so that memory which the call's kernels
+    use returns to the allocator in that stream's order."""
+
+    def __init__(self, stream):
+        self.device = torch._C._cuda_getDevice()
+        self.guard = None
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(self.device)
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream))
+            self.guard = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *error):
+        if self.guard is not None:
+            self.guard.__exit__(*error)
 
 
-def _on_current_device(*tensors):
-    device = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and (t.device.type != "cuda" or t.device.index != device):
-            raise ValueError(f"every tensor must be on the current device cuda:{device}, not {t.device}")
+def _views(name, ts, P, shape, dtype, device):
+    """(pointer array, strides) of P views of this shape, type and device with equal strides, the last one 1."""
+    if len(ts) != P:
+        raise ValueError(f"{name} must be a list of {P} head groups")
+    s = ts[0].stride()
+    ptrs = (ctypes.c_void_p * P)()
+    for i, t in enumerate(ts):
+        if t.shape != shape or t.dtype != dtype or t.stride() != s:
+            raise ValueError(f"{name} must be {dtype} views of shape {tuple(shape)} with the same strides, not {t.dtype} "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on the current device cuda:{device}, not {t.device}")
+        ptrs[i] = t.data_ptr()
+    if s[-1] != 1 and shape[-1] > 1:
+        raise ValueError("the D dimension must have stride 1")
+    return ptrs, Strides(s[0], s[1], s[2]) if len(s) == 4 else Strides(0, s[0], s[1])
 
 
-def _plain_array(name, t, dtype, shape):
-    """Data pointer of a contiguous tensor of this type and shape, or None."""
+def _made(P, shape, dtype, device):
+    """P new contiguous tensors of one allocation, and their pointer array."""
+    whole = torch.empty((P, *shape), dtype=dtype, device=device)
+    ts = list(whole.unbind(0))
+    return ts, (ctypes.c_void_p * P)(*[t.data_ptr() for t in ts])
+
+
+def _plain_array(name, t, dtype, shape, device):
+    """Data pointer of a contiguous tensor of this type and shape on the device, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}, not {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _groups(name, ts, shape, dtype):
-    """Strides of P views of this shape and type."""
-    if tuple(ts[0].shape) != tuple(shape) or ts[0].dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} views of shape {tuple(shape)}, not {ts[0].dtype} {tuple(ts[0].shape)}")
-    return _strides_of(ts)
-
-
-def _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs):
-    P = len(q)
-    if not 1 <= P <= MAX_SHARDS or len(k) != P or len(v) != P:
-        raise ValueError(f"q, k and v must be lists of the same P in [1, {MAX_SHARDS}] head groups")
-    if q[0].dim() != 4 or k[0].dim() != 4:
-        raise ValueError("expected 4-d views [B, tokens, heads, D]")
-    B, Sq, Hl, D = q[0].shape
-    Sk, Hkl = k[0].shape[1:3]
-    dtype = q[0].dtype
-    _on_current_device(*q, *k, *v, slopes, prefix, q_docs, k_docs)
-    a = Attention(P, B, Sq, Sk, P * Hl, P * Hkl, D, _dtype_code(dtype), D ** -0.5 if scale is None else float(scale),
-                  float(softcap), 1 if causal else 0, _plain_array("slopes", slopes, torch.float32, (P * Hl,)),
-                  _plain_array("prefix", prefix, torch.int32, (B,)), _plain_array("q_docs", q_docs, torch.int32, (B, Sq)),
-                  _plain_array("k_docs", k_docs, torch.int32, (B, Sk)))
-    strides = (_groups("q", q, q[0].shape, dtype), _groups("k", k, (B, Sk, Hkl, D), dtype),
-               _groups("v", v, (B, Sk, Hkl, D), dtype))
-    return a, strides
-
-
-def _workspace(a, backward):
-    n = ctypes.c_size_t()
-    _check(lib().tf_ulysses_attention_workspace(ctypes.byref(a), backward, ctypes.byref(n)))
-    return torch.empty(n.value, dtype=torch.uint8, device="cuda") if n.value else None
-
-
-def _lse_arrays(lse, P, shape):
-    if lse is None:
-        return None
+def _lse_arrays(lse, P, shape, device):
     if len(lse) != P:
         raise ValueError(f"lse must be a list of {P} tensors")
-    _on_current_device(*lse)
-    return (ctypes.c_void_p * P)(*[_plain_array("lse", t, torch.float32, shape) for t in lse])
+    return (ctypes.c_void_p * P)(*[_plain_array("lse", t, torch.float32, shape, device) for t in lse])
+
+
+def _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs, device):
+    P = len(q)
+    if not 1 <= P <= MAX_SHARDS:
+        raise ValueError(f"q, k and v must be lists of the same P in [1, {MAX_SHARDS}] head groups")
+    q_shape, k_shape, dtype = q[0].shape, k[0].shape, q[0].dtype
+    if len(q_shape) != 4 or len(k_shape) != 4:
+        raise ValueError("expected 4-d views [B, tokens, heads, D]")
+    B, Sq, Hl, D = q_shape
+    Sk, Hkl = k_shape[1], k_shape[2]
+    qs, ks = _views("q", q, P, q_shape, dtype, device), _views("k", k, P, (B, Sk, Hkl, D), dtype, device)
+    vs = _views("v", v, P, k_shape, dtype, device)
+    a = Attention(P, B, Sq, Sk, P * Hl, P * Hkl, D, _dtype_code(dtype), D ** -0.5 if scale is None else scale, softcap,
+                  1 if causal else 0, _plain_array("slopes", slopes, torch.float32, (P * Hl,), device),
+                  _plain_array("prefix", prefix, torch.int32, (B,), device),
+                  _plain_array("q_docs", q_docs, torch.int32, (B, Sq), device),
+                  _plain_array("k_docs", k_docs, torch.int32, (B, Sk), device))
+    return a, qs, ks, vs
+
+
+def _workspace(ask, *args, device):
+    """A tensor of the bytes that the library asks for (None for 0), its address and size."""
+    n = ctypes.c_size_t()
+    _check(ask(*args, ctypes.byref(n)))
+    if n.value == 0:
+        return None, None, 0
+    t = torch.empty(n.value, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), n.value
 
 
 def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=None, causal=False, prefix=None,
@@ -522,22 +550,24 @@ def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=No
     P tensors ``[B, Sq, H/P, D]`` and fp32 ``[B, H/P, Sq]``, 0 and -inf for rows that see
     nothing; both are made here unless given.
     """
-    a, strides = _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs)
-    shape, rows = q[0].shape, (a.B, a.H // a.P, a.Sq)
-    with _allocating_on(stream):
+    L = lib()
+    with _OnStream(stream) as on:
+        device = on.device
+        a, (qp, q_str), (kp, k_str), (vp, v_str) = _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs,
+                                                              device)
+        shape, rows, dtype, P = q[0].shape, (a.B, a.H // a.P, a.Sq), q[0].dtype, a.P
         if out is None:
-            out = [torch.empty(shape, dtype=q[0].dtype, device=q[0].device) for _ in q]
+            (out, op), o_str = _made(P, shape, dtype, q[0].device), None
+        else:
+            op, o_str = _views("out", out, P, shape, dtype, device)
         if lse is None:
-            lse = [torch.empty(rows, dtype=torch.float32, device=q[0].device) for _ in q]
-        if len(out) != a.P:
-            raise ValueError(f"out must be a list of {a.P} tensors")
-        _on_current_device(*out)
-        o_str = _groups("out", out, shape, q[0].dtype)
-        ws = _workspace(a, 0)
-        _check(lib().tf_ulysses_attention(
-            ctypes.byref(a), _ptr_array(q), _ptr_array(k), _ptr_array(v), (Strides * 3)(*strides), _ptr_array(out),
-            ctypes.byref(o_str), _lse_arrays(lse, a.P, rows), ws.data_ptr() if ws is not None else None,
-            ws.numel() if ws is not None else 0, _stream_handle(stream)))
+            lse, lp = _made(P, rows, torch.float32, q[0].device)
+        else:
+            lp = _lse_arrays(lse, P, rows, device)
+        ws, ws_at, ws_size = (None, None, 0) if q_docs is None else _workspace(
+            L.tf_ulysses_attention_workspace, a, 0, device=q[0].device)
+        _check(L.tf_ulysses_attention(a, qp, kp, vp, (Strides * 3)(q_str, k_str, v_str), op, o_str, lp, ws_at, ws_size,
+                                      on.handle))
     return out, lse
 
 
@@ -547,35 +577,31 @@ def attention_backward(dout, q, k, v, out, lse, dq=None, dk=None, dv=None, *, sc
     the same inputs and options and its results ``out`` and ``lse``: lists of P tensors
     shaped like q, k and v, made here unless given.  Shared key heads get the sum over
     their query heads.  The same inputs give the same bits."""
-    a, (q_str, k_str, v_str) = _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs)
-    dtype, P = q[0].dtype, a.P
-    if len(dout) != P or len(out) != P or lse is None:
-        raise ValueError(f"dout, out and lse must be lists of {P} tensors")
-    _on_current_device(*dout, *out)
-    strides = (Strides * 5)(_groups("dout", dout, q[0].shape, dtype), q_str, k_str, v_str,
-                            _groups("out", out, q[0].shape, dtype))
-    with _allocating_on(stream):
-        made = []
-        for grads, like in ((dq, q), (dk, k), (dv, v)):
-            if grads is None:
-                grads = [torch.empty(like[0].shape, dtype=dtype, device=like[0].device) for _ in like]
-            if len(grads) != P:
-                raise ValueError(f"dq, dk and dv must be lists of {P} tensors")
-            _on_current_device(*grads)
-            made.append(grads)
-        dq, dk, dv = made
-        g_strides = (Strides * 3)(_groups("dq", dq, q[0].shape, dtype), _groups("dk", dk, k[0].shape, dtype),
-                                  _groups("dv", dv, v[0].shape, dtype))
-        ws = _workspace(a, 1)
-        _check(lib().tf_ulysses_attention_backward(
-            ctypes.byref(a), _ptr_array(dout), _ptr_array(q), _ptr_array(k), _ptr_array(v), _ptr_array(out),
-            _lse_arrays(lse, P, (a.B, a.H // P, a.Sq)), strides, _ptr_array(dq), _ptr_array(dk), _ptr_array(dv),
-            g_strides, ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
-            _stream_handle(stream)))
-    return dq, dk, dv
+    L = lib()
+    with _OnStream(stream) as on:
+        device = on.device
+        a, (qp, q_str), (kp, k_str), (vp, v_str) = _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs,
+                                                              device)
+        dtype, P, q_shape, k_shape = q[0].dtype, a.P, q[0].shape, k[0].shape
+        dp, d_str = _views("dout", dout, P, q_shape, dtype, device)
+        op, o_str = _views("out", out, P, q_shape, dtype, device)
+        lp = _lse_arrays(lse, P, (a.B, a.H // P, a.Sq), device)
+        grads, ptrs, strides = [], [], None
+        for name, ts, shape in (("dq", dq, q_shape), ("dk", dk, k_shape), ("dv", dv, k_shape)):
+            if ts is None:
+                ts, p = _made(P, shape, dtype, q[0].device)
+                own = Strides(shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3])
+            else:
+                p, own = _views(name, ts, P, shape, dtype, device)
+            grads.append(ts)
+            ptrs.append(p)
+            strides = (strides or []) + [own]
+        ws, ws_at, ws_size = _workspace(L.tf_ulysses_attention_workspace, a, 1, device=q[0].device)
+        _check(L.tf_ulysses_attention_backward(a, dp, qp, kp, vp, op, lp, (Strides * 5)(d_str, q_str, k_str, v_str, o_str), *ptrs,
+                                               (Strides * 3)(*strides), ws_at, ws_size, on.handle))
+    return tuple(grads)
 
 
-# ---------------------------------------------------------------- key-value cache
 _ROPE = {None: 0, "interleaved": 1, "neox": 2}
 
 
@@ -587,35 +613,23 @@ def kv_cache(num_pages, Hkv, page_size, D, *, device="cuda"):
     return PagedCache(codes(), codes(), scales(), scales())
 
 
-def _kv_cache(cache, page_table, lens, starts):
+def _kv_cache(cache, page_table, lens, starts, device):
     k, v, k_scale, v_scale = cache
     if k.dim() != 4:
         raise ValueError("the cache's codes must be [pages, Hkv, page_size, D]")
-    pages, Hkv, page, D = k.shape
-    _on_current_device(k, v, k_scale, v_scale, page_table, lens, starts)
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be int32 [N, max_pages] with unit stride along a row")
+    shape, e4m3 = k.shape, torch.float8_e4m3fn
+    pages, Hkv, page, D = shape
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.get_device() != device:
+        raise ValueError(f"page_table must be int32 [N, max_pages] on cuda:{device}")
     N, most = page_table.shape
-    return KvCache(_plain_array("k", k, torch.float8_e4m3fn, (pages, Hkv, page, D)),
-                   _plain_array("v", v, torch.float8_e4m3fn, (pages, Hkv, page, D)),
-                   _plain_array("k_scale", k_scale, torch.float32, (pages, Hkv)),
-                   _plain_array("v_scale", v_scale, torch.float32, (pages, Hkv)), pages, Hkv, page, D, N, most,
+    if most > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table must have unit stride along a row")
+    return KvCache(_plain_array("k", k, e4m3, shape, device), _plain_array("v", v, e4m3, shape, device),
+                   _plain_array("k_scale", k_scale, torch.float32, shape[:2], device),
+                   _plain_array("v_scale", v_scale, torch.float32, shape[:2], device), pages, Hkv, page, D, N, most,
                    page_table.data_ptr(), page_table.stride(0) if N > 1 else most,
-                   _plain_array("lens", lens, torch.int32, (N,)), _plain_array("starts", starts, torch.int32, (N + 1,)))
-
-
-def _rows(name, ts, P, shape, dtype):
-    """Strides of P row views [T, heads, D]."""
-    if len(ts) != P:
-        raise ValueError(f"{name} must be a list of {P} head groups")
-    s = ts[0].stride()
-    for t in ts:
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.stride() != s:
-            raise ValueError(f"{name} must be {dtype} views of shape {tuple(shape)} with the same strides")
-    if shape[2] > 1 and s[2] != 1:
-        raise ValueError("the D dimension must have stride 1")
-    _on_current_device(*ts)
-    return Strides(0, s[0], s[1])
+                   _plain_array("lens", lens, torch.int32, (N,), device),
+                   _plain_array("starts", starts, torch.int32, (N + 1,), device))
 
 
 def kv_append(cache, page_table, lens, starts, k, v, q=None, q_out=None, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -629,32 +643,34 @@ def kv_append(cache, page_table, lens, starts, k, v, q=None, q_out=None, *, q_we
     ``q`` ``[T, H/P, D]`` of the same tokens likewise into ``q_out`` (made here unless given; ``q`` itself is fine).
     Returns ``q_out``, or None without q.
     """
-    c = _kv_cache(cache, page_table, lens, starts)
-    P, T, dtype = len(k), k[0].shape[0], k[0].dtype
-    if not 1 <= P <= MAX_SHARDS or c.Hkv % P:
-        raise ValueError(f"k must be a list of P in [1, {MAX_SHARDS}] head groups, P dividing Hkv={c.Hkv}")
     if rope not in _ROPE:
         raise ValueError(f"rope must be 'interleaved', 'neox' or None, not {rope!r}")
-    strides = (Strides * 3)(_rows("k", k, P, (T, c.Hkv // P, c.D), dtype), _rows("v", v, P, (T, c.Hkv // P, c.D), dtype))
-    weights = [_plain_array(n, w, dtype, (c.D,)) for n, w in (("q_weight", q_weight), ("k_weight", k_weight))]
-    _on_current_device(q_weight, k_weight, cos_sin)
-    rows = 0
-    if cos_sin is not None:
-        rows = cos_sin.shape[0]
-        _plain_array("cos_sin", cos_sin, torch.float32, (rows, c.D // 2, 2))
-    nr = NormRope(*weights, float(eps), float(theta), cos_sin.data_ptr() if cos_sin is not None else None)
-    H, o_str = 0, None
-    with _allocating_on(stream):
+    with _OnStream(stream) as on:
+        device = on.device
+        c = _kv_cache(cache, page_table, lens, starts, device)
+        P, T, dtype, D = len(k), k[0].shape[0], k[0].dtype, c.D
+        if not 1 <= P <= MAX_SHARDS or c.Hkv % P:
+            raise ValueError(f"k must be a list of P in [1, {MAX_SHARDS}] head groups, P dividing Hkv={c.Hkv}")
+        shape = (T, c.Hkv // P, D)
+        kp, k_str = _views("k", k, P, shape, dtype, device)
+        vp, v_str = _views("v", v, P, shape, dtype, device)
+        rows = 0
+        if cos_sin is not None:
+            rows = cos_sin.shape[0]
+            cos_sin = _plain_array("cos_sin", cos_sin, torch.float32, (rows, D // 2, 2), device)
+        nr = NormRope(_plain_array("q_weight", q_weight, dtype, (D,), device),
+                      _plain_array("k_weight", k_weight, dtype, (D,), device), eps, theta, cos_sin)
+        H, qp, q_str, op, o_str = 0, None, k_str, None, None
         if q is not None:
             H = P * q[0].shape[1]
-            strides[2] = _rows("q", q, P, (T, H // P, c.D), dtype)
+            q_shape = (T, q[0].shape[1], D)
+            qp, q_str = _views("q", q, P, q_shape, dtype, device)
             if q_out is None:
-                q_out = [torch.empty((T, H // P, c.D), dtype=dtype, device=t.device) for t in q]
-            o_str = _rows("q_out", q_out, P, (T, H // P, c.D), dtype)
-        _check(lib().tf_ulysses_kv_append(
-            ctypes.byref(c), P, T, H, _dtype_code(dtype), _ptr_array(k), _ptr_array(v), _ptr_array(q), strides,
-            _ptr_array(q_out), ctypes.byref(o_str) if o_str is not None else None, ctypes.byref(nr), _ROPE[rope], rows,
-            _stream_handle(stream)))
+                q_out, op = _made(P, q_shape, dtype, q[0].device)
+            else:
+                op, o_str = _views("q_out", q_out, P, q_shape, dtype, device)
+        _check(lib().tf_ulysses_kv_append(c, P, T, H, _dtype_code(dtype), kp, vp, qp, (Strides * 3)(k_str, v_str, q_str), op, o_str,
+                                          nr, _ROPE[rope], rows, on.handle))
     return q_out
 
 
@@ -667,27 +683,28 @@ def kv_attend(cache, page_table, lens, starts, q, out=None, lse=None, *, max_tok
     Returns ``(out, lse)``: P tensors ``[T, H/P, D]`` and fp32 ``[H/P, T]``, made here unless given (rows of no sequence
     are then undefined; given tensors keep them).
     """
-    c = _kv_cache(cache, page_table, lens, starts)
-    P, (T, Hl, D), dtype = len(q), q[0].shape, q[0].dtype
-    if not 1 <= P <= MAX_SHARDS or D != c.D:
-        raise ValueError(f"q must be a list of P in [1, {MAX_SHARDS}] views [T, heads, {c.D}]")
-    _on_current_device(slopes)
-    a = KvAttention(P, T, P * Hl, _dtype_code(dtype), T if max_tokens is None else int(max_tokens),
-                    c.max_pages * c.page_size if max_len is None else int(max_len), D ** -0.5 if scale is None else float(scale),
-                    float(softcap), 1 if causal else 0, _plain_array("slopes", slopes, torch.float32, (P * Hl,)))
-    q_str = _rows("q", q, P, (T, Hl, D), dtype)
-    with _allocating_on(stream):
+    L = lib()
+    with _OnStream(stream) as on:
+        device = on.device
+        c = _kv_cache(cache, page_table, lens, starts, device)
+        P, shape, dtype = len(q), q[0].shape, q[0].dtype
+        if not 1 <= P <= MAX_SHARDS or len(shape) != 3 or shape[2] != c.D:
+            raise ValueError(f"q must be a list of P in [1, {MAX_SHARDS}] views [T, heads, {c.D}]")
+        T, Hl, D = shape
+        qp, q_str = _views("q", q, P, shape, dtype, device)
+        a = KvAttention(P, T, P * Hl, _dtype_code(dtype), T if max_tokens is None else max_tokens,
+                        c.max_pages * c.page_size if max_len is None else max_len, D ** -0.5 if scale is None else scale, softcap,
+                        1 if causal else 0, _plain_array("slopes", slopes, torch.float32, (P * Hl,), device))
         if out is None:
-            out = [torch.empty((T, Hl, D), dtype=dtype, device=t.device) for t in q]
+            (out, op), o_str = _made(P, shape, dtype, q[0].device), None
+        else:
+            op, o_str = _views("out", out, P, shape, dtype, device)
         if lse is None:
-            lse = [torch.empty((Hl, T), dtype=torch.float32, device=t.device) for t in q]
-        o_str = _rows("out", out, P, (T, Hl, D), dtype)
-        n = ctypes.c_size_t()
-        _check(lib().tf_ulysses_kv_attend_workspace(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)))
-        ws = torch.empty(n.value, dtype=torch.uint8, device="cuda") if n.value else None
-        _check(lib().tf_ulysses_kv_attend(
-            ctypes.byref(c), ctypes.byref(a), _ptr_array(q), ctypes.byref(q_str), _ptr_array(out), ctypes.byref(o_str),
-            _lse_arrays(lse, P, (Hl, T)), ws.data_ptr() if ws is not None else None, n.value, _stream_handle(stream)))
+            lse, lp = _made(P, (Hl, T), torch.float32, q[0].device)
+        else:
+            lp = _lse_arrays(lse, P, (Hl, T), device)
+        ws, ws_at, ws_size = _workspace(L.tf_ulysses_kv_attend_workspace, c, a, device=q[0].device)
+        _check(L.tf_ulysses_kv_attend(c, a, qp, q_str, op, o_str, lp, ws_at, ws_size, on.handle))
     return out, lse
 
 

@@ -41,14 +41,15 @@ tf_status view(const char* name, const void* const* base, const tf_strides* give
     if (!empty && (s = check_ptrs(name, base, a.P)) != TF_OK) return s;
     const tf_strides st = given ? *given : tf_strides{tokens * hl * a.D, hl * a.D, a.D};
     if ((s = check_strides(name, st, 2, a.B, tokens, hl)) != TF_OK) return s;
-    if (!written && ((a.B > 1 && st.b == 0) || (tokens > 1 && st.t == 0) || (hl > 1 && st.h == 0)))
-        return fail(TF_ERR_UNSUPPORTED, "%s has a stride of 0 (key heads are shared through Hkv)", name);
-    if (written && ((a.B > 1 && st.b == 0) || (tokens > 1 && st.t == 0) || (hl > 1 && st.h == 0)))
-        return fail(TF_ERR_INVALID, "%s is written and has a stride of 0", name);
     for (int g = 0; g < a.P; ++g) out->base[g] = static_cast<uint8_t*>(const_cast<void*>(base[g]));
     out->b = st.b * 2;
     out->t = st.t * 2;
     out->h = st.h * 2;
+    if (empty) return TF_OK;  // no element is read or written
+    if (!written && ((a.B > 1 && st.b == 0) || (tokens > 1 && st.t == 0) || (hl > 1 && st.h == 0)))
+        return fail(TF_ERR_UNSUPPORTED, "%s has a stride of 0 (key heads are shared through Hkv)", name);
+    if (written && ((a.B > 1 && st.b == 0) || (tokens > 1 && st.t == 0) || (hl > 1 && st.h == 0)))
+        return fail(TF_ERR_INVALID, "%s is written and has a stride of 0", name);
     return TF_OK;
 }
 
