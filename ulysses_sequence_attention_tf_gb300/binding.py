@@ -83,6 +83,8 @@ class PagedCache(NamedTuple):
     v_scale: torch.Tensor
 
 
+_Strides3, _Strides5 = Strides * 3, Strides * 5
+
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 FREE_FN = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 
@@ -468,28 +470,27 @@ class _OnStream:
 
 
 def _views(name, ts, P, shape, dtype, device):
-    """(pointer array, strides) of P views of this shape, type and device with equal strides, the last one 1."""
+    """(pointers, strides) of P views of this shape, type and device with equal strides, the last one 1."""
     if len(ts) != P:
         raise ValueError(f"{name} must be a list of {P} head groups")
     s = ts[0].stride()
-    ptrs = (ctypes.c_void_p * P)()
-    for i, t in enumerate(ts):
+    ptrs = []
+    for t in ts:
         if t.shape != shape or t.dtype != dtype or t.stride() != s:
             raise ValueError(f"{name} must be {dtype} views of shape {tuple(shape)} with the same strides, not {t.dtype} "
                              f"{tuple(t.shape)} with strides {t.stride()}")
         if t.get_device() != device:
             raise ValueError(f"{name} must be on the current device cuda:{device}, not {t.device}")
-        ptrs[i] = t.data_ptr()
+        ptrs.append(t.data_ptr())
     if s[-1] != 1 and shape[-1] > 1:
         raise ValueError("the D dimension must have stride 1")
-    return ptrs, Strides(s[0], s[1], s[2]) if len(s) == 4 else Strides(0, s[0], s[1])
+    return ptrs, s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
 def _made(P, shape, dtype, device):
-    """P new contiguous tensors of one allocation, and their pointer array."""
-    whole = torch.empty((P, *shape), dtype=dtype, device=device)
-    ts = list(whole.unbind(0))
-    return ts, (ctypes.c_void_p * P)(*[t.data_ptr() for t in ts])
+    """P new contiguous tensors and their pointers."""
+    ts = [torch.empty(shape, dtype=dtype, device=device) for _ in range(P)]
+    return ts, [t.data_ptr() for t in ts]
 
 
 def _plain_array(name, t, dtype, shape, device):
@@ -505,7 +506,7 @@ def _plain_array(name, t, dtype, shape, device):
 def _lse_arrays(lse, P, shape, device):
     if len(lse) != P:
         raise ValueError(f"lse must be a list of {P} tensors")
-    return (ctypes.c_void_p * P)(*[_plain_array("lse", t, torch.float32, shape, device) for t in lse])
+    return [_plain_array("lse", t, torch.float32, shape, device) for t in lse]
 
 
 def _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs, device):
@@ -566,8 +567,9 @@ def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=No
             lp = _lse_arrays(lse, P, rows, device)
         ws, ws_at, ws_size = (None, None, 0) if q_docs is None else _workspace(
             L.tf_ulysses_attention_workspace, a, 0, device=q[0].device)
-        _check(L.tf_ulysses_attention(a, qp, kp, vp, (Strides * 3)(q_str, k_str, v_str), op, o_str, lp, ws_at, ws_size,
-                                      on.handle))
+        each = ctypes.c_void_p * P
+        _check(L.tf_ulysses_attention(a, each(*qp), each(*kp), each(*vp), _Strides3(q_str, k_str, v_str), each(*op),
+                                      Strides(*o_str) if o_str is not None else None, each(*lp), ws_at, ws_size, on.handle))
     return out, lse
 
 
@@ -586,19 +588,21 @@ def attention_backward(dout, q, k, v, out, lse, dq=None, dk=None, dv=None, *, sc
         dp, d_str = _views("dout", dout, P, q_shape, dtype, device)
         op, o_str = _views("out", out, P, q_shape, dtype, device)
         lp = _lse_arrays(lse, P, (a.B, a.H // P, a.Sq), device)
-        grads, ptrs, strides = [], [], None
+        each = ctypes.c_void_p * P
+        grads, ptrs, strides = [], [], []
         for name, ts, shape in (("dq", dq, q_shape), ("dk", dk, k_shape), ("dv", dv, k_shape)):
             if ts is None:
                 ts, p = _made(P, shape, dtype, q[0].device)
-                own = Strides(shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3])
+                own = (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3])
             else:
                 p, own = _views(name, ts, P, shape, dtype, device)
             grads.append(ts)
-            ptrs.append(p)
-            strides = (strides or []) + [own]
+            ptrs.append(each(*p))
+            strides.append(own)
         ws, ws_at, ws_size = _workspace(L.tf_ulysses_attention_workspace, a, 1, device=q[0].device)
-        _check(L.tf_ulysses_attention_backward(a, dp, qp, kp, vp, op, lp, (Strides * 5)(d_str, q_str, k_str, v_str, o_str), *ptrs,
-                                               (Strides * 3)(*strides), ws_at, ws_size, on.handle))
+        _check(L.tf_ulysses_attention_backward(a, each(*dp), each(*qp), each(*kp), each(*vp), each(*op), each(*lp),
+                                               _Strides5(d_str, q_str, k_str, v_str, o_str), *ptrs, _Strides3(*strides), ws_at,
+                                               ws_size, on.handle))
     return tuple(grads)
 
 
@@ -669,8 +673,11 @@ def kv_append(cache, page_table, lens, starts, k, v, q=None, q_out=None, *, q_we
                 q_out, op = _made(P, q_shape, dtype, q[0].device)
             else:
                 op, o_str = _views("q_out", q_out, P, q_shape, dtype, device)
-        _check(lib().tf_ulysses_kv_append(c, P, T, H, _dtype_code(dtype), kp, vp, qp, (Strides * 3)(k_str, v_str, q_str), op, o_str,
-                                          nr, _ROPE[rope], rows, on.handle))
+        each = ctypes.c_void_p * P
+        _check(lib().tf_ulysses_kv_append(
+            c, P, T, H, _dtype_code(dtype), each(*kp), each(*vp), each(*qp) if qp is not None else None,
+            _Strides3(k_str, v_str, q_str), each(*op) if op is not None else None,
+            Strides(*o_str) if o_str is not None else None, nr, _ROPE[rope], rows, on.handle))
     return q_out
 
 
@@ -704,7 +711,9 @@ def kv_attend(cache, page_table, lens, starts, q, out=None, lse=None, *, max_tok
         else:
             lp = _lse_arrays(lse, P, (Hl, T), device)
         ws, ws_at, ws_size = _workspace(L.tf_ulysses_kv_attend_workspace, c, a, device=q[0].device)
-        _check(L.tf_ulysses_kv_attend(c, a, qp, q_str, op, o_str, lp, ws_at, ws_size, on.handle))
+        each = ctypes.c_void_p * P
+        _check(L.tf_ulysses_kv_attend(c, a, each(*qp), Strides(*q_str), each(*op),
+                                      Strides(*o_str) if o_str is not None else None, each(*lp), ws_at, ws_size, on.handle))
     return out, lse
 
 
