@@ -251,27 +251,22 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         constexpr uint32_t kIdescQ = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
         const int steps = exact ? 2 * visits : visits;
         auto landed = [&](uint32_t k) { return wait_for(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag); };
-        auto stage = [&](uint32_t k) { return ring + (k % kStages) * kTile; };
-        auto product = [&](uint32_t d, uint32_t a_smem, uint32_t b_smem) {
-#pragma unroll
-            for (uint32_t kk = 0; kk < kD / 16; ++kk) {
-                const uint32_t off = kk / 4 * kHalfTile + kk % 4 * 32;
-                tc_mma(d, sw128_desc(a_smem + off), sw128_desc(b_smem + off), kIdescS, kk != 0);
-            }
-        };
+        const uint32_t q_low = desc_low(q_smem), do_low = desc_low(do_smem), kv_low = desc_low(ring),
+                       k_low = desc_low(ring, kHalfTile);
+        auto offset = [&](uint32_t k) { return (k % kStages) * (kTile >> 4); };
         bool ok = steps == 0 || wait_for(q_full, 0, abort_flag);
         // step i: K at ring tile 2i, V at 2i + 1
         auto scores = [&](int i) {
             if (!landed(2 * i)) return false;
             tc_fence_after();
-            product(tmem + (i & 1) * kAttnRows, q_smem, stage(2 * i));
+            tc_product<kD, kHalfTile, kHalfTile>(tmem + (i & 1) * kAttnRows, q_low, kv_low + offset(2 * i), kIdescS);
             tc_commit(s_full0 + 8 * (i & 1));
             return true;
         };
         auto dp = [&](int i) {
             if (!landed(2 * i + 1)) return false;
             tc_fence_after();
-            product(dp_tmem, do_smem, stage(2 * i + 1));
+            tc_product<kD, kHalfTile, kHalfTile>(dp_tmem, do_low, kv_low + offset(2 * i + 1), kIdescS);
             tc_commit(dp_full);
             tc_commit(empty0 + 8 * ((2 * i + 1) % kStages));
             return true;
@@ -290,10 +285,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             if (!sums_only) {
                 const uint32_t a = tmem + (i & 1) * kAttnRows;
                 const bool first = i == (exact ? visits : 0);
-#pragma unroll
-                for (uint32_t kk = 0; kk < kAttnRows / 16; ++kk)
-                    tc_mma_ts(dq_tmem, a + kk / 4 * 64 + kk % 4 * 8, sw128_desc(stage(2 * i) + kk * 2048, kHalfTile), kIdescQ,
-                              !first || kk != 0);
+                // the two halves of the keys lie 64 columns apart
+                tc_product_ts<kAttnRows / 2>(dq_tmem, a, k_low + offset(2 * i), kIdescQ, !first);
+                tc_product_ts<kAttnRows / 2>(dq_tmem, a + 64, k_low + offset(2 * i) + (64 * kSwizzleRow >> 4), kIdescQ, 1u);
             }
             tc_commit(empty0 + 8 * (2 * i % kStages));
         }
@@ -576,18 +570,15 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kQueries, false);
         constexpr uint32_t kIdescD = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
         auto landed = [&](uint32_t k) { return wait_for(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag); };
-        auto stage = [&](uint32_t k) { return ring + (k % kStages) * kBlock; };
+        const uint32_t k_low = desc_low(k_smem), v_low = desc_low(v_smem), n_low = desc_low(ring),
+                       t_low = desc_low(ring, kHalfBlock);
+        auto offset = [&](uint32_t k) { return (k % kStages) * (kBlock >> 4); };
         auto transposed = [&](int n) {  // S and dP of block n
             if (!landed(2 * n) || !landed(2 * n + 1)) return false;
             tc_fence_after();
             const uint32_t d = tmem + (n & 1) * 2 * kQueries;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                for (uint32_t kk = 0; kk < kD / 16; ++kk)
-                    tc_mma(d + x * kQueries, sw128_desc((x ? v_smem : k_smem) + kk / 4 * kHalfTile + kk % 4 * 32),
-                           sw128_desc(stage(2 * n + x) + kk / 4 * kHalfBlock + kk % 4 * 32), kIdescS, kk != 0);
-            }
+            tc_product<kD, kHalfTile, kHalfBlock>(d, k_low, n_low + offset(2 * n), kIdescS);
+            tc_product<kD, kHalfTile, kHalfBlock>(d + kQueries, v_low, n_low + offset(2 * n + 1), kIdescS);
             tc_commit(s_full0 + 8 * (n & 1));
             return true;
         };
@@ -599,13 +590,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
             if (!(ok = wait_for(dx_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag))) break;
             tc_fence_after();
             const uint32_t a = tmem + (n & 1) * 2 * kQueries;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {  // dV += P dO, dK += dx Q
-#pragma unroll
-                for (uint32_t kk = 0; kk < kQueries / 16; ++kk)
-                    tc_mma_ts(x ? dk_tmem : dv_tmem, a + x * kQueries + kk * 8,
-                              sw128_desc(stage(2 * n + 1 - x) + kk * 2048, kHalfBlock), kIdescD, (uint32_t(n) | kk) != 0);
-            }
+            tc_product_ts<kQueries>(dv_tmem, a, t_low + offset(2 * n + 1), kIdescD, uint32_t(n));         // dV += P dO
+            tc_product_ts<kQueries>(dk_tmem, a + kQueries, t_low + offset(2 * n), kIdescD, uint32_t(n));  // dK += dx Q
             tc_commit(empty0 + 8 * (2 * n % kStages));
             tc_commit(empty0 + 8 * ((2 * n + 1) % kStages));
         }

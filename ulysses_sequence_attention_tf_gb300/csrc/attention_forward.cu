@@ -137,49 +137,47 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
         // ---------------- MMA issuer
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
         constexpr uint32_t kIdescO = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
-        auto scores = [&](int t, uint32_t k_smem) {
-#pragma unroll
-            for (uint32_t kk = 0; kk < kD / 16; ++kk) {
-                const uint32_t off = kk / 4 * kHalfTile + kk % 4 * 32;
-                tc_mma(tmem + t * kAttnRows, sw128_desc(q_smem + t * kTile + off), sw128_desc(k_smem + off), kIdescS, kk != 0);
-            }
+        const uint32_t q_low = desc_low(q_smem), k_low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
+        auto scores = [&](int t, uint32_t s) {
+            tc_product<kD, kHalfTile, kHalfTile>(tmem + t * kAttnRows, q_low + t * (kTile >> 4), k_low + s * (kTile >> 4), kIdescS);
             tc_commit(s_full0 + 8 * t);
         };
-        uint32_t n = 0;  // ring tiles consumed
-        int i = 0;       // key tiles finished
-        auto landed = [&](uint32_t k) {
-            return bounded_wait(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag, &g_attention_status);
+        // the ring's next tile: stage and phase
+        uint32_t s = 0, phase = 0;
+        auto landed = [&]() { return bounded_wait(full0 + 8 * s, phase, abort_flag, &g_attention_status); };
+        auto advance = [&]() {
+            if (++s == uint32_t(kStages)) s = 0, phase ^= 1u;
         };
-        auto stage = [&](uint32_t k) { return ring + (k % kStages) * kTile; };
+        int i = 0;  // key tiles finished
         int j = it.next();
-        bool ok = j < 0 || (bounded_wait(q_full, 0, abort_flag, &g_attention_status) && landed(0));
+        bool ok = j < 0 || (bounded_wait(q_full, 0, abort_flag, &g_attention_status) && landed());
         if (ok && j >= 0) {
             tc_fence_after();
-            for (int t = 0; t < tiles; ++t) scores(t, stage(0));
+            for (int t = 0; t < tiles; ++t) scores(t, 0);
             tc_commit(empty0);
-            n = 1;
+            advance();
         }
         for (; ok && j >= 0; ++i) {
             j = it.next();
-            const uint32_t v = n, k = n + 1;
-            n += j >= 0 ? 2 : 1;
-            if (!(ok = landed(v))) break;
+            if (!(ok = landed())) break;
+            const uint32_t v = s;
+            advance();
             for (int t = 0; t < tiles; ++t) {
                 if (!(ok = bounded_wait(p_full0 + 8 * t, i & 1u, abort_flag, &g_attention_status))) break;
                 tc_fence_after();
-#pragma unroll
-                for (uint32_t kk = 0; kk < kAttnRows / 16; ++kk)
-                    tc_mma_ts(o_tmem + t * kD, tmem + t * kAttnRows + kk * 8, sw128_desc(stage(v) + kk * 2048, kHalfTile),
-                              kIdescO, (uint32_t(i) | kk) != 0);
+                tc_product_ts<kAttnRows>(o_tmem + t * kD, tmem + t * kAttnRows, v_low + v * (kTile >> 4), kIdescO, uint32_t(i));
                 if (j >= 0) {
-                    if (t == 0 && !(ok = landed(k))) break;
+                    if (t == 0 && !(ok = landed())) break;
                     tc_fence_after();
-                    scores(t, stage(k));
+                    scores(t, s);
                 }
             }
             if (!ok) break;
-            tc_commit(empty0 + 8 * (v % kStages));
-            if (j >= 0) tc_commit(empty0 + 8 * (k % kStages));
+            tc_commit(empty0 + 8 * v);
+            if (j >= 0) {
+                tc_commit(empty0 + 8 * s);
+                advance();
+            }
         }
         tc_commit(o_full);
         drain_phase(o_full, 0);  // every MMA of this CTA has completed

@@ -130,20 +130,16 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             // ---------------- MMA issuer
             constexpr uint32_t kIdescS = f16_idesc(false, kAttnRows, kAttnRows, false);
             constexpr uint32_t kIdescO = f16_idesc(false, kAttnRows, kD, true);
-            auto scores = [&](int t, uint32_t k_smem) {
-#pragma unroll
-                for (uint32_t kk = 0; kk < kD / 16; ++kk) {
-                    const uint32_t off = kk / 4 * kHalfTile + kk % 4 * 32;
-                    tc_mma(tmem + t * kAttnRows, sw128_desc(q_smem + t * kTile + off), sw128_desc(k_smem + off), kIdescS, kk != 0);
-                }
+            const uint32_t q_low = desc_low(q_smem), k_low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
+            auto scores = [&](int t, uint32_t s) {
+                tc_product<kD, kHalfTile, kHalfTile>(tmem + t * kAttnRows, q_low + t * (kTile >> 4), k_low + s * (kTile >> 4), kIdescS);
                 tc_commit(s_full0 + 8 * t);
             };
             auto landed = [&](uint32_t k) { return wait_for(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag); };
-            auto stage = [&](uint32_t k) { return ring + (k % kStages) * kTile; };
             bool ok = wait_for(q_full, 0, abort_flag) && landed(0);
             if (ok) {
                 tc_fence_after();
-                for (int t = 0; t < tiles; ++t) scores(t, stage(0));
+                for (int t = 0; t < tiles; ++t) scores(t, 0);
                 tc_commit(empty0);
             }
             for (int i = 0; ok && i < n_tiles; ++i) {
@@ -153,14 +149,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
                 for (int t = 0; t < tiles; ++t) {
                     if (!(ok = wait_for(p_full0 + 8 * t, i & 1u, abort_flag))) break;
                     tc_fence_after();
-#pragma unroll
-                    for (uint32_t kk = 0; kk < kAttnRows / 16; ++kk)
-                        tc_mma_ts(o_tmem + t * kD, tmem + t * kAttnRows + kk * 8, sw128_desc(stage(v) + kk * 2048, kHalfTile),
-                                  kIdescO, (uint32_t(i) | kk) != 0);
+                    tc_product_ts<kAttnRows>(o_tmem + t * kD, tmem + t * kAttnRows, v_low + v % kStages * (kTile >> 4), kIdescO,
+                                             uint32_t(i));
                     if (more) {
                         if (t == 0 && !(ok = landed(k))) break;
                         tc_fence_after();
-                        scores(t, stage(k));
+                        scores(t, k % kStages);
                     }
                 }
                 if (!ok) break;

@@ -194,16 +194,54 @@ __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// the same with A in TMEM: lane = row, a 32-bit column holds two K elements
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// The descriptor of sw128_desc in halves: everything but the low word is the same for every
+// tile, and an offset inside a tile is an addition to the low word.  One thread issues all
+// products of a CTA while its other warps keep the schedulers busy, so what it
+// computes between two of them counts.
+constexpr uint32_t kDescHigh = ((8 * kSwizzleRow) >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, uint32_t leading_bytes = 16) {
+    return ((smem_addr & 0x3FFFFu) >> 4) | (leading_bytes >> 4) << 16;
+}
+template <bool kAccumulate>
+__device__ __forceinline__ void tc_mma_low(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_low), "r"(b_low), "r"(idesc), "n"(kDescHigh), "n"(kAccumulate ? 1 : 0)
         : "memory");
 }
+// A in TMEM: lane = row, a 32-bit column holds two K elements.
+__device__ __forceinline__ void tc_mma_ts_low(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %4};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_low), "r"(idesc), "n"(kDescHigh), "r"(accumulate)
+        : "memory");
+}
+// D = A B^T over kD elements of K: both operands K-major, 64 elements a half, halves
+// kHalfA and kHalfB bytes apart.
+template <int kD, uint32_t kHalfA, uint32_t kHalfB>
+__device__ __forceinline__ void tc_product(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc) {
+    tc_mma_low<false>(d_tmem, a_low, b_low, idesc);
+#pragma unroll
+    for (uint32_t kk = 1; kk < kD / 16; ++kk)
+        tc_mma_low<true>(d_tmem, a_low + ((kk / 4 * kHalfA + kk % 4 * 32) >> 4), b_low + ((kk / 4 * kHalfB + kk % 4 * 32) >> 4),
+                         idesc);
+}
+// D (+)= A B with A from TMEM (kK elements of K, 32-bit columns of two), B MN-major.
+template <int kK>
+__device__ __forceinline__ void tc_product_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc,
+                                              uint32_t accumulate) {
+    tc_mma_ts_low(d_tmem, a_tmem, b_low, idesc, accumulate);
+#pragma unroll
+    for (uint32_t kk = 1; kk < kK / 16; ++kk) tc_mma_ts_low(d_tmem, a_tmem + kk * 8, b_low + kk * (2048 >> 4), idesc, 1u);
+}
+
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far completed.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
