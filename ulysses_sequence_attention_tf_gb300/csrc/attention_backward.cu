@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && elect_one()) {
         const CUtensorMap* maps[2] = {&bp.k.m[g], &bp.v.m[g]};
         const int kh = int(h / p.shared);
         uint32_t n = 0;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         if (visits > 0) drain_phase(q_full, 0);
         for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
             drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9 && elect_one()) {
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
         constexpr uint32_t kIdescQ = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
         const int steps = exact ? 2 * visits : visits;
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && elect_one()) {
         uint32_t n = 0;
         bool ok = true;
         int i0 = it.next();
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         if (any) drain_phase(kv_full, 0);
         for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
             drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9 && elect_one()) {
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kQueries, false);
         constexpr uint32_t kIdescD = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
         auto landed = [&](uint32_t k) { return wait_for(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag); };

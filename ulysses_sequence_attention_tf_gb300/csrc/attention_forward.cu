@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
     // 384 * 168 registers at launch = 256 * 216 + 128 * 72
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && elect_one()) {
         // ---------------- TMA producer
         const CUtensorMap* maps[2] = {&fp.k.m[g], &fp.v.m[g]};
         const int kh = int(h / p.shared);
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
         if (n > 0) drain_phase(q_full, 0);
         for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
             drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9 && elect_one()) {
         // ---------------- MMA issuer
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
         constexpr uint32_t kIdescO = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);

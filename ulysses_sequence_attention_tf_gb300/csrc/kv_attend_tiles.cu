@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
     // 512 * 128 registers at launch = 256 * 176 + 128 * 104 + 128 * 56
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 12 && lane == 0 && n_tiles > 0) {
+        if (warp == 12 && n_tiles > 0 && elect_one()) {
             // ---------------- MMA issuer
             constexpr uint32_t kIdescS = f16_idesc(false, kAttnRows, kAttnRows, false);
             constexpr uint32_t kIdescO = f16_idesc(false, kAttnRows, kD, true);
