@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         mbar_init(s_full0, 1);
         mbar_init(s_full0 + 8, 1);
         mbar_init(dp_full, 1);
-        mbar_init(dp_free, 2 * kAttnRows);
-        mbar_init(dx_full, 2 * kAttnRows);
+        mbar_init(dp_free, 8);  // a warp each
+        mbar_init(dx_full, 8);
         mbar_init(sums_full, 2 * kAttnRows);
         mbar_init(done, 1);
         *abort_flag = 0;
@@ -369,8 +369,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 tc_fence_after();
                 float d[64];
                 load_row<64>(dp_tmem + half * 64 + lane_base, d);
-                tc_fence_before();
-                mbar_arrive(dp_free);
+                warp_arrive(dp_free);
                 if (phase == 0) {
 #pragma unroll
                     for (int x = 0; x < 64; ++x) sum += s[x] == 0.f ? 0.f : s[x] * d[x];
@@ -384,8 +383,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                     store_row16<kF, 64>(s_row, d);
                     tc_wait_st();
                 }
-                tc_fence_before();
-                mbar_arrive(dx_full);
+                warp_arrive(dx_full);
             }
             if (phase == 0 && ok) {  // the two halves of the row
                 sums[half * kAttnRows + r] = sum;
@@ -505,11 +503,11 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         mbar_init(kv_full, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full0 + 8 * t, 1);
-            mbar_init(dx_full0 + 8 * t, kAttnRows);
+            mbar_init(dx_full0 + 8 * t, 4);  // a warp each
         }
         for (int t = 0; t < kStatSlots; ++t) {
-            mbar_init(stat_full0 + 8 * t, 32);
-            mbar_init(stat_free0 + 8 * t, kAttnRows);
+            mbar_init(stat_full0 + 8 * t, 1);
+            mbar_init(stat_free0 + 8 * t, 4);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
@@ -620,7 +618,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                 }
                 stats[n % kStatSlots * kQueries + x] = q;
             }
-            mbar_arrive(stat_full0 + 8 * (n % kStatSlots));
+            warp_arrive(stat_full0 + 8 * (n % kStatSlots));
         }
     }
     } else {
@@ -683,9 +681,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
             }
             store_row16<kF, 64>(dp_row, d);
             tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(dx_full0 + 8 * t);
-            mbar_arrive(stat_free0 + 8 * slot);
+            warp_arrive(dx_full0 + 8 * t);
+            if (lane == 0) mbar_arrive(stat_free0 + 8 * slot);
         }
         // n counts every block, of both halves of the warps
         if (ok) ok = wait_for(done, 0, abort_flag);

@@ -58,12 +58,14 @@ __device__ __forceinline__ float tanh_wide(float x) {
 // tanh x / x for |x| <= kTanhNear as a polynomial in y = x^2, fitted for the least
 // relative error (7.3e-8): no transcendental instruction.
 constexpr float kTanhNear = 0.6f;
+constexpr float kTanh0 = 0.9999999403953552f, kTanh1 = -0.33332309126853943f, kTanh2 = 0.13310173153877258f,
+                kTanh3 = -0.05210147425532341f, kTanh4 = 0.015475417487323284f;
 __device__ __forceinline__ uint64_t tanh_over_x(uint64_t y) {
     auto both = [](float c) { return f2_pack(c, c); };
-    uint64_t r = f2_fma(y, both(0.015475417487323284f), both(-0.05210147425532341f));
-    r = f2_fma(y, r, both(0.13310173153877258f));
-    r = f2_fma(y, r, both(-0.33332309126853943f));
-    return f2_fma(y, r, both(0.9999999403953552f));
+    uint64_t r = f2_fma(y, both(kTanh4), both(kTanh3));
+    r = f2_fma(y, r, both(kTanh2));
+    r = f2_fma(y, r, both(kTanh1));
+    return f2_fma(y, r, both(kTanh0));
 }
 
 // The tiles of the other side that a row tile visits, in order: all of [0, n), or
@@ -147,43 +149,57 @@ __device__ __forceinline__ void finish_scores(float (&s)[128], float scale, floa
 
 constexpr float kSlack = 8.0f;  // growth of a row's maximum that its reference lets pass, in powers of two
 
-// One tile of keys into a row's softmax: s holds 128 scores (z = c * s, -inf where masked),
-// m the reference, l the sum, s_tmem the row's score columns, which take the weights in 16
-// bits, o_row its output columns (they hold something when `started`), which are
-// scaled by `down` and by 2^(m_old - m) when the reference moves.
-template <Fused kF, int kD>
-__device__ __forceinline__ void fold_tile(float (&s)[128], float c, float down, bool started, float& m, float& l,
-                                          uint32_t s_tmem, uint32_t o_row) {
-    float top[4];
+// One arrival of a warp whose lanes are done with what they wrote to TMEM and shared memory.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    tc_fence_before();
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void bounds_of(const float (&s)[128], float& top, float& low, bool with_low) {
+    float t[4], u[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-        top[x] = fmaxf(s[x], s[x + 4]);
+        t[x] = u[x] = s[x];
 #pragma unroll
-        for (int y = x + 8; y < 128; y += 8) top[x] = fmaxf(top[x], fmaxf(s[y], s[y + 4]));
-    }
-    const float most = c * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    const bool grow = most > m + kSlack;  // from -inf: on any visible key
-    if (__any_sync(0xffffffffu, grow || down != 1.0f)) {
-        const float to = grow ? most : m;
-        const float shrink = grow ? ex2(m - to) : 1.0f;
-        l *= shrink;
-        m = to;
-        if (started) {
-            const float f = shrink * down;
-#pragma unroll 1
-            for (int x = 0; x < kD; x += 32) {
-                uint32_t r[32];
-                tc_ld32(o_row + x, r);
-                tc_wait_ld();
-                tc_landed(r);
-#pragma unroll
-                for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * f);
-                tc_st32(o_row + x, r);
-            }
+        for (int y = x + 4; y < 128; y += 4) {
+            t[x] = fmaxf(t[x], s[y]);
+            if (with_low) u[x] = fminf(u[x], s[y]);
         }
     }
-    const float base = m == -INFINITY ? 0.f : m;
-    const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base);
+    top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    low = fminf(fminf(u[0], u[1]), fminf(u[2], u[3]));
+}
+
+// The row's reference m follows the tile's maximum z when that outgrows it (or V's scale
+// changed: down); l and the kD output columns, which hold something when `started`, go along.
+template <int kD>
+__device__ __forceinline__ void move_reference(float most, float down, bool started, float& m, float& l, uint32_t o_row) {
+    const bool grow = most > m + kSlack;  // from -inf: on any visible key
+    if (!__any_sync(0xffffffffu, grow || down != 1.0f)) return;
+    const float to = grow ? most : m;
+    const float shrink = grow ? ex2(m - to) : 1.0f;
+    l *= shrink;
+    m = to;
+    if (!started) return;
+    const float f = shrink * down;
+#pragma unroll 1
+    for (int x = 0; x < kD; x += 32) {
+        uint32_t r[32];
+        tc_ld32(o_row + x, r);
+        tc_wait_ld();
+        tc_landed(r);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * f);
+        tc_st32(o_row + x, r);
+    }
+}
+
+// Weights 2^(argument of two scores) of a row's 128 scores: summed into l, and in 16 bits over
+// the row's score columns.  The first 64 keys are announced on p_half, the others on p_half + 8.
+template <Fused kF, typename Argument>
+__device__ __forceinline__ void write_weights(const float (&s)[128], float& l, uint32_t s_tmem, uint32_t p_half,
+                                              Argument argument) {
     uint64_t sum[2] = {0, 0};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -192,17 +208,76 @@ __device__ __forceinline__ void fold_tile(float (&s)[128], float c, float down, 
         for (int y = 0; y < 16; ++y) {
             const int e = x * 32 + 2 * y;
             float lo, hi;
-            f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, b2), lo, hi);
+            f2_unpack(argument(f2_pack(s[e], s[e + 1])), lo, hi);
             lo = ex2(lo);
             hi = ex2(hi);
             sum[y & 1] = f2_add(sum[y & 1], f2_pack(lo, hi));
             w[y] = pack2<kF>(lo, hi);
         }
         tc_st16(s_tmem + x * 16, w);
+        if (x == 1 || x == 3) {
+            tc_wait_st();
+            warp_arrive(p_half + (x == 3 ? 8 : 0));
+        }
     }
     float a0, a1;
     f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
     l += a0 + a1;
+}
+
+// One tile of keys into a row's softmax: s holds 128 scores (z = c * s, -inf where masked), m the
+// reference, l the sum, s_tmem the row's score columns, o_row its output columns.
+template <Fused kF, int kD>
+__device__ __forceinline__ void fold_tile(float (&s)[128], float c, float down, bool started, float& m, float& l,
+                                          uint32_t s_tmem, uint32_t o_row, uint32_t p_half) {
+    float top, low;
+    bounds_of(s, top, low, false);
+    move_reference<kD>(c * top, down, started, m, l, o_row);
+    const float base = m == -INFINITY ? 0.f : m;
+    const uint64_t c2 = f2_pack(c, c), b2 = f2_pack(-base, -base);
+    write_weights<kF>(s, l, s_tmem, p_half, [&](uint64_t v) { return f2_fma(v, c2, b2); });
+}
+
+// The same for capped scores without a mask or a bias, from the raw products: z is a polynomial
+// (tanh x / x in x^2 times x, the cap folded in), so that the exponent's argument takes 4 to 7
+// fused operations; the maximum of z is z of the maximum.  kRaw: the nearest scores skip the
+// product x = s * scale / cap, its factor folded into the coefficients (for a factor that
+// leaves them in range).  False, with nothing done, where |x| of some row of the warp is
+// beyond the polynomials.
+constexpr float kTanhNearest = 0.2f;  // second degree in x^2: 1.1e-7 relative
+constexpr float kTanhNearest0 = 0.9999998807907104f, kTanhNearest1 = -0.3332858979701996f, kTanhNearest2 = 0.1301540732383728f;
+template <Fused kF, int kD, bool kRaw>
+__device__ __forceinline__ bool fold_capped_tile(float (&s)[128], float scale, float cap, float down, bool started, float& m,
+                                                 float& l, uint32_t s_tmem, uint32_t o_row, uint32_t p_half) {
+    const float to_x = scale / cap, to_z = cap * kLog2e;
+    float top, low;
+    bounds_of(s, top, low, true);
+    const float far = fmaxf(fabsf(top), fabsf(low)) * to_x;
+    if (!__all_sync(0xffffffffu, far <= kTanhNear)) return false;
+    auto both = [](float v) { return f2_pack(v, v); };
+    if (__all_sync(0xffffffffu, far <= kTanhNearest && (!kRaw || to_x >= 0x1p-16f))) {
+        const float unit = kRaw ? to_x : 1.0f, a0 = to_z * unit * kTanhNearest0, a1 = to_z * unit * unit * unit * kTanhNearest1,
+                    a2 = to_z * unit * unit * unit * unit * unit * kTanhNearest2;
+        const float x = kRaw ? top : top * to_x, y = x * x;
+        move_reference<kD>(x * fmaf(y, fmaf(y, a2, a1), a0), down, started, m, l, o_row);
+        const uint64_t nb = both(m == -INFINITY ? 0.f : -m), b0 = both(a0), b1 = both(a1), b2 = both(a2), x2 = both(to_x);
+        write_weights<kF>(s, l, s_tmem, p_half, [&](uint64_t v) {
+            if (!kRaw) v = f2_mul(v, x2);
+            const uint64_t y2 = f2_mul(v, v);
+            return f2_fma(v, f2_fma(y2, f2_fma(y2, b2, b1), b0), nb);
+        });
+    } else {
+        const float x = top * to_x;
+        float t, unused;
+        f2_unpack(tanh_over_x(both(x * x)), t, unused);
+        move_reference<kD>(to_z * x * t, down, started, m, l, o_row);
+        const uint64_t nb = both(m == -INFINITY ? 0.f : -m), x2 = both(to_x), z2 = both(to_z);
+        write_weights<kF>(s, l, s_tmem, p_half, [&](uint64_t v) {
+            v = f2_mul(v, x2);
+            return f2_fma(f2_mul(v, z2), tanh_over_x(f2_mul(v, v)), nb);
+        });
+    }
+    return true;
 }
 
 }  // namespace dev

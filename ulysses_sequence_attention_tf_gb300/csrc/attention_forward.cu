@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kStages) * size_t(kTile));
     const uint32_t q_smem = smem_u32(smem), ring = q_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
-    const uint32_t s_full0 = q_full + 8, p_full0 = s_full0 + 16, o_full = p_full0 + 16;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 6);
+    const uint32_t s_full0 = q_full + 8, p_half0 = s_full0 + 16, o_full = p_half0 + 32;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
         mbar_init(q_full, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full0 + 8 * t, 1);
-            mbar_init(p_full0 + 8 * t, kAttnRows);
+            mbar_init(p_half0 + 16 * t, 4);  // a warp each
+            mbar_init(p_half0 + 16 * t + 8, 4);
         }
         mbar_init(o_full, 1);
         *abort_flag = 0;
@@ -163,9 +164,15 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
             const uint32_t v = s;
             advance();
             for (int t = 0; t < tiles; ++t) {
-                if (!(ok = bounded_wait(p_full0 + 8 * t, i & 1u, abort_flag, &g_attention_status))) break;
-                tc_fence_after();
-                tc_product_ts<kAttnRows>(o_tmem + t * kD, tmem + t * kAttnRows, v_low + v * (kTile >> 4), kIdescO, uint32_t(i));
+                // P of the first 64 keys while the weights of the others are computed
+                for (int x = 0; ok && x < 2; ++x) {
+                    ok = bounded_wait(p_half0 + 16 * t + 8 * x, i & 1u, abort_flag, &g_attention_status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    tc_product_ts<kAttnRows / 2>(o_tmem + t * kD, tmem + t * kAttnRows + x * 32,
+                                                 v_low + v * (kTile >> 4) + x * (64 * kSwizzleRow >> 4), kIdescO, uint32_t(i | x));
+                }
+                if (!ok) break;
                 if (j >= 0) {
                     if (t == 0 && !(ok = landed())) break;
                     tc_fence_after();
@@ -211,10 +218,14 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
             float s[128];
             load_row<128>(s_tmem, s);
             const int j0 = j * int(kAttnRows);
+            const bool whole = __all_sync(0xffffffffu, plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u
+                                                            : j0 + int(kAttnRows) <= bound);
+            if (kScore == Score::kCap && whole &&
+                fold_capped_tile<kF, kD, true>(s, p.scale, p.cap, 1.0f, n > 0, m, l, s_tmem, o_row, p_half0 + 16 * t))
+                continue;
             if (kScore != Score::kPlain)
                 finish_scores<kScore>(s, p.scale, p.cap, slope, float(i + (int(p.Sk) - int(p.Sq)) - j0));
-            const bool whole = plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + int(kAttnRows) <= bound;
-            if (!__all_sync(0xffffffffu, whole)) {
+            if (!whole) {
                 if (plan) {
                     // the tile's documents, four keys a lane; a warp of tile 0 also clears the
                     // V rows of padding, whose contents may be anything
@@ -250,10 +261,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
                     for (int x = 0; x < 128; ++x) s[x] = j0 + x < bound ? s[x] : -INFINITY;
                 }
             }
-            fold_tile<kF, kD>(s, c, 1.0f, n > 0, m, l, s_tmem, o_row);
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(p_full0 + 8 * t);
+            fold_tile<kF, kD>(s, c, 1.0f, n > 0, m, l, s_tmem, o_row, p_half0 + 16 * t);
         }
         if (int(t) < tiles && ok) {
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);

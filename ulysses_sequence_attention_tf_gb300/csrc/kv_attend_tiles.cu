@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
     static_assert(kInfos * sizeof(TileInfo) <= 64, "the barriers follow the tile infos");
     const uint32_t q_smem = smem_u32(smem), ring = q_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
-    const uint32_t s_full0 = q_full + 8, p_full0 = s_full0 + 16, o_full = p_full0 + 16, info_full0 = o_full + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 6 + kInfos);
+    const uint32_t s_full0 = q_full + 8, p_half0 = s_full0 + 16, o_full = p_half0 + 32, info_full0 = o_full + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 8 + kInfos);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const KvCache& c = p.c;
@@ -99,13 +99,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full0 + 8 * s, 128);
+            mbar_init(full0 + 8 * s, 4);  // a warp each
             mbar_init(empty0 + 8 * s, 1);
         }
-        mbar_init(q_full, 128);
+        mbar_init(q_full, 4);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full0 + 8 * t, 1);
-            mbar_init(p_full0 + 8 * t, kAttnRows);
+            mbar_init(p_half0 + 16 * t, 4);  // a warp each
+            mbar_init(p_half0 + 16 * t + 8, 4);
         }
         mbar_init(o_full, 1);
         for (int t = 0; t < kInfos; ++t) mbar_init(info_full0 + 8 * t, 1);
@@ -147,10 +148,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
                 const bool more = i + 1 < n_tiles;
                 if (!(ok = landed(v))) break;
                 for (int t = 0; t < tiles; ++t) {
-                    if (!(ok = wait_for(p_full0 + 8 * t, i & 1u, abort_flag))) break;
-                    tc_fence_after();
-                    tc_product_ts<kAttnRows>(o_tmem + t * kD, tmem + t * kAttnRows, v_low + v % kStages * (kTile >> 4), kIdescO,
-                                             uint32_t(i));
+                    for (int x = 0; x < 2; ++x) {
+                        if (!(ok = wait_for(p_half0 + 16 * t + 8 * x, i & 1u, abort_flag))) break;
+                        tc_fence_after();
+                        tc_product_ts<kAttnRows / 2>(o_tmem + t * kD, tmem + t * kAttnRows + x * 32,
+                                                     v_low + v % kStages * (kTile >> 4) + x * (64 * kSwizzleRow >> 4), kIdescO,
+                                                     uint32_t(i | x));
+                    }
+                    if (!ok) break;
                     if (more) {
                         if (t == 0 && !(ok = landed(k))) break;
                         tc_fence_after();
@@ -207,7 +212,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
                 }
             }
             fence_async_shared();
-            mbar_arrive(q_full);
+            warp_arrive(q_full);
         }
         // lane l < 8: the page of keys [key0 + 128 * tile + 16 l, + 16)
         int id_of = -1, id_next = -1;
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
                 } else {
                     convert(raw[1], k, scale_of[1], v_ref);
                 }
-                mbar_arrive(full0 + 8 * s);
+                warp_arrive(full0 + 8 * s);
             }
             id_of = id_next;
             scale_of[0] = scale_next[0];
@@ -337,19 +342,20 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             load_row<128>(s_tmem, s);
             const int j0 = key0 + j * int(kAttnRows);
             const float f = factor * info.k_ref;
+            const float down = v_ref / info.v_ref;
+            v_ref = info.v_ref;
+            const bool whole = __all_sync(0xffffffffu, j0 + int(kAttnRows) <= bound && info.bad == 0);
+            if (kScore == Score::kCap && whole &&
+                fold_capped_tile<Fused::kFP16, kD, false>(s, f, p.cap, down, j > 0, m, l, s_tmem, o_row, p_half0 + 16 * t))
+                continue;
             if (kScore != Score::kPlain) finish_scores<kScore>(s, f, p.cap, slope, float(pos - j0));
             const float to_z = kScore == Score::kPlain ? fmaxf(f * kLog2e, 0x1p-126f) : 1.0f;
-            if (!__all_sync(0xffffffffu, j0 + int(kAttnRows) <= bound && info.bad == 0)) {
+            if (!whole) {
 #pragma unroll
                 for (int x = 0; x < 128; ++x)
                     s[x] = j0 + x < bound && !((info.bad >> (x / 16)) & 1u) ? s[x] : -INFINITY;
             }
-            const float down = v_ref / info.v_ref;
-            v_ref = info.v_ref;
-            fold_tile<Fused::kFP16, kD>(s, to_z, down, j > 0, m, l, s_tmem, o_row);
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(p_full0 + 8 * t);
+            fold_tile<Fused::kFP16, kD>(s, to_z, down, j > 0, m, l, s_tmem, o_row, p_half0 + 16 * t);
         }
         if (int(t) < tiles && ok) {
             if (n_tiles > 0) ok = wait_for(o_full, 0, abort_flag);
