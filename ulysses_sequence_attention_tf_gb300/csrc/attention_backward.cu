@@ -35,45 +35,41 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
     return bounded_wait(bar, parity, abort_flag, &g_attention_backward_status);
 }
 
-// Weights w = 2^(z log2 e - lse2) of kN scores in place, and (capped) the factor
-// bend = 1 - tanh^2 of each.  far0: pos - key of element 0, one less (kStep = -1, a row
-// of keys) or one more (kStep = 1, a row of queries) for each next element.
-template <bool kCap, bool kBias, int kN, int kStep>
-__device__ __forceinline__ void to_scores(float (&s)[kN], float (&bend)[kCap ? kN : 2], float scale, float cap, float slope,
-                                          float far0) {
-    if constexpr (kCap) {
-        const float to_x = scale / cap, to_z = cap * kLog2e;
-        float most = 0.f;
+// Arguments of the weights of a row's scores, for pairs of them: log2 e z - lse2, where `add`
+// holds -lse2 and what the bias gives; and (capped) the slope 1 - tanh^2 of each.
+template <bool kCap>
+struct ToWeight {
+    uint64_t c2, x2, z2;  // log2 e scale; scale / cap, log2 e cap
+    bool near;            // |x| of every score of the warp is within the polynomial
+    template <int kN>
+    __device__ __forceinline__ ToWeight(const AttentionParams& p, const float (&s)[kN]) {
+        const float c = p.scale * kLog2e, to_x = kCap ? p.scale / p.cap : 0.f, to_z = p.cap * kLog2e;
+        c2 = f2_pack(c, c);
+        x2 = f2_pack(to_x, to_x);
+        z2 = f2_pack(to_z, to_z);
+        near = true;
+        if constexpr (kCap) {
+            float most = 0.f;
 #pragma unroll
-        for (int i = 0; i < kN; i += 2) most = fmaxf(fmaxf(fabsf(s[i]), fabsf(s[i + 1])), most);
-        if (__all_sync(0xffffffffu, most * fabsf(to_x) <= kTanhNear)) {
-            const uint64_t x2 = f2_pack(to_x, to_x), z2 = f2_pack(to_z, to_z), one = f2_pack(1.f, 1.f);
-#pragma unroll
-            for (int i = 0; i < kN; i += 2) {
-                const uint64_t x = f2_mul(f2_pack(s[i], s[i + 1]), x2);
-                const uint64_t t = f2_mul(x, tanh_over_x(f2_mul(x, x)));
-                f2_unpack(f2_mul(t, z2), s[i], s[i + 1]);
-                f2_unpack(f2_sub(one, f2_mul(t, t)), bend[i], bend[i + 1]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                const float t = tanh_wide(s[i] * to_x);
-                s[i] = to_z * t;
-                bend[i] = fmaf(-t, t, 1.0f);
-            }
+            for (int i = 0; i < kN; ++i) most = fmaxf(fabsf(s[i]), most);
+            near = __all_sync(0xffffffffu, most * fabsf(to_x) <= kTanhNear);
         }
-    } else {
-        const uint64_t c2 = f2_pack(scale * kLog2e, scale * kLog2e);
-#pragma unroll
-        for (int i = 0; i < kN; i += 2) f2_unpack(f2_mul(f2_pack(s[i], s[i + 1]), c2), s[i], s[i + 1]);
     }
-    if constexpr (kBias) {
-        const float m = slope * kLog2e;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) s[i] = fmaf(-m, fabsf(far0 + float(kStep * i)), s[i]);
+    __device__ __forceinline__ uint64_t operator()(uint64_t s, uint64_t add, uint64_t& bend) const {
+        if constexpr (!kCap) return f2_fma(s, c2, add);
+        uint64_t t = f2_mul(s, x2);
+        if (near) {
+            t = f2_mul(t, tanh_over_x(f2_mul(t, t)));
+        } else {
+            float a, b;
+            f2_unpack(t, a, b);
+            t = f2_pack(tanh_wide(a), tanh_wide(b));
+        }
+        const uint64_t one = f2_pack(1.f, 1.f);
+        bend = f2_sub(one, f2_mul(t, t));
+        return f2_fma(t, z2, add);
     }
-}
+};
 
 // 16-bit pairs of kN values over TMEM columns from taddr
 template <Fused kF, int kN>
@@ -309,12 +305,14 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         const float slope = kBias && p.slopes ? p.slopes[g * p.Hl + h] : 0.f;
         const int64_t stat = (int64_t(b) * p.Hl + h) * p.Sq + (valid ? i : 0);
         float* delta_at = p.delta + int64_t(g) * p.B * p.Hl * p.Sq + stat;
-        const float lse2 = valid ? p.lse[g][stat] * kLog2e : 0.f;
+        const float lse = valid ? p.lse[g][stat] : 0.f;
+        const float less = lse == -INFINITY ? 0.f : -lse * kLog2e, slope2 = slope * kLog2e;
         const int64_t at = valid ? i : 0;
         float delta = 0.f;
         if (!exact && valid) {
             delta = row_dot<kF, kD>(p.dout.base[g] + b * p.dout.b + at * p.dout.t + h * p.dout.h,
                                     p.out.base[g] + b * p.out.b + at * p.out.t + h * p.out.h);
+            if (p.plan && doc < 0) delta = 0.f;  // padding: its output gradient may be anything
             if (half == 0) *delta_at = delta;
         }
         bool ok = true;
@@ -331,13 +329,32 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 }
                 tc_fence_after();
                 const int j0 = j * int(kAttnRows) + int(half) * 64;
-                float s[64], bend[kCap ? 64 : 2];
+                float s[64];
+                uint64_t bend[kCap ? 32 : 1];
                 load_row<64>(s_row, s);
-                to_scores<kCap, kBias, 64, -1>(s, bend, p.scale, p.cap, slope, float(i + (int(p.Sk) - int(p.Sq)) - j0));
+                const int pos = i + int(p.Sk) - int(p.Sq), pos0 = row0 + int(p.Sk) - int(p.Sq);
+                const int side = kBias ? bias_side(pos0, int(kAttnRows), j0, 64, p.causal && !p.prefix) : 1;
+                const float at = kBias && side != 0 ? less - float(side) * slope2 * float(pos - j0) : less;
+                const uint64_t at2 = f2_pack(at, at), by2 = f2_pack(float(side) * slope2, float(side) * slope2);
+                const ToWeight<kCap> weight(p, s);
 #pragma unroll
-                for (int x = 0; x < 64; ++x) s[x] = ex2(s[x] - lse2);
-                const bool whole = plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + 64 <= bound;
-                if (!__all_sync(0xffffffffu, whole)) {
+                for (int x = 0; x < 64; x += 2) {
+                    uint64_t add = at2;
+                    if constexpr (kBias) {
+                        if (side != 0)
+                            add = f2_fma(f2_pack(float(x), float(x + 1)), by2, at2);
+                        else
+                            add = f2_pack(fmaf(-slope2, fabsf(float(pos - j0 - x)), less), fmaf(-slope2, fabsf(float(pos - j0 - x - 1)), less));
+                    }
+                    f2_unpack(weight(f2_pack(s[x], s[x + 1]), add, bend[kCap ? x / 2 : 0]), s[x], s[x + 1]);
+                    s[x] = ex2(s[x]);
+                    s[x + 1] = ex2(s[x + 1]);
+                }
+                const bool whole = __all_sync(0xffffffffu, plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + 64 <= bound);
+                uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+                if (!whole) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) bits[x] = bound_bits(bound, j0 + 32 * x);
                     if (plan) {
                         int32_t kd[2];
 #pragma unroll
@@ -345,9 +362,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                             const int key = j0 + x * 32 + int(lane);
                             kd[x] = key < int(p.Sk) ? __ldg(p.k_docs + int64_t(b) * p.Sk + key) : -1;
                         }
-#pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            s[x] = __shfl_sync(0xffffffffu, kd[x / 32], x % 32) == doc && j0 + x < bound ? s[x] : 0.f;
+                        keep_document(bits, kd, doc);
                         // padding's K rows may hold anything: clear them for the product with dx
                         if (quarter < 2 && (quarter == 0 ? kd[0] : kd[1]) < 0) {
                             uint4* k = reinterpret_cast<uint4*>(smem + (2 + 2 * n % kStages) * size_t(kTile) +
@@ -356,10 +371,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                                 for (int y = 0; y < 8; ++y) k[x * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
                         }
                         fence_async_shared();
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 64; ++x) s[x] = j0 + x < bound ? s[x] : 0.f;
                     }
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) s[x] = (bits[x / 32] >> (x % 32)) & 1u ? s[x] : 0.f;
                 }
                 ok = wait_for(dp_full, n & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -370,15 +384,20 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 float d[64];
                 load_row<64>(dp_tmem + half * 64 + lane_base, d);
                 warp_arrive(dp_free);
+                if (!whole) {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) d[x] = (bits[x / 32] >> (x % 32)) & 1u ? d[x] : 0.f;
+                }
                 if (phase == 0) {
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) sum += s[x] == 0.f ? 0.f : s[x] * d[x];
+                    for (int x = 0; x < 64; ++x) sum = fmaf(s[x], d[x], sum);
                 } else {
+                    const uint64_t nd = f2_pack(-delta, -delta);
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) {
-                        float dx = s[x] == 0.f ? 0.f : s[x] * (d[x] - delta);
-                        if constexpr (kCap) dx *= bend[x];
-                        d[x] = dx;
+                    for (int x = 0; x < 64; x += 2) {
+                        uint64_t dx = f2_mul(f2_pack(s[x], s[x + 1]), f2_add(f2_pack(d[x], d[x + 1]), nd));
+                        if constexpr (kCap) dx = f2_mul(dx, bend[x / 2]);
+                        f2_unpack(dx, d[x], d[x + 1]);
                     }
                     store_row16<kF, 64>(s_row, d);
                     tc_wait_st();
@@ -427,9 +446,11 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
 constexpr uint32_t kQueries = 64;
 constexpr int kStatSlots = 4;
 
-struct QueryStat {
-    float lse2, delta;
-    int bound, doc;
+// What a block's columns need of their queries.
+struct QueryStats {
+    float less[kQueries];   // -lse2 (fp16: + 8) and the query's part of the bias
+    float delta[kQueries];  // -delta (fp16: * 2^-8)
+    int bound[kQueries], doc[kQueries];
 };
 
 template <int kD>
@@ -438,7 +459,7 @@ struct DkvShape {
     static constexpr uint32_t kBlock = kTile / 2;         // 64 queries
     static constexpr uint32_t kHalfBlock = kHalfTile / 2;
     static constexpr int kStages = 8;
-    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kBlock + kStatSlots * kQueries * sizeof(QueryStat) + 512 + 1024;
+    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kBlock + kStatSlots * sizeof(QueryStats) + 512 + 1024;
 };
 
 // The blocks of a key tile, in order: query heads outer, tiles of 128 queries that can see
@@ -479,8 +500,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     const AttentionParams& p = bp.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    QueryStat* stats = reinterpret_cast<QueryStat*>(smem + 2 * size_t(kTile) + kStages * size_t(kBlock));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(stats + kStatSlots * kQueries);
+    QueryStats* stats = reinterpret_cast<QueryStats*>(smem + 2 * size_t(kTile) + kStages * size_t(kBlock));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(stats + kStatSlots);
     const uint32_t k_smem = smem_u32(smem), v_smem = k_smem + kTile, ring = k_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, kv_full = empty0 + 8 * kStages;
     const uint32_t s_full0 = kv_full + 8, dx_full0 = s_full0 + 16, stat_full0 = dx_full0 + 16;
@@ -603,20 +624,30 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                 if (!__all_sync(0xffffffffu, ok)) break;
             }
             const int64_t stat = (int64_t(b) * p.Hl + kh * p.shared + it.head) * p.Sq;
+            const float slope2 = kBias && p.slopes ? p.slopes[g * p.Hl + kh * p.shared + it.head] * kLog2e : 0.f;
+            const int side = kBias ? bias_side(i0 + ahead, int(kQueries), row0, int(kAttnRows), p.causal && !p.prefix) : 0;
+            QueryStats& st = stats[n % kStatSlots];
             for (int x = int(lane); x < int(kQueries); x += 32) {
                 const int i = i0 + x;
-                QueryStat q{INFINITY, 0.f, 0, -1};  // no such query: weight 0
+                float less = -INFINITY, delta = 0.f;  // no such query: weight 0
+                int bound = 0, doc = -1;
                 if (i < int(p.Sq)) {
                     const float lse = p.lse[g][stat + i];
-                    q.lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e - kUp;
-                    q.delta = p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat + i];
-                    q.bound = key_bound(p, b, i);
+                    less = lse == -INFINITY ? -INFINITY : kUp - lse * kLog2e - float(side * x) * slope2;
+                    delta = -kDown * p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat + i];
+                    bound = key_bound(p, b, i);
                     if (plan) {
-                        q.doc = p.q_docs[int64_t(b) * p.Sq + i];
-                        if (q.doc < 0) q.bound = 0;
+                        doc = p.q_docs[int64_t(b) * p.Sq + i];
+                        if (doc < 0) {
+                            bound = 0;
+                            delta = 0.f;
+                        }
                     }
                 }
-                stats[n % kStatSlots * kQueries + x] = q;
+                st.less[x] = less;
+                st.delta[x] = delta;
+                st.bound[x] = bound;
+                st.doc[x] = doc;
             }
             warp_arrive(stat_full0 + 8 * (n % kStatSlots));
         }
@@ -641,44 +672,72 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                 break;
             }
             tc_fence_after();
-            const QueryStat* st = stats + slot * kQueries;
-            const float slope = kBias && p.slopes ? p.slopes[g * p.Hl + kh * p.shared + it.head] : 0.f;
-            float s[64], bend[kCap ? 64 : 2];
+            const QueryStats& st = stats[slot];
+            const float slope2 = kBias && p.slopes ? p.slopes[g * p.Hl + kh * p.shared + it.head] * kLog2e : 0.f;
+            const int side = kBias ? bias_side(i0 + ahead, int(kQueries), row0, int(kAttnRows), p.causal && !p.prefix) : 0;
+            const float far = float(i0 + ahead - j), own = -float(side) * slope2 * far;
+            const uint64_t own2 = f2_pack(own, own), down2 = f2_pack(kDown, kDown);
+            float s[64], d[64];
             load_row<64>(s_row, s);
-            to_scores<kCap, kBias, 64, 1>(s, bend, p.scale, p.cap, slope, float(i0 + ahead - j));
-#pragma unroll
-            for (int x = 0; x < 64; ++x) s[x] = ex2(s[x] - st[x].lse2);
+            const ToWeight<kCap> weight(p, s);
             const int qt = i0 / int(kAttnRows);
-            const bool whole = plan ? (__ldg(plan + words + (qt >> 5)) >> (qt & 31)) & 1u
-                                    : i0 + int(kQueries) <= int(p.Sq) && row0 + int(kAttnRows) <= st[0].bound;
-            if (!whole) {  // the same for every thread
-                if (plan) {
+            const bool whole = plan ? (__ldg(plan + words + (qt >> 5)) >> (qt & 31)) & 1u  // the same for every thread
+                                    : i0 + int(kQueries) <= int(p.Sq) && row0 + int(kAttnRows) <= st.bound[0];
+            uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+            if (!whole) {
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) s[x] = st[x].doc == doc && j < st[x].bound ? s[x] : 0.f;
-                    // padding's Q and dO rows may hold anything: clear them for the products with dx and P
-                    if (r < kQueries && st[r].doc < 0) {
-                        for (int qd = 0; qd < 2; ++qd) {
-                            uint4* row = reinterpret_cast<uint4*>(smem + 2 * size_t(kTile) +
-                                                                  ((2 * n + qd) % kStages) * size_t(kBlock) + r * kSwizzleRow);
-                            for (int x = 0; x < kD / 64; ++x)
-                                for (int y = 0; y < 8; ++y) row[x * (kHalfBlock / 16) + y] = make_uint4(0, 0, 0, 0);
-                        }
+                for (int x = 0; x < 64; x += 4) {
+                    const int4 bound = *reinterpret_cast<const int4*>(st.bound + x), doc4 = *reinterpret_cast<const int4*>(st.doc + x);
+                    const int* bo = &bound.x;
+                    const int* dc = &doc4.x;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        if (j >= bo[y] || (plan && dc[y] != doc)) bits[x / 32] &= ~(1u << ((x + y) % 32));
+                }
+                // padding's Q and dO rows may hold anything: clear them for the products with dx and P
+                if (plan && r < kQueries && st.doc[r] < 0) {
+                    for (int qd = 0; qd < 2; ++qd) {
+                        uint4* row = reinterpret_cast<uint4*>(smem + 2 * size_t(kTile) +
+                                                              ((2 * n + qd) % kStages) * size_t(kBlock) + r * kSwizzleRow);
+                        for (int x = 0; x < kD / 64; ++x)
+                            for (int y = 0; y < 8; ++y) row[x * (kHalfBlock / 16) + y] = make_uint4(0, 0, 0, 0);
                     }
-                    fence_async_shared();
-                } else {
+                }
+                if (plan) fence_async_shared();
+            }
+            load_row<64>(dp_row, d);
+            if (!whole) {
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) s[x] = j < st[x].bound ? s[x] : 0.f;
+                for (int x = 0; x < 64; ++x) d[x] = (bits[x / 32] >> (x % 32)) & 1u ? d[x] : 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < 64; x += 4) {
+                const float4 less = *reinterpret_cast<const float4*>(st.less + x), nd = *reinterpret_cast<const float4*>(st.delta + x);
+#pragma unroll
+                for (int y = 0; y < 4; y += 2) {
+                    const int e = x + y;
+                    const float l0 = y ? less.z : less.x, l1 = y ? less.w : less.y;
+                    uint64_t add = f2_pack(l0, l1), bend = 0;
+                    if constexpr (kBias) {
+                        if (side != 0)
+                            add = f2_add(add, own2);
+                        else
+                            add = f2_pack(fmaf(-slope2, fabsf(far + float(e)), l0), fmaf(-slope2, fabsf(far + float(e + 1)), l1));
+                    }
+                    f2_unpack(weight(f2_pack(s[e], s[e + 1]), add, bend), s[e], s[e + 1]);
+                    s[e] = ex2(s[e]);
+                    s[e + 1] = ex2(s[e + 1]);
+                    if (!whole) {
+                        s[e] = (bits[e / 32] >> (e % 32)) & 1u ? s[e] : 0.f;
+                        s[e + 1] = (bits[e / 32] >> (e % 32 + 1)) & 1u ? s[e + 1] : 0.f;
+                    }
+                    const uint64_t off = y ? f2_pack(nd.z, nd.w) : f2_pack(nd.x, nd.y), d2 = f2_pack(d[e], d[e + 1]);
+                    uint64_t dx = f2_mul(f2_pack(s[e], s[e + 1]), kF == Fused::kFP16 ? f2_fma(d2, down2, off) : f2_add(d2, off));
+                    if constexpr (kCap) dx = f2_mul(dx, bend);
+                    f2_unpack(dx, d[e], d[e + 1]);
                 }
             }
-            float d[64];
-            load_row<64>(dp_row, d);
             store_row16<kF, 64>(s_row, s);
-#pragma unroll
-            for (int x = 0; x < 64; ++x) {
-                float dx = s[x] == 0.f ? 0.f : s[x] * ((d[x] - st[x].delta) * kDown);
-                if constexpr (kCap) dx *= bend[x];
-                d[x] = dx;
-            }
             store_row16<kF, 64>(dp_row, d);
             tc_wait_st();
             warp_arrive(dx_full0 + 8 * t);

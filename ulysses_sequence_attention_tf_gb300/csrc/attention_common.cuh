@@ -116,16 +116,26 @@ __device__ __forceinline__ void load_row(uint32_t taddr, float (&v)[kN]) {
 // Scores beyond scale * q.k: none, the cap, or cap (if any) and bias and any scale.
 enum class Score { kPlain, kCap, kAny };
 
-// z of one row's 128 scores, times log2 e, in place (kCap, kAny).
+// The bias of a tile is linear in the key where all of its keys lie on one side of the query:
+// side = 1 (keys at or before it), -1 (behind it), 0 (both).  rows, keys: first ones of the
+// tile; under a plain causal mask what lies behind a query does not count.
+__device__ __forceinline__ int bias_side(int row_pos0, int rows, int key0, int keys, bool causal_only) {
+    return row_pos0 >= key0 + keys - 1 || causal_only ? 1 : row_pos0 + rows - 1 <= key0 ? -1 : 0;
+}
+
+// z of one row's 128 scores, times log2 e, in place (kCap, kAny).  far: the query's position
+// less the tile's first key.
 template <Score kScore>
-__device__ __forceinline__ void finish_scores(float (&s)[128], float scale, float cap, float slope, float far) {
+__device__ __forceinline__ void finish_scores(float (&s)[128], float scale, float cap, float slope, float far, int side) {
+    auto both = [](float v) { return f2_pack(v, v); };
+    const float k = slope * kLog2e;
     if (kScore == Score::kCap || cap != 0.f) {
         const float to_x = scale / cap, to_z = cap * kLog2e;
         float most = 0.f;
 #pragma unroll
         for (int i = 0; i < 128; i += 2) most = fmaxf(fmaxf(fabsf(s[i]), fabsf(s[i + 1])), most);
         if (__all_sync(0xffffffffu, most * fabsf(to_x) <= kTanhNear)) {
-            const uint64_t x2 = f2_pack(to_x, to_x), z2 = f2_pack(to_z, to_z);
+            const uint64_t x2 = both(to_x), z2 = both(to_z);
 #pragma unroll
             for (int i = 0; i < 128; i += 2) {
                 const uint64_t x = f2_mul(f2_pack(s[i], s[i + 1]), x2);
@@ -135,16 +145,45 @@ __device__ __forceinline__ void finish_scores(float (&s)[128], float scale, floa
 #pragma unroll
             for (int i = 0; i < 128; ++i) s[i] = to_z * tanh_wide(s[i] * to_x);
         }
+        if (kScore == Score::kCap) return;
+        scale = kLn2;  // s is z already
+    }
+    const float c = scale * kLog2e;
+    if (side != 0) {  // z = c s - side k (far - i)
+        const float at = side > 0 ? -k * far : k * far, by = side > 0 ? k : -k;
+        const uint64_t c2 = both(c), at2 = both(at), by2 = both(by);
+#pragma unroll
+        for (int i = 0; i < 128; i += 2)
+            f2_unpack(f2_fma(f2_pack(s[i], s[i + 1]), c2, f2_fma(f2_pack(float(i), float(i + 1)), by2, at2)), s[i], s[i + 1]);
     } else {
-        const float c = scale * kLog2e;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] *= c;
+        for (int i = 0; i < 128; ++i) s[i] = fmaf(-k, fabsf(far - float(i)), s[i] * c);
     }
-    if (kScore == Score::kAny) {
-        const float m = slope * kLog2e;
+}
+
+// Bit x: key x of a block of 32 that starts at key0 lies below the row's bound.
+__device__ __forceinline__ uint32_t bound_bits(int bound, int key0) {
+    const int n = bound - key0;
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// bits[g] &= keys of block g (its lane's document kd[g]) that belong to the row's document: one
+// ballot a block for every document among the warp's rows, one or two as a rule.
+template <int kBlocks>
+__device__ __forceinline__ void keep_document(uint32_t (&bits)[kBlocks], const int32_t (&kd)[kBlocks], int32_t doc) {
+    uint32_t mine[kBlocks] = {};
+    for (uint32_t left = 0xffffffffu; left;) {
+        const int32_t d = __shfl_sync(0xffffffffu, doc, __ffs(left) - 1);
+        const bool here = doc == d;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] = fmaf(-m, fabsf(far - float(i)), s[i]);
+        for (int g = 0; g < kBlocks; ++g) {
+            const uint32_t same = __ballot_sync(0xffffffffu, kd[g] == d);
+            if (here) mine[g] = same;
+        }
+        left &= ~__ballot_sync(0xffffffffu, here);
     }
+#pragma unroll
+    for (int g = 0; g < kBlocks; ++g) bits[g] &= mine[g];
 }
 
 constexpr float kSlack = 8.0f;  // growth of a row's maximum that its reference lets pass, in powers of two

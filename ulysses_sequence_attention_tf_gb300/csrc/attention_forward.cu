@@ -223,31 +223,33 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
             if (kScore == Score::kCap && whole &&
                 fold_capped_tile<kF, kD, true>(s, p.scale, p.cap, 1.0f, n > 0, m, l, s_tmem, o_row, p_half0 + 16 * t))
                 continue;
+            const int pos0 = row0 + int(t * kAttnRows) + int(p.Sk) - int(p.Sq);
             if (kScore != Score::kPlain)
-                finish_scores<kScore>(s, p.scale, p.cap, slope, float(i + (int(p.Sk) - int(p.Sq)) - j0));
+                finish_scores<kScore>(s, p.scale, p.cap, slope, float(i + (int(p.Sk) - int(p.Sq)) - j0),
+                                      bias_side(pos0, int(kAttnRows), j0, int(kAttnRows), p.causal && !p.prefix));
             if (!whole) {
+                uint32_t bits[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) bits[x] = bound_bits(bound, j0 + 32 * x);
                 if (plan) {
-                    // the tile's documents, four keys a lane; a warp of tile 0 also clears the
-                    // V rows of padding, whose contents may be anything
-                    int32_t kd[4];
+                    int32_t kd[4];  // the tile's documents, four keys a lane
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const int key = j0 + x * 32 + int(lane);
                         kd[x] = key < int(p.Sk) ? __ldg(p.k_docs + int64_t(b) * p.Sk + key) : -1;
                     }
+                    keep_document(bits, kd, doc);
+                    // the warps of tile 0 clear the V rows of padding, whose contents may be anything
+                    int32_t own = kd[0];
 #pragma unroll
-                    for (int x = 0; x < 128; ++x)
-                        s[x] = __shfl_sync(0xffffffffu, kd[x / 32], x % 32) == doc && j0 + x < bound ? s[x] : -INFINITY;
-                    if (t == 0) {
+                    for (int x = 1; x < 4; ++x) own = quarter == uint32_t(x) ? kd[x] : own;
+                    if (t == 0 && __any_sync(0xffffffffu, own < 0)) {
                         const uint32_t vn = 2 * uint32_t(n) + 1;
                         ok = bounded_wait(full0 + 8 * (vn % kStages), (vn / kStages) & 1u, abort_flag, &g_attention_status);
                         if (!__all_sync(0xffffffffu, ok)) {
                             ok = false;
                             break;
                         }
-                        int32_t own = kd[0];
-#pragma unroll
-                        for (int x = 1; x < 4; ++x) own = quarter == uint32_t(x) ? kd[x] : own;
                         if (own < 0) {
                             uint4* v = reinterpret_cast<uint4*>(smem + (2 + vn % kStages) * size_t(kTile) +
                                                                 (quarter * 32 + lane) * kSwizzleRow);
@@ -256,10 +258,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
                         }
                         fence_async_shared();
                     }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 128; ++x) s[x] = j0 + x < bound ? s[x] : -INFINITY;
                 }
+#pragma unroll
+                for (int x = 0; x < 128; ++x) s[x] = (bits[x / 32] >> (x % 32)) & 1u ? s[x] : -INFINITY;
             }
             fold_tile<kF, kD>(s, c, 1.0f, n > 0, m, l, s_tmem, o_row, p_half0 + 16 * t);
         }

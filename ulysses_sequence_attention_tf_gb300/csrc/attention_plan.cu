@@ -46,6 +46,7 @@ template <bool kRowsAreKeys>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ AttentionParams p, uint32_t* plan,
                                                              uint32_t rows_per_tile, uint32_t words) {
     __shared__ DocRange row;
+    __shared__ uint32_t bits[2];
     grid_dependency_wait();
     const uint32_t rt = blockIdx.x, b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rows = int(kRowsAreKeys ? p.Sk : p.Sq), cols = int(kRowsAreKeys ? p.Sq : p.Sk);
@@ -59,25 +60,59 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
     const DocRange rr = row;
     uint32_t* out = plan + (size_t(b) * gridDim.x + rt) * 2 * words;
-    const int col_tiles = (cols + int(kAttnRows) - 1) / int(kAttnRows);
-    for (uint32_t w = warp; w < words; w += kPlanThreads / 32) {
+    constexpr int kWarps = kPlanThreads / 32, kAhead = 4;  // a warp takes kAhead neighbours at a time
+    static_assert(kWarps * kAhead == 32, "the CTA covers a word at a time");
+    for (uint32_t w = 0; w < words; ++w) {
+        __syncthreads();
+        if (threadIdx.x < 2) bits[threadIdx.x] = 0;
+        __syncthreads();
+        int lo[kAhead], hi[kAhead];
+        bool hole[kAhead];
+        const int t0 = int(w) * 32 + int(warp) * kAhead;
+        int32_t v[kAhead][4];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int at = (t0 + k) * int(kAttnRows) + x * 32 + int(lane);
+                v[k][x] = at < cols ? col_docs[at] : -1;
+            }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            lo[k] = INT32_MAX;
+            hi[k] = -1;
+            bool h = false;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                h |= v[k][x] < 0;
+                if (v[k][x] >= 0) {
+                    lo[k] = min(lo[k], v[k][x]);
+                    hi[k] = max(hi[k], v[k][x]);
+                }
+            }
+            lo[k] = __reduce_min_sync(0xffffffffu, lo[k]);
+            hi[k] = __reduce_max_sync(0xffffffffu, hi[k]);
+            hole[k] = __any_sync(0xffffffffu, h);
+        }
         uint32_t some = 0, all = 0;
-        for (int k = 0; k < 32 && int(w) * 32 + k < col_tiles; ++k) {
-            const int c0 = (int(w) * 32 + k) * int(kAttnRows);
-            const DocRange cr = warp_range(col_docs, c0, int(kAttnRows), cols);
-            const int c1 = min(cols, c0 + int(kAttnRows));
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int c0 = (t0 + k) * int(kAttnRows), c1 = min(cols, c0 + int(kAttnRows));
+            if (c0 >= cols) break;
             // the last query of the pair reaches furthest, its first one least
             const int far = key_bound(p, b, (kRowsAreKeys ? c1 : r1) - 1), near = key_bound(p, b, kRowsAreKeys ? c0 : r0);
             const int k0 = kRowsAreKeys ? r0 : c0, k1 = kRowsAreKeys ? r0 + int(kAttnRows) : c0 + int(kAttnRows);
-            const bool meet = rr.lo <= cr.hi && cr.lo <= rr.hi && rr.hi >= 0 && cr.hi >= 0 && k0 < far;
-            const bool whole = meet && rr.lo == rr.hi && cr.lo == cr.hi && !rr.hole && !cr.hole && k1 <= near;
-            some |= uint32_t(meet) << k;
-            all |= uint32_t(whole) << k;
+            const bool meet = rr.lo <= hi[k] && lo[k] <= rr.hi && rr.hi >= 0 && hi[k] >= 0 && k0 < far;
+            const bool whole = meet && rr.lo == rr.hi && lo[k] == hi[k] && !rr.hole && !hole[k] && k1 <= near;
+            some |= uint32_t(meet) << ((t0 + k) % 32);
+            all |= uint32_t(whole) << ((t0 + k) % 32);
         }
-        if (lane == 0) {
-            out[w] = some;
-            out[words + w] = all;
+        if (lane == 0 && some) {
+            atomicOr(&bits[0], some);
+            atomicOr(&bits[1], all);
         }
+        __syncthreads();
+        if (threadIdx.x < 2) out[threadIdx.x * words + w] = bits[threadIdx.x];
     }
 }
 

@@ -323,6 +323,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
         const int pos = seq.len - seq.tokens + int(token);
         const int bound = !valid ? 0 : p.causal ? pos + 1 : seq.len;
         const float slope = kScore == Score::kAny && p.slopes ? p.slopes[head] : 0.f;
+        // positions of the warp's rows (those behind the last row count as its first one)
+        const int pos_lo = __reduce_min_sync(0xffffffffu, pos), pos_hi = __reduce_max_sync(0xffffffffu, pos);
         float m = -INFINITY, l = 0.f, v_ref = 0x1p-126f, factor = 0.f;
         bool ok = true;
         for (int j = 0; j < (int(t) < tiles ? n_tiles : 0); ++j) {
@@ -348,12 +350,19 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             if (kScore == Score::kCap && whole &&
                 fold_capped_tile<Fused::kFP16, kD, false>(s, f, p.cap, down, j > 0, m, l, s_tmem, o_row, p_half0 + 16 * t))
                 continue;
-            if (kScore != Score::kPlain) finish_scores<kScore>(s, f, p.cap, slope, float(pos - j0));
+            if (kScore != Score::kPlain)
+                finish_scores<kScore>(s, f, p.cap, slope, float(pos - j0), bias_side(pos_lo, pos_hi - pos_lo + 1, j0, int(kAttnRows), p.causal));
             const float to_z = kScore == Score::kPlain ? fmaxf(f * kLog2e, 0x1p-126f) : 1.0f;
             if (!whole) {
+                uint32_t bits[4];
 #pragma unroll
-                for (int x = 0; x < 128; ++x)
-                    s[x] = j0 + x < bound && !((info.bad >> (x / 16)) & 1u) ? s[x] : -INFINITY;
+                for (int x = 0; x < 4; ++x) {
+                    bits[x] = bound_bits(bound, j0 + 32 * x);
+                    if ((info.bad >> (2 * x)) & 1u) bits[x] &= 0xffff0000u;
+                    if ((info.bad >> (2 * x)) & 2u) bits[x] &= 0x0000ffffu;
+                }
+#pragma unroll
+                for (int x = 0; x < 128; ++x) s[x] = (bits[x / 32] >> (x % 32)) & 1u ? s[x] : -INFINITY;
             }
             fold_tile<Fused::kFP16, kD>(s, to_z, down, j > 0, m, l, s_tmem, o_row, p_half0 + 16 * t);
         }
