@@ -28,6 +28,12 @@ namespace {
 using namespace dev;
 
 constexpr int kThreadsB = 384;
+
+// compile-time switches of the inner loops
+template <bool kV>
+struct Bool {
+    static constexpr bool value = kV;
+};
 constexpr uint32_t kHalfTile = kAttnRows * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
 constexpr int kExactTiles = 4;
 
@@ -337,19 +343,23 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 const float at = kBias && side != 0 ? less - float(side) * slope2 * float(pos - j0) : less;
                 const uint64_t at2 = f2_pack(at, at), by2 = f2_pack(float(side) * slope2, float(side) * slope2);
                 const ToWeight<kCap> weight(p, s);
+                auto weights = [&](auto linear) {
 #pragma unroll
-                for (int x = 0; x < 64; x += 2) {
-                    uint64_t add = at2;
-                    if constexpr (kBias) {
-                        if (side != 0)
+                    for (int x = 0; x < 64; x += 2) {
+                        uint64_t add = at2;
+                        if constexpr (kBias && decltype(linear)::value)
                             add = f2_fma(f2_pack(float(x), float(x + 1)), by2, at2);
-                        else
+                        else if constexpr (kBias)
                             add = f2_pack(fmaf(-slope2, fabsf(float(pos - j0 - x)), less), fmaf(-slope2, fabsf(float(pos - j0 - x - 1)), less));
+                        f2_unpack(weight(f2_pack(s[x], s[x + 1]), add, bend[kCap ? x / 2 : 0]), s[x], s[x + 1]);
+                        s[x] = ex2(s[x]);
+                        s[x + 1] = ex2(s[x + 1]);
                     }
-                    f2_unpack(weight(f2_pack(s[x], s[x + 1]), add, bend[kCap ? x / 2 : 0]), s[x], s[x + 1]);
-                    s[x] = ex2(s[x]);
-                    s[x + 1] = ex2(s[x + 1]);
-                }
+                };
+                if (!kBias || side != 0)
+                    weights(Bool<true>{});
+                else
+                    weights(Bool<false>{});
                 const bool whole = __all_sync(0xffffffffu, plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + 64 <= bound);
                 uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
                 if (!whole) {
@@ -438,7 +448,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
 //  * warp 8, one lane: TMA.  K and V once, Q and dO blocks through a ring.
 //  * warp 9, one lane: S(n+1) = K Q^T and dP(n+1) = V dO^T into the other pair of
 //    buffers, then dV += P(n) dO, dK += dx(n) Q (P, dx from TMEM, dO, Q MN-major).
-//  * warp 10: the queries' log-sum-exp, delta, bounds and documents into shared memory.
+//  * warps 10 and 11: the queries' log-sum-exp, delta, bounds and documents into shared memory.
 //  * warps 0-3 take the even blocks, warps 4-7 the odd ones: a thread per key row.
 // P goes over S, dx over dP, both in 16 bits.  fp16: P is kept times 2^8, away from
 // fp16's subnormals (weights of a long row are about 1 / Sk).
@@ -458,8 +468,8 @@ struct DkvShape {
     static constexpr uint32_t kTile = kHalfTile * (kD / 64);
     static constexpr uint32_t kBlock = kTile / 2;         // 64 queries
     static constexpr uint32_t kHalfBlock = kHalfTile / 2;
-    static constexpr int kStages = 8;
-    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kBlock + kStatSlots * sizeof(QueryStats) + 512 + 1024;
+    static constexpr int kStages = 4;                     // of a block's Q and dO
+    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * 2 * kBlock + kStatSlots * sizeof(QueryStats) + 512 + 1024;
 };
 
 // The blocks of a key tile, in order: query heads outer, tiles of 128 queries that can see
@@ -491,6 +501,15 @@ struct BlockIter {
     }
 };
 
+// Blocks that one query head gives.
+__device__ __forceinline__ uint32_t blocks_of(const uint32_t* words, int first, int q_tiles, int Sq) {
+    const bool odd = Sq > 0 && (Sq - 1) % int(kAttnRows) < int(kQueries);  // the last tile has one block
+    if (!words) return first < q_tiles ? 2 * uint32_t(q_tiles - first) - odd : 0;
+    uint32_t n = 0;
+    for (int w = 0; w * 32 < q_tiles; ++w) n += 2 * __popc(__ldg(words + w));
+    return n - (odd && (__ldg(words + (q_tiles - 1) / 32) >> ((q_tiles - 1) % 32) & 1u));
+}
+
 template <Fused kF, int kD, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant__ BackwardParams bp) {
     using S = DkvShape<kD>;
@@ -500,7 +519,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     const AttentionParams& p = bp.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    QueryStats* stats = reinterpret_cast<QueryStats*>(smem + 2 * size_t(kTile) + kStages * size_t(kBlock));
+    QueryStats* stats = reinterpret_cast<QueryStats*>(smem + 2 * size_t(kTile) + kStages * 2 * size_t(kBlock));
     uint64_t* bars = reinterpret_cast<uint64_t*>(stats + kStatSlots);
     const uint32_t k_smem = smem_u32(smem), v_smem = k_smem + kTile, ring = k_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, kv_full = empty0 + 8 * kStages;
@@ -553,6 +572,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     const uint32_t words = (uint32_t(q_tiles) + 31) / 32;
     const uint32_t* plan = p.plan ? p.plan + (size_t(b) * bp.k_tiles + kt) * 2 * words : nullptr;
     BlockIter it(plan, first, q_tiles, int(p.Sq), p.shared);
+    const uint32_t blocks = p.shared * blocks_of(plan, first, q_tiles, int(p.Sq));
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -570,17 +590,18 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         const bool any = i0 >= 0;
         for (; ok && i0 >= 0; i0 = it.next()) {
             const int h = int(kh * p.shared + it.head);
-            for (int qd = 0; qd < 2; ++qd, ++n) {
-                const uint32_t s = n % kStages, use = n / kStages;
-                if (use > 0 && !wait_for(empty0 + 8 * s, (use - 1) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                mbar_expect_tx(full0 + 8 * s, kBlock);
-                for (int x = 0; x < kD / 64; ++x)
-                    tma_load_4d(ring + s * kBlock + x * kHalfBlock, qd == 0 ? &bp.q_half.m[g] : &bp.dout_half.m[g], x * 64, h, i0,
-                                int(b), full0 + 8 * s);
+            const uint32_t s = n % kStages, use = n / kStages;
+            ++n;
+            if (use > 0 && !wait_for(empty0 + 8 * s, (use - 1) & 1u, abort_flag)) {
+                ok = false;
+                --n;
+                break;
             }
+            mbar_expect_tx(full0 + 8 * s, 2 * kBlock);
+            for (int qd = 0; qd < 2; ++qd)
+                for (int x = 0; x < kD / 64; ++x)
+                    tma_load_4d(ring + (2 * s + qd) * kBlock + x * kHalfBlock, qd == 0 ? &bp.q_half.m[g] : &bp.dout_half.m[g], x * 64,
+                                h, i0, int(b), full0 + 8 * s);
         }
         if (any) drain_phase(kv_full, 0);
         for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
@@ -588,66 +609,73 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     } else if (warp == 9 && elect_one()) {
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kQueries, false);
         constexpr uint32_t kIdescD = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
-        auto landed = [&](uint32_t k) { return wait_for(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag); };
         const uint32_t k_low = desc_low(k_smem), v_low = desc_low(v_smem), n_low = desc_low(ring),
                        t_low = desc_low(ring, kHalfBlock);
-        auto offset = [&](uint32_t k) { return (k % kStages) * (kBlock >> 4); };
-        auto transposed = [&](int n) {  // S and dP of block n
-            if (!landed(2 * n) || !landed(2 * n + 1)) return false;
+        auto transposed = [&](uint32_t n) {  // S and dP of block n
+            const uint32_t s = n % kStages;
+            if (!wait_for(full0 + 8 * s, (n / kStages) & 1u, abort_flag)) return false;
             tc_fence_after();
-            const uint32_t d = tmem + (n & 1) * 2 * kQueries;
-            tc_product<kD, kHalfTile, kHalfBlock>(d, k_low, n_low + offset(2 * n), kIdescS);
-            tc_product<kD, kHalfTile, kHalfBlock>(d + kQueries, v_low, n_low + offset(2 * n + 1), kIdescS);
+            const uint32_t d = tmem + (n & 1) * 2 * kQueries, q = n_low + s * (2 * kBlock >> 4);
+            tc_product<kD, kHalfTile, kHalfBlock>(d, k_low, q, kIdescS);
+            tc_product<kD, kHalfTile, kHalfBlock>(d + kQueries, v_low, q + (kBlock >> 4), kIdescS);
             tc_commit(s_full0 + 8 * (n & 1));
             return true;
         };
-        bool more = it.next() >= 0;
-        bool ok = !more || (wait_for(kv_full, 0, abort_flag) && transposed(0));
-        for (int n = 0; ok && more; ++n) {
-            more = it.next() >= 0;
-            if (more && !(ok = transposed(n + 1))) break;
+        bool ok = blocks == 0 || (wait_for(kv_full, 0, abort_flag) && transposed(0));
+        for (uint32_t n = 0; ok && n < blocks; ++n) {
+            if (n + 1 < blocks && !(ok = transposed(n + 1))) break;
             if (!(ok = wait_for(dx_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag))) break;
             tc_fence_after();
-            const uint32_t a = tmem + (n & 1) * 2 * kQueries;
-            tc_product_ts<kQueries>(dv_tmem, a, t_low + offset(2 * n + 1), kIdescD, uint32_t(n));         // dV += P dO
-            tc_product_ts<kQueries>(dk_tmem, a + kQueries, t_low + offset(2 * n), kIdescD, uint32_t(n));  // dK += dx Q
-            tc_commit(empty0 + 8 * (2 * n % kStages));
-            tc_commit(empty0 + 8 * ((2 * n + 1) % kStages));
+            const uint32_t a = tmem + (n & 1) * 2 * kQueries, q = t_low + n % kStages * (2 * kBlock >> 4);
+            tc_product_ts<kQueries>(dv_tmem, a, q + (kBlock >> 4), kIdescD, n);  // dV += P dO
+            tc_product_ts<kQueries>(dk_tmem, a + kQueries, q, kIdescD, n);       // dK += dx Q
+            tc_commit(empty0 + 8 * (n % kStages));
         }
         tc_commit(done);
         drain_phase(done, 0);
-    } else if (warp == 10) {
+    } else if (warp >= 10) {
         uint32_t n = 0;
         for (int i0 = it.next(); i0 >= 0; i0 = it.next(), ++n) {
+            if ((n & 1u) != (warp & 1u)) continue;
+            // two queries a lane; what is read is on its way before the slot is free
+            const int64_t stat = (int64_t(b) * p.Hl + kh * p.shared + it.head) * p.Sq;
+            const float slope2 = kBias && p.slopes ? p.slopes[g * p.Hl + kh * p.shared + it.head] * kLog2e : 0.f;
+            const int side = kBias ? bias_side(i0 + ahead, int(kQueries), row0, int(kAttnRows), p.causal && !p.prefix) : 0;
+            float less[2], delta[2];
+            int bound[2], doc[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int i = i0 + int(lane) + 32 * x;
+                less[x] = -INFINITY;  // no such query: weight 0
+                delta[x] = 0.f;
+                bound[x] = 0;
+                doc[x] = -1;
+                if (i < int(p.Sq)) {
+                    const float lse = p.lse[g][stat + i];
+                    delta[x] = -kDown * p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat + i];
+                    bound[x] = key_bound(p, b, i);
+                    if (plan) {
+                        doc[x] = p.q_docs[int64_t(b) * p.Sq + i];
+                        if (doc[x] < 0) {
+                            bound[x] = 0;
+                            delta[x] = 0.f;
+                        }
+                    }
+                    if (lse != -INFINITY) less[x] = kUp - lse * kLog2e - float(side * (int(lane) + 32 * x)) * slope2;
+                }
+            }
             if (n >= uint32_t(kStatSlots)) {  // block n - kStatSlots has been computed
                 const bool ok = wait_for(stat_free0 + 8 * (n % kStatSlots), (n / kStatSlots - 1) & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) break;
             }
-            const int64_t stat = (int64_t(b) * p.Hl + kh * p.shared + it.head) * p.Sq;
-            const float slope2 = kBias && p.slopes ? p.slopes[g * p.Hl + kh * p.shared + it.head] * kLog2e : 0.f;
-            const int side = kBias ? bias_side(i0 + ahead, int(kQueries), row0, int(kAttnRows), p.causal && !p.prefix) : 0;
             QueryStats& st = stats[n % kStatSlots];
-            for (int x = int(lane); x < int(kQueries); x += 32) {
-                const int i = i0 + x;
-                float less = -INFINITY, delta = 0.f;  // no such query: weight 0
-                int bound = 0, doc = -1;
-                if (i < int(p.Sq)) {
-                    const float lse = p.lse[g][stat + i];
-                    less = lse == -INFINITY ? -INFINITY : kUp - lse * kLog2e - float(side * x) * slope2;
-                    delta = -kDown * p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat + i];
-                    bound = key_bound(p, b, i);
-                    if (plan) {
-                        doc = p.q_docs[int64_t(b) * p.Sq + i];
-                        if (doc < 0) {
-                            bound = 0;
-                            delta = 0.f;
-                        }
-                    }
-                }
-                st.less[x] = less;
-                st.delta[x] = delta;
-                st.bound[x] = bound;
-                st.doc[x] = doc;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int at = int(lane) + 32 * x;
+                st.less[at] = less[x];
+                st.delta[at] = delta[x];
+                st.bound[at] = bound[x];
+                st.doc[at] = doc[x];
             }
             warp_arrive(stat_full0 + 8 * (n % kStatSlots));
         }
@@ -698,7 +726,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                 if (plan && r < kQueries && st.doc[r] < 0) {
                     for (int qd = 0; qd < 2; ++qd) {
                         uint4* row = reinterpret_cast<uint4*>(smem + 2 * size_t(kTile) +
-                                                              ((2 * n + qd) % kStages) * size_t(kBlock) + r * kSwizzleRow);
+                                                              (2 * (n % kStages) + qd) * size_t(kBlock) + r * kSwizzleRow);
                         for (int x = 0; x < kD / 64; ++x)
                             for (int y = 0; y < 8; ++y) row[x * (kHalfBlock / 16) + y] = make_uint4(0, 0, 0, 0);
                     }
@@ -706,37 +734,44 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                 if (plan) fence_async_shared();
             }
             load_row<64>(dp_row, d);
-            if (!whole) {
+            auto gradients = [&](auto masked, auto linear) {
 #pragma unroll
-                for (int x = 0; x < 64; ++x) d[x] = (bits[x / 32] >> (x % 32)) & 1u ? d[x] : 0.f;
-            }
+                for (int x = 0; x < 64; x += 4) {
+                    const float4 less = *reinterpret_cast<const float4*>(st.less + x),
+                                 nd = *reinterpret_cast<const float4*>(st.delta + x);
 #pragma unroll
-            for (int x = 0; x < 64; x += 4) {
-                const float4 less = *reinterpret_cast<const float4*>(st.less + x), nd = *reinterpret_cast<const float4*>(st.delta + x);
-#pragma unroll
-                for (int y = 0; y < 4; y += 2) {
-                    const int e = x + y;
-                    const float l0 = y ? less.z : less.x, l1 = y ? less.w : less.y;
-                    uint64_t add = f2_pack(l0, l1), bend = 0;
-                    if constexpr (kBias) {
-                        if (side != 0)
+                    for (int y = 0; y < 4; y += 2) {
+                        const int e = x + y;
+                        const float l0 = y ? less.z : less.x, l1 = y ? less.w : less.y;
+                        uint64_t add = f2_pack(l0, l1), bend = 0;
+                        if constexpr (kBias && decltype(linear)::value)
                             add = f2_add(add, own2);
-                        else
+                        else if constexpr (kBias)
                             add = f2_pack(fmaf(-slope2, fabsf(far + float(e)), l0), fmaf(-slope2, fabsf(far + float(e + 1)), l1));
+                        f2_unpack(weight(f2_pack(s[e], s[e + 1]), add, bend), s[e], s[e + 1]);
+                        s[e] = ex2(s[e]);
+                        s[e + 1] = ex2(s[e + 1]);
+                        if constexpr (decltype(masked)::value) {
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const bool see = (bits[e / 32] >> (e % 32 + z)) & 1u;
+                                s[e + z] = see ? s[e + z] : 0.f;
+                                d[e + z] = see ? d[e + z] : 0.f;
+                            }
+                        }
+                        const uint64_t off = y ? f2_pack(nd.z, nd.w) : f2_pack(nd.x, nd.y), d2 = f2_pack(d[e], d[e + 1]);
+                        uint64_t dx = f2_mul(f2_pack(s[e], s[e + 1]), kF == Fused::kFP16 ? f2_fma(d2, down2, off) : f2_add(d2, off));
+                        if constexpr (kCap) dx = f2_mul(dx, bend);
+                        f2_unpack(dx, d[e], d[e + 1]);
                     }
-                    f2_unpack(weight(f2_pack(s[e], s[e + 1]), add, bend), s[e], s[e + 1]);
-                    s[e] = ex2(s[e]);
-                    s[e + 1] = ex2(s[e + 1]);
-                    if (!whole) {
-                        s[e] = (bits[e / 32] >> (e % 32)) & 1u ? s[e] : 0.f;
-                        s[e + 1] = (bits[e / 32] >> (e % 32 + 1)) & 1u ? s[e + 1] : 0.f;
-                    }
-                    const uint64_t off = y ? f2_pack(nd.z, nd.w) : f2_pack(nd.x, nd.y), d2 = f2_pack(d[e], d[e + 1]);
-                    uint64_t dx = f2_mul(f2_pack(s[e], s[e + 1]), kF == Fused::kFP16 ? f2_fma(d2, down2, off) : f2_add(d2, off));
-                    if constexpr (kCap) dx = f2_mul(dx, bend);
-                    f2_unpack(dx, d[e], d[e + 1]);
                 }
-            }
+            };
+            if (whole && (!kBias || side != 0))
+                gradients(Bool<false>{}, Bool<true>{});
+            else if (!kBias || side != 0)
+                gradients(Bool<true>{}, Bool<true>{});
+            else
+                gradients(Bool<true>{}, Bool<false>{});
             store_row16<kF, 64>(s_row, s);
             store_row16<kF, 64>(dp_row, d);
             tc_wait_st();
