@@ -27,7 +27,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreadsB = 384;
+constexpr int kThreadsB = 640;  // 16 warps for the rows, 4 for the rest
 
 // compile-time switches of the inner loops
 template <bool kV>
@@ -89,11 +89,11 @@ __device__ __forceinline__ void store_row16(uint32_t taddr, const float (&v)[kN]
     }
 }
 
-// kD accumulator columns times `factor` to a row of 16-bit values
-template <Fused kF, int kD>
+// kCols accumulator columns times `factor` to a row of 16-bit values
+template <Fused kF, int kCols>
 __device__ __forceinline__ void write_row(uint32_t taddr, bool any, bool valid, float factor, uint8_t* dst) {
 #pragma unroll 1
-    for (int x = 0; x < kD; x += 32) {
+    for (int x = 0; x < kCols; x += 32) {
         uint32_t r[32];
         if (any) {
             tc_ld32(taddr + x, r);
@@ -138,17 +138,17 @@ __device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b) {
 
 // ---------------------------------------------------------------- dQ
 // One CTA: 128 query rows of one head, tiles of 128 keys.
-//  * warp 8, one lane: TMA.  Q and dO once, K and V through a ring K0 V0 K1 V1 ...
-//  * warp 9, one lane: S(j+1) = Q K^T into the other S buffer, dP(j+1) = dO V^T once
+//  * warp 16, one lane: TMA.  Q and dO once, K and V through a ring K0 V0 K1 V1 ...
+//  * warp 17, one lane: S(j+1) = Q K^T into the other S buffer, dP(j+1) = dO V^T once
 //    dP(j) has been read, dQ += dx(j) K (dx from TMEM, K read MN-major).
-//  * warps 0-3 and 4-7: a thread per row and half of the tile's keys; dx in 16 bits goes
+//  * warps 0-15: a thread per row and quarter of the tile's keys; dx in 16 bits goes
 //    over the scores it came from.
 // TMEM: S0 S1 dP (128 columns each), dQ (D columns).
 template <int kD>
 struct DqShape {
     static constexpr uint32_t kTile = kHalfTile * (kD / 64);
     static constexpr int kStages = kD == 128 ? 4 : 8;
-    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kTile + 1024 + 512 + 1024;  // + the rows' sums, barriers, alignment
+    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kTile + 2048 + 512 + 1024;  // + the rows' sums, barriers, alignment
 };
 
 template <Fused kF, int kD, bool kCap, bool kBias>
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     const AttentionParams& p = bp.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* sums = reinterpret_cast<float*>(smem + (2 + kStages) * size_t(kTile));  // [2][128]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sums + 2 * kAttnRows);
+    float* sums = reinterpret_cast<float*>(smem + (2 + kStages) * size_t(kTile));  // [4][128]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sums + 4 * kAttnRows);
     const uint32_t q_smem = smem_u32(smem), do_smem = q_smem + kTile, ring = q_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
     const uint32_t s_full0 = q_full + 8, dp_full = s_full0 + 16, dp_free = dp_full + 8, dx_full = dp_free + 8;
@@ -185,14 +185,14 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         mbar_init(s_full0, 1);
         mbar_init(s_full0 + 8, 1);
         mbar_init(dp_full, 1);
-        mbar_init(dp_free, 8);  // a warp each
-        mbar_init(dx_full, 8);
-        mbar_init(sums_full, 2 * kAttnRows);
+        mbar_init(dp_free, 16);  // a warp each
+        mbar_init(dx_full, 16);
+        mbar_init(sums_full, 4 * kAttnRows);
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -215,9 +215,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     }
     const bool exact = visits <= kExactTiles;  // two phases: delta from P dP, then dQ
 
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8 && elect_one()) {
+    if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");  // 640 * 96 at launch >= 512 * 104 + 128 * 56
+    if (warp == 16 && elect_one()) {
         const CUtensorMap* maps[2] = {&bp.k.m[g], &bp.v.m[g]};
         const int kh = int(h / p.shared);
         uint32_t n = 0;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         if (visits > 0) drain_phase(q_full, 0);
         for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
             drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
-    } else if (warp == 9 && elect_one()) {
+    } else if (warp == 17 && elect_one()) {
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
         constexpr uint32_t kIdescQ = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
         const int steps = exact ? 2 * visits : visits;
@@ -287,9 +287,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             if (!sums_only) {
                 const uint32_t a = tmem + (i & 1) * kAttnRows;
                 const bool first = i == (exact ? visits : 0);
-                // the two halves of the keys lie 64 columns apart
-                tc_product_ts<kAttnRows / 2>(dq_tmem, a, k_low + offset(2 * i), kIdescQ, !first);
-                tc_product_ts<kAttnRows / 2>(dq_tmem, a + 64, k_low + offset(2 * i) + (64 * kSwizzleRow >> 4), kIdescQ, 1u);
+#pragma unroll
+                for (uint32_t x = 0; x < 4; ++x)  // the quarters of the keys lie 32 columns apart
+                    tc_product_ts<32>(dq_tmem, a + 32 * x, k_low + offset(2 * i) + (32 * x * kSwizzleRow >> 4), kIdescQ, !first || x != 0);
             }
             tc_commit(empty0 + 8 * (2 * i % kStages));
         }
@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         drain_phase(done, 0);
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const uint32_t half = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const uint32_t part = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;  // part: 32 keys of the tile
         const int i = row0 + int(r);
         const bool valid = i < int(p.Sq);
         const uint32_t lane_base = (quarter * 32u) << 16;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             delta = row_dot<kF, kD>(p.dout.base[g] + b * p.dout.b + at * p.dout.t + h * p.dout.h,
                                     p.out.base[g] + b * p.out.b + at * p.out.t + h * p.out.h);
             if (p.plan && doc < 0) delta = 0.f;  // padding: its output gradient may be anything
-            if (half == 0) *delta_at = delta;
+            if (part == 0) *delta_at = delta;
         }
         bool ok = true;
         int n = 0;
@@ -327,25 +327,25 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             TileIter it(plan, n_tiles);
             float sum = 0.f;
             for (int j = it.next(); j >= 0; j = it.next(), ++n) {
-                const uint32_t s_row = tmem + (n & 1) * kAttnRows + half * 64 + lane_base;
+                const uint32_t s_row = tmem + (n & 1) * kAttnRows + part * 32 + lane_base;
                 ok = wait_for(s_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const int j0 = j * int(kAttnRows) + int(half) * 64;
-                float s[64];
-                uint64_t bend[kCap ? 32 : 1];
-                load_row<64>(s_row, s);
+                const int j0 = j * int(kAttnRows) + int(part) * 32;
+                float s[32];
+                uint64_t bend[kCap ? 16 : 1];
+                load_row<32>(s_row, s);
                 const int pos = i + int(p.Sk) - int(p.Sq), pos0 = row0 + int(p.Sk) - int(p.Sq);
-                const int side = kBias ? bias_side(pos0, int(kAttnRows), j0, 64, p.causal && !p.prefix) : 1;
+                const int side = kBias ? bias_side(pos0, int(kAttnRows), j0, 32, p.causal && !p.prefix) : 1;
                 const float at = kBias && side != 0 ? less - float(side) * slope2 * float(pos - j0) : less;
                 const uint64_t at2 = f2_pack(at, at), by2 = f2_pack(float(side) * slope2, float(side) * slope2);
                 const ToWeight<kCap> weight(p, s);
                 auto weights = [&](auto linear) {
 #pragma unroll
-                    for (int x = 0; x < 64; x += 2) {
+                    for (int x = 0; x < 32; x += 2) {
                         uint64_t add = at2;
                         if constexpr (kBias && decltype(linear)::value)
                             add = f2_fma(f2_pack(float(x), float(x + 1)), by2, at2);
@@ -360,30 +360,25 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                     weights(Bool<true>{});
                 else
                     weights(Bool<false>{});
-                const bool whole = __all_sync(0xffffffffu, plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + 64 <= bound);
-                uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+                const bool whole = __all_sync(0xffffffffu, plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + 32 <= bound);
+                uint32_t bits[1] = {0xffffffffu};
                 if (!whole) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) bits[x] = bound_bits(bound, j0 + 32 * x);
+                    bits[0] = bound_bits(bound, j0);
                     if (plan) {
-                        int32_t kd[2];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int key = j0 + x * 32 + int(lane);
-                            kd[x] = key < int(p.Sk) ? __ldg(p.k_docs + int64_t(b) * p.Sk + key) : -1;
-                        }
+                        const int key = j0 + int(lane);
+                        const int32_t kd[1] = {key < int(p.Sk) ? __ldg(p.k_docs + int64_t(b) * p.Sk + key) : -1};
                         keep_document(bits, kd, doc);
                         // padding's K rows may hold anything: clear them for the product with dx
-                        if (quarter < 2 && (quarter == 0 ? kd[0] : kd[1]) < 0) {
+                        if (quarter == 0 && kd[0] < 0) {
                             uint4* k = reinterpret_cast<uint4*>(smem + (2 + 2 * n % kStages) * size_t(kTile) +
-                                                                (half * 64 + quarter * 32 + lane) * kSwizzleRow);
+                                                                (part * 32 + lane) * kSwizzleRow);
                             for (int x = 0; x < kD / 64; ++x)
                                 for (int y = 0; y < 8; ++y) k[x * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
                         }
                         fence_async_shared();
                     }
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) s[x] = (bits[x / 32] >> (x % 32)) & 1u ? s[x] : 0.f;
+                    for (int x = 0; x < 32; ++x) s[x] = (bits[0] >> x) & 1u ? s[x] : 0.f;
                 }
                 ok = wait_for(dp_full, n & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -391,51 +386,51 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                     break;
                 }
                 tc_fence_after();
-                float d[64];
-                load_row<64>(dp_tmem + half * 64 + lane_base, d);
+                float d[32];
+                load_row<32>(dp_tmem + part * 32 + lane_base, d);
                 warp_arrive(dp_free);
                 if (!whole) {
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) d[x] = (bits[x / 32] >> (x % 32)) & 1u ? d[x] : 0.f;
+                    for (int x = 0; x < 32; ++x) d[x] = (bits[0] >> x) & 1u ? d[x] : 0.f;
                 }
                 if (phase == 0) {
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) sum = fmaf(s[x], d[x], sum);
+                    for (int x = 0; x < 32; ++x) sum = fmaf(s[x], d[x], sum);
                 } else {
                     const uint64_t nd = f2_pack(-delta, -delta);
 #pragma unroll
-                    for (int x = 0; x < 64; x += 2) {
+                    for (int x = 0; x < 32; x += 2) {
                         uint64_t dx = f2_mul(f2_pack(s[x], s[x + 1]), f2_add(f2_pack(d[x], d[x + 1]), nd));
                         if constexpr (kCap) dx = f2_mul(dx, bend[x / 2]);
                         f2_unpack(dx, d[x], d[x + 1]);
                     }
-                    store_row16<kF, 64>(s_row, d);
+                    store_row16<kF, 32>(s_row, d);
                     tc_wait_st();
                 }
                 warp_arrive(dx_full);
             }
-            if (phase == 0 && ok) {  // the two halves of the row
-                sums[half * kAttnRows + r] = sum;
+            if (phase == 0 && ok) {  // the four parts of the row
+                sums[part * kAttnRows + r] = sum;
                 mbar_arrive(sums_full);
                 ok = wait_for(sums_full, 0, abort_flag);
-                delta = sums[r] + sums[kAttnRows + r];
-                if (half == 0 && valid) *delta_at = delta;
+                delta = (sums[r] + sums[kAttnRows + r]) + (sums[2 * kAttnRows + r] + sums[3 * kAttnRows + r]);
+                if (part == 0 && valid) *delta_at = delta;
                 ok = __all_sync(0xffffffffu, ok);
             }
         }
-        if (ok && half == 0) {
+        if (ok && part < kD / 32) {
             ok = wait_for(done, 0, abort_flag);
             if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
                 tc_fence_after();
-                write_row<kF, kD>(dq_tmem + lane_base, visits > 0, valid, p.scale,
-                                  p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h);
+                write_row<kF, 32>(dq_tmem + lane_base + part * 32, visits > 0, valid, p.scale,
+                                  p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h + part * 64);
             }
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -445,11 +440,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
 // One CTA: 128 key rows of one key head, blocks of 64 queries of every query head that
 // shares it.  Scores are taken transposed, keys on the TMEM lanes, so that P and dx
 // are operands as they stand:
-//  * warp 8, one lane: TMA.  K and V once, Q and dO blocks through a ring.
-//  * warp 9, one lane: S(n+1) = K Q^T and dP(n+1) = V dO^T into the other pair of
+//  * warp 16, one lane: TMA.  K and V once, Q and dO blocks through a ring.
+//  * warp 17, one lane: S(n+1) = K Q^T and dP(n+1) = V dO^T into the other pair of
 //    buffers, then dV += P(n) dO, dK += dx(n) Q (P, dx from TMEM, dO, Q MN-major).
-//  * warps 10 and 11: the queries' log-sum-exp, delta, bounds and documents into shared memory.
-//  * warps 0-3 take the even blocks, warps 4-7 the odd ones: a thread per key row.
+//  * warps 18 and 19: the queries' log-sum-exp, delta, bounds and documents into shared memory.
+//  * warps 0-3 and 8-11 take the even blocks, warps 4-7 and 12-15 the odd ones: a thread per
+//    key row and half of the block's queries.
 // P goes over S, dx over dP, both in 16 bits.  fp16: P is kept times 2^8, away from
 // fp16's subnormals (weights of a long row are about 1 / Sk).
 // TMEM: S0 dP0 S1 dP1 (64 columns each), dK, dV (D columns each).
@@ -543,17 +539,17 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         mbar_init(kv_full, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full0 + 8 * t, 1);
-            mbar_init(dx_full0 + 8 * t, 4);  // a warp each
+            mbar_init(dx_full0 + 8 * t, 8);  // a warp each
         }
         for (int t = 0; t < kStatSlots; ++t) {
             mbar_init(stat_full0 + 8 * t, 1);
-            mbar_init(stat_free0 + 8 * t, 4);
+            mbar_init(stat_free0 + 8 * t, 8);
         }
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -574,9 +570,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     BlockIter it(plan, first, q_tiles, int(p.Sq), p.shared);
     const uint32_t blocks = p.shared * blocks_of(plan, first, q_tiles, int(p.Sq));
 
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8 && elect_one()) {
+    if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");  // 640 * 96 at launch >= 512 * 104 + 128 * 56
+    if (warp == 16 && elect_one()) {
         uint32_t n = 0;
         bool ok = true;
         int i0 = it.next();
@@ -606,7 +602,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         if (any) drain_phase(kv_full, 0);
         for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
             drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
-    } else if (warp == 9 && elect_one()) {
+    } else if (warp == 17 && elect_one()) {
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kQueries, false);
         constexpr uint32_t kIdescD = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
         const uint32_t k_low = desc_low(k_smem), v_low = desc_low(v_smem), n_low = desc_low(ring),
@@ -627,13 +623,17 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
             if (!(ok = wait_for(dx_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag))) break;
             tc_fence_after();
             const uint32_t a = tmem + (n & 1) * 2 * kQueries, q = t_low + n % kStages * (2 * kBlock >> 4);
-            tc_product_ts<kQueries>(dv_tmem, a, q + (kBlock >> 4), kIdescD, n);  // dV += P dO
-            tc_product_ts<kQueries>(dk_tmem, a + kQueries, q, kIdescD, n);       // dK += dx Q
+#pragma unroll
+            for (uint32_t x = 0; x < 2; ++x)  // dV += P dO; the halves of the queries lie 32 columns apart
+                tc_product_ts<32>(dv_tmem, a + 32 * x, q + (kBlock >> 4) + (32 * x * kSwizzleRow >> 4), kIdescD, n | x);
+#pragma unroll
+            for (uint32_t x = 0; x < 2; ++x)  // dK += dx Q
+                tc_product_ts<32>(dk_tmem, a + kQueries + 32 * x, q + (32 * x * kSwizzleRow >> 4), kIdescD, n | x);
             tc_commit(empty0 + 8 * (n % kStages));
         }
         tc_commit(done);
         drain_phase(done, 0);
-    } else if (warp >= 10) {
+    } else if (warp >= 18) {
         uint32_t n = 0;
         for (int i0 = it.next(); i0 >= 0; i0 = it.next(), ++n) {
             if ((n & 1u) != (warp & 1u)) continue;
@@ -681,13 +681,13 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         }
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const uint32_t t = warp / 4, quarter = warp % 4, r = quarter * 32 + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const uint32_t t = warp / 4 % 2, half = warp / 8, quarter = warp % 4, r = quarter * 32 + lane;
         const int j = row0 + int(r);
         const bool valid = j < int(p.Sk);
         const uint32_t lane_base = (quarter * 32u) << 16;
         const int32_t doc = plan && valid ? p.k_docs[int64_t(b) * p.Sk + j] : -1;
-        const uint32_t s_row = tmem + t * 2 * kQueries + lane_base, dp_row = s_row + kQueries;
+        const uint32_t s_row = tmem + t * 2 * kQueries + 32 * half + lane_base, dp_row = s_row + kQueries;
         bool ok = true;
         uint32_t n = 0;
         for (int i0 = it.next(); i0 >= 0; i0 = it.next(), ++n) {
@@ -703,27 +703,29 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
             const QueryStats& st = stats[slot];
             const float slope2 = kBias && p.slopes ? p.slopes[g * p.Hl + kh * p.shared + it.head] * kLog2e : 0.f;
             const int side = kBias ? bias_side(i0 + ahead, int(kQueries), row0, int(kAttnRows), p.causal && !p.prefix) : 0;
-            const float far = float(i0 + ahead - j), own = -float(side) * slope2 * far;
+            // the query's part of the bias counts from the block's first one
+            const float far = float(i0 + int(32 * half) + ahead - j), own = -float(side) * slope2 * float(i0 + ahead - j);
             const uint64_t own2 = f2_pack(own, own), down2 = f2_pack(kDown, kDown);
-            float s[64], d[64];
-            load_row<64>(s_row, s);
+            float s[32], d[32];
+            load_row<32>(s_row, s);
             const ToWeight<kCap> weight(p, s);
             const int qt = i0 / int(kAttnRows);
             const bool whole = plan ? (__ldg(plan + words + (qt >> 5)) >> (qt & 31)) & 1u  // the same for every thread
                                     : i0 + int(kQueries) <= int(p.Sq) && row0 + int(kAttnRows) <= st.bound[0];
-            uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+            uint32_t bits = 0xffffffffu;
             if (!whole) {
 #pragma unroll
-                for (int x = 0; x < 64; x += 4) {
-                    const int4 bound = *reinterpret_cast<const int4*>(st.bound + x), doc4 = *reinterpret_cast<const int4*>(st.doc + x);
+                for (int x = 0; x < 32; x += 4) {
+                    const int4 bound = *reinterpret_cast<const int4*>(st.bound + 32 * half + x),
+                               doc4 = *reinterpret_cast<const int4*>(st.doc + 32 * half + x);
                     const int* bo = &bound.x;
                     const int* dc = &doc4.x;
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
-                        if (j >= bo[y] || (plan && dc[y] != doc)) bits[x / 32] &= ~(1u << ((x + y) % 32));
+                        if (j >= bo[y] || (plan && dc[y] != doc)) bits &= ~(1u << (x + y));
                 }
                 // padding's Q and dO rows may hold anything: clear them for the products with dx and P
-                if (plan && r < kQueries && st.doc[r] < 0) {
+                if (plan && half == 0 && r < kQueries && st.doc[r] < 0) {
                     for (int qd = 0; qd < 2; ++qd) {
                         uint4* row = reinterpret_cast<uint4*>(smem + 2 * size_t(kTile) +
                                                               (2 * (n % kStages) + qd) * size_t(kBlock) + r * kSwizzleRow);
@@ -733,12 +735,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                 }
                 if (plan) fence_async_shared();
             }
-            load_row<64>(dp_row, d);
+            load_row<32>(dp_row, d);
             auto gradients = [&](auto masked, auto linear) {
 #pragma unroll
-                for (int x = 0; x < 64; x += 4) {
-                    const float4 less = *reinterpret_cast<const float4*>(st.less + x),
-                                 nd = *reinterpret_cast<const float4*>(st.delta + x);
+                for (int x = 0; x < 32; x += 4) {
+                    const float4 less = *reinterpret_cast<const float4*>(st.less + 32 * half + x),
+                                 nd = *reinterpret_cast<const float4*>(st.delta + 32 * half + x);
 #pragma unroll
                     for (int y = 0; y < 4; y += 2) {
                         const int e = x + y;
@@ -754,7 +756,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                         if constexpr (decltype(masked)::value) {
 #pragma unroll
                             for (int z = 0; z < 2; ++z) {
-                                const bool see = (bits[e / 32] >> (e % 32 + z)) & 1u;
+                                const bool see = (bits >> (e + z)) & 1u;
                                 s[e + z] = see ? s[e + z] : 0.f;
                                 d[e + z] = see ? d[e + z] : 0.f;
                             }
@@ -772,8 +774,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                 gradients(Bool<true>{}, Bool<true>{});
             else
                 gradients(Bool<true>{}, Bool<false>{});
-            store_row16<kF, 64>(s_row, s);
-            store_row16<kF, 64>(dp_row, d);
+            store_row16<kF, 32>(s_row, s);
+            store_row16<kF, 32>(dp_row, d);
             tc_wait_st();
             warp_arrive(dx_full0 + 8 * t);
             if (lane == 0) mbar_arrive(stat_free0 + 8 * slot);
@@ -783,18 +785,19 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
             tc_fence_after();
             const int64_t at = valid ? j : 0;
+            constexpr int kCols = kD / 2;  // of each half of the warps
             if (t == 0)
-                write_row<kF, kD>(dv_tmem + lane_base, n > 0, valid, kDown,
-                                  p.dv.base[g] + b * p.dv.b + at * p.dv.t + kh * p.dv.h);
+                write_row<kF, kCols>(dv_tmem + lane_base + half * kCols, n > 0, valid, kDown,
+                                     p.dv.base[g] + b * p.dv.b + at * p.dv.t + kh * p.dv.h + half * kCols * 2);
             else
-                write_row<kF, kD>(dk_tmem + lane_base, n > 0, valid, p.scale,
-                                  p.dk.base[g] + b * p.dk.b + at * p.dk.t + kh * p.dk.h);
+                write_row<kF, kCols>(dk_tmem + lane_base + half * kCols, n > 0, valid, p.scale,
+                                     p.dk.base[g] + b * p.dk.b + at * p.dk.t + kh * p.dk.h + half * kCols * 2);
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
