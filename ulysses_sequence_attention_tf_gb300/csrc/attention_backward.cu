@@ -144,23 +144,25 @@ __device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b) {
 //  * warps 0-15: a thread per row and quarter of the tile's keys; dx in 16 bits goes
 //    over the scores it came from.
 // TMEM: S0 S1 dP (128 columns each), dQ (D columns).
+// K is held from S to dQ, about two tiles, V only for dP: three stages and two fill the shared
+// memory at D = 128 (with four shared ones the load of K waited for the dQ product before it).
 template <int kD>
 struct DqShape {
     static constexpr uint32_t kTile = kHalfTile * (kD / 64);
-    static constexpr int kStages = kD == 128 ? 4 : 8;
-    static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * kTile + 2048 + 512 + 1024;  // + the rows' sums, barriers, alignment
+    static constexpr uint32_t kKeyStages = kD == 128 ? 3 : 4, kValueStages = kD == 128 ? 2 : 4;
+    static constexpr uint32_t kStages = kKeyStages + kValueStages;
+    static constexpr size_t kSmem = (2 + kStages) * size_t(kTile) + 512 + 1024;  // + barriers, alignment
 };
 
 template <Fused kF, int kD, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant__ BackwardParams bp) {
     using S = DqShape<kD>;
     constexpr uint32_t kTile = S::kTile;
-    constexpr int kStages = S::kStages;
+    constexpr uint32_t kStages = S::kStages;
     const AttentionParams& p = bp.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* sums = reinterpret_cast<float*>(smem + (2 + kStages) * size_t(kTile));  // [4][128]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sums + 4 * kAttnRows);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kStages) * size_t(kTile));
     const uint32_t q_smem = smem_u32(smem), do_smem = q_smem + kTile, ring = q_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
     const uint32_t s_full0 = q_full + 8, dp_full = s_full0 + 16, dp_free = dp_full + 8, dx_full = dp_free + 8;
@@ -168,6 +170,11 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // stage of tile n of K, of V, and the phase of its barriers
+    auto key_stage = [](uint32_t n) { return n % S::kKeyStages; };
+    auto value_stage = [](uint32_t n) { return S::kKeyStages + n % S::kValueStages; };
+    auto key_phase = [](uint32_t n) { return (n / S::kKeyStages) & 1u; };
+    auto value_phase = [](uint32_t n) { return (n / S::kValueStages) & 1u; };
 
     uint32_t u = blockIdx.x;
     uint32_t qt = u % bp.q_tiles;
@@ -177,7 +184,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     const int row0 = int(qt * kAttnRows);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (uint32_t s = 0; s < kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
@@ -187,7 +194,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         mbar_init(dp_full, 1);
         mbar_init(dp_free, 16);  // a warp each
         mbar_init(dx_full, 16);
-        mbar_init(sums_full, 4 * kAttnRows);
+        mbar_init(sums_full, 16);
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -220,7 +227,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     if (warp == 16 && elect_one()) {
         const CUtensorMap* maps[2] = {&bp.k.m[g], &bp.v.m[g]};
         const int kh = int(h / p.shared);
-        uint32_t n = 0;
+        uint32_t n = 0, loaded[2] = {0, 0};
         bool ok = true;
         if (visits > 0) {
             mbar_expect_tx(q_full, 2 * kTile);
@@ -232,9 +239,10 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         for (int phase = exact ? 0 : 1; phase < 2; ++phase) {
             TileIter it(plan, n_tiles);
             for (int j = it.next(); ok && j >= 0; j = it.next()) {
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const uint32_t s = n % kStages, use = n / kStages;
-                    if (use > 0 && !wait_for(empty0 + 8 * s, (use - 1) & 1u, abort_flag)) {
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t s = kv ? value_stage(n) : key_stage(n), phase_of = kv ? value_phase(n) : key_phase(n);
+                    const bool again = n >= (kv ? S::kValueStages : S::kKeyStages);
+                    if (again && !wait_for(empty0 + 8 * s, phase_of ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -242,35 +250,37 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                     for (int x = 0; x < kD / 64; ++x)
                         tma_load_4d(ring + s * kTile + x * kHalfTile, maps[kv], x * 64, kh, j * int(kAttnRows), int(b),
                                     full0 + 8 * s);
+                    loaded[kv] = n + 1;
                 }
+                ++n;
             }
         }
         if (visits > 0) drain_phase(q_full, 0);
-        for (uint32_t k = n > uint32_t(kStages) ? n - kStages : 0; k < n; ++k)
-            drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
+        for (uint32_t k = loaded[0] > S::kKeyStages ? loaded[0] - S::kKeyStages : 0; k < loaded[0]; ++k)
+            drain_phase(full0 + 8 * key_stage(k), key_phase(k));
+        for (uint32_t k = loaded[1] > S::kValueStages ? loaded[1] - S::kValueStages : 0; k < loaded[1]; ++k)
+            drain_phase(full0 + 8 * value_stage(k), value_phase(k));
     } else if (warp == 17 && elect_one()) {
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
         constexpr uint32_t kIdescQ = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
         const int steps = exact ? 2 * visits : visits;
-        auto landed = [&](uint32_t k) { return wait_for(full0 + 8 * (k % kStages), (k / kStages) & 1u, abort_flag); };
         const uint32_t q_low = desc_low(q_smem), do_low = desc_low(do_smem), kv_low = desc_low(ring),
                        k_low = desc_low(ring, kHalfTile);
-        auto offset = [&](uint32_t k) { return (k % kStages) * (kTile >> 4); };
+        auto offset = [](uint32_t s) { return s * (kTile >> 4); };
         bool ok = steps == 0 || wait_for(q_full, 0, abort_flag);
-        // step i: K at ring tile 2i, V at 2i + 1
         auto scores = [&](int i) {
-            if (!landed(2 * i)) return false;
+            if (!wait_for(full0 + 8 * key_stage(i), key_phase(i), abort_flag)) return false;
             tc_fence_after();
-            tc_product<kD, kHalfTile, kHalfTile>(tmem + (i & 1) * kAttnRows, q_low, kv_low + offset(2 * i), kIdescS);
+            tc_product<kD, kHalfTile, kHalfTile>(tmem + (i & 1) * kAttnRows, q_low, kv_low + offset(key_stage(i)), kIdescS);
             tc_commit(s_full0 + 8 * (i & 1));
             return true;
         };
         auto dp = [&](int i) {
-            if (!landed(2 * i + 1)) return false;
+            if (!wait_for(full0 + 8 * value_stage(i), value_phase(i), abort_flag)) return false;
             tc_fence_after();
-            tc_product<kD, kHalfTile, kHalfTile>(dp_tmem, do_low, kv_low + offset(2 * i + 1), kIdescS);
+            tc_product<kD, kHalfTile, kHalfTile>(dp_tmem, do_low, kv_low + offset(value_stage(i)), kIdescS);
             tc_commit(dp_full);
-            tc_commit(empty0 + 8 * ((2 * i + 1) % kStages));
+            tc_commit(empty0 + 8 * value_stage(i));
             return true;
         };
         if (ok && steps > 0) ok = scores(0) && dp(0);
@@ -289,9 +299,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 const bool first = i == (exact ? visits : 0);
 #pragma unroll
                 for (uint32_t x = 0; x < 4; ++x)  // the quarters of the keys lie 32 columns apart
-                    tc_product_ts<32>(dq_tmem, a + 32 * x, k_low + offset(2 * i) + (32 * x * kSwizzleRow >> 4), kIdescQ, !first || x != 0);
+                    tc_product_ts<32>(dq_tmem, a + 32 * x, k_low + offset(key_stage(i)) + (32 * x * kSwizzleRow >> 4), kIdescQ, !first || x != 0);
             }
-            tc_commit(empty0 + 8 * (2 * i % kStages));
+            tc_commit(empty0 + 8 * key_stage(i));
         }
         tc_commit(done);
         drain_phase(done, 0);
@@ -341,14 +351,15 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 const int pos = i + int(p.Sk) - int(p.Sq), pos0 = row0 + int(p.Sk) - int(p.Sq);
                 const int side = kBias ? bias_side(pos0, int(kAttnRows), j0, 32, p.causal && !p.prefix) : 1;
                 const float at = kBias && side != 0 ? less - float(side) * slope2 * float(pos - j0) : less;
-                const uint64_t at2 = f2_pack(at, at), by2 = f2_pack(float(side) * slope2, float(side) * slope2);
+                const float by = float(side) * slope2;
+                const uint64_t at2 = f2_pack(at, at);
                 const ToWeight<kCap> weight(p, s);
                 auto weights = [&](auto linear) {
 #pragma unroll
                     for (int x = 0; x < 32; x += 2) {
                         uint64_t add = at2;
                         if constexpr (kBias && decltype(linear)::value)
-                            add = f2_fma(f2_pack(float(x), float(x + 1)), by2, at2);
+                            add = f2_pack(fmaf(float(x), by, at), fmaf(float(x + 1), by, at));
                         else if constexpr (kBias)
                             add = f2_pack(fmaf(-slope2, fabsf(float(pos - j0 - x)), less), fmaf(-slope2, fabsf(float(pos - j0 - x - 1)), less));
                         f2_unpack(weight(f2_pack(s[x], s[x + 1]), add, bend[kCap ? x / 2 : 0]), s[x], s[x + 1]);
@@ -370,7 +381,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                         keep_document(bits, kd, doc);
                         // padding's K rows may hold anything: clear them for the product with dx
                         if (quarter == 0 && kd[0] < 0) {
-                            uint4* k = reinterpret_cast<uint4*>(smem + (2 + 2 * n % kStages) * size_t(kTile) +
+                            uint4* k = reinterpret_cast<uint4*>(smem + (2 + key_stage(n)) * size_t(kTile) +
                                                                 (part * 32 + lane) * kSwizzleRow);
                             for (int x = 0; x < kD / 64; ++x)
                                 for (int y = 0; y < 8; ++y) k[x * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
@@ -410,12 +421,18 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 warp_arrive(dx_full);
             }
             if (phase == 0 && ok) {  // the four parts of the row
-                sums[part * kAttnRows + r] = sum;
-                mbar_arrive(sums_full);
-                ok = wait_for(sums_full, 0, abort_flag);
-                delta = (sums[r] + sums[kAttnRows + r]) + (sums[2 * kAttnRows + r] + sums[3 * kAttnRows + r]);
+                // meet in four columns of the accumulator, which nothing has written yet
+                tc_st1(dq_tmem + lane_base + part, __float_as_uint(sum));
+                tc_wait_st();
+                warp_arrive(sums_full);
+                ok = __all_sync(0xffffffffu, wait_for(sums_full, 0, abort_flag));
+                tc_fence_after();
+                uint32_t part_sum[4];
+                tc_ld4(dq_tmem + lane_base, part_sum);
+                delta = (__uint_as_float(part_sum[0]) + __uint_as_float(part_sum[1])) +
+                        (__uint_as_float(part_sum[2]) + __uint_as_float(part_sum[3]));
+                tc_fence_before();
                 if (part == 0 && valid) *delta_at = delta;
-                ok = __all_sync(0xffffffffu, ok);
             }
         }
         if (ok && part < kD / 32) {

@@ -151,10 +151,10 @@ __device__ __forceinline__ void finish_scores(float (&s)[128], float scale, floa
     const float c = scale * kLog2e;
     if (side != 0) {  // z = c s - side k (far - i)
         const float at = side > 0 ? -k * far : k * far, by = side > 0 ? k : -k;
-        const uint64_t c2 = both(c), at2 = both(at), by2 = both(by);
+        const uint64_t c2 = both(c);
 #pragma unroll
         for (int i = 0; i < 128; i += 2)
-            f2_unpack(f2_fma(f2_pack(s[i], s[i + 1]), c2, f2_fma(f2_pack(float(i), float(i + 1)), by2, at2)), s[i], s[i + 1]);
+            f2_unpack(f2_fma(f2_pack(s[i], s[i + 1]), c2, f2_pack(fmaf(float(i), by, at), fmaf(float(i + 1), by, at))), s[i], s[i + 1]);
     } else {
 #pragma unroll
         for (int i = 0; i < 128; ++i) s[i] = fmaf(-k, fabsf(far - float(i)), s[i] * c);
