@@ -331,18 +331,15 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             if (p.plan && doc < 0) delta = 0.f;  // padding: its output gradient may be anything
             if (part == 0) *delta_at = delta;
         }
-        bool ok = true;
+        // A wait that gives up raises the abort flag: the loop then runs on over what there is, and
+        // nothing is written at its end.
         int n = 0;
-        for (int phase = exact ? 0 : 1; ok && phase < 2; ++phase) {
+        for (int phase = exact ? 0 : 1; phase < 2; ++phase) {
             TileIter it(plan, n_tiles);
             float sum = 0.f;
             for (int j = it.next(); j >= 0; j = it.next(), ++n) {
                 const uint32_t s_row = tmem + (n & 1) * kAttnRows + part * 32 + lane_base;
-                ok = wait_for(s_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                wait_for(s_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag);
                 tc_fence_after();
                 const int j0 = j * int(kAttnRows) + int(part) * 32;
                 float s[32];
@@ -391,11 +388,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
 #pragma unroll
                     for (int x = 0; x < 32; ++x) s[x] = (bits[0] >> x) & 1u ? s[x] : 0.f;
                 }
-                ok = wait_for(dp_full, n & 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                wait_for(dp_full, n & 1u, abort_flag);
                 tc_fence_after();
                 float d[32];
                 load_row<32>(dp_tmem + part * 32 + lane_base, d);
@@ -420,12 +413,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 }
                 warp_arrive(dx_full);
             }
-            if (phase == 0 && ok) {  // the four parts of the row
+            if (phase == 0) {  // the four parts of the row
                 // meet in four columns of the accumulator, which nothing has written yet
                 tc_st1(dq_tmem + lane_base + part, __float_as_uint(sum));
                 tc_wait_st();
                 warp_arrive(sums_full);
-                ok = __all_sync(0xffffffffu, wait_for(sums_full, 0, abort_flag));
+                wait_for(sums_full, 0, abort_flag);
                 tc_fence_after();
                 uint32_t part_sum[4];
                 tc_ld4(dq_tmem + lane_base, part_sum);
@@ -435,9 +428,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 if (part == 0 && valid) *delta_at = delta;
             }
         }
-        if (ok && part < kD / 32) {
-            ok = wait_for(done, 0, abort_flag);
-            if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
+        if (part < kD / 32) {
+            const bool ok = wait_for(done, 0, abort_flag);
+            if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
                 tc_fence_after();
                 write_row<kF, 32>(dq_tmem + lane_base + part * 32, visits > 0, valid, p.scale,
                                   p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h + part * 64);
@@ -485,19 +478,25 @@ struct DkvShape {
     static constexpr size_t kSmem = 2 * kTile + size_t(kStages) * 2 * kBlock + kStatSlots * sizeof(QueryStats) + 512 + 1024;
 };
 
-// The blocks of a key tile, in order: query heads outer, tiles of 128 queries that can see
-// the keys, two blocks each.
+// The blocks of a key tile, in order: query heads outer; all `per_head` blocks from the query
+// tile `first` on, or two (one, at the end) for each tile with a bit in `words`.
 struct BlockIter {
     TileIter it;
     const uint32_t* words;
-    int n, first, Sq, tile, part;
+    int q_tiles, first, Sq, tile, part, per_head, m;
     uint32_t head, heads;
-    __device__ BlockIter(const uint32_t* w, int first_tile, int tiles, int sq, uint32_t shared)
-        : it(w, tiles), words(w), n(tiles), first(first_tile), Sq(sq), tile(-1), part(1), head(0), heads(shared) {
-        if (!w) it.pos = first_tile;
-    }
+    __device__ BlockIter(const uint32_t* w, int first_tile, int tiles, int sq, uint32_t per, uint32_t shared)
+        : it(w, tiles), words(w), q_tiles(tiles), first(first_tile), Sq(sq), tile(-1), part(1), per_head(int(per)), m(-1),
+          head(per == 0 ? shared : 0), heads(shared) {}
     // first query of the next block, or -1
     __device__ __forceinline__ int next() {
+        if (!words) {
+            if (++m >= per_head) {
+                m = 0;
+                ++head;
+            }
+            return head < heads && per_head > 0 ? first * int(kAttnRows) + m * int(kQueries) : -1;
+        }
         if (part == 0 && tile * int(kAttnRows) + int(kQueries) < Sq) {
             part = 1;
             return tile * int(kAttnRows) + int(kQueries);
@@ -506,8 +505,7 @@ struct BlockIter {
             tile = it.next();
             if (tile >= 0) break;
             if (++head >= heads) return -1;
-            it = TileIter(words, n);
-            if (!words) it.pos = first;
+            it = TileIter(words, q_tiles);
         }
         part = 0;
         return tile * int(kAttnRows);
@@ -584,8 +582,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     if (p.causal && !(p.prefix && row0 < p.prefix[b])) first = min(q_tiles, max(0, row0 - ahead) / int(kAttnRows));
     const uint32_t words = (uint32_t(q_tiles) + 31) / 32;
     const uint32_t* plan = p.plan ? p.plan + (size_t(b) * bp.k_tiles + kt) * 2 * words : nullptr;
-    BlockIter it(plan, first, q_tiles, int(p.Sq), p.shared);
-    const uint32_t blocks = p.shared * blocks_of(plan, first, q_tiles, int(p.Sq));
+    const uint32_t per_head = blocks_of(plan, first, q_tiles, int(p.Sq)), blocks = p.shared * per_head;
+    BlockIter it(plan, first, q_tiles, int(p.Sq), per_head, p.shared);
 
     if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");  // 640 * 96 at launch >= 512 * 104 + 128 * 56
@@ -705,17 +703,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
         const uint32_t lane_base = (quarter * 32u) << 16;
         const int32_t doc = plan && valid ? p.k_docs[int64_t(b) * p.Sk + j] : -1;
         const uint32_t s_row = tmem + t * 2 * kQueries + 32 * half + lane_base, dp_row = s_row + kQueries;
-        bool ok = true;
         uint32_t n = 0;
         for (int i0 = it.next(); i0 >= 0; i0 = it.next(), ++n) {
             if ((n & 1u) != t) continue;
             const uint32_t slot = n % kStatSlots;
-            ok = wait_for(stat_full0 + 8 * slot, (n / kStatSlots) & 1u, abort_flag) &&
-                 wait_for(s_full0 + 8 * t, (n >> 1) & 1u, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+            wait_for(stat_full0 + 8 * slot, (n / kStatSlots) & 1u, abort_flag);  // (see dq_kernel for a wait that gives up)
+            wait_for(s_full0 + 8 * t, (n >> 1) & 1u, abort_flag);
             tc_fence_after();
             const QueryStats& st = stats[slot];
             const float slope2 = kBias && p.slopes ? p.slopes[g * p.Hl + kh * p.shared + it.head] * kLog2e : 0.f;
@@ -798,8 +791,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
             if (lane == 0) mbar_arrive(stat_free0 + 8 * slot);
         }
         // n counts every block, of both halves of the warps
-        if (ok) ok = wait_for(done, 0, abort_flag);
-        if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
+        const bool ok = wait_for(done, 0, abort_flag);
+        if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
             tc_fence_after();
             const int64_t at = valid ? j : 0;
             constexpr int kCols = kD / 2;  // of each half of the warps

@@ -214,47 +214,49 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             fence_async_shared();
             warp_arrive(q_full);
         }
-        // lane l < 8: the page of keys [key0 + 128 * tile + 16 l, + 16)
-        int id_of = -1, id_next = -1;
-        float scale_of[2] = {0.f, 0.f}, scale_next[2] = {0.f, 0.f};
-        auto pages = [&](int tile, int& id, float (&scale)[2]) {
+        // lane l of eight: the group of keys [key0 + 128 * tile + 16 l, + 16), which lies in one page:
+        // whether there is one, where its K codes start (V's at the same offset), its scales
+        struct Group {
+            int64_t at;  // -1: behind the sequence, or its page is out of range
+            float scale[2];
+        };
+        auto group_of = [&](int tile) {
+            Group d{-1, {0.f, 0.f}};
             const int key = key0 + tile * int(kAttnRows) + int(lane % 8) * 16;
-            id = -1;
-            scale[0] = scale[1] = 0.f;
             if (tile < n_tiles && key < seq.len) {
                 const int x = c.table[int64_t(n) * c.table_stride + uint32_t(key) / c.page];
                 if (x >= 0 && uint32_t(x) < c.pages) {
-                    id = x;
-                    scale[0] = c.scales[0][int64_t(x) * c.Hkv + kh];
-                    scale[1] = c.scales[1][int64_t(x) * c.Hkv + kh];
+                    const int64_t slot = int64_t(x) * c.Hkv + kh;
+                    d.at = (slot * c.page + uint32_t(key) % c.page) * kD;
+                    d.scale[0] = c.scales[0][slot];
+                    d.scale[1] = c.scales[1][slot];
                 } else {
                     atomicOr(&g_kv_tiles_status, 1u);
                 }
             }
+            return d;
         };
-        // piece x of this thread: key group (16 keys) and key in it, piece of the key's row
+        // piece x of a thread: 16 codes of a key
         constexpr uint32_t kRowsPer = 128 / kPieces;  // keys that a pass of the 128 threads covers
         const uint32_t piece = i % kPieces, key_in = i / kPieces;
-        uint4 raw[2][kLoads];
-        auto load = [&](uint4 (&d)[kLoads], int tile, int kv, int id) {
+        const uint32_t own = key_in % 16 * kD + piece * 16;  // in a group
+        auto load = [&](uint4 (&d)[kLoads], int tile, int kv, int64_t at) {
+            const int left = seq.len - key0 - tile * int(kAttnRows);
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
                 const uint32_t row = x * kRowsPer + key_in;
-                const int page = __shfl_sync(0xffffffffu, id, row / 16);
-                const int key = key0 + tile * int(kAttnRows) + int(row);
+                const int64_t from = __shfl_sync(0xffffffffu, at, row / 16);
                 d[x] = make_uint4(0, 0, 0, 0);
-                if (page >= 0 && key < seq.len)
-                    d[x] = ld_codes16(c.codes[kv] + ((int64_t(page) * c.Hkv + kh) * c.page + uint32_t(key) % c.page) * kD + piece * 16);
+                if (from >= 0 && int(row) < left) d[x] = ld_codes16(c.codes[kv] + from + own);
             }
         };
         auto convert = [&](const uint4 (&d)[kLoads], uint32_t k, float scale, float ref) {
             uint8_t* tile = smem + (2 + k % kStages) * size_t(kTile);
-            const float inv = 1.0f / ref;
+            const __half2 own_factor = __float2half2_rn(scale / ref);
+            const uint32_t factor = *reinterpret_cast<const uint32_t*>(&own_factor);
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
-                const uint32_t row = x * kRowsPer + key_in;
-                const float f = __shfl_sync(0xffffffffu, scale, row / 16) * inv;
-                const __half2 f2 = __float2half2_rn(f);
+                const uint32_t row = x * kRowsPer + key_in, f = __shfl_sync(0xffffffffu, factor, row / 16);
                 const uint32_t* w = &d[x].x;
                 uint32_t h[8];
 #pragma unroll
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const uint32_t v = to_f16x2(w[y] >> (16 * z));
-                        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), f2);
+                        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&f));
                         h[2 * y + z] = *reinterpret_cast<const uint32_t*>(&r);
                     }
                 }
@@ -275,41 +277,33 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
             return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         };
-        pages(0, id_of, scale_of);
-        if (n_tiles > 0) load(raw[0], 0, 0, id_of);
+        Group now = group_of(0);
+        uint4 raw[2][kLoads];
+        load(raw[0], 0, 0, now.at);
         float v_ref = 0x1p-126f;
         bool ok = true;
         for (int j = 0; ok && j < n_tiles; ++j) {
-            pages(j + 1, id_next, scale_next);
-            const float k_ref = fmaxf(largest(scale_of[0]), 0x1p-126f);
-            v_ref = fmaxf(v_ref, largest(scale_of[1]));
-            const int at = key0 + j * int(kAttnRows) + int(lane % 8) * 16;
-            const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && id_of < 0 && at < seq.len);
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t k = 2 * j + kv, s = k % kStages, use = k / kStages;
-                if (kv == 0)
-                    load(raw[1], j, 1, id_of);
-                else
-                    load(raw[0], j + 1, 0, id_next);
-                ok = use == 0 || wait_for(empty0 + 8 * s, (use - 1) & 1u, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                if (kv == 0) {
-                    convert(raw[0], k, scale_of[0], k_ref);
-                    if (i == 0) {
-                        infos[j % kInfos] = TileInfo{k_ref, v_ref, bad};
-                        mbar_arrive(info_full0 + 8 * (j % kInfos));
-                    }
-                } else {
-                    convert(raw[1], k, scale_of[1], v_ref);
-                }
-                warp_arrive(full0 + 8 * s);
+            const Group next = group_of(j + 1);
+            const float k_ref = fmaxf(largest(now.scale[0]), 0x1p-126f);
+            v_ref = fmaxf(v_ref, largest(now.scale[1]));
+            const int key = key0 + j * int(kAttnRows) + int(lane % 8) * 16;
+            const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && now.at < 0 && key < seq.len);
+            load(raw[1], j, 1, now.at);
+            const uint32_t k = 2 * j, s = k % kStages;  // K of tile j, V in the next stage
+            ok = __all_sync(0xffffffffu, k < uint32_t(kStages) || wait_for(empty0 + 8 * s, (k / kStages - 1) & 1u, abort_flag));
+            if (!ok) break;
+            convert(raw[0], k, now.scale[0], k_ref);
+            if (i == 0) {
+                infos[j % kInfos] = TileInfo{k_ref, v_ref, bad};
+                mbar_arrive(info_full0 + 8 * (j % kInfos));
             }
-            id_of = id_next;
-            scale_of[0] = scale_next[0];
-            scale_of[1] = scale_next[1];
+            warp_arrive(full0 + 8 * s);
+            load(raw[0], j + 1, 0, next.at);
+            ok = __all_sync(0xffffffffu, k < uint32_t(kStages) || wait_for(empty0 + 8 * (s + 1), (k / kStages - 1) & 1u, abort_flag));
+            if (!ok) break;
+            convert(raw[1], k + 1, now.scale[1], v_ref);
+            warp_arrive(full0 + 8 * (s + 1));
+            now = next;
         }
     } else {
         // ---------------- softmax: a thread per row
