@@ -143,6 +143,16 @@ def test_views_into_fused_payloads_and_strided_results(tf, D):
         assert bool((t[..., :D] == 7).all()) and bool((t[..., 2 * D:] == 7).all())
 
 
+@pytest.mark.parametrize("D,dtype", [(64, FP16), (128, BF16)])
+@pytest.mark.parametrize("P,B,Sq,Sk,Hl,Hkl", [(1, 1, 300, 2200, 1, 1), (1, 1, 2300, 2200, 1, 1), (2, 2, 1100, 3001, 2, 1),
+                                              (1, 1, 5000, 1100, 4, 1)])
+def test_units_cut_along_the_other_side(tf, P, B, Sq, Sk, Hl, Hkl, D, dtype):
+    """Few row tiles over many of the other side: their sums are joined from parts."""
+    x = make(P, B, Sq, Sk, Hl, Hkl, D, dtype, Sq)
+    both(tf, *x)
+    both(tf, *x, softcap=4.0, slopes=torch.linspace(0.0, 0.05, P * Hl, device="cuda"))
+
+
 def test_large_scores_and_equal_keys(tf):
     q, k, v, dout = make(1, 1, 140, 300, 2, 2, 64, BF16, 23)
     both(tf, [30 * t for t in q], k, v, dout)          # one weight takes nearly all

@@ -565,8 +565,7 @@ def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=No
             lse, lp = _made(P, rows, torch.float32, q[0].device)
         else:
             lp = _lse_arrays(lse, P, rows, device)
-        ws, ws_at, ws_size = (None, None, 0) if q_docs is None else _workspace(
-            L.tf_ulysses_attention_workspace, a, 0, device=q[0].device)
+        ws, ws_at, ws_size = _workspace(L.tf_ulysses_attention_workspace, a, 0, device=q[0].device)
         each = ctypes.c_void_p * P
         _check(L.tf_ulysses_attention(a, each(*qp), each(*kp), each(*vp), _Strides3(q_str, k_str, v_str), each(*op),
                                       Strides(*o_str) if o_str is not None else None, each(*lp), ws_at, ws_size, on.handle))

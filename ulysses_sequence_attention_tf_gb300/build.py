@@ -22,7 +22,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               f"-I{INCLUDE}", f"-I{CSRC}"]
 SOURCES = ["block_kernels.cu", "block_kernels_v16.cu", "gemm_kernels.cu", "relayout_kernels.cu", "staged_kernels.cu",
-           "tf_ulysses.cpp", "noalloc.cu", "attention_plan.cu", "attention_forward.cu", "attention_backward.cu", "tf_attention.cpp", "kv_append.cu", "kv_attend.cu", "kv_attend_tiles.cu",
+           "tf_ulysses.cpp", "noalloc.cu", "attention_plan.cu", "attention_forward.cu", "attention_backward.cu", "attention_join.cu", "tf_attention.cpp", "kv_append.cu", "kv_attend.cu", "kv_attend_tiles.cu",
            "tf_kv_cache.cpp"]
 DEPS = SOURCES + ["relayout.h", "noalloc.h", "device_common.cuh", "block_kernel.cuh", "tma_plan.h", "gemm.h", "host.h",
                   "attention.h", "attention_common.cuh", "attention_plan.h",

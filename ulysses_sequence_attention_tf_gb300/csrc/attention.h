@@ -44,10 +44,34 @@ struct GroupMaps {
     CUtensorMap m[kMaxShards];
 };
 
+// CTAs run one an SM, in rounds.  The units (row tiles of a head) of the last, partly
+// filled round are cut into `parts` along the other side; a part leaves fp32 sums at
+// part[slot], slot = its CTA's number behind the whole units, and a second kernel joins
+// them in order.  Without documents and causal mask only: the units cost the same then.
+struct Split {
+    uint32_t whole, parts;  // units that are not cut, parts of each other one (1: none is cut)
+    float* part;            // forward: O rows; dQ rows; dK rows, then dV rows
+    float2* stat;           // forward: a row's reference (log2) and sum
+};
+constexpr uint32_t kAttnSms = 152;   // SMs of a GB300
+constexpr uint32_t kLeastPart = 8;   // tiles of the other side in a part: below, the join costs more than it gives
+inline Split plan_split(const uint64_t units, const uint32_t tiles, bool even) {
+    Split s{uint32_t(units), 1, nullptr, nullptr};
+    const uint32_t rest = uint32_t(units % kAttnSms);
+    if (!even || rest == 0) return s;
+    uint32_t parts = kAttnSms / rest;
+    if (parts > tiles / kLeastPart) parts = tiles / kLeastPart;
+    if (parts < 2) return s;
+    s.whole = uint32_t(units - rest);
+    s.parts = parts;
+    return s;
+}
+
 struct ForwardParams {
     GroupMaps q, k, v;
     AttentionParams a;
     uint32_t q_tiles;  // of kAttnPair rows
+    Split split;
 };
 
 struct BackwardParams {
@@ -56,6 +80,7 @@ struct BackwardParams {
     AttentionParams a;
     uint32_t* key_plan;           // with documents: row tiles of keys (a.plan: of 128 queries)
     uint32_t q_tiles, k_tiles;    // of kAttnRows rows
+    Split dq_split, dkv_split;
 };
 
 // With documents, a kernel in front of the attention writes for every row tile
@@ -74,6 +99,11 @@ inline TilePlan tile_plan(uint32_t rows, uint32_t rows_per_tile, uint32_t cols) 
 // false if the driver refuses.
 bool encode_group_maps(GroupMaps* maps, const GroupView& v, uint32_t P, uint32_t B, uint32_t tokens, uint32_t heads,
                        uint32_t D, uint32_t box_tokens, bool bf16);
+
+// Join the parts of cut units: rows of kAttnPair (forward) or kAttnRows a unit.
+cudaError_t launch_join_forward(const ForwardParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_join_gradient(const AttentionParams& p, const Split& s, const GroupView& out, const float* part, float factor,
+                                 uint32_t row_tiles, uint32_t rows, uint32_t heads, bool bf16, cudaStream_t stream);
 
 // *launches: kernels launched
 cudaError_t launch_attention(const ForwardParams& p, bool bf16, cudaStream_t stream, int* launches);

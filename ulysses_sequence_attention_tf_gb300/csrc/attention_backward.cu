@@ -115,6 +115,20 @@ __device__ __forceinline__ void write_row(uint32_t taddr, bool any, bool valid, 
     }
 }
 
+// the same in fp32, for a part of a unit
+template <int kCols>
+__device__ __forceinline__ void write_sums(uint32_t taddr, float* dst) {
+#pragma unroll 1
+    for (int x = 0; x < kCols; x += 32) {
+        uint32_t r[32];
+        tc_ld32(taddr + x, r);
+        tc_wait_ld();
+        tc_landed(r);
+#pragma unroll
+        for (int y = 0; y < 32; y += 4) *reinterpret_cast<uint4*>(dst + x + y) = make_uint4(r[y], r[y + 1], r[y + 2], r[y + 3]);
+    }
+}
+
 // sum_d a_d b_d of two 16-bit rows
 template <Fused kF, int kD>
 __device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b) {
@@ -176,7 +190,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     auto key_phase = [](uint32_t n) { return (n / S::kKeyStages) & 1u; };
     auto value_phase = [](uint32_t n) { return (n / S::kValueStages) & 1u; };
 
-    uint32_t u = blockIdx.x;
+    const Unit unit(bp.dq_split, blockIdx.x);
+    uint32_t u = unit.u;
     uint32_t qt = u % bp.q_tiles;
     u /= bp.q_tiles;
     if (p.causal) qt = bp.q_tiles - 1 - qt;
@@ -212,15 +227,16 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     const uint32_t dp_tmem = tmem + 2 * kAttnRows, dq_tmem = tmem + 3 * kAttnRows;
 
     const int last = min(row0 + int(kAttnRows), int(p.Sq)) - 1;
-    const int n_tiles = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
+    const int reach = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
+    const int first_tile = unit.begin(reach), n_tiles = unit.end(reach);
     const uint32_t words = (((p.Sk + kAttnRows - 1) / kAttnRows) + 31) / 32;
     const uint32_t* plan = p.plan ? p.plan + (size_t(b) * bp.q_tiles + qt) * 2 * words : nullptr;
-    int visits = n_tiles;
+    int visits = n_tiles - first_tile;
     if (plan) {
         visits = 0;
         for (uint32_t w = 0; w < words; ++w) visits += __popc(__ldg(plan + w));
     }
-    const bool exact = visits <= kExactTiles;  // two phases: delta from P dP, then dQ
+    const bool exact = visits <= kExactTiles && unit.parts == 1;  // two phases: delta from P dP, then dQ
 
     if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");  // 640 * 96 at launch >= 512 * 104 + 128 * 56
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             }
         }
         for (int phase = exact ? 0 : 1; phase < 2; ++phase) {
-            TileIter it(plan, n_tiles);
+            TileIter it(plan, n_tiles, first_tile);
             for (int j = it.next(); ok && j >= 0; j = it.next()) {
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t s = kv ? value_stage(n) : key_stage(n), phase_of = kv ? value_phase(n) : key_phase(n);
@@ -329,13 +345,13 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             delta = row_dot<kF, kD>(p.dout.base[g] + b * p.dout.b + at * p.dout.t + h * p.dout.h,
                                     p.out.base[g] + b * p.out.b + at * p.out.t + h * p.out.h);
             if (p.plan && doc < 0) delta = 0.f;  // padding: its output gradient may be anything
-            if (part == 0) *delta_at = delta;
+            if (part == 0 && unit.part == 0) *delta_at = delta;
         }
         // A wait that gives up raises the abort flag: the loop then runs on over what there is, and
         // nothing is written at its end.
         int n = 0;
         for (int phase = exact ? 0 : 1; phase < 2; ++phase) {
-            TileIter it(plan, n_tiles);
+            TileIter it(plan, n_tiles, first_tile);
             float sum = 0.f;
             for (int j = it.next(); j >= 0; j = it.next(), ++n) {
                 const uint32_t s_row = tmem + (n & 1) * kAttnRows + part * 32 + lane_base;
@@ -432,8 +448,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             const bool ok = wait_for(done, 0, abort_flag);
             if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
                 tc_fence_after();
-                write_row<kF, 32>(dq_tmem + lane_base + part * 32, visits > 0, valid, p.scale,
-                                  p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h + part * 64);
+                const uint32_t from = dq_tmem + lane_base + part * 32;
+                if (unit.parts > 1)
+                    write_sums<32>(from, bp.dq_split.part + (int64_t(unit.slot) * kAttnRows + r) * kD + part * 32);
+                else
+                    write_row<kF, 32>(from, visits > 0, valid, p.scale,
+                                      p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h + part * 64);
             }
         }
     }
@@ -484,27 +504,28 @@ struct BlockIter {
     TileIter it;
     const uint32_t* words;
     int q_tiles, first, Sq, tile, part, per_head, m;
-    uint32_t head, heads;
-    __device__ BlockIter(const uint32_t* w, int first_tile, int tiles, int sq, uint32_t per, uint32_t shared)
-        : it(w, tiles), words(w), q_tiles(tiles), first(first_tile), Sq(sq), tile(-1), part(1), per_head(int(per)), m(-1),
-          head(per == 0 ? shared : 0), heads(shared) {}
+    uint32_t head, left;
+    // without words: `count` blocks from block `from` of the whole order on
+    __device__ BlockIter(const uint32_t* w, int first_tile, int tiles, int sq, uint32_t per, uint32_t from, uint32_t count)
+        : it(w, tiles), words(w), q_tiles(tiles), first(first_tile), Sq(sq), tile(-1), part(1), per_head(int(per)),
+          m(per ? int(from % per) - 1 : -1), head(per ? from / per : 0), left(count) {}
     // first query of the next block, or -1
     __device__ __forceinline__ int next() {
+        if (left == 0) return -1;
+        --left;
         if (!words) {
             if (++m >= per_head) {
                 m = 0;
                 ++head;
             }
-            return head < heads && per_head > 0 ? first * int(kAttnRows) + m * int(kQueries) : -1;
+            return first * int(kAttnRows) + m * int(kQueries);
         }
         if (part == 0 && tile * int(kAttnRows) + int(kQueries) < Sq) {
             part = 1;
             return tile * int(kAttnRows) + int(kQueries);
         }
-        while (true) {
-            tile = it.next();
-            if (tile >= 0) break;
-            if (++head >= heads) return -1;
+        while ((tile = it.next()) < 0) {  // there is one more block: in the next head
+            ++head;
             it = TileIter(words, q_tiles);
         }
         part = 0;
@@ -540,7 +561,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    uint32_t u = blockIdx.x;
+    const Unit unit(bp.dkv_split, blockIdx.x);
+    uint32_t u = unit.u;
     const uint32_t kt = u % bp.k_tiles;  // causal: the first keys are seen by most queries
     u /= bp.k_tiles;
     const uint32_t kh = u % p.Hkl, b = u / p.Hkl % p.B, g = u / p.Hkl / p.B;
@@ -582,8 +604,10 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     if (p.causal && !(p.prefix && row0 < p.prefix[b])) first = min(q_tiles, max(0, row0 - ahead) / int(kAttnRows));
     const uint32_t words = (uint32_t(q_tiles) + 31) / 32;
     const uint32_t* plan = p.plan ? p.plan + (size_t(b) * bp.k_tiles + kt) * 2 * words : nullptr;
-    const uint32_t per_head = blocks_of(plan, first, q_tiles, int(p.Sq)), blocks = p.shared * per_head;
-    BlockIter it(plan, first, q_tiles, int(p.Sq), per_head, p.shared);
+    const uint32_t per_head = blocks_of(plan, first, q_tiles, int(p.Sq));
+    const uint32_t first_block = uint32_t(unit.begin(int(p.shared * per_head)));
+    const uint32_t blocks = uint32_t(unit.end(int(p.shared * per_head))) - first_block;
+    BlockIter it(plan, first, q_tiles, int(p.Sq), per_head, first_block, blocks);
 
     if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");  // 640 * 96 at launch >= 512 * 104 + 128 * 56
@@ -796,12 +820,17 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
             tc_fence_after();
             const int64_t at = valid ? j : 0;
             constexpr int kCols = kD / 2;  // of each half of the warps
-            if (t == 0)
-                write_row<kF, kCols>(dv_tmem + lane_base + half * kCols, n > 0, valid, kDown,
-                                     p.dv.base[g] + b * p.dv.b + at * p.dv.t + kh * p.dv.h + half * kCols * 2);
-            else
-                write_row<kF, kCols>(dk_tmem + lane_base + half * kCols, n > 0, valid, p.scale,
+            const uint32_t from = (t == 0 ? dv_tmem : dk_tmem) + lane_base + half * kCols;
+            if (unit.parts > 1) {
+                const int64_t cut = int64_t(bp.k_tiles) * p.P * p.B * p.Hkl - bp.dkv_split.whole;  // units in parts
+                const int64_t row = (t == 0 ? cut * unit.parts + unit.slot : int64_t(unit.slot)) * kAttnRows + r;
+                write_sums<kCols>(from, bp.dkv_split.part + row * kD + half * kCols);
+            } else if (t == 0) {
+                write_row<kF, kCols>(from, n > 0, valid, kDown, p.dv.base[g] + b * p.dv.b + at * p.dv.t + kh * p.dv.h + half * kCols * 2);
+            } else {
+                write_row<kF, kCols>(from, n > 0, valid, p.scale,
                                      p.dk.base[g] + b * p.dk.b + at * p.dk.t + kh * p.dk.h + half * kCols * 2);
+            }
         }
     }
     __syncwarp();
@@ -825,9 +854,16 @@ cudaError_t launch(const BackwardParams& p, cudaStream_t stream, int* launches) 
         auto kernel = dq_kernel<kF, kD, kCap, kBias>;
         constexpr size_t smem = DqShape<kD>::kSmem;
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) != cudaSuccess) return e;
-        e = launch_overlapped(kernel, p.q_tiles * p.a.P * p.a.B * p.a.Hl, kThreadsB, smem, stream, p);
+        const uint32_t units = p.q_tiles * p.a.P * p.a.B * p.a.Hl;
+        const Split& cut = p.dq_split;
+        e = launch_overlapped(kernel, cut.whole + (units - cut.whole) * cut.parts, kThreadsB, smem, stream, p);
         if (e != cudaSuccess) return e;
         *launches += 1;
+        if (cut.parts > 1) {
+            e = launch_join_gradient(p.a, cut, p.a.dq, cut.part, p.a.scale, p.q_tiles, p.a.Sq, p.a.Hl, kF == Fused::kBF16, stream);
+            if (e != cudaSuccess) return e;
+            *launches += 1;
+        }
     }
     if (p.a.Sk > 0) {
         if (p.a.plan) {
@@ -838,9 +874,20 @@ cudaError_t launch(const BackwardParams& p, cudaStream_t stream, int* launches) 
         auto kernel = dkv_kernel<kF, kD, kCap, kBias>;
         constexpr size_t smem = DkvShape<kD>::kSmem;
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) != cudaSuccess) return e;
-        e = launch_overlapped(kernel, p.k_tiles * p.a.P * p.a.B * p.a.Hkl, kThreadsB, smem, stream, q);
+        const uint32_t units = p.k_tiles * p.a.P * p.a.B * p.a.Hkl;
+        const Split& cut = p.dkv_split;
+        e = launch_overlapped(kernel, cut.whole + (units - cut.whole) * cut.parts, kThreadsB, smem, stream, q);
         if (e != cudaSuccess) return e;
         *launches += 1;
+        if (cut.parts > 1) {
+            const float* dv_part = cut.part + int64_t(units - cut.whole) * cut.parts * kAttnRows * kD;
+            constexpr float kDown = kF == Fused::kFP16 ? 0x1p-8f : 1.0f;
+            e = launch_join_gradient(p.a, cut, p.a.dk, cut.part, p.a.scale, p.k_tiles, p.a.Sk, p.a.Hkl, kF == Fused::kBF16, stream);
+            if (e == cudaSuccess)
+                e = launch_join_gradient(p.a, cut, p.a.dv, dv_part, kDown, p.k_tiles, p.a.Sk, p.a.Hkl, kF == Fused::kBF16, stream);
+            if (e != cudaSuccess) return e;
+            *launches += 2;
+        }
     }
     return cudaSuccess;
 }

@@ -68,13 +68,28 @@ __device__ __forceinline__ uint64_t tanh_over_x(uint64_t y) {
     return f2_fma(y, r, both(kTanh0));
 }
 
-// The tiles of the other side that a row tile visits, in order: all of [0, n), or
+// The unit of a CTA, and which part of how many it takes.
+struct Unit {
+    uint32_t u, part, parts, slot;
+    __device__ Unit(const Split& s, uint32_t cta) : u(cta), part(0), parts(1), slot(0) {
+        if (cta >= s.whole) {
+            slot = cta - s.whole;
+            u = s.whole + slot / s.parts;
+            part = slot % s.parts;
+            parts = s.parts;
+        }
+    }
+    __device__ int begin(int n) const { return int(int64_t(n) * part / parts); }
+    __device__ int end(int n) const { return int(int64_t(n) * (part + 1) / parts); }
+};
+
+// The tiles of the other side that a row tile visits, in order: all of [from, n), or
 // those with a bit in `words`.
 struct TileIter {
     const uint32_t* words;
     int n, pos;
     uint32_t bits;
-    __device__ TileIter(const uint32_t* w, int count) : words(w), n(count), pos(w ? -32 : 0), bits(0) {}
+    __device__ TileIter(const uint32_t* w, int count, int from = 0) : words(w), n(count), pos(w ? -32 : from), bits(0) {}
     __device__ __forceinline__ int next() {
         if (!words) return pos < n ? pos++ : -1;
         while (bits == 0) {

@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    uint32_t u = blockIdx.x;
+    const Unit unit(fp.split, blockIdx.x);
+    uint32_t u = unit.u;
     uint32_t qt = u % fp.q_tiles;
     u /= fp.q_tiles;
     if (p.causal) qt = fp.q_tiles - 1 - qt;  // the rows that see most first
@@ -95,10 +96,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
 
     // the keys in reach of the last row, in tiles; with documents the plan picks among them
     const int last = min(row0 + int(kAttnPair), int(p.Sq)) - 1;
-    const int n_tiles = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
+    const int reach = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
+    const int n_tiles = unit.end(reach);
     const uint32_t words = (((p.Sk + kAttnRows - 1) / kAttnRows) + 31) / 32;
     const uint32_t* plan = p.plan ? p.plan + (size_t(b) * fp.q_tiles + qt) * 2 * words : nullptr;
-    TileIter it(plan, n_tiles);
+    TileIter it(plan, n_tiles, unit.begin(reach));
 
     // 384 * 168 registers at launch = 256 * 216 + 128 * 72
     if (warp >= 8) {
@@ -267,6 +269,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
         if (int(t) < tiles && ok) {
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             uint8_t* dst = p.out.base[g] + int64_t(b) * p.out.b + int64_t(valid ? i : 0) * p.out.t + int64_t(h) * p.out.h;
+            const int64_t row = int64_t(unit.slot) * kAttnPair + t * kAttnRows + quarter * 32 + lane;  // of a part's sums
             if (n > 0) ok = bounded_wait(o_full, 0, abort_flag, &g_attention_status);
             if (__all_sync(0xffffffffu, ok) && !*abort_flag) {
                 tc_fence_after();
@@ -281,6 +284,12 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
 #pragma unroll
                         for (int y = 0; y < 32; ++y) r[y] = 0;
                     }
+                    if (unit.parts > 1) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4)
+                            *reinterpret_cast<uint4*>(fp.split.part + row * kD + x + y) = make_uint4(r[y], r[y + 1], r[y + 2], r[y + 3]);
+                        continue;
+                    }
 #pragma unroll
                     for (int y = 0; y < 32; y += 8) {
                         uint4 w;
@@ -292,7 +301,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
                         if (valid) *reinterpret_cast<uint4*>(dst + (x + y) * 2) = w;
                     }
                 }
-                if (valid && p.lse[g])
+                if (unit.parts > 1)
+                    fp.split.stat[row] = make_float2(m, l);
+                else if (valid && p.lse[g])
                     p.lse[g][(int64_t(b) * p.Hl + h) * p.Sq + i] = (m == -INFINITY ? 0.f : m * kLn2) + logf(l);
             }
         }
@@ -315,7 +326,8 @@ cudaError_t launch(const ForwardParams& p, cudaStream_t stream) {
     // setting it twice is harmless; the cost is a fraction of a microsecond
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    return launch_overlapped(kernel, p.q_tiles * p.a.P * p.a.B * p.a.Hl, kThreadsA, smem, stream, p);
+    const uint32_t units = p.q_tiles * p.a.P * p.a.B * p.a.Hl;
+    return launch_overlapped(kernel, p.split.whole + (units - p.split.whole) * p.split.parts, kThreadsA, smem, stream, p);
 }
 
 template <Fused kF, int kD>
@@ -333,10 +345,15 @@ cudaError_t launch_attention(const ForwardParams& p, bool bf16, cudaStream_t str
         if (e != cudaSuccess) return e;
         *launches = 1;
     }
-    const cudaError_t e = p.a.D == 64 ? (bf16 ? launch_scored<Fused::kBF16, 64>(p, stream) : launch_scored<Fused::kFP16, 64>(p, stream))
-                                      : (bf16 ? launch_scored<Fused::kBF16, 128>(p, stream) : launch_scored<Fused::kFP16, 128>(p, stream));
-    if (e == cudaSuccess) *launches += 1;
-    return e;
+    cudaError_t e = p.a.D == 64 ? (bf16 ? launch_scored<Fused::kBF16, 64>(p, stream) : launch_scored<Fused::kFP16, 64>(p, stream))
+                                : (bf16 ? launch_scored<Fused::kBF16, 128>(p, stream) : launch_scored<Fused::kFP16, 128>(p, stream));
+    if (e != cudaSuccess) return e;
+    *launches += 1;
+    if (p.split.parts > 1) {
+        if ((e = launch_join_forward(p, bf16, stream)) != cudaSuccess) return e;
+        *launches += 1;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t read_attention_status(unsigned* out, bool clear) {

@@ -71,18 +71,38 @@ void describe(const tf_attention& a, tfu::AttentionParams* p) {
     p->causal = uint32_t(a.causal);
 }
 
-// Parts of the workspace, in order, each a multiple of 16 bytes.
+uint64_t units_of(const tf_attention& a, int tokens, uint32_t rows, int heads) {
+    return (uint64_t(tokens) + rows - 1) / rows * uint64_t(a.B) * uint64_t(heads);
+}
+
+// How the units of a pass are cut (Split), and the parts of the workspace, in order, each a
+// multiple of 16 bytes.
 struct Workspace {
-    size_t delta = 0, plan = 0, key_plan = 0;  // bytes
+    tfu::Split forward{}, dq{}, dkv{};
+    size_t delta = 0, plan = 0, key_plan = 0, parts = 0;  // bytes
     Workspace(const tf_attention& a, bool backward) {
         auto up = [](size_t n) { return (n + 15) / 16 * 16; };
-        const uint32_t B = uint32_t(a.B), Sq = uint32_t(a.Sq), Sk = uint32_t(a.Sk);
-        const bool docs = a.q_docs && Sq > 0 && Sk > 0;
-        if (backward) delta = up(size_t(B) * size_t(a.H) * Sq * sizeof(float));
+        const uint32_t B = uint32_t(a.B), Sq = uint32_t(a.Sq), Sk = uint32_t(a.Sk), D = uint32_t(a.D);
+        const bool docs = a.q_docs && Sq > 0 && Sk > 0, even = !a.q_docs && !a.causal;
+        const uint32_t q_tiles = (Sq + tfu::kAttnRows - 1) / tfu::kAttnRows, k_tiles = (Sk + tfu::kAttnRows - 1) / tfu::kAttnRows;
+        auto cut = [](const tfu::Split& s, uint64_t units) { return s.parts > 1 ? (units - s.whole) * s.parts : 0; };
         if (docs) plan = up(tfu::tile_plan(Sq, backward ? tfu::kAttnRows : tfu::kAttnPair, Sk).bytes(B));
-        if (docs && backward) key_plan = up(tfu::tile_plan(Sk, tfu::kAttnRows, Sq).bytes(B));
+        if (!backward) {
+            const uint64_t units = units_of(a, a.Sq, tfu::kAttnPair, a.H);
+            forward = tfu::plan_split(units, k_tiles, even);
+            parts = cut(forward, units) * tfu::kAttnPair * (D * sizeof(float) + sizeof(float2));
+            return;
+        }
+        if (docs) key_plan = up(tfu::tile_plan(Sk, tfu::kAttnRows, Sq).bytes(B));
+        delta = up(size_t(B) * size_t(a.H) * Sq * sizeof(float));
+        const uint64_t rows = units_of(a, a.Sq, tfu::kAttnRows, a.H), keys = units_of(a, a.Sk, tfu::kAttnRows, a.Hkv);
+        dq = tfu::plan_split(rows, k_tiles, even);
+        dkv = tfu::plan_split(keys, q_tiles * uint32_t(a.H / a.Hkv), even);
+        // one after the other in the same place
+        const size_t sums = tfu::kAttnRows * D * sizeof(float), first = cut(dq, rows) * sums, second = 2 * cut(dkv, keys) * sums;
+        parts = first > second ? first : second;
     }
-    size_t bytes() const { return delta + plan + key_plan; }
+    size_t bytes() const { return delta + plan + key_plan + parts; }
 };
 
 size_t workspace_bytes_of(const tf_attention& a, bool backward) { return Workspace(a, backward).bytes(); }
@@ -138,7 +158,15 @@ TF_API tf_status tf_ulysses_attention(const tf_attention* a, const void* const* 
         (a->Sk > 0 && (!tfu::encode_group_maps(&fp.k, p.k, p.P, p.B, p.Sk, p.Hkl, p.D, tfu::kAttnRows, bf16) ||
                        !tfu::encode_group_maps(&fp.v, p.v, p.P, p.B, p.Sk, p.Hkl, p.D, tfu::kAttnRows, bf16))))
         return fail(TF_ERR_UNSUPPORTED, "the driver refused a tensor map of q, k or v");
-    p.plan = Workspace(*a, false).plan > 0 ? static_cast<uint32_t*>(workspace) : nullptr;
+    const Workspace ws(*a, false);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    p.plan = ws.plan > 0 ? reinterpret_cast<uint32_t*>(at) : nullptr;
+    fp.split = ws.forward;
+    if (ws.parts > 0) {
+        const size_t rows = ws.parts / (size_t(a->D) * sizeof(float) + sizeof(float2));
+        fp.split.part = reinterpret_cast<float*>(at + ws.plan);
+        fp.split.stat = reinterpret_cast<float2*>(fp.split.part + rows * size_t(a->D));
+    }
     fp.q_tiles = (p.Sq + tfu::kAttnPair - 1) / tfu::kAttnPair;
     int launches = 0;
     const cudaError_t e = tfu::launch_attention(fp, bf16, static_cast<cudaStream_t>(stream), &launches);
@@ -194,6 +222,9 @@ TF_API tf_status tf_ulysses_attention_backward(const tf_attention* a, const void
     p.delta = reinterpret_cast<float*>(at);
     p.plan = ws.plan > 0 ? reinterpret_cast<uint32_t*>(at + ws.delta) : nullptr;
     bp.key_plan = ws.plan > 0 ? reinterpret_cast<uint32_t*>(at + ws.delta + ws.plan) : nullptr;
+    bp.dq_split = ws.dq;
+    bp.dkv_split = ws.dkv;
+    bp.dq_split.part = bp.dkv_split.part = reinterpret_cast<float*>(at + ws.delta + ws.plan + ws.key_plan);
     bp.q_tiles = (p.Sq + tfu::kAttnRows - 1) / tfu::kAttnRows;
     bp.k_tiles = (p.Sk + tfu::kAttnRows - 1) / tfu::kAttnRows;
     int launches = 0;
