@@ -6,11 +6,11 @@
 // reading the codes once, 2 D bytes a key and head.
 //
 // kv_decode_kernel: a CTA of 4 warps takes 16 rows of one key head and a chunk of the
-// keys; each warp walks its own part in steps of 16 keys and the warps join at the end.
-// Codes go from memory straight into registers in the layout of mma.m16n8k16 -- the order
-// of the summed dimensions is free, so lane (g, t) takes 16 consecutive bytes of key g for
-// Q K^T, and of keys 2t, 2t+1, 2t+8, 2t+9 for P V, where bytes of two keys are paired by a
-// permute -- and become fp16 exactly (e4m3 fits); no shared memory is passed.
+// keys; each warp walks its own part in steps of 16 keys, copied ahead into a ring of its own in
+// shared memory, and the warps join at the end.  The products are mma.m16n8k16: the order of
+// the summed dimensions is free, so lane (g, t) takes 16 consecutive bytes of key g for Q K^T,
+// and of keys 2t, 2t+1, 2t+8, 2t+9 for P V, where bytes of two keys are paired by a permute;
+// codes become fp16 exactly (e4m3 fits).
 //  * Q in fp16 times a power of two for each row that puts its largest value at 2^14: exact
 //    but for values 2^28 below it; the factor goes into the score's scale.
 //  * P in fp16 times the page's V scale relative to the largest one so far (O is rescaled
@@ -28,6 +28,7 @@ using namespace dev;
 
 constexpr int kWarps = 4;
 constexpr int kStep = 16;      // keys of a warp's step; a page is a whole number of steps
+constexpr int kRing = 4;       // steps of a warp in shared memory: one computed, three on their way
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -35,27 +36,49 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+__device__ __forceinline__ void copy_async16(uint32_t smem, const void* global) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// The codes of one step in flight.
+// A step in shared memory: 16 keys of K, then of V, rows of kD codes in 16-byte chunks that are
+// swapped about so that the fragments' reads meet no bank twice: K by rows g with chunks
+// t, V by rows 2t with chunks g.
 template <int kD>
-struct Codes {
-    uint32_t k[2][kD / 16];  // keys g and g + 8: kD / 64 pieces of 16 bytes
-    uint32_t v[4][kD / 32];  // keys 2t, 2t + 1, 2t + 8, 2t + 9: kD / 8 bytes from dim g * kD / 8
+struct StepLayout {
+    static constexpr uint32_t kHalf = kStep * kD, kBytes = 2 * kHalf;
+    static constexpr uint32_t kChunks = kD / 16;  // of a row
+    __device__ static __forceinline__ uint32_t k(uint32_t row, uint32_t chunk) {
+        if constexpr (kD == 128) return row * 128 + ((chunk ^ ((row & 1u) * 4 | (row >> 1 & 3u))) * 16);
+        return row * 64 + chunk * 16;
+    }
+    __device__ static __forceinline__ uint32_t v(uint32_t row, uint32_t chunk) {
+        if constexpr (kD == 128) return kHalf + row * 128 + ((chunk ^ (row >> 1 & 3u) * 2) * 16);
+        return kHalf + (row >> 1) * 128 + ((((row & 1u) * 4 + chunk) ^ (row >> 1 & 3u) * 2) * 16);
+    }
+};
+
+// What a step needs beside its codes.
+struct StepInfo {
     float ks, vs;
-    int keys;                // visible ones of the step
+    int keys;  // visible ones; 0: its page is out of range
 };
 
 template <Fused kF, int kD>
-__global__ void __launch_bounds__(kWarps * 32, 2) kv_decode_kernel(const __grid_constant__ KvAttendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) kv_decode_kernel(const __grid_constant__ KvAttendParams p) {
     constexpr int kSteps = kD / 16;   // k-steps of Q K^T
     constexpr int kTilesO = kD / 8;   // column tiles of O
-    __shared__ float o_all[kWarps][kDecodeRows][kD + 4];
+    using Layout = StepLayout<kD>;
+    // the rings; at the end the warps' sums
+    extern __shared__ __align__(16) uint8_t rings[];
+    auto o_all = reinterpret_cast<float(*)[kDecodeRows][kD + 4]>(rings);
+    static_assert(sizeof(float) * kDecodeRows * (kD + 4) <= kRing * Layout::kBytes, "the sums take the rings' place");
     __shared__ float m_all[kWarps][kDecodeRows], l_all[kWarps][kDecodeRows];
+    __shared__ StepInfo infos[kWarps][kRing];
     grid_dependency_wait();
     const KvCache& c = p.c;
     const uint32_t n = blockIdx.z, row_tiles = gridDim.y / c.Hkv, kh = blockIdx.y / row_tiles;
@@ -109,57 +132,67 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_decode_kernel(const __grid_
 #pragma unroll
         for (int y = 0; y < 4; ++y) o[s][y] = 0.f;
 
-    // the pages of 32 steps at a time, one a lane
-    int id_of = 0;
-    float ks_of = 0.f, vs_of = 0.f;
+    // the pages of 32 steps, one a lane, and of the 32 after them
+    struct Pages {
+        int id;
+        float ks, vs;
+    };
     auto pages = [&](int j) {
+        Pages d{-1, 0.f, 0.f};
         const int key = j + int(lane) * kStep;
-        id_of = -1;
-        ks_of = vs_of = 0.f;
         if (key < last) {
             const int id = c.table[int64_t(n) * c.table_stride + uint32_t(key) / c.page];
             if (id >= 0 && uint32_t(id) < c.pages) {
-                id_of = id;
-                ks_of = c.scales[0][int64_t(id) * c.Hkv + kh];
-                vs_of = c.scales[1][int64_t(id) * c.Hkv + kh];
+                d.id = id;
+                d.ks = c.scales[0][int64_t(id) * c.Hkv + kh];
+                d.vs = c.scales[1][int64_t(id) * c.Hkv + kh];
             } else {
                 atomicOr(&g_kv_attend_status, 1u);
             }
         }
+        return d;
     };
-    auto load = [&](Codes<kD>& d, int j) {  // j - first is a multiple of kStep
-        const int w = (j - first) / kStep % 32;
-        if (w == 0) pages(j);
-        const int id = __shfl_sync(0xffffffffu, id_of, w);
-        d.ks = __shfl_sync(0xffffffffu, ks_of, w);
-        d.vs = __shfl_sync(0xffffffffu, vs_of, w);
-        d.keys = id < 0 ? 0 : min(kStep, last - j);
-        if (id < 0) return;
-        const int64_t at = (int64_t(id) * c.Hkv + kh) * c.page + uint32_t(j) % c.page;
-        const uint8_t* k = c.codes[0] + at * kD;
-        const uint8_t* v = c.codes[1] + at * kD;
+    const uint32_t ring = smem_u32(rings) + warp * (kRing * Layout::kBytes);
+    Pages now = pages(first), next = pages(first + 32 * kStep);
+    auto load = [&](int s) {  // step s of this warp; always one group
+        const int j = first + s * kStep;
+        if (j < last) {
+            if (s > 0 && s % 32 == 0) {
+                now = next;
+                next = pages(j + 32 * kStep);
+            }
+            const int id = __shfl_sync(0xffffffffu, now.id, s % 32);
+            const float ks = __shfl_sync(0xffffffffu, now.ks, s % 32), vs = __shfl_sync(0xffffffffu, now.vs, s % 32);
+            if (lane == 0) infos[warp][s % kRing] = StepInfo{ks, vs, id < 0 ? 0 : min(kStep, last - j)};
+            if (id >= 0) {
+                const int64_t at = ((int64_t(id) * c.Hkv + kh) * c.page + uint32_t(j) % c.page) * kD;
+                const uint32_t to = ring + s % kRing * Layout::kBytes;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int y = 0; y < kD / 64; ++y)
-                *reinterpret_cast<uint4*>(&d.k[x][4 * y]) = ld_codes16(k + (g + 8 * x) * kD + y * 64 + t * 16);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint8_t* row = v + (2 * t + x % 2 + x / 2 * 8) * kD + g * (kD / 8);
-            if constexpr (kD == 128)
-                *reinterpret_cast<uint4*>(&d.v[x][0]) = ld_codes16(row);
-            else
-                *reinterpret_cast<uint2*>(&d.v[x][0]) = ld_codes8(row);
+                for (uint32_t x = 0; x < Layout::kHalf / 512; ++x) {
+                    const uint32_t piece = x * 32 + lane, row = piece / Layout::kChunks, chunk = piece % Layout::kChunks;
+                    copy_async16(to + Layout::k(row, chunk), c.codes[0] + at + piece * 16);
+                    copy_async16(to + Layout::v(row, chunk), c.codes[1] + at + piece * 16);
+                }
+            }
         }
+        copy_async_commit();
     };
-    auto step = [&](Codes<kD>& d, int j) {
+    auto step = [&](int number) {
+        const int j = first + number * kStep;
+        const StepInfo d = infos[warp][number % kRing];
         if (d.keys == 0) return;
+        const uint8_t* codes = rings + warp * (kRing * Layout::kBytes) + number % kRing * Layout::kBytes;
         float s[2][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
 #pragma unroll
-            for (int y = 0; y < kSteps; ++y) mma_f16(s[x], qf[y], to_f16x2(d.k[x][y]), to_f16x2(d.k[x][y] >> 16));
+            for (int z = 0; z < kD / 64; ++z) {
+                const uint4 w4 = *reinterpret_cast<const uint4*>(codes + Layout::k(g + 8 * x, 4 * z + t));
+                const uint32_t* w = &w4.x;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mma_f16(s[x], qf[4 * z + y], to_f16x2(w[y]), to_f16x2(w[y] >> 16));
+            }
         }
         // s[x][2 * row + e]: key j + 8x + 2t + e
         float top[2] = {-INFINITY, -INFINITY};
@@ -237,18 +270,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_decode_kernel(const __grid_
                 a[2 * x + r] = pack2<Fused::kFP16>(e0 * fv, e1 * fv);
             }
         }
+        uint32_t v[4][kD / 32];  // keys 2t, 2t + 1, 2t + 8, 2t + 9: kD / 8 codes from dimension g * kD / 8 on
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const uint32_t row = 2 * t + x % 2 + x / 2 * 8;
+            if constexpr (kD == 128)
+                *reinterpret_cast<uint4*>(v[x]) = *reinterpret_cast<const uint4*>(codes + Layout::v(row, g));
+            else
+                *reinterpret_cast<uint2*>(v[x]) = *reinterpret_cast<const uint2*>(codes + Layout::v(row, g / 2) + g % 2 * 8);
+        }
         if (d.keys < kStep) {  // what lies behind the sequence may be anything
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 if (2 * int(t) + x % 2 + x / 2 * 8 >= d.keys) {
 #pragma unroll
-                    for (int y = 0; y < kD / 32; ++y) d.v[x][y] = 0;
+                    for (int y = 0; y < kD / 32; ++y) v[x][y] = 0;
                 }
         }
 #pragma unroll
         for (int y = 0; y < kD / 32; ++y) {
-            const uint32_t lo0 = __byte_perm(d.v[0][y], d.v[1][y], 0x5140), hi0 = __byte_perm(d.v[0][y], d.v[1][y], 0x7362);
-            const uint32_t lo1 = __byte_perm(d.v[2][y], d.v[3][y], 0x5140), hi1 = __byte_perm(d.v[2][y], d.v[3][y], 0x7362);
+            const uint32_t lo0 = __byte_perm(v[0][y], v[1][y], 0x5140), hi0 = __byte_perm(v[0][y], v[1][y], 0x7362);
+            const uint32_t lo1 = __byte_perm(v[2][y], v[3][y], 0x5140), hi1 = __byte_perm(v[2][y], v[3][y], 0x7362);
             mma_f16(o[4 * y], a, to_f16x2(lo0), to_f16x2(lo1));
             mma_f16(o[4 * y + 1], a, to_f16x2(lo0 >> 16), to_f16x2(lo1 >> 16));
             mma_f16(o[4 * y + 2], a, to_f16x2(hi0), to_f16x2(hi1));
@@ -256,19 +298,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_decode_kernel(const __grid_
         }
     };
 
-    // two steps in flight behind the one that is computed
-    if (first < last) {
-        Codes<kD> d[2];
-        load(d[0], first);
-        for (int j = first; j < last; j += 2 * kStep) {
-            if (j + kStep < last) load(d[1], j + kStep);
-            step(d[0], j);
-            if (j + kStep < last) {
-                if (j + 2 * kStep < last) load(d[0], j + 2 * kStep);
-                step(d[1], j + kStep);
-            }
-        }
+    const int mine = first < last ? (last - first + kStep - 1) / kStep : 0;
+#pragma unroll
+    for (int s = 0; s < kRing - 1; ++s) load(s);
+    for (int s = 0; s < mine; ++s) {
+        copy_async_wait<kRing - 2>();
+        __syncwarp();  // every lane's copies of step s have landed; step s - 1 has been read
+        load(s + kRing - 1);
+        step(s);
     }
+    copy_async_wait<0>();
+    __syncthreads();  // the sums take the rings' place
 
     // join the warps: column 2t + e of O's tile s is dimension (2t + e) * kD / 8 + s
 #pragma unroll
@@ -367,10 +407,11 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
 }
 
 template <typename... Args>
-cudaError_t launch_grid(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t stream, const Args&... args) {
+cudaError_t launch_grid(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -383,13 +424,20 @@ cudaError_t launch_grid(void (*kernel)(Args...), dim3 grid, int threads, cudaStr
 template <Fused kF, int kD>
 cudaError_t launch(const KvAttendParams& p, cudaStream_t stream, int* launches) {
     const uint32_t rows = p.max_tokens * p.shared;
-    cudaError_t e = p.tiles ? launch_kv_tiles(p, kF == Fused::kBF16, stream)
-                            : launch_grid(kv_decode_kernel<kF, kD>, dim3(p.chunks, p.c.Hkv * (p.row_cap / kDecodeRows), p.c.N), kWarps * 32,
-                                stream, p);
+    cudaError_t e;
+    if (p.tiles) {
+        e = launch_kv_tiles(p, kF == Fused::kBF16, stream);
+    } else {
+        constexpr size_t smem = size_t(kWarps) * kRing * StepLayout<kD>::kBytes;
+        e = cudaFuncSetAttribute(kv_decode_kernel<kF, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+        e = launch_grid(kv_decode_kernel<kF, kD>, dim3(p.chunks, p.c.Hkv * (p.row_cap / kDecodeRows), p.c.N), kWarps * 32, smem,
+                        stream, p);
+    }
     if (e != cudaSuccess) return e;
     *launches += 1;
     if (p.chunks > 1) {
-        e = launch_grid(kv_join_kernel<kF, kD>, dim3((rows + 7) / 8, p.c.Hkv, p.c.N), 256, stream, p);
+        e = launch_grid(kv_join_kernel<kF, kD>, dim3((rows + 7) / 8, p.c.Hkv, p.c.N), 256, 0, stream, p);
         if (e != cudaSuccess) return e;
         *launches += 1;
     }
