@@ -53,6 +53,7 @@ struct KvAttendParams {
     float2* part_stat;       // [N][Hkv][row_cap][chunks] (reference in log2 units, sum)
     uint32_t chunk, chunks;  // keys of a chunk, chunks of the longest sequence
     uint32_t row_cap;        // rows (token, query head) of a key head, rounded up to row tiles
+    uint32_t unit;           // rows of a CTA
     bool tiles;              // many rows: kv_attend_tiles.cu
     float* lse[kMaxShards];  // [Hl][T] per group, or null
     const float* slopes;     // [P * Hl] or null
@@ -62,8 +63,7 @@ struct KvAttendParams {
     uint32_t causal;
 };
 
-constexpr uint32_t kDecodeRows = 16;  // rows of a CTA of the decode kernel
-constexpr uint32_t kTileRows = 256;   // of the tile kernel
+constexpr uint32_t kTileRows = 256;  // rows of a CTA of the tile kernel
 
 cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_kv_attend(const KvAttendParams& p, bool bf16, cudaStream_t stream, int* launches);

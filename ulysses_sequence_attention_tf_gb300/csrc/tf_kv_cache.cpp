@@ -83,7 +83,8 @@ constexpr uint32_t kTargetCtas = 2432, kLeastChunk = 512, kMostChunk = 8192, kCh
 void plan_chunks(tfu::KvAttendParams* p) {
     const uint32_t rows = p->max_tokens * p->shared;
     p->tiles = rows > kDecodeMost;
-    const uint32_t unit = p->tiles ? tfu::kTileRows : tfu::kDecodeRows;
+    const uint32_t unit = p->tiles ? tfu::kTileRows : rows <= 8 ? 8 : 16;
+    p->unit = unit;
     p->row_cap = (rows + unit - 1) / unit * unit;
     const uint64_t ctas = uint64_t(p->c.N) * p->c.Hkv * (p->row_cap / unit);
     uint64_t chunk;
@@ -133,7 +134,7 @@ tf_status check_kv_attention(const tf_kv_cache* c, const tf_kv_attention* a, tfu
     p->max_len = uint32_t(a->max_len);
     p->causal = uint32_t(a->causal);
     plan_chunks(p);
-    if (uint64_t(c->N) * c->Hkv * (p->row_cap / tfu::kDecodeRows) * p->chunks >= (uint64_t(1) << 31))
+    if (uint64_t(c->N) * c->Hkv * (p->row_cap / p->unit) * p->chunks >= (uint64_t(1) << 31))
         return fail(TF_ERR_UNSUPPORTED, "problem exceeds 2^31 work units");
     return TF_OK;
 }
