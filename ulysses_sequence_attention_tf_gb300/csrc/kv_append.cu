@@ -49,209 +49,239 @@ __device__ __forceinline__ float scale_of(float most) {
     return __uint_as_float(uint32_t((e < kLeastExponent ? kLeastExponent : e) + 127) << 23);
 }
 
-// The lane's 8 values of a row, normalised (weight not null) and rotated.
-template <Fused kF, int kLanes>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], const uint32_t (&raw)[4], const uint32_t* weight, float eps,
-                                            const float* table, Rope rope) {
-    const uint32_t lane = threadIdx.x % kLanes;
+// A lane's 16 values of a row: elements [8l, 8l + 8) and kD / 2 further on, so that both kinds of
+// pairs lie within a lane.  raw[i]: values 2i, 2i + 1 of x.
+template <int kD>
+struct Lane {
+    static constexpr int kLanes = kD / 16;  // of a row
+    __device__ static __forceinline__ void load(uint32_t (&raw)[8], const uint8_t* row, bool in) {
+        const uint32_t l = threadIdx.x % kLanes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack2<kF>(raw[i], x[2 * i], x[2 * i + 1]);
-    if (weight) {
-        uint64_t x2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x2[i] = f2_pack(x[2 * i], x[2 * i + 1]);
-        const float ms = row_mean_sq<kLanes, 4, true>(x2, nullptr);
-        const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(ms, eps)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float a, b;
-            unpack2<kF>(__ldg(weight + lane * 4 + i), a, b);
-            x[2 * i] = __fmul_rn(__fmul_rn(x[2 * i], inv), a);
-            x[2 * i + 1] = __fmul_rn(__fmul_rn(x[2 * i + 1], inv), b);
+        for (int h = 0; h < 2; ++h) {
+            const uint4 w = in ? *reinterpret_cast<const uint4*>(row + h * kD + l * 16) : make_uint4(0, 0, 0, 0);
+            raw[4 * h] = w.x, raw[4 * h + 1] = w.y, raw[4 * h + 2] = w.z, raw[4 * h + 3] = w.w;
         }
     }
-    if (rope == Rope::kInterleaved) {
-        const float* t = table + lane * 8;  // entries 4 * lane ..: (cos, sin) of pairs (2i, 2i + 1)
+};
+
+// The lane's values, normalised (kNorm: w holds the weights) and rotated; table: the row's
+// (cos, sin) entries.
+template <Fused kF, int kD>
+__device__ __forceinline__ void norm_rotate(float (&x)[16], const uint32_t (&raw)[8], bool norm, const float (&w)[16], float eps,
+                                            const float* table, Rope rope) {
+    constexpr int kLanes = Lane<kD>::kLanes;
+    const uint32_t l = threadIdx.x % kLanes;
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const float4 cs = ld_table(t + 2 * i);
-            float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x));
-            a = x[2 * i + 2];
-            b = x[2 * i + 3];
-            x[2 * i + 2] = __fsub_rn(__fmul_rn(a, cs.z), __fmul_rn(b, cs.w));
-            x[2 * i + 3] = __fadd_rn(__fmul_rn(a, cs.w), __fmul_rn(b, cs.z));
-        }
+    for (int i = 0; i < 8; ++i) unpack2<kF>(raw[i], x[2 * i], x[2 * i + 1]);
+    if (norm) {
+        uint64_t x2[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x2[i] = f2_pack(x[2 * i], x[2 * i + 1]);
+        const float ms = row_mean_sq<kLanes, 8, true>(x2, nullptr);
+        const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(ms, eps)));
+        const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f2_unpack(f2_mul(f2_mul(x2[i], inv2), f2_pack(w[2 * i], w[2 * i + 1])), x[2 * i], x[2 * i + 1]);
+    }
+    if (rope == Rope::kInterleaved) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {  // entries of pairs (8h + 2i, + 1) and (8h + 2i + 2, + 3)
+                const float4 cs = ld_table(table + h * (kD / 2) + l * 8 + 2 * i);
+                float* v = x + 8 * h + 2 * i;
+                float a = v[0], b = v[1];
+                v[0] = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+                v[1] = __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x));
+                a = v[2];
+                b = v[3];
+                v[2] = __fsub_rn(__fmul_rn(a, cs.z), __fmul_rn(b, cs.w));
+                v[3] = __fadd_rn(__fmul_rn(a, cs.w), __fmul_rn(b, cs.z));
+            }
     } else if (rope == Rope::kHalfSplit) {
-        const bool upper = lane >= kLanes / 2;
-        const float* t = table + (lane % (kLanes / 2)) * 16;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float4 cs = ld_table(t + 2 * i);
-            const float y0 = __shfl_xor_sync(0xffffffffu, x[i], kLanes / 2);
-            const float y1 = __shfl_xor_sync(0xffffffffu, x[i + 1], kLanes / 2);
-            x[i] = upper ? __fadd_rn(__fmul_rn(y0, cs.y), __fmul_rn(x[i], cs.x))
-                         : __fsub_rn(__fmul_rn(x[i], cs.x), __fmul_rn(y0, cs.y));
-            x[i + 1] = upper ? __fadd_rn(__fmul_rn(y1, cs.w), __fmul_rn(x[i + 1], cs.z))
-                             : __fsub_rn(__fmul_rn(x[i + 1], cs.z), __fmul_rn(y1, cs.w));
+            const float4 cs = ld_table(table + l * 16 + 2 * i);
+            float a = x[i], b = x[i + 8];
+            x[i] = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+            x[i + 8] = __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x));
+            a = x[i + 1];
+            b = x[i + 9];
+            x[i + 1] = __fsub_rn(__fmul_rn(a, cs.z), __fmul_rn(b, cs.w));
+            x[i + 9] = __fadd_rn(__fmul_rn(a, cs.w), __fmul_rn(b, cs.z));
         }
     }
 }
 
-// kIters: passes of kAppendThreads / (D / 8) rows that a page takes.
+// kIters: passes of kAppendThreads / (D / 16) rows that a page takes.
 template <Fused kF, int kD, int kIters>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
-    constexpr int kLanes = kD / 8, kRows = kAppendThreads / kLanes;
-    __shared__ float most_of[kAppendThreads / 32];
+__global__ void __launch_bounds__(kAppendThreads, kIters == 4 ? 2 : 3) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+    constexpr int kLanes = Lane<kD>::kLanes, kRows = kAppendThreads / kLanes;
+    __shared__ float most_of[2][kAppendThreads / 32];
     grid_dependency_wait();
     const KvCache& c = p.c;
-    const uint32_t unit = blockIdx.x;
+    const uint32_t unit = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+    const uint32_t shift = 31 - __clz(c.page);  // pages are powers of two
     // the last sequence whose first unit is not behind this one
     uint32_t before = 0;
     for (uint32_t n0 = 0; n0 < c.N; n0 += kAppendThreads) {
         const uint32_t n = n0 + threadIdx.x;
-        before += __syncthreads_count(n < c.N && int64_t(c.starts[n]) / c.page + 2 * int64_t(n) <= int64_t(unit));
+        before += __syncthreads_count(n < c.N && int64_t(c.starts[n] >> shift) + 2 * int64_t(n) <= int64_t(unit));
     }
     if (before == 0) return;  // rows in front of starts[0] belong to no sequence
     const uint32_t n = before - 1;
     const int64_t s0 = c.starts[n], s1 = c.starts[n + 1], len = c.lens[n];
     const int64_t new_rows = s1 - s0;
-    if (s0 < 0 || new_rows < 0 || s1 > int64_t(p.T) || len < new_rows || len > int64_t(c.max_pages) * c.page ||
+    if (s0 < 0 || new_rows < 0 || s1 > int64_t(p.T) || len < new_rows || len > int64_t(c.max_pages) << shift ||
         (p.rope != Rope::kNone && len > int64_t(p.table_rows))) {
         if (threadIdx.x == 0) atomicOr(&g_kv_append_status, 1u);
         return;
     }
     const int64_t first = len - new_rows;
-    const int64_t at = first / c.page + (int64_t(unit) - (s0 / c.page + 2 * int64_t(n)));  // page of the sequence
-    const int64_t lo = max(first, at * c.page), hi = min(len, (at + 1) * c.page);
+    const int64_t at = (first >> shift) + (int64_t(unit) - ((s0 >> shift) + 2 * int64_t(n)));  // page of the sequence
+    const int64_t lo = max(first, at << shift), hi = min(len, (at + 1) << shift);
     if (lo >= hi) return;
-    const uint32_t rows = uint32_t(hi - lo), off = uint32_t(lo - at * c.page);
+    const uint32_t rows = uint32_t(hi - lo), off = uint32_t(lo - (at << shift));
     const int64_t row0 = s0 + (lo - first);
     const uint32_t lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-
-    uint32_t y = blockIdx.y;
-    const bool is_q = y >= 2 * c.Hkv;
-    const uint32_t x = is_q ? 0 : y / c.Hkv;  // 0: K, 1: V
-    const uint32_t head = is_q ? y - 2 * c.Hkv : y % c.Hkv;
-    const uint32_t per_group = is_q ? p.Hl : p.Hkl;
-    const RowView& v = is_q ? p.q : p.src[x];
-    const uint8_t* src = v.base[head / per_group] + int64_t(head % per_group) * v.h + row0 * v.t + lane * 16;
-    const bool plain = !is_q && x == 1;
-    const uint32_t* weight = plain ? nullptr : static_cast<const uint32_t*>(p.weight[is_q ? 1 : 0]);
-    const Rope rope = plain ? Rope::kNone : p.rope;
-
-    if (is_q) {
-        uint8_t* dst = p.q_out.base[head / per_group] + int64_t(head % per_group) * p.q_out.h + row0 * p.q_out.t + lane * 16;
-#pragma unroll 1
-        for (uint32_t r0 = 0; r0 < rows; r0 += kRows) {
-            const uint32_t r = r0 + slot;
-            const bool in = r < rows;
-            uint32_t raw[4] = {0, 0, 0, 0};
-            if (in) {
-                const uint4 w = *reinterpret_cast<const uint4*>(src + int64_t(r) * v.t);
-                raw[0] = w.x, raw[1] = w.y, raw[2] = w.z, raw[3] = w.w;
-            }
-            float f[8];
-            norm_rotate<kF, kLanes>(f, raw, weight, p.eps, p.table + (in ? lo + r : lo) * kD, rope);
-            if (in)
-                *reinterpret_cast<uint4*>(dst + int64_t(r) * p.q_out.t) = make_uint4(
-                    pack2<kF>(f[0], f[1]), pack2<kF>(f[2], f[3]), pack2<kF>(f[4], f[5]), pack2<kF>(f[6], f[7]));
-        }
-        return;
-    }
-
     const int64_t id = c.table[int64_t(n) * c.table_stride + at];
-    if (id < 0 || id >= int64_t(c.pages)) {
-        if (threadIdx.x == 0) atomicOr(&g_kv_append_status, 1u);
-        return;
-    }
-    uint8_t* codes = c.codes[x] + (id * c.Hkv + head) * int64_t(c.page) * kD;
-    float* scale_at = c.scales[x] + id * c.Hkv + head;
-    const float old = off ? *scale_at : 0.f;
+    const bool bad = id < 0 || id >= int64_t(c.pages);
+    if (bad && threadIdx.x == 0) atomicOr(&g_kv_append_status, 1u);
 
-    float f[kIters][8];
-    float most = 0.f;
-    uint32_t raw[kIters][4];
+    // heads of K, of V, of Q: this CTA takes every slices-th; the next one's rows are on their way
+    // while one is computed
+    struct Head {
+        uint32_t kind, head;  // 0: K, 1: V, 2: Q
+        const uint8_t* src;
+        int64_t step;
+    };
+    const uint32_t heads = 2 * c.Hkv + (p.q.base[0] ? p.P * p.Hl : 0);
+    auto head_of = [&](uint32_t y) {
+        Head d;
+        d.kind = y < c.Hkv ? 0 : y < 2 * c.Hkv ? 1 : 2;
+        d.head = y - d.kind * c.Hkv;
+        const RowView& v = d.kind == 2 ? p.q : p.src[d.kind];
+        const uint32_t per_group = d.kind == 2 ? p.Hl : p.Hkl;
+        d.step = v.t;
+        d.src = v.base[d.head / per_group] + int64_t(d.head % per_group) * v.h + row0 * v.t;
+        return d;
+    };
+    auto load = [&](uint32_t (&raw)[kIters][8], const Head& d, bool any) {
 #pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-        const uint32_t r = it * kRows + slot;
-        const uint4 w = r < rows ? *reinterpret_cast<const uint4*>(src + int64_t(r) * v.t) : make_uint4(0, 0, 0, 0);
-        raw[it][0] = w.x, raw[it][1] = w.y, raw[it][2] = w.z, raw[it][3] = w.w;
-    }
+        for (int it = 0; it < kIters; ++it) {
+            const uint32_t r = it * kRows + slot;
+            Lane<kD>::load(raw[it], d.src + int64_t(r) * d.step, any && r < rows);
+        }
+    };
+    uint32_t raw[kIters][8];
+    Head now = head_of(slice);
+    load(raw, now, slice < heads);
+    uint32_t turn = 0;
+    for (uint32_t y = slice; y < heads; y += p.slices, turn ^= 1u) {
+        const bool plain = now.kind == 1;
+        const uint8_t* weight = plain ? nullptr : static_cast<const uint8_t*>(p.weight[now.kind == 2 ? 1 : 0]);
+        const Rope rope = plain ? Rope::kNone : p.rope;
+        float w[16];
+        {
+            uint32_t packed[8];
+            Lane<kD>::load(packed, weight, weight != nullptr);
 #pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-        const uint32_t r = it * kRows + slot;
-        norm_rotate<kF, kLanes>(f[it], raw[it], weight, p.eps, p.table + (r < rows ? lo + r : lo) * kD, rope);
-        if (r < rows) {
+            for (int i = 0; i < 8; ++i) unpack2<kF>(packed[i], w[2 * i], w[2 * i + 1]);
+        }
+        float* scale_at = c.scales[plain ? 1 : 0] + (bad ? 0 : id * c.Hkv + now.head);
+        const float old = now.kind < 2 && off && !bad ? *scale_at : 0.f;
+        float f[kIters][16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+        for (int it = 0; it < kIters; ++it) {
+            const uint32_t r = it * kRows + slot;
+            norm_rotate<kF, kD>(f[it], raw[it], weight != nullptr, w, p.eps, p.table + (r < rows ? lo + r : lo) * kD, rope);
+        }
+        const Head done = now;
+        now = head_of(y + p.slices < heads ? y + p.slices : y);
+        load(raw, now, y + p.slices < heads);
+        if (done.kind == 2) {
+            const uint32_t g = done.head / p.Hl, h = done.head % p.Hl;
+            uint8_t* dst = p.q_out.base[g] + int64_t(h) * p.q_out.h + row0 * p.q_out.t + lane * 16;
+#pragma unroll
+            for (int it = 0; it < kIters; ++it) {
+                const uint32_t r = it * kRows + slot;
+                if (r >= rows) continue;
+                const float* e = f[it];
+#pragma unroll
+                for (int x = 0; x < 2; ++x, e += 8)
+                    *reinterpret_cast<uint4*>(dst + int64_t(r) * p.q_out.t + x * kD) =
+                        make_uint4(pack2<kF>(e[0], e[1]), pack2<kF>(e[2], e[3]), pack2<kF>(e[4], e[5]), pack2<kF>(e[6], e[7]));
+            }
+            continue;
+        }
+        if (bad) continue;  // the same for the whole CTA
+        float most = 0.f;
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+            if (it * kRows + slot >= rows) continue;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
                 const float a = fabsf(f[it][i]);
                 most = a <= kFltMax ? fmaxf(most, a) : most;
             }
         }
-    }
 #pragma unroll
-    for (int w = 16; w; w >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
-    if (threadIdx.x % 32 == 0) most_of[threadIdx.x / 32] = most;
-    __syncthreads();
+        for (int x = 16; x; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+        if (threadIdx.x % 32 == 0) most_of[turn][threadIdx.x / 32] = most;
+        __syncthreads();  // also: every thread has read the old scale, and the other turn's maxima
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) most = fmaxf(most, most_of[w]);
-    const float fresh = scale_of(most);
-    const float scale = fmaxf(old, fresh);
-    const float inv = 1.0f / scale;  // exact
-    if (off && old < scale) {  // the page's older tokens move to the larger scale
-        const float ratio = old * inv;
-        for (uint32_t i = threadIdx.x; i < off * kD / 8; i += kAppendThreads) {
-            uint2 w = reinterpret_cast<const uint2*>(codes)[i];
-            uint32_t* parts[2] = {&w.x, &w.y};
+        for (int x = 0; x < kAppendThreads / 32; ++x) most = fmaxf(most, most_of[turn][x]);
+        const float scale = fmaxf(old, scale_of(most));
+        const float inv = 1.0f / scale;  // exact
+        uint8_t* codes = c.codes[done.kind] + ((id * c.Hkv + done.head) << shift) * kD;
+        if (off && old < scale) {  // the page's older tokens move to the larger scale
+            const float ratio = old * inv;
+            for (uint32_t i = threadIdx.x; i < off * kD / 8; i += kAppendThreads) {
+                uint2 u = reinterpret_cast<const uint2*>(codes)[i];
+                uint32_t* parts[2] = {&u.x, &u.y};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 a = from_e4m3x2(uint16_t(*parts[h])), b = from_e4m3x2(uint16_t(*parts[h] >> 16));
+                    *parts[h] = uint32_t(e4m3x2(a.x * ratio, a.y * ratio)) | uint32_t(e4m3x2(b.x * ratio, b.y * ratio)) << 16;
+                }
+                reinterpret_cast<uint2*>(codes)[i] = u;
+            }
+        }
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+            const uint32_t r = it * kRows + slot;
+            if (r >= rows) continue;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float2 a = from_e4m3x2(uint16_t(*parts[h])), b = from_e4m3x2(uint16_t(*parts[h] >> 16));
-                *parts[h] = uint32_t(e4m3x2(a.x * ratio, a.y * ratio)) | uint32_t(e4m3x2(b.x * ratio, b.y * ratio)) << 16;
+                uint32_t u[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const float* e = f[it] + 8 * h + 4 * z;
+                    u[z] = uint32_t(e4m3x2(e[0] * inv, e[1] * inv)) | uint32_t(e4m3x2(e[2] * inv, e[3] * inv)) << 16;
+                }
+                *reinterpret_cast<uint2*>(codes + int64_t(off + r) * kD + h * (kD / 2) + lane * 8) = make_uint2(u[0], u[1]);
             }
-            reinterpret_cast<uint2*>(codes)[i] = w;
         }
+        if (threadIdx.x == 0) *scale_at = scale;
     }
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-        const uint32_t r = it * kRows + slot;
-        if (r >= rows) continue;
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            w[h] = uint32_t(e4m3x2(f[it][4 * h] * inv, f[it][4 * h + 1] * inv)) |
-                   uint32_t(e4m3x2(f[it][4 * h + 2] * inv, f[it][4 * h + 3] * inv)) << 16;
-        *reinterpret_cast<uint2*>(codes + int64_t(off + r) * kD + lane * 8) = make_uint2(w[0], w[1]);
-    }
-    if (threadIdx.x == 0) *scale_at = scale;  // every thread read the old one before the barrier above
 }
 
+// CTAs of a call: enough for kAppendCtas, so that a CTA takes several heads and has the next
+// one's rows on their way; a head each where there are few units.
+constexpr uint32_t kAppendCtas = 1824;
+
 template <Fused kF, int kD, int kIters>
-cudaError_t launch(const KvAppendParams& p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.units, 2 * p.c.Hkv + (p.q.base[0] ? p.P * p.Hl : 0));
-    cfg.blockDim = dim3(kAppendThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_append_kernel<kF, kD, kIters>, p);
+cudaError_t launch(KvAppendParams p, cudaStream_t stream) {
+    const uint32_t heads = 2 * p.c.Hkv + (p.q.base[0] ? p.P * p.Hl : 0), want = (kAppendCtas + p.units - 1) / p.units;
+    p.slices = want < heads ? want : heads;
+    return launch_overlapped(kv_append_kernel<kF, kD, kIters>, p.units * p.slices, kAppendThreads, 0, stream, p);
 }
 
 template <Fused kF>
 cudaError_t launch_typed(const KvAppendParams& p, cudaStream_t stream) {
-    if (p.c.D == 64)
-        return p.c.page <= 32 ? launch<kF, 64, 1>(p, stream) : p.c.page == 64 ? launch<kF, 64, 2>(p, stream)
-                                                                              : launch<kF, 64, 4>(p, stream);
-    switch (p.c.page) {
-        case 16: return launch<kF, 128, 1>(p, stream);
-        case 32: return launch<kF, 128, 2>(p, stream);
-        case 64: return launch<kF, 128, 4>(p, stream);
-        default: return launch<kF, 128, 8>(p, stream);
-    }
+    if (p.c.D == 64) return p.c.page <= 64 ? launch<kF, 64, 1>(p, stream) : launch<kF, 64, 2>(p, stream);
+    return p.c.page <= 32 ? launch<kF, 128, 1>(p, stream) : p.c.page == 64 ? launch<kF, 128, 2>(p, stream)
+                                                                           : launch<kF, 128, 4>(p, stream);
 }
 
 }  // namespace

@@ -40,6 +40,7 @@ struct KvAppendParams {
     Rope rope;
     uint32_t P, T, Hl, Hkl;
     uint32_t units;        // upper bound of the (sequence, page) pairs that get rows
+    uint32_t slices;       // CTAs of a unit (set by the launch)
 };
 
 // Attention over long caches is split along the keys: chunk c of a sequence is keys

@@ -190,7 +190,7 @@ TF_API tf_status tf_ulysses_kv_append(const tf_kv_cache* c, int P, int T, int H,
     }
     const int64_t heads = 2 * int64_t(c->Hkv) + (q ? H : 0);
     const int64_t units = int64_t(T) / c->page_size + 2 * int64_t(c->N);
-    if (heads > 65535 || units >= (int64_t(1) << 31)) return fail(TF_ERR_UNSUPPORTED, "too many heads, rows or sequences");
+    if (units * heads >= (int64_t(1) << 31)) return fail(TF_ERR_UNSUPPORTED, "too many heads, rows or sequences");
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;
     if (T == 0 || c->N == 0) return TF_OK;
