@@ -83,8 +83,6 @@ class PagedCache(NamedTuple):
     v_scale: torch.Tensor
 
 
-_Strides3, _Strides5 = Strides * 3, Strides * 5
-
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 FREE_FN = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
 
@@ -443,99 +441,39 @@ def gather_out(tag, attn, out=None, *, stream=None):
 
 
 # ---------------------------------------------------------------- attention and key-value cache
-# These calls are short on the GPU, so their checks take one pass over the tensors.
-class _OnStream:
-    """The stream of a call: torch allocates for it inside the context, so that memory which the call's kernels
-    use returns to the allocator in that stream's order."""
-
-    def __init__(self, stream):
-        self.device = torch._C._cuda_getDevice()
-        self.guard = None
-        if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(self.device)
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream))
-            self.guard = torch.cuda.stream(stream)
-            self.handle = stream.cuda_stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *error):
-        if self.guard is not None:
-            self.guard.__exit__(*error)
+# These calls are short on the GPU: their checks and marshalling are in csrc/torch_calls.cpp.
+_calls = None
 
 
-def _views(name, ts, P, shape, dtype, device):
-    """(pointers, strides) of P views of this shape, type and device with equal strides, the last one 1."""
-    if len(ts) != P:
-        raise ValueError(f"{name} must be a list of {P} head groups")
-    s = ts[0].stride()
-    ptrs = []
-    for t in ts:
-        if t.shape != shape or t.dtype != dtype or t.stride() != s:
-            raise ValueError(f"{name} must be {dtype} views of shape {tuple(shape)} with the same strides, not {t.dtype} "
-                             f"{tuple(t.shape)} with strides {t.stride()}")
-        if t.get_device() != device:
-            raise ValueError(f"{name} must be on the current device cuda:{device}, not {t.device}")
-        ptrs.append(t.data_ptr())
-    if s[-1] != 1 and shape[-1] > 1:
-        raise ValueError("the D dimension must have stride 1")
-    return ptrs, s[:3] if len(s) == 4 else (0, s[0], s[1])
+def _torch_calls():
+    """The module that marshals these calls, bound to the library's entry points; raises if it has not been built."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        try:
+            from . import _torch_calls as module
+        except ImportError as e:
+            raise TfUlyssesError(TF_ERR_INVALID, f"_torch_calls is not built (run __graft_entry__.build()): {e}") from e
+        names = ("attention", "attention_backward", "attention_workspace", "kv_append", "kv_attend", "kv_attend_workspace")
+        module.bind(_check, *[ctypes.cast(getattr(L, "tf_ulysses_" + n), ctypes.c_void_p).value for n in names])
+        _calls = module
+    return _calls
 
 
-def _made(P, shape, dtype, device):
-    """P new contiguous tensors and their pointers."""
-    ts = [torch.empty(shape, dtype=dtype, device=device) for _ in range(P)]
-    return ts, [t.data_ptr() for t in ts]
+def _on_stream(stream):
+    """The stream of a call as a context in which torch allocates for it, so that memory which the call's kernels use
+    returns to the allocator in that stream's order."""
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
-def _plain_array(name, t, dtype, shape, device):
-    """Data pointer of a contiguous tensor of this type and shape on the device, or None."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}, not {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _lse_arrays(lse, P, shape, device):
-    if len(lse) != P:
-        raise ValueError(f"lse must be a list of {P} tensors")
-    return [_plain_array("lse", t, torch.float32, shape, device) for t in lse]
-
-
-def _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs, device):
-    P = len(q)
-    if not 1 <= P <= MAX_SHARDS:
-        raise ValueError(f"q, k and v must be lists of the same P in [1, {MAX_SHARDS}] head groups")
-    q_shape, k_shape, dtype = q[0].shape, k[0].shape, q[0].dtype
-    if len(q_shape) != 4 or len(k_shape) != 4:
-        raise ValueError("expected 4-d views [B, tokens, heads, D]")
-    B, Sq, Hl, D = q_shape
-    Sk, Hkl = k_shape[1], k_shape[2]
-    qs, ks = _views("q", q, P, q_shape, dtype, device), _views("k", k, P, (B, Sk, Hkl, D), dtype, device)
-    vs = _views("v", v, P, k_shape, dtype, device)
-    a = Attention(P, B, Sq, Sk, P * Hl, P * Hkl, D, _dtype_code(dtype), D ** -0.5 if scale is None else scale, softcap,
-                  1 if causal else 0, _plain_array("slopes", slopes, torch.float32, (P * Hl,), device),
-                  _plain_array("prefix", prefix, torch.int32, (B,), device),
-                  _plain_array("q_docs", q_docs, torch.int32, (B, Sq), device),
-                  _plain_array("k_docs", k_docs, torch.int32, (B, Sk), device))
-    return a, qs, ks, vs
-
-
-def _workspace(ask, *args, device):
-    """A tensor of the bytes that the library asks for (None for 0), its address and size."""
-    n = ctypes.c_size_t()
-    _check(ask(*args, ctypes.byref(n)))
-    if n.value == 0:
-        return None, None, 0
-    t = torch.empty(n.value, dtype=torch.uint8, device=device)
-    return t, t.data_ptr(), n.value
+def _run(name, stream, before, after):
+    """``name`` of the module with the current device and the stream between its arguments."""
+    call = getattr(_calls or _torch_calls(), name)
+    device = torch._C._cuda_getDevice()
+    if stream is None:
+        return call(*before, device, torch._C._cuda_getCurrentRawStream(device), *after)
+    with _on_stream(stream):
+        return call(*before, device, torch._C._cuda_getCurrentRawStream(device), *after)
 
 
 def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=None, causal=False, prefix=None,
@@ -551,25 +489,7 @@ def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=No
     P tensors ``[B, Sq, H/P, D]`` and fp32 ``[B, H/P, Sq]``, 0 and -inf for rows that see
     nothing; both are made here unless given.
     """
-    L = lib()
-    with _OnStream(stream) as on:
-        device = on.device
-        a, (qp, q_str), (kp, k_str), (vp, v_str) = _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs,
-                                                              device)
-        shape, rows, dtype, P = q[0].shape, (a.B, a.H // a.P, a.Sq), q[0].dtype, a.P
-        if out is None:
-            (out, op), o_str = _made(P, shape, dtype, q[0].device), None
-        else:
-            op, o_str = _views("out", out, P, shape, dtype, device)
-        if lse is None:
-            lse, lp = _made(P, rows, torch.float32, q[0].device)
-        else:
-            lp = _lse_arrays(lse, P, rows, device)
-        ws, ws_at, ws_size = _workspace(L.tf_ulysses_attention_workspace, a, 0, device=q[0].device)
-        each = ctypes.c_void_p * P
-        _check(L.tf_ulysses_attention(a, each(*qp), each(*kp), each(*vp), _Strides3(q_str, k_str, v_str), each(*op),
-                                      Strides(*o_str) if o_str is not None else None, each(*lp), ws_at, ws_size, on.handle))
-    return out, lse
+    return _run("attention", stream, (q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs), (out, lse))
 
 
 def attention_backward(dout, q, k, v, out, lse, dq=None, dk=None, dv=None, *, scale=None, softcap=0.0, slopes=None,
@@ -578,31 +498,8 @@ def attention_backward(dout, q, k, v, out, lse, dq=None, dk=None, dv=None, *, sc
     the same inputs and options and its results ``out`` and ``lse``: lists of P tensors
     shaped like q, k and v, made here unless given.  Shared key heads get the sum over
     their query heads.  The same inputs give the same bits."""
-    L = lib()
-    with _OnStream(stream) as on:
-        device = on.device
-        a, (qp, q_str), (kp, k_str), (vp, v_str) = _attention(q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs,
-                                                              device)
-        dtype, P, q_shape, k_shape = q[0].dtype, a.P, q[0].shape, k[0].shape
-        dp, d_str = _views("dout", dout, P, q_shape, dtype, device)
-        op, o_str = _views("out", out, P, q_shape, dtype, device)
-        lp = _lse_arrays(lse, P, (a.B, a.H // P, a.Sq), device)
-        each = ctypes.c_void_p * P
-        grads, ptrs, strides = [], [], []
-        for name, ts, shape in (("dq", dq, q_shape), ("dk", dk, k_shape), ("dv", dv, k_shape)):
-            if ts is None:
-                ts, p = _made(P, shape, dtype, q[0].device)
-                own = (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3])
-            else:
-                p, own = _views(name, ts, P, shape, dtype, device)
-            grads.append(ts)
-            ptrs.append(each(*p))
-            strides.append(own)
-        ws, ws_at, ws_size = _workspace(L.tf_ulysses_attention_workspace, a, 1, device=q[0].device)
-        _check(L.tf_ulysses_attention_backward(a, each(*dp), each(*qp), each(*kp), each(*vp), each(*op), each(*lp),
-                                               _Strides5(d_str, q_str, k_str, v_str, o_str), *ptrs, _Strides3(*strides), ws_at,
-                                               ws_size, on.handle))
-    return tuple(grads)
+    return _run("attention_backward", stream, (q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs),
+                (dout, out, lse, dq, dk, dv))
 
 
 _ROPE = {None: 0, "interleaved": 1, "neox": 2}
@@ -614,25 +511,6 @@ def kv_cache(num_pages, Hkv, page_size, D, *, device="cuda"):
     codes = lambda: torch.zeros((num_pages, Hkv, page_size, D), dtype=torch.float8_e4m3fn, device=device)  # noqa: E731
     scales = lambda: torch.ones((num_pages, Hkv), dtype=torch.float32, device=device)  # noqa: E731
     return PagedCache(codes(), codes(), scales(), scales())
-
-
-def _kv_cache(cache, page_table, lens, starts, device):
-    k, v, k_scale, v_scale = cache
-    if k.dim() != 4:
-        raise ValueError("the cache's codes must be [pages, Hkv, page_size, D]")
-    shape, e4m3 = k.shape, torch.float8_e4m3fn
-    pages, Hkv, page, D = shape
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.get_device() != device:
-        raise ValueError(f"page_table must be int32 [N, max_pages] on cuda:{device}")
-    N, most = page_table.shape
-    if most > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table must have unit stride along a row")
-    return KvCache(_plain_array("k", k, e4m3, shape, device), _plain_array("v", v, e4m3, shape, device),
-                   _plain_array("k_scale", k_scale, torch.float32, shape[:2], device),
-                   _plain_array("v_scale", v_scale, torch.float32, shape[:2], device), pages, Hkv, page, D, N, most,
-                   page_table.data_ptr(), page_table.stride(0) if N > 1 else most,
-                   _plain_array("lens", lens, torch.int32, (N,), device),
-                   _plain_array("starts", starts, torch.int32, (N + 1,), device))
 
 
 def kv_append(cache, page_table, lens, starts, k, v, q=None, q_out=None, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -648,36 +526,8 @@ def kv_append(cache, page_table, lens, starts, k, v, q=None, q_out=None, *, q_we
     """
     if rope not in _ROPE:
         raise ValueError(f"rope must be 'interleaved', 'neox' or None, not {rope!r}")
-    with _OnStream(stream) as on:
-        device = on.device
-        c = _kv_cache(cache, page_table, lens, starts, device)
-        P, T, dtype, D = len(k), k[0].shape[0], k[0].dtype, c.D
-        if not 1 <= P <= MAX_SHARDS or c.Hkv % P:
-            raise ValueError(f"k must be a list of P in [1, {MAX_SHARDS}] head groups, P dividing Hkv={c.Hkv}")
-        shape = (T, c.Hkv // P, D)
-        kp, k_str = _views("k", k, P, shape, dtype, device)
-        vp, v_str = _views("v", v, P, shape, dtype, device)
-        rows = 0
-        if cos_sin is not None:
-            rows = cos_sin.shape[0]
-            cos_sin = _plain_array("cos_sin", cos_sin, torch.float32, (rows, D // 2, 2), device)
-        nr = NormRope(_plain_array("q_weight", q_weight, dtype, (D,), device),
-                      _plain_array("k_weight", k_weight, dtype, (D,), device), eps, theta, cos_sin)
-        H, qp, q_str, op, o_str = 0, None, k_str, None, None
-        if q is not None:
-            H = P * q[0].shape[1]
-            q_shape = (T, q[0].shape[1], D)
-            qp, q_str = _views("q", q, P, q_shape, dtype, device)
-            if q_out is None:
-                q_out, op = _made(P, q_shape, dtype, q[0].device)
-            else:
-                op, o_str = _views("q_out", q_out, P, q_shape, dtype, device)
-        each = ctypes.c_void_p * P
-        _check(lib().tf_ulysses_kv_append(
-            c, P, T, H, _dtype_code(dtype), each(*kp), each(*vp), each(*qp) if qp is not None else None,
-            _Strides3(k_str, v_str, q_str), each(*op) if op is not None else None,
-            Strides(*o_str) if o_str is not None else None, nr, _ROPE[rope], rows, on.handle))
-    return q_out
+    return _run("kv_append", stream, (*cache, page_table, lens, starts),
+                (k, v, q, q_out, q_weight, k_weight, eps, theta, cos_sin, _ROPE[rope]))
 
 
 def kv_attend(cache, page_table, lens, starts, q, out=None, lse=None, *, max_tokens=None, max_len=None, scale=None,
@@ -689,31 +539,8 @@ def kv_attend(cache, page_table, lens, starts, q, out=None, lse=None, *, max_tok
     Returns ``(out, lse)``: P tensors ``[T, H/P, D]`` and fp32 ``[H/P, T]``, made here unless given (rows of no sequence
     are then undefined; given tensors keep them).
     """
-    L = lib()
-    with _OnStream(stream) as on:
-        device = on.device
-        c = _kv_cache(cache, page_table, lens, starts, device)
-        P, shape, dtype = len(q), q[0].shape, q[0].dtype
-        if not 1 <= P <= MAX_SHARDS or len(shape) != 3 or shape[2] != c.D:
-            raise ValueError(f"q must be a list of P in [1, {MAX_SHARDS}] views [T, heads, {c.D}]")
-        T, Hl, D = shape
-        qp, q_str = _views("q", q, P, shape, dtype, device)
-        a = KvAttention(P, T, P * Hl, _dtype_code(dtype), T if max_tokens is None else max_tokens,
-                        c.max_pages * c.page_size if max_len is None else max_len, D ** -0.5 if scale is None else scale, softcap,
-                        1 if causal else 0, _plain_array("slopes", slopes, torch.float32, (P * Hl,), device))
-        if out is None:
-            (out, op), o_str = _made(P, shape, dtype, q[0].device), None
-        else:
-            op, o_str = _views("out", out, P, shape, dtype, device)
-        if lse is None:
-            lse, lp = _made(P, (Hl, T), torch.float32, q[0].device)
-        else:
-            lp = _lse_arrays(lse, P, (Hl, T), device)
-        ws, ws_at, ws_size = _workspace(L.tf_ulysses_kv_attend_workspace, c, a, device=q[0].device)
-        each = ctypes.c_void_p * P
-        _check(L.tf_ulysses_kv_attend(c, a, each(*qp), Strides(*q_str), each(*op),
-                                      Strides(*o_str) if o_str is not None else None, each(*lp), ws_at, ws_size, on.handle))
-    return out, lse
+    return _run("kv_attend", stream, (*cache, page_table, lens, starts),
+                (q, out, lse, max_tokens, max_len, scale, softcap, slopes, causal))
 
 
 def rope_table(theta, S, D, *, stream=None, device=None):

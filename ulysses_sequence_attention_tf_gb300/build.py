@@ -1,7 +1,8 @@
 """Build ``libtf_ulysses.so`` (in-tree) with nvcc for sm_103a.
 
 The translation units (kernels, host ABI) compile in parallel into
-``_build/`` and link into ``ulysses_sequence_attention_tf_gb300/libtf_ulysses.so``.
+``_build/`` and link into ``ulysses_sequence_attention_tf_gb300/libtf_ulysses.so``;
+``_torch_calls.so`` beside it marshals the attention and cache calls.
 cudart is linked statically, so the library depends only on the driver.
 """
 from __future__ import annotations
@@ -29,6 +30,30 @@ DEPS = SOURCES + ["relayout.h", "noalloc.h", "device_common.cuh", "block_kernel.
                   "tcgen05.cuh", "kv_cache.h", "kv_common.cuh"]
 
 
+# The Python module that marshals the attention and cache calls: C++ against the installed torch.
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
+CALLS = os.path.join(PKG, "_torch_calls.so")
+
+
+def _calls_command(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], INCLUDE]
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in include], CALLS_SOURCE, "-o", out,
+            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+
+
+def _calls_stale() -> bool:
+    if not os.path.exists(CALLS):
+        return True
+    t = os.path.getmtime(CALLS)
+    return any(os.path.getmtime(d) > t for d in (CALLS_SOURCE, os.path.join(INCLUDE, "tf_ulysses.h")))
+
+
 def nvcc() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -44,13 +69,30 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _finish_calls(calls, tmp: str, verbose: bool) -> None:
+    cmd, p = calls
+    text, _ = p.communicate()
+    if verbose or p.returncode != 0:
+        sys.stderr.write(text)
+    if p.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd))
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False, defines=(), out: str | None = None) -> str:
     """Compile the library if it is missing or older than its sources.
 
     ``defines``: extra ``-D`` macros (tuning constants); ``out``: library path
     (default: the in-tree ``libtf_ulysses.so``)."""
     lib = out or LIB
+    calls = None  # the in-tree module goes with the in-tree library
+    if out is None and (force or _calls_stale()):
+        tmp_calls = CALLS + f".tmp{os.getpid()}"
+        cmd = _calls_command(tmp_calls)
+        calls = (cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
     if not force and not defines and out is None and not _stale():
+        if calls is not None:
+            _finish_calls(calls, tmp_calls, verbose)
         return LIB
     build_dir = BUILD_DIR if out is None else os.path.join(os.path.dirname(lib), "_obj")
     os.makedirs(build_dir, exist_ok=True)
@@ -73,6 +115,8 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: str | Non
             failed.append(" ".join(cmd))
     if failed:
         raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+    if calls is not None:
+        _finish_calls(calls, tmp_calls, verbose)
     tmp = lib + f".tmp{os.getpid()}"
     subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, lib)
