@@ -4,8 +4,8 @@
 //
 // A CTA of 512 threads takes two tiles of 128 rows -- row r of a key head is token
 // r / shared, query head r % shared of its group -- and a chunk of the keys:
-//  * warps 8-11: turn codes into operand tiles.  A thread reads eight pieces of 16 codes of
-//    the next tile while it converts the present one, exactly, to fp16 in the swizzled
+//  * warps 8-11: turn codes into operand tiles.  A thread copies its pieces of 16 codes of the
+//    next tile ahead into shared memory and converts the present ones, exactly, to fp16 in the swizzled
 //    layout; K relative to the tile's largest page scale, V relative to the largest
 //    one so far.  Before that they lay down Q, each row times a power of two
 //    (f16_factor).  Keys behind the sequence become zeros, whatever the page holds.
@@ -36,7 +36,9 @@ struct TileInfo {
 template <int kD>
 struct TilesShape {
     static constexpr uint32_t kTile = kHalfTile * (kD / 64);
-    static constexpr size_t kSmem = (2 + kStages) * size_t(kTile) + 2 * kAttnRows * sizeof(float) + kInfos * sizeof(TileInfo) + 512 + 1024;
+    static constexpr int kSlots = kD == 64 ? 4 : 2;              // code tiles under way
+    static constexpr uint32_t kSlot = kAttnRows * kD;
+    static constexpr size_t kSmem = (2 + kStages) * size_t(kTile) + kSlots * size_t(kSlot) + 2 * kAttnRows * sizeof(float) + kInfos * sizeof(TileInfo) + 512 + 1024;
 };
 
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -64,9 +66,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
     constexpr int kLoads = kAttnRows * kPieces / 128;  // pieces of a thread in a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* factors = reinterpret_cast<float*>(smem + (2 + kStages) * size_t(kTile));  // scale / Q's factor, by row
+    constexpr int kSlots = TilesShape<kD>::kSlots;
+    uint8_t* slots = smem + (2 + kStages) * size_t(kTile);
+    float* factors = reinterpret_cast<float*>(slots + kSlots * size_t(TilesShape<kD>::kSlot));  // scale / Q's factor, by row
     TileInfo* infos = reinterpret_cast<TileInfo*>(factors + 2 * kAttnRows);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kStages) * size_t(kTile) + 2 * kAttnRows * sizeof(float) + 64);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(infos) + 64);
     static_assert(kInfos * sizeof(TileInfo) <= 64, "the barriers follow the tile infos");
     const uint32_t q_smem = smem_u32(smem), ring = q_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
@@ -124,7 +128,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
     const uint32_t tmem = *tmem_slot;
     const uint32_t o_tmem = tmem + 2 * kAttnRows;
 
-    // 512 * 128 registers at launch = 256 * 176 + 128 * 104 + 128 * 56
+    // 512 * 128 registers at launch = 256 * 184 + 128 * 88 + 128 * 56
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 12 && n_tiles > 0 && elect_one()) {
@@ -170,9 +174,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             drain_phase(o_full, 0);  // every MMA of this CTA has completed
         }
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---------------- converters
-        const uint32_t i = threadIdx.x - 256;
+        const uint32_t i = threadIdx.x - 256, slot_smem = smem_u32(slots) + i * 16;
         if (n_tiles > 0) {
             for (int t = 0; t < tiles; ++t) {  // Q: a row a thread
                 const uint32_t r = row0 + t * kAttnRows + i;
@@ -240,24 +244,25 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
         constexpr uint32_t kRowsPer = 128 / kPieces;  // keys that a pass of the 128 threads covers
         const uint32_t piece = i % kPieces, key_in = i / kPieces;
         const uint32_t own = key_in % 16 * kD + piece * 16;  // in a group
-        auto load = [&](uint4 (&d)[kLoads], int tile, int kv, int64_t at) {
-            const int left = seq.len - key0 - tile * int(kAttnRows);
-#pragma unroll
-            for (int x = 0; x < kLoads; ++x) {
-                const uint32_t row = x * kRowsPer + key_in;
-                const int64_t from = __shfl_sync(0xffffffffu, at, row / 16);
-                d[x] = make_uint4(0, 0, 0, 0);
-                if (from >= 0 && int(row) < left) d[x] = ld_codes16(c.codes[kv] + from + own);
-            }
+        // ask for piece x of tile `tile`; only this thread reads what lands in its 16 bytes
+        auto ask = [&](int x, int tile, int kv, int64_t at) {
+            const uint32_t row = x * kRowsPer + key_in;
+            const int64_t from = __shfl_sync(0xffffffffu, at, row / 16);
+            const bool there = from >= 0 && int(row) < seq.len - key0 - tile * int(kAttnRows);
+            copy_async16(slot_smem + (2 * tile + kv) % kSlots * TilesShape<kD>::kSlot + x * 2048, c.codes[kv] + (there ? from + own : 0), there);
         };
-        auto convert = [&](const uint4 (&d)[kLoads], uint32_t k, float scale, float ref) {
+        // step k (tile k / 2; K, then V) into the ring, and the codes of step k + kSlots asked for
+        auto convert = [&](uint32_t k, float scale, float ref, int64_t ahead) {
             uint8_t* tile = smem + (2 + k % kStages) * size_t(kTile);
             const __half2 own_factor = __float2half2_rn(scale / ref);
             const uint32_t factor = *reinterpret_cast<const uint32_t*>(&own_factor);
+            copy_async_wait<kSlots - 1>();
+            const uint8_t* codes = slots + k % kSlots * TilesShape<kD>::kSlot + i * 16;
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
                 const uint32_t row = x * kRowsPer + key_in, f = __shfl_sync(0xffffffffu, factor, row / 16);
-                const uint32_t* w = &d[x].x;
+                const uint4 d = *reinterpret_cast<const uint4*>(codes + x * 2048);
+                const uint32_t* w = &d.x;
                 uint32_t h[8];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
@@ -269,7 +274,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
                     }
                 }
                 store_piece<kD>(tile, row, piece, h);
+                ask(x, k / 2 + kSlots / 2, k % 2, ahead);  // the piece has been read
             }
+            copy_async_commit();
             fence_async_shared();
         };
         auto largest = [&](float v) {
@@ -277,37 +284,49 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
             return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         };
-        Group now = group_of(0);
-        uint4 raw[2][kLoads];
-        load(raw[0], 0, 0, now.at);
+        constexpr int kAhead = kSlots / 2;  // tiles
+        Group groups[kAhead + 1];  // of tiles j .. j + kAhead
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) {
+            groups[t] = group_of(t);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+                for (int x = 0; x < kLoads; ++x) ask(x, t, kv, groups[t].at);
+                copy_async_commit();
+            }
+        }
+        groups[kAhead] = group_of(kAhead);
         float v_ref = 0x1p-126f;
-        bool ok = true;
-        for (int j = 0; ok && j < n_tiles; ++j) {
-            const Group next = group_of(j + 1);
+        for (int j = 0; j < n_tiles; ++j) {
+            const Group now = groups[0];
+            const int64_t ahead = groups[kAhead].at;
+#pragma unroll
+            for (int t = 0; t < kAhead; ++t) groups[t] = groups[t + 1];
+            groups[kAhead] = group_of(j + 1 + kAhead);
             const float k_ref = fmaxf(largest(now.scale[0]), 0x1p-126f);
             v_ref = fmaxf(v_ref, largest(now.scale[1]));
             const int key = key0 + j * int(kAttnRows) + int(lane % 8) * 16;
             const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && now.at < 0 && key < seq.len);
-            load(raw[1], j, 1, now.at);
-            const uint32_t k = 2 * j, s = k % kStages;  // K of tile j, V in the next stage
-            ok = __all_sync(0xffffffffu, k < uint32_t(kStages) || wait_for(empty0 + 8 * s, (k / kStages - 1) & 1u, abort_flag));
-            if (!ok) break;
-            convert(raw[0], k, now.scale[0], k_ref);
+            const uint32_t k = 2 * j;
+            auto stage_free = [&](uint32_t k) {
+                return __all_sync(0xffffffffu, k < uint32_t(kStages) || wait_for(empty0 + 8 * (k % kStages), (k / kStages - 1) & 1u, abort_flag));
+            };
+            if (!stage_free(k)) break;
+            convert(k, now.scale[0], k_ref, ahead);
             if (i == 0) {
                 infos[j % kInfos] = TileInfo{k_ref, v_ref, bad};
                 mbar_arrive(info_full0 + 8 * (j % kInfos));
             }
-            warp_arrive(full0 + 8 * s);
-            load(raw[0], j + 1, 0, next.at);
-            ok = __all_sync(0xffffffffu, k < uint32_t(kStages) || wait_for(empty0 + 8 * (s + 1), (k / kStages - 1) & 1u, abort_flag));
-            if (!ok) break;
-            convert(raw[1], k + 1, now.scale[1], v_ref);
-            warp_arrive(full0 + 8 * (s + 1));
-            now = next;
+            warp_arrive(full0 + 8 * (k % kStages));
+            if (!stage_free(k + 1)) break;
+            convert(k + 1, now.scale[1], v_ref, ahead);
+            warp_arrive(full0 + 8 * ((k + 1) % kStages));
         }
+        copy_async_wait<0>();
     } else {
         // ---------------- softmax: a thread per row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const uint32_t t = warp / 4, quarter = warp % 4, at = t * kAttnRows + quarter * 32 + lane;
         const uint32_t r = row0 + at;
         const bool valid = r < rows;

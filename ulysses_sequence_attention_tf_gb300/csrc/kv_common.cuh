@@ -39,12 +39,14 @@ __device__ __forceinline__ float f16_factor(float most) {
     return most == 0.f || !(most <= kFltMax) ? 1.0f : __uint_as_float(uint32_t(min(e, 100) + 127) << 23);
 }
 
-__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// 16 bytes into shared memory as they come; zeros if not `there` (then nothing is read).
+__device__ __forceinline__ void copy_async16(uint32_t smem, const void* global, bool there = true) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(global), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 }  // namespace dev
 }  // namespace tfu
