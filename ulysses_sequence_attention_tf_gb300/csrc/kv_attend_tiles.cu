@@ -4,11 +4,12 @@
 //
 // A CTA of 512 threads takes two tiles of 128 rows -- row r of a key head is token
 // r / shared, query head r % shared of its group -- and a chunk of the keys:
-//  * warps 8-11: turn codes into operand tiles.  A thread copies its pieces of 16 codes of the
-//    next tile ahead into shared memory and converts the present ones, exactly, to fp16 in the swizzled
-//    layout; K relative to the tile's largest page scale, V relative to the largest
-//    one so far.  Before that they lay down Q, each row times a power of two
-//    (f16_factor).  Keys behind the sequence become zeros, whatever the page holds.
+//  * warp 13: looks up the pages of the tiles to come and copies their codes into a ring in
+//    shared memory (bulk copies of a group of 16 keys, which lies in one page).
+//  * warps 8-11: turn codes into operand tiles, exactly, in fp16 and the swizzled layout;
+//    K relative to the tile's largest page scale, V relative to the largest one so far.
+//    Before that they lay down Q, each row times a power of two (f16_factor).  Keys
+//    behind the sequence become zeros, whatever the page holds.
 //  * warp 12, one lane: the products, as in the forward kernel.
 //  * warps 0-3 and 4-7: softmax, a thread a row.
 // TMEM: S0 S1 (128 columns each, P on top of S), O0 O1 (D columns each).
@@ -25,24 +26,37 @@ using namespace dev;
 
 constexpr int kThreadsT = 512;
 constexpr uint32_t kHalfTile = kAttnRows * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
-constexpr int kStages = 4;                               // K V K V
-constexpr int kInfos = 4;  // the converters are at most two K tiles ahead of the slowest reader
+constexpr int kStages = 3;                               // operand tiles: K V K, V K V, ...
+constexpr int kSlots = 4;                                // tiles of codes: K V K V
+// Warp 13 is at most kSlots / 2 tiles ahead of the converters, and those at most
+// kStages / 2 ahead of the slowest softmax warp.
+constexpr int kInfos = 8;
 
 struct TileInfo {
-    float k_ref, v_ref;  // scales that the tile's K and V are relative to
-    uint32_t bad;        // groups of 16 keys whose page is out of range
+    uint32_t factor[2][8];  // K's and V's groups of 16 keys: the page's scale over the tile's, a pair of fp16
+    float k_ref, v_ref;     // scales that the tile's K and V are relative to
+    uint32_t bad;           // groups of 16 keys whose page is out of range
+    int left;               // keys of the sequence in the tile
 };
 
 template <int kD>
 struct TilesShape {
     static constexpr uint32_t kTile = kHalfTile * (kD / 64);
-    static constexpr int kSlots = kD == 64 ? 4 : 2;              // code tiles under way
     static constexpr uint32_t kSlot = kAttnRows * kD;
-    static constexpr size_t kSmem = (2 + kStages) * size_t(kTile) + kSlots * size_t(kSlot) + 2 * kAttnRows * sizeof(float) + kInfos * sizeof(TileInfo) + 512 + 1024;
+    static constexpr size_t kSmem = (2 + kStages) * size_t(kTile) + kSlots * size_t(kSlot) + 2 * kAttnRows * sizeof(float) +
+                                    kInfos * sizeof(TileInfo) + 256 + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     return bounded_wait(bar, parity, abort_flag, &g_kv_tiles_waits);
+}
+
+// A bulk copy from device memory, counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_copy(uint32_t smem, const void* global, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem), "l"(global), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
 }
 
 // 16 values of row `row` from element 16 * piece on, as two swizzled 16-byte chunks.  The
@@ -66,16 +80,17 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
     constexpr int kLoads = kAttnRows * kPieces / 128;  // pieces of a thread in a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    constexpr int kSlots = TilesShape<kD>::kSlots;
+    constexpr uint32_t kSlot = TilesShape<kD>::kSlot;
     uint8_t* slots = smem + (2 + kStages) * size_t(kTile);
-    float* factors = reinterpret_cast<float*>(slots + kSlots * size_t(TilesShape<kD>::kSlot));  // scale / Q's factor, by row
+    float* factors = reinterpret_cast<float*>(slots + kSlots * size_t(kSlot));  // scale / Q's factor, by row
     TileInfo* infos = reinterpret_cast<TileInfo*>(factors + 2 * kAttnRows);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(infos) + 64);
-    static_assert(kInfos * sizeof(TileInfo) <= 64, "the barriers follow the tile infos");
-    const uint32_t q_smem = smem_u32(smem), ring = q_smem + 2 * kTile;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(infos + kInfos);
+    const uint32_t q_smem = smem_u32(smem), ring = q_smem + 2 * kTile, slot_smem = smem_u32(slots);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
     const uint32_t s_full0 = q_full + 8, p_half0 = s_full0 + 16, o_full = p_half0 + 32, info_full0 = o_full + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 8 + kInfos);
+    const uint32_t code_full0 = info_full0 + 8 * kInfos, code_empty0 = code_full0 + 8 * kSlots;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 8 + kInfos + 2 * kSlots);
+    static_assert((2 * kStages + 8 + kInfos + 2 * kSlots) * 8 + 8 <= 256, "the barriers' room");
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const KvCache& c = p.c;
@@ -114,6 +129,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
         }
         mbar_init(o_full, 1);
         for (int t = 0; t < kInfos; ++t) mbar_init(info_full0 + 8 * t, 1);
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(code_full0 + 8 * s, 1);
+            mbar_init(code_empty0 + 8 * s, 4);  // a warp each
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -172,11 +191,80 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             }
             tc_commit(o_full);
             drain_phase(o_full, 0);  // every MMA of this CTA has completed
+        } else if (warp == 13) {
+            // ---------------- codes.  Lane l of sixteen has K (l < 8) or V of the group of keys
+            // [key0 + 128 * tile + 16 (l % 8), + 16)
+            const uint32_t kv = lane / 8 % 2, group = lane % 8;
+            struct Group {
+                int64_t at;  // where its codes start; -1: behind the sequence, or its page is out of range
+                float scale;
+            };
+            auto group_of = [&](int tile) {
+                Group d{-1, 0.f};
+                const int key = key0 + tile * int(kAttnRows) + int(group) * 16;
+                if (tile < n_tiles && key < seq.len) {
+                    const int x = c.table[int64_t(n) * c.table_stride + uint32_t(key) / c.page];
+                    if (x >= 0 && uint32_t(x) < c.pages) {
+                        const int64_t slot = int64_t(x) * c.Hkv + kh;
+                        d.at = (slot * c.page + uint32_t(key) % c.page) * kD;
+                        d.scale = c.scales[kv][slot];
+                    } else if (lane < 8) {
+                        atomicOr(&g_kv_tiles_status, 1u);
+                    }
+                }
+                return d;
+            };
+            Group now = group_of(0);
+            float v_ref = 0x1p-126f;
+            uint32_t asked = 0;
+            bool ok = true;
+            for (int j = 0; ok && j < n_tiles; ++j) {
+                const Group next = group_of(j + 1);
+                float most = now.scale;
+#pragma unroll
+                for (int w = 1; w < 8; w <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
+                const float k_ref = fmaxf(__shfl_sync(0xffffffffu, most, 0), 0x1p-126f);
+                v_ref = fmaxf(v_ref, __shfl_sync(0xffffffffu, most, 8));
+                const int left = min(seq.len - key0 - j * int(kAttnRows), int(kAttnRows));
+                const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && now.at < 0 && int(group) * 16 < left);
+                const uint32_t bytes = now.at < 0 ? 0 : min(left - int(group) * 16, 16) * kD;
+#pragma unroll
+                for (uint32_t side = 0; side < 2; ++side) {
+                    const uint32_t k = 2 * j + side, s = k % kSlots;
+                    ok = k < uint32_t(kSlots) || wait_for(code_empty0 + 8 * s, (k / kSlots - 1) & 1u, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const bool own = lane < 16 && kv == side;
+                    if (side == 0) {
+                        TileInfo& info = infos[j % kInfos];
+                        if (lane < 16) {
+                            const __half2 f = __float2half2_rn(now.scale / (kv == 0 ? k_ref : v_ref));
+                            info.factor[kv][group] = *reinterpret_cast<const uint32_t*>(&f);
+                        }
+                        if (lane == 0) {
+                            info.k_ref = k_ref;
+                            info.v_ref = v_ref;
+                            info.bad = bad;
+                            info.left = left;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(info_full0 + 8 * (j % kInfos));
+                    }
+                    const uint32_t total = __reduce_add_sync(0xffffffffu, own ? bytes : 0);
+                    if (lane == 0) mbar_expect_tx(code_full0 + 8 * s, total);
+                    __syncwarp();
+                    if (own && bytes) bulk_copy(slot_smem + s * kSlot + group * 16 * kD, c.codes[kv] + now.at, bytes, code_full0 + 8 * s);
+                    asked = k + 1;
+                }
+                now = next;
+            }
+            __syncwarp();
+            for (uint32_t k = asked > kSlots ? asked - kSlots : 0; k < asked; ++k)
+                drain_phase(code_full0 + 8 * (k % kSlots), (k / kSlots) & 1u);
         }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---------------- converters
-        const uint32_t i = threadIdx.x - 256, slot_smem = smem_u32(slots) + i * 16;
+        const uint32_t i = threadIdx.x - 256;
         if (n_tiles > 0) {
             for (int t = 0; t < tiles; ++t) {  // Q: a row a thread
                 const uint32_t r = row0 + t * kAttnRows + i;
@@ -218,50 +306,24 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
             fence_async_shared();
             warp_arrive(q_full);
         }
-        // lane l of eight: the group of keys [key0 + 128 * tile + 16 l, + 16), which lies in one page:
-        // whether there is one, where its K codes start (V's at the same offset), its scales
-        struct Group {
-            int64_t at;  // -1: behind the sequence, or its page is out of range
-            float scale[2];
-        };
-        auto group_of = [&](int tile) {
-            Group d{-1, {0.f, 0.f}};
-            const int key = key0 + tile * int(kAttnRows) + int(lane % 8) * 16;
-            if (tile < n_tiles && key < seq.len) {
-                const int x = c.table[int64_t(n) * c.table_stride + uint32_t(key) / c.page];
-                if (x >= 0 && uint32_t(x) < c.pages) {
-                    const int64_t slot = int64_t(x) * c.Hkv + kh;
-                    d.at = (slot * c.page + uint32_t(key) % c.page) * kD;
-                    d.scale[0] = c.scales[0][slot];
-                    d.scale[1] = c.scales[1][slot];
-                } else {
-                    atomicOr(&g_kv_tiles_status, 1u);
-                }
-            }
-            return d;
-        };
-        // piece x of a thread: 16 codes of a key
+        // a thread's piece x: 16 codes of key x * kRowsPer + i / kPieces of the tile
         constexpr uint32_t kRowsPer = 128 / kPieces;  // keys that a pass of the 128 threads covers
         const uint32_t piece = i % kPieces, key_in = i / kPieces;
-        const uint32_t own = key_in % 16 * kD + piece * 16;  // in a group
-        // ask for piece x of tile `tile`; only this thread reads what lands in its 16 bytes
-        auto ask = [&](int x, int tile, int kv, int64_t at) {
-            const uint32_t row = x * kRowsPer + key_in;
-            const int64_t from = __shfl_sync(0xffffffffu, at, row / 16);
-            const bool there = from >= 0 && int(row) < seq.len - key0 - tile * int(kAttnRows);
-            copy_async16(slot_smem + (2 * tile + kv) % kSlots * TilesShape<kD>::kSlot + x * 2048, c.codes[kv] + (there ? from + own : 0), there);
-        };
-        // step k (tile k / 2; K, then V) into the ring, and the codes of step k + kSlots asked for
-        auto convert = [&](uint32_t k, float scale, float ref, int64_t ahead) {
+        for (uint32_t k = 0; k < 2 * uint32_t(n_tiles); ++k) {  // K of tile k / 2, then V
+            bool ok = wait_for(code_full0 + 8 * (k % kSlots), (k / kSlots) & 1u, abort_flag);
+            ok = ok && (k < uint32_t(kStages) || wait_for(empty0 + 8 * (k % kStages), (k / kStages - 1) & 1u, abort_flag));
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const TileInfo& info = infos[k / 2 % kInfos];
+            const int left = info.left;
+            const uint32_t bad = info.bad;
+            const bool whole = left == int(kAttnRows) && bad == 0;
             uint8_t* tile = smem + (2 + k % kStages) * size_t(kTile);
-            const __half2 own_factor = __float2half2_rn(scale / ref);
-            const uint32_t factor = *reinterpret_cast<const uint32_t*>(&own_factor);
-            copy_async_wait<kSlots - 1>();
-            const uint8_t* codes = slots + k % kSlots * TilesShape<kD>::kSlot + i * 16;
+            const uint8_t* codes = slots + k % kSlots * kSlot + i * 16;
 #pragma unroll
             for (int x = 0; x < kLoads; ++x) {
-                const uint32_t row = x * kRowsPer + key_in, f = __shfl_sync(0xffffffffu, factor, row / 16);
-                const uint4 d = *reinterpret_cast<const uint4*>(codes + x * 2048);
+                const uint32_t row = x * kRowsPer + key_in, f = info.factor[k % 2][row / 16];
+                uint4 d = *reinterpret_cast<const uint4*>(codes + x * 2048);
+                if (!whole && (int(row) >= left || (bad >> (row / 16)) & 1u)) d = make_uint4(0, 0, 0, 0);
                 const uint32_t* w = &d.x;
                 uint32_t h[8];
 #pragma unroll
@@ -274,56 +336,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) kv_tiles_kernel(const __grid_con
                     }
                 }
                 store_piece<kD>(tile, row, piece, h);
-                ask(x, k / 2 + kSlots / 2, k % 2, ahead);  // the piece has been read
             }
-            copy_async_commit();
             fence_async_shared();
-        };
-        auto largest = [&](float v) {
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        };
-        constexpr int kAhead = kSlots / 2;  // tiles
-        Group groups[kAhead + 1];  // of tiles j .. j + kAhead
-#pragma unroll
-        for (int t = 0; t < kAhead; ++t) {
-            groups[t] = group_of(t);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-                for (int x = 0; x < kLoads; ++x) ask(x, t, kv, groups[t].at);
-                copy_async_commit();
-            }
-        }
-        groups[kAhead] = group_of(kAhead);
-        float v_ref = 0x1p-126f;
-        for (int j = 0; j < n_tiles; ++j) {
-            const Group now = groups[0];
-            const int64_t ahead = groups[kAhead].at;
-#pragma unroll
-            for (int t = 0; t < kAhead; ++t) groups[t] = groups[t + 1];
-            groups[kAhead] = group_of(j + 1 + kAhead);
-            const float k_ref = fmaxf(largest(now.scale[0]), 0x1p-126f);
-            v_ref = fmaxf(v_ref, largest(now.scale[1]));
-            const int key = key0 + j * int(kAttnRows) + int(lane % 8) * 16;
-            const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && now.at < 0 && key < seq.len);
-            const uint32_t k = 2 * j;
-            auto stage_free = [&](uint32_t k) {
-                return __all_sync(0xffffffffu, k < uint32_t(kStages) || wait_for(empty0 + 8 * (k % kStages), (k / kStages - 1) & 1u, abort_flag));
-            };
-            if (!stage_free(k)) break;
-            convert(k, now.scale[0], k_ref, ahead);
-            if (i == 0) {
-                infos[j % kInfos] = TileInfo{k_ref, v_ref, bad};
-                mbar_arrive(info_full0 + 8 * (j % kInfos));
-            }
             warp_arrive(full0 + 8 * (k % kStages));
-            if (!stage_free(k + 1)) break;
-            convert(k + 1, now.scale[1], v_ref, ahead);
-            warp_arrive(full0 + 8 * ((k + 1) % kStages));
+            warp_arrive(code_empty0 + 8 * (k % kSlots));
         }
-        copy_async_wait<0>();
     } else {
         // ---------------- softmax: a thread per row
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
