@@ -369,6 +369,9 @@ TF_API tf_status tf_ulysses_gather_out(const char *tag, const void *const *attn,
  * over the visible keys; a row without one gets out = 0 and lse = -infinity.
  * Scores, softmax and sums are fp32; the weights are rounded to the I/O type
  * for the product with V, and the result once more.
+ * What a token holds whose document number is negative does not matter.  Other tokens should
+ * be finite where they are masked too: a masked weight is 0, and 0 times infinity or NaN
+ * in V (and in the gradients Q, K and dout) is NaN.
  */
 typedef struct tf_attention {
     int P, B;              /* head groups (1..8), batch rows */
@@ -487,7 +490,7 @@ typedef enum tf_rope {
  * the page already holds tokens of the sequence; when the scale grows, the older codes
  * are rounded again to the new one.  Infinities are stored as the largest code and
  * NaN as NaN; neither moves the scale.  Two sequences may share a page only if
- * neither gets new rows in it.
+ * neither gets new rows in it, and a sequence names a page that gets new rows once.
  */
 TF_API tf_status tf_ulysses_kv_append(const tf_kv_cache *c, int P, int T, int H, tf_dtype dtype,
                                       const void *const *k, const void *const *v, const void *const *q,

@@ -214,6 +214,73 @@ def test_another_stream(tf):
         assert all(torch.equal(m, n) for s, t in zip(want, got) for m, n in zip(s, t))
 
 
+def test_two_calls_at_once(tf):
+    """Calls in flight on two streams, each joining parts from a workspace of its own."""
+    x = [make(1, 1, 1100, 3001, 2, 1, 128, BF16, seed) for seed in (51, 52)]
+    want = [both(tf, *y) for y in x]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for y, s in zip(x, streams):
+            out, lse = tf.attention(*y[:3], stream=s)
+            got.append((out, lse, *tf.attention_backward(y[3], *y[:3], out, lse, stream=s)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(m, n) for a, b in zip(want, got) for s, t in zip(a, b) for m, n in zip(s, t))
+
+
+def test_many_batch_rows_of_documents(tf):
+    """More batch rows than one dimension of a grid may count (65535)."""
+    B, S = 65600, 3
+    g = torch.Generator(device="cuda").manual_seed(53)
+    docs = torch.randint(-1, 2, (B, S), generator=g, device="cuda", dtype=torch.int32)
+    both(tf, *make(1, B, S, S, 1, 1, 64, BF16, 54), q_docs=docs, k_docs=docs)
+
+
+def test_values_of_masked_keys(tf):
+    """A key that a row does not see may hold anything in K.  In V too, if it is padding (see above) or lies in a
+    tile that the row's 256 rows skip; in a visited tile its weight is 0, and 0 times infinity is NaN."""
+    q, k, v, _ = make(1, 1, 512, 512, 1, 1, 64, BF16, 55)
+    want, lse = tf.attention(q, k, v, causal=True)
+    for bad in (math.nan, math.inf, -math.inf):
+        kb, vb = [k[0].clone()], [v[0].clone()]
+        kb[0][:, 300:], vb[0][:, 256:] = bad, bad
+        out, got = tf.attention(q, kb, vb, causal=True)
+        assert torch.equal(out[0][:, :256], want[0][:, :256]) and torch.equal(got[0][..., :300], lse[0][..., :300])
+
+
+REFUSED = {
+    "q no list": lambda a: dict(q=a["q"][0]), "no groups": lambda a: dict(q=[]), "one group more": lambda a: dict(q=a["q"] * 2),
+    "no tensor": lambda a: dict(k=[0]), "two types": lambda a: dict(v=[a["v"][0].half()]), "fp32": lambda a: {n: [a[n][0].float()] for n in "qkv"},
+    "another batch": lambda a: dict(k=[a["k"][0][:1]], v=[a["v"][0][:1]]), "K and V differ": lambda a: dict(v=[a["v"][0][:, :7]]),
+    "another D": lambda a: dict(k=[a["k"][0][..., :32]], v=[a["v"][0][..., :32]]), "three dimensions": lambda a: dict(q=[a["q"][0][0]]),
+    "D not innermost": lambda a: dict(q=[a["q"][0].transpose(2, 3).contiguous().transpose(2, 3)]), "q on the CPU": lambda a: dict(q=[a["q"][0].cpu()]),
+    "v on the CPU": lambda a: dict(v=[a["v"][0].cpu()]), "broadcast k": lambda a: dict(k=[a["k"][0][:, :1].expand(-1, 8, -1, -1)]),
+    "short slopes": lambda a: dict(slopes=torch.zeros(1, device="cuda")), "fp16 slopes": lambda a: dict(slopes=torch.zeros(2, dtype=FP16, device="cuda")),
+    "64-bit documents": lambda a: dict.fromkeys(("q_docs", "k_docs"), torch.zeros((2, 8), dtype=torch.int64, device="cuda")),
+    "documents of one side": lambda a: dict(q_docs=torch.zeros((2, 8), dtype=torch.int32, device="cuda")),
+    "prefix on the CPU": lambda a: dict(causal=True, prefix=torch.zeros(2, dtype=torch.int32)),
+    "prefix without causal": lambda a: dict(prefix=torch.zeros(2, dtype=torch.int32, device="cuda")),
+    "short out": lambda a: dict(out=[a["q"][0][:, :7]]), "two outs": lambda a: dict(out=a["q"] * 2),
+    "fp16 lse": lambda a: dict(lse=[torch.zeros((2, 2, 8), dtype=FP16, device="cuda")]),
+    "strided lse": lambda a: dict(lse=[torch.zeros((2, 2, 16), device="cuda")[..., ::2]]),
+    "scale no number": lambda a: dict(scale="x"), "scale NaN": lambda a: dict(scale=math.nan), "negative cap": lambda a: dict(softcap=-1.0)}
+
+
+@pytest.mark.parametrize("how", REFUSED)
+def test_refused_tensors(tf, how):
+    q, k, v, dout = make(1, 2, 8, 8, 2, 2, 64, BF16, 56)
+    args = dict(q=q, k=k, v=v)
+    args.update(REFUSED[how](args))
+    n = tf.launch_count()
+    with pytest.raises((ValueError, TypeError, tf.TfUlyssesError)):
+        tf.attention(**args)
+    out, lse = args.pop("out", q), args.pop("lse", [torch.zeros((2, 2, 8), device="cuda")])
+    with pytest.raises((ValueError, TypeError, tf.TfUlyssesError)):
+        tf.attention_backward(dout, args.pop("q"), args.pop("k"), args.pop("v"), out, lse, **args)
+    assert tf.launch_count() == n
+
+
 def test_captured_and_replayed_with_new_inputs(tf):
     x = make(2, 1, 300, 300, 2, 2, 64, BF16, 43)
     docs = torch.tensor([DOCS["packed"](300)], dtype=torch.int32, device="cuda")

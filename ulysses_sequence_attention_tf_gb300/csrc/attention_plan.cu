@@ -44,11 +44,11 @@ __device__ __forceinline__ DocRange warp_range(const int32_t* docs, int first, i
 // rows), the column tiles queries.
 template <bool kRowsAreKeys>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ AttentionParams p, uint32_t* plan,
-                                                             uint32_t rows_per_tile, uint32_t words) {
+                                                             uint32_t rows_per_tile, uint32_t row_tiles, uint32_t words) {
     __shared__ DocRange row;
     __shared__ uint32_t bits[2];
     grid_dependency_wait();
-    const uint32_t rt = blockIdx.x, b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rt = blockIdx.x % row_tiles, b = blockIdx.x / row_tiles, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rows = int(kRowsAreKeys ? p.Sk : p.Sq), cols = int(kRowsAreKeys ? p.Sq : p.Sk);
     const int32_t* row_docs = (kRowsAreKeys ? p.k_docs : p.q_docs) + int64_t(b) * rows;
     const int32_t* col_docs = (kRowsAreKeys ? p.q_docs : p.k_docs) + int64_t(b) * cols;
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     __syncthreads();
     const DocRange rr = row;
-    uint32_t* out = plan + (size_t(b) * gridDim.x + rt) * 2 * words;
+    uint32_t* out = plan + size_t(blockIdx.x) * 2 * words;
     constexpr int kWarps = kPlanThreads / 32, kAhead = 4;  // a warp takes kAhead neighbours at a time
     static_assert(kWarps * kAhead == 32, "the CTA covers a word at a time");
     for (uint32_t w = 0; w < words; ++w) {
@@ -122,7 +122,7 @@ cudaError_t launch_plan(const AttentionParams& p, uint32_t* plan, bool rows_are_
                         cudaStream_t stream) {
     const TilePlan t = tile_plan(rows_are_keys ? p.Sk : p.Sq, rows_per_tile, rows_are_keys ? p.Sq : p.Sk);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(t.row_tiles, p.B);
+    cfg.gridDim = dim3(t.row_tiles * p.B);  // below 2^31 units
     cfg.blockDim = dim3(kPlanThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -130,8 +130,8 @@ cudaError_t launch_plan(const AttentionParams& p, uint32_t* plan, bool rows_are_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return rows_are_keys ? cudaLaunchKernelEx(&cfg, plan_kernel<true>, p, plan, rows_per_tile, t.words)
-                         : cudaLaunchKernelEx(&cfg, plan_kernel<false>, p, plan, rows_per_tile, t.words);
+    return rows_are_keys ? cudaLaunchKernelEx(&cfg, plan_kernel<true>, p, plan, rows_per_tile, t.row_tiles, t.words)
+                         : cudaLaunchKernelEx(&cfg, plan_kernel<false>, p, plan, rows_per_tile, t.row_tiles, t.words);
 }
 
 }  // namespace tfu
