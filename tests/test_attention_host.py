@@ -79,3 +79,31 @@ def test_gradient_needs_its_statistics_and_workspace(tf):
     assert backward(tf, a, FAKE, n.value, lse=None) == 1
     assert backward(tf, a, FAKE, n.value, lse=0) == 1
     assert backward(tf, a, FAKE, n.value, dk=0) == 1
+
+
+def test_tensors_off_the_device_refused(tf):
+    """The binding's checks of tensors, which need no GPU to refuse a call."""
+    torch = pytest.importorskip("torch")
+    calls = tf._torch_calls()
+    q = [torch.zeros((1, 8, 2, 64), dtype=torch.bfloat16)]
+    before, none = (q, q, q, None, 0.0, None, False, None, None, None, 0, 0), [None] * 5
+    with pytest.raises(ValueError, match="on the current device"):
+        calls.attention(*before, None, None)
+    with pytest.raises(ValueError, match="on the current device"):
+        calls.attention_backward(*before, q, q, [torch.zeros((1, 2, 8))], None, None, None)
+    for bad in (None, 1, q[0], [], q * 9, [None]):
+        with pytest.raises(ValueError):
+            calls.attention(bad, *before[1:], None, None)
+    with pytest.raises(TypeError):
+        calls.attention(*before)
+    cache = tf.kv_cache(4, 2, 16, 64, device="cpu")
+    where = [torch.zeros(s, dtype=torch.int32) for s in ((1, 2), (1,), (2,))]
+    rows = [torch.zeros((3, 2, 64), dtype=torch.bfloat16)]
+    with pytest.raises(ValueError, match="page_table"):
+        calls.kv_append(*cache, *where, 0, 0, rows, rows, None, None, None, None, 1e-6, 1e4, None, 0)
+    with pytest.raises(ValueError, match="page_table"):
+        calls.kv_attend(*cache, *where, 0, 0, rows, *none, 0.0, None, True)
+    with pytest.raises(ValueError):
+        calls.kv_attend(*[None] * 7, 0, 0, rows, *none, 0.0, None, True)
+    with pytest.raises(ValueError, match="rope"):
+        tf.kv_append(cache, *where, rows, rows, rope="other")

@@ -317,6 +317,60 @@ def test_captured_and_replayed_as_the_sequences_grow(tf):
             s.table[2, 1], s.table[0, 4] = s.table_[2][1], s.table_[0][4]
 
 
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_two_calls_at_once(tf, tokens):
+    """Calls in flight on two streams, each joining chunks from a workspace of its own."""
+    both = [Setup(tf, [9000, 5000 + i], [tokens, tokens], H=8, Hkv=2, D=128, page=64, seed=30 + i) for i in range(2)]
+    want = [s.attend(tf) for s in both]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [tf.kv_attend(*s.args, s.q, stream=st) for s, st in zip(both, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(m, n) for a, b in zip(want, got) for x, y in zip(a, b) for m, n in zip(x, y))
+
+
+REFUSED = {"cache on the CPU": dict(k=lambda t: t.cpu()), "codes of another type": dict(k=lambda t: t.view(torch.uint8)),
+           "scales of another shape": dict(v_scale=lambda t: t[:, :1]), "a cache without V": dict(v=lambda t: None),
+           "64-bit lengths": dict(lens=lambda t: t.long()), "starts too short": dict(starts=lambda t: t[:-1]),
+           "64-bit table": dict(page_table=lambda t: t.long()), "table on the CPU": dict(page_table=lambda t: t.cpu()),
+           "table by columns": dict(page_table=lambda t: t.t().contiguous().t()), "one-dimensional table": dict(page_table=lambda t: t[0])}
+
+
+@pytest.mark.parametrize("how", REFUSED)
+def test_refused_caches(tf, how):
+    s = Setup(tf, [20, 30], [1, 1])
+    names = ("k", "v", "k_scale", "v_scale", "page_table", "lens", "starts")
+    x = dict(zip(names, (*s.cache, s.table, s.lens, s.starts)))
+    for n, f in REFUSED[how].items():
+        x[n] = f(x[n])
+    args = ([x[n] for n in names[:4]], x["page_table"], x["lens"], x["starts"])
+    before = s.copy()
+    with pytest.raises(ValueError):
+        tf.kv_attend(*args, s.q)
+    with pytest.raises(ValueError):
+        tf.kv_append(*args, s.k, s.v, rope=None)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(before, s.cache))
+
+
+def test_refused_rows(tf):
+    s = Setup(tf, [20, 30], [1, 1], H=4, Hkv=2, P=2)
+    for k, v, q in ((s.k[:1], s.v, s.q), (s.k, [t.half() for t in s.v], s.q), (s.k, s.v, s.q[:1]), (s.q[0], s.v, s.q),
+                    (s.k, s.v, [t[:1] for t in s.q]), ([t[:, :0] for t in s.k], s.v, s.q), (s.k, s.v, [t.float() for t in s.q])):
+        with pytest.raises(ValueError):
+            tf.kv_append(*s.args, k, v, q)
+    for kw in (dict(q_weight=s.weights[0].float()), dict(k_weight=s.weights[1][:8]), dict(rope="other"),
+               dict(cos_sin=torch.zeros((50, 64), device="cuda")), dict(q_out=s.k), dict(eps="x")):
+        with pytest.raises((ValueError, TypeError)):
+            tf.kv_append(*s.args, s.k, s.v, s.q, **kw)
+    for kw in (dict(max_tokens=0), dict(max_tokens=3), dict(max_len=0), dict(max_len=10 ** 6), dict(softcap=-1.0), dict(eps=1)):
+        with pytest.raises((ValueError, TypeError, tf.TfUlyssesError)):
+            tf.kv_attend(*s.args, s.q, **kw)
+    for q in ([t[..., :32] for t in s.q], [t.float() for t in s.q], s.q[:1] * 9, [s.q[0], s.q[1][:1]]):
+        with pytest.raises((ValueError, tf.TfUlyssesError)):
+            tf.kv_attend(*s.args, q)
+
+
 def test_the_same_inputs_give_the_same_bits_on_any_stream(tf):
     s = Setup(tf, [3000, 500], [1, 9], H=8, Hkv=2, D=128, page=64, seed=22)
     want = s.attend(tf)

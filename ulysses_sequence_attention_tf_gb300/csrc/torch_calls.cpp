@@ -2,7 +2,7 @@
 //
 // These calls are short on the GPU, and checking and unpacking a dozen tensors in Python
 // takes longer than the kernels of a small call (35 us of host time for two head groups of
-// 256 tokens; here 11).  This module does what the ctypes binding does for the other
+// 256 tokens through ctypes, 11 through this module).  This module does what the ctypes binding does for the other
 // calls: checks shapes, types, strides and devices, allocates results and workspace from torch on
 // the current stream, and calls the C ABI, whose entry points binding.py hands over.
 #include <Python.h>
@@ -344,7 +344,8 @@ PyObject* kv_append(PyObject* const* x, Py_ssize_t n) {
     const List k("k", x[9]), v("v", x[10], k.P);
     const int P = k.P;
     if (k.t[0].dim() != 3) refuse("expected 3-d views [T, heads, D]");
-    const int64_t T = k.t[0].size(0), D = c.c.D;
+    const int T = extent(k.t[0].size(0));
+    const int64_t D = c.c.D;
     const ScalarType type = k.t[0].scalar_type();
     if (c.c.Hkv % P) refuse("the " + std::to_string(P) + " head groups of k do not divide Hkv=" + std::to_string(c.c.Hkv));
     const int64_t shape[3] = {T, c.c.Hkv / P, D};
@@ -365,7 +366,7 @@ PyObject* kv_append(PyObject* const* x, Py_ssize_t n) {
     if (x[11] == Py_None) {
         const tf_strides st[3] = {kv.st, vv.st, kv.st};
         call([&] {
-            return g_abi.kv_append(&c.c, P, extent(T), 0, code, kv.ptr, vv.ptr, nullptr, st, nullptr, nullptr, &nr, rope, rows, stream);
+            return g_abi.kv_append(&c.c, P, T, 0, code, kv.ptr, vv.ptr, nullptr, st, nullptr, nullptr, &nr, rope, rows, stream);
         });
         Py_RETURN_NONE;
     }
@@ -376,8 +377,9 @@ PyObject* kv_append(PyObject* const* x, Py_ssize_t n) {
     const List out = x[12] == Py_None ? List(P, q_shape, q.t[0].options()) : List("q_out", x[12], P);
     const Views ov("q_out", out, q_shape, type, device);
     const tf_strides st[3] = {kv.st, vv.st, qv.st};
+    const int H = extent(P * q_shape[1]);
     call([&] {
-        return g_abi.kv_append(&c.c, P, int(T), extent(P * q_shape[1]), code, kv.ptr, vv.ptr, qv.ptr, st, ov.ptr, &ov.st, &nr, rope, rows,
+        return g_abi.kv_append(&c.c, P, T, H, code, kv.ptr, vv.ptr, qv.ptr, st, ov.ptr, &ov.st, &nr, rope, rows,
                                stream);
     });
     return x[12] == Py_None ? out.wrap() : same(x[12]);
