@@ -7,13 +7,18 @@
   python -m ulysses_sequence_attention_tf_gb300.profile_cases scatter --S 4096 --H 24 --layout fused
   python -m ulysses_sequence_attention_tf_gb300.profile_cases gather --P 8 --H 48 --D 64 --B 2 --S 6008
   python -m ulysses_sequence_attention_tf_gb300.profile_cases rope_table [--S 32760] [--iters 3]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases attention --P 1 --H 5 [--S 8192] [--softcap 50]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases attention_backward --P 1 --H 5 [--S 8192] [--alibi]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases kv_append [--S 32760] [--tokens 4680] [--page 64]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases kv_attend --B 24 --P 1 --H 16 --Hkv 4 --page 128
 
 ``--layout``: v_strided (Q/K contiguous, V a view into a fused projection; the
 default), fused (Q/K/V all views of one fused projection), contiguous, pad16
 (every head row followed by 16 bytes of padding: sources only 16-byte aligned,
 which sends fused scatters to the register kernel).  ``rope_table`` builds the
 resident cos/sin table of (theta, S, D) once per iteration, each time for
-another theta.
+another theta.  ``attention`` and ``attention_backward`` see every key (``--alibi``: causal, with
+distances as a bias); the ``kv`` cases have --B sequences of --S tokens, the last --tokens of them new.
 
 Inputs are the seeded synthetic ones of ``synth``; shapes default to the
 video-DiT workload's head geometry (P=4, H=40, D=128, bf16) with a smaller
@@ -31,7 +36,7 @@ from . import binding, build, synth
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("case", choices=["projection", "scatter", "scatter_fused", "scatter_fused_qk", "gather",
-                                     "rope_table"])
+                                     "rope_table", "attention", "attention_backward", "kv_append", "kv_attend"])
     ap.add_argument("--P", type=int, default=4)
     ap.add_argument("--B", type=int, default=1)
     ap.add_argument("--D", type=int, default=128)
@@ -41,9 +46,15 @@ def main(argv=None):
     ap.add_argument("--rope", choices=["interleaved", "neox"], default="interleaved")
     ap.add_argument("--layout", choices=["v_strided", "fused", "contiguous", "pad16"], default="v_strided")
     ap.add_argument("--dtype", choices=["bf16", "fp16"], default="bf16", help="element type of the scatters")
+    ap.add_argument("--Hkv", type=int, default=None, help="key heads of the attention and cache cases (default H)")
+    ap.add_argument("--softcap", type=float, default=0.0)
+    ap.add_argument("--alibi", action="store_true")
+    ap.add_argument("--tokens", type=int, default=None, help="new tokens of a sequence (default 4680 kv_append, 1 kv_attend)")
+    ap.add_argument("--page", type=int, default=64)
     args = ap.parse_args(argv)
     P, H, D, B = args.P, args.H, args.D, args.B
-    S = args.S or (8192 if args.case == "projection" else 32760)
+    S = args.S or (8192 if args.case in ("projection", "attention", "attention_backward") else 32760)
+    Hkv = args.Hkv or H
     Sl, Hl = S // P, H // P
     build.build()
     binding.lib()
@@ -63,6 +74,40 @@ def main(argv=None):
 
         def call():
             binding.rope_table(10000.0 + next(it), S, D)
+    elif args.case in ("attention", "attention_backward"):
+        def rows(heads, seed):
+            gen = torch.Generator(device=dev).manual_seed(seed)
+            return [torch.randn((B, S, heads // P, D), generator=gen, device=dev).to(dt) for _ in range(P)]
+        q, k, v, dout = rows(H, 0), rows(Hkv, 1), rows(Hkv, 2), rows(H, 3)
+        kw = dict(softcap=args.softcap, causal=args.alibi)
+        if args.alibi:
+            kw["slopes"] = torch.exp2(-8.0 * torch.arange(1, H + 1, device=dev) / H)
+        out, lse = binding.attention(q, k, v, **kw)
+
+        def call():
+            if args.case == "attention":
+                binding.attention(q, k, v, out, lse, **kw)
+            else:
+                binding.attention_backward(dout, q, k, v, out, lse, **kw)
+    elif args.case in ("kv_append", "kv_attend"):
+        n = args.tokens or (4680 if args.case == "kv_append" else 1)
+        used = -(-S // args.page)
+        gen = torch.Generator(device=dev).manual_seed(0)
+        cache = binding.kv_cache(B * used, Hkv, args.page, D, device=dev)
+        for codes in cache[:2]:  # any finite codes
+            codes.view(torch.uint8).random_(0, 0x70, generator=gen)
+        where = (torch.randperm(B * used, generator=gen, device=dev).to(torch.int32).view(B, used),
+                 torch.full((B,), S, dtype=torch.int32, device=dev),
+                 torch.arange(0, B * n + 1, n, dtype=torch.int32, device=dev))
+        q, k, v = ([torch.randn((B * n, heads // P, D), generator=gen, device=dev).to(dt) for _ in range(P)]
+                   for heads in (H, Hkv, Hkv))
+        q_out = [torch.empty_like(t) for t in q]
+
+        def call():
+            if args.case == "kv_append":
+                binding.kv_append(cache, *where, k, v, q, q_out, q_weight=wq, k_weight=wk, rope=args.rope)
+            else:
+                binding.kv_attend(cache, *where, q, q_out, max_tokens=n, max_len=S, softcap=args.softcap, causal=n == 1)
     elif args.case in ("scatter", "scatter_fused", "scatter_fused_qk"):
         if args.layout == "pad16":
             pad = 16 // 2
