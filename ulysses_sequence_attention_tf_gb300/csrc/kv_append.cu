@@ -13,7 +13,12 @@
 // with first(n) <= u < first(n + 1), first(n) = starts[n] / page + 2n, which leaves
 // room for every page that t = starts[n + 1] - starts[n] rows can touch
 // (at most (t - 1) / page + 2), so that the grid needs no length from the device.
-// One CTA per unit and head of K, of V and of Q; D / 8 lanes hold a row.
+// A CTA takes a unit and every slices-th head of K, of V and of Q; D / 16 lanes hold a row.
+//
+// Bound by instructions, not bytes: 4680 rows of 40 heads (D = 128, bf16, norm and rotation, pages of
+// 64) take 68 us, 3.6 TB/s of 243 MB.  A lane's 16 values cost about 250 instructions a row --
+// unpack, squares, weights, rotation, maximum, two roundings.  Summing the squares plainly where the sum is
+// finite instead of exactly took 85 us to 79, room in registers for two passes 79 to 68.
 #include <cuda_fp8.h>
 
 #include "device_common.cuh"
@@ -27,7 +32,6 @@ namespace {
 
 using namespace dev;
 
-constexpr int kAppendThreads = 256;
 constexpr int kLeastExponent = -100;
 
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
@@ -77,7 +81,16 @@ __device__ __forceinline__ void norm_rotate(float (&x)[16], const uint32_t (&raw
         uint64_t x2[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x2[i] = f2_pack(x[2 * i], x[2 * i + 1]);
-        const float ms = row_mean_sq<kLanes, 8, true>(x2, nullptr);
+        // 8 squares a half, then the halves and kLanes lanes: within 6 * 2^-24 of the sum where it is finite
+        uint64_t s2 = f2_mul(x2[0], x2[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s2 = f2_fma(x2[i], x2[i], s2);
+        float ms, other;
+        f2_unpack(s2, ms, other);
+        ms = __fadd_rn(ms, other);
+#pragma unroll
+        for (int m = 1; m < kLanes; m <<= 1) ms = __fadd_rn(ms, __shfl_xor_sync(0xffffffffu, ms, m));
+        ms = ms <= kFltMax ? __fmul_rn(ms, 1.0f / kD) : row_mean_sq<kLanes, 8, true>(x2, nullptr);  // the same in a row's lanes
         const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(ms, eps)));
         const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
@@ -113,18 +126,19 @@ __device__ __forceinline__ void norm_rotate(float (&x)[16], const uint32_t (&raw
     }
 }
 
-// kIters: passes of kAppendThreads / (D / 16) rows that a page takes.
-template <Fused kF, int kD, int kIters>
-__global__ void __launch_bounds__(kAppendThreads, kIters == 4 ? 2 : 3) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
-    constexpr int kLanes = Lane<kD>::kLanes, kRows = kAppendThreads / kLanes;
-    __shared__ float most_of[2][kAppendThreads / 32];
+// kIters: passes of kThreads / (D / 16) rows that a page takes.  Registers: two passes in 128 of them
+// without spills took 68 us for 4680 rows of 40 heads in pages of 64, in 80 with spills 79.
+template <Fused kF, int kD, int kIters, int kThreads>
+__global__ void __launch_bounds__(kThreads, kIters == 1 ? 1024 / kThreads : 2) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+    constexpr int kLanes = Lane<kD>::kLanes, kRows = kThreads / kLanes;
+    __shared__ float most_of[2][kThreads / 32];
     grid_dependency_wait();
     const KvCache& c = p.c;
     const uint32_t unit = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
     const uint32_t shift = 31 - __clz(c.page);  // pages are powers of two
     // the last sequence whose first unit is not behind this one
     uint32_t before = 0;
-    for (uint32_t n0 = 0; n0 < c.N; n0 += kAppendThreads) {
+    for (uint32_t n0 = 0; n0 < c.N; n0 += kThreads) {
         const uint32_t n = n0 + threadIdx.x;
         before += __syncthreads_count(n < c.N && int64_t(c.starts[n] >> shift) + 2 * int64_t(n) <= int64_t(unit));
     }
@@ -220,23 +234,30 @@ __global__ void __launch_bounds__(kAppendThreads, kIters == 4 ? 2 : 3) kv_append
         for (int it = 0; it < kIters; ++it) {
             if (it * kRows + slot >= rows) continue;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float a = fabsf(f[it][i]);
-                most = a <= kFltMax ? fmaxf(most, a) : most;
-            }
+            for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(f[it][i]));  // passes over NaN
+        }
+        if (!(most <= kFltMax)) {  // infinities do not count
+            most = 0.f;
+#pragma unroll
+            for (int it = 0; it < kIters; ++it)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a = fabsf(f[it][i]);
+                    if (it * kRows + slot < rows && a <= kFltMax) most = fmaxf(most, a);
+                }
         }
 #pragma unroll
         for (int x = 16; x; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
         if (threadIdx.x % 32 == 0) most_of[turn][threadIdx.x / 32] = most;
         __syncthreads();  // also: every thread has read the old scale, and the other turn's maxima
 #pragma unroll
-        for (int x = 0; x < kAppendThreads / 32; ++x) most = fmaxf(most, most_of[turn][x]);
+        for (int x = 0; x < kThreads / 32; ++x) most = fmaxf(most, most_of[turn][x]);
         const float scale = fmaxf(old, scale_of(most));
         const float inv = 1.0f / scale;  // exact
         uint8_t* codes = c.codes[done.kind] + ((id * c.Hkv + done.head) << shift) * kD;
         if (off && old < scale) {  // the page's older tokens move to the larger scale
             const float ratio = old * inv;
-            for (uint32_t i = threadIdx.x; i < off * kD / 8; i += kAppendThreads) {
+            for (uint32_t i = threadIdx.x; i < off * kD / 8; i += kThreads) {
                 uint2 u = reinterpret_cast<const uint2*>(codes)[i];
                 uint32_t* parts[2] = {&u.x, &u.y};
 #pragma unroll
@@ -270,24 +291,34 @@ __global__ void __launch_bounds__(kAppendThreads, kIters == 4 ? 2 : 3) kv_append
 // one's rows on their way; a head each where there are few units.
 constexpr uint32_t kAppendCtas = 1824;
 
-template <Fused kF, int kD, int kIters>
+template <Fused kF, int kD, int kIters, int kThreads>
 cudaError_t launch(KvAppendParams p, cudaStream_t stream) {
     const uint32_t heads = 2 * p.c.Hkv + (p.q.base[0] ? p.P * p.Hl : 0), want = (kAppendCtas + p.units - 1) / p.units;
     p.slices = want < heads ? want : heads;
-    return launch_overlapped(kv_append_kernel<kF, kD, kIters>, p.units * p.slices, kAppendThreads, 0, stream, p);
+    return launch_overlapped(kv_append_kernel<kF, kD, kIters, kThreads>, p.units * p.slices, kThreads, 0, stream, p);
+}
+
+// As many threads as a page's rows have lanes, up to 256.
+template <Fused kF, int kD>
+cudaError_t launch_typed(const KvAppendParams& p, cudaStream_t stream) {
+    switch (p.c.page * Lane<kD>::kLanes) {
+        case 64: return launch<kF, kD, 1, 64>(p, stream);
+        case 128: return launch<kF, kD, 1, 128>(p, stream);
+        case 256: return launch<kF, kD, 1, 256>(p, stream);
+        case 512: return launch<kF, kD, 2, 256>(p, stream);
+        default: return launch<kF, kD, 4, 256>(p, stream);  // 1024
+    }
 }
 
 template <Fused kF>
-cudaError_t launch_typed(const KvAppendParams& p, cudaStream_t stream) {
-    if (p.c.D == 64) return p.c.page <= 64 ? launch<kF, 64, 1>(p, stream) : launch<kF, 64, 2>(p, stream);
-    return p.c.page <= 32 ? launch<kF, 128, 1>(p, stream) : p.c.page == 64 ? launch<kF, 128, 2>(p, stream)
-                                                                           : launch<kF, 128, 4>(p, stream);
+cudaError_t launch_sized(const KvAppendParams& p, cudaStream_t stream) {
+    return p.c.D == 64 ? launch_typed<kF, 64>(p, stream) : launch_typed<kF, 128>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, cudaStream_t stream) {
-    return bf16 ? launch_typed<Fused::kBF16>(p, stream) : launch_typed<Fused::kFP16>(p, stream);
+    return bf16 ? launch_sized<Fused::kBF16>(p, stream) : launch_sized<Fused::kFP16>(p, stream);
 }
 
 cudaError_t read_kv_append_status(unsigned* out, bool clear) {
