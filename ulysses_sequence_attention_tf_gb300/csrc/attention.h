@@ -67,10 +67,18 @@ inline Split plan_split(const uint64_t units, const uint32_t tiles, bool even) {
     return s;
 }
 
+// Heads whose tiles the units interleave: one, but with the causal mask as many as have their other
+// side (two tensors of `tokens` rows) in half of the L2 together.
+inline uint32_t head_block(bool causal, uint64_t heads, uint64_t tokens, uint32_t D) {
+    const uint64_t bytes = 4 * tokens * D, fit = bytes ? (uint64_t(64) << 20) / bytes : heads;
+    return !causal || fit < 1 ? 1 : uint32_t(fit < heads ? fit : heads);
+}
+
 struct ForwardParams {
     GroupMaps q, k, v;
     AttentionParams a;
-    uint32_t q_tiles;  // of kAttnPair rows
+    uint32_t q_tiles;     // of kAttnPair rows
+    uint32_t head_block;  // heads that units interleave (head_block())
     Split split;
 };
 
@@ -80,6 +88,7 @@ struct BackwardParams {
     AttentionParams a;
     uint32_t* key_plan;           // with documents: row tiles of keys (a.plan: of 128 queries)
     uint32_t q_tiles, k_tiles;    // of kAttnRows rows
+    uint32_t head_block, key_head_block;
     Split dq_split, dkv_split;
 };
 

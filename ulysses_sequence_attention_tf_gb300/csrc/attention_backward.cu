@@ -191,11 +191,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     auto value_phase = [](uint32_t n) { return (n / S::kValueStages) & 1u; };
 
     const Unit unit(bp.dq_split, blockIdx.x);
-    uint32_t u = unit.u;
-    uint32_t qt = u % bp.q_tiles;
-    u /= bp.q_tiles;
-    if (p.causal) qt = bp.q_tiles - 1 - qt;
-    const uint32_t h = u % p.Hl, b = u / p.Hl % p.B, g = u / p.Hl / p.B;
+    const TileHead th(unit.u, bp.q_tiles, p.P * p.B * p.Hl, bp.head_block);
+    const uint32_t qt = p.causal ? bp.q_tiles - 1 - th.tile : th.tile;
+    const uint32_t h = th.head % p.Hl, b = th.head / p.Hl % p.B, g = th.head / p.Hl / p.B;
     const int row0 = int(qt * kAttnRows);
 
     if (threadIdx.x == 0) {
@@ -562,10 +560,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     const Unit unit(bp.dkv_split, blockIdx.x);
-    uint32_t u = unit.u;
-    const uint32_t kt = u % bp.k_tiles;  // causal: the first keys are seen by most queries
-    u /= bp.k_tiles;
-    const uint32_t kh = u % p.Hkl, b = u / p.Hkl % p.B, g = u / p.Hkl / p.B;
+    const TileHead th(unit.u, bp.k_tiles, p.P * p.B * p.Hkl, bp.key_head_block);
+    const uint32_t kt = th.tile;  // causal: the first keys are seen by most queries
+    const uint32_t kh = th.head % p.Hkl, b = th.head / p.Hkl % p.B, g = th.head / p.Hkl / p.B;
     const int row0 = int(kt * kAttnRows);
 
     if (threadIdx.x == 0) {

@@ -83,6 +83,17 @@ struct Unit {
     __device__ int end(int n) const { return int(int64_t(n) * (part + 1) / parts); }
 };
 
+// Row tile and head of unit u: tile by tile over `block` heads, then the next heads.  causal: unequal
+// tiles, the longest first over many heads, so that the last units to start are short.
+struct TileHead {
+    uint32_t tile, head;
+    __device__ TileHead(uint32_t u, uint32_t tiles, uint32_t heads, uint32_t block) {
+        const uint32_t first = u / (tiles * block) * block, in = u % (tiles * block), here = min(block, heads - first);
+        tile = in / here;
+        head = first + in % here;
+    }
+};
+
 // The tiles of the other side that a row tile visits, in order: all of [from, n), or
 // those with a bit in `words`.
 struct TileIter {

@@ -59,11 +59,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
     const Unit unit(fp.split, blockIdx.x);
-    uint32_t u = unit.u;
-    uint32_t qt = u % fp.q_tiles;
-    u /= fp.q_tiles;
-    if (p.causal) qt = fp.q_tiles - 1 - qt;  // the rows that see most first
-    const uint32_t h = u % p.Hl, b = u / p.Hl % p.B, g = u / p.Hl / p.B;
+    const TileHead th(unit.u, fp.q_tiles, p.P * p.B * p.Hl, fp.head_block);
+    const uint32_t qt = p.causal ? fp.q_tiles - 1 - th.tile : th.tile;  // the rows that see most first
+    const uint32_t h = th.head % p.Hl, b = th.head / p.Hl % p.B, g = th.head / p.Hl / p.B;
     const int row0 = int(qt * kAttnPair);
     const int tiles = row0 + int(kAttnRows) < int(p.Sq) ? 2 : 1;
 

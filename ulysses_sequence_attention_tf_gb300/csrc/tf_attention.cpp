@@ -168,6 +168,7 @@ TF_API tf_status tf_ulysses_attention(const tf_attention* a, const void* const* 
         fp.split.stat = reinterpret_cast<float2*>(fp.split.part + rows * size_t(a->D));
     }
     fp.q_tiles = (p.Sq + tfu::kAttnPair - 1) / tfu::kAttnPair;
+    fp.head_block = tfu::head_block(a->causal, uint64_t(a->B) * a->H, p.Sk, p.D);
     int launches = 0;
     const cudaError_t e = tfu::launch_attention(fp, bf16, static_cast<cudaStream_t>(stream), &launches);
     count_launches(launches);
@@ -227,6 +228,8 @@ TF_API tf_status tf_ulysses_attention_backward(const tf_attention* a, const void
     bp.dq_split.part = bp.dkv_split.part = reinterpret_cast<float*>(at + ws.delta + ws.plan + ws.key_plan);
     bp.q_tiles = (p.Sq + tfu::kAttnRows - 1) / tfu::kAttnRows;
     bp.k_tiles = (p.Sk + tfu::kAttnRows - 1) / tfu::kAttnRows;
+    bp.head_block = tfu::head_block(a->causal, uint64_t(a->B) * a->H, p.Sk, p.D);
+    bp.key_head_block = tfu::head_block(a->causal, uint64_t(a->B) * a->Hkv, uint64_t(p.Sq) * p.shared, p.D);
     int launches = 0;
     const cudaError_t e = tfu::launch_attention_backward(bp, bf16, static_cast<cudaStream_t>(stream), &launches);
     count_launches(launches);
