@@ -94,6 +94,29 @@ struct TileHead {
     }
 };
 
+// Documents make row tiles unequal in no known order: the row tile (of all batch rows' `entries`) that
+// visits the rank-th most tiles, found by every CTA for itself from the plan.  For all threads;
+// scratch: 1 + entries words of shared memory, free for bulk copies afterwards.
+__device__ __forceinline__ uint32_t ranked_entry(const uint32_t* plan, uint32_t entries, uint32_t words, uint32_t rank, uint32_t* scratch) {
+    for (uint32_t e = threadIdx.x; e < entries; e += blockDim.x) {
+        uint32_t visits = 0;
+        for (uint32_t w = 0; w < words; ++w) visits += __popc(__ldg(plan + size_t(e) * 2 * words + w));
+        scratch[1 + e] = visits;
+    }
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < entries; e += blockDim.x) {
+        const uint32_t own = scratch[1 + e];
+        uint32_t before = 0;
+        for (uint32_t f = 0; f < entries; ++f) before += scratch[1 + f] > own || (scratch[1 + f] == own && f < e);
+        if (before == rank) scratch[0] = e;
+    }
+    __syncthreads();
+    const uint32_t found = scratch[0];
+    fence_async_shared();
+    __syncthreads();
+    return found;
+}
+
 // The tiles of the other side that a row tile visits, in order: all of [from, n), or
 // those with a bit in `words`.
 struct TileIter {

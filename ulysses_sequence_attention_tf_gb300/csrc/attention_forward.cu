@@ -60,10 +60,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
 
     const Unit unit(fp.split, blockIdx.x);
     const TileHead th(unit.u, fp.q_tiles, p.P * p.B * p.Hl, fp.head_block);
-    const uint32_t qt = p.causal ? fp.q_tiles - 1 - th.tile : th.tile;  // the rows that see most first
-    const uint32_t h = th.head % p.Hl, b = th.head / p.Hl % p.B, g = th.head / p.Hl / p.B;
-    const int row0 = int(qt * kAttnPair);
-    const int tiles = row0 + int(kAttnRows) < int(p.Sq) ? 2 : 1;
+    uint32_t qt = p.causal ? fp.q_tiles - 1 - th.tile : th.tile;  // the rows that see most first
+    uint32_t h = th.head % p.Hl, b = th.head / p.Hl % p.B, g = th.head / p.Hl / p.B;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -92,11 +90,19 @@ __global__ void __launch_bounds__(kThreadsA, 1) attention_kernel(const __grid_co
     const uint32_t tmem = *tmem_slot;
     const uint32_t o_tmem = tmem + 2 * kAttnRows;
 
+    const uint32_t words = (((p.Sk + kAttnRows - 1) / kAttnRows) + 31) / 32;
+    if (fp.ranked) {
+        const uint32_t heads = p.P * p.Hl, head = unit.u % heads;
+        const uint32_t e = ranked_entry(p.plan, p.B * fp.q_tiles, words, unit.u / heads, reinterpret_cast<uint32_t*>(smem));
+        qt = e % fp.q_tiles, b = e / fp.q_tiles, h = head % p.Hl, g = head / p.Hl;
+    }
+    const int row0 = int(qt * kAttnPair);
+    const int tiles = row0 + int(kAttnRows) < int(p.Sq) ? 2 : 1;
+
     // the keys in reach of the last row, in tiles; with documents the plan picks among them
     const int last = min(row0 + int(kAttnPair), int(p.Sq)) - 1;
     const int reach = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
     const int n_tiles = unit.end(reach);
-    const uint32_t words = (((p.Sk + kAttnRows - 1) / kAttnRows) + 31) / 32;
     const uint32_t* plan = p.plan ? p.plan + (size_t(b) * fp.q_tiles + qt) * 2 * words : nullptr;
     TileIter it(plan, n_tiles, unit.begin(reach));
 

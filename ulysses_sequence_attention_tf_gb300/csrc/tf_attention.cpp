@@ -168,6 +168,8 @@ TF_API tf_status tf_ulysses_attention(const tf_attention* a, const void* const* 
         fp.split.stat = reinterpret_cast<float2*>(fp.split.part + rows * size_t(a->D));
     }
     fp.q_tiles = (p.Sq + tfu::kAttnPair - 1) / tfu::kAttnPair;
+    fp.ranked = p.plan && tfu::rank_units(uint64_t(p.B) * fp.q_tiles, tfu::tile_plan(p.Sq, tfu::kAttnPair, p.Sk).words,
+                                          uint64_t(a->B) * a->Hkv, p.Sk, p.D);
     fp.head_block = tfu::head_block(a->causal, uint64_t(a->B) * a->H, p.Sk, p.D);
     int launches = 0;
     const cudaError_t e = tfu::launch_attention(fp, bf16, static_cast<cudaStream_t>(stream), &launches);
