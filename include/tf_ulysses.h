@@ -417,6 +417,8 @@ TF_API tf_status tf_ulysses_attention(const tf_attention *a, const void *const *
  *               gradients are summed over its query heads.
  *  grad_strides host array of 3 tf_strides: dq, dk, dv (NULL = contiguous).
  *  workspace    as above, tf_ulysses_attention_workspace(a, 1) bytes.
+ * Sums are fp32; the weights and the gradients of the scores are rounded to the I/O type for
+ * the products with dout, K and Q, and the results once more.
  * There is no gradient of the slopes.  The same inputs give the same bits.
  */
 TF_API tf_status tf_ulysses_attention_backward(const tf_attention *a, const void *const *dout, const void *const *q,

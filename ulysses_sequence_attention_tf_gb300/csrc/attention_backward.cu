@@ -17,10 +17,14 @@
 // A row tile that visits at most kExactTiles key tiles therefore sums P dP over its keys
 // first and uses that; the others take dO . O.
 //
-// Bound: the products.  8192 tokens, 5 heads, D = 128, bf16: dQ 189 us with the matrix pipe busy 61 % of the
-// cycles, dK and dV 275 us and 54 % (two kernels' 14 D flops a pair at 1300 TFLOP/s).  TMEM holds dK, dV and
+// P and dx are rounded to the I/O type as operands (one MMA takes A and B of one type; a second product
+// for the rest would cost a seventh more for each): with bf16 that adds about 0.0017 of the norm to
+// gradients whose own rounding is as large.
+//
+// Bound: the products.  8192 tokens, 5 heads, D = 128, bf16: dQ 190 us with the matrix pipe busy 61 % of the
+// cycles, dK and dV 272 us and 54 % (two kernels' 14 D flops a pair at 1300 TFLOP/s).  TMEM holds dK, dV and
 // two pairs of S and dP of 64 queries, whose products take 391 cycles where 256 would be ideal; 128 queries a step
-// do not fit.  D = 64 with bias is bound by the rows' warps: 257 and 404 us for 24 causal heads of 6001 tokens, pipe busy
+// do not fit.  D = 64 with bias is bound by the rows' warps: 234 and 369 us for 24 causal heads of 6001 tokens, pipe busy
 // 32 and 26 %, issue slots 56 and 53 %.  16 row warps took 2.72 ms where 8 took 2.88 (16380 tokens,
 // 5 heads); rings of their own for K and V in dQ 2.46; units cut along the other side 2.09.
 #include "attention_common.cuh"
