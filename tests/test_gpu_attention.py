@@ -214,6 +214,21 @@ def test_another_stream(tf):
         assert all(torch.equal(m, n) for s, t in zip(want, got) for m, n in zip(s, t))
 
 
+@pytest.mark.parametrize("Sq,Sk", [(300, 40000), (40000, 300)])
+def test_causal_heads_in_blocks(tf, Sq, Sk):
+    """Heads whose keys (queries, for dK and dV) are too many to be interleaved all at once: blocks of 3 and 2."""
+    both(tf, *make(1, 1, Sq, Sk, 5, 5, 128, BF16, 57), causal=True)
+
+
+@pytest.mark.parametrize("B,S", [(1, 600), (3, 600), (2, 5000), (70, 300)])
+def test_documents_ranked_over_batch_rows(tf, B, S):
+    """Row tiles of all batch rows in the order of their work, with ties and with rows of padding only."""
+    g = torch.Generator(device="cuda").manual_seed(58)
+    docs = torch.randint(0, 3, (B, S), generator=g, device="cuda", dtype=torch.int32).sort(1).values
+    docs[0] = -1
+    both(tf, *make(2, B, S, S, 1, 1, 64, FP16, 59), q_docs=docs, k_docs=docs, causal=B == 3)
+
+
 def test_two_calls_at_once(tf):
     """Calls in flight on two streams, each joining parts from a workspace of its own."""
     x = [make(1, 1, 1100, 3001, 2, 1, 128, BF16, seed) for seed in (51, 52)]

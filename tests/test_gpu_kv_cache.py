@@ -289,6 +289,20 @@ def test_out_of_range_lengths_starts_and_pages_are_left_out(tf):
     assert bool((out[0][:3] == 7).all()) and not bool((out[0][3] == 7).all())
 
 
+@pytest.mark.parametrize("tokens,D,page", [(1, 64, 64), (1, 128, 16), (100, 128, 64), (100, 64, 16), (300, 128, 128)])
+@pytest.mark.parametrize("missing", [(0,), (2, 3), (1, -2)])
+def test_keys_of_missing_pages_are_left_out(tf, tokens, D, page, missing):
+    """As if the sequence were shorter by them (without mask and bias positions do not matter)."""
+    s = Setup(tf, [1000], [tokens], H=4, Hkv=2, D=D, page=page, seed=33)
+    used = -(-1000 // page)
+    for m in missing:
+        s.table[0, m % used] = len(s.cache.k) if m % 2 else -1
+    got = tf.kv_attend(*s.args, s.q, causal=False)
+    assert tf.device_status(clear=True) == 8
+    left = [p for i, p in enumerate(s.table_[0][:used]) if i not in {m % used for m in missing}]
+    kv_util.check_attend(got, s.q, s.cache, [left], [1000 - page * len(missing)], s.starts_, causal=False)
+
+
 def test_captured_and_replayed_as_the_sequences_grow(tf):
     s = Setup(tf, [60, 30, 16], [1, 1, 1], H=4, Hkv=2, page=16, seed=21)
     s.append(tf)
