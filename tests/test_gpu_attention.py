@@ -229,6 +229,15 @@ def test_documents_ranked_over_batch_rows(tf, B, S):
     both(tf, *make(2, B, S, S, 1, 1, 64, FP16, 59), q_docs=docs, k_docs=docs, causal=B == 3)
 
 
+def test_documents_of_any_number(tf):
+    docs = torch.full((1, 300), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    docs[:, 10:20], docs[:, 150:], docs[:, 299] = -2 ** 31, 0, -7
+    both(tf, *make(1, 1, 300, 300, 2, 1, 64, BF16, 60), q_docs=docs, k_docs=docs)
+    docs = torch.zeros((1, 256), dtype=torch.int32, device="cuda")
+    docs[:, 3] = -2 ** 31  # the only padding of its tile
+    both(tf, *make(1, 1, 256, 256, 2, 1, 64, BF16, 61), q_docs=docs, k_docs=docs)
+
+
 def test_two_calls_at_once(tf):
     """Calls in flight on two streams, each joining parts from a workspace of its own."""
     x = [make(1, 1, 1100, 3001, 2, 1, 128, BF16, seed) for seed in (51, 52)]

@@ -22,16 +22,18 @@ struct DocRange {
     bool hole;    // padding, or a place behind the end
 };
 
-__device__ __forceinline__ DocRange warp_range(const int32_t* docs, int first, int count, int end) {
+// The range of kN numbers of each lane (-1: padding, INT32_MIN: none).
+template <int kN>
+__device__ __forceinline__ DocRange warp_range(const int32_t (&v)[kN]) {
     DocRange r{INT32_MAX, -1, false};
     bool hole = false;
-    for (int i = threadIdx.x % 32; i < count; i += 32) {
-        const int d = first + i < end ? docs[first + i] : -1;
-        if (d >= 0) {
-            r.lo = min(r.lo, d);
-            r.hi = max(r.hi, d);
+#pragma unroll
+    for (int x = 0; x < kN; ++x) {
+        if (v[x] >= 0) {
+            r.lo = min(r.lo, v[x]);
+            r.hi = max(r.hi, v[x]);
         } else {
-            hole = true;
+            hole |= v[x] != INT32_MIN;
         }
     }
     r.lo = __reduce_min_sync(0xffffffffu, r.lo);
@@ -45,7 +47,9 @@ __device__ __forceinline__ DocRange warp_range(const int32_t* docs, int first, i
 template <bool kRowsAreKeys>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ AttentionParams p, uint32_t* plan,
                                                              uint32_t rows_per_tile, uint32_t row_tiles, uint32_t words) {
-    __shared__ DocRange row;
+    constexpr int kWarps = kPlanThreads / 32, kAhead = 4;  // a warp takes kAhead neighbours at a time
+    static_assert(kWarps * kAhead == 32, "the CTA covers a word at a time");
+    __shared__ DocRange row[kWarps];
     __shared__ uint32_t bits[2];
     grid_dependency_wait();
     const uint32_t rt = blockIdx.x % row_tiles, b = blockIdx.x / row_tiles, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -53,47 +57,41 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int32_t* row_docs = (kRowsAreKeys ? p.k_docs : p.q_docs) + int64_t(b) * rows;
     const int32_t* col_docs = (kRowsAreKeys ? p.q_docs : p.k_docs) + int64_t(b) * cols;
     const int r0 = int(rt * rows_per_tile), r1 = min(rows, r0 + int(rows_per_tile));
-    if (warp == 0) {
-        const DocRange r = warp_range(row_docs, r0, r1 - r0, rows);
-        if (lane == 0) row = r;
-    }
-    __syncthreads();
-    const DocRange rr = row;
-    uint32_t* out = plan + size_t(blockIdx.x) * 2 * words;
-    constexpr int kWarps = kPlanThreads / 32, kAhead = 4;  // a warp takes kAhead neighbours at a time
-    static_assert(kWarps * kAhead == 32, "the CTA covers a word at a time");
-    for (uint32_t w = 0; w < words; ++w) {
-        __syncthreads();
-        if (threadIdx.x < 2) bits[threadIdx.x] = 0;
-        __syncthreads();
-        int lo[kAhead], hi[kAhead];
-        bool hole[kAhead];
+    // the row tile's numbers, 32 a warp, and the first word's column tiles at the same time
+    int32_t own[1], v[kAhead][4];
+    const int mine = r0 + int(threadIdx.x);
+    own[0] = mine < r1 ? max(row_docs[mine], -1) : INT32_MIN;
+    auto load = [&](uint32_t w) {
         const int t0 = int(w) * 32 + int(warp) * kAhead;
-        int32_t v[kAhead][4];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int at = (t0 + k) * int(kAttnRows) + x * 32 + int(lane);
-                v[k][x] = at < cols ? col_docs[at] : -1;
+                v[k][x] = at < cols ? max(col_docs[at], -1) : -1;
             }
+    };
+    load(0);
+    const DocRange part = warp_range(own);
+    if (lane == 0) row[warp] = part;
+    __syncthreads();
+    DocRange rr = row[0];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            lo[k] = INT32_MAX;
-            hi[k] = -1;
-            bool h = false;
+    for (int x = 1; x < kWarps; ++x) {
+        rr.lo = min(rr.lo, row[x].lo);
+        rr.hi = max(rr.hi, row[x].hi);
+        rr.hole |= row[x].hole;
+    }
+    uint32_t* out = plan + size_t(blockIdx.x) * 2 * words;
+    for (uint32_t w = 0; w < words; ++w) {
+        __syncthreads();
+        if (threadIdx.x < 2) bits[threadIdx.x] = 0;
+        __syncthreads();
+        const int t0 = int(w) * 32 + int(warp) * kAhead;
+        DocRange c[kAhead];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                h |= v[k][x] < 0;
-                if (v[k][x] >= 0) {
-                    lo[k] = min(lo[k], v[k][x]);
-                    hi[k] = max(hi[k], v[k][x]);
-                }
-            }
-            lo[k] = __reduce_min_sync(0xffffffffu, lo[k]);
-            hi[k] = __reduce_max_sync(0xffffffffu, hi[k]);
-            hole[k] = __any_sync(0xffffffffu, h);
-        }
+        for (int k = 0; k < kAhead; ++k) c[k] = warp_range(v[k]);
+        if (w + 1 < words) load(w + 1);
         uint32_t some = 0, all = 0;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -102,8 +100,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             // the last query of the pair reaches furthest, its first one least
             const int far = key_bound(p, b, (kRowsAreKeys ? c1 : r1) - 1), near = key_bound(p, b, kRowsAreKeys ? c0 : r0);
             const int k0 = kRowsAreKeys ? r0 : c0, k1 = kRowsAreKeys ? r0 + int(kAttnRows) : c0 + int(kAttnRows);
-            const bool meet = rr.lo <= hi[k] && lo[k] <= rr.hi && rr.hi >= 0 && hi[k] >= 0 && k0 < far;
-            const bool whole = meet && rr.lo == rr.hi && lo[k] == hi[k] && !rr.hole && !hole[k] && k1 <= near;
+            const bool meet = rr.lo <= c[k].hi && c[k].lo <= rr.hi && rr.hi >= 0 && c[k].hi >= 0 && k0 < far;
+            const bool whole = meet && rr.lo == rr.hi && c[k].lo == c[k].hi && !rr.hole && !c[k].hole && k1 <= near;
             some |= uint32_t(meet) << ((t0 + k) % 32);
             all |= uint32_t(whole) << ((t0 + k) % 32);
         }
