@@ -6,8 +6,9 @@
 // r / shared, query head r % shared of its group -- and a chunk of the keys:
 //  * warp 13: looks up the pages of the tiles to come and copies their codes into a ring in
 //    shared memory (bulk copies of a group of 16 keys, which lies in one page).
-//  * warps 8-11: turn codes into operand tiles, exactly, in fp16 and the swizzled layout;
-//    K relative to the tile's largest page scale, V relative to the largest one so far.
+//  * warps 8-11: turn codes into operand tiles in fp16 and the swizzled layout; K relative
+//    to the tile's largest page scale, V relative to the largest one so far.  Exact for scales
+//    within 2^15 of that; codes of smaller ones round to multiples of 2^-24 of it.
 //    Before that they lay down Q, each row times a power of two (f16_factor).  Keys
 //    behind the sequence become zeros, whatever the page holds.
 //  * warp 12, one lane: the products, as in the forward kernel.
