@@ -26,7 +26,7 @@ SOURCES = ["block_kernels.cu", "block_kernels_v16.cu", "gemm_kernels.cu", "relay
            "tf_ulysses.cpp", "noalloc.cu", "attention_plan.cu", "attention_forward.cu", "attention_backward.cu", "attention_join.cu", "tf_attention.cpp", "kv_append.cu", "kv_attend.cu", "kv_attend_tiles.cu",
            "tf_kv_cache.cpp"]
 DEPS = SOURCES + ["relayout.h", "noalloc.h", "device_common.cuh", "block_kernel.cuh", "tma_plan.h", "gemm.h", "host.h",
-                  "attention.h", "attention_common.cuh", "attention_plan.h",
+                  "attention.h", "attention_common.cuh", "attention_order.h", "attention_plan.h",
                   "tcgen05.cuh", "kv_cache.h", "kv_common.cuh"]
 
 

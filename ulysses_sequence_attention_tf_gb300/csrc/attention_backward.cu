@@ -28,6 +28,7 @@
 // 32 and 26 %, issue slots 56 and 53 %.  16 row warps took 2.72 ms where 8 took 2.88 (16380 tokens,
 // 5 heads); rings of their own for K and V in dQ 2.46; units cut along the other side 2.09.
 #include "attention_common.cuh"
+#include "attention_order.h"
 #include "attention_plan.h"
 
 namespace tfu {
@@ -164,11 +165,11 @@ __device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b) {
 // ---------------------------------------------------------------- dQ
 // One CTA: 128 query rows of one head, tiles of 128 keys.
 //  * warp 16, one lane: TMA.  Q and dO once, K and V through a ring K0 V0 K1 V1 ...
-//  * warp 17, one lane: S(j+1) = Q K^T into the other S buffer, dP(j+1) = dO V^T once
-//    dP(j) has been read, dQ += dx(j) K (dx from TMEM, K read MN-major).
+//  * warp 17, one lane: S(j+1) = Q K^T once S(j) has been read, dQ += dx(j) K (dx from
+//    TMEM, K read MN-major), dP(j+1) = dO V^T (dq_order).
 //  * warps 0-15: a thread per row and quarter of the tile's keys; dx in 16 bits goes
-//    over the scores it came from.
-// TMEM: S0 S1 dP (128 columns each), dQ (D columns).
+//    over the dP it came from.
+// TMEM: S, dP (128 columns each), dQ (D columns).
 // K is held from S to dQ, about two tiles, V only for dP: three stages and two fill the shared
 // memory at D = 128 (with four shared ones the load of K waited for the dQ product before it).
 template <int kD>
@@ -190,9 +191,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kStages) * size_t(kTile));
     const uint32_t q_smem = smem_u32(smem), do_smem = q_smem + kTile, ring = q_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
-    const uint32_t s_full0 = q_full + 8, dp_full = s_full0 + 16, dp_free = dp_full + 8, dx_full = dp_free + 8;
+    const uint32_t s_full = q_full + 8, dp_full = s_full + 8, s_read = dp_full + 8, dx_full = s_read + 8;
     const uint32_t sums_full = dx_full + 8, done = sums_full + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 8);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 7);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // stage of tile n of K, of V, and the phase of its barriers
@@ -213,10 +214,9 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(q_full, 1);
-        mbar_init(s_full0, 1);
-        mbar_init(s_full0 + 8, 1);
+        mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
-        mbar_init(dp_free, 16);  // a warp each
+        mbar_init(s_read, 16);  // a warp each
         mbar_init(dx_full, 16);
         mbar_init(sums_full, 16);
         mbar_init(done, 1);
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     tc_fence_after();
     grid_dependency_wait();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t dp_tmem = tmem + 2 * kAttnRows, dq_tmem = tmem + 3 * kAttnRows;
+    const uint32_t dp_tmem = tmem + kAttnRows, dq_tmem = tmem + 2 * kAttnRows;
 
     const int last = min(row0 + int(kAttnRows), int(p.Sq)) - 1;
     const int reach = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
@@ -289,45 +289,47 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
         constexpr uint32_t kIdescQ = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
         const int steps = exact ? 2 * visits : visits;
-        const uint32_t q_low = desc_low(q_smem), do_low = desc_low(do_smem), kv_low = desc_low(ring),
-                       k_low = desc_low(ring, kHalfTile);
-        auto offset = [](uint32_t s) { return s * (kTile >> 4); };
-        bool ok = steps == 0 || wait_for(q_full, 0, abort_flag);
-        auto scores = [&](int i) {
-            if (!wait_for(full0 + 8 * key_stage(i), key_phase(i), abort_flag)) return false;
-            tc_fence_after();
-            tc_product<kD, kHalfTile, kHalfTile>(tmem + (i & 1) * kAttnRows, q_low, kv_low + offset(key_stage(i)), kIdescS);
-            tc_commit(s_full0 + 8 * (i & 1));
-            return true;
-        };
-        auto dp = [&](int i) {
-            if (!wait_for(full0 + 8 * value_stage(i), value_phase(i), abort_flag)) return false;
-            tc_fence_after();
-            tc_product<kD, kHalfTile, kHalfTile>(dp_tmem, do_low, kv_low + offset(value_stage(i)), kIdescS);
-            tc_commit(dp_full);
-            tc_commit(empty0 + 8 * value_stage(i));
-            return true;
-        };
-        if (ok && steps > 0) ok = scores(0) && dp(0);
-        for (int i = 0; ok && i < steps; ++i) {
-            const bool sums_only = exact && i < visits;
-            if (i + 1 < steps) {
-                // the other S buffer: its dx was read by the dQ product issued before
-                if (!(ok = scores(i + 1))) break;
-                if (!(ok = wait_for(dp_free, i & 1u, abort_flag))) break;
-                if (!(ok = dp(i + 1))) break;
+        struct Pipe {
+            decltype(key_stage) k_stage;
+            decltype(value_stage) v_stage;
+            decltype(key_phase) k_phase;
+            decltype(value_phase) v_phase;
+            uint32_t full0, empty0, s_full, dp_full, s_read, dx_full, tmem, dp_tmem, dq_tmem, q_low, do_low, kv_low, k_low;
+            int first;  // tile from which on dx is taken
+            volatile int* abort_flag;
+            __device__ __forceinline__ static uint32_t offset(uint32_t s) { return s * (kTile >> 4); }
+            __device__ __forceinline__ bool scores(int i) {
+                if (!wait_for(full0 + 8 * k_stage(i), k_phase(i), abort_flag)) return false;
+                tc_fence_after();
+                tc_product<kD, kHalfTile, kHalfTile>(tmem, q_low, kv_low + offset(k_stage(i)), kIdescS);
+                tc_commit(s_full);
+                return true;
             }
-            if (!(ok = wait_for(dx_full, i & 1u, abort_flag))) break;
-            tc_fence_after();
-            if (!sums_only) {
-                const uint32_t a = tmem + (i & 1) * kAttnRows;
-                const bool first = i == (exact ? visits : 0);
+            __device__ __forceinline__ bool gradients(int i) {
+                if (!wait_for(full0 + 8 * v_stage(i), v_phase(i), abort_flag)) return false;
+                tc_fence_after();
+                tc_product<kD, kHalfTile, kHalfTile>(dp_tmem, do_low, kv_low + offset(v_stage(i)), kIdescS);
+                tc_commit(dp_full);
+                tc_commit(empty0 + 8 * v_stage(i));
+                return true;
+            }
+            __device__ __forceinline__ bool wait(DqBarrier b, uint32_t parity) {
+                if (!wait_for(b == DqBarrier::kScoresRead ? s_read : dx_full, parity, abort_flag)) return false;
+                tc_fence_after();
+                return true;
+            }
+            __device__ __forceinline__ void update(int i) {
+                if (i >= first) {
 #pragma unroll
-                for (uint32_t x = 0; x < 4; ++x)  // the quarters of the keys lie 32 columns apart
-                    tc_product_ts<32>(dq_tmem, a + 32 * x, k_low + offset(key_stage(i)) + (32 * x * kSwizzleRow >> 4), kIdescQ, !first || x != 0);
+                    for (uint32_t x = 0; x < 4; ++x)  // the quarters of the keys lie 32 columns apart
+                        tc_product_ts<32>(dq_tmem, dp_tmem + 32 * x, k_low + offset(k_stage(i)) + (32 * x * kSwizzleRow >> 4), kIdescQ,
+                                          i != first || x != 0);
+                }
+                tc_commit(empty0 + 8 * k_stage(i));
             }
-            tc_commit(empty0 + 8 * key_stage(i));
-        }
+        } pipe{key_stage, value_stage, key_phase, value_phase, full0, empty0, s_full, dp_full, s_read, dx_full, tmem, dp_tmem, dq_tmem,
+               desc_low(q_smem), desc_low(do_smem), desc_low(ring), desc_low(ring, kHalfTile), exact ? visits : 0, abort_flag};
+        if (steps > 0 && wait_for(q_full, 0, abort_flag)) dq_order(steps, pipe);
         tc_commit(done);
         drain_phase(done, 0);
     }
@@ -363,13 +365,14 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             TileIter it(plan, n_tiles, first_tile);
             float sum = 0.f;
             for (int j = it.next(); j >= 0; j = it.next(), ++n) {
-                const uint32_t s_row = tmem + (n & 1) * kAttnRows + part * 32 + lane_base;
-                wait_for(s_full0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag);
+                const uint32_t dp_row = dp_tmem + part * 32 + lane_base;
+                wait_for(s_full, n & 1u, abort_flag);
                 tc_fence_after();
                 const int j0 = j * int(kAttnRows) + int(part) * 32;
                 float s[32];
                 uint64_t bend[kCap ? 16 : 1];
-                load_row<32>(s_row, s);
+                load_row<32>(tmem + part * 32 + lane_base, s);
+                warp_arrive(s_read);
                 const int pos = i + int(p.Sk) - int(p.Sq), pos0 = row0 + int(p.Sk) - int(p.Sq);
                 const int side = kBias ? bias_side(pos0, int(kAttnRows), j0, 32, p.causal && !p.prefix) : 1;
                 const float at = kBias && side != 0 ? less - float(side) * slope2 * float(pos - j0) : less;
@@ -416,8 +419,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 wait_for(dp_full, n & 1u, abort_flag);
                 tc_fence_after();
                 float d[32];
-                load_row<32>(dp_tmem + part * 32 + lane_base, d);
-                warp_arrive(dp_free);
+                load_row<32>(dp_row, d);
                 if (!whole) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) d[x] = (bits[0] >> x) & 1u ? d[x] : 0.f;
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                         if constexpr (kCap) dx = f2_mul(dx, bend[x / 2]);
                         f2_unpack(dx, d[x], d[x + 1]);
                     }
-                    store_row16<kF, 32>(s_row, d);
+                    store_row16<kF, 32>(dp_row, d);
                     tc_wait_st();
                 }
                 warp_arrive(dx_full);
