@@ -53,6 +53,13 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
     return bounded_wait(bar, parity, abort_flag, &g_attention_backward_status);
 }
 
+// What of a pair is seen (bits 0 and 1): NaN in padding must not reach a product as a factor of a weight 0.
+__device__ __forceinline__ uint64_t keep_pair(uint64_t v, uint32_t see) {
+    float a, b;
+    f2_unpack(v, a, b);
+    return f2_pack(see & 1u ? a : 0.f, see & 2u ? b : 0.f);
+}
+
 // Arguments of the weights of a row's scores, for pairs of them: log2 e z - lse2, where `add`
 // holds -lse2 and what the bias gives; and (capped) the slope 1 - tanh^2 of each.
 template <bool kCap>
@@ -415,6 +422,10 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                     }
 #pragma unroll
                     for (int x = 0; x < 32; ++x) s[x] = (bits[0] >> x) & 1u ? s[x] : 0.f;
+                    if constexpr (kCap) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) bend[x / 2] = keep_pair(bend[x / 2], bits[0] >> x);
+                    }
                 }
                 wait_for(dp_full, n & 1u, abort_flag);
                 tc_fence_after();
@@ -804,6 +815,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                                 s[e + z] = see ? s[e + z] : 0.f;
                                 d[e + z] = see ? d[e + z] : 0.f;
                             }
+                            if constexpr (kCap) bend = keep_pair(bend, bits >> e);
                         }
                         const uint64_t off = y ? f2_pack(nd.z, nd.w) : f2_pack(nd.x, nd.y), d2 = f2_pack(d[e], d[e + 1]);
                         uint64_t dx = f2_mul(f2_pack(s[e], s[e + 1]), kF == Fused::kFP16 ? f2_fma(d2, down2, off) : f2_add(d2, off));
