@@ -90,7 +90,17 @@ __device__ __forceinline__ void norm_rotate(float (&x)[16], const uint32_t (&raw
         ms = __fadd_rn(ms, other);
 #pragma unroll
         for (int m = 1; m < kLanes; m <<= 1) ms = __fadd_rn(ms, __shfl_xor_sync(0xffffffffu, ms, m));
-        ms = ms <= kFltMax ? __fmul_rn(ms, 1.0f / kD) : row_mean_sq<kLanes, 8, true>(x2, nullptr);  // the same in a row's lanes
+        ms = __fmul_rn(ms, 1.0f / kD);
+        // A sum that is not finite: again from 2^-72 x, for the whole warp (it holds several rows, and
+        // shuffles over all of its lanes).  A mean beyond fp32 is infinite, and its row 0.
+        if (!__all_sync(0xffffffffu, ms <= kFltMax)) {
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t = fmaf(x[i] * 0x1p-72f, x[i] * 0x1p-72f, t);
+#pragma unroll
+            for (int m = 1; m < kLanes; m <<= 1) t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, m));
+            if (!(ms <= kFltMax)) ms = t * (1.0f / kD) * 0x1p72f * 0x1p72f;
+        }
         const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(ms, eps)));
         const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
