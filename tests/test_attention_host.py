@@ -107,3 +107,34 @@ def test_tensors_off_the_device_refused(tf):
         calls.kv_attend(*[None] * 7, 0, 0, rows, *none, 0.0, None, True)
     with pytest.raises(ValueError, match="rope"):
         tf.kv_append(cache, *where, rows, rows, rope="other")
+
+
+@pytest.mark.parametrize("name", ["attention", "attention_backward", "kv_append", "kv_attend"])
+def test_a_call_on_a_stream_takes_the_streams_device(tf, monkeypatch, name):
+    """The device that tensors are checked against and the raw stream are those of the stream's context, whose
+    device may be another than the caller's; no GPU is needed to see which are handed over."""
+    import contextlib
+
+    import torch
+    current = [0]
+
+    @contextlib.contextmanager
+    def entered(stream):
+        before, current[0] = current[0], stream
+        try:
+            yield
+        finally:
+            current[0] = before
+
+    class Calls:
+        def __getattr__(self, called):
+            return lambda *args: (called, args)
+
+    monkeypatch.setattr(tf, "_calls", Calls())
+    monkeypatch.setattr(tf, "_on_stream", entered)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 1000 * (device + 1) + current[0], raising=False)
+    for stream, device in ((1, 1), (0, 0), (None, 0)):
+        called, args = tf._run(name, stream, ("before",), ("after",))
+        assert called == name and args == ("before", device, 1001 * device + 1000, "after")
+    assert current == [0]

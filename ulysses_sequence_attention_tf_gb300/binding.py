@@ -467,13 +467,17 @@ def _on_stream(stream):
 
 
 def _run(name, stream, before, after):
-    """``name`` of the module with the current device and the stream between its arguments."""
+    """``name`` of the module with the device and the stream of the call between its arguments."""
     call = getattr(_calls or _torch_calls(), name)
-    device = torch._C._cuda_getDevice()
     if stream is None:
-        return call(*before, device, torch._C._cuda_getCurrentRawStream(device), *after)
-    with _on_stream(stream):
-        return call(*before, device, torch._C._cuda_getCurrentRawStream(device), *after)
+        return _on_device(call, before, after)
+    with _on_stream(stream):  # whose device is current in here
+        return _on_device(call, before, after)
+
+
+def _on_device(call, before, after):
+    device = torch._C._cuda_getDevice()
+    return call(*before, device, torch._C._cuda_getCurrentRawStream(device), *after)
 
 
 def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=None, causal=False, prefix=None,
