@@ -19,24 +19,25 @@ struct Bar { int done = 0; bool over(uint32_t parity) const { return (uint32_t(d
 struct Model {
     int steps;
     bool eager;
-    Bar s_full, dp_full, s_read, dx;
+    Bar s_full, dp_full, p, dx;
     int row = 0, at = 0;                       // the rows' step, and how far they are in it
-    int s = -1, dp = -1, updated = -1;         // what S and dP hold; the last dx that was taken
+    int s = -1, dp = -1, weighed = -1, updated = -1;  // what S and dP hold; the last P and dx that were taken
     long bad = 0;
     bool row_step() {                          // one action of the rows, if they can go on
         if (row >= steps) return false;
         const uint32_t parity = uint32_t(row) & 1u;
-        if (at == 0) { if (!s_full.over(parity)) return false; bad += s != row; ++s_read.done; at = 1; return true; }
+        if (at == 0) { if (!s_full.over(parity)) return false; bad += s != row; ++p.done; at = 1; return true; }
         if (!dp_full.over(parity)) return false;
         bad += dp != row; ++dx.done; at = 0; ++row;
         return true;
     }
     void run() { while (row_step()) {} }
-    bool scores(int i) { bad += row < i - 1 || (row == i - 1 && at == 0); s = i; ++s_full.done; if (eager) run(); return true; }
+    bool scores(int i) { bad += weighed != i - 1; s = i; ++s_full.done; if (eager) run(); return true; }
     bool gradients(int i) { bad += updated != i - 1; dp = i; ++dp_full.done; if (eager) run(); return true; }
+    void weights(int i) { bad += row < i || (row == i && at == 0) || weighed != i - 1; weighed = i; if (eager) run(); }
     void update(int i) { bad += row <= i || updated != i - 1; updated = i; if (eager) run(); }
     bool wait(DqBarrier b, uint32_t parity) {
-        Bar& bar = b == DqBarrier::kScoresRead ? s_read : dx;
+        Bar& bar = b == DqBarrier::kWeightsWritten ? p : dx;
         while (!bar.over(parity)) if (!row_step()) { ++bad; return false; }   // a wait that cannot end
         return true;
     }
@@ -46,7 +47,9 @@ struct Model {
 template <typename Pipe> bool ahead(int steps, Pipe& p) {
     if (!p.scores(0) || !p.gradients(0)) return false;
     for (int i = 0; i < steps; ++i) {
-        if (i + 1 < steps && (!p.wait(DqBarrier::kScoresRead, i & 1u) || !p.scores(i + 1) || !p.gradients(i + 1))) return false;
+        if (!p.wait(DqBarrier::kWeightsWritten, i & 1u)) return false;
+        p.weights(i);
+        if (i + 1 < steps && (!p.scores(i + 1) || !p.gradients(i + 1))) return false;
         if (!p.wait(DqBarrier::kDxWritten, i & 1u)) return false;
         p.update(i);
     }
@@ -60,7 +63,7 @@ int main() {
             Model m{steps, eager != 0};
             const bool ok = dq_order(steps, m);
             m.run();
-            bad += m.bad + !ok + (m.row != steps) + (m.updated != steps - 1);
+            bad += m.bad + !ok + (m.row != steps) + (m.updated != steps - 1) + (m.weighed != steps - 1);
             if (steps < 2) continue;
             Model n{steps, eager != 0};
             found += !ahead(steps, n) && eager;

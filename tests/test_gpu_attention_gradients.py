@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from attention_util import Reference
+from gradient_util import Gradients
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,60 @@ def test_padding_may_hold_anything_under_a_cap(tf, biased, cap, causal, D, dtype
         dq, dk, dv = tf.attention_backward(dout, q, k, v, out, lse, **kw)
         for name, got in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
             ref.check(name, got)
+
+
+def sharp(tf, q, k, v, dout, *, docs=None, **kw):
+    """Gradients against bounds in which the output's rounding has no part but times another rounding."""
+    call = dict(kw, **({} if docs is None else dict(q_docs=docs, k_docs=docs)))
+    out, lse = tf.attention(q, k, v, **call)
+    dq, dk, dv = tf.attention_backward(dout, q, k, v, out, lse, **call)
+    ref = Gradients(q, k, v, dout, out, docs=docs, **kw)
+    ref.check("dq", dq)
+    ref.check("dk", dk)
+    Reference(q, k, v, dout, **call).check("dv", dv)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_rows_in_which_few_keys_weigh(tf, cap, D, dtype):
+    """Steep distances leave a row one to six of two thousand keys that it sees."""
+    gen = torch.Generator(device="cuda").manual_seed(63)
+    x = [rows(gen, 1, 2000, 2, D, dtype, P=2) for _ in range(4)]
+    for causal in (True, False):
+        sharp(tf, *x, slopes=torch.tensor([0.5, 0.63, 1.0, 2.0], device="cuda"), softcap=cap, causal=causal)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_short_documents_behind_long_ones(tf, causal, D, dtype):
+    """A document's gradients do not depend on what shares its tiles."""
+    gen = torch.Generator(device="cuda").manual_seed(64)
+    lens = [1500, 3, 1, 2, 700, 1, 1, 5, 20, 400]
+    docs = torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(lens)).to(torch.int32).cuda()[None]
+    x = [rows(gen, 1, sum(lens), 2, D, dtype) for _ in range(4)]
+    sharp(tf, *x, docs=docs, causal=causal)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D,Sq,Sk", [(64, 2100, 2100), (128, 2100, 2100), (128, 300, 5000), (64, 20000, 1100)])
+def test_keys_and_values_with_a_common_part(tf, Sq, Sk, D, dtype):
+    """Their means as large as their spread: what delta lacks adds up over a row (the last two: units in parts)."""
+    gen = torch.Generator(device="cuda").manual_seed(65)
+    q, dout = rows(gen, 1, Sq, 1, D, dtype), rows(gen, 1, Sq, 1, D, dtype)
+    k, v = ([t + 1 for t in rows(gen, 1, Sk, 1, D, dtype)] for _ in range(2))
+    sharp(tf, q, k, v, dout)
+    sharp(tf, q, k, v, dout, softcap=5.0)
+    if Sq == Sk:
+        sharp(tf, q, k, v, dout, causal=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_score_that_dominates(tf, D, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(66)
+    q, k, v, dout = (rows(gen, 1, 1100, 2, D, dtype) for _ in range(4))
+    q[0] += 3 * k[0]  # a query close to the key at its own position
+    sharp(tf, q, k, v, dout)
+    sharp(tf, q, k, v, dout, causal=True)

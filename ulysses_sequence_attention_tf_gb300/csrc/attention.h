@@ -25,7 +25,7 @@ struct AttentionParams {
     GroupView q, k, v, out;
     GroupView dout, dq, dk, dv;  // backward only
     float* lse[kMaxShards];      // [B][Hl][Sq] per group, or null
-    float* delta;                // backward: workspace [P][B][Hl][Sq], sum_d dO * O of each row
+    float* delta;                // backward: workspace [P][B][Hl][Sq], sum_j P dP of each row
     uint32_t* plan;              // with documents: the visible tiles (TilePlan)
     const float* slopes;         // [P * Hl] or null
     const int32_t* prefix;       // [B] or null
@@ -50,8 +50,8 @@ struct GroupMaps {
 // them in order.  Without documents and causal mask only: the units cost the same then.
 struct Split {
     uint32_t whole, parts;  // units that are not cut, parts of each other one (1: none is cut)
-    float* part;            // forward: O rows; dQ rows; dK rows, then dV rows
-    float2* stat;           // forward: a row's reference (log2) and sum
+    float* part;            // forward: O rows; dQ rows, then W rows; dK rows, then dV rows
+    float2* stat;           // forward: a row's reference (log2) and sum; dQ: what delta lacks (x)
 };
 constexpr uint32_t kAttnSms = 152;   // SMs of a GB300
 constexpr uint32_t kLeastPart = 8;   // tiles of the other side in a part: below, the join costs more than it gives
@@ -119,6 +119,7 @@ bool encode_group_maps(GroupMaps* maps, const GroupView& v, uint32_t P, uint32_t
 
 // Join the parts of cut units: rows of kAttnPair (forward) or kAttnRows a unit.
 cudaError_t launch_join_forward(const ForwardParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_join_dq(const BackwardParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_join_gradient(const AttentionParams& p, const Split& s, const GroupView& out, const float* part, float factor,
                                  uint32_t row_tiles, uint32_t rows, uint32_t heads, bool bf16, cudaStream_t stream);
 

@@ -2,20 +2,25 @@
 // 5th-generation tensor cores.
 //
 // With the weights P_ij = e^(z_ij - lse_i) recomputed from Q, K and the saved
-// log-sum-exp, and delta_i = sum_j P_ij dP_ij (= sum_d dO_id O_id):
+// log-sum-exp, and delta_i = sum_j P_ij dP_ij:
 //   dP_ij = dO_i . V_j                          dV_j = sum_i P_ij dO_i
-//   dx_ij = P_ij (dP_ij - delta_i) (1 - tanh^2(x_ij / cap))    (the last factor where scores are capped)
+//   dx_ij = P_ij (dP_ij - delta_i) bend_ij      bend = 1 - tanh^2(x / cap) where scores are capped, else 1
 //   dQ_i  = scale * sum_j dx_ij K_j             dK_j = scale * sum_i dx_ij Q_i
 //
 // Two kernels: dq_kernel owns query rows and sums over the keys, dkv_kernel owns
 // key rows and sums over the queries of every head that shares the key head.  S and
-// dP are computed in both (7 products instead of 5), which spares the read-modify-
-// write of dQ in memory: no atomics, so the same inputs give the same bits.
+// dP are computed in both, which spares the read-modify-write of dQ in memory: no
+// atomics, so the same inputs give the same bits.
 //
-// delta_i: the output O holds a rounding of 2^-9 (bf16), and where a row sees few keys
-// dP - delta cancels, so that dO . O is not enough (a row of three keys: dQ off by 2 %).
-// A row tile that visits at most kExactTiles key tiles therefore sums P dP over its keys
-// first and uses that; the others take dO . O.
+// delta_i = sum_d dO_id O_id, but O is given rounded (by up to 2^-8 in bf16), and what that leaves out, e_i,
+// counts times P_ij against dx.  Modelled in 64 bits with bf16 roundings, one row in a hundred was off by 2.4 % with a
+// distance bias of 0.63, by 31 % with 2, and by 14 % where keys and values have means as large as their
+// spread, instead of 0.3 to 0.5 %; rows of three keys by 2 %.  dq_kernel therefore takes d0 = dO . O
+// only as a first value, sums what is missing,
+//   e_i = sum_j P_ij (dP_ij - d0_i) = delta_i - d0_i      (sum_j P_ij = 1), and
+//   dQ_i = scale * (sum_j P_ij (dP_ij - d0_i) bend_ij K_j - e_i * sum_j P_ij bend_ij K_j):
+// one product more, whose roundings count only times e_i.  It hands d0 + e to dkv_kernel.
+// Eight products are executed where five would do.
 //
 // P and dx are rounded to the I/O type as operands (one MMA takes A and B of one type; a second product
 // for the rest would cost a seventh more for each): with bf16 that adds about 0.0017 of the norm to
@@ -47,7 +52,6 @@ struct Bool {
     static constexpr bool value = kV;
 };
 constexpr uint32_t kHalfTile = kAttnRows * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
-constexpr int kExactTiles = 4;
 
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     return bounded_wait(bar, parity, abort_flag, &g_attention_backward_status);
@@ -134,7 +138,25 @@ __device__ __forceinline__ void write_row(uint32_t taddr, bool any, bool valid, 
     }
 }
 
-// the same in fp32, for a part of a unit
+// 32 columns of dQ: factor * (sums - e * weights)
+template <Fused kF>
+__device__ __forceinline__ void write_dq(uint32_t sums, uint32_t weights, bool any, bool valid, float e, float factor, uint8_t* dst) {
+    float a[32] = {}, w[32] = {};
+    if (any) {
+        load_row<32>(sums, a);
+        load_row<32>(weights, w);
+    }
+#pragma unroll
+    for (int x = 0; x < 32; x += 8) {
+        uint32_t o[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            o[z] = pack2<kF>(fmaf(-e, w[x + 2 * z], a[x + 2 * z]) * factor, fmaf(-e, w[x + 2 * z + 1], a[x + 2 * z + 1]) * factor);
+        if (valid) *reinterpret_cast<uint4*>(dst + x * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// accumulator columns in fp32, for a part of a unit
 template <int kCols>
 __device__ __forceinline__ void write_sums(uint32_t taddr, float* dst) {
 #pragma unroll 1
@@ -172,11 +194,11 @@ __device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b) {
 // ---------------------------------------------------------------- dQ
 // One CTA: 128 query rows of one head, tiles of 128 keys.
 //  * warp 16, one lane: TMA.  Q and dO once, K and V through a ring K0 V0 K1 V1 ...
-//  * warp 17, one lane: S(j+1) = Q K^T once S(j) has been read, dQ += dx(j) K (dx from
-//    TMEM, K read MN-major), dP(j+1) = dO V^T (dq_order).
-//  * warps 0-15: a thread per row and quarter of the tile's keys; dx in 16 bits goes
-//    over the dP it came from.
-// TMEM: S, dP (128 columns each), dQ (D columns).
+//  * warp 17, one lane: W += P(j) K, S(j+1) = Q K^T; dQ += dx(j) K, dP(j+1) = dO V^T, the first two
+//    when P is there, the others when dx is (dq_order; P, dx from TMEM, K read MN-major for them).
+//  * warps 0-15: a thread per row and quarter of the tile's keys; P (times bend) in 16 bits goes over
+//    the scores it came from, dx over the dP.
+// TMEM: S, dP (128 columns each), dQ, W (D columns each).
 // K is held from S to dQ, about two tiles, V only for dP: three stages and two fill the shared
 // memory at D = 128 (with four shared ones the load of K waited for the dQ product before it).
 template <int kD>
@@ -198,7 +220,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (2 + kStages) * size_t(kTile));
     const uint32_t q_smem = smem_u32(smem), do_smem = q_smem + kTile, ring = q_smem + 2 * kTile;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages, q_full = empty0 + 8 * kStages;
-    const uint32_t s_full = q_full + 8, dp_full = s_full + 8, s_read = dp_full + 8, dx_full = s_read + 8;
+    const uint32_t s_full = q_full + 8, dp_full = s_full + 8, p_full = dp_full + 8, dx_full = p_full + 8;
     const uint32_t sums_full = dx_full + 8, done = sums_full + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 7);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -223,7 +245,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         mbar_init(q_full, 1);
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
-        mbar_init(s_read, 16);  // a warp each
+        mbar_init(p_full, 16);  // a warp each
         mbar_init(dx_full, 16);
         mbar_init(sums_full, 16);
         mbar_init(done, 1);
@@ -240,7 +262,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     tc_fence_after();
     grid_dependency_wait();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t dp_tmem = tmem + kAttnRows, dq_tmem = tmem + 2 * kAttnRows;
+    const uint32_t dp_tmem = tmem + kAttnRows, dq_tmem = tmem + 2 * kAttnRows, w_tmem = dq_tmem + kD;
 
     const int last = min(row0 + int(kAttnRows), int(p.Sq)) - 1;
     const int reach = (key_bound(p, b, last) + int(kAttnRows) - 1) / int(kAttnRows);
@@ -252,7 +274,6 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         visits = 0;
         for (uint32_t w = 0; w < words; ++w) visits += __popc(__ldg(plan + w));
     }
-    const bool exact = visits <= kExactTiles && unit.parts == 1;  // two phases: delta from P dP, then dQ
 
     if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");  // 640 * 96 at launch >= 512 * 104 + 128 * 56
@@ -268,23 +289,19 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 tma_load_4d(do_smem + x * kHalfTile, &bp.dout.m[g], x * 64, int(h), row0, int(b), q_full);
             }
         }
-        for (int phase = exact ? 0 : 1; phase < 2; ++phase) {
-            TileIter it(plan, n_tiles, first_tile);
-            for (int j = it.next(); ok && j >= 0; j = it.next()) {
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t s = kv ? value_stage(n) : key_stage(n), phase_of = kv ? value_phase(n) : key_phase(n);
-                    const bool again = n >= (kv ? S::kValueStages : S::kKeyStages);
-                    if (again && !wait_for(empty0 + 8 * s, phase_of ^ 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(full0 + 8 * s, kTile);
-                    for (int x = 0; x < kD / 64; ++x)
-                        tma_load_4d(ring + s * kTile + x * kHalfTile, maps[kv], x * 64, kh, j * int(kAttnRows), int(b),
-                                    full0 + 8 * s);
-                    loaded[kv] = n + 1;
+        TileIter it(plan, n_tiles, first_tile);
+        for (int j = it.next(); ok && j >= 0; j = it.next(), ++n) {
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t s = kv ? value_stage(n) : key_stage(n), phase_of = kv ? value_phase(n) : key_phase(n);
+                const bool again = n >= (kv ? S::kValueStages : S::kKeyStages);
+                if (again && !wait_for(empty0 + 8 * s, phase_of ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
                 }
-                ++n;
+                mbar_expect_tx(full0 + 8 * s, kTile);
+                for (int x = 0; x < kD / 64; ++x)
+                    tma_load_4d(ring + s * kTile + x * kHalfTile, maps[kv], x * 64, kh, j * int(kAttnRows), int(b), full0 + 8 * s);
+                loaded[kv] = n + 1;
             }
         }
         if (visits > 0) drain_phase(q_full, 0);
@@ -295,14 +312,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     } else if (warp == 17 && elect_one()) {
         constexpr uint32_t kIdescS = f16_idesc(kF == Fused::kBF16, kAttnRows, kAttnRows, false);
         constexpr uint32_t kIdescQ = f16_idesc(kF == Fused::kBF16, kAttnRows, kD, true);
-        const int steps = exact ? 2 * visits : visits;
         struct Pipe {
             decltype(key_stage) k_stage;
             decltype(value_stage) v_stage;
             decltype(key_phase) k_phase;
             decltype(value_phase) v_phase;
-            uint32_t full0, empty0, s_full, dp_full, s_read, dx_full, tmem, dp_tmem, dq_tmem, q_low, do_low, kv_low, k_low;
-            int first;  // tile from which on dx is taken
+            uint32_t full0, empty0, s_full, dp_full, p_full, dx_full, tmem, dp_tmem, dq_tmem, w_tmem, q_low, do_low, kv_low, k_low;
             volatile int* abort_flag;
             __device__ __forceinline__ static uint32_t offset(uint32_t s) { return s * (kTile >> 4); }
             __device__ __forceinline__ bool scores(int i) {
@@ -321,22 +336,24 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 return true;
             }
             __device__ __forceinline__ bool wait(DqBarrier b, uint32_t parity) {
-                if (!wait_for(b == DqBarrier::kScoresRead ? s_read : dx_full, parity, abort_flag)) return false;
+                if (!wait_for(b == DqBarrier::kWeightsWritten ? p_full : dx_full, parity, abort_flag)) return false;
                 tc_fence_after();
                 return true;
             }
-            __device__ __forceinline__ void update(int i) {
-                if (i >= first) {
+            // sum += a K, a in TMEM: the quarters of the keys lie 32 columns apart
+            __device__ __forceinline__ void add(uint32_t sum, uint32_t a, int i) {
 #pragma unroll
-                    for (uint32_t x = 0; x < 4; ++x)  // the quarters of the keys lie 32 columns apart
-                        tc_product_ts<32>(dq_tmem, dp_tmem + 32 * x, k_low + offset(k_stage(i)) + (32 * x * kSwizzleRow >> 4), kIdescQ,
-                                          i != first || x != 0);
-                }
+                for (uint32_t x = 0; x < 4; ++x)
+                    tc_product_ts<32>(sum, a + 32 * x, k_low + offset(k_stage(i)) + (32 * x * kSwizzleRow >> 4), kIdescQ, i != 0 || x != 0);
+            }
+            __device__ __forceinline__ void weights(int i) { add(w_tmem, tmem, i); }
+            __device__ __forceinline__ void update(int i) {
+                add(dq_tmem, dp_tmem, i);
                 tc_commit(empty0 + 8 * k_stage(i));
             }
-        } pipe{key_stage, value_stage, key_phase, value_phase, full0, empty0, s_full, dp_full, s_read, dx_full, tmem, dp_tmem, dq_tmem,
-               desc_low(q_smem), desc_low(do_smem), desc_low(ring), desc_low(ring, kHalfTile), exact ? visits : 0, abort_flag};
-        if (steps > 0 && wait_for(q_full, 0, abort_flag)) dq_order(steps, pipe);
+        } pipe{key_stage, value_stage, key_phase, value_phase, full0, empty0, s_full, dp_full, p_full, dx_full, tmem, dp_tmem, dq_tmem, w_tmem,
+               desc_low(q_smem), desc_low(do_smem), desc_low(ring), desc_low(ring, kHalfTile), abort_flag};
+        if (visits > 0 && wait_for(q_full, 0, abort_flag)) dq_order(visits, pipe);
         tc_commit(done);
         drain_phase(done, 0);
     }
@@ -358,124 +375,134 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         const float lse = valid ? p.lse[g][stat] : 0.f;
         const float less = lse == -INFINITY ? 0.f : -lse * kLog2e, slope2 = slope * kLog2e;
         const int64_t at = valid ? i : 0;
-        float delta = 0.f;
-        if (!exact && valid) {
+        float delta = 0.f;  // d0
+        if (visits > 0 && valid) {
             delta = row_dot<kF, kD>(p.dout.base[g] + b * p.dout.b + at * p.dout.t + h * p.dout.h,
                                     p.out.base[g] + b * p.out.b + at * p.out.t + h * p.out.h);
             if (p.plan && doc < 0) delta = 0.f;  // padding: its output gradient may be anything
-            if (part == 0 && unit.part == 0) *delta_at = delta;
         }
         // A wait that gives up raises the abort flag: the loop then runs on over what there is, and
         // nothing is written at its end.
+        TileIter it(plan, n_tiles, first_tile);
+        uint64_t missing = 0;  // e, in pairs
         int n = 0;
-        for (int phase = exact ? 0 : 1; phase < 2; ++phase) {
-            TileIter it(plan, n_tiles, first_tile);
-            float sum = 0.f;
-            for (int j = it.next(); j >= 0; j = it.next(), ++n) {
-                const uint32_t dp_row = dp_tmem + part * 32 + lane_base;
-                wait_for(s_full, n & 1u, abort_flag);
-                tc_fence_after();
-                const int j0 = j * int(kAttnRows) + int(part) * 32;
-                float s[32];
-                uint64_t bend[kCap ? 16 : 1];
-                load_row<32>(tmem + part * 32 + lane_base, s);
-                warp_arrive(s_read);
-                const int pos = i + int(p.Sk) - int(p.Sq), pos0 = row0 + int(p.Sk) - int(p.Sq);
-                const int side = kBias ? bias_side(pos0, int(kAttnRows), j0, 32, p.causal && !p.prefix) : 1;
-                const float at = kBias && side != 0 ? less - float(side) * slope2 * float(pos - j0) : less;
-                const float by = float(side) * slope2;
-                const uint64_t at2 = f2_pack(at, at);
-                const ToWeight<kCap> weight(p, s);
-                auto weights = [&](auto linear) {
+        for (int j = it.next(); j >= 0; j = it.next(), ++n) {
+            const uint32_t s_row = tmem + part * 32 + lane_base, dp_row = dp_tmem + part * 32 + lane_base;
+            wait_for(s_full, n & 1u, abort_flag);
+            tc_fence_after();
+            const int j0 = j * int(kAttnRows) + int(part) * 32;
+            float s[32];
+            uint64_t bend[kCap ? 16 : 1];
+            load_row<32>(s_row, s);
+            const int pos = i + int(p.Sk) - int(p.Sq), pos0 = row0 + int(p.Sk) - int(p.Sq);
+            const int side = kBias ? bias_side(pos0, int(kAttnRows), j0, 32, p.causal && !p.prefix) : 1;
+            const float at = kBias && side != 0 ? less - float(side) * slope2 * float(pos - j0) : less;
+            const float by = float(side) * slope2;
+            const uint64_t at2 = f2_pack(at, at);
+            const ToWeight<kCap> weight(p, s);
+            auto weights = [&](auto linear) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        uint64_t add = at2;
-                        if constexpr (kBias && decltype(linear)::value)
-                            add = f2_pack(fmaf(float(x), by, at), fmaf(float(x + 1), by, at));
-                        else if constexpr (kBias)
-                            add = f2_pack(fmaf(-slope2, fabsf(float(pos - j0 - x)), less), fmaf(-slope2, fabsf(float(pos - j0 - x - 1)), less));
-                        f2_unpack(weight(f2_pack(s[x], s[x + 1]), add, bend[kCap ? x / 2 : 0]), s[x], s[x + 1]);
-                        s[x] = ex2(s[x]);
-                        s[x + 1] = ex2(s[x + 1]);
-                    }
-                };
-                if (!kBias || side != 0)
-                    weights(Bool<true>{});
-                else
-                    weights(Bool<false>{});
-                const bool whole = __all_sync(0xffffffffu, plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + 32 <= bound);
-                uint32_t bits[1] = {0xffffffffu};
-                if (!whole) {
-                    bits[0] = bound_bits(bound, j0);
-                    if (plan) {
-                        const int key = j0 + int(lane);
-                        const int32_t kd[1] = {key < int(p.Sk) ? __ldg(p.k_docs + int64_t(b) * p.Sk + key) : -1};
-                        keep_document(bits, kd, doc);
-                        // padding's K rows may hold anything: clear them for the product with dx
-                        if (quarter == 0 && kd[0] < 0) {
-                            uint4* k = reinterpret_cast<uint4*>(smem + (2 + key_stage(n)) * size_t(kTile) +
-                                                                (part * 32 + lane) * kSwizzleRow);
-                            for (int x = 0; x < kD / 64; ++x)
-                                for (int y = 0; y < 8; ++y) k[x * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async_shared();
-                    }
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) s[x] = (bits[0] >> x) & 1u ? s[x] : 0.f;
-                    if constexpr (kCap) {
-#pragma unroll
-                        for (int x = 0; x < 32; x += 2) bend[x / 2] = keep_pair(bend[x / 2], bits[0] >> x);
-                    }
+                for (int x = 0; x < 32; x += 2) {
+                    uint64_t add = at2;
+                    if constexpr (kBias && decltype(linear)::value)
+                        add = f2_pack(fmaf(float(x), by, at), fmaf(float(x + 1), by, at));
+                    else if constexpr (kBias)
+                        add = f2_pack(fmaf(-slope2, fabsf(float(pos - j0 - x)), less), fmaf(-slope2, fabsf(float(pos - j0 - x - 1)), less));
+                    f2_unpack(weight(f2_pack(s[x], s[x + 1]), add, bend[kCap ? x / 2 : 0]), s[x], s[x + 1]);
+                    s[x] = ex2(s[x]);
+                    s[x + 1] = ex2(s[x + 1]);
                 }
-                wait_for(dp_full, n & 1u, abort_flag);
-                tc_fence_after();
-                float d[32];
-                load_row<32>(dp_row, d);
-                if (!whole) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) d[x] = (bits[0] >> x) & 1u ? d[x] : 0.f;
-                }
-                if (phase == 0) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) sum = fmaf(s[x], d[x], sum);
-                } else {
-                    const uint64_t nd = f2_pack(-delta, -delta);
-#pragma unroll
-                    for (int x = 0; x < 32; x += 2) {
-                        uint64_t dx = f2_mul(f2_pack(s[x], s[x + 1]), f2_add(f2_pack(d[x], d[x + 1]), nd));
-                        if constexpr (kCap) dx = f2_mul(dx, bend[x / 2]);
-                        f2_unpack(dx, d[x], d[x + 1]);
+            };
+            if (!kBias || side != 0)
+                weights(Bool<true>{});
+            else
+                weights(Bool<false>{});
+            const bool whole = __all_sync(0xffffffffu, plan ? (__ldg(plan + words + (j >> 5)) >> (j & 31)) & 1u : j0 + 32 <= bound);
+            uint32_t bits[1] = {0xffffffffu};
+            if (!whole) {
+                bits[0] = bound_bits(bound, j0);
+                if (plan) {
+                    const int key = j0 + int(lane);
+                    const int32_t kd[1] = {key < int(p.Sk) ? __ldg(p.k_docs + int64_t(b) * p.Sk + key) : -1};
+                    keep_document(bits, kd, doc);
+                    // padding's K rows may hold anything: clear them for the product with dx
+                    if (quarter == 0 && kd[0] < 0) {
+                        uint4* k = reinterpret_cast<uint4*>(smem + (2 + key_stage(n)) * size_t(kTile) +
+                                                            (part * 32 + lane) * kSwizzleRow);
+                        for (int x = 0; x < kD / 64; ++x)
+                            for (int y = 0; y < 8; ++y) k[x * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
                     }
-                    store_row16<kF, 32>(dp_row, d);
-                    tc_wait_st();
+                    fence_async_shared();
                 }
-                warp_arrive(dx_full);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[x] = (bits[0] >> x) & 1u ? s[x] : 0.f;
+                if constexpr (kCap) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) bend[x / 2] = keep_pair(bend[x / 2], bits[0] >> x);
+                }
             }
-            if (phase == 0) {  // the four parts of the row
-                // meet in four columns of the accumulator, which nothing has written yet
-                tc_st1(dq_tmem + lane_base + part, __float_as_uint(sum));
-                tc_wait_st();
-                warp_arrive(sums_full);
-                wait_for(sums_full, 0, abort_flag);
-                tc_fence_after();
-                uint32_t part_sum[4];
-                tc_ld4(dq_tmem + lane_base, part_sum);
-                delta = (__uint_as_float(part_sum[0]) + __uint_as_float(part_sum[1])) +
-                        (__uint_as_float(part_sum[2]) + __uint_as_float(part_sum[3]));
-                tc_fence_before();
-                if (part == 0 && valid) *delta_at = delta;
+            if constexpr (kCap) {
+                float w[32];
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) f2_unpack(f2_mul(f2_pack(s[x], s[x + 1]), bend[x / 2]), w[x], w[x + 1]);
+                store_row16<kF, 32>(s_row, w);
+            } else {
+                store_row16<kF, 32>(s_row, s);
             }
+            tc_wait_st();
+            warp_arrive(p_full);
+            wait_for(dp_full, n & 1u, abort_flag);
+            tc_fence_after();
+            float d[32];
+            load_row<32>(dp_row, d);
+            if (!whole) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) d[x] = (bits[0] >> x) & 1u ? d[x] : 0.f;
+            }
+            const uint64_t nd = f2_pack(-delta, -delta);
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+                uint64_t dx = f2_mul(f2_pack(s[x], s[x + 1]), f2_add(f2_pack(d[x], d[x + 1]), nd));
+                missing = f2_add(missing, dx);
+                if constexpr (kCap) dx = f2_mul(dx, bend[x / 2]);
+                f2_unpack(dx, d[x], d[x + 1]);
+            }
+            store_row16<kF, 32>(dp_row, d);
+            tc_wait_st();
+            warp_arrive(dx_full);
         }
-        if (part < kD / 32) {
-            const bool ok = wait_for(done, 0, abort_flag);
-            if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
-                tc_fence_after();
-                const uint32_t from = dq_tmem + lane_base + part * 32;
-                if (unit.parts > 1)
-                    write_sums<32>(from, bp.dq_split.part + (int64_t(unit.slot) * kAttnRows + r) * kD + part * 32);
-                else
-                    write_row<kF, 32>(from, visits > 0, valid, p.scale,
-                                      p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h + part * 64);
+        // e of the row's four parts meets in columns of S, which no product reads any more
+        bool ok = wait_for(done, 0, abort_flag);
+        tc_fence_after();
+        float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
+        if (visits > 0) {
+            float lo, hi;
+            f2_unpack(missing, lo, hi);
+            tc_st1(tmem + lane_base + part, __float_as_uint(lo + hi));
+            tc_wait_st();
+            warp_arrive(sums_full);
+            ok = wait_for(sums_full, 0, abort_flag) && ok;
+            tc_fence_after();
+            uint32_t bits[4];
+            tc_ld4(tmem + lane_base, bits);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) part_sum[x] = __uint_as_float(bits[x]);
+        }
+        if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
+            const float e = (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+            const int64_t row = int64_t(unit.slot) * kAttnRows + r;  // of a part's sums
+            if (part == 0 && unit.parts > 1) bp.dq_split.stat[row] = make_float2(e, 0.f);
+            if (part == 0 && valid && unit.part == 0) *delta_at = unit.parts > 1 ? delta : delta + e;
+            if (part < kD / 32) {
+                const uint32_t from = lane_base + part * 32;
+                if (unit.parts > 1) {
+                    float* dst = bp.dq_split.part + row * kD + part * 32;
+                    write_sums<32>(dq_tmem + from, dst);
+                    write_sums<32>(w_tmem + from, dst + int64_t(gridDim.x - bp.dq_split.whole) * kAttnRows * kD);
+                } else {
+                    write_dq<kF>(dq_tmem + from, w_tmem + from, visits > 0, valid, e, p.scale,
+                                 p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h + part * 64);
+                }
             }
         }
     }
@@ -882,7 +909,7 @@ cudaError_t launch(const BackwardParams& p, cudaStream_t stream, int* launches) 
         if (e != cudaSuccess) return e;
         *launches += 1;
         if (cut.parts > 1) {
-            e = launch_join_gradient(p.a, cut, p.a.dq, cut.part, p.a.scale, p.q_tiles, p.a.Sq, p.a.Hl, kF == Fused::kBF16, stream);
+            e = launch_join_dq(p, kF == Fused::kBF16, stream);
             if (e != cudaSuccess) return e;
             *launches += 1;
         }

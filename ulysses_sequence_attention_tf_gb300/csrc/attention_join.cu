@@ -61,7 +61,38 @@ __global__ void __launch_bounds__(kJoinThreads) join_forward_kernel(const __grid
         p.lse[g][(int64_t(b) * p.Hl + h) * p.Sq + i] = (top == -INFINITY ? 0.f : top * kLn2) + logf(l);
 }
 
-// Gradients: the sum of the parts times `factor`.
+// dQ = scale * (sum of the parts' sums - e * sum of their W), e the sum of what they lack of delta.
+template <Fused kF, int kD>
+__global__ void __launch_bounds__(kJoinThreads) join_dq_kernel(const __grid_constant__ AttentionParams p, const Split s, uint32_t row_tiles,
+                                                               int64_t rows_in_parts) {
+    constexpr int kPer = kD / 32;
+    grid_dependency_wait();
+    const uint32_t lane = threadIdx.x % 32, at = blockIdx.x * kJoinRows + threadIdx.x / 32;
+    const uint32_t cut = at / kAttnRows, r = at % kAttnRows;
+    uint32_t u = s.whole + cut;
+    const uint32_t i = u % row_tiles * kAttnRows + r;
+    u /= row_tiles;
+    const uint32_t h = u % p.Hl, b = u / p.Hl % p.B, g = u / p.Hl / p.B;
+    if (i >= p.Sq) return;
+    float o[kPer] = {}, w[kPer] = {}, e = 0.f;
+    for (uint32_t c = 0; c < s.parts; ++c) {
+        const int64_t row = (int64_t(cut) * s.parts + c) * kAttnRows + r;
+        float v[kPer];
+        e += s.stat[row].x;
+        load_lane(v, s.part + row * kD, lane);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) o[x] += v[x];
+        load_lane(v, s.part + (rows_in_parts + row) * kD, lane);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) w[x] += v[x];
+    }
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) o[x] = fmaf(-e, w[x], o[x]) * p.scale;
+    store_lane<kF>(p.dq.base[g] + int64_t(b) * p.dq.b + int64_t(i) * p.dq.t + int64_t(h) * p.dq.h, lane, o);
+    if (lane == 0) p.delta[(int64_t(u) * p.Sq) + i] += e;
+}
+
+// dK, dV: the sum of the parts times `factor`.
 template <Fused kF, int kD>
 __global__ void __launch_bounds__(kJoinThreads) join_gradient_kernel(const __grid_constant__ GroupView out, const float* part,
                                                                      const Split s, float factor, uint32_t row_tiles, uint32_t rows,
@@ -98,6 +129,14 @@ cudaError_t forward(const ForwardParams& p, cudaStream_t stream) {
 cudaError_t launch_join_forward(const ForwardParams& p, bool bf16, cudaStream_t stream) {
     if (p.a.D == 64) return bf16 ? forward<Fused::kBF16, 64>(p, stream) : forward<Fused::kFP16, 64>(p, stream);
     return bf16 ? forward<Fused::kBF16, 128>(p, stream) : forward<Fused::kFP16, 128>(p, stream);
+}
+
+cudaError_t launch_join_dq(const BackwardParams& p, bool bf16, cudaStream_t stream) {
+    const AttentionParams& a = p.a;
+    const uint32_t cut = p.q_tiles * a.P * a.B * a.Hl - p.dq_split.whole, grid = cut * kAttnRows / kJoinRows;
+    auto kernel = a.D == 64 ? (bf16 ? join_dq_kernel<Fused::kBF16, 64> : join_dq_kernel<Fused::kFP16, 64>)
+                            : (bf16 ? join_dq_kernel<Fused::kBF16, 128> : join_dq_kernel<Fused::kFP16, 128>);
+    return launch_overlapped(kernel, grid, kJoinThreads, 0, stream, a, p.dq_split, p.q_tiles, int64_t(cut) * p.dq_split.parts * kAttnRows);
 }
 
 cudaError_t launch_join_gradient(const AttentionParams& p, const Split& s, const GroupView& out, const float* part, float factor,

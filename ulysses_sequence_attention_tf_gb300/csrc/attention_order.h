@@ -3,20 +3,21 @@
 //
 // A barrier tells the phase its waiter expects only by a bit.  It is sound where none can complete
 // two phases ahead of a waiter that still expects the first.  With S and dP once in TMEM:
-//   scores_read(i)  all rows hold S(i) in registers     -> S(i + 1) may be issued
-//   dx_written(i)   all rows have put dx(i) over dP(i)  -> dQ += dx(i) K, then dP(i + 1)
-// The rows arrive on scores_read(i + 1) after S(i + 1), on dx_written(i + 1) after dP(i + 1), and both
-// are issued only behind the wait for phase i of the same barrier.
+//   weights_written(i)  all rows hold S(i) in registers, P(i) over it  -> P(i) K, then S(i + 1)
+//   dx_written(i)       all rows have put dx(i) over dP(i)             -> dx(i) K, then dP(i + 1)
+// The rows arrive on weights_written(i + 1) after S(i + 1), on dx_written(i + 1) after dP(i + 1), and both
+// are issued only behind the wait for phase i of the same barrier.  While the pipe works on
+// one pair of products the rows compute what the other one takes.
 #pragma once
 
 #include <cstdint>
 
 namespace tfu {
 
-enum class DqBarrier { kScoresRead, kDxWritten };
+enum class DqBarrier { kWeightsWritten, kDxWritten };
 
-// Pipe: scores(i) and gradients(i) wait for tile i of K, of V and issue S(i), dP(i); update(i) issues
-// what takes dx(i); wait(barrier, parity).  False: a wait gave up.
+// Pipe: scores(i) and gradients(i) wait for tile i of K, of V and issue S(i), dP(i); weights(i) and update(i)
+// issue what takes P(i), dx(i); wait(barrier, parity).  False: a wait gave up.
 template <typename Pipe>
 #ifdef __CUDACC__
 __host__ __device__ __forceinline__
@@ -29,7 +30,9 @@ bool dq_order(int steps, Pipe& pipe) {
     for (int i = 0; i < steps; ++i) {
         const bool more = i + 1 < steps;
         const uint32_t parity = uint32_t(i) & 1u;
-        if (more && (!pipe.wait(DqBarrier::kScoresRead, parity) || !pipe.scores(i + 1))) return false;
+        if (!pipe.wait(DqBarrier::kWeightsWritten, parity)) return false;
+        pipe.weights(i);
+        if (more && !pipe.scores(i + 1)) return false;
         if (!pipe.wait(DqBarrier::kDxWritten, parity)) return false;
         pipe.update(i);
         if (more && !pipe.gradients(i + 1)) return false;

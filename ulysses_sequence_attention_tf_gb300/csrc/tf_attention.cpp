@@ -80,6 +80,7 @@ uint64_t units_of(const tf_attention& a, int tokens, uint32_t rows, int heads) {
 struct Workspace {
     tfu::Split forward{}, dq{}, dkv{};
     size_t delta = 0, plan = 0, key_plan = 0, parts = 0;  // bytes
+    size_t dq_sums = 0;                                   // of the parts: dQ's sums, the statistics behind them
     Workspace(const tf_attention& a, bool backward) {
         auto up = [](size_t n) { return (n + 15) / 16 * 16; };
         const uint32_t B = uint32_t(a.B), Sq = uint32_t(a.Sq), Sk = uint32_t(a.Sk), D = uint32_t(a.D);
@@ -99,7 +100,9 @@ struct Workspace {
         dq = tfu::plan_split(rows, k_tiles, even);
         dkv = tfu::plan_split(keys, q_tiles * uint32_t(a.H / a.Hkv), even);
         // one after the other in the same place
-        const size_t sums = tfu::kAttnRows * D * sizeof(float), first = cut(dq, rows) * sums, second = 2 * cut(dkv, keys) * sums;
+        const size_t sums = tfu::kAttnRows * D * sizeof(float);
+        dq_sums = 2 * cut(dq, rows) * sums;
+        const size_t first = dq_sums + cut(dq, rows) * tfu::kAttnRows * sizeof(float2), second = 2 * cut(dkv, keys) * sums;
         parts = first > second ? first : second;
     }
     size_t bytes() const { return delta + plan + key_plan + parts; }
@@ -228,6 +231,7 @@ TF_API tf_status tf_ulysses_attention_backward(const tf_attention* a, const void
     bp.dq_split = ws.dq;
     bp.dkv_split = ws.dkv;
     bp.dq_split.part = bp.dkv_split.part = reinterpret_cast<float*>(at + ws.delta + ws.plan + ws.key_plan);
+    if (bp.dq_split.parts > 1) bp.dq_split.stat = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bp.dq_split.part) + ws.dq_sums);
     bp.q_tiles = (p.Sq + tfu::kAttnRows - 1) / tfu::kAttnRows;
     bp.k_tiles = (p.Sk + tfu::kAttnRows - 1) / tfu::kAttnRows;
     bp.head_block = tfu::head_block(a->causal, uint64_t(a->B) * a->H, p.Sk, p.D);
