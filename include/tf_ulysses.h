@@ -418,7 +418,8 @@ TF_API tf_status tf_ulysses_attention(const tf_attention *a, const void *const *
  *  grad_strides host array of 3 tf_strides: dq, dk, dv (NULL = contiguous).
  *  workspace    as above, tf_ulysses_attention_workspace(a, 1) bytes.
  * Sums are fp32; the weights and the gradients of the scores are rounded to the I/O type for
- * the products with dout, K and Q, and the results once more.  The row sums of P dP are the kernel's
+ * the products with dout, K and Q (in fp16 times powers of two that keep them in its normal
+ * range), and the results once more.  The row sums of P dP are the kernel's
  * own: dout . out, which holds the rounding of out, is only where they start from.
  * There is no gradient of the slopes.  The same inputs give the same bits.
  */

@@ -110,3 +110,41 @@ def test_one_score_that_dominates(tf, D, dtype):
     q[0] += 3 * k[0]  # a query close to the key at its own position
     sharp(tf, q, k, v, dout)
     sharp(tf, q, k, v, dout, causal=True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("factor", [2.0 ** -14, 2.0 ** -10, 1.0, 2.0 ** 8])
+@pytest.mark.parametrize("Sq,Sk,kw", [(300, 6000, {}), (2500, 2500, dict(causal=True)), (2500, 2500, dict(softcap=3.0))])
+def test_fp16_gradients_of_any_size(tf, Sq, Sk, kw, factor, D):
+    """Gradients of the scores are about |dout| / Sk: far below fp16's normal range, or (times large values) above it.
+    dout is a multiple of 2^-2 below 4, exact in fp16 times each factor."""
+    gen = torch.Generator(device="cuda").manual_seed(67)
+    q, k, v = (rows(gen, 1, S, 2, D, FP16) for S in (Sq, Sk, Sk))
+    dout = [(4 * t).round().clamp(-15, 15) / 4 * factor for t in rows(gen, 1, Sq, 2, D, FP16)]
+    if factor > 1:
+        v = [64 * t for t in v]
+        k = [t / 16 for t in k]  # dQ stays within fp16
+    out, lse = tf.attention(q, k, v, **kw)
+    dq, dk, dv = tf.attention_backward(dout, q, k, v, out, lse, **kw)
+    # dx is kept times a power of two that puts |dout| |v| at 2^13 or above; below fp16's normal range a
+    # rounding is off by 2^-25 at most
+    flush = 2.0 ** -38 * max(float(t.double().norm(dim=-1).max()) for t in dout) * max(float(t.double().norm(dim=-1).max()) for t in v)
+    ref = Gradients(q, k, v, dout, out, flush=flush, **kw)
+    ref.check("dq", dq)
+    ref.check("dk", dk)
+    assert dv[0].isfinite().all()
+
+
+def test_fp16_padding_has_no_part_in_the_gradients_size(tf):
+    gen = torch.Generator(device="cuda").manual_seed(68)
+    q, k, v, dout = (rows(gen, 1, 900, 2, 64, FP16) for _ in range(4))
+    dout = [t * 2.0 ** -9 for t in dout]
+    docs = torch.tensor([[0] * 700 + [-1] * 200], dtype=torch.int32, device="cuda")
+    kw = dict(q_docs=docs, k_docs=docs)
+    got = []
+    for value in (0.0, 60000.0, math.inf, math.nan):
+        for ts in (q, k, v, dout):
+            ts[0][:, 700:] = value
+        out, lse = tf.attention(q, k, v, **kw)
+        got.append(tf.attention_backward(dout, q, k, v, out, lse, **kw))
+        assert all(torch.equal(a, b) for x, y in zip(got[0], got[-1]) for a, b in zip(x, y)), value

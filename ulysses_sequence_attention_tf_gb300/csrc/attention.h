@@ -95,6 +95,7 @@ struct BackwardParams {
     GroupMaps q_half, dout_half;  // boxes of 64
     AttentionParams a;
     uint32_t* key_plan;           // with documents: row tiles of keys (a.plan: of 128 queries)
+    float* sizes;                 // fp16: largest |dO|^2 by head and q_tile, then |V|^2 by key head and k_tile
     uint32_t q_tiles, k_tiles;    // of kAttnRows rows
     uint32_t head_block, key_head_block;
     Split dq_split, dkv_split;

@@ -22,6 +22,11 @@
 // one product more, whose roundings count only times e_i.  It hands d0 + e to dkv_kernel.
 // Eight products are executed where five would do.
 //
+// fp16: dx of a long row is about |dO| |V| / Sk and would fall into the subnormals, so it is kept times a power of
+// two: |dx| <= P |dO_i| 2 max_j |V_j|, of which sizes_kernel finds the parts in front, and lift puts that
+// bound below 2^15.  dq_kernel takes a factor for each row, dkv_kernel, which sums over them, one for its key head.
+// P is kept times 2^8 for the same reason.
+//
 // P and dx are rounded to the I/O type as operands (one MMA takes A and B of one type; a second product
 // for the rest would cost a seventh more for each): with bf16 that adds about 0.0017 of the norm to
 // gradients whose own rounding is as large.
@@ -138,9 +143,10 @@ __device__ __forceinline__ void write_row(uint32_t taddr, bool any, bool valid, 
     }
 }
 
-// 32 columns of dQ: factor * (sums - e * weights)
+// 32 columns of dQ: factor * (back * sums - e * weights)
 template <Fused kF>
-__device__ __forceinline__ void write_dq(uint32_t sums, uint32_t weights, bool any, bool valid, float e, float factor, uint8_t* dst) {
+__device__ __forceinline__ void write_dq(uint32_t sums, uint32_t weights, bool any, bool valid, float back, float e, float factor,
+                                         uint8_t* dst) {
     float a[32] = {}, w[32] = {};
     if (any) {
         load_row<32>(sums, a);
@@ -151,14 +157,15 @@ __device__ __forceinline__ void write_dq(uint32_t sums, uint32_t weights, bool a
         uint32_t o[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z)
-            o[z] = pack2<kF>(fmaf(-e, w[x + 2 * z], a[x + 2 * z]) * factor, fmaf(-e, w[x + 2 * z + 1], a[x + 2 * z + 1]) * factor);
+            o[z] = pack2<kF>(fmaf(-e, w[x + 2 * z], a[x + 2 * z] * back) * factor,
+                             fmaf(-e, w[x + 2 * z + 1], a[x + 2 * z + 1] * back) * factor);
         if (valid) *reinterpret_cast<uint4*>(dst + x * 2) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
-// accumulator columns in fp32, for a part of a unit
+// accumulator columns times `factor` in fp32, for a part of a unit
 template <int kCols>
-__device__ __forceinline__ void write_sums(uint32_t taddr, float* dst) {
+__device__ __forceinline__ void write_sums(uint32_t taddr, float factor, float* dst) {
 #pragma unroll 1
     for (int x = 0; x < kCols; x += 32) {
         uint32_t r[32];
@@ -166,14 +173,16 @@ __device__ __forceinline__ void write_sums(uint32_t taddr, float* dst) {
         tc_wait_ld();
         tc_landed(r);
 #pragma unroll
+        for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * factor);
+#pragma unroll
         for (int y = 0; y < 32; y += 4) *reinterpret_cast<uint4*>(dst + x + y) = make_uint4(r[y], r[y + 1], r[y + 2], r[y + 3]);
     }
 }
 
-// sum_d a_d b_d of two 16-bit rows
+// sum_d a_d b_d of two 16-bit rows; squares: sum_d a_d^2
 template <Fused kF, int kD>
-__device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b) {
-    float s = 0.f;
+__device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b, float& squares) {
+    float s = 0.f, t = 0.f;
 #pragma unroll 4
     for (int x = 0; x < kD / 8; ++x) {
         const uint4 u = __ldg(reinterpret_cast<const uint4*>(a) + x), v = __ldg(reinterpret_cast<const uint4*>(b) + x);
@@ -186,10 +195,81 @@ __device__ __forceinline__ float row_dot(const uint8_t* a, const uint8_t* b) {
             unpack2<kF>(vw[y], b0, b1);
             s = fmaf(a0, b0, s);
             s = fmaf(a1, b1, s);
+            t = fmaf(a0, a0, t);
+            t = fmaf(a1, a1, t);
         }
     }
+    squares = t;
     return s;
 }
+
+// ---------------------------------------------------------------- fp16: sizes
+// The largest |dO_i|^2 of every query row tile of a head, then the largest |V_j|^2 of every key
+// tile of a key head; padding left out.  A CTA a tile, D / 8 lanes a row.
+constexpr int kSizeThreads = 256;
+template <int kD>
+__global__ void __launch_bounds__(kSizeThreads) sizes_kernel(const __grid_constant__ BackwardParams bp) {
+    constexpr uint32_t kLanes = kD / 8, kPass = kSizeThreads / kLanes;
+    const AttentionParams& p = bp.a;
+    __shared__ float most_of[kSizeThreads / 32];
+    grid_dependency_wait();
+    const uint32_t q_units = bp.q_tiles * p.P * p.B * p.Hl;
+    const bool keys = blockIdx.x >= q_units;
+    const uint32_t tiles = keys ? bp.k_tiles : bp.q_tiles, heads = keys ? p.Hkl : p.Hl, tokens = keys ? p.Sk : p.Sq;
+    uint32_t u = keys ? blockIdx.x - q_units : blockIdx.x;
+    const uint32_t row0 = u % tiles * kAttnRows;
+    u /= tiles;
+    const uint32_t h = u % heads, b = u / heads % p.B, g = u / heads / p.B;
+    const GroupView& view = keys ? p.v : p.dout;
+    const int32_t* docs = keys ? p.k_docs : p.q_docs;
+    const uint8_t* base = view.base[g] + int64_t(b) * view.b + int64_t(h) * view.h + threadIdx.x % kLanes * 16;
+    float most = 0.f;
+#pragma unroll
+    for (uint32_t x = 0; x < kAttnRows / kPass; ++x) {
+        const uint32_t i = row0 + x * kPass + threadIdx.x / kLanes;
+        float t = 0.f;
+        if (i < tokens && !(docs && docs[int64_t(b) * tokens + i] < 0)) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(base + int64_t(i) * view.t));
+            const uint32_t* v = &w.x;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                float a0, a1;
+                unpack2<Fused::kFP16>(v[y], a0, a1);
+                t = fmaf(a0, a0, t);
+                t = fmaf(a1, a1, t);
+            }
+        }
+#pragma unroll
+        for (uint32_t m = 1; m < kLanes; m <<= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+        most = fmaxf(most, t);  // passes over NaN
+    }
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    if (threadIdx.x % 32 == 0) most_of[threadIdx.x / 32] = most;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_of[threadIdx.x % (kSizeThreads / 32)])));
+    if (threadIdx.x == 0) bp.sizes[blockIdx.x] = most;
+}
+
+// The largest of n sizes, for a whole warp.
+__device__ __forceinline__ float largest_of(const float* sizes, uint32_t n) {
+    float most = 0.f;
+    for (uint32_t x = threadIdx.x % 32; x < n; x += 32) most = fmaxf(most, __ldg(sizes + x));
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+}
+
+// 2^k with 2^k |dO| |V| in [2^13, 2^14), from the squares of the two; 1 where that is 0 or not finite.
+__device__ __forceinline__ float lift(float out_squares, float value_squares) {
+    const float t = sqrtf(out_squares) * sqrtf(value_squares);
+    const int e = int(__float_as_uint(t) >> 23) - 127;
+    return t > 0.f && t <= kFltMax ? __uint_as_float(uint32_t(13 - e + 127) << 23) : 1.0f;
+}
+
+// fp16: what the exponent of P is raised by, and the factor that takes it back
+template <Fused kF>
+struct Raised {
+    static constexpr float kUp = kF == Fused::kFP16 ? 8.0f : 0.0f, kDown = kF == Fused::kFP16 ? 0x1p-8f : 1.0f;
+};
 
 // ---------------------------------------------------------------- dQ
 // One CTA: 128 query rows of one head, tiles of 128 keys.
@@ -212,6 +292,7 @@ struct DqShape {
 template <Fused kF, int kD, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant__ BackwardParams bp) {
     using S = DqShape<kD>;
+    constexpr float kUp = Raised<kF>::kUp, kDown = Raised<kF>::kDown;
     constexpr uint32_t kTile = S::kTile;
     constexpr uint32_t kStages = S::kStages;
     const AttentionParams& p = bp.a;
@@ -236,6 +317,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
     const uint32_t qt = p.causal ? bp.q_tiles - 1 - th.tile : th.tile;
     const uint32_t h = th.head % p.Hl, b = th.head / p.Hl % p.B, g = th.head / p.Hl / p.B;
     const int row0 = int(qt * kAttnRows);
+    const float* value_sizes = bp.sizes + size_t(bp.q_tiles) * p.P * p.B * p.Hl + size_t(th.head / p.shared) * bp.k_tiles;
 
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < kStages; ++s) {
@@ -373,18 +455,20 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
         const int64_t stat = (int64_t(b) * p.Hl + h) * p.Sq + (valid ? i : 0);
         float* delta_at = p.delta + int64_t(g) * p.B * p.Hl * p.Sq + stat;
         const float lse = valid ? p.lse[g][stat] : 0.f;
-        const float less = lse == -INFINITY ? 0.f : -lse * kLog2e, slope2 = slope * kLog2e;
+        const float less = kUp - (lse == -INFINITY ? 0.f : lse * kLog2e), slope2 = slope * kLog2e;
         const int64_t at = valid ? i : 0;
-        float delta = 0.f;  // d0
+        float delta = 0.f, squares = 0.f;  // d0, |dO|^2
         if (visits > 0 && valid) {
             delta = row_dot<kF, kD>(p.dout.base[g] + b * p.dout.b + at * p.dout.t + h * p.dout.h,
-                                    p.out.base[g] + b * p.out.b + at * p.out.t + h * p.out.h);
+                                    p.out.base[g] + b * p.out.b + at * p.out.t + h * p.out.h, squares);
             if (p.plan && doc < 0) delta = 0.f;  // padding: its output gradient may be anything
         }
+        // dx is kept times up, from P times 2^kUp
+        const float up = kF == Fused::kFP16 && visits > 0 ? lift(squares, largest_of(value_sizes, bp.k_tiles)) : 1.0f, down = up * kDown;
         // A wait that gives up raises the abort flag: the loop then runs on over what there is, and
         // nothing is written at its end.
         TileIter it(plan, n_tiles, first_tile);
-        uint64_t missing = 0;  // e, in pairs
+        uint64_t missing = 0;  // e times up, in pairs
         int n = 0;
         for (int j = it.next(); j >= 0; j = it.next(), ++n) {
             const uint32_t s_row = tmem + part * 32 + lane_base, dp_row = dp_tmem + part * 32 + lane_base;
@@ -459,10 +543,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
 #pragma unroll
                 for (int x = 0; x < 32; ++x) d[x] = (bits[0] >> x) & 1u ? d[x] : 0.f;
             }
-            const uint64_t nd = f2_pack(-delta, -delta);
+            const float off = kF == Fused::kFP16 ? -delta * down : -delta;
+            const uint64_t nd = f2_pack(off, off), down2 = f2_pack(down, down);
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-                uint64_t dx = f2_mul(f2_pack(s[x], s[x + 1]), f2_add(f2_pack(d[x], d[x + 1]), nd));
+                const uint64_t d2 = f2_pack(d[x], d[x + 1]);
+                uint64_t dx = f2_mul(f2_pack(s[x], s[x + 1]), kF == Fused::kFP16 ? f2_fma(d2, down2, nd) : f2_add(d2, nd));
                 missing = f2_add(missing, dx);
                 if constexpr (kCap) dx = f2_mul(dx, bend[x / 2]);
                 f2_unpack(dx, d[x], d[x + 1]);
@@ -489,7 +575,8 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
             for (int x = 0; x < 4; ++x) part_sum[x] = __uint_as_float(bits[x]);
         }
         if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
-            const float e = (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+            const float back = 1.0f / up;  // exact
+            const float e = ((part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3])) * back;
             const int64_t row = int64_t(unit.slot) * kAttnRows + r;  // of a part's sums
             if (part == 0 && unit.parts > 1) bp.dq_split.stat[row] = make_float2(e, 0.f);
             if (part == 0 && valid && unit.part == 0) *delta_at = unit.parts > 1 ? delta : delta + e;
@@ -497,10 +584,10 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
                 const uint32_t from = lane_base + part * 32;
                 if (unit.parts > 1) {
                     float* dst = bp.dq_split.part + row * kD + part * 32;
-                    write_sums<32>(dq_tmem + from, dst);
-                    write_sums<32>(w_tmem + from, dst + int64_t(gridDim.x - bp.dq_split.whole) * kAttnRows * kD);
+                    write_sums<32>(dq_tmem + from, back, dst);
+                    write_sums<32>(w_tmem + from, kDown, dst + int64_t(gridDim.x - bp.dq_split.whole) * kAttnRows * kD);
                 } else {
-                    write_dq<kF>(dq_tmem + from, w_tmem + from, visits > 0, valid, e, p.scale,
+                    write_dq<kF>(dq_tmem + from, w_tmem + from, visits > 0, valid, back, e * kDown, p.scale,
                                  p.dq.base[g] + b * p.dq.b + at * p.dq.t + h * p.dq.h + part * 64);
                 }
             }
@@ -525,8 +612,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dq_kernel(const __grid_constant_
 //  * warps 18 and 19: the queries' log-sum-exp, delta, bounds and documents into shared memory.
 //  * warps 0-3 and 8-11 take the even blocks, warps 4-7 and 12-15 the odd ones: a thread per
 //    key row and half of the block's queries.
-// P goes over S, dx over dP, both in 16 bits.  fp16: P is kept times 2^8, away from
-// fp16's subnormals (weights of a long row are about 1 / Sk).
+// P goes over S, dx over dP, both in 16 bits.
 // TMEM: S0 dP0 S1 dP1 (64 columns each), dK, dV (D columns each).
 constexpr uint32_t kQueries = 64;
 constexpr int kStatSlots = 4;
@@ -534,7 +620,7 @@ constexpr int kStatSlots = 4;
 // What a block's columns need of their queries.
 struct QueryStats {
     float less[kQueries];   // -lse2 (fp16: + 8) and the query's part of the bias
-    float delta[kQueries];  // -delta (fp16: * 2^-8)
+    float delta[kQueries];  // -delta (fp16: times what dx is kept times, and 2^-8)
     int bound[kQueries], doc[kQueries];
 };
 
@@ -596,7 +682,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     using S = DkvShape<kD>;
     constexpr uint32_t kTile = S::kTile, kBlock = S::kBlock, kHalfBlock = S::kHalfBlock;
     constexpr int kStages = S::kStages;
-    constexpr float kUp = kF == Fused::kFP16 ? 8.0f : 0.0f, kDown = kF == Fused::kFP16 ? 0x1p-8f : 1.0f;
+    constexpr float kUp = Raised<kF>::kUp, kDown = Raised<kF>::kDown;
     const AttentionParams& p = bp.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -655,6 +741,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
     const uint32_t per_head = blocks_of(plan, first, q_tiles, int(p.Sq));
     const uint32_t first_block = uint32_t(unit.begin(int(p.shared * per_head)));
     const uint32_t blocks = uint32_t(unit.end(int(p.shared * per_head))) - first_block;
+    // dx is kept times up, from P times 2^kUp: one factor for all queries of the key head
+    float up = 1.0f;
+    if (kF == Fused::kFP16 && blocks > 0)
+        up = lift(largest_of(bp.sizes + size_t(th.head) * p.shared * q_tiles, p.shared * q_tiles),
+                  largest_of(bp.sizes + size_t(q_tiles) * p.P * p.B * p.Hl + size_t(th.head) * bp.k_tiles, bp.k_tiles));
+    const float down = up * kDown;
     BlockIter it(plan, first, q_tiles, int(p.Sq), per_head, first_block, blocks);
 
     if (warp >= 16) {
@@ -739,7 +831,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
                 doc[x] = -1;
                 if (i < int(p.Sq)) {
                     const float lse = p.lse[g][stat + i];
-                    delta[x] = -kDown * p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat + i];
+                    delta[x] = -down * p.delta[int64_t(g) * p.B * p.Hl * p.Sq + stat + i];
                     bound[x] = key_bound(p, b, i);
                     if (plan) {
                         doc[x] = p.q_docs[int64_t(b) * p.Sq + i];
@@ -787,7 +879,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
             const int side = kBias ? bias_side(i0 + ahead, int(kQueries), row0, int(kAttnRows), p.causal && !p.prefix) : 0;
             // the query's part of the bias counts from the block's first one
             const float far = float(i0 + int(32 * half) + ahead - j), own = -float(side) * slope2 * float(i0 + ahead - j);
-            const uint64_t own2 = f2_pack(own, own), down2 = f2_pack(kDown, kDown);
+            const uint64_t own2 = f2_pack(own, own), down2 = f2_pack(down, down);
             float s[32], d[32];
             load_row<32>(s_row, s);
             const ToWeight<kCap> weight(p, s);
@@ -873,11 +965,11 @@ __global__ void __launch_bounds__(kThreadsB, 1) dkv_kernel(const __grid_constant
             if (unit.parts > 1) {
                 const int64_t cut = int64_t(bp.k_tiles) * p.P * p.B * p.Hkl - bp.dkv_split.whole;  // units in parts
                 const int64_t row = (t == 0 ? cut * unit.parts + unit.slot : int64_t(unit.slot)) * kAttnRows + r;
-                write_sums<kCols>(from, bp.dkv_split.part + row * kD + half * kCols);
+                write_sums<kCols>(from, t == 0 ? 1.0f : 1.0f / up, bp.dkv_split.part + row * kD + half * kCols);
             } else if (t == 0) {
                 write_row<kF, kCols>(from, n > 0, valid, kDown, p.dv.base[g] + b * p.dv.b + at * p.dv.t + kh * p.dv.h + half * kCols * 2);
             } else {
-                write_row<kF, kCols>(from, n > 0, valid, p.scale,
+                write_row<kF, kCols>(from, n > 0, valid, p.scale / up,
                                      p.dk.base[g] + b * p.dk.b + at * p.dk.t + kh * p.dk.h + half * kCols * 2);
             }
         }
@@ -895,6 +987,11 @@ template <Fused kF, int kD, bool kCap, bool kBias>
 cudaError_t launch(const BackwardParams& p, cudaStream_t stream, int* launches) {
     cudaError_t e;
     BackwardParams q = p;
+    if (kF == Fused::kFP16 && p.a.Sq > 0 && p.a.Sk > 0) {
+        const uint32_t tiles = p.q_tiles * p.a.P * p.a.B * p.a.Hl + p.k_tiles * p.a.P * p.a.B * p.a.Hkl;
+        if ((e = launch_overlapped(sizes_kernel<kD>, tiles, kSizeThreads, 0, stream, p)) != cudaSuccess) return e;
+        *launches += 1;
+    }
     if (p.a.Sq > 0) {
         if (p.a.plan) {
             if ((e = launch_plan(p.a, p.a.plan, false, kAttnRows, stream)) != cudaSuccess) return e;
@@ -930,7 +1027,7 @@ cudaError_t launch(const BackwardParams& p, cudaStream_t stream, int* launches) 
         *launches += 1;
         if (cut.parts > 1) {
             const float* dv_part = cut.part + int64_t(units - cut.whole) * cut.parts * kAttnRows * kD;
-            constexpr float kDown = kF == Fused::kFP16 ? 0x1p-8f : 1.0f;
+            constexpr float kDown = Raised<kF>::kDown;
             e = launch_join_gradient(p.a, cut, p.a.dk, cut.part, p.a.scale, p.k_tiles, p.a.Sk, p.a.Hkl, kF == Fused::kBF16, stream);
             if (e == cudaSuccess)
                 e = launch_join_gradient(p.a, cut, p.a.dv, dv_part, kDown, p.k_tiles, p.a.Sk, p.a.Hkl, kF == Fused::kBF16, stream);

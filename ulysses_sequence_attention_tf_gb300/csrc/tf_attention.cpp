@@ -79,7 +79,7 @@ uint64_t units_of(const tf_attention& a, int tokens, uint32_t rows, int heads) {
 // multiple of 16 bytes.
 struct Workspace {
     tfu::Split forward{}, dq{}, dkv{};
-    size_t delta = 0, plan = 0, key_plan = 0, parts = 0;  // bytes
+    size_t delta = 0, plan = 0, key_plan = 0, sizes = 0, parts = 0;  // bytes
     size_t dq_sums = 0;                                   // of the parts: dQ's sums, the statistics behind them
     Workspace(const tf_attention& a, bool backward) {
         auto up = [](size_t n) { return (n + 15) / 16 * 16; };
@@ -97,6 +97,7 @@ struct Workspace {
         if (docs) key_plan = up(tfu::tile_plan(Sk, tfu::kAttnRows, Sq).bytes(B));
         delta = up(size_t(B) * size_t(a.H) * Sq * sizeof(float));
         const uint64_t rows = units_of(a, a.Sq, tfu::kAttnRows, a.H), keys = units_of(a, a.Sk, tfu::kAttnRows, a.Hkv);
+        if (a.dtype == TF_FP16 && Sq > 0 && Sk > 0) sizes = up(size_t(rows + keys) * sizeof(float));
         dq = tfu::plan_split(rows, k_tiles, even);
         dkv = tfu::plan_split(keys, q_tiles * uint32_t(a.H / a.Hkv), even);
         // one after the other in the same place
@@ -105,7 +106,7 @@ struct Workspace {
         const size_t first = dq_sums + cut(dq, rows) * tfu::kAttnRows * sizeof(float2), second = 2 * cut(dkv, keys) * sums;
         parts = first > second ? first : second;
     }
-    size_t bytes() const { return delta + plan + key_plan + parts; }
+    size_t bytes() const { return delta + plan + key_plan + sizes + parts; }
 };
 
 size_t workspace_bytes_of(const tf_attention& a, bool backward) { return Workspace(a, backward).bytes(); }
@@ -228,9 +229,10 @@ TF_API tf_status tf_ulysses_attention_backward(const tf_attention* a, const void
     p.delta = reinterpret_cast<float*>(at);
     p.plan = ws.plan > 0 ? reinterpret_cast<uint32_t*>(at + ws.delta) : nullptr;
     bp.key_plan = ws.plan > 0 ? reinterpret_cast<uint32_t*>(at + ws.delta + ws.plan) : nullptr;
+    bp.sizes = reinterpret_cast<float*>(at + ws.delta + ws.plan + ws.key_plan);
     bp.dq_split = ws.dq;
     bp.dkv_split = ws.dkv;
-    bp.dq_split.part = bp.dkv_split.part = reinterpret_cast<float*>(at + ws.delta + ws.plan + ws.key_plan);
+    bp.dq_split.part = bp.dkv_split.part = reinterpret_cast<float*>(at + ws.delta + ws.plan + ws.key_plan + ws.sizes);
     if (bp.dq_split.parts > 1) bp.dq_split.stat = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bp.dq_split.part) + ws.dq_sums);
     bp.q_tiles = (p.Sq + tfu::kAttnRows - 1) / tfu::kAttnRows;
     bp.k_tiles = (p.Sk + tfu::kAttnRows - 1) / tfu::kAttnRows;
