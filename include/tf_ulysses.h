@@ -379,7 +379,7 @@ typedef struct tf_attention {
     int H, Hkv, D;         /* heads over all groups: Hkv % P == 0, H % Hkv == 0; D is 64 or 128 */
     tf_dtype dtype;        /* TF_BF16 or TF_FP16 */
     float scale;           /* finite; 1/sqrt(D) as a rule */
-    float softcap;         /* >= 0, finite; 0: scores are not capped */
+    float softcap;         /* >= 0; 0: scores are not capped.  Else at most 2^127, and scale / softcap 0 or a normal fp32 number */
     int causal;            /* 0 or 1 */
     const float *slopes;   /* device [H] (H over all groups), or NULL: no bias.  Finite, read-only */
     const int32_t *prefix; /* device [B], or NULL; needs causal */

@@ -138,3 +138,23 @@ def test_a_call_on_a_stream_takes_the_streams_device(tf, monkeypatch, name):
         called, args = tf._run(name, stream, ("before",), ("after",))
         assert called == name and args == ("before", device, 1001 * device + 1000, "after")
     assert current == [0]
+
+
+@pytest.mark.parametrize("kw", [dict(softcap=1e-40), dict(softcap=2.0 ** -127, scale=4.0), dict(softcap=3e38), dict(softcap=1e38, scale=1e-3),
+                                dict(softcap=1e-45, scale=-1.0), dict(softcap=1e38, scale=1.0)])
+def test_caps_out_of_the_kernels_range_refused(tf, kw):
+    """Scores are divided by the cap as scale / softcap, in fp32."""
+    a = describe(tf, **kw)
+    n = ctypes.c_size_t()
+    assert forward(tf, a) == 4 and backward(tf, a) == 4
+    assert tf.lib().tf_ulysses_attention_workspace(ctypes.byref(a), 0, ctypes.byref(n)) == 4
+    c = tf.KvCache(FAKE, FAKE, FAKE, FAKE, 8, 2, 16, 64, 2, 4, FAKE, 4, FAKE, FAKE)
+    a = tf.KvAttention(2, 8, 8, 1, 8, 64, kw.get("scale", 0.125), kw["softcap"], 1, None)
+    assert tf.lib().tf_ulysses_kv_attend_workspace(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)) == 4
+
+
+@pytest.mark.parametrize("kw", [dict(softcap=1e-30), dict(softcap=1e30), dict(softcap=1e38, scale=2.0), dict(softcap=1e-38, scale=0.0),
+                                dict(softcap=1e-37, scale=-0.5)])
+def test_caps_in_the_kernels_range(tf, kw):
+    a, n = describe(tf, **kw), ctypes.c_size_t()
+    assert tf.lib().tf_ulysses_attention_workspace(ctypes.byref(a), 1, ctypes.byref(n)) == 0

@@ -148,3 +148,22 @@ def test_fp16_padding_has_no_part_in_the_gradients_size(tf):
         out, lse = tf.attention(q, k, v, **kw)
         got.append(tf.attention_backward(dout, q, k, v, out, lse, **kw))
         assert all(torch.equal(a, b) for x, y in zip(got[0], got[-1]) for a, b in zip(x, y)), value
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,scale", [(1e-12, 1.0), (1e-30, 0.125), (1e-37, 0.125), (1e27, 1e30), (1e30, 0.125), (1e38, 2.0)])
+def test_caps_of_any_size_over_scores_of_zero(tf, cap, scale, D):
+    """The cap's polynomial takes factors of scale and cap; rows of zeros weigh all of their keys alike."""
+    gen = torch.Generator(device="cuda").manual_seed(69)
+    k, v, dout = (rows(gen, 1, 400, 2, D, BF16) for _ in range(3))
+    q = [torch.zeros_like(t) for t in dout]
+    out, lse = tf.attention(q, k, v, softcap=cap, scale=scale)
+    Reference(q, k, v, softcap=0.0, scale=0.0).check("out", out)
+    assert bool(((lse[0] - math.log(400)).abs() <= 2.0 ** -16).all())
+    if cap >= 1e30:  # scores far below the cap: as without one
+        q = rows(gen, 1, 400, 2, D, BF16)
+        out, lse = tf.attention(q, k, v, softcap=cap, scale=scale)
+        ref = Reference(q, k, v, dout, scale=scale)
+        ref.check("out", out)
+        for name, got in zip(("dq", "dk", "dv"), tf.attention_backward(dout, q, k, v, out, lse, softcap=cap, scale=scale)):
+            ref.check(name, got)

@@ -343,9 +343,9 @@ __device__ __forceinline__ bool fold_capped_tile(float (&s)[128], float scale, f
     const float far = fmaxf(fabsf(top), fabsf(low)) * to_x;
     if (!__all_sync(0xffffffffu, far <= kTanhNear)) return false;
     auto both = [](float v) { return f2_pack(v, v); };
-    if (__all_sync(0xffffffffu, far <= kTanhNearest && (!kRaw || to_x >= 0x1p-16f))) {
-        const float unit = kRaw ? to_x : 1.0f, a0 = to_z * unit * kTanhNearest0, a1 = to_z * unit * unit * unit * kTanhNearest1,
-                    a2 = to_z * unit * unit * unit * unit * unit * kTanhNearest2;
+    const float unit = kRaw ? to_x : 1.0f, a2 = to_z * unit * unit * unit * unit * unit * kTanhNearest2;
+    if (__all_sync(0xffffffffu, far <= kTanhNearest && (!kRaw || (to_x >= 0x1p-16f && a2 <= kFltMax)))) {
+        const float a0 = to_z * unit * kTanhNearest0, a1 = to_z * unit * unit * unit * kTanhNearest1;
         const float x = kRaw ? top : top * to_x, y = x * x;
         move_reference<kD>(x * fmaf(y, fmaf(y, a2, a1), a0), down, started, m, l, o_row);
         const uint64_t nb = both(m == -INFINITY ? 0.f : -m), b0 = both(a0), b1 = both(a1), b2 = both(a2), x2 = both(to_x);

@@ -39,6 +39,9 @@ tf_status check_ptrs(const char* what, const void* const* a, int P);
 // strides of a [nb, nt, nh, D] view; a stride of an extent-1 dimension is never used
 tf_status check_strides(const char* what, const tf_strides& s, int esize, int64_t nb, int64_t nt, int64_t nh);
 
+// scale and cap of attention scores
+tf_status check_scores(float scale, float softcap);
+
 void count_launches(int n);
 uint64_t launch_count();
 const char* last_error();

@@ -7,6 +7,16 @@
 
 using namespace tfu::host;
 
+tf_status tfu::host::check_scores(float scale, float softcap) {
+    if (!std::isfinite(scale)) return fail(TF_ERR_INVALID, "scale must be finite");
+    if (!std::isfinite(softcap) || softcap < 0) return fail(TF_ERR_INVALID, "softcap must be finite and >= 0");
+    if (softcap == 0) return TF_OK;
+    const float to_x = scale / softcap;
+    if ((to_x != 0 && !std::isnormal(to_x)) || softcap > 0x1p127f)
+        return fail(TF_ERR_UNSUPPORTED, "softcap=%g: scale / softcap must be 0 or a normal fp32 number, softcap at most 2^127", double(softcap));
+    return TF_OK;
+}
+
 namespace {
 
 tf_status check_attention(const tf_attention* a) {
@@ -21,8 +31,8 @@ tf_status check_attention(const tf_attention* a) {
     if (a->dtype != TF_BF16 && a->dtype != TF_FP16)
         return fail(TF_ERR_UNSUPPORTED, "attention needs bf16 or fp16 (dtype %d)", int(a->dtype));
     if (a->D != 64 && a->D != 128) return fail(TF_ERR_UNSUPPORTED, "attention is built for D in {64, 128}, not %d", a->D);
-    if (!std::isfinite(a->scale)) return fail(TF_ERR_INVALID, "scale must be finite");
-    if (!std::isfinite(a->softcap) || a->softcap < 0) return fail(TF_ERR_INVALID, "softcap must be finite and >= 0");
+    const tf_status s = check_scores(a->scale, a->softcap);
+    if (s != TF_OK) return s;
     if (a->causal != 0 && a->causal != 1) return fail(TF_ERR_INVALID, "causal=%d is neither 0 nor 1", a->causal);
     if (a->prefix && !a->causal) return fail(TF_ERR_INVALID, "a prefix needs the causal mask");
     if (!a->q_docs != !a->k_docs) return fail(TF_ERR_INVALID, "q_docs and k_docs are given together or not at all");

@@ -113,8 +113,7 @@ tf_status check_kv_attention(const tf_kv_cache* c, const tf_kv_attention* a, tfu
     if (s != TF_OK) return s;
     if (a->H < 1) return fail(TF_ERR_INVALID, "H=%d must be >= 1", a->H);
     if (a->H % c->Hkv != 0) return fail(TF_ERR_DIVISIBILITY, "H=%d is not divisible by Hkv=%d", a->H, c->Hkv);
-    if (!std::isfinite(a->scale)) return fail(TF_ERR_INVALID, "scale must be finite");
-    if (!std::isfinite(a->softcap) || a->softcap < 0) return fail(TF_ERR_INVALID, "softcap must be finite and >= 0");
+    if ((s = check_scores(a->scale, a->softcap)) != TF_OK) return s;
     if (a->causal != 0 && a->causal != 1) return fail(TF_ERR_INVALID, "causal=%d is neither 0 nor 1", a->causal);
     if (a->T > 0 && (a->max_tokens < 1 || a->max_tokens > a->T))
         return fail(TF_ERR_INVALID, "max_tokens=%d outside [1, T=%d]", a->max_tokens, a->T);
