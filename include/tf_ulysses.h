@@ -449,7 +449,8 @@ TF_API tf_status tf_ulysses_attention_workspace(const tf_attention *a, int backw
  * sequence whose length is out of range (starts[n+1] - starts[n] <= lens[n] <=
  * max_pages * page_size) is left out, a page number outside [0, num_pages) leaves out
  * that page's tokens, and both set bit 3 of tf_ulysses_device_status.  So do starts
- * that do not ascend within [0, T]; any sequence of such a call may be left out.
+ * that do not ascend within [0, T]; any sequence of such a call may be left out.  A call
+ * without rows (T == 0) reads nothing.
  */
 typedef struct tf_kv_cache {
     void *k, *v;                /* device, e4m3 [num_pages][Hkv][page_size][D] contiguous, 16-byte aligned */

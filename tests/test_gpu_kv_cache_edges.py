@@ -37,3 +37,20 @@ def test_rows_whose_squares_overflow_beside_ordinary_ones(tf, rope, page, D):  #
     assert torch.equal(got[0].isnan(), ref.isnan())
     tol = 2.0 ** -8 * ref.abs() + 2.0 ** -20 * size + 2.0 ** -25
     assert bool((((got[0].double() - ref).abs() <= tol) | ref.isnan()).all())
+
+
+@pytest.mark.parametrize("starts", [[1000, 1000, 1000], [1000, 1001, 1005], [2 ** 31 - 3] * 3, [24, 24, 40], [0, 1000, 1000], [-7, -7, -7],
+                                    [23, 1, 0]])
+def test_starts_that_do_not_ascend_within_the_rows(tf, starts):  # noqa: F811
+    """Both calls say so, also where no sequence has new tokens or all of them lie behind the rows."""
+    s = Setup(tf, [70, 33], [20, 3], page=16, seed=22)
+    assert s.T == 23
+    s.starts.copy_(torch.tensor(starts, dtype=torch.int32))
+    before, out = s.copy(), [torch.full_like(t, 7.0) for t in s.q]
+    tf.kv_append(*s.args, s.k, s.v, s.q, [t.clone() for t in out])
+    assert tf.device_status(clear=True) == 8
+    tf.kv_attend(*s.args, s.q, out)
+    assert tf.device_status(clear=True) == 8
+    if starts[0] > s.T or starts[-1] < 0:
+        assert bool((out[0] == 7).all())
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(before, s.copy()))

@@ -146,10 +146,15 @@ __global__ void __launch_bounds__(kThreads, kIters == 1 ? 1024 / kThreads : 2) k
     const KvCache& c = p.c;
     const uint32_t unit = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
     const uint32_t shift = 31 - __clz(c.page);  // pages are powers of two
-    // the last sequence whose first unit is not behind this one
+    // the last sequence whose first unit is not behind this one.  Starts that do not ascend within [0, T] may
+    // have units that nothing visits: the first CTA looks at all of them
     uint32_t before = 0;
     for (uint32_t n0 = 0; n0 < c.N; n0 += kThreads) {
         const uint32_t n = n0 + threadIdx.x;
+        if (blockIdx.x == 0 && n < c.N) {
+            const int s0 = c.starts[n], s1 = c.starts[n + 1];
+            if (s0 < 0 || s1 < s0 || s1 > int64_t(p.T)) atomicOr(&g_kv_append_status, 1u);
+        }
         before += __syncthreads_count(n < c.N && int64_t(c.starts[n] >> shift) + 2 * int64_t(n) <= int64_t(unit));
     }
     if (before == 0) return;  // rows in front of starts[0] belong to no sequence
