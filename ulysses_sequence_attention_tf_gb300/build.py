@@ -33,6 +33,7 @@ DEPS = SOURCES + ["relayout.h", "noalloc.h", "device_common.cuh", "block_kernel.
 # The Python module that marshals the attention and cache calls: C++ against the installed torch.
 CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 CALLS = os.path.join(PKG, "_torch_calls.so")
+CALLS_MADE_FOR = os.path.join(BUILD_DIR, "torch_calls_made_for.txt")
 
 
 def _calls_command(out: str) -> list[str]:
@@ -47,9 +48,18 @@ def _calls_command(out: str) -> list[str]:
             f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
 
 
+def _calls_made_for() -> str:
+    """What the module is compiled against beside its sources."""
+    import torch
+    return f"Python {sys.version}\ntorch {torch.__version__}\n{' '.join(_calls_command('module'))}\n"
+
+
 def _calls_stale() -> bool:
-    if not os.path.exists(CALLS):
+    if not os.path.exists(CALLS) or not os.path.exists(CALLS_MADE_FOR):
         return True
+    with open(CALLS_MADE_FOR) as f:
+        if f.read() != _calls_made_for():
+            return True
     t = os.path.getmtime(CALLS)
     return any(os.path.getmtime(d) > t for d in (CALLS_SOURCE, os.path.join(INCLUDE, "tf_ulysses.h")))
 
@@ -77,6 +87,9 @@ def _finish_calls(calls, tmp: str, verbose: bool) -> None:
     if p.returncode != 0:
         raise RuntimeError("g++ failed:\n" + " ".join(cmd))
     os.replace(tmp, CALLS)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(CALLS_MADE_FOR, "w") as f:
+        f.write(_calls_made_for())
 
 
 def build(force: bool = False, verbose: bool = False, defines=(), out: str | None = None) -> str:
