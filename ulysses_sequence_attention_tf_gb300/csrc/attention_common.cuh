@@ -55,8 +55,8 @@ __device__ __forceinline__ float tanh_wide(float x) {
     return fmaf(-2.0f, r, 1.0f);
 }
 
-// tanh x / x for |x| <= kTanhNear as a polynomial in y = x^2, fitted for the least
-// relative error (7.3e-8): no transcendental instruction.
+// tanh x / x for |x| <= kTanhNear as a polynomial in y = x^2 without a transcendental instruction, fitted
+// to it for a small relative error: 9.1e-8 with the coefficients as stored, evaluated in 64 bits.
 constexpr float kTanhNear = 0.6f;
 constexpr float kTanh0 = 0.9999999403953552f, kTanh1 = -0.33332309126853943f, kTanh2 = 0.13310173153877258f,
                 kTanh3 = -0.05210147425532341f, kTanh4 = 0.015475417487323284f;
@@ -332,7 +332,7 @@ __device__ __forceinline__ void fold_tile(float (&s)[128], float c, float down, 
 // product x = s * scale / cap, its factor folded into the coefficients (for a factor that
 // leaves them in range).  False, with nothing done, where |x| of some row of the warp is
 // beyond the polynomials.
-constexpr float kTanhNearest = 0.2f;  // second degree in x^2: 1.1e-7 relative
+constexpr float kTanhNearest = 0.2f;  // second degree in x^2: 1.2e-7 relative
 constexpr float kTanhNearest0 = 0.9999998807907104f, kTanhNearest1 = -0.3332858979701996f, kTanhNearest2 = 0.1301540732383728f;
 template <Fused kF, int kD, bool kRaw>
 __device__ __forceinline__ bool fold_capped_tile(float (&s)[128], float scale, float cap, float down, bool started, float& m,
