@@ -316,12 +316,12 @@ cudaError_t launch(KvAppendParams p, cudaStream_t stream) {
 // As many threads as a page's rows have lanes, up to 256.
 template <Fused kF, int kD>
 cudaError_t launch_typed(const KvAppendParams& p, cudaStream_t stream) {
-    switch (p.c.page * Lane<kD>::kLanes) {
-        case 64: return launch<kF, kD, 1, 64>(p, stream);
-        case 128: return launch<kF, kD, 1, 128>(p, stream);
-        case 256: return launch<kF, kD, 1, 256>(p, stream);
-        case 512: return launch<kF, kD, 2, 256>(p, stream);
-        default: return launch<kF, kD, 4, 256>(p, stream);  // 1024
+    constexpr int kLeast = 16 * Lane<kD>::kLanes;  // a page of 16: 64 threads at D = 64, 128 at D = 128
+    switch (p.c.page) {
+        case 16: return launch<kF, kD, 1, kLeast>(p, stream);
+        case 32: return launch<kF, kD, 1, 2 * kLeast>(p, stream);
+        case 64: return launch<kF, kD, kLeast / 64, 256>(p, stream);
+        default: return launch<kF, kD, kLeast / 32, 256>(p, stream);  // 128
     }
 }
 
