@@ -520,6 +520,9 @@ typedef struct tf_kv_attention {
  * bias and softmax are those of tf_attention with the token's position in its
  * sequence; a sequence of length 0 or without new tokens has nothing to write.
  * A sequence above max_tokens or max_len is out of range.
+ * Products are taken in fp16 with fp32 sums: codes times their page's scale relative to the largest
+ * one at hand (K's of 128 keys, V's so far), exact within 2^15 of that and to multiples of 2^-24 of it
+ * below; weights, times V's relative scale, with one rounding, to multiples of 2^-24 at least.
  *  q            host array of P device pointers to row views [T, H/P, D], q_strides (t, h).
  *  out          the same through out_strides (NULL = contiguous).
  *  lse          host array of P device pointers to fp32 [H/P, T], or NULL.

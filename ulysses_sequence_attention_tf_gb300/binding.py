@@ -491,7 +491,8 @@ def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=No
     ``[B]``) always.  ``q_docs`` / ``k_docs`` (int32 ``[B, Sq]``, ``[B, Sk]``): only equal
     document numbers see one another; negative ones are padding.  Returns ``(out, lse)``:
     P tensors ``[B, Sq, H/P, D]`` and fp32 ``[B, H/P, Sq]``, 0 and -inf for rows that see
-    nothing; both are made here unless given.
+    nothing; both are made here unless given.  The call is not recorded by autograd, also where a tensor requires a
+    gradient: ``attention_backward`` gives the gradients.
     """
     return _run("attention", stream, (q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs), (out, lse))
 
@@ -501,7 +502,7 @@ def attention_backward(dout, q, k, v, out, lse, dq=None, dk=None, dv=None, *, sc
     """Gradients ``(dq, dk, dv)`` of ``attention`` for the gradient ``dout`` of its output, from
     the same inputs and options and its results ``out`` and ``lse``: lists of P tensors
     shaped like q, k and v, made here unless given.  Shared key heads get the sum over
-    their query heads.  The same inputs give the same bits."""
+    their query heads.  The same inputs give the same bits.  Not recorded by autograd."""
     return _run("attention_backward", stream, (q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs),
                 (dout, out, lse, dq, dk, dv))
 

@@ -27,16 +27,19 @@
 // bound below 2^15.  dq_kernel takes a factor for each row, dkv_kernel, which sums over them, one for its key head.
 // P is kept times 2^8 for the same reason.
 //
-// P and dx are rounded to the I/O type as operands (one MMA takes A and B of one type; a second product
-// for the rest would cost a seventh more for each): with bf16 that adds about 0.0017 of the norm to
+// P and dx are rounded to the I/O type as operands (one MMA takes A and B of one type; a second operand
+// for the rest would cost a product more for each): with bf16 that adds about 0.0017 of the norm to
 // gradients whose own rounding is as large.
 //
-// Bound: the products.  8192 tokens, 5 heads, D = 128, bf16: dQ 190 us with the matrix pipe busy 61 % of the
-// cycles, dK and dV 272 us and 54 % (two kernels' 14 D flops a pair at 1300 TFLOP/s).  TMEM holds dK, dV and
-// two pairs of S and dP of 64 queries, whose products take 391 cycles where 256 would be ideal; 128 queries a step
-// do not fit.  D = 64 with bias is bound by the rows' warps: 234 and 369 us for 24 causal heads of 6001 tokens, pipe busy
-// 32 and 26 %, issue slots 56 and 53 %.  16 row warps took 2.72 ms where 8 took 2.88 (16380 tokens,
-// 5 heads); rings of their own for K and V in dQ 2.46; units cut along the other side 2.09.
+// Bound: the products, and the rows' threads beside them that wait for TMEM.  8192 tokens, 5 heads, D = 128, bf16:
+//  * dQ 245 us, the matrix pipe busy 62 % of the cycles.  The rows' P, P K and S of the next tile wait for one
+//    another: without the product P K 215 us, with two buffers for S besides (no room at D = 128 with W) 190.
+//  * dK and dV 273 us and 54 %: TMEM holds dK, dV and two pairs of S and dP of 64 queries, whose products take
+//    391 cycles where 256 would be ideal; 128 queries a step do not fit.  fp16 290: the factor costs registers.
+// D = 64 with bias, 24 causal heads of 6001 tokens: 267 and 369 us, pipe busy 37 and 26 %, issue slots 51 and 53 %: the
+// rows' threads.  Spills: dkv_kernel 40 to 184 bytes, 3 % of its instructions at D = 128, 8 % with bias; the capped
+// dq_kernel 64 to 92, 1 %.  Earlier forms (16380 tokens, 5 heads, before P K): 8 row warps 2.88 ms, 16 2.72; rings
+// of their own for K and V in dQ 2.46; units cut along the other side 2.09; with P K 2.42.
 #include "attention_common.cuh"
 #include "attention_order.h"
 #include "attention_plan.h"

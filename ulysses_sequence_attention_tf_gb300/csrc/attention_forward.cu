@@ -23,11 +23,12 @@
 // TMEM: S0 S1 (128 columns each, P on top of S), O0 O1 (D columns each).
 //
 // Bound: the products, 4 D flops a pair of tokens, and beside them the rows' threads.  32760 tokens, 5
-// heads, D = 128, bf16, capped scores: 2.14 ms, 1270 TFLOP/s; 8192 tokens: the matrix pipe is busy 69 % of the
-// cycles, the exponentials' pipe 34 %.  A pair of tiles keeps the pipe fed through the softmax of
-// either; one elected thread issues a 128 x 128 x 128 product in 518 cycles of 512.  D = 64 halves
+// heads, D = 128, bf16, capped scores: 2.14 to 2.23 ms, 1230 to 1280 TFLOP/s; 8192 tokens uncapped: the matrix pipe is busy
+// 67 % of the cycles, the exponentials' pipe 34 %; capped: 53 and 27 %.  A pair of tiles keeps the pipe fed through the
+// softmax of either; one elected thread issues a 128 x 128 x 128 product in 518 cycles of 512.  D = 64 halves
 // the products, not the scores: 24 heads of 6001 tokens with causal mask and bias take 196 us,
-// the pipe busy 26 %, issue slots 48 %.
+// the pipe busy 26 %, issue slots 48 %.  Every instance spills 56 to 80 bytes: local loads and stores
+// are 1.1 to 1.4 % of its instructions.
 #include "attention_common.cuh"
 #include "attention_plan.h"
 

@@ -15,10 +15,11 @@
 // (at most (t - 1) / page + 2), so that the grid needs no length from the device.
 // A CTA takes a unit and every slices-th head of K, of V and of Q; D / 16 lanes hold a row.
 //
-// Bound by instructions, not bytes: 4680 rows of 40 heads (D = 128, bf16, norm and rotation, pages of
-// 64) take 68 us, 3.6 TB/s of 243 MB.  A lane's 16 values cost about 250 instructions a row --
-// unpack, squares, weights, rotation, maximum, two roundings.  Summing the squares plainly where the sum is
-// finite instead of exactly took 85 us to 79, room in registers for two passes 79 to 68.
+// Bound by latency and instructions: 4680 rows of 40 heads (D = 128, bf16, norm and rotation, pages of 64) take
+// 67 us, 3.6 TB/s of 243 MB, with issue slots busy 49 % of the cycles, 16 warps an SM and long_scoreboard as the first
+// stall: a CTA's every head loads its rows' rotation and the norm's weights again.  A lane's 16 values cost
+// about 240 instructions a row.  Summing the squares plainly took 85 us to 79, room in registers for
+// two passes 79 to 68.  Pages of 128 (four passes at D = 128, 84 bytes spilled): 77 us.
 #include <cuda_fp8.h>
 
 #include "device_common.cuh"

@@ -7,7 +7,7 @@
   python -m ulysses_sequence_attention_tf_gb300.profile_cases scatter --S 4096 --H 24 --layout fused
   python -m ulysses_sequence_attention_tf_gb300.profile_cases gather --P 8 --H 48 --D 64 --B 2 --S 6008
   python -m ulysses_sequence_attention_tf_gb300.profile_cases rope_table [--S 32760] [--iters 3]
-  python -m ulysses_sequence_attention_tf_gb300.profile_cases attention --P 1 --H 5 [--S 8192] [--softcap 50]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases attention --P 1 --H 5 [--S 8192] [--softcap 50] [--docs 5]
   python -m ulysses_sequence_attention_tf_gb300.profile_cases attention_backward --P 1 --H 5 [--S 8192] [--alibi]
   python -m ulysses_sequence_attention_tf_gb300.profile_cases kv_append [--S 32760] [--tokens 4680] [--page 64]
   python -m ulysses_sequence_attention_tf_gb300.profile_cases kv_attend --B 24 --P 1 --H 16 --Hkv 4 --page 128
@@ -18,7 +18,7 @@ default), fused (Q/K/V all views of one fused projection), contiguous, pad16
 which sends fused scatters to the register kernel).  ``rope_table`` builds the
 resident cos/sin table of (theta, S, D) once per iteration, each time for
 another theta.  ``attention`` and ``attention_backward`` see every key (``--alibi``: causal, with
-distances as a bias); the ``kv`` cases have --B sequences of --S tokens, the last --tokens of them new.
+distances as a bias; ``--docs``: within documents); the ``kv`` cases have --B sequences of --S tokens, the last --tokens of them new.
 
 Inputs are the seeded synthetic ones of ``synth``; shapes default to the
 video-DiT workload's head geometry (P=4, H=40, D=128, bf16) with a smaller
@@ -49,6 +49,7 @@ def main(argv=None):
     ap.add_argument("--Hkv", type=int, default=None, help="key heads of the attention and cache cases (default H)")
     ap.add_argument("--softcap", type=float, default=0.0)
     ap.add_argument("--alibi", action="store_true")
+    ap.add_argument("--docs", type=int, default=0, help="documents of unequal length in every batch row of the attention cases")
     ap.add_argument("--tokens", type=int, default=None, help="new tokens of a sequence (default 4680 kv_append, 1 kv_attend)")
     ap.add_argument("--page", type=int, default=64)
     args = ap.parse_args(argv)
@@ -82,6 +83,11 @@ def main(argv=None):
         kw = dict(softcap=args.softcap, causal=args.alibi)
         if args.alibi:
             kw["slopes"] = torch.exp2(-8.0 * torch.arange(1, H + 1, device=dev) / H)
+        if args.docs:
+            parts = [1 + 7 * i % 5 for i in range(args.docs)]
+            ends = [S * sum(parts[:i]) // sum(parts) for i in range(1, args.docs)]
+            docs = torch.bucketize(torch.arange(S, device=dev), torch.tensor(ends, device=dev), right=True).to(torch.int32)
+            kw.update(q_docs=docs.expand(B, S).contiguous(), k_docs=docs.expand(B, S).contiguous())
         out, lse = binding.attention(q, k, v, **kw)
 
         def call():
