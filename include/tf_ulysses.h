@@ -410,7 +410,9 @@ TF_API tf_status tf_ulysses_attention(const tf_attention *a, const void *const *
 /*
  * tf_ulysses_attention_backward -- the gradients of Q, K and V.
  *  dout         host array of P device pointers, the gradient of out.
- *  q, k, v, out, lse   the forward pass's inputs and results (lse is required).
+ *  q, k, v, out, lse   the forward pass's inputs and results (lse is required): those of the same
+ *               description, so that a row's weights add up to 1.  Statistics of more keys than
+ *               the call holds (attention joined from blocks of keys) do not fit.
  *  strides      host array of 5 tf_strides: dout, q, k, v, out.
  *  dq, dk, dv   host arrays of P device pointers, [B, Sq, H/P, D] and twice
  *               [B, Sk, Hkv/P, D]; every element is written.  A shared key head's

@@ -500,7 +500,7 @@ def attention(q, k, v, out=None, lse=None, *, scale=None, softcap=0.0, slopes=No
 def attention_backward(dout, q, k, v, out, lse, dq=None, dk=None, dv=None, *, scale=None, softcap=0.0, slopes=None,
                        causal=False, prefix=None, q_docs=None, k_docs=None, stream=None):
     """Gradients ``(dq, dk, dv)`` of ``attention`` for the gradient ``dout`` of its output, from
-    the same inputs and options and its results ``out`` and ``lse``: lists of P tensors
+    the same inputs and options and its results ``out`` and ``lse`` (not those of more keys): lists of P tensors
     shaped like q, k and v, made here unless given.  Shared key heads get the sum over
     their query heads.  The same inputs give the same bits.  Not recorded by autograd."""
     return _run("attention_backward", stream, (q, k, v, scale, softcap, slopes, causal, prefix, q_docs, k_docs),
