@@ -538,6 +538,212 @@ TF_API tf_status tf_ulysses_kv_attend(const tf_kv_cache *c, const tf_kv_attentio
 TF_API tf_status tf_ulysses_kv_attend_workspace(const tf_kv_cache *c, const tf_kv_attention *a, size_t *bytes);
 
 /*
+ * tf_ulysses_kv_plan -- what the cache calls above need of a step's requests, built on
+ * the device from their lengths in one launch: pages for the new tokens, the pages of
+ * ended requests given back, the new lengths, the rows' starts, and every row's position
+ * and slot.
+ *
+ * Free pages are a ring of num_pages entries, free_count of them in use from entry
+ * free_head on (entries behind the last continue at 0).  Pages are taken from its head
+ * and given back behind its end.  With had(n) = ceil(lens[n] / page_size):
+ *   new_tokens[n] < 0   the request has ended: its had(n) pages go back, in order;
+ *                       lens_out[n] = 0.
+ *   new_tokens[n] >= 0  the request gets pages had(n), had(n) + 1, ... of its table row up
+ *                       to ceil((lens[n] + new_tokens[n]) / page_size), and lens_out[n] =
+ *                       lens[n] + new_tokens[n].
+ * Requests are served in order: where the pages that were free before the call, or the
+ * rows, do not suffice for a request and those in front of it, this request and all
+ * behind it get nothing (starts[n + 1] == starts[n], lens_out[n] = lens[n]).  Pages that
+ * the call itself gets back are free for the next one.
+ * A request whose length is out of range (0 <= lens[n], lens[n] + new_tokens[n] <=
+ * max_pages * page_size) gets and gives nothing, and a span that does not describe the
+ * ring (0 <= head < num_pages, 0 <= count <= num_pages) stands for one without free pages
+ * that takes none back; pages given back beyond the ring's capacity are dropped.  All
+ * three set bit 3 of tf_ulysses_device_status.
+ * The inputs are left as they were but for the table's new entries and the ring's, so the
+ * same call again gives the same results.
+ */
+typedef struct tf_kv_plan {
+    int N, max_pages;            /* requests (at most 8192), entries of a table row in use */
+    int page_size, num_pages;    /* 16, 32, 64 or 128 tokens; capacity of the ring */
+    int T;                       /* rows: capacity of positions and slots, below 2^30 */
+    int32_t *page_table;         /* device, [N][max_pages], rows table_stride entries apart; new entries are written */
+    int64_t table_stride;        /* >= max_pages */
+    const int32_t *lens;         /* device, [N]: tokens of each request so far */
+    const int32_t *new_tokens;   /* device, [N]: new ones, or negative: the request has ended */
+    int32_t *free_pages;         /* device, [num_pages]: the ring; pages given back are written */
+    const int32_t *free_span;    /* device, [2]: free_head, free_count */
+    int32_t *lens_out;           /* device, [N] */
+    int32_t *starts;             /* device, [N + 1]: request n has rows [starts[n], starts[n + 1]) */
+    int32_t *positions;          /* device, [T]: a row's position in its request; 0 behind the last row */
+    int32_t *slots;              /* device, [T]: page * page_size + position % page_size; -1 behind the last row */
+    int32_t *span_out;           /* device, [2]: head and count after the call */
+} tf_kv_plan;
+
+/* Arrays are contiguous, 4-byte aligned, and overlap one another nowhere.  Nothing is
+ * allocated and nothing is kept between calls; the call may be captured. */
+TF_API tf_status tf_ulysses_kv_plan(const tf_kv_plan *p, void *stream);
+
+/*
+ * tf_ulysses_rope -- rotary positions of Q and K (the scatter and tf_ulysses_kv_append
+ * rotate whole heads of the rows they move; this call rotates where these rows lie, a
+ * part of the head, by any frequencies, at any positions).  For token t of batch row b at
+ * position p, pair i < R/2 (R = rotary_dim) with elements x0, x1 -- (2i, 2i + 1)
+ * or (i, i + R/2) of the head -- and angle p * frequencies[i]:
+ *     x0' = m (x0 cos - x1 sin)      x1' = m (x0 sin + x1 cos)        m = magnitude
+ * and elements R..D-1 are copied.  inverse != 0 takes the negative angle: applied to the
+ * gradient of x' it gives the gradient of x.
+ * Angles are held as 64-bit fractions of a turn, so a position of any size gives its
+ * sine and cosine within 3e-7; the rest is fp32 with one rounding to the I/O type.
+ */
+typedef struct tf_rotary {
+    int P, B, T;                 /* head groups (1..8), batch rows, tokens of each */
+    int H, Hk, D;                /* heads of q and of k over all groups (H % P == 0, Hk % P == 0; Hk is ignored
+                                    without k); D a multiple of 8, at most 256 */
+    int rotary_dim;              /* R: even, 2..D */
+    tf_dtype dtype;              /* TF_BF16 or TF_FP16 */
+    tf_rope rope;                /* TF_ROPE_INTERLEAVED or TF_ROPE_HALF_SPLIT */
+    int inverse;                 /* 0 or 1 */
+    float magnitude;             /* finite; 1 as a rule */
+    const double *frequencies;   /* host, [R/2], finite, read before the call returns: radians a position */
+    const int32_t *positions;    /* device, [B][T] contiguous, or NULL: token t stands at first + t */
+    int first;
+} tf_rotary;
+
+/*
+ *  q, k         host arrays of P device pointers to views [B, T, heads/P, D]; k may be NULL.
+ *  strides      host array of 2 tf_strides: q, k.
+ *  q_out, k_out host arrays of P device pointers through out_strides (2 tf_strides, NULL =
+ *               contiguous).  q_out may be q itself, with its strides, and k_out k (elements R..D-1
+ *               are then not touched); they overlap nothing else.  k_out is NULL without k.
+ * One launch, nothing is allocated; the call may be captured (positions are read on the device).
+ */
+TF_API tf_status tf_ulysses_rope(const tf_rotary *r, const void *const *q, const void *const *k, const tf_strides *strides,
+                                 void *const *q_out, void *const *k_out, const tf_strides *out_strides, void *stream);
+
+/*
+ * Frequencies for tf_ulysses_rope, f_i = theta^(-2i/R), and what is done to them for contexts
+ * longer than the trained one (original tokens):
+ *   TF_ROPE_SCALE_NONE    f_i
+ *   TF_ROPE_SCALE_LINEAR  f_i / factor: positions interpolated (Chen et al. 2023, "Extending
+ *                         Context Window of Large Language Models via Positional Interpolation")
+ *   TF_ROPE_SCALE_BASE    theta * factor^(R/(R-2)) in place of theta: the fastest pair keeps its
+ *                         frequency, the slowest is interpolated (R > 2)
+ *   TF_ROPE_SCALE_PARTS   f_i (g + (1 - g) / factor), g = clamp((original f_i / 2 pi - low) /
+ *                         (high - low), 0, 1): pairs that turn more than `high` times in the trained
+ *                         context keep their frequency, below `low` times they are interpolated
+ *                         (Peng et al. 2023, "YaRN", section 3.2; its 0.1 ln(factor) + 1 is a magnitude)
+ */
+typedef enum tf_rope_scale {
+    TF_ROPE_SCALE_NONE = 0,
+    TF_ROPE_SCALE_LINEAR = 1,
+    TF_ROPE_SCALE_BASE = 2,
+    TF_ROPE_SCALE_PARTS = 3
+} tf_rope_scale;
+
+/* Host arithmetic in 64 bits into out[rotary_dim / 2]; factor > 0 unless scale is NONE; original > 0 and
+ * low < high for PARTS. */
+TF_API tf_status tf_ulysses_rope_frequencies(int rotary_dim, double theta, tf_rope_scale scale, double factor,
+                                             double original, double low, double high, double *out);
+
+/*
+ * Linear attention over the head groups: attention without a softmax, whose weights fade
+ * with the distance by a factor e^-decay[h] a token, so that a state of fixed size stands
+ * for all earlier tokens.  With k_t, v_t rows of one batch row and head,
+ *     S_t = e^-decay S_(t-1) + k_t^T v_t          [D, D], S_(-1) = state or 0
+ *     o_t = scale * q_t S_t
+ *         = scale * ( sum_(j <= t) e^(-decay (t - j)) (q_t . k_j) v_j + e^(-decay (t + 1)) q_t state )
+ * States, sums and decays are fp32.  Chunks of tokens go through the tensor cores: the
+ * weights e^(-decay (t - j)) (q_t . k_j) and the states are rounded to the I/O type for the products
+ * with V and q (in fp16 times powers of two that keep them in its normal range); keys
+ * times their decay enter a state as two numbers of the I/O type, 2^-17 (fp16: 2^-22) of the key apart.
+ * Inputs should be finite: a token's infinity or NaN reaches every later output of its head.
+ */
+typedef struct tf_linear {
+    int P, B, S;             /* head groups (1..8), batch rows, tokens of each (0 is valid) */
+    int H, D;                /* heads over all groups (H % P == 0); 64 or 128 */
+    tf_dtype dtype;          /* TF_BF16 or TF_FP16 */
+    float scale;             /* finite; 1/sqrt(D) as a rule */
+    const float *decay;      /* device, [H] (over all groups), finite and >= 0, read-only */
+} tf_linear;
+
+/*
+ * tf_ulysses_linear_attention -- the forward pass.
+ *  q, k, v      host arrays of P device pointers: group g's views [B, S, H/P, D].
+ *  strides      host array of 3 tf_strides: q, k, v.
+ *  state        device fp32 [B][H][D][D] contiguous, 16-byte aligned, the state in front of the first
+ *               token (rows belong to k, columns to v), or NULL: zeros.
+ *  out          host array of P device pointers, [B, S, H/P, D] through out_strides
+ *               (NULL = contiguous); must not overlap the inputs.
+ *  final_state  as state, the one behind the last token, or NULL.  May be `state` itself.
+ *  workspace    device memory of at least tf_ulysses_linear_attention_workspace(a, 0)
+ *               bytes, 16-byte aligned (NULL where that is 0), one for each call that may run
+ *               at the same time (replays of graphs among them); its contents need not be kept.
+ * Nothing is allocated and nothing is kept between calls; the call may be captured.  The same
+ * inputs give the same bits.
+ */
+TF_API tf_status tf_ulysses_linear_attention(const tf_linear *a, const void *const *q, const void *const *k,
+                                             const void *const *v, const tf_strides *strides, const float *state,
+                                             void *const *out, const tf_strides *out_strides, float *final_state,
+                                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * tf_ulysses_linear_attention_backward -- the gradients of Q, K, V and of the state in front.
+ *  dout         host array of P device pointers, the gradient of out.
+ *  q, k, v, state   the forward pass's inputs.  strides: host array of 4 tf_strides: dout, q, k, v.
+ *  dfinal_state the gradient of the final state, or NULL: zeros.
+ *  dq, dk, dv   host arrays of P device pointers, [B, S, H/P, D] through grad_strides (3
+ *               tf_strides: dq, dk, dv; NULL = contiguous); every element is written.
+ *  dstate       the gradient of `state`, or NULL.  May be dfinal_state itself.
+ *  workspace    as above, tf_ulysses_linear_attention_workspace(a, 1) bytes.
+ * States are computed again; nothing of the forward pass but its inputs is needed.  There is
+ * no gradient of the decay.
+ */
+TF_API tf_status tf_ulysses_linear_attention_backward(const tf_linear *a, const void *const *dout, const void *const *q,
+                                                      const void *const *k, const void *const *v,
+                                                      const tf_strides *strides, const float *state,
+                                                      const float *dfinal_state, void *const *dq, void *const *dk,
+                                                      void *const *dv, const tf_strides *grad_strides, float *dstate,
+                                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the two calls above for `a` (its device pointer is not read); backward != 0: of the second. */
+TF_API tf_status tf_ulysses_linear_attention_workspace(const tf_linear *a, int backward, size_t *bytes);
+
+/*
+ * tf_ulysses_linear_attend -- linear attention of the newest tokens of N sequences
+ * through their states in a pool, which move on: prompts, chunks of a stream and single
+ * tokens alike.  Rows [starts[n], starts[n + 1]) of the row tensors are the newest tokens of
+ * sequence n, whose state is slot slots[n] of the pool; rows in front of starts[0] and behind
+ * starts[N], and slots that no sequence names, are neither read nor written.  A sequence
+ * without new rows keeps its state.  Slots and starts are read on the device, so a captured call
+ * follows their contents.  A sequence whose slot lies outside [0, num_slots), whose starts do not
+ * ascend within [0, T] or which has more than max_tokens rows is left out and sets bit 3 of
+ * tf_ulysses_device_status.  Sequences with new rows name different slots.
+ */
+typedef struct tf_linear_pool {
+    float *states;           /* device, fp32 [num_slots][H][D][D] contiguous, 16-byte aligned */
+    int num_slots, N;        /* slots of the pool, sequences of the call */
+    const int32_t *slots;    /* device, [N] */
+    const int32_t *starts;   /* device, [N + 1] */
+    int max_tokens;          /* bound of the new tokens of one sequence, 1..T */
+} tf_linear_pool;
+
+/*
+ *  a            as above with B = 1 and S = T, the rows of the row tensors.
+ *  q, k, v      host arrays of P device pointers to row views [T, H/P, D]; strides: host array
+ *               of 3 tf_strides (t and h used).
+ *  out          the same through out_strides (NULL = contiguous); must not overlap the inputs.
+ *  workspace    tf_ulysses_linear_attend_workspace bytes, 16-byte aligned, one for each call
+ *               that may run at the same time.
+ */
+TF_API tf_status tf_ulysses_linear_attend(const tf_linear *a, const tf_linear_pool *pool, const void *const *q,
+                                          const void *const *k, const void *const *v, const tf_strides *strides,
+                                          void *const *out, const tf_strides *out_strides, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+TF_API tf_status tf_ulysses_linear_attend_workspace(const tf_linear *a, const tf_linear_pool *pool, size_t *bytes);
+
+/*
  * tf_ulysses_rope_table -- the resident fp32 cos/sin table [S][D/2][2] for
  * (theta, S, D) on the current device, built on `stream` on first use and kept
  * (up to 4 tables; least recently used evicted).  *table receives its device

@@ -75,6 +75,38 @@ class KvAttention(ctypes.Structure):
                [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("causal", ctypes.c_int), ("slopes", ctypes.c_void_p)]
 
 
+class KvPlan(NamedTuple):
+    """What ``kv_plan`` gives: int32 ``lens [N]``, ``starts [N + 1]``, ``positions [rows]``, ``slots [rows]``, ``span [2]``."""
+    lens: torch.Tensor
+    starts: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    span: torch.Tensor
+
+
+class Plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("N", "max_pages", "page_size", "num_pages", "T")] + \
+               [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_void_p) for n in ("lens", "new_tokens", "free_pages", "free_span", "lens_out", "starts", "positions",
+                                               "slots", "span_out")]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("P", "B", "T", "H", "Hk", "D", "rotary_dim", "dtype", "rope", "inverse")] + \
+               [("magnitude", ctypes.c_float), ("frequencies", ctypes.POINTER(ctypes.c_double)), ("positions", ctypes.c_void_p),
+                ("first", ctypes.c_int)]
+
+
+class Linear(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("P", "B", "S", "H", "D", "dtype")] + \
+               [("scale", ctypes.c_float), ("decay", ctypes.c_void_p)]
+
+
+class LinearPool(ctypes.Structure):
+    _fields_ = [("states", ctypes.c_void_p), ("num_slots", ctypes.c_int), ("N", ctypes.c_int), ("slots", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("max_tokens", ctypes.c_int)]
+
+
 class PagedCache(NamedTuple):
     """A paged key-value cache: e4m3 codes ``[pages, Hkv, page_size, D]`` and their fp32 scales ``[pages, Hkv]``."""
     k: torch.Tensor
@@ -116,7 +148,19 @@ def _declare(lib):
                                          i32, vp]
     lib.tf_ulysses_kv_attend.argtypes = [CP, KP, PP, SP, PP, SP, PP, vp, size_t, vp]
     lib.tf_ulysses_kv_attend_workspace.argtypes = [CP, KP, ctypes.POINTER(size_t)]
-    for name in ("tf_ulysses_kv_append", "tf_ulysses_kv_attend", "tf_ulysses_kv_attend_workspace",
+    lib.tf_ulysses_kv_plan.argtypes = [ctypes.POINTER(Plan), vp]
+    lib.tf_ulysses_rope.argtypes = [ctypes.POINTER(Rotary), PP, PP, SP, PP, PP, SP, vp]
+    f64 = ctypes.c_double
+    lib.tf_ulysses_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, ctypes.POINTER(f64)]
+    LP, OP = ctypes.POINTER(Linear), ctypes.POINTER(LinearPool)
+    lib.tf_ulysses_linear_attention.argtypes = [LP, PP, PP, PP, SP, vp, PP, SP, vp, vp, size_t, vp]
+    lib.tf_ulysses_linear_attention_backward.argtypes = [LP, PP, PP, PP, PP, SP, vp, vp, PP, PP, PP, SP, vp, vp, size_t, vp]
+    lib.tf_ulysses_linear_attention_workspace.argtypes = [LP, i32, ctypes.POINTER(size_t)]
+    lib.tf_ulysses_linear_attend.argtypes = [LP, OP, PP, PP, PP, SP, PP, SP, vp, size_t, vp]
+    lib.tf_ulysses_linear_attend_workspace.argtypes = [LP, OP, ctypes.POINTER(size_t)]
+    for name in ("tf_ulysses_kv_plan", "tf_ulysses_rope", "tf_ulysses_rope_frequencies", "tf_ulysses_linear_attention",
+                 "tf_ulysses_linear_attention_backward", "tf_ulysses_linear_attention_workspace", "tf_ulysses_linear_attend",
+                 "tf_ulysses_linear_attend_workspace", "tf_ulysses_kv_append", "tf_ulysses_kv_attend", "tf_ulysses_kv_attend_workspace",
                  "tf_ulysses_attention", "tf_ulysses_attention_backward", "tf_ulysses_attention_workspace",
                  "tf_ulysses_scatter_qkv_heads_into", "tf_ulysses_exchange_chunks", "tf_ulysses_project_qkv_into",
                  "tf_ulysses_scatter_qkv", "tf_ulysses_scatter_qkv_into", "tf_ulysses_scatter_qkv_noalloc",
@@ -454,7 +498,9 @@ def _torch_calls():
             from . import _torch_calls as module
         except ImportError as e:
             raise TfUlyssesError(TF_ERR_INVALID, f"_torch_calls is not built (run __graft_entry__.build()): {e}") from e
-        names = ("attention", "attention_backward", "attention_workspace", "kv_append", "kv_attend", "kv_attend_workspace")
+        names = ("attention", "attention_backward", "attention_workspace", "kv_append", "kv_attend", "kv_attend_workspace",
+                 "kv_plan", "rope", "rope_frequencies", "linear_attention", "linear_attention_backward",
+                 "linear_attention_workspace", "linear_attend", "linear_attend_workspace")
         module.bind(_check, *[ctypes.cast(getattr(L, "tf_ulysses_" + n), ctypes.c_void_p).value for n in names])
         _calls = module
     return _calls
@@ -546,6 +592,88 @@ def kv_attend(cache, page_table, lens, starts, q, out=None, lse=None, *, max_tok
     """
     return _run("kv_attend", stream, (*cache, page_table, lens, starts),
                 (q, out, lse, max_tokens, max_len, scale, softcap, slopes, causal))
+
+
+def kv_plan(page_table, lens, new, free, span, *, page_size, rows, lens_out=None, starts=None, positions=None, slots=None,
+            span_out=None, stream=None):
+    """What a step's requests need of a paged cache, built on the device from their lengths: ``lens`` (int32 ``[N]``)
+    tokens so far and ``new`` (int32 ``[N]``) tokens that each one gets now, or a negative number where it has ended.
+
+    ``free`` (int32 ``[num_pages]``) is a ring of free page numbers, ``span`` (int32 ``[2]``) its head and how many are
+    free.  New pages go into ``page_table`` (int32 ``[N, max_pages]``), those of ended requests back into ``free``; both are
+    written in place, ``lens`` and ``span`` are not.  Returns ``KvPlan(lens, starts, positions, slots, span)``: the new
+    lengths, the first row of each request among ``rows`` (the ``lens`` and ``starts`` of ``kv_append``), each row's position
+    (that of ``rope``) and its slot ``page * page_size + position % page_size``, 0 and -1 behind the last, and the ring's new
+    span.  They are made here unless given.  Requests are served in order: where pages or rows run out, the first one
+    that does not fit and all behind it get nothing, which their ``starts`` tell.
+    """
+    return KvPlan(*_run("kv_plan", stream, (page_table, lens, new, free, span),
+                        (page_size, rows, lens_out, starts, positions, slots, span_out)))
+
+
+_ROPE_SCALE = {None: 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def rope_frequencies(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, original=4096, low=1.0, high=32.0):
+    """Frequencies ``[rotary_dim / 2]`` (float64 on the CPU) for ``rope``: ``theta^(-2i / rotary_dim)``, for contexts longer
+    than the trained one divided by ``factor`` ("linear"), with a larger base ("base"), or divided for the
+    pairs only that turn less than ``low`` times in ``original`` tokens, kept above ``high``, in between by parts ("parts",
+    which goes with a magnitude of ``0.1 * log(factor) + 1`` as a rule)."""
+    if scaling not in _ROPE_SCALE:
+        raise ValueError(f"scaling must be 'linear', 'base', 'parts' or None, not {scaling!r}")
+    out = (ctypes.c_double * 128)()
+    _check(lib().tf_ulysses_rope_frequencies(int(rotary_dim), float(theta), _ROPE_SCALE[scaling], float(factor), float(original),
+                                             float(low), float(high), out))
+    return torch.tensor(out[:rotary_dim // 2], dtype=torch.float64)
+
+
+def rope(q, k=None, q_out=None, k_out=None, *, positions=None, first=0, frequencies=None, rotary_dim=None, theta=10000.0,
+         magnitude=1.0, rope="interleaved", inverse=False, stream=None):
+    """Rotary positions of P head groups: ``q`` and ``k`` P views ``[B, tokens, heads/P, D]`` or rows ``[T, heads/P, D]``
+    (bf16 or fp16, D a multiple of 8 up to 256), at ``positions`` (int32 ``[B, tokens]`` or ``[T]``) or ``first + token``.
+
+    Pairs (2i, 2i+1) ("interleaved") or (i, i + R/2) ("neox") of the first R elements of a head turn by
+    ``position * frequencies[i]`` (``rope_frequencies``, float64 ``[R / 2]`` on the CPU; default: those of ``theta`` and
+    ``rotary_dim``, which is D unless given) and are multiplied by ``magnitude``; the other elements are copied.
+    ``inverse=True`` turns the other way: the gradient of the inputs from that of the outputs.  Returns
+    ``(q_out, k_out)``, lists of P tensors made here unless given (``q`` and ``k`` themselves are fine); k_out is None
+    without k.
+    """
+    if rope not in ("interleaved", "neox"):
+        raise ValueError(f"rope must be 'interleaved' or 'neox', not {rope!r}")
+    return _run("rope", stream, (q, k), (q_out, k_out, positions, first, frequencies, rotary_dim, theta, magnitude, _ROPE[rope],
+                                         inverse))
+
+
+def linear_attention(q, k, v, out=None, *, decay, scale=None, state=None, final_state=False, stream=None):
+    """Attention without a softmax over P head groups, ``q``, ``k`` and ``v`` P views ``[B, S, H/P, D]`` (bf16 or fp16, D 64
+    or 128): with ``S_t = exp(-decay[h]) S_(t-1) + k_t^T v_t`` the output is ``scale * q_t S_t`` (default 1/sqrt(D)).
+
+    ``decay``: fp32 ``[H]``, >= 0.  ``state``: fp32 ``[B, H, D, D]``, what the sequence starts from (default: zeros);
+    ``final_state=True`` (or a tensor, ``state`` itself too) asks for the one behind the last token.  Returns
+    ``(out, final_state)``, the latter None unless asked for.  Not recorded by autograd: ``linear_attention_backward``
+    gives the gradients.
+    """
+    return _run("linear_attention", stream, (q, k, v, decay, scale, state), (out, final_state))
+
+
+def linear_attention_backward(dout, q, k, v, dq=None, dk=None, dv=None, *, decay, scale=None, state=None, dstate=None,
+                              dstate_out=None, stream=None):
+    """Gradients ``(dq, dk, dv, dstate_out)`` of ``linear_attention`` for the gradients ``dout`` of its output and ``dstate`` of
+    its final state (fp32 ``[B, H, D, D]`` or None), from the same inputs: lists of P tensors shaped like q, k and v, and
+    the gradient of ``state`` (None without state, unless a tensor or True is given).  Not recorded by autograd.
+    There is no gradient of the decay."""
+    return _run("linear_attention_backward", stream, (q, k, v, decay, scale, state), (dout, dstate, dq, dk, dv, dstate_out))
+
+
+def linear_attend(states, slots, starts, q, k, v, out=None, *, decay, scale=None, max_tokens=None, stream=None):
+    """Linear attention of each sequence's newest tokens through its state, which moves on: rows ``[starts[n],
+    starts[n + 1])`` (int32 ``[N + 1]``) of the P row views ``q``, ``k``, ``v`` ``[T, H/P, D]`` belong to sequence n, whose
+    state is ``states[slots[n]]`` (fp32 ``[slots, H, D, D]``, updated in place; ``slots`` int32 ``[N]``, different for
+    sequences with new rows).  Prompts, chunks and single tokens alike; ``max_tokens`` bounds the rows of one sequence
+    (default: T), and a tight one spares work.  Returns ``out``, P tensors ``[T, H/P, D]`` made here unless given (rows
+    of no sequence are then undefined; given tensors keep them)."""
+    return _run("linear_attend", stream, (q, k, v, decay, scale, states, slots, starts), (out, max_tokens))
 
 
 def rope_table(theta, S, D, *, stream=None, device=None):

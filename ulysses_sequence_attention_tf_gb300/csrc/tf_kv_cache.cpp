@@ -259,4 +259,64 @@ TF_API tf_status tf_ulysses_kv_attend(const tf_kv_cache* c, const tf_kv_attentio
     return TF_OK;
 }
 
+TF_API tf_status tf_ulysses_kv_plan(const tf_kv_plan* p, void* stream) {
+    CallRange call_range("tf_ulysses_kv_plan");
+    if (!p) return fail(TF_ERR_INVALID, "the plan's description is NULL");
+    if (p->N < 0 || p->T < 0) return fail(TF_ERR_INVALID, "N=%d, T=%d must be >= 0", p->N, p->T);
+    if (p->max_pages < 1 || p->num_pages < 1)
+        return fail(TF_ERR_INVALID, "max_pages=%d, num_pages=%d must be >= 1", p->max_pages, p->num_pages);
+    if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128)
+        return fail(TF_ERR_UNSUPPORTED, "the cache is built for pages of 16, 32, 64 or 128 tokens, not %d", p->page_size);
+    if (p->N > tfu::kMostRequests) return fail(TF_ERR_UNSUPPORTED, "the plan is built for up to %d requests, not %d", tfu::kMostRequests, p->N);
+    if (p->T >= 1 << 30) return fail(TF_ERR_UNSUPPORTED, "T=%d exceeds 2^30 - 1 rows", p->T);
+    if (int64_t(p->max_pages) * p->page_size > (int64_t(1) << 30))
+        return fail(TF_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^30 tokens");
+    if (int64_t(p->num_pages) * p->page_size >= (int64_t(1) << 31))
+        return fail(TF_ERR_UNSUPPORTED, "num_pages * page_size exceeds 2^31 - 1 slots");
+    if (p->table_stride < p->max_pages)
+        return fail(TF_ERR_INVALID, "table_stride=%lld is below max_pages=%d", (long long)p->table_stride, p->max_pages);
+    // by size in entries; of size 0 may be NULL
+    const int64_t N = p->N, table = N ? (N - 1) * p->table_stride + p->max_pages : 0;
+    const struct {
+        const char* name;
+        const int32_t* at;
+        int64_t size;
+    } a[] = {{"page_table", p->page_table, table}, {"free_pages", p->free_pages, p->num_pages}, {"lens_out", p->lens_out, N},
+             {"starts", p->starts, N + 1}, {"positions", p->positions, p->T}, {"slots", p->slots, p->T},
+             {"span_out", p->span_out, 2}, {"lens", p->lens, N}, {"new_tokens", p->new_tokens, N}, {"free_span", p->free_span, 2}};
+    constexpr int kWritten = 7;
+    for (const auto& x : a) {
+        if (x.size > 0 && !x.at) return fail(TF_ERR_INVALID, "%s is NULL", x.name);
+        if (reinterpret_cast<uintptr_t>(x.at) % 4) return fail(TF_ERR_ALIGNMENT, "%s must be 4-byte aligned", x.name);
+    }
+    for (int i = 0; i < kWritten; ++i)
+        for (const auto& y : a)
+            if (&y != &a[i] && a[i].size > 0 && y.size > 0 && a[i].at < y.at + y.size && y.at < a[i].at + a[i].size)
+                return fail(TF_ERR_INVALID, "%s overlaps %s", a[i].name, y.name);
+    int device = 0;
+    tf_status s = current_device(&device);
+    if (s != TF_OK) return s;
+    tfu::KvPlanParams k{};
+    k.lens = p->lens;
+    k.new_tokens = p->new_tokens;
+    k.free_span = p->free_span;
+    k.table = p->page_table;
+    k.free_pages = p->free_pages;
+    k.lens_out = p->lens_out;
+    k.starts = p->starts;
+    k.positions = p->positions;
+    k.slots = p->slots;
+    k.span_out = p->span_out;
+    k.table_stride = p->table_stride;
+    k.N = uint32_t(p->N);
+    k.max_pages = uint32_t(p->max_pages);
+    k.page = uint32_t(p->page_size);
+    k.num_pages = uint32_t(p->num_pages);
+    k.T = uint32_t(p->T);
+    const cudaError_t e = tfu::launch_kv_plan(k, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "launching the cache's plan");
+    count_launches(1);
+    return TF_OK;
+}
+
 }  // extern "C"

@@ -1,0 +1,221 @@
+// tf_linear.cpp -- host side of the linear attention entry points of tf_ulysses.h:
+// argument checks (all of them before any CUDA call) and the launches.
+#include <cmath>
+
+#include "host.h"
+#include "linear.h"
+
+using namespace tfu::host;
+
+namespace {
+
+tf_status check_linear(const tf_linear* a) {
+    if (!a) return fail(TF_ERR_INVALID, "the linear attention's description is NULL");
+    if (a->P < 1 || a->P > TF_ULYSSES_MAX_SHARDS)
+        return fail(TF_ERR_INVALID, "P=%d outside [1, %d]", a->P, TF_ULYSSES_MAX_SHARDS);
+    if (a->B < 0 || a->S < 0) return fail(TF_ERR_INVALID, "B=%d, S=%d must be >= 0", a->B, a->S);
+    if (a->H < 1) return fail(TF_ERR_INVALID, "H=%d must be >= 1", a->H);
+    if (a->H % a->P != 0) return fail(TF_ERR_DIVISIBILITY, "H=%d is not divisible by P=%d", a->H, a->P);
+    if (a->dtype != TF_BF16 && a->dtype != TF_FP16)
+        return fail(TF_ERR_UNSUPPORTED, "linear attention needs bf16 or fp16 (dtype %d)", int(a->dtype));
+    if (a->D != 64 && a->D != 128) return fail(TF_ERR_UNSUPPORTED, "linear attention is built for D in {64, 128}, not %d", a->D);
+    if (!std::isfinite(a->scale)) return fail(TF_ERR_INVALID, "scale must be finite");
+    if (!a->decay) return fail(TF_ERR_INVALID, "decay is NULL");
+    if (reinterpret_cast<uintptr_t>(a->decay) % 4) return fail(TF_ERR_ALIGNMENT, "decay must be 4-byte aligned");
+    if (a->S > 1 << 30) return fail(TF_ERR_UNSUPPORTED, "S exceeds 2^30 tokens");
+    if (int64_t(a->B) * a->H * ((int64_t(a->S) + 127) / 128) >= (int64_t(1) << 28))
+        return fail(TF_ERR_UNSUPPORTED, "problem exceeds 2^28 work units");
+    return TF_OK;
+}
+
+tf_status view(const char* name, const void* const* base, const tf_strides* given, const tf_linear& a, bool written, tfu::GroupView* out) {
+    const int64_t hl = a.H / a.P;
+    const bool empty = a.B == 0 || a.S == 0;
+    if (!base) return fail(TF_ERR_INVALID, "%s is NULL", name);
+    tf_status s;
+    if (!empty && (s = check_ptrs(name, base, a.P)) != TF_OK) return s;
+    const tf_strides st = given ? *given : tf_strides{a.S * hl * a.D, hl * a.D, a.D};
+    if ((s = check_strides(name, st, 2, a.B, a.S, hl)) != TF_OK) return s;
+    for (int g = 0; g < a.P; ++g) out->base[g] = static_cast<uint8_t*>(const_cast<void*>(base[g]));
+    out->b = st.b * 2;
+    out->t = st.t * 2;
+    out->h = st.h * 2;
+    if (!empty && ((a.B > 1 && st.b == 0) || (a.S > 1 && st.t == 0) || (hl > 1 && st.h == 0)))
+        return fail(written ? TF_ERR_INVALID : TF_ERR_UNSUPPORTED, "%s has a stride of 0", name);
+    return TF_OK;
+}
+
+tf_status check_state(const char* name, const float* s) {
+    return aligned16(s) ? TF_OK : fail(TF_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
+}
+
+tf_status check_workspace(size_t need, const void* workspace, size_t bytes) {
+    if (need == 0) return TF_OK;
+    if (!workspace || bytes < need)
+        return fail(TF_ERR_INVALID, "the workspace holds %zu bytes of the %zu needed", workspace ? bytes : size_t(0), need);
+    if (!aligned16(workspace)) return fail(TF_ERR_ALIGNMENT, "the workspace is not 16-byte aligned");
+    return TF_OK;
+}
+
+tfu::LinearPass pass_of(const tf_linear& a) {
+    tfu::LinearPass p{};
+    p.decay = a.decay;
+    p.P = uint32_t(a.P);
+    p.N = uint32_t(a.B);
+    p.S = p.most = uint32_t(a.S);
+    p.Hl = uint32_t(a.H / a.P);
+    p.D = uint32_t(a.D);
+    p.kv_scale = 1.f;
+    p.out_scale = a.scale;
+    return p;
+}
+
+size_t workspace_of(const tfu::LinearPass&) { return 0; }
+
+tf_status run(const tfu::LinearPass& p, bool bf16, void*, cudaStream_t stream) {
+    const cudaError_t e = tfu::launch_linear_steps(p, bf16, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "launching linear attention");
+    count_launches(1);
+    return TF_OK;
+}
+
+tf_status check_pool(const tf_linear* a, const tf_linear_pool* pool, tfu::LinearPass* p) {
+    tf_status s = check_linear(a);
+    if (s != TF_OK) return s;
+    if (!pool) return fail(TF_ERR_INVALID, "the pool's description is NULL");
+    if (a->B != 1) return fail(TF_ERR_INVALID, "B=%d must be 1 for rows", a->B);
+    if (pool->N < 0 || pool->num_slots < 1)
+        return fail(TF_ERR_INVALID, "N=%d must be >= 0 and num_slots=%d >= 1", pool->N, pool->num_slots);
+    if (!pool->states || !pool->starts || (pool->N > 0 && !pool->slots))
+        return fail(TF_ERR_INVALID, "the pool's states, slots or starts are NULL");
+    if ((s = check_state("states", pool->states)) != TF_OK) return s;
+    if (reinterpret_cast<uintptr_t>(pool->slots) % 4 || reinterpret_cast<uintptr_t>(pool->starts) % 4)
+        return fail(TF_ERR_ALIGNMENT, "slots and starts must be 4-byte aligned");
+    if (a->S > 0 && (pool->max_tokens < 1 || pool->max_tokens > a->S))
+        return fail(TF_ERR_INVALID, "max_tokens=%d outside [1, T=%d]", pool->max_tokens, a->S);
+    if (int64_t(pool->N) * a->H * ((int64_t(pool->max_tokens) + 127) / 128) >= (int64_t(1) << 28))
+        return fail(TF_ERR_UNSUPPORTED, "problem exceeds 2^28 work units");
+    *p = pass_of(*a);
+    p->N = uint32_t(pool->N);
+    p->most = uint32_t(pool->max_tokens);
+    p->starts = pool->starts;
+    p->slots = pool->slots;
+    p->num_slots = uint32_t(pool->num_slots);
+    p->state = p->final_state = pool->states;
+    return TF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+TF_API tf_status tf_ulysses_linear_attention_workspace(const tf_linear* a, int backward, size_t* bytes) {
+    (void)backward;  // its passes run one after another in the same place
+    if (!bytes) return fail(TF_ERR_INVALID, "bytes is NULL");
+    const tf_status s = check_linear(a);
+    if (s != TF_OK) return s;
+    *bytes = workspace_of(pass_of(*a));
+    return TF_OK;
+}
+
+TF_API tf_status tf_ulysses_linear_attention(const tf_linear* a, const void* const* q, const void* const* k,
+                                             const void* const* v, const tf_strides* strides, const float* state,
+                                             void* const* out, const tf_strides* out_strides, float* final_state,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange call_range("tf_ulysses_linear_attention");
+    tf_status s = check_linear(a);
+    if (s != TF_OK) return s;
+    if (!strides) return fail(TF_ERR_INVALID, "strides is NULL");
+    tfu::LinearPass p = pass_of(*a);
+    if ((s = view("q", q, &strides[0], *a, false, &p.q)) != TF_OK || (s = view("k", k, &strides[1], *a, false, &p.k)) != TF_OK ||
+        (s = view("v", v, &strides[2], *a, false, &p.v)) != TF_OK || (s = view("out", out, out_strides, *a, true, &p.out)) != TF_OK)
+        return s;
+    if ((s = check_state("state", state)) != TF_OK || (s = check_state("final_state", final_state)) != TF_OK) return s;
+    if ((s = check_workspace(workspace_of(p), workspace, workspace_bytes)) != TF_OK) return s;
+    int device = 0;
+    if ((s = current_device(&device)) != TF_OK) return s;
+    if (a->B == 0 || (a->S == 0 && !final_state)) return TF_OK;
+    p.state = state;
+    p.final_state = final_state;
+    return run(p, a->dtype == TF_BF16, workspace, static_cast<cudaStream_t>(stream));
+}
+
+TF_API tf_status tf_ulysses_linear_attention_backward(const tf_linear* a, const void* const* dout, const void* const* q,
+                                                      const void* const* k, const void* const* v,
+                                                      const tf_strides* strides, const float* state,
+                                                      const float* dfinal_state, void* const* dq, void* const* dk,
+                                                      void* const* dv, const tf_strides* grad_strides, float* dstate,
+                                                      void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange call_range("tf_ulysses_linear_attention_backward");
+    tf_status s = check_linear(a);
+    if (s != TF_OK) return s;
+    if (!strides) return fail(TF_ERR_INVALID, "strides is NULL");
+    const tf_strides* gs = grad_strides;
+    tfu::GroupView vdout, vq, vk, vv, vdq, vdk, vdv;
+    if ((s = view("dout", dout, &strides[0], *a, false, &vdout)) != TF_OK || (s = view("q", q, &strides[1], *a, false, &vq)) != TF_OK ||
+        (s = view("k", k, &strides[2], *a, false, &vk)) != TF_OK || (s = view("v", v, &strides[3], *a, false, &vv)) != TF_OK ||
+        (s = view("dq", dq, gs ? &gs[0] : nullptr, *a, true, &vdq)) != TF_OK ||
+        (s = view("dk", dk, gs ? &gs[1] : nullptr, *a, true, &vdk)) != TF_OK ||
+        (s = view("dv", dv, gs ? &gs[2] : nullptr, *a, true, &vdv)) != TF_OK)
+        return s;
+    if ((s = check_state("state", state)) != TF_OK || (s = check_state("dfinal_state", dfinal_state)) != TF_OK ||
+        (s = check_state("dstate", dstate)) != TF_OK)
+        return s;
+    const tfu::LinearPass all = pass_of(*a);
+    if ((s = check_workspace(workspace_of(all), workspace, workspace_bytes)) != TF_OK) return s;
+    int device = 0;
+    if ((s = current_device(&device)) != TF_OK) return s;
+    if (a->B == 0 || (a->S == 0 && !dstate)) return TF_OK;
+    const bool bf16 = a->dtype == TF_BF16;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (a->S > 0) {
+        tfu::LinearPass p = all;  // dq
+        p.q = vdout, p.k = vv, p.v = vk, p.out = vdq;
+        p.state = state;
+        p.transposed = 1;
+        if ((s = run(p, bf16, workspace, st)) != TF_OK) return s;
+        p = all;  // dk: in front of the pass that may write dstate over dfinal_state
+        p.q = vv, p.k = vdout, p.v = vq, p.out = vdk;
+        p.state = dfinal_state;
+        p.transposed = p.reverse = 1;
+        p.kv_scale = a->scale, p.out_scale = 1.f;
+        if ((s = run(p, bf16, workspace, st)) != TF_OK) return s;
+    }
+    tfu::LinearPass p = all;  // dv
+    p.q = vk, p.k = vq, p.v = vdout, p.out = vdv;
+    p.state = dfinal_state;
+    p.final_state = dstate;
+    p.reverse = 1;
+    p.kv_scale = a->scale, p.out_scale = 1.f;
+    return run(p, bf16, workspace, st);
+}
+
+TF_API tf_status tf_ulysses_linear_attend_workspace(const tf_linear* a, const tf_linear_pool* pool, size_t* bytes) {
+    if (!bytes) return fail(TF_ERR_INVALID, "bytes is NULL");
+    tfu::LinearPass p{};
+    const tf_status s = check_pool(a, pool, &p);
+    if (s != TF_OK) return s;
+    *bytes = workspace_of(p);
+    return TF_OK;
+}
+
+TF_API tf_status tf_ulysses_linear_attend(const tf_linear* a, const tf_linear_pool* pool, const void* const* q,
+                                          const void* const* k, const void* const* v, const tf_strides* strides,
+                                          void* const* out, const tf_strides* out_strides, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+    CallRange call_range("tf_ulysses_linear_attend");
+    tfu::LinearPass p{};
+    tf_status s = check_pool(a, pool, &p);
+    if (s != TF_OK) return s;
+    if (!strides) return fail(TF_ERR_INVALID, "strides is NULL");
+    if ((s = view("q", q, &strides[0], *a, false, &p.q)) != TF_OK || (s = view("k", k, &strides[1], *a, false, &p.k)) != TF_OK ||
+        (s = view("v", v, &strides[2], *a, false, &p.v)) != TF_OK || (s = view("out", out, out_strides, *a, true, &p.out)) != TF_OK)
+        return s;
+    if ((s = check_workspace(workspace_of(p), workspace, workspace_bytes)) != TF_OK) return s;
+    int device = 0;
+    if ((s = current_device(&device)) != TF_OK) return s;
+    if (a->S == 0 || pool->N == 0) return TF_OK;
+    return run(p, a->dtype == TF_BF16, workspace, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

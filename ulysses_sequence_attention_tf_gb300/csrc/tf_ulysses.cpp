@@ -25,6 +25,7 @@
 #include "gemm.h"
 #include "host.h"
 #include "kv_cache.h"
+#include "linear.h"
 #include "noalloc.h"
 #include "relayout.h"
 #include "tf_ulysses.h"
@@ -1162,12 +1163,14 @@ TF_API tf_status tf_ulysses_device_status(int clear, unsigned* status) {
     if (e == cudaSuccess) e = tfu::read_block_status_v16(&block16, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_append_status(&append, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_attend_status(&attend, clear != 0);
-    unsigned gradient = 0, tiles = 0, tile_waits = 0;
+    unsigned gradient = 0, tiles = 0, tile_waits = 0, plan = 0, steps = 0;
+    if (e == cudaSuccess) e = tfu::read_kv_plan_status(&plan, clear != 0);
+    if (e == cudaSuccess) e = tfu::read_linear_steps_status(&steps, clear != 0);
     if (e == cudaSuccess) e = tfu::read_kv_tiles_status(&tiles, &tile_waits, clear != 0);
     if (e == cudaSuccess) e = tfu::read_attention_status(&attention, clear != 0);
     if (e == cudaSuccess) e = tfu::read_attention_backward_status(&gradient, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device status words");
-    *status = (staged ? 1u : 0u) | (gemm ? 2u : 0u) | ((block | block16) ? 4u : 0u) | ((append | attend | tiles) ? 8u : 0u) |
+    *status = (staged ? 1u : 0u) | (gemm ? 2u : 0u) | ((block | block16) ? 4u : 0u) | ((append | attend | tiles | plan | steps) ? 8u : 0u) |
               ((attention | gradient | tile_waits) ? 16u : 0u);
     return TF_OK;
 }

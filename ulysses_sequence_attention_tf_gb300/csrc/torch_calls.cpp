@@ -1,4 +1,4 @@
-// torch_calls.cpp -- the attention and key-value cache calls of the binding, marshalled in C++.
+// torch_calls.cpp -- the attention, rotation and key-value cache calls of the binding, marshalled in C++.
 //
 // These calls are short on the GPU, and checking and unpacking a dozen tensors in Python
 // takes longer than the kernels of a small call (35 us of host time for two head groups of
@@ -26,6 +26,14 @@ struct EntryPoints {
     decltype(&tf_ulysses_kv_append) kv_append;
     decltype(&tf_ulysses_kv_attend) kv_attend;
     decltype(&tf_ulysses_kv_attend_workspace) kv_attend_workspace;
+    decltype(&tf_ulysses_kv_plan) kv_plan;
+    decltype(&tf_ulysses_rope) rope;
+    decltype(&tf_ulysses_rope_frequencies) rope_frequencies;
+    decltype(&tf_ulysses_linear_attention) linear_attention;
+    decltype(&tf_ulysses_linear_attention_backward) linear_attention_backward;
+    decltype(&tf_ulysses_linear_attention_workspace) linear_attention_workspace;
+    decltype(&tf_ulysses_linear_attend) linear_attend;
+    decltype(&tf_ulysses_linear_attend_workspace) linear_attend_workspace;
 };
 EntryPoints g_abi{};
 PyObject* g_check = nullptr;  // raises for a status that is not TF_OK
@@ -420,6 +428,254 @@ PyObject* kv_attend(PyObject* const* x, Py_ssize_t n) {
     return pair(x[10] == Py_None ? out.wrap() : same(x[10]), x[11] == Py_None ? lse.wrap() : same(x[11]));
 }
 
+// (page_table, lens, new, free, span, device, stream, page_size, rows, lens_out, starts, positions, slots, span_out)
+//   -> (lens_out, starts, positions, slots, span_out)
+PyObject* kv_plan(PyObject* const* x, Py_ssize_t n) {
+    count(n, 14);
+    const int device = small("device", x[5]);
+    void* stream = address(x[6]);
+    const Tensor& table = tensor("page_table", x[0]);
+    if (table.dim() != 2 || table.scalar_type() != ScalarType::Int || !table.is_cuda() || table.get_device() != device)
+        refuse("page_table must be int32 [N, max_pages] on cuda:" + std::to_string(device));
+    const int64_t N = table.size(0), most = table.size(1);
+    if (most > 1 && table.stride(1) != 1) refuse("page_table must have unit stride along a row");
+    for (int i = 1; i < 5; ++i)
+        if (x[i] == Py_None) refuse("lens, new, free and span are required");
+    const Tensor& free = tensor("free", x[3]);
+    if (free.dim() != 1) refuse("free must be int32 [num_pages]");
+    auto ints = [&](const char* name, PyObject* o, int64_t size) { return static_cast<int32_t*>(plain(name, o, ScalarType::Int, {size}, device)); };
+    tf_kv_plan p{};
+    p.N = extent(N);
+    p.max_pages = extent(most);
+    p.page_size = small("page_size", x[7]);
+    p.num_pages = extent(free.size(0));
+    p.T = small("rows", x[8]);
+    if (p.T < 0) refuse("rows=" + std::to_string(p.T) + " must be >= 0");
+    p.page_table = static_cast<int32_t*>(table.data_ptr());
+    p.table_stride = N > 1 ? table.stride(0) : most;
+    p.lens = ints("lens", x[1], N);
+    p.new_tokens = ints("new", x[2], N);
+    p.free_pages = ints("free", x[3], p.num_pages);
+    p.free_span = ints("span", x[4], 2);
+    const char* names[5] = {"lens_out", "starts", "positions", "slots", "span_out"};
+    const int64_t sizes[5] = {N, N + 1, p.T, p.T, 2};
+    Tensor made[5];
+    int32_t* at[5];
+    for (int i = 0; i < 5; ++i) {
+        if (x[9 + i] == Py_None) {
+            made[i] = at::empty({sizes[i]}, table.options());
+            at[i] = static_cast<int32_t*>(made[i].data_ptr());
+        } else {
+            at[i] = ints(names[i], x[9 + i], sizes[i]);
+        }
+    }
+    p.lens_out = at[0];
+    p.starts = at[1];
+    p.positions = at[2];
+    p.slots = at[3];
+    p.span_out = at[4];
+    call([&] { return g_abi.kv_plan(&p, stream); });
+    PyObject* t = PyTuple_New(5);
+    if (!t) throw PythonError{};
+    for (int i = 0; i < 5; ++i) {
+        PyObject* o = x[9 + i] == Py_None ? THPVariable_Wrap(made[i]) : same(x[9 + i]);
+        if (!o) {
+            Py_DECREF(t);
+            throw PythonError{};
+        }
+        PyTuple_SET_ITEM(t, i, o);
+    }
+    return t;
+}
+
+// (q, k, device, stream, q_out, k_out, positions, first, frequencies, rotary_dim, theta, magnitude, rope, inverse) -> (q_out, k_out)
+PyObject* rope(PyObject* const* x, Py_ssize_t n) {
+    count(n, 14);
+    const int device = small("device", x[2]);
+    void* stream = address(x[3]);
+    const List q("q", x[0]);
+    const int64_t dims = q.t[0].dim();
+    if (dims != 3 && dims != 4) refuse("expected views [B, tokens, heads, D] or [T, heads, D]");
+    const ScalarType type = q.t[0].scalar_type();
+    const std::vector<int64_t> shape = q.t[0].sizes().vec();
+    const Views qv("q", q, shape, type, device);
+    tf_rotary r{};
+    r.P = q.P;
+    r.B = dims == 4 ? extent(shape[0]) : 1;
+    r.T = extent(shape[dims - 3]);
+    r.H = extent(q.P * shape[dims - 2]);
+    r.D = extent(shape[dims - 1]);
+    r.dtype = dtype_code(type);
+    r.rope = tf_rope(small("rope", x[12]));
+    r.inverse = truth(x[13]);
+    r.magnitude = float(number(x[11]));
+    r.first = small("first", x[7]);
+    const std::vector<int64_t> rows(shape.begin(), shape.end() - 2);
+    r.positions = static_cast<int32_t*>(plain("positions", x[6], ScalarType::Int, rows, device));
+    double made[128];
+    if (x[8] == Py_None) {
+        r.rotary_dim = x[9] == Py_None ? r.D : small("rotary_dim", x[9]);
+        check(g_abi.rope_frequencies(r.rotary_dim, number(x[10]), TF_ROPE_SCALE_NONE, 1.0, 1.0, 0.0, 1.0, made));
+        r.frequencies = made;
+    } else {
+        const Tensor& f = tensor("frequencies", x[8]);
+        if (f.dim() != 1 || f.scalar_type() != ScalarType::Double || !f.device().is_cpu() || !f.is_contiguous() || f.size(0) > 128)
+            refuse("frequencies must be a contiguous Double tensor [rotary_dim / 2] of up to 128 on the CPU, not " + text(f));
+        r.rotary_dim = int(2 * f.size(0));
+        if (x[9] != Py_None && small("rotary_dim", x[9]) != r.rotary_dim)
+            refuse("rotary_dim does not go with " + std::to_string(f.size(0)) + " frequencies");
+        r.frequencies = static_cast<const double*>(f.data_ptr());
+    }
+    const List qo = x[4] == Py_None ? List(q.P, shape, q.t[0].options()) : List("q_out", x[4], q.P);
+    const Views qov("q_out", qo, shape, type, device);
+    if (x[1] == Py_None) {
+        if (x[5] != Py_None) refuse("k_out is given without k");
+        const tf_strides st[2] = {qv.st, qv.st}, os[2] = {qov.st, qov.st};
+        call([&] { return g_abi.rope(&r, qv.ptr, nullptr, st, qov.ptr, nullptr, os, stream); });
+        return pair(x[4] == Py_None ? qo.wrap() : same(x[4]), same(Py_None));
+    }
+    const List k("k", x[1], q.P);
+    if (k.t[0].dim() != dims) refuse("q and k must have the same number of dimensions");
+    std::vector<int64_t> k_shape = shape;
+    k_shape[dims - 2] = k.t[0].size(dims - 2);
+    const Views kv("k", k, k_shape, type, device);
+    r.Hk = extent(q.P * k_shape[dims - 2]);
+    const List ko = x[5] == Py_None ? List(q.P, k_shape, k.t[0].options()) : List("k_out", x[5], q.P);
+    const Views kov("k_out", ko, k_shape, type, device);
+    const tf_strides st[2] = {qv.st, kv.st}, os[2] = {qov.st, kov.st};
+    call([&] { return g_abi.rope(&r, qv.ptr, kv.ptr, st, qov.ptr, kov.ptr, os, stream); });
+    return pair(x[4] == Py_None ? qo.wrap() : same(x[4]), x[5] == Py_None ? ko.wrap() : same(x[5]));
+}
+
+// what the linear attention calls share: (q, k, v, decay, scale, device)
+struct Linear {
+    List q, k, v;
+    tf_linear a{};
+    ScalarType type;
+    std::vector<int64_t> shape;
+    Views qv, kv, vv;
+    Linear(PyObject* const* x, int device, int64_t dims)
+        : q("q", x[0]), k("k", x[1], q.P), v("v", x[2], q.P), type(q.t[0].scalar_type()), shape(shape_of(q, dims)),
+          qv("q", q, shape, type, device), kv("k", k, shape, type, device), vv("v", v, shape, type, device) {
+        a.P = q.P;
+        a.B = dims == 4 ? extent(shape[0]) : 1;
+        a.S = extent(shape[dims - 3]);
+        a.H = extent(q.P * shape[dims - 2]);
+        a.D = extent(shape[dims - 1]);
+        a.dtype = dtype_code(type);
+        if (x[3] == Py_None) refuse("decay is required");
+        a.decay = static_cast<float*>(plain("decay", x[3], ScalarType::Float, {a.H}, device));
+        a.scale = float(x[4] == Py_None ? 1.0 / std::sqrt(double(a.D)) : number(x[4]));
+    }
+    static std::vector<int64_t> shape_of(const List& l, int64_t dims) {
+        if (l.t[0].dim() != dims) refuse(dims == 4 ? "expected 4-d views [B, tokens, heads, D]" : "expected 3-d views [T, heads, D]");
+        return l.t[0].sizes().vec();
+    }
+    at::TensorOptions options() const { return q.t[0].options(); }
+    std::vector<int64_t> states() const { return {a.B, a.H, a.D, a.D}; }
+    size_t workspace(bool backward) const {
+        size_t n = 0;
+        check(g_abi.linear_attention_workspace(&a, backward, &n));
+        return n;
+    }
+};
+
+// A state that may be given (a tensor), asked for (True) or left out (False, None).
+struct State {
+    Tensor t;
+    PyObject* given = nullptr;
+    float* at = nullptr;
+    State(const char* name, PyObject* o, const Linear& c, int device) {
+        if (o == Py_None || o == Py_False) return;
+        if (o == Py_True) {
+            t = at::empty(c.states(), c.options().dtype(ScalarType::Float));
+            at = static_cast<float*>(t.data_ptr());
+        } else {
+            given = o;
+            at = static_cast<float*>(plain(name, o, ScalarType::Float, c.states(), device));
+        }
+    }
+    PyObject* wrap() const { return given ? same(given) : at || t.defined() ? THPVariable_Wrap(t) : same(Py_None); }
+};
+
+// (q, k, v, decay, scale, state, device, stream, out, final_state) -> (out, final_state)
+PyObject* linear_attention(PyObject* const* x, Py_ssize_t n) {
+    count(n, 10);
+    const int device = small("device", x[6]);
+    void* stream = address(x[7]);
+    const Linear c(x, device, 4);
+    const float* state = static_cast<float*>(plain("state", x[5], ScalarType::Float, c.states(), device));
+    const List out = x[8] == Py_None ? List(c.a.P, c.shape, c.options()) : List("out", x[8], c.a.P);
+    const Views ov("out", out, c.shape, c.type, device);
+    const State last("final_state", x[9], c, device);
+    const Workspace ws(c.workspace(false), c.options());
+    const tf_strides st[3] = {c.qv.st, c.kv.st, c.vv.st};
+    call([&] {
+        return g_abi.linear_attention(&c.a, c.qv.ptr, c.kv.ptr, c.vv.ptr, st, state, ov.ptr, &ov.st, last.at, ws.at_(), ws.bytes, stream);
+    });
+    return pair(x[8] == Py_None ? out.wrap() : same(x[8]), last.wrap());
+}
+
+// (q, k, v, decay, scale, state, device, stream, dout, dfinal_state, dq, dk, dv, dstate) -> (dq, dk, dv, dstate)
+PyObject* linear_attention_backward(PyObject* const* x, Py_ssize_t n) {
+    count(n, 14);
+    const int device = small("device", x[6]);
+    void* stream = address(x[7]);
+    const Linear c(x, device, 4);
+    const float* state = static_cast<float*>(plain("state", x[5], ScalarType::Float, c.states(), device));
+    const List dout("dout", x[8], c.a.P);
+    const Views dv("dout", dout, c.shape, c.type, device);
+    const float* dfinal = static_cast<float*>(plain("dstate", x[9], ScalarType::Float, c.states(), device));
+    const char* names[3] = {"dq", "dk", "dv"};
+    auto made = [&](int i) { return x[10 + i] == Py_None ? List(c.a.P, c.shape, c.options()) : List(names[i], x[10 + i], c.a.P); };
+    const List gq = made(0), gk = made(1), gv = made(2);
+    const Views gqv("dq", gq, c.shape, c.type, device), gkv("dk", gk, c.shape, c.type, device), gvv("dv", gv, c.shape, c.type, device);
+    const State first("dstate_out", x[13] == Py_None && state ? Py_True : x[13], c, device);
+    const Workspace ws(c.workspace(true), c.options());
+    const tf_strides st[4] = {dv.st, c.qv.st, c.kv.st, c.vv.st}, gs[3] = {gqv.st, gkv.st, gvv.st};
+    call([&] {
+        return g_abi.linear_attention_backward(&c.a, dv.ptr, c.qv.ptr, c.kv.ptr, c.vv.ptr, st, state, dfinal, gqv.ptr, gkv.ptr, gvv.ptr,
+                                               gs, first.at, ws.at_(), ws.bytes, stream);
+    });
+    PyObject* t = PyTuple_New(4);
+    if (!t) throw PythonError{};
+    PyTuple_SET_ITEM(t, 0, x[10] == Py_None ? gq.wrap() : same(x[10]));
+    PyTuple_SET_ITEM(t, 1, x[11] == Py_None ? gk.wrap() : same(x[11]));
+    PyTuple_SET_ITEM(t, 2, x[12] == Py_None ? gv.wrap() : same(x[12]));
+    PyTuple_SET_ITEM(t, 3, first.wrap());
+    return t;
+}
+
+// (q, k, v, decay, scale, states, slots, starts, device, stream, out, max_tokens) -> out
+PyObject* linear_attend(PyObject* const* x, Py_ssize_t n) {
+    count(n, 12);
+    const int device = small("device", x[8]);
+    void* stream = address(x[9]);
+    const Linear c(x, device, 3);
+    const Tensor& states = tensor("states", x[5]);
+    if (states.dim() != 4) refuse("states must be [slots, H, D, D]");
+    const Tensor& slots = tensor("slots", x[6]);
+    if (slots.dim() != 1) refuse("slots must be int32 [N]");
+    if (x[7] == Py_None) refuse("starts is required");
+    tf_linear_pool p{};
+    p.states = static_cast<float*>(plain("states", x[5], ScalarType::Float, {states.size(0), c.a.H, c.a.D, c.a.D}, device));
+    p.num_slots = extent(states.size(0));
+    p.N = extent(slots.size(0));
+    p.slots = static_cast<int32_t*>(plain("slots", x[6], ScalarType::Int, {p.N}, device));
+    p.starts = static_cast<int32_t*>(plain("starts", x[7], ScalarType::Int, {int64_t(p.N) + 1}, device));
+    p.max_tokens = x[11] == Py_None ? c.a.S : small("max_tokens", x[11]);
+    const List out = x[10] == Py_None ? List(c.a.P, c.shape, c.options()) : List("out", x[10], c.a.P);
+    const Views ov("out", out, c.shape, c.type, device);
+    size_t need = 0;
+    check(g_abi.linear_attend_workspace(&c.a, &p, &need));
+    const Workspace ws(need, c.options());
+    const tf_strides st[3] = {c.qv.st, c.kv.st, c.vv.st};
+    call([&] {
+        return g_abi.linear_attend(&c.a, &p, c.qv.ptr, c.kv.ptr, c.vv.ptr, st, ov.ptr, &ov.st, ws.at_(), ws.bytes, stream);
+    });
+    return x[10] == Py_None ? out.wrap() : same(x[10]);
+}
+
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* x, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -431,13 +687,14 @@ PyObject* entry(PyObject*, PyObject* const* x, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(check, six addresses in the order of EntryPoints)
+// bind(check, addresses in the order of EntryPoints)
 PyObject* bind(PyObject*, PyObject* const* x, Py_ssize_t n) {
     try {
-        count(n, 7);
+        constexpr Py_ssize_t kSlots = sizeof(EntryPoints) / sizeof(void*);
+        count(n, 1 + kSlots);
         EntryPoints e;
         void** slots = reinterpret_cast<void**>(&e);
-        for (int i = 0; i < 6; ++i) slots[i] = address(x[1 + i]);
+        for (Py_ssize_t i = 0; i < kSlots; ++i) slots[i] = address(x[1 + i]);
         Py_INCREF(x[0]);
         Py_XDECREF(g_check);
         g_check = x[0];
@@ -457,6 +714,11 @@ PyMethodDef g_methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                            {"attention_backward", fast(entry<attention_backward>), METH_FASTCALL, nullptr},
                            {"kv_append", fast(entry<kv_append>), METH_FASTCALL, nullptr},
                            {"kv_attend", fast(entry<kv_attend>), METH_FASTCALL, nullptr},
+                           {"kv_plan", fast(entry<kv_plan>), METH_FASTCALL, nullptr},
+                           {"rope", fast(entry<rope>), METH_FASTCALL, nullptr},
+                           {"linear_attention", fast(entry<linear_attention>), METH_FASTCALL, nullptr},
+                           {"linear_attention_backward", fast(entry<linear_attention_backward>), METH_FASTCALL, nullptr},
+                           {"linear_attend", fast(entry<linear_attend>), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
