@@ -24,7 +24,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibilit
               f"-I{INCLUDE}", f"-I{CSRC}"]
 SOURCES = ["block_kernels.cu", "block_kernels_v16.cu", "gemm_kernels.cu", "relayout_kernels.cu", "staged_kernels.cu",
            "tf_ulysses.cpp", "noalloc.cu", "attention_plan.cu", "attention_forward.cu", "attention_backward.cu", "attention_join.cu", "tf_attention.cpp", "kv_append.cu", "kv_attend.cu", "kv_attend_tiles.cu",
-           "tf_kv_cache.cpp", "kv_plan.cu", "rotary.cu", "tf_rotary.cpp", "linear_steps.cu", "tf_linear.cpp"]
+           "tf_kv_cache.cpp", "kv_plan.cu", "rotary.cu", "tf_rotary.cpp", "linear_steps.cu", "linear_chunks.cu", "tf_linear.cpp"]
 DEPS = SOURCES + ["relayout.h", "noalloc.h", "device_common.cuh", "block_kernel.cuh", "tma_plan.h", "gemm.h", "host.h",
                   "attention.h", "attention_common.cuh", "attention_order.h", "attention_plan.h",
                   "tcgen05.cuh", "kv_cache.h", "kv_common.cuh", "rotary.h", "linear.h"]

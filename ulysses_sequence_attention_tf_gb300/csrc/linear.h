@@ -61,10 +61,22 @@ __device__ __forceinline__ LinearSequence linear_sequence(const LinearPass& p, u
 }
 #endif
 
+constexpr uint32_t kLinearChunk = 128;  // tokens: TMEM lanes
+
+// The chunk kernels' launches: every sequence cut into `segments` of seg_chunks chunks (1: not cut).
+struct LinearChunkParams {
+    GroupMaps q, k, v;  // boxes of 128 tokens
+    LinearPass p;
+    uint32_t segments, seg_chunks;
+    float* parts;       // workspace [N * H][segments][D][D], used where there are several
+};
+cudaError_t launch_linear_chunks(const LinearChunkParams& p, bool bf16, cudaStream_t stream, int* launches);
+
 // token by token: single ones and short runs
 cudaError_t launch_linear_steps(const LinearPass& p, bool bf16, cudaStream_t stream);
 
 // Status words: 0, or 1 when a sequence's slot or starts were out of range and it was left out.
 cudaError_t read_linear_steps_status(unsigned* out, bool clear);
+cudaError_t read_linear_chunks_status(unsigned* out, unsigned* waits, bool clear);  // *waits: 1 when a bounded wait gave up
 
 }  // namespace tfu

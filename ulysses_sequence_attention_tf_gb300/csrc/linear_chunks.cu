@@ -1,0 +1,588 @@
+// linear_chunks.cu -- linear attention chunk by chunk on the 5th-generation tensor cores.
+//
+// For a chunk of L <= 128 tokens, rows a and columns b, and the state S in front of it:
+//
+//   out_a = out_scale ( kv_scale sum_(b <= a) lambda^(a - b) (q_a . k_b) v_b + lambda^(a + 1) q_a S )
+//   S    <- lambda^L S + kv_scale sum_b (lambda^(L - 1 - b) k_b)^T v_b
+//   reverse, the last chunk first: b >= a, lambda^(b - a), lambda^(L - 1 - a) q_a S, lambda^(b + 1) k_b
+//
+// -- four products of 128 x 128 x D or 128 x D x D.  A CTA of 384 threads walks the chunks of one head (or of a segment
+// of them, below):
+//  * warp 8, one lane: TMA producer.  Q, K, V tiles through a ring of stages.
+//  * warp 9, one lane: X = Q K^T, then O1 = P V with P from TMEM.
+//  * warp 10, one lane: O2 = Q S, then dS = K_w^T V twice: K_w is kept as two 16-bit tiles.
+//  * warps 0-3: a thread a row of the chunk.  P = X times the decays and the mask, in 16 bits over the scores; then
+//    the row of O1 + lambda^(a + 1) O2 to memory.
+//  * warps 4-7: a thread a row of S (D = 64: half a row; dS comes twice then), in registers in fp32.  S in 16 bits into
+//    shared memory for O2; the chunk's keys times their decay, in place and the rest in a tile beside; dS into S.
+// Each chunk's dS starts at zero and is added to S in fp32 with one rounding, so what the tensor cores' sums drop does not
+// add up over the chunks.  K_w needs the second tile because S outlives the chunk: its fp32 is worth 2^-17 (bf16) or
+// 2^-22 (fp16) of a key, while P and S only enter the chunk's own output, in 16 bits like it.
+// fp16: P is scaled by a power of two by its row, S and K_w by that of their largest value, so that none of them
+// leaves fp16's normal range.
+//
+// Segments: where there are fewer heads than SMs, each sequence is cut.  A first launch finds what every segment but the
+// last adds to the state (K and V only), a second one runs these sums up to the states in front of the
+// segments, and the segments then go on their own.
+#include "attention_common.cuh"
+#include "linear.h"
+
+namespace tfu {
+
+__device__ unsigned g_linear_chunks_status, g_linear_chunks_waits;
+
+namespace {
+
+using namespace dev;
+
+constexpr int kThreadsC = 384;
+constexpr uint32_t kChunk = kLinearChunk;
+constexpr uint32_t kHalfTile = kChunk * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
+
+template <int kD, bool kOutputs>
+struct Shape {
+    static constexpr uint32_t kTile = kHalfTile * (kD / 64);
+    static constexpr uint32_t kStateTile = kD * kSwizzleRow * (kD / 64);
+    static constexpr int kTiles = kOutputs ? 3 : 2;  // a chunk's
+    static constexpr int kStages = kD == 128 ? (kOutputs ? 5 : 6) : 9;
+    static constexpr size_t kSmem = (kStages + 1) * size_t(kTile) + (kOutputs ? kStateTile : 0) + 1024 + 1024;  // barriers, alignment
+};
+
+constexpr uint32_t kRowsTransposed = 1u << 15;  // of f16_idesc: A MN-major
+
+// 128 threads' largest value through shared memory; false if a wait gave up.
+struct Largest {
+    float* slots;  // [2][4]
+    uint32_t bar, phase;
+    __device__ bool of(float& v, uint32_t quarter, uint32_t lane, volatile int* abort_flag) {
+        v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+        float* at = slots + phase * 4;
+        if (lane == 0) {
+            at[quarter] = v;
+            mbar_arrive(bar);
+        }
+        const bool ok = __all_sync(0xffffffffu, bounded_wait(bar, phase, abort_flag, &g_linear_chunks_waits));
+        phase ^= 1u;
+        if (ok) v = fmaxf(fmaxf(at[0], at[1]), fmaxf(at[2], at[3]));
+        return ok;
+    }
+};
+
+// A power of two that takes a largest magnitude v into [2^13, 2^14), as far as fp32's range goes.  1 for 0, infinities and NaN.
+__device__ __forceinline__ float up_scale(float v) {
+    const int e = int(__float_as_uint(v) >> 23);  // biased; 0: below the normal range
+    if (!(v > 0.f) || e == 255) return 1.f;
+    const int to = 127 + 13 - (e - 127);
+    return __uint_as_float(uint32_t(min(to, 253)) << 23);
+}
+__device__ __forceinline__ float inverse(float power_of_two) { return __uint_as_float((254u << 23) - __float_as_uint(power_of_two)); }
+
+template <Fused kF, int kD, bool kOutputs>
+__global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
+    using Sh = Shape<kD, kOutputs>;
+    constexpr uint32_t kTile = Sh::kTile;
+    constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles;
+    constexpr bool kFp16 = kF == Fused::kFP16;
+    const LinearPass& p = cp.p;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* rest_tile = smem + kStages * size_t(kTile);  // of K_w
+    uint8_t* state_tile = rest_tile + kTile;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(state_tile + (kOutputs ? Sh::kStateTile : 0));
+    const uint32_t ring = smem_u32(smem);
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
+    const uint32_t x_full = empty0 + 8 * kStages, p_ready = x_full + 8, o1_full = p_ready + 8, o2_full = o1_full + 8,
+                   o_free = o2_full + 8, s_ready = o_free + 8, k_ready = s_ready + 8, ds_full = k_ready + 8, done_a = ds_full + 8,
+                   done_b = done_a + 8, largest_bar = done_b + 8;
+    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 12);
+    float* decays = floats;            // [32]: lambda^(31 - r), reverse: lambda^r
+    float* state_factor = floats + 32;  // [2], by parity of the chunk: what the state's tile is to be multiplied by
+    float* largest = floats + 36;       // [2][4]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 44);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, kOutputs ? 2 : 1);
+        }
+        mbar_init(x_full, 1);
+        mbar_init(p_ready, 4);  // a warp each
+        mbar_init(o1_full, 1);
+        mbar_init(o2_full, 1);
+        mbar_init(o_free, 4);
+        mbar_init(s_ready, 4);
+        mbar_init(k_ready, 4);
+        mbar_init(ds_full, 1);
+        mbar_init(done_a, 1);
+        mbar_init(done_b, 1);
+        mbar_init(largest_bar, 4);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dependency_wait();
+    const uint32_t tmem = *tmem_slot, o1_tmem = tmem + kChunk, o2_tmem = o1_tmem + kD, ds_tmem = o2_tmem + kD;
+
+    // the unit: sequence, head, segment.  Segments of one head lie beside one another in the grid's order
+    const uint32_t heads = p.P * p.Hl, here = kOutputs ? cp.segments : cp.segments - 1;
+    const uint32_t seg = blockIdx.x % here, unit = blockIdx.x / here, head = unit % heads, n = unit / heads;
+    const uint32_t g = head / p.Hl, h = head % p.Hl;
+    const LinearSequence seq = linear_sequence(p, n, &g_linear_chunks_status);
+    const uint32_t chunks = (seq.len + kChunk - 1) / kChunk, first = seg * cp.seg_chunks;
+    const uint32_t count = seq.ok && chunks > first ? min(chunks - first, cp.seg_chunks) : 0;
+    const bool last = first + count == chunks;  // of this sequence's segments
+    const bool work = count > 0 && (kOutputs || !last);
+    const float decay = p.decay[head];
+    // chunk x of the unit: its first token and how many it has
+    auto chunk_at = [&](uint32_t x) { return (p.reverse ? chunks - 1 - first - x : first + x) * kChunk; };
+    auto chunk_len = [&](uint32_t at) { return min(seq.len - at, kChunk); };
+
+    if (work) {
+    // 384 * 168 registers at launch = 256 * 216 + 128 * 72
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8 && elect_one()) {
+            // ---------------- TMA producer
+            const CUtensorMap* maps[3] = {&cp.q.m[g], &cp.k.m[g], &cp.v.m[g]};
+            uint32_t m = 0;  // tiles loaded
+            bool ok = true;
+            for (uint32_t x = 0; ok && x < count; ++x) {
+                const int token = int(seq.first + chunk_at(x));
+                for (int y = 0; y < kTiles; ++y, ++m) {
+                    const uint32_t s = m % kStages, use = m / kStages;
+                    if (use > 0 && !bounded_wait(empty0 + 8 * s, (use - 1) & 1u, abort_flag, &g_linear_chunks_waits)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(full0 + 8 * s, kTile);
+                    for (int z = 0; z < kD / 64; ++z)
+                        tma_load_4d(ring + s * kTile + z * kHalfTile, maps[3 - kTiles + y], z * 64, int(h), token, int(seq.b), full0 + 8 * s);
+                }
+            }
+            // every load has landed before the CTA exits
+            for (uint32_t k = m > uint32_t(kStages) ? m - kStages : 0; k < m; ++k)
+                drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
+        } else if (kOutputs && warp == 9 && elect_one()) {
+            // ---------------- X = Q K^T, O1 = P V
+            constexpr uint32_t kIdescX = f16_idesc(!kFp16, kChunk, kChunk, false);
+            constexpr uint32_t kIdescO = f16_idesc(!kFp16, kChunk, kD, true);
+            const uint32_t low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
+            auto landed = [&](uint32_t m) { return bounded_wait(full0 + 8 * (m % kStages), (m / kStages) & 1u, abort_flag, &g_linear_chunks_waits); };
+            for (uint32_t x = 0; x < count; ++x) {
+                const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + 1) % kStages, vs = (m + 2) % kStages;
+                if (!landed(m) || !landed(m + 1)) break;
+                // the scores of the chunk before were the last product that its keys were needed for as they came: they are
+                // weighted now, and no arrival on x_full can run two phases ahead of those who weight them
+                if (x > 0 && !bounded_wait(k_ready, (x - 1) & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                tc_fence_after();
+                tc_product<kD, kHalfTile, kHalfTile>(tmem, low + qs * (kTile >> 4), low + ks * (kTile >> 4), kIdescX);
+                tc_commit(x_full);
+                tc_commit(empty0 + 8 * qs);
+                tc_commit(empty0 + 8 * ks);
+                if (!bounded_wait(p_ready, x & 1u, abort_flag, &g_linear_chunks_waits) || !landed(m + 2)) break;
+                tc_fence_after();
+                tc_product_ts<kChunk>(o1_tmem, tmem, v_low + vs * (kTile >> 4), kIdescO, 0u);
+                tc_commit(o1_full);
+                tc_commit(empty0 + 8 * vs);
+            }
+            tc_commit(done_a);
+            drain_phase(done_a, 0);  // every product of this thread has completed
+        } else if (warp == 10 && elect_one()) {
+            // ---------------- O2 = Q S, dS = K_w^T V
+            constexpr uint32_t kIdesc2 = f16_idesc(!kFp16, kChunk, kD, true);
+            constexpr uint32_t kIdescS = f16_idesc(!kFp16, kChunk, kD, true) | kRowsTransposed;
+            const uint32_t q_low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
+            // 128 rows of K_w^T; D = 64: its 64 rows twice
+            const uint32_t k_low = desc_low(ring, kD == 128 ? kHalfTile : 0), rest_low = desc_low(smem_u32(rest_tile), kD == 128 ? kHalfTile : 0);
+            const uint32_t state_low = desc_low(smem_u32(state_tile), kD * kSwizzleRow);
+            auto landed = [&](uint32_t m) { return bounded_wait(full0 + 8 * (m % kStages), (m / kStages) & 1u, abort_flag, &g_linear_chunks_waits); };
+            for (uint32_t x = 0; x < count; ++x) {
+                const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + kTiles - 2) % kStages, vs = (m + kTiles - 1) % kStages;
+                if (kOutputs) {
+                    if (!landed(m) || !bounded_wait(s_ready, x & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                    if (x > 0 && !bounded_wait(o_free, (x - 1) & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (uint32_t kk = 0; kk < kD / 16; ++kk) {
+                        const uint32_t a = q_low + qs * (kTile >> 4) + ((kk / 4 * kHalfTile + kk % 4 * 32) >> 4), b = state_low + kk * (2048 >> 4);
+                        if (kk == 0)
+                            tc_mma_low<false>(o2_tmem, a, b, kIdesc2);
+                        else
+                            tc_mma_low<true>(o2_tmem, a, b, kIdesc2);
+                    }
+                    tc_commit(o2_full);
+                    tc_commit(empty0 + 8 * qs);
+                }
+                if (!landed(m + kTiles - 1) || !bounded_wait(k_ready, x & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                // a short chunk among rows of other sequences: the rows behind it are cleared with P
+                if (kOutputs && p.starts && chunk_len(chunk_at(x)) < kChunk && !bounded_wait(p_ready, x & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                tc_fence_after();
+                const uint32_t b = v_low + vs * (kTile >> 4), a = k_low + ks * (kTile >> 4);
+                tc_mma_low<false>(ds_tmem, a, b, kIdescS);
+#pragma unroll
+                for (uint32_t kk = 1; kk < kChunk / 16; ++kk) tc_mma_low<true>(ds_tmem, a + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescS);
+#pragma unroll
+                for (uint32_t kk = 0; kk < kChunk / 16; ++kk)
+                    tc_mma_low<true>(ds_tmem, rest_low + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescS);
+                tc_commit(ds_full);
+                tc_commit(empty0 + 8 * ks);
+                tc_commit(empty0 + 8 * vs);
+            }
+            tc_commit(done_b);
+            drain_phase(done_b, 0);
+        }
+    } else if (warp < 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if (kOutputs) {
+            // ---------------- P and the output: a thread a row
+            const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
+            const float c = decay * kLog2e;
+            if (warp == 0) decays[lane] = ex2(-c * float(p.reverse ? lane : 31 - lane));
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // these four warps, before any wait
+            float age_factor = 0.f;
+            for (uint32_t x = 0; x < count; ++x) {
+                const uint32_t at = chunk_at(x), len = chunk_len(at);
+                const bool valid = a < len;
+                if (x == 0 || len < kChunk || p.reverse) age_factor = p.out_scale * expf(-decay * float(p.reverse ? int(len) - 1 - int(a) : int(a) + 1));
+                bool ok = bounded_wait(x_full, x & 1u, abort_flag, &g_linear_chunks_waits);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                const float unit_scale = p.out_scale * p.kv_scale;
+                float row_factor = 1.f;  // fp16: the row is kept times its inverse
+                auto weighted = [&](uint32_t (&r)[32], uint32_t j) {
+                    if (j == quarter) {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            const int gone = p.reverse ? y - int(lane) : int(lane) - y;
+                            const float w = ex2(-c * float(max(gone, 0))) * unit_scale;
+                            r[y] = gone >= 0 ? __float_as_uint(__uint_as_float(r[y]) * w) : 0u;
+                        }
+                    } else {
+                        const int gone = p.reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
+                        const float f = ex2(-c * float(gone)) * unit_scale;
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4) {
+                            const float4 t = *reinterpret_cast<const float4*>(decays + y);
+                            r[y] = __float_as_uint(__uint_as_float(r[y]) * (t.x * f));
+                            r[y + 1] = __float_as_uint(__uint_as_float(r[y + 1]) * (t.y * f));
+                            r[y + 2] = __float_as_uint(__uint_as_float(r[y + 2]) * (t.z * f));
+                            r[y + 3] = __float_as_uint(__uint_as_float(r[y + 3]) * (t.w * f));
+                        }
+                    }
+                };
+                auto seen = [&](uint32_t j) { return p.reverse ? j >= quarter : j <= quarter; };
+                float to_half = 1.f;
+                if (kFp16) {
+                    float most = 0.f;
+#pragma unroll 1
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        if (!seen(j)) continue;
+                        uint32_t r[32];
+                        tc_ld32(tmem + lane_base + j * 32, r);
+                        tc_wait_ld();
+                        tc_landed(r);
+                        weighted(r, j);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) most = fmaxf(most, fabsf(__uint_as_float(r[y])));
+                    }
+                    to_half = up_scale(most);
+                    row_factor = inverse(to_half);
+                }
+#pragma unroll 1
+                for (uint32_t j = 0; j < 4; ++j) {
+                    uint32_t w[16];
+                    if (seen(j)) {
+                        uint32_t r[32];
+                        tc_ld32(tmem + lane_base + j * 32, r);
+                        tc_wait_ld();
+                        tc_landed(r);
+                        weighted(r, j);
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) w[y] = pack2<kF>(__uint_as_float(r[2 * y]) * to_half, __uint_as_float(r[2 * y + 1]) * to_half);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) w[y] = 0u;
+                    }
+                    tc_st16(tmem + lane_base + j * 16, w);
+                }
+                if (p.starts && len < kChunk) {  // rows of other sequences, whose V may be anything
+                    const uint32_t m = x * kTiles + 2;
+                    ok = bounded_wait(full0 + 8 * (m % kStages), (m / kStages) & 1u, abort_flag, &g_linear_chunks_waits);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    if (!valid) {
+                        uint4* v = reinterpret_cast<uint4*>(smem + (m % kStages) * size_t(kTile) + a * kSwizzleRow);
+                        for (int z = 0; z < kD / 64; ++z)
+                            for (int y = 0; y < 8; ++y) v[z * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_shared();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready);
+                ok = bounded_wait(o1_full, x & 1u, abort_flag, &g_linear_chunks_waits) &&
+                     bounded_wait(o2_full, x & 1u, abort_flag, &g_linear_chunks_waits);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                const float f2 = age_factor * (kFp16 ? state_factor[x & 1u] : 1.f);
+                uint8_t* dst = p.out.base[g] + int64_t(seq.b) * p.out.b + (seq.first + at + (valid ? a : 0)) * p.out.t + int64_t(h) * p.out.h;
+#pragma unroll 1
+                for (int z = 0; z < kD; z += 32) {
+                    uint32_t r1[32], r2[32];
+                    tc_ld32(o1_tmem + lane_base + z, r1);
+                    tc_ld32(o2_tmem + lane_base + z, r2);
+                    tc_wait_ld();
+                    tc_landed(r1);
+                    tc_landed(r2);
+                    if (z + 32 == kD) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_free);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8) {
+                        uint4 w;
+                        uint32_t* o = &w.x;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = y + 2 * i;
+                            o[i] = pack2<kF>(fmaf(__uint_as_float(r2[e]), f2, __uint_as_float(r1[e]) * row_factor),
+                                             fmaf(__uint_as_float(r2[e + 1]), f2, __uint_as_float(r1[e + 1]) * row_factor));
+                        }
+                        if (valid) *reinterpret_cast<uint4*>(dst + (z + y) * 2) = w;
+                    }
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ---------------- the state: a thread a row of it (D = 64: half a row), and a row of the chunk's keys
+        constexpr int kCols = kD == 128 ? 128 : 32;
+        const uint32_t t = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
+        const uint32_t row = t % kD, col = kD == 128 ? 0 : t / 64 * 32;
+        Largest most{largest, largest_bar, 0};
+        float s[kCols];
+        const int64_t own = (int64_t(seq.slot) * heads + head) * (kD * kD);
+        // in front of a segment; the state itself only where there is one segment: another one's CTA may write it
+        float* const parts = cp.parts + (int64_t(unit) * cp.segments + seg) * (kD * kD);
+        const bool joined = kOutputs && chunks > cp.seg_chunks;
+        const float* from = joined ? (seg > 0 || p.state ? parts : nullptr) : kOutputs && p.state ? p.state + own : nullptr;
+        if (!from) {
+#pragma unroll
+            for (int y = 0; y < kCols; ++y) s[y] = 0.f;
+        } else if (!joined && p.transposed) {
+#pragma unroll
+            for (int y = 0; y < kCols; ++y) s[y] = from[(col + y) * kD + row];
+        } else {
+#pragma unroll
+            for (int y = 0; y < kCols; y += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(from + row * kD + col + y);
+                s[y] = v.x, s[y + 1] = v.y, s[y + 2] = v.z, s[y + 3] = v.w;
+            }
+        }
+        bool ok = true;
+        for (uint32_t x = 0; x < count; ++x) {
+            const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2, ks = m % kStages;
+            if (kOutputs) {
+                // QS of the chunk before has completed: ds_full
+                float to_half = 1.f;
+                if (kFp16) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int y = 0; y < kCols; ++y) v = fmaxf(v, fabsf(s[y]));
+                    if (!(ok = most.of(v, quarter, lane, abort_flag))) break;
+                    to_half = up_scale(v);
+                    if (t == 0) state_factor[x & 1u] = inverse(to_half);
+                }
+                uint8_t* dst = state_tile + row * kSwizzleRow;
+#pragma unroll
+                for (int y = 0; y < kCols; y += 8) {
+                    uint4 w;
+                    w.x = pack2<kF>(s[y] * to_half, s[y + 1] * to_half);
+                    w.y = pack2<kF>(s[y + 2] * to_half, s[y + 3] * to_half);
+                    w.z = pack2<kF>(s[y + 4] * to_half, s[y + 5] * to_half);
+                    w.w = pack2<kF>(s[y + 6] * to_half, s[y + 7] * to_half);
+                    const uint32_t e = col + y;
+                    *reinterpret_cast<uint4*>(dst + e / 64 * (kD * kSwizzleRow) + ((e % 64 / 8) ^ (row & 7u)) * 16) = w;
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_ready);
+                ok = bounded_wait(x_full, x & 1u, abort_flag, &g_linear_chunks_waits);  // the scores no longer need K
+            }
+            ok = ok && bounded_wait(full0 + 8 * ks, (m / kStages) & 1u, abort_flag, &g_linear_chunks_waits);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            const float w = t < len ? expf(-decay * float(p.reverse ? t + 1 : len - 1 - t)) : 0.f;
+            uint8_t* key = smem + ks * size_t(kTile) + t * kSwizzleRow;
+            uint8_t* rest = rest_tile + t * kSwizzleRow;
+            float key_scale = w, back = p.kv_scale;
+            if (kFp16) {
+                float v = 0.f;
+#pragma unroll 1
+                for (int y = 0; y < kD / 8; ++y) {
+                    const uint4 k = *reinterpret_cast<const uint4*>(key + y / 8 * kHalfTile + ((uint32_t(y) % 8) ^ (t & 7u)) * 16);
+                    const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float lo, hi;
+                        unpack2<kF>(kw[i], lo, hi);
+                        v = fmaxf(v, fmaxf(fabsf(lo), fabsf(hi)));
+                    }
+                }
+                v = t < len ? v * w : 0.f;
+                if (!(ok = most.of(v, quarter, lane, abort_flag))) break;
+                const float to_half = up_scale(v);
+                key_scale = w * to_half;
+                back = p.kv_scale * inverse(to_half);
+            }
+#pragma unroll 4
+            for (int y = 0; y < kD / 8; ++y) {
+                uint4* at = reinterpret_cast<uint4*>(key + y / 8 * kHalfTile + ((uint32_t(y) % 8) ^ (t & 7u)) * 16);
+                const uint4 k = *at;
+                const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
+                uint32_t a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi, lo1, hi1;
+                    unpack2<kF>(kw[i], lo, hi);
+                    lo *= key_scale;
+                    hi *= key_scale;
+                    a[i] = pack2<kF>(lo, hi);
+                    unpack2<kF>(a[i], lo1, hi1);
+                    b[i] = pack2<kF>(lo - lo1, hi - hi1);
+                    if (t >= len) a[i] = b[i] = 0u;
+                }
+                *at = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4*>(rest + y / 8 * kHalfTile + ((uint32_t(y) % 8) ^ (t & 7u)) * 16) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+            fence_async_shared();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(k_ready);
+            const Fade fade(decay * float(len));
+            ok = bounded_wait(ds_full, x & 1u, abort_flag, &g_linear_chunks_waits);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int z = 0; z < kCols; z += 32) {
+                uint32_t r[32];
+                tc_ld32(ds_tmem + lane_base + col + z, r);
+                tc_wait_ld();
+                tc_landed(r);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) s[z + y] = fade.of(s[z + y], __uint_as_float(r[y]) * back);
+            }
+        }
+        if (ok && !*abort_flag) {
+            float* to = !kOutputs ? parts + kD * kD  // what is in front of the next one
+                        : last && p.final_state ? p.final_state + own : nullptr;
+            if (to && kOutputs && p.transposed) {
+#pragma unroll
+                for (int y = 0; y < kCols; ++y) to[(col + y) * kD + row] = s[y];
+            } else if (to) {
+#pragma unroll
+                for (int y = 0; y < kCols; y += 4) *reinterpret_cast<float4*>(to + row * kD + col + y) = make_float4(s[y], s[y + 1], s[y + 2], s[y + 3]);
+            }
+        }
+    }
+    }
+    // teardown: every product has completed (their threads drained them) and every TMEM access has finished before
+    // the columns are freed
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The sums of the segments, run up to the states in front of them: parts[0] of a head becomes the state that the sequence
+// starts from (where there is one), parts[1], what segment 0 adds, the state in front of segment 1, and so on.  Four
+// elements a thread.
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearPass p, float* parts, uint32_t segments, uint32_t seg_chunks) {
+    grid_dependency_wait();
+    const uint32_t size = p.D * p.D, blocks = size / 1024, heads = p.P * p.Hl;
+    const uint32_t unit = blockIdx.x / blocks, e = (blockIdx.x % blocks * 256 + threadIdx.x) * 4, head = unit % heads, n = unit / heads;
+    unsigned unused = 0;
+    const LinearSequence seq = linear_sequence(p, n, p.starts ? &g_linear_chunks_status : &unused);
+    if (!seq.ok) return;
+    const uint32_t chunks = (seq.len + kChunk - 1) / kChunk, used = (chunks + seg_chunks - 1) / seg_chunks;
+    if (used < 2) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.state) {
+        const float* from = p.state + (int64_t(seq.slot) * heads + head) * size;
+        const uint32_t row = e / p.D, col = e % p.D;
+        s = p.transposed ? make_float4(from[col * p.D + row], from[(col + 1) * p.D + row], from[(col + 2) * p.D + row], from[(col + 3) * p.D + row])
+                         : *reinterpret_cast<const float4*>(from + e);
+    }
+    const float decay = p.decay[head];
+    float4* at = reinterpret_cast<float4*>(parts + int64_t(unit) * segments * size + e);
+    if (p.state) *at = s;
+    const uint32_t whole = seg_chunks * kChunk, short_by = chunks * kChunk - seq.len;
+    const Fade fade(decay * float(whole)), begin(decay * float(p.reverse ? whole - short_by : whole));
+    for (uint32_t x = 0; x + 1 < used; ++x) {
+        at += size / 4;
+        const float4 add = *at;
+        const Fade& f = x == 0 ? begin : fade;
+        s = make_float4(f.of(s.x, add.x), f.of(s.y, add.y), f.of(s.z, add.z), f.of(s.w, add.w));
+        *at = s;
+    }
+}
+
+template <Fused kF, int kD, bool kOutputs>
+cudaError_t launch(const LinearChunkParams& p, uint32_t grid, cudaStream_t stream) {
+    const size_t smem = Shape<kD, kOutputs>::kSmem;
+    auto kernel = linear_chunks_kernel<kF, kD, kOutputs>;
+    // setting it twice is harmless; the cost is a fraction of a microsecond
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kernel, grid, kThreadsC, smem, stream, p);
+}
+
+template <Fused kF, int kD>
+cudaError_t launch_all(const LinearChunkParams& p, cudaStream_t stream, int* launches) {
+    const uint32_t units = p.p.N * p.p.P * p.p.Hl;
+    cudaError_t e;
+    if (p.segments > 1) {
+        if ((e = launch<kF, kD, false>(p, units * (p.segments - 1), stream)) != cudaSuccess) return e;
+        if ((e = launch_overlapped(linear_join_kernel, units * (kD * kD / 1024), 256, 0, stream, p.p, p.parts, p.segments, p.seg_chunks)) !=
+            cudaSuccess)
+            return e;
+        *launches += 2;
+    }
+    if ((e = launch<kF, kD, true>(p, units * p.segments, stream)) != cudaSuccess) return e;
+    *launches += 1;
+    return cudaSuccess;
+}
+
+cudaError_t read_word(const unsigned& symbol, unsigned* out, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, symbol, sizeof(unsigned));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(symbol, &zero, sizeof(unsigned));
+}
+
+}  // namespace
+
+cudaError_t launch_linear_chunks(const LinearChunkParams& p, bool bf16, cudaStream_t stream, int* launches) {
+    *launches = 0;
+    if (p.p.D == 64) return bf16 ? launch_all<Fused::kBF16, 64>(p, stream, launches) : launch_all<Fused::kFP16, 64>(p, stream, launches);
+    return bf16 ? launch_all<Fused::kBF16, 128>(p, stream, launches) : launch_all<Fused::kFP16, 128>(p, stream, launches);
+}
+
+cudaError_t read_linear_chunks_status(unsigned* out, unsigned* waits, bool clear) {
+    const cudaError_t e = read_word(g_linear_chunks_status, out, clear);
+    return e != cudaSuccess ? e : read_word(g_linear_chunks_waits, waits, clear);
+}
+
+}  // namespace tfu

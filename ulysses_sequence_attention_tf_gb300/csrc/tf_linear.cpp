@@ -70,12 +70,62 @@ tfu::LinearPass pass_of(const tf_linear& a) {
     return p;
 }
 
-size_t workspace_of(const tfu::LinearPass&) { return 0; }
+// Up to this many tokens of a sequence go token by token; more in chunks.
+constexpr uint32_t kStepsMost = 8;
 
-tf_status run(const tfu::LinearPass& p, bool bf16, void*, cudaStream_t stream) {
-    const cudaError_t e = tfu::launch_linear_steps(p, bf16, stream);
+// How the sequences are cut.  A CTA runs alone on its SM; `units` sequences and heads of `chunks` chunks each.  In chunks of
+// time, a CTA's start costs kStart, the sums of a segment kSums of a chunk each (K and V only), their join kJoin.
+struct Cut {
+    uint32_t segments = 1, seg_chunks = 0;
+};
+Cut plan_cut(uint64_t units, uint32_t chunks) {
+    constexpr double kStart = 1.5, kSums = 0.6, kJoin = 1.5;
+    Cut best;
+    double least = 0;
+    for (uint32_t want = 1; want <= chunks && want <= 64; ++want) {
+        const uint32_t size = (chunks + want - 1) / want, n = (chunks + size - 1) / size;
+        if (n != want) continue;
+        auto rounds = [&](uint64_t ctas) { return double((ctas + tfu::kAttnSms - 1) / tfu::kAttnSms); };
+        const double cost = rounds(units * n) * (size + kStart) + (n > 1 ? rounds(units * (n - 1)) * (kSums * size + kStart) + kJoin : 0);
+        if (want == 1 || cost < least) {
+            least = cost;
+            best.segments = n;
+            best.seg_chunks = size;
+        }
+    }
+    return best;
+}
+Cut cut_of(const tfu::LinearPass& p) {
+    if (p.most <= kStepsMost) return {};
+    return plan_cut(uint64_t(p.N) * p.P * p.Hl, (p.most + tfu::kLinearChunk - 1) / tfu::kLinearChunk);
+}
+
+size_t workspace_of(const tfu::LinearPass& p) {
+    const uint32_t segments = cut_of(p).segments;
+    return segments > 1 ? size_t(segments) * p.N * p.P * p.Hl * p.D * p.D * sizeof(float) : 0;
+}
+
+tf_status run(const tfu::LinearPass& p, bool bf16, void* workspace, cudaStream_t stream) {
+    int launches = 1;
+    cudaError_t e;
+    if (p.most <= kStepsMost) {
+        e = tfu::launch_linear_steps(p, bf16, stream);
+    } else {
+        tfu::LinearChunkParams c{};
+        const uint32_t B = p.starts ? 1 : p.N;
+        if (!tfu::encode_group_maps(&c.q, p.q, p.P, B, p.S, p.Hl, p.D, tfu::kLinearChunk, bf16) ||
+            !tfu::encode_group_maps(&c.k, p.k, p.P, B, p.S, p.Hl, p.D, tfu::kLinearChunk, bf16) ||
+            !tfu::encode_group_maps(&c.v, p.v, p.P, B, p.S, p.Hl, p.D, tfu::kLinearChunk, bf16))
+            return fail(TF_ERR_UNSUPPORTED, "the driver refuses a tensor map of these views");
+        c.p = p;
+        const Cut cut = cut_of(p);
+        c.segments = cut.segments;
+        c.seg_chunks = cut.seg_chunks;
+        c.parts = static_cast<float*>(workspace);
+        e = tfu::launch_linear_chunks(c, bf16, stream, &launches);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "launching linear attention");
-    count_launches(1);
+    count_launches(launches);
     return TF_OK;
 }
 
