@@ -68,6 +68,7 @@ struct LinearChunkParams {
     GroupMaps q, k, v;  // boxes of 128 tokens
     LinearPass p;
     uint32_t segments, seg_chunks;
+    uint32_t wide_out;  // rows of out are 32-byte aligned
     float* parts;       // workspace [N * H][segments][D][D], used where there are several
 };
 cudaError_t launch_linear_chunks(const LinearChunkParams& p, bool bf16, cudaStream_t stream, int* launches);

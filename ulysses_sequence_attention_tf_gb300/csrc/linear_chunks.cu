@@ -6,18 +6,19 @@
 //   S    <- lambda^L S + kv_scale sum_b (lambda^(L - 1 - b) k_b)^T v_b
 //   reverse, the last chunk first: b >= a, lambda^(b - a), lambda^(L - 1 - a) q_a S, lambda^(b + 1) k_b
 //
-// -- four products of 128 x 128 x D or 128 x D x D.  A CTA of 384 threads walks the chunks of one head (or of a segment
-// of them, below):
-//  * warp 8, one lane: TMA producer.  Q, K, V tiles through a ring of stages.
-//  * warp 9, one lane: X = Q K^T, then O1 = P V with P from TMEM.
-//  * warp 10, one lane: O2 = Q S, then dS = K_w^T V twice: K_w is kept as two 16-bit tiles.
-//  * warps 0-3: a thread a row of the chunk.  P = X times the decays and the mask, in 16 bits over the scores; then
-//    the row of O1 + lambda^(a + 1) O2 to memory.
-//  * warps 4-7: a thread a row of S (D = 64: half a row; dS comes twice then), in registers in fp32.  S in 16 bits into
-//    shared memory for O2; the chunk's keys times their decay, in place and the rest in a tile beside; dS into S.
+// -- four products of 128 x 128 x D or 128 x D x D.  A CTA of five warpgroups walks the chunks of one head (or of a segment
+// of them, below), each of them at its own step:
+//  * warps 0-3: a thread a row of the chunk.  P = X times the decays and the mask, in 16 bits over the scores.
+//  * warps 4-7: a thread a row of the output, O1 + lambda^(a + 1) O2, to memory.
+//  * warps 8-11: a thread a row of S (D = 64: half a row; dS comes twice then), in registers in fp32.  S in 16 bits into
+//    shared memory for O2, and dS into S.
+//  * warps 12-15: a thread a row of the chunk's keys, K_w = K times its decay, in place and the rest in tiles beside.
+//  * warp 16, one lane: TMA producer.  Q, K, V tiles through a ring of stages.
+//  * warp 17, one lane: X = Q K^T, then O1 = P V with P from TMEM.
+//  * warp 18, one lane: O2 = Q S, then dS = K_w^T V.
 // Each chunk's dS starts at zero and is added to S in fp32 with one rounding, so what the tensor cores' sums drop does not
-// add up over the chunks.  K_w needs the second tile because S outlives the chunk: its fp32 is worth 2^-17 (bf16) or
-// 2^-22 (fp16) of a key, while P and S only enter the chunk's own output, in 16 bits like it.
+// add up over the chunks.  K_w is a sum of three bf16 or two fp16 numbers, because S is fp32 and outlives the chunk: two bf16
+// ones left it 2.4e-6 off, three 3e-7.  P and S only enter the chunk's own output, in 16 bits like it.
 // fp16: P is scaled by a power of two by its row, S and K_w by that of their largest value, so that none of them
 // leaves fp16's normal range.
 //
@@ -35,17 +36,19 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreadsC = 384;
+constexpr int kThreadsC = 640;
 constexpr uint32_t kChunk = kLinearChunk;
 constexpr uint32_t kHalfTile = kChunk * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
 
-template <int kD, bool kOutputs>
+template <Fused kF, int kD, bool kOutputs>
 struct Shape {
     static constexpr uint32_t kTile = kHalfTile * (kD / 64);
     static constexpr uint32_t kStateTile = kD * kSwizzleRow * (kD / 64);
-    static constexpr int kTiles = kOutputs ? 3 : 2;  // a chunk's
-    static constexpr int kStages = kD == 128 ? (kOutputs ? 5 : 6) : 9;
-    static constexpr size_t kSmem = (kStages + 1) * size_t(kTile) + (kOutputs ? kStateTile : 0) + 1024 + 1024;  // barriers, alignment
+    static constexpr int kTiles = kOutputs ? 3 : 2;                      // a chunk's
+    static constexpr int kRests = kF == Fused::kBF16 ? 2 : 1;            // of K_w
+    static constexpr int kStages = kD == 128 ? (kOutputs ? 6 : 7) - kRests : 9;
+    static constexpr size_t kBars = 2048;
+    static constexpr size_t kSmem = (kStages + kRests) * size_t(kTile) + (kOutputs ? kStateTile : 0) + kBars + 1024;  // and alignment
 };
 
 constexpr uint32_t kRowsTransposed = 1u << 15;  // of f16_idesc: A MN-major
@@ -79,28 +82,31 @@ __device__ __forceinline__ float inverse(float power_of_two) { return __uint_as_
 
 template <Fused kF, int kD, bool kOutputs>
 __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
-    using Sh = Shape<kD, kOutputs>;
+    using Sh = Shape<kF, kD, kOutputs>;
     constexpr uint32_t kTile = Sh::kTile;
-    constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles;
+    constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles, kRests = Sh::kRests;
     constexpr bool kFp16 = kF == Fused::kFP16;
     const LinearPass& p = cp.p;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* rest_tile = smem + kStages * size_t(kTile);  // of K_w
-    uint8_t* state_tile = rest_tile + kTile;
+    uint8_t* rest_tiles = smem + kStages * size_t(kTile);  // of K_w
+    uint8_t* state_tile = rest_tiles + kRests * kTile;
     uint64_t* bars = reinterpret_cast<uint64_t*>(state_tile + (kOutputs ? Sh::kStateTile : 0));
     const uint32_t ring = smem_u32(smem);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
     const uint32_t x_full = empty0 + 8 * kStages, p_ready = x_full + 8, o1_full = p_ready + 8, o2_full = o1_full + 8,
-                   o_free = o2_full + 8, s_ready = o_free + 8, k_ready = s_ready + 8, ds_full = k_ready + 8, done_a = ds_full + 8,
-                   done_b = done_a + 8, largest_bar = done_b + 8;
-    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 12);
-    float* decays = floats;            // [32]: lambda^(31 - r), reverse: lambda^r
-    float* state_factor = floats + 32;  // [2], by parity of the chunk: what the state's tile is to be multiplied by
-    float* largest = floats + 36;       // [2][4]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 44);
+                   o_free = o2_full + 8, s_ready = o_free + 8, k_ready = s_ready + 8, ds_full = k_ready + 8, ds_free = ds_full + 8,
+                   done_a = ds_free + 8, done_b = done_a + 8, state_largest = done_b + 8, key_largest = state_largest + 8;
+    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 14);
+    float* decays = floats;             // [32]: lambda^(31 - r), reverse: lambda^r
+    float* row_factor = floats + 32;    // fp16, [2][128] by parity of the chunk: what O1's rows are to be multiplied by,
+    float* state_factor = floats + 288;  // [2] O2,
+    float* key_factor = floats + 290;    // [2] dS
+    float* largest = floats + 292;       // [2][2][4]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 308);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4;
+    static_assert((2 * kStages + 14) * 8 + 310 * 4 <= int(Sh::kBars), "barriers and factors");
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4, group = warp / 4;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -115,13 +121,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         mbar_init(s_ready, 4);
         mbar_init(k_ready, 4);
         mbar_init(ds_full, 1);
+        mbar_init(ds_free, 4);
         mbar_init(done_a, 1);
         mbar_init(done_b, 1);
-        mbar_init(largest_bar, 4);
+        mbar_init(state_largest, 4);
+        mbar_init(key_largest, 4);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -145,12 +153,19 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     // chunk x of the unit: its first token and how many it has
     auto chunk_at = [&](uint32_t x) { return (p.reverse ? chunks - 1 - first - x : first + x) * kChunk; };
     auto chunk_len = [&](uint32_t at) { return min(seq.len - at, kChunk); };
+    auto wait = [&](uint32_t bar, uint32_t x) { return bounded_wait(bar, x & 1u, abort_flag, &g_linear_chunks_waits); };
+    auto all_wait = [&](uint32_t bar, uint32_t x) { return bool(__all_sync(0xffffffffu, wait(bar, x))); };
+    auto landed = [&](uint32_t m) { return wait(full0 + 8 * (m % kStages), m / kStages); };  // the ring's tile m
+    auto arrive = [&](uint32_t bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
 
-    if (work) {
-    // 384 * 168 registers at launch = 256 * 216 + 128 * 72
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8 && elect_one()) {
+    // 640 * 96 registers at launch = 128 * (80 + 88 + 192 + 72 + 48)
+    if (!work) {
+    } else if (group == 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 16 && elect_one()) {
             // ---------------- TMA producer
             const CUtensorMap* maps[3] = {&cp.q.m[g], &cp.k.m[g], &cp.v.m[g]};
             uint32_t m = 0;  // tiles loaded
@@ -159,7 +174,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 const int token = int(seq.first + chunk_at(x));
                 for (int y = 0; y < kTiles; ++y, ++m) {
                     const uint32_t s = m % kStages, use = m / kStages;
-                    if (use > 0 && !bounded_wait(empty0 + 8 * s, (use - 1) & 1u, abort_flag, &g_linear_chunks_waits)) {
+                    if (use > 0 && !wait(empty0 + 8 * s, use - 1)) {
                         ok = false;
                         break;
                     }
@@ -171,24 +186,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             // every load has landed before the CTA exits
             for (uint32_t k = m > uint32_t(kStages) ? m - kStages : 0; k < m; ++k)
                 drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
-        } else if (kOutputs && warp == 9 && elect_one()) {
+        } else if (kOutputs && warp == 17 && elect_one()) {
             // ---------------- X = Q K^T, O1 = P V
             constexpr uint32_t kIdescX = f16_idesc(!kFp16, kChunk, kChunk, false);
             constexpr uint32_t kIdescO = f16_idesc(!kFp16, kChunk, kD, true);
             const uint32_t low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
-            auto landed = [&](uint32_t m) { return bounded_wait(full0 + 8 * (m % kStages), (m / kStages) & 1u, abort_flag, &g_linear_chunks_waits); };
             for (uint32_t x = 0; x < count; ++x) {
                 const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + 1) % kStages, vs = (m + 2) % kStages;
                 if (!landed(m) || !landed(m + 1)) break;
-                // the scores of the chunk before were the last product that its keys were needed for as they came: they are
-                // weighted now, and no arrival on x_full can run two phases ahead of those who weight them
-                if (x > 0 && !bounded_wait(k_ready, (x - 1) & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                // the keys of the chunk before are weighted: no arrival on x_full can run two phases ahead of the warps that
+                // wait for it to do so
+                if (x > 0 && !wait(k_ready, x - 1)) break;
                 tc_fence_after();
                 tc_product<kD, kHalfTile, kHalfTile>(tmem, low + qs * (kTile >> 4), low + ks * (kTile >> 4), kIdescX);
                 tc_commit(x_full);
                 tc_commit(empty0 + 8 * qs);
                 tc_commit(empty0 + 8 * ks);
-                if (!bounded_wait(p_ready, x & 1u, abort_flag, &g_linear_chunks_waits) || !landed(m + 2)) break;
+                if (!wait(p_ready, x) || !landed(m + 2) || (x > 0 && !wait(o_free, x - 1))) break;
                 tc_fence_after();
                 tc_product_ts<kChunk>(o1_tmem, tmem, v_low + vs * (kTile >> 4), kIdescO, 0u);
                 tc_commit(o1_full);
@@ -196,20 +210,18 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
             tc_commit(done_a);
             drain_phase(done_a, 0);  // every product of this thread has completed
-        } else if (warp == 10 && elect_one()) {
+        } else if (warp == 18 && elect_one()) {
             // ---------------- O2 = Q S, dS = K_w^T V
             constexpr uint32_t kIdesc2 = f16_idesc(!kFp16, kChunk, kD, true);
             constexpr uint32_t kIdescS = f16_idesc(!kFp16, kChunk, kD, true) | kRowsTransposed;
             const uint32_t q_low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
             // 128 rows of K_w^T; D = 64: its 64 rows twice
-            const uint32_t k_low = desc_low(ring, kD == 128 ? kHalfTile : 0), rest_low = desc_low(smem_u32(rest_tile), kD == 128 ? kHalfTile : 0);
+            const uint32_t k_low = desc_low(ring, kD == 128 ? kHalfTile : 0), rest_low = desc_low(smem_u32(rest_tiles), kD == 128 ? kHalfTile : 0);
             const uint32_t state_low = desc_low(smem_u32(state_tile), kD * kSwizzleRow);
-            auto landed = [&](uint32_t m) { return bounded_wait(full0 + 8 * (m % kStages), (m / kStages) & 1u, abort_flag, &g_linear_chunks_waits); };
             for (uint32_t x = 0; x < count; ++x) {
                 const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + kTiles - 2) % kStages, vs = (m + kTiles - 1) % kStages;
                 if (kOutputs) {
-                    if (!landed(m) || !bounded_wait(s_ready, x & 1u, abort_flag, &g_linear_chunks_waits)) break;
-                    if (x > 0 && !bounded_wait(o_free, (x - 1) & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                    if (!landed(m) || !wait(s_ready, x) || (x > 0 && !wait(o_free, x - 1))) break;
                     tc_fence_after();
 #pragma unroll
                     for (uint32_t kk = 0; kk < kD / 16; ++kk) {
@@ -222,17 +234,19 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     tc_commit(o2_full);
                     tc_commit(empty0 + 8 * qs);
                 }
-                if (!landed(m + kTiles - 1) || !bounded_wait(k_ready, x & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                if (!landed(m + kTiles - 1) || !wait(k_ready, x) || (x > 0 && !wait(ds_free, x - 1))) break;
                 // a short chunk among rows of other sequences: the rows behind it are cleared with P
-                if (kOutputs && p.starts && chunk_len(chunk_at(x)) < kChunk && !bounded_wait(p_ready, x & 1u, abort_flag, &g_linear_chunks_waits)) break;
+                if (kOutputs && p.starts && chunk_len(chunk_at(x)) < kChunk && !wait(p_ready, x)) break;
                 tc_fence_after();
                 const uint32_t b = v_low + vs * (kTile >> 4), a = k_low + ks * (kTile >> 4);
                 tc_mma_low<false>(ds_tmem, a, b, kIdescS);
 #pragma unroll
                 for (uint32_t kk = 1; kk < kChunk / 16; ++kk) tc_mma_low<true>(ds_tmem, a + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescS);
+#pragma unroll 1
+                for (int r = 0; r < kRests; ++r)
 #pragma unroll
-                for (uint32_t kk = 0; kk < kChunk / 16; ++kk)
-                    tc_mma_low<true>(ds_tmem, rest_low + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescS);
+                    for (uint32_t kk = 0; kk < kChunk / 16; ++kk)
+                        tc_mma_low<true>(ds_tmem, rest_low + r * (kTile >> 4) + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescS);
                 tc_commit(ds_full);
                 tc_commit(empty0 + 8 * ks);
                 tc_commit(empty0 + 8 * vs);
@@ -240,85 +254,85 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             tc_commit(done_b);
             drain_phase(done_b, 0);
         }
-    } else if (warp < 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    } else if (group == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (kOutputs) {
-            // ---------------- P and the output: a thread a row
+            // ---------------- P: a thread a row
             const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
-            const float c = decay * kLog2e;
+            const float c = decay * kLog2e, both_scales = p.out_scale * p.kv_scale;
             if (warp == 0) decays[lane] = ex2(-c * float(p.reverse ? lane : 31 - lane));
             asm volatile("bar.sync 1, 128;" ::: "memory");  // these four warps, before any wait
-            float age_factor = 0.f;
-            for (uint32_t x = 0; x < count; ++x) {
-                const uint32_t at = chunk_at(x), len = chunk_len(at);
-                const bool valid = a < len;
-                if (x == 0 || len < kChunk || p.reverse) age_factor = p.out_scale * expf(-decay * float(p.reverse ? int(len) - 1 - int(a) : int(a) + 1));
-                bool ok = bounded_wait(x_full, x & 1u, abort_flag, &g_linear_chunks_waits);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                tc_fence_after();
-                const float unit_scale = p.out_scale * p.kv_scale;
-                float row_factor = 1.f;  // fp16: the row is kept times its inverse
-                auto weighted = [&](uint32_t (&r)[32], uint32_t j) {
-                    if (j == quarter) {
+            // scores of 32 columns times their decays, from column 32 j of the row on
+            auto weighted = [&](uint32_t j, uint64_t (&w)[16]) {
+                uint32_t r[32];
+                tc_ld32(tmem + lane_base + j * 32, r);
+                tc_wait_ld();
+                tc_landed(r);
+                if (j == quarter) {
+                    const float f = both_scales;
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) {
-                            const int gone = p.reverse ? y - int(lane) : int(lane) - y;
-                            const float w = ex2(-c * float(max(gone, 0))) * unit_scale;
-                            r[y] = gone >= 0 ? __float_as_uint(__uint_as_float(r[y]) * w) : 0u;
-                        }
-                    } else {
-                        const int gone = p.reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
-                        const float f = ex2(-c * float(gone)) * unit_scale;
-#pragma unroll
-                        for (int y = 0; y < 32; y += 4) {
-                            const float4 t = *reinterpret_cast<const float4*>(decays + y);
-                            r[y] = __float_as_uint(__uint_as_float(r[y]) * (t.x * f));
-                            r[y + 1] = __float_as_uint(__uint_as_float(r[y + 1]) * (t.y * f));
-                            r[y + 2] = __float_as_uint(__uint_as_float(r[y + 2]) * (t.z * f));
-                            r[y + 3] = __float_as_uint(__uint_as_float(r[y + 3]) * (t.w * f));
-                        }
+                    for (int y = 0; y < 16; ++y) {
+                        const int gone0 = p.reverse ? 2 * y - int(lane) : int(lane) - 2 * y, gone1 = p.reverse ? gone0 + 1 : gone0 - 1;
+                        const float w0 = ex2(-c * float(max(gone0, 0))) * f, w1 = ex2(-c * float(max(gone1, 0))) * f;
+                        w[y] = f2_pack(gone0 >= 0 ? __uint_as_float(r[2 * y]) * w0 : 0.f, gone1 >= 0 ? __uint_as_float(r[2 * y + 1]) * w1 : 0.f);
                     }
-                };
-                auto seen = [&](uint32_t j) { return p.reverse ? j >= quarter : j <= quarter; };
+                } else {
+                    const int gone = p.reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
+                    const float f = ex2(-c * float(gone)) * both_scales;
+                    const uint64_t f2 = f2_pack(f, f);
+#pragma unroll
+                    for (int y = 0; y < 16; y += 2) {
+                        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(decays + 2 * y);
+                        w[y] = f2_mul(f2_pack(__uint_as_float(r[2 * y]), __uint_as_float(r[2 * y + 1])), f2_mul(t.x, f2));
+                        w[y + 1] = f2_mul(f2_pack(__uint_as_float(r[2 * y + 2]), __uint_as_float(r[2 * y + 3])), f2_mul(t.y, f2));
+                    }
+                }
+            };
+            auto seen = [&](uint32_t j) { return p.reverse ? j >= quarter : j <= quarter; };
+            for (uint32_t x = 0; x < count; ++x) {
+                const uint32_t len = chunk_len(chunk_at(x));
+                if (!all_wait(x_full, x)) break;
+                tc_fence_after();
                 float to_half = 1.f;
                 if (kFp16) {
                     float most = 0.f;
 #pragma unroll 1
                     for (uint32_t j = 0; j < 4; ++j) {
                         if (!seen(j)) continue;
-                        uint32_t r[32];
-                        tc_ld32(tmem + lane_base + j * 32, r);
-                        tc_wait_ld();
-                        tc_landed(r);
-                        weighted(r, j);
+                        uint64_t w[16];
+                        weighted(j, w);
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) most = fmaxf(most, fabsf(__uint_as_float(r[y])));
+                        for (int y = 0; y < 16; ++y) {
+                            float lo, hi;
+                            f2_unpack(w[y], lo, hi);
+                            most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
+                        }
                     }
                     to_half = up_scale(most);
-                    row_factor = inverse(to_half);
+                    row_factor[(x & 1u) * kChunk + a] = inverse(to_half);
                 }
 #pragma unroll 1
                 for (uint32_t j = 0; j < 4; ++j) {
-                    uint32_t w[16];
+                    uint32_t o[16];
                     if (seen(j)) {
-                        uint32_t r[32];
-                        tc_ld32(tmem + lane_base + j * 32, r);
-                        tc_wait_ld();
-                        tc_landed(r);
-                        weighted(r, j);
+                        uint64_t w[16];
+                        weighted(j, w);
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) w[y] = pack2<kF>(__uint_as_float(r[2 * y]) * to_half, __uint_as_float(r[2 * y + 1]) * to_half);
+                        for (int y = 0; y < 16; ++y) {
+                            float lo, hi;
+                            f2_unpack(kFp16 ? f2_mul(w[y], f2_pack(to_half, to_half)) : w[y], lo, hi);
+                            o[y] = pack2<kF>(lo, hi);
+                        }
                     } else {
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) w[y] = 0u;
+                        for (int y = 0; y < 16; ++y) o[y] = 0u;
                     }
-                    tc_st16(tmem + lane_base + j * 16, w);
+                    tc_st16(tmem + lane_base + j * 16, o);
                 }
                 if (p.starts && len < kChunk) {  // rows of other sequences, whose V may be anything
                     const uint32_t m = x * kTiles + 2;
-                    ok = bounded_wait(full0 + 8 * (m % kStages), (m / kStages) & 1u, abort_flag, &g_linear_chunks_waits);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    if (!valid) {
+                    if (!__all_sync(0xffffffffu, landed(m))) break;
+                    if (a >= len) {
                         uint4* v = reinterpret_cast<uint4*>(smem + (m % kStages) * size_t(kTile) + a * kSwizzleRow);
                         for (int z = 0; z < kD / 64; ++z)
                             for (int y = 0; y < 8; ++y) v[z * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
@@ -327,13 +341,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 }
                 tc_wait_st();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready);
-                ok = bounded_wait(o1_full, x & 1u, abort_flag, &g_linear_chunks_waits) &&
-                     bounded_wait(o2_full, x & 1u, abort_flag, &g_linear_chunks_waits);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                arrive(p_ready);
+            }
+        }
+    } else if (group == 1) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (kOutputs) {
+            // ---------------- the output: a thread a row
+            const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
+            float age = p.out_scale * expf(-decay * float(a + 1));
+            for (uint32_t x = 0; x < count; ++x) {
+                const uint32_t at = chunk_at(x), len = chunk_len(at);
+                const bool valid = a < len;
+                if (p.reverse) age = p.out_scale * expf(-decay * float(int(len) - 1 - int(a)));
+                if (!all_wait(o1_full, x) || !all_wait(o2_full, x)) break;
                 tc_fence_after();
-                const float f2 = age_factor * (kFp16 ? state_factor[x & 1u] : 1.f);
+                const float f1 = kFp16 ? row_factor[(x & 1u) * kChunk + a] : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
+                const uint64_t f1_2 = f2_pack(f1, f1), f2_2 = f2_pack(f2, f2);
                 uint8_t* dst = p.out.base[g] + int64_t(seq.b) * p.out.b + (seq.first + at + (valid ? a : 0)) * p.out.t + int64_t(h) * p.out.h;
 #pragma unroll 1
                 for (int z = 0; z < kD; z += 32) {
@@ -345,32 +369,40 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     tc_landed(r2);
                     if (z + 32 == kD) {
                         tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(o_free);
+                        arrive(o_free);
                     }
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8) {
-                        uint4 w;
-                        uint32_t* o = &w.x;
+                    for (int y = 0; y < 32; y += 16) {
+                        Vec<32> w;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             const int e = y + 2 * i;
-                            o[i] = pack2<kF>(fmaf(__uint_as_float(r2[e]), f2, __uint_as_float(r1[e]) * row_factor),
-                                             fmaf(__uint_as_float(r2[e + 1]), f2, __uint_as_float(r1[e + 1]) * row_factor));
+                            uint64_t v = f2_pack(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1]));
+                            if (kFp16) v = f2_mul(v, f1_2);
+                            v = f2_fma(f2_pack(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1])), f2_2, v);
+                            float lo, hi;
+                            f2_unpack(v, lo, hi);
+                            w.w[i] = pack2<kF>(lo, hi);
                         }
-                        if (valid) *reinterpret_cast<uint4*>(dst + (z + y) * 2) = w;
+                        if (!valid) continue;
+                        if (cp.wide_out) {
+                            st_stream<32>(dst + (z + y) * 2, w);
+                        } else {
+                            *reinterpret_cast<uint4*>(dst + (z + y) * 2) = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
+                            *reinterpret_cast<uint4*>(dst + (z + y) * 2 + 16) = make_uint4(w.w[4], w.w[5], w.w[6], w.w[7]);
+                        }
                     }
                 }
             }
         }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        // ---------------- the state: a thread a row of it (D = 64: half a row), and a row of the chunk's keys
+    } else if (group == 2) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        // ---------------- the state: a thread a row of it (D = 64: half a row)
         constexpr int kCols = kD == 128 ? 128 : 32;
         const uint32_t t = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
         const uint32_t row = t % kD, col = kD == 128 ? 0 : t / 64 * 32;
-        Largest most{largest, largest_bar, 0};
-        float s[kCols];
+        Largest most{largest, state_largest, 0};
+        uint64_t s[kCols / 2];
         const int64_t own = (int64_t(seq.slot) * heads + head) * (kD * kD);
         // in front of a segment; the state itself only where there is one segment: another one's CTA may write it
         float* const parts = cp.parts + (int64_t(unit) * cp.segments + seg) * (kD * kD);
@@ -378,27 +410,31 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         const float* from = joined ? (seg > 0 || p.state ? parts : nullptr) : kOutputs && p.state ? p.state + own : nullptr;
         if (!from) {
 #pragma unroll
-            for (int y = 0; y < kCols; ++y) s[y] = 0.f;
+            for (int y = 0; y < kCols / 2; ++y) s[y] = 0;
         } else if (!joined && p.transposed) {
 #pragma unroll
-            for (int y = 0; y < kCols; ++y) s[y] = from[(col + y) * kD + row];
+            for (int y = 0; y < kCols / 2; ++y) s[y] = f2_pack(from[(col + 2 * y) * kD + row], from[(col + 2 * y + 1) * kD + row]);
         } else {
 #pragma unroll
-            for (int y = 0; y < kCols; y += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(from + row * kD + col + y);
-                s[y] = v.x, s[y + 1] = v.y, s[y + 2] = v.z, s[y + 3] = v.w;
+            for (int y = 0; y < kCols / 2; y += 2) {
+                const float4 v = *reinterpret_cast<const float4*>(from + row * kD + col + 2 * y);
+                s[y] = f2_pack(v.x, v.y), s[y + 1] = f2_pack(v.z, v.w);
             }
         }
         bool ok = true;
         for (uint32_t x = 0; x < count; ++x) {
-            const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2, ks = m % kStages;
+            const uint32_t len = chunk_len(chunk_at(x));
             if (kOutputs) {
-                // QS of the chunk before has completed: ds_full
+                // the product with the tile's last contents has completed: ds_full of the chunk before
                 float to_half = 1.f;
                 if (kFp16) {
                     float v = 0.f;
 #pragma unroll
-                    for (int y = 0; y < kCols; ++y) v = fmaxf(v, fabsf(s[y]));
+                    for (int y = 0; y < kCols / 2; ++y) {
+                        float lo, hi;
+                        f2_unpack(s[y], lo, hi);
+                        v = fmaxf(v, fmaxf(fabsf(lo), fabsf(hi)));
+                    }
                     if (!(ok = most.of(v, quarter, lane, abort_flag))) break;
                     to_half = up_scale(v);
                     if (t == 0) state_factor[x & 1u] = inverse(to_half);
@@ -406,30 +442,80 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 uint8_t* dst = state_tile + row * kSwizzleRow;
 #pragma unroll
                 for (int y = 0; y < kCols; y += 8) {
-                    uint4 w;
-                    w.x = pack2<kF>(s[y] * to_half, s[y + 1] * to_half);
-                    w.y = pack2<kF>(s[y + 2] * to_half, s[y + 3] * to_half);
-                    w.z = pack2<kF>(s[y + 4] * to_half, s[y + 5] * to_half);
-                    w.w = pack2<kF>(s[y + 6] * to_half, s[y + 7] * to_half);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float lo, hi;
+                        f2_unpack(kFp16 ? f2_mul(s[y / 2 + i], f2_pack(to_half, to_half)) : s[y / 2 + i], lo, hi);
+                        w[i] = pack2<kF>(lo, hi);
+                    }
                     const uint32_t e = col + y;
-                    *reinterpret_cast<uint4*>(dst + e / 64 * (kD * kSwizzleRow) + ((e % 64 / 8) ^ (row & 7u)) * 16) = w;
+                    *reinterpret_cast<uint4*>(dst + e / 64 * (kD * kSwizzleRow) + ((e % 64 / 8) ^ (row & 7u)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_ready);
-                ok = bounded_wait(x_full, x & 1u, abort_flag, &g_linear_chunks_waits);  // the scores no longer need K
+                arrive(s_ready);
             }
-            ok = ok && bounded_wait(full0 + 8 * ks, (m / kStages) & 1u, abort_flag, &g_linear_chunks_waits);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            const float w = t < len ? expf(-decay * float(p.reverse ? t + 1 : len - 1 - t)) : 0.f;
-            uint8_t* key = smem + ks * size_t(kTile) + t * kSwizzleRow;
-            uint8_t* rest = rest_tile + t * kSwizzleRow;
-            float key_scale = w, back = p.kv_scale;
+            const Fade fade(decay * float(len));
+            if (!(ok = all_wait(ds_full, x))) break;
+            tc_fence_after();
+            const float back = kFp16 ? p.kv_scale * key_factor[x & 1u] : p.kv_scale;
+            const uint64_t back2 = f2_pack(back, back), factor2 = f2_pack(fade.factor, fade.factor), whole2 = f2_pack(fade.whole, fade.whole);
+#pragma unroll
+            for (int z = 0; z < kCols; z += 32) {
+                uint32_t r[32];
+                tc_ld32(ds_tmem + lane_base + col + z, r);
+                tc_wait_ld();
+                tc_landed(r);
+                if (z + 32 == kCols) {
+                    tc_fence_before();
+                    arrive(ds_free);
+                }
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    const uint64_t add = f2_mul(f2_pack(__uint_as_float(r[2 * y]), __uint_as_float(r[2 * y + 1])), back2);
+                    s[z / 2 + y] = f2_fma(whole2, s[z / 2 + y], f2_fma(s[z / 2 + y], factor2, add));
+                }
+            }
+        }
+        if (ok && !*abort_flag) {
+            float* to = !kOutputs ? parts + kD * kD  // what is in front of the next one
+                        : last && p.final_state ? p.final_state + own : nullptr;
+            if (to) {
+#pragma unroll
+                for (int y = 0; y < kCols / 2; y += 2) {
+                    float4 v;
+                    f2_unpack(s[y], v.x, v.y);
+                    f2_unpack(s[y + 1], v.z, v.w);
+                    if (kOutputs && p.transposed) {
+                        to[(col + 2 * y) * kD + row] = v.x;
+                        to[(col + 2 * y + 1) * kD + row] = v.y;
+                        to[(col + 2 * y + 2) * kD + row] = v.z;
+                        to[(col + 2 * y + 3) * kD + row] = v.w;
+                    } else {
+                        *reinterpret_cast<float4*>(to + row * kD + col + 2 * y) = v;
+                    }
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---------------- the keys times their decay: a thread a row of the chunk
+        const uint32_t t = quarter * 32 + lane;
+        Largest most{largest + 8, key_largest, 0};
+        for (uint32_t x = 0; x < count; ++x) {
+            const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2;
+            // the scores no longer need K as it came; the products with the rest tiles' last contents have completed
+            if ((kOutputs && !all_wait(x_full, x)) || !__all_sync(0xffffffffu, landed(m)) || (x > 0 && !all_wait(ds_full, x - 1))) break;
+            const bool valid = t < len;
+            float w = valid ? expf(-decay * float(p.reverse ? t + 1 : len - 1 - t)) : 0.f;
+            uint8_t* key = smem + (m % kStages) * size_t(kTile) + t * kSwizzleRow;
+            uint8_t* rest = rest_tiles + t * kSwizzleRow;
+            auto vec = [&](int y) { return y / 8 * kHalfTile + ((uint32_t(y) % 8) ^ (t & 7u)) * 16; };
             if (kFp16) {
                 float v = 0.f;
-#pragma unroll 1
+#pragma unroll 4
                 for (int y = 0; y < kD / 8; ++y) {
-                    const uint4 k = *reinterpret_cast<const uint4*>(key + y / 8 * kHalfTile + ((uint32_t(y) % 8) ^ (t & 7u)) * 16);
+                    const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
                     const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -438,69 +524,47 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                         v = fmaxf(v, fmaxf(fabsf(lo), fabsf(hi)));
                     }
                 }
-                v = t < len ? v * w : 0.f;
-                if (!(ok = most.of(v, quarter, lane, abort_flag))) break;
+                v = valid ? v * w : 0.f;
+                if (!most.of(v, quarter, lane, abort_flag)) break;
                 const float to_half = up_scale(v);
-                key_scale = w * to_half;
-                back = p.kv_scale * inverse(to_half);
+                w *= to_half;
+                if (t == 0) key_factor[x & 1u] = inverse(to_half);
             }
-#pragma unroll 4
+            const uint64_t w2 = f2_pack(w, w);
+#pragma unroll 2
             for (int y = 0; y < kD / 8; ++y) {
-                uint4* at = reinterpret_cast<uint4*>(key + y / 8 * kHalfTile + ((uint32_t(y) % 8) ^ (t & 7u)) * 16);
-                const uint4 k = *at;
+                const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
                 const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
-                uint32_t a[4], b[4];
+                uint32_t part[1 + kRests][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float lo, hi, lo1, hi1;
+                    float lo, hi;
                     unpack2<kF>(kw[i], lo, hi);
-                    lo *= key_scale;
-                    hi *= key_scale;
-                    a[i] = pack2<kF>(lo, hi);
-                    unpack2<kF>(a[i], lo1, hi1);
-                    b[i] = pack2<kF>(lo - lo1, hi - hi1);
-                    if (t >= len) a[i] = b[i] = 0u;
+                    uint64_t v = f2_mul(f2_pack(lo, hi), w2);
+#pragma unroll
+                    for (int r = 0; r <= kRests; ++r) {
+                        f2_unpack(v, lo, hi);
+                        part[r][i] = pack2<kF>(lo, hi);
+                        unpack2<kF>(part[r][i], lo, hi);
+                        v = f2_sub(v, f2_pack(lo, hi));
+                        if (!valid) part[r][i] = 0u;
+                    }
                 }
-                *at = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4*>(rest + y / 8 * kHalfTile + ((uint32_t(y) % 8) ^ (t & 7u)) * 16) = make_uint4(b[0], b[1], b[2], b[3]);
+                *reinterpret_cast<uint4*>(key + vec(y)) = make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]);
+#pragma unroll
+                for (int r = 0; r < kRests; ++r)
+                    *reinterpret_cast<uint4*>(rest + r * kTile + vec(y)) = make_uint4(part[r + 1][0], part[r + 1][1], part[r + 1][2], part[r + 1][3]);
             }
             fence_async_shared();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(k_ready);
-            const Fade fade(decay * float(len));
-            ok = bounded_wait(ds_full, x & 1u, abort_flag, &g_linear_chunks_waits);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int z = 0; z < kCols; z += 32) {
-                uint32_t r[32];
-                tc_ld32(ds_tmem + lane_base + col + z, r);
-                tc_wait_ld();
-                tc_landed(r);
-#pragma unroll
-                for (int y = 0; y < 32; ++y) s[z + y] = fade.of(s[z + y], __uint_as_float(r[y]) * back);
-            }
+            arrive(k_ready);
         }
-        if (ok && !*abort_flag) {
-            float* to = !kOutputs ? parts + kD * kD  // what is in front of the next one
-                        : last && p.final_state ? p.final_state + own : nullptr;
-            if (to && kOutputs && p.transposed) {
-#pragma unroll
-                for (int y = 0; y < kCols; ++y) to[(col + y) * kD + row] = s[y];
-            } else if (to) {
-#pragma unroll
-                for (int y = 0; y < kCols; y += 4) *reinterpret_cast<float4*>(to + row * kD + col + y) = make_float4(s[y], s[y + 1], s[y + 2], s[y + 3]);
-            }
-        }
-    }
     }
     // teardown: every product has completed (their threads drained them) and every TMEM access has finished before
     // the columns are freed
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -541,7 +605,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 
 template <Fused kF, int kD, bool kOutputs>
 cudaError_t launch(const LinearChunkParams& p, uint32_t grid, cudaStream_t stream) {
-    const size_t smem = Shape<kD, kOutputs>::kSmem;
+    const size_t smem = Shape<kF, kD, kOutputs>::kSmem;
     auto kernel = linear_chunks_kernel<kF, kD, kOutputs>;
     // setting it twice is harmless; the cost is a fraction of a microsecond
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));

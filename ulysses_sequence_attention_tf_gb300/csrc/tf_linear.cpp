@@ -121,6 +121,9 @@ tf_status run(const tfu::LinearPass& p, bool bf16, void* workspace, cudaStream_t
         const Cut cut = cut_of(p);
         c.segments = cut.segments;
         c.seg_chunks = cut.seg_chunks;
+        uintptr_t bits = uintptr_t(p.out.b | p.out.t | p.out.h);
+        for (uint32_t g = 0; g < p.P; ++g) bits |= reinterpret_cast<uintptr_t>(p.out.base[g]);
+        c.wide_out = bits % 32 == 0;
         c.parts = static_cast<float*>(workspace);
         e = tfu::launch_linear_chunks(c, bf16, stream, &launches);
     }
