@@ -6,16 +6,16 @@
 //   S    <- lambda^L S + kv_scale sum_b (lambda^(L - 1 - b) k_b)^T v_b
 //   reverse, the last chunk first: b >= a, lambda^(b - a), lambda^(L - 1 - a) q_a S, lambda^(b + 1) k_b
 //
-// -- four products of 128 x 128 x D or 128 x D x D.  A CTA of five warpgroups walks the chunks of one head (or of a segment
+// -- four products of 128 x 128 x D or 128 x D x D.  A CTA of six warpgroups walks the chunks of one head (or of a segment
 // of them, below), each of them at its own step:
 //  * warps 0-3: a thread a row of the chunk.  P = X times the decays and the mask, in 16 bits over the scores.
 //  * warps 4-7: a thread a row of the output, O1 + lambda^(a + 1) O2, to memory.
 //  * warps 8-11: a thread a row of S (D = 64: half a row; dS comes twice then), in registers in fp32.  S in 16 bits into
 //    shared memory for O2, and dS into S.
-//  * warps 12-15: a thread a row of the chunk's keys, K_w = K times its decay, in place and the rest in tiles beside.
-//  * warp 16, one lane: TMA producer.  Q, K, V tiles through a ring of stages.
-//  * warp 17, one lane: X = Q K^T, then O1 = P V with P from TMEM.
-//  * warp 18, one lane: O2 = Q S, then dS = K_w^T V.
+//  * warps 12-19: a thread half a row of the chunk's keys, K_w = K times its decay, in place and the rest in tiles beside.
+//  * warp 20, one lane: TMA producer.  Q, K, V tiles through a ring of stages.
+//  * warp 21, one lane: X = Q K^T, then O1 = P V with P from TMEM.
+//  * warp 22, one lane: O2 = Q S, then dS = K_w^T V.
 // Each chunk's dS starts at zero and is added to S in fp32 with one rounding, so what the tensor cores' sums drop does not
 // add up over the chunks.  K_w is a sum of three bf16 or two fp16 numbers, because S is fp32 and outlives the chunk: two bf16
 // ones left it 2.4e-6 off, three 3e-7.  P and S only enter the chunk's own output, in 16 bits like it.
@@ -36,7 +36,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreadsC = 640;
+constexpr int kThreadsC = 768;
 constexpr uint32_t kChunk = kLinearChunk;
 constexpr uint32_t kHalfTile = kChunk * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
 
@@ -53,20 +53,22 @@ struct Shape {
 
 constexpr uint32_t kRowsTransposed = 1u << 15;  // of f16_idesc: A MN-major
 
-// 128 threads' largest value through shared memory; false if a wait gave up.
+// The largest value of kWarps warps through shared memory; false if a wait gave up.
+template <int kWarps>
 struct Largest {
-    float* slots;  // [2][4]
+    float* slots;  // [2][kWarps]
     uint32_t bar, phase;
-    __device__ bool of(float& v, uint32_t quarter, uint32_t lane, volatile int* abort_flag) {
+    __device__ bool of(float& v, uint32_t warp, uint32_t lane, volatile int* abort_flag) {
         v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-        float* at = slots + phase * 4;
+        float* at = slots + phase * kWarps;
         if (lane == 0) {
-            at[quarter] = v;
+            at[warp] = v;
             mbar_arrive(bar);
         }
         const bool ok = __all_sync(0xffffffffu, bounded_wait(bar, phase, abort_flag, &g_linear_chunks_waits));
         phase ^= 1u;
-        if (ok) v = fmaxf(fmaxf(at[0], at[1]), fmaxf(at[2], at[3]));
+        if (ok)
+            for (int x = 0; x < kWarps; ++x) v = fmaxf(v, at[x]);
         return ok;
     }
 };
@@ -79,6 +81,29 @@ __device__ __forceinline__ float up_scale(float v) {
     return __uint_as_float(uint32_t(min(to, 253)) << 23);
 }
 __device__ __forceinline__ float inverse(float power_of_two) { return __uint_as_float((254u << 23) - __float_as_uint(power_of_two)); }
+
+// tcgen05.wait::ld orders the registers of loads in flight for the compiler too (tc_landed in 16s)
+__device__ __forceinline__ void landed16(uint32_t (&r)[16]) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
+// Takes 16 bits off two numbers and leaves the rest: bf16 by cutting (three parts of 8 bits hold a number of 24), fp16 rounded.
+template <Fused kF>
+__device__ __forceinline__ uint32_t take_part(uint64_t& v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    uint32_t part;
+    if constexpr (kF == Fused::kBF16) {
+        part = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+        v = f2_sub(v, f2_pack(__uint_as_float(__float_as_uint(lo) & 0xffff0000u), __uint_as_float(__float_as_uint(hi) & 0xffff0000u)));
+    } else {
+        part = pack2<kF>(lo, hi);
+        unpack2<kF>(part, lo, hi);
+        v = f2_sub(v, f2_pack(lo, hi));
+    }
+    return part;
+}
 
 template <Fused kF, int kD, bool kOutputs>
 __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
@@ -102,10 +127,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     float* row_factor = floats + 32;    // fp16, [2][128] by parity of the chunk: what O1's rows are to be multiplied by,
     float* state_factor = floats + 288;  // [2] O2,
     float* key_factor = floats + 290;    // [2] dS
-    float* largest = floats + 292;       // [2][2][4]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 308);
+    float* largest = floats + 292;       // [2][4], [2][8]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 316);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 14) * 8 + 310 * 4 <= int(Sh::kBars), "barriers and factors");
+    static_assert((2 * kStages + 14) * 8 + 318 * 4 <= int(Sh::kBars), "barriers and factors");
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4, group = warp / 4;
 
     if (threadIdx.x == 0) {
@@ -119,17 +144,17 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         mbar_init(o2_full, 1);
         mbar_init(o_free, 4);
         mbar_init(s_ready, 4);
-        mbar_init(k_ready, 4);
+        mbar_init(k_ready, 8);
         mbar_init(ds_full, 1);
         mbar_init(ds_free, 4);
         mbar_init(done_a, 1);
         mbar_init(done_b, 1);
         mbar_init(state_largest, 4);
-        mbar_init(key_largest, 4);
+        mbar_init(key_largest, 8);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 17) {
+    if (warp == 21) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -161,11 +186,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         if (lane == 0) mbar_arrive(bar);
     };
 
-    // 640 * 96 registers at launch = 128 * (80 + 88 + 192 + 72 + 48)
+    // 768 * 80 registers at launch = 128 * (80 + 64 + 192 + 48 + 48 + 48)
     if (!work) {
-    } else if (group == 4) {
+    } else if (group == 5) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 16 && elect_one()) {
+        if (warp == 20 && elect_one()) {
             // ---------------- TMA producer
             const CUtensorMap* maps[3] = {&cp.q.m[g], &cp.k.m[g], &cp.v.m[g]};
             uint32_t m = 0;  // tiles loaded
@@ -186,7 +211,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             // every load has landed before the CTA exits
             for (uint32_t k = m > uint32_t(kStages) ? m - kStages : 0; k < m; ++k)
                 drain_phase(full0 + 8 * (k % kStages), (k / kStages) & 1u);
-        } else if (kOutputs && warp == 17 && elect_one()) {
+        } else if (kOutputs && warp == 21 && elect_one()) {
             // ---------------- X = Q K^T, O1 = P V
             constexpr uint32_t kIdescX = f16_idesc(!kFp16, kChunk, kChunk, false);
             constexpr uint32_t kIdescO = f16_idesc(!kFp16, kChunk, kD, true);
@@ -210,7 +235,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
             tc_commit(done_a);
             drain_phase(done_a, 0);  // every product of this thread has completed
-        } else if (warp == 18 && elect_one()) {
+        } else if (warp == 22 && elect_one()) {
             // ---------------- O2 = Q S, dS = K_w^T V
             constexpr uint32_t kIdesc2 = f16_idesc(!kFp16, kChunk, kD, true);
             constexpr uint32_t kIdescS = f16_idesc(!kFp16, kChunk, kD, true) | kRowsTransposed;
@@ -255,7 +280,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             drain_phase(done_b, 0);
         }
     } else if (group == 0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (kOutputs) {
             // ---------------- P: a thread a row
             const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
@@ -345,7 +369,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
         }
     } else if (group == 1) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (kOutputs) {
             // ---------------- the output: a thread a row
             const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
@@ -360,37 +384,33 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 const uint64_t f1_2 = f2_pack(f1, f1), f2_2 = f2_pack(f2, f2);
                 uint8_t* dst = p.out.base[g] + int64_t(seq.b) * p.out.b + (seq.first + at + (valid ? a : 0)) * p.out.t + int64_t(h) * p.out.h;
 #pragma unroll 1
-                for (int z = 0; z < kD; z += 32) {
-                    uint32_t r1[32], r2[32];
-                    tc_ld32(o1_tmem + lane_base + z, r1);
-                    tc_ld32(o2_tmem + lane_base + z, r2);
+                for (int z = 0; z < kD; z += 16) {
+                    uint32_t r1[16], r2[16];
+                    tc_ld16(o1_tmem + lane_base + z, r1);
+                    tc_ld16(o2_tmem + lane_base + z, r2);
                     tc_wait_ld();
-                    tc_landed(r1);
-                    tc_landed(r2);
-                    if (z + 32 == kD) {
+                    landed16(r1);
+                    landed16(r2);
+                    if (z + 16 == kD) {
                         tc_fence_before();
                         arrive(o_free);
                     }
+                    Vec<32> w;
 #pragma unroll
-                    for (int y = 0; y < 32; y += 16) {
-                        Vec<32> w;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int e = y + 2 * i;
-                            uint64_t v = f2_pack(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1]));
-                            if (kFp16) v = f2_mul(v, f1_2);
-                            v = f2_fma(f2_pack(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1])), f2_2, v);
-                            float lo, hi;
-                            f2_unpack(v, lo, hi);
-                            w.w[i] = pack2<kF>(lo, hi);
-                        }
-                        if (!valid) continue;
-                        if (cp.wide_out) {
-                            st_stream<32>(dst + (z + y) * 2, w);
-                        } else {
-                            *reinterpret_cast<uint4*>(dst + (z + y) * 2) = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
-                            *reinterpret_cast<uint4*>(dst + (z + y) * 2 + 16) = make_uint4(w.w[4], w.w[5], w.w[6], w.w[7]);
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        uint64_t v = f2_pack(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1]));
+                        if (kFp16) v = f2_mul(v, f1_2);
+                        v = f2_fma(f2_pack(__uint_as_float(r2[2 * i]), __uint_as_float(r2[2 * i + 1])), f2_2, v);
+                        float lo, hi;
+                        f2_unpack(v, lo, hi);
+                        w.w[i] = pack2<kF>(lo, hi);
+                    }
+                    if (!valid) continue;
+                    if (cp.wide_out) {
+                        st_stream<32>(dst + z * 2, w);
+                    } else {
+                        *reinterpret_cast<uint4*>(dst + z * 2) = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
+                        *reinterpret_cast<uint4*>(dst + z * 2 + 16) = make_uint4(w.w[4], w.w[5], w.w[6], w.w[7]);
                     }
                 }
             }
@@ -401,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         constexpr int kCols = kD == 128 ? 128 : 32;
         const uint32_t t = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
         const uint32_t row = t % kD, col = kD == 128 ? 0 : t / 64 * 32;
-        Largest most{largest, state_largest, 0};
+        Largest<4> most{largest, state_largest, 0};
         uint64_t s[kCols / 2];
         const int64_t own = (int64_t(seq.slot) * heads + head) * (kD * kD);
         // in front of a segment; the state itself only where there is one segment: another one's CTA may write it
@@ -498,23 +518,26 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        // ---------------- the keys times their decay: a thread a row of the chunk
-        const uint32_t t = quarter * 32 + lane;
-        Largest most{largest + 8, key_largest, 0};
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        // ---------------- the keys times their decay: a thread half a row of the chunk
+        const uint32_t t = quarter * 32 + lane, half = group - 3;
+        Largest<8> most{largest + 8, key_largest, 0};
         for (uint32_t x = 0; x < count; ++x) {
             const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2;
             // the scores no longer need K as it came; the products with the rest tiles' last contents have completed
             if ((kOutputs && !all_wait(x_full, x)) || !__all_sync(0xffffffffu, landed(m)) || (x > 0 && !all_wait(ds_full, x - 1))) break;
             const bool valid = t < len;
             float w = valid ? expf(-decay * float(p.reverse ? t + 1 : len - 1 - t)) : 0.f;
+            // D = 128: 64 elements are a half of the tile; D = 64: 32 of the row
             uint8_t* key = smem + (m % kStages) * size_t(kTile) + t * kSwizzleRow;
             uint8_t* rest = rest_tiles + t * kSwizzleRow;
-            auto vec = [&](int y) { return y / 8 * kHalfTile + ((uint32_t(y) % 8) ^ (t & 7u)) * 16; };
+            auto vec = [&](int y) {
+                return kD == 128 ? half * kHalfTile + ((uint32_t(y) ^ (t & 7u)) * 16) : ((half * 4 + uint32_t(y)) ^ (t & 7u)) * 16;
+            };
             if (kFp16) {
                 float v = 0.f;
-#pragma unroll 4
-                for (int y = 0; y < kD / 8; ++y) {
+#pragma unroll 2
+                for (int y = 0; y < kD / 16; ++y) {
                     const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
                     const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
@@ -525,16 +548,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     }
                 }
                 v = valid ? v * w : 0.f;
-                if (!most.of(v, quarter, lane, abort_flag)) break;
+                if (!most.of(v, warp - 12, lane, abort_flag)) break;
                 const float to_half = up_scale(v);
                 w *= to_half;
-                if (t == 0) key_factor[x & 1u] = inverse(to_half);
+                if (t == 0 && half == 0) key_factor[x & 1u] = inverse(to_half);
             }
             const uint64_t w2 = f2_pack(w, w);
 #pragma unroll 2
-            for (int y = 0; y < kD / 8; ++y) {
+            for (int y = 0; y < kD / 16; ++y) {
                 const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
-                const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
+                const uint32_t kw[4] = {valid ? k.x : 0u, valid ? k.y : 0u, valid ? k.z : 0u, valid ? k.w : 0u};
                 uint32_t part[1 + kRests][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -542,13 +565,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     unpack2<kF>(kw[i], lo, hi);
                     uint64_t v = f2_mul(f2_pack(lo, hi), w2);
 #pragma unroll
-                    for (int r = 0; r <= kRests; ++r) {
-                        f2_unpack(v, lo, hi);
-                        part[r][i] = pack2<kF>(lo, hi);
-                        unpack2<kF>(part[r][i], lo, hi);
-                        v = f2_sub(v, f2_pack(lo, hi));
-                        if (!valid) part[r][i] = 0u;
-                    }
+                    for (int r = 0; r < kRests; ++r) part[r][i] = take_part<kF>(v);
+                    f2_unpack(v, lo, hi);
+                    part[kRests][i] = pack2<kF>(lo, hi);
                 }
                 *reinterpret_cast<uint4*>(key + vec(y)) = make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]);
 #pragma unroll
@@ -564,7 +583,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 17) {
+    if (warp == 21) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
