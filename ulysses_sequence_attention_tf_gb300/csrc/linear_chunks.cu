@@ -19,8 +19,8 @@
 // Each chunk's dS starts at zero and is added to S in fp32 with one rounding, so what the tensor cores' sums drop does not
 // add up over the chunks.  K_w is a sum of three bf16 or two fp16 numbers, because S is fp32 and outlives the chunk: two bf16
 // ones left it 2.4e-6 off, three 3e-7.  P and S only enter the chunk's own output, in 16 bits like it.
-// fp16: P is scaled by a power of two by its row, S and K_w by that of their largest value, so that none of them
-// leaves fp16's normal range.
+// fp16: P, S and K_w are scaled by powers of two from the largest values of Q and K in the chunk (warp 23 looks for them)
+// and of S, so that none of them leaves fp16's normal range.
 //
 // Segments: where there are fewer heads than SMs, each sequence is cut.  A first launch finds what every segment but the
 // last adds to the state (K and V only), a second one runs these sums up to the states in front of the
@@ -47,28 +47,26 @@ struct Shape {
     static constexpr int kTiles = kOutputs ? 3 : 2;                      // a chunk's
     static constexpr int kRests = kF == Fused::kBF16 ? 2 : 1;            // of K_w
     static constexpr int kStages = kD == 128 ? (kOutputs ? 6 : 7) - kRests : 9;
-    static constexpr size_t kBars = 2048;
+    static constexpr size_t kBars = 1024;
     static constexpr size_t kSmem = (kStages + kRests) * size_t(kTile) + (kOutputs ? kStateTile : 0) + kBars + 1024;  // and alignment
 };
 
 constexpr uint32_t kRowsTransposed = 1u << 15;  // of f16_idesc: A MN-major
 
-// The largest value of kWarps warps through shared memory; false if a wait gave up.
-template <int kWarps>
+// The largest value of four warps through shared memory; false if a wait gave up.
 struct Largest {
-    float* slots;  // [2][kWarps]
+    float* slots;  // [2][4]
     uint32_t bar, phase;
-    __device__ bool of(float& v, uint32_t warp, uint32_t lane, volatile int* abort_flag) {
+    __device__ bool of(float& v, uint32_t quarter, uint32_t lane, volatile int* abort_flag) {
         v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-        float* at = slots + phase * kWarps;
+        float* at = slots + phase * 4;
         if (lane == 0) {
-            at[warp] = v;
+            at[quarter] = v;
             mbar_arrive(bar);
         }
         const bool ok = __all_sync(0xffffffffu, bounded_wait(bar, phase, abort_flag, &g_linear_chunks_waits));
         phase ^= 1u;
-        if (ok)
-            for (int x = 0; x < kWarps; ++x) v = fmaxf(v, at[x]);
+        if (ok) v = fmaxf(fmaxf(at[0], at[1]), fmaxf(at[2], at[3]));
         return ok;
     }
 };
@@ -121,16 +119,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
     const uint32_t x_full = empty0 + 8 * kStages, p_ready = x_full + 8, o1_full = p_ready + 8, o2_full = o1_full + 8,
                    o_free = o2_full + 8, s_ready = o_free + 8, k_ready = s_ready + 8, ds_full = k_ready + 8, ds_free = ds_full + 8,
-                   done_a = ds_free + 8, done_b = done_a + 8, state_largest = done_b + 8, key_largest = state_largest + 8;
+                   done_a = ds_free + 8, done_b = done_a + 8, state_largest = done_b + 8, sizes = state_largest + 8;
     float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 14);
     float* decays = floats;             // [32]: lambda^(31 - r), reverse: lambda^r
-    float* row_factor = floats + 32;    // fp16, [2][128] by parity of the chunk: what O1's rows are to be multiplied by,
-    float* state_factor = floats + 288;  // [2] O2,
-    float* key_factor = floats + 290;    // [2] dS
-    float* largest = floats + 292;       // [2][4], [2][8]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 316);
+    float* state_factor = floats + 32;  // fp16: what O2 is to be multiplied by, [2] by parity of the chunk
+    float* key_scale = floats + 36;     // fp16: what the keys and the weights P are to be multiplied by, [4] by the chunk
+    float* p_scale = floats + 40;
+    float* largest = floats + 44;       // [2][4]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 52);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 14) * 8 + 318 * 4 <= int(Sh::kBars), "barriers and factors");
+    static_assert((2 * kStages + 14) * 8 + 54 * 4 <= int(Sh::kBars), "barriers and factors");
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4, group = warp / 4;
 
     if (threadIdx.x == 0) {
@@ -150,7 +148,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         mbar_init(done_a, 1);
         mbar_init(done_b, 1);
         mbar_init(state_largest, 4);
-        mbar_init(key_largest, 8);
+        mbar_init(sizes, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -175,8 +173,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     const bool last = first + count == chunks;  // of this sequence's segments
     const bool work = count > 0 && (kOutputs || !last);
     const float decay = p.decay[head];
-    // chunk x of the unit: its first token and how many it has
-    auto chunk_at = [&](uint32_t x) { return (p.reverse ? chunks - 1 - first - x : first + x) * kChunk; };
+    // a segment's sum: what is more than kGone / decay tokens in front of its end weighs less than fp32's least number (e^-104 < 2^-149)
+    constexpr float kGone = 104.f;
+    const float reach = kGone / (decay * float(kChunk)) + 1.f;  // chunks
+    const uint32_t skipped = !kOutputs && reach < float(count) ? count - uint32_t(reach) - 1 : 0;
+    const uint32_t visits = count - skipped;
+    // chunk x of those visited: its first token and how many it has
+    auto chunk_at = [&](uint32_t x) { return (p.reverse ? chunks - 1 - first - skipped - x : first + skipped + x) * kChunk; };
     auto chunk_len = [&](uint32_t at) { return min(seq.len - at, kChunk); };
     auto wait = [&](uint32_t bar, uint32_t x) { return bounded_wait(bar, x & 1u, abort_flag, &g_linear_chunks_waits); };
     auto all_wait = [&](uint32_t bar, uint32_t x) { return bool(__all_sync(0xffffffffu, wait(bar, x))); };
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const CUtensorMap* maps[3] = {&cp.q.m[g], &cp.k.m[g], &cp.v.m[g]};
             uint32_t m = 0;  // tiles loaded
             bool ok = true;
-            for (uint32_t x = 0; ok && x < count; ++x) {
+            for (uint32_t x = 0; ok && x < visits; ++x) {
                 const int token = int(seq.first + chunk_at(x));
                 for (int y = 0; y < kTiles; ++y, ++m) {
                     const uint32_t s = m % kStages, use = m / kStages;
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             constexpr uint32_t kIdescX = f16_idesc(!kFp16, kChunk, kChunk, false);
             constexpr uint32_t kIdescO = f16_idesc(!kFp16, kChunk, kD, true);
             const uint32_t low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
-            for (uint32_t x = 0; x < count; ++x) {
+            for (uint32_t x = 0; x < visits; ++x) {
                 const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + 1) % kStages, vs = (m + 2) % kStages;
                 if (!landed(m) || !landed(m + 1)) break;
                 // the keys of the chunk before are weighted: no arrival on x_full can run two phases ahead of the warps that
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             // 128 rows of K_w^T; D = 64: its 64 rows twice
             const uint32_t k_low = desc_low(ring, kD == 128 ? kHalfTile : 0), rest_low = desc_low(smem_u32(rest_tiles), kD == 128 ? kHalfTile : 0);
             const uint32_t state_low = desc_low(smem_u32(state_tile), kD * kSwizzleRow);
-            for (uint32_t x = 0; x < count; ++x) {
+            for (uint32_t x = 0; x < visits; ++x) {
                 const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + kTiles - 2) % kStages, vs = (m + kTiles - 1) % kStages;
                 if (kOutputs) {
                     if (!landed(m) || !wait(s_ready, x) || (x > 0 && !wait(o_free, x - 1))) break;
@@ -278,6 +281,34 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
             tc_commit(done_b);
             drain_phase(done_b, 0);
+        } else if (kFp16 && warp == 23) {
+            // ---------------- the largest values of a chunk's keys and queries, and the scales that follow
+            for (uint32_t x = 0; x < visits; ++x) {
+                const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles;
+                uint32_t found[2] = {0, 0};  // two fp16 numbers without their signs: those order as integers
+                bool ok = true;
+#pragma unroll
+                for (int y = 0; y < (kOutputs ? 2 : 1); ++y) {  // Q, K; or K
+                    if (!(ok = __all_sync(0xffffffffu, landed(m + y)))) break;
+                    const uint8_t* tile = smem + ((m + y) % kStages) * size_t(kTile);
+                    for (uint32_t r = lane; r < len; r += 32)
+#pragma unroll 4
+                        for (int z = 0; z < kD / 8; ++z) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(tile + z / 8 * kHalfTile + r * kSwizzleRow + ((uint32_t(z) % 8) ^ (r & 7u)) * 16);
+                            found[y] = __vmaxu2(__vmaxu2(found[y], w.x & 0x7fff7fffu), __vmaxu2(w.y & 0x7fff7fffu, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+                        }
+                    found[y] = __reduce_max_sync(0xffffffffu, max(found[y] & 0xffffu, found[y] >> 16));
+                }
+                // nobody that waits for `sizes` is a phase behind
+                if (!ok || (x > 0 && (!all_wait(k_ready, x - 1) || (kOutputs && !all_wait(p_ready, x - 1))))) break;
+                if (lane == 0) {
+                    const float key = __half2float(__ushort_as_half(uint16_t(found[kOutputs ? 1 : 0]))), query = __half2float(__ushort_as_half(uint16_t(found[0])));
+                    key_scale[x & 3u] = up_scale(key * (p.reverse ? expf(-decay) : 1.f));  // the largest weight
+                    // |q . k| <= D times both; typical scores are some 2^10 below that and stay normal numbers
+                    p_scale[x & 3u] = up_scale(query * key * float(kD) * fabsf(p.out_scale * p.kv_scale));
+                }
+                arrive(sizes);
+            }
         }
     } else if (group == 0) {
         if (kOutputs) {
@@ -287,22 +318,21 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             if (warp == 0) decays[lane] = ex2(-c * float(p.reverse ? lane : 31 - lane));
             asm volatile("bar.sync 1, 128;" ::: "memory");  // these four warps, before any wait
             // scores of 32 columns times their decays, from column 32 j of the row on
-            auto weighted = [&](uint32_t j, uint64_t (&w)[16]) {
+            auto weighted = [&](uint32_t j, uint64_t (&w)[16], const float scales) {
                 uint32_t r[32];
                 tc_ld32(tmem + lane_base + j * 32, r);
                 tc_wait_ld();
                 tc_landed(r);
                 if (j == quarter) {
-                    const float f = both_scales;
-#pragma unroll
+                    #pragma unroll
                     for (int y = 0; y < 16; ++y) {
                         const int gone0 = p.reverse ? 2 * y - int(lane) : int(lane) - 2 * y, gone1 = p.reverse ? gone0 + 1 : gone0 - 1;
-                        const float w0 = ex2(-c * float(max(gone0, 0))) * f, w1 = ex2(-c * float(max(gone1, 0))) * f;
+                        const float w0 = ex2(-c * float(max(gone0, 0))) * scales, w1 = ex2(-c * float(max(gone1, 0))) * scales;
                         w[y] = f2_pack(gone0 >= 0 ? __uint_as_float(r[2 * y]) * w0 : 0.f, gone1 >= 0 ? __uint_as_float(r[2 * y + 1]) * w1 : 0.f);
                     }
                 } else {
                     const int gone = p.reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
-                    const float f = ex2(-c * float(gone)) * both_scales;
+                    const float f = ex2(-c * float(gone)) * scales;
                     const uint64_t f2 = f2_pack(f, f);
 #pragma unroll
                     for (int y = 0; y < 16; y += 2) {
@@ -313,38 +343,25 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 }
             };
             auto seen = [&](uint32_t j) { return p.reverse ? j >= quarter : j <= quarter; };
-            for (uint32_t x = 0; x < count; ++x) {
+            for (uint32_t x = 0; x < visits; ++x) {
                 const uint32_t len = chunk_len(chunk_at(x));
                 if (!all_wait(x_full, x)) break;
                 tc_fence_after();
-                float to_half = 1.f;
+                float f = both_scales;
                 if (kFp16) {
-                    float most = 0.f;
-#pragma unroll 1
-                    for (uint32_t j = 0; j < 4; ++j) {
-                        if (!seen(j)) continue;
-                        uint64_t w[16];
-                        weighted(j, w);
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            float lo, hi;
-                            f2_unpack(w[y], lo, hi);
-                            most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
-                        }
-                    }
-                    to_half = up_scale(most);
-                    row_factor[(x & 1u) * kChunk + a] = inverse(to_half);
+                    if (!all_wait(sizes, x)) break;
+                    f *= p_scale[x & 3u];
                 }
 #pragma unroll 1
                 for (uint32_t j = 0; j < 4; ++j) {
                     uint32_t o[16];
                     if (seen(j)) {
                         uint64_t w[16];
-                        weighted(j, w);
+                        weighted(j, w, f);
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
                             float lo, hi;
-                            f2_unpack(kFp16 ? f2_mul(w[y], f2_pack(to_half, to_half)) : w[y], lo, hi);
+                            f2_unpack(w[y], lo, hi);
                             o[y] = pack2<kF>(lo, hi);
                         }
                     } else {
@@ -374,13 +391,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             // ---------------- the output: a thread a row
             const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
             float age = p.out_scale * expf(-decay * float(a + 1));
-            for (uint32_t x = 0; x < count; ++x) {
+            for (uint32_t x = 0; x < visits; ++x) {
                 const uint32_t at = chunk_at(x), len = chunk_len(at);
                 const bool valid = a < len;
                 if (p.reverse) age = p.out_scale * expf(-decay * float(int(len) - 1 - int(a)));
                 if (!all_wait(o1_full, x) || !all_wait(o2_full, x)) break;
                 tc_fence_after();
-                const float f1 = kFp16 ? row_factor[(x & 1u) * kChunk + a] : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
+                const float f1 = kFp16 ? inverse(p_scale[x & 3u]) : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
                 const uint64_t f1_2 = f2_pack(f1, f1), f2_2 = f2_pack(f2, f2);
                 uint8_t* dst = p.out.base[g] + int64_t(seq.b) * p.out.b + (seq.first + at + (valid ? a : 0)) * p.out.t + int64_t(h) * p.out.h;
 #pragma unroll 1
@@ -421,7 +438,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         constexpr int kCols = kD == 128 ? 128 : 32;
         const uint32_t t = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
         const uint32_t row = t % kD, col = kD == 128 ? 0 : t / 64 * 32;
-        Largest<4> most{largest, state_largest, 0};
+        Largest most{largest, state_largest, 0};
         uint64_t s[kCols / 2];
         const int64_t own = (int64_t(seq.slot) * heads + head) * (kD * kD);
         // in front of a segment; the state itself only where there is one segment: another one's CTA may write it
@@ -442,7 +459,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
         }
         bool ok = true;
-        for (uint32_t x = 0; x < count; ++x) {
+        for (uint32_t x = 0; x < visits; ++x) {
             const uint32_t len = chunk_len(chunk_at(x));
             if (kOutputs) {
                 // the product with the tile's last contents has completed: ds_full of the chunk before
@@ -478,7 +495,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const Fade fade(decay * float(len));
             if (!(ok = all_wait(ds_full, x))) break;
             tc_fence_after();
-            const float back = kFp16 ? p.kv_scale * key_factor[x & 1u] : p.kv_scale;
+            const float back = kFp16 ? p.kv_scale * inverse(key_scale[x & 3u]) : p.kv_scale;
             const uint64_t back2 = f2_pack(back, back), factor2 = f2_pack(fade.factor, fade.factor), whole2 = f2_pack(fade.whole, fade.whole);
 #pragma unroll
             for (int z = 0; z < kCols; z += 32) {
@@ -521,8 +538,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         // ---------------- the keys times their decay: a thread half a row of the chunk
         const uint32_t t = quarter * 32 + lane, half = group - 3;
-        Largest<8> most{largest + 8, key_largest, 0};
-        for (uint32_t x = 0; x < count; ++x) {
+        for (uint32_t x = 0; x < visits; ++x) {
             const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2;
             // the scores no longer need K as it came; the products with the rest tiles' last contents have completed
             if ((kOutputs && !all_wait(x_full, x)) || !__all_sync(0xffffffffu, landed(m)) || (x > 0 && !all_wait(ds_full, x - 1))) break;
@@ -535,23 +551,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 return kD == 128 ? half * kHalfTile + ((uint32_t(y) ^ (t & 7u)) * 16) : ((half * 4 + uint32_t(y)) ^ (t & 7u)) * 16;
             };
             if (kFp16) {
-                float v = 0.f;
-#pragma unroll 2
-                for (int y = 0; y < kD / 16; ++y) {
-                    const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
-                    const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float lo, hi;
-                        unpack2<kF>(kw[i], lo, hi);
-                        v = fmaxf(v, fmaxf(fabsf(lo), fabsf(hi)));
-                    }
-                }
-                v = valid ? v * w : 0.f;
-                if (!most.of(v, warp - 12, lane, abort_flag)) break;
-                const float to_half = up_scale(v);
-                w *= to_half;
-                if (t == 0 && half == 0) key_factor[x & 1u] = inverse(to_half);
+                if (!all_wait(sizes, x)) break;
+                w *= key_scale[x & 3u];
             }
             const uint64_t w2 = f2_pack(w, w);
 #pragma unroll 2
@@ -613,12 +614,19 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     if (p.state) *at = s;
     const uint32_t whole = seg_chunks * kChunk, short_by = chunks * kChunk - seq.len;
     const Fade fade(decay * float(whole)), begin(decay * float(p.reverse ? whole - short_by : whole));
-    for (uint32_t x = 0; x + 1 < used; ++x) {
-        at += size / 4;
-        const float4 add = *at;
-        const Fade& f = x == 0 ? begin : fade;
-        s = make_float4(f.of(s.x, add.x), f.of(s.y, add.y), f.of(s.z, add.z), f.of(s.w, add.w));
-        *at = s;
+    constexpr uint32_t kAhead = 8;  // loads on their way together
+    for (uint32_t x0 = 0; x0 + 1 < used; x0 += kAhead) {
+        float4 add[kAhead];
+#pragma unroll
+        for (uint32_t y = 0; y < kAhead; ++y)
+            if (x0 + y + 1 < used) add[y] = at[(x0 + y + 1) * (size / 4)];
+#pragma unroll
+        for (uint32_t y = 0; y < kAhead; ++y) {
+            if (x0 + y + 1 >= used) break;
+            const Fade& f = x0 + y == 0 ? begin : fade;
+            s = make_float4(f.of(s.x, add[y].x), f.of(s.y, add[y].y), f.of(s.z, add[y].z), f.of(s.w, add[y].w));
+            at[(x0 + y + 1) * (size / 4)] = s;
+        }
     }
 }
 

@@ -79,7 +79,7 @@ struct Cut {
     uint32_t segments = 1, seg_chunks = 0;
 };
 Cut plan_cut(uint64_t units, uint32_t chunks) {
-    constexpr double kStart = 1.5, kSums = 0.6, kJoin = 1.5;
+    constexpr double kStart = 3, kSums = 0.6, kJoin = 1.5;
     Cut best;
     double least = 0;
     for (uint32_t want = 1; want <= chunks && want <= 64; ++want) {
