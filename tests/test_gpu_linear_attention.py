@@ -339,7 +339,9 @@ def test_empty(tf):
 def test_what_is_not_asked_for(tf):
     c = Case(1, 300, 2, 64)
     out, last = tf.linear_attention(c.q, c.k, c.v, decay=c.decay)
-    assert last is None and torch.equal(out[0], c.forward(tf)[0][0])
+    assert last is None
+    # a call that hands out no state may keep fewer parts of the keys: the same bounds, not the same bits
+    check_rows("out", out, *recurrence(wide(c.q), wide(c.k), wide(c.v), c.decay, c.scale)[:2], c.dtype)
     dq, dk, dv, first = tf.linear_attention_backward(c.dout, c.q, c.k, c.v, decay=c.decay)
     assert first is None
 

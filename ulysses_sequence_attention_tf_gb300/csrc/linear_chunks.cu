@@ -15,12 +15,13 @@
 //  * warps 12-19: a thread half a row of the chunk's keys, K_w = K times its decay, in place and the rest in tiles beside.
 //  * warp 20, one lane: TMA producer.  Q, K, V tiles through a ring of stages.
 //  * warp 21, one lane: X = Q K^T, then O1 = P V with P from TMEM.
-//  * warp 22, one lane: O2 = Q S, then dS = K_w^T V.
+//  * warp 22, one lane: O2 = Q S.  Warp 23, one lane: dS = K_w^T V.
 // Each chunk's dS starts at zero and is added to S in fp32 with one rounding, so what the tensor cores' sums drop does not
-// add up over the chunks.  K_w is a sum of three bf16 or two fp16 numbers, because S is fp32 and outlives the chunk: two bf16
-// ones left it 2.4e-6 off, three 3e-7.  P and S only enter the chunk's own output, in 16 bits like it.
-// fp16: P, S and K_w are scaled by powers of two from the largest values of Q and K in the chunk (warp 23 looks for them)
-// and of S, so that none of them leaves fp16's normal range.
+// add up over the chunks.  K_w is a sum of several 16-bit numbers, because S is fp32 and outlives the chunk: two fp16 ones, two
+// bf16 ones (2^-17 of a key: S is 2.4e-6 off) for states that only enter outputs, three (S 3e-7 off) for those handed
+// out.  P and S only enter the chunk's own output, in 16 bits like it.
+// fp16: P is scaled by a power of two by its row, S and K_w by that of their largest value, so that none of them
+// leaves fp16's normal range.
 //
 // Segments: where there are fewer heads than SMs, each sequence is cut.  A first launch finds what every segment but the
 // last adds to the state (K and V only), a second one runs these sums up to the states in front of the
@@ -40,33 +41,35 @@ constexpr int kThreadsC = 768;
 constexpr uint32_t kChunk = kLinearChunk;
 constexpr uint32_t kHalfTile = kChunk * kSwizzleRow;  // 128 rows of 64 elements: 16 KiB
 
-template <Fused kF, int kD, bool kOutputs>
+// kRests: tiles that hold what the first part of K_w leaves
+template <int kD, bool kOutputs, int kRests>
 struct Shape {
     static constexpr uint32_t kTile = kHalfTile * (kD / 64);
     static constexpr uint32_t kStateTile = kD * kSwizzleRow * (kD / 64);
     static constexpr int kTiles = kOutputs ? 3 : 2;                      // a chunk's
-    static constexpr int kRests = kF == Fused::kBF16 ? 2 : 1;            // of K_w
     static constexpr int kStages = kD == 128 ? (kOutputs ? 6 : 7) - kRests : 9;
-    static constexpr size_t kBars = 1024;
+    static constexpr size_t kBars = 2048;
     static constexpr size_t kSmem = (kStages + kRests) * size_t(kTile) + (kOutputs ? kStateTile : 0) + kBars + 1024;  // and alignment
 };
 
 constexpr uint32_t kRowsTransposed = 1u << 15;  // of f16_idesc: A MN-major
 
-// The largest value of four warps through shared memory; false if a wait gave up.
+// The largest value of kWarps warps through shared memory; false if a wait gave up.
+template <int kWarps>
 struct Largest {
-    float* slots;  // [2][4]
+    float* slots;  // [2][kWarps]
     uint32_t bar, phase;
-    __device__ bool of(float& v, uint32_t quarter, uint32_t lane, volatile int* abort_flag) {
+    __device__ bool of(float& v, uint32_t warp, uint32_t lane, volatile int* abort_flag) {
         v = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
-        float* at = slots + phase * 4;
+        float* at = slots + phase * kWarps;
         if (lane == 0) {
-            at[quarter] = v;
+            at[warp] = v;
             mbar_arrive(bar);
         }
         const bool ok = __all_sync(0xffffffffu, bounded_wait(bar, phase, abort_flag, &g_linear_chunks_waits));
         phase ^= 1u;
-        if (ok) v = fmaxf(fmaxf(at[0], at[1]), fmaxf(at[2], at[3]));
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) v = fmaxf(v, at[x]);
         return ok;
     }
 };
@@ -103,11 +106,11 @@ __device__ __forceinline__ uint32_t take_part(uint64_t& v) {
     return part;
 }
 
-template <Fused kF, int kD, bool kOutputs>
+template <Fused kF, int kD, bool kOutputs, int kRests>
 __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
-    using Sh = Shape<kF, kD, kOutputs>;
+    using Sh = Shape<kD, kOutputs, kRests>;
     constexpr uint32_t kTile = Sh::kTile;
-    constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles, kRests = Sh::kRests;
+    constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles;
     constexpr bool kFp16 = kF == Fused::kFP16;
     const LinearPass& p = cp.p;
     extern __shared__ uint8_t smem_raw[];
@@ -119,16 +122,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
     const uint32_t x_full = empty0 + 8 * kStages, p_ready = x_full + 8, o1_full = p_ready + 8, o2_full = o1_full + 8,
                    o_free = o2_full + 8, s_ready = o_free + 8, k_ready = s_ready + 8, ds_full = k_ready + 8, ds_free = ds_full + 8,
-                   done_a = ds_free + 8, done_b = done_a + 8, state_largest = done_b + 8, sizes = state_largest + 8;
-    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 14);
-    float* decays = floats;             // [32]: lambda^(31 - r), reverse: lambda^r
-    float* state_factor = floats + 32;  // fp16: what O2 is to be multiplied by, [2] by parity of the chunk
-    float* key_scale = floats + 36;     // fp16: what the keys and the weights P are to be multiplied by, [4] by the chunk
-    float* p_scale = floats + 40;
-    float* largest = floats + 44;       // [2][4]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 52);
+                   done_a = ds_free + 8, done_b = done_a + 8, done_c = done_b + 8, state_largest = done_c + 8, key_largest = state_largest + 8;
+    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 16);
+    float* decays = floats;             // [64]: lambda^(31 - r), reverse: lambda^(r - 32), 0 where that is no decay
+    float* state_factor = floats + 64;  // fp16: what O2 is to be multiplied by, [2] by parity of the chunk
+    float* key_factor = floats + 66;    // dS, [2]
+    float* largest = floats + 68;       // [2][4], [2][8]
+    float* row_factor = floats + 92;    // O1's rows, [2][128]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 348);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 14) * 8 + 54 * 4 <= int(Sh::kBars), "barriers and factors");
+    static_assert((2 * kStages + 16) * 8 + 350 * 4 <= int(Sh::kBars), "barriers and factors");
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4, group = warp / 4;
 
     if (threadIdx.x == 0) {
@@ -147,8 +150,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         mbar_init(ds_free, 4);
         mbar_init(done_a, 1);
         mbar_init(done_b, 1);
+        mbar_init(done_c, 1);
         mbar_init(state_largest, 4);
-        mbar_init(sizes, 1);
+        mbar_init(key_largest, 8);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -189,10 +193,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         if (lane == 0) mbar_arrive(bar);
     };
 
-    // 768 * 80 registers at launch = 128 * (80 + 64 + 192 + 48 + 48 + 48)
+    // 768 * 80 registers at launch = 128 * (72 + 64 + 192 + 56 + 56 + 40)
     if (!work) {
     } else if (group == 5) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 20 && elect_one()) {
             // ---------------- TMA producer
             const CUtensorMap* maps[3] = {&cp.q.m[g], &cp.k.m[g], &cp.v.m[g]};
@@ -238,30 +242,35 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
             tc_commit(done_a);
             drain_phase(done_a, 0);  // every product of this thread has completed
-        } else if (warp == 22 && elect_one()) {
-            // ---------------- O2 = Q S, dS = K_w^T V
+        } else if (kOutputs && warp == 22 && elect_one()) {
+            // ---------------- O2 = Q S
             constexpr uint32_t kIdesc2 = f16_idesc(!kFp16, kChunk, kD, true);
+            const uint32_t q_low = desc_low(ring), state_low = desc_low(smem_u32(state_tile), kD * kSwizzleRow);
+            for (uint32_t x = 0; x < visits; ++x) {
+                const uint32_t m = x * kTiles, qs = m % kStages;
+                if (!landed(m) || !wait(s_ready, x) || (x > 0 && !wait(o_free, x - 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (uint32_t kk = 0; kk < kD / 16; ++kk) {
+                    const uint32_t a = q_low + qs * (kTile >> 4) + ((kk / 4 * kHalfTile + kk % 4 * 32) >> 4), b = state_low + kk * (2048 >> 4);
+                    if (kk == 0)
+                        tc_mma_low<false>(o2_tmem, a, b, kIdesc2);
+                    else
+                        tc_mma_low<true>(o2_tmem, a, b, kIdesc2);
+                }
+                tc_commit(o2_full);
+                tc_commit(empty0 + 8 * qs);
+            }
+            tc_commit(done_b);
+            drain_phase(done_b, 0);
+        } else if (warp == 23 && elect_one()) {
+            // ---------------- dS = K_w^T V
             constexpr uint32_t kIdescS = f16_idesc(!kFp16, kChunk, kD, true) | kRowsTransposed;
-            const uint32_t q_low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
+            const uint32_t v_low = desc_low(ring, kHalfTile);
             // 128 rows of K_w^T; D = 64: its 64 rows twice
             const uint32_t k_low = desc_low(ring, kD == 128 ? kHalfTile : 0), rest_low = desc_low(smem_u32(rest_tiles), kD == 128 ? kHalfTile : 0);
-            const uint32_t state_low = desc_low(smem_u32(state_tile), kD * kSwizzleRow);
             for (uint32_t x = 0; x < visits; ++x) {
-                const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + kTiles - 2) % kStages, vs = (m + kTiles - 1) % kStages;
-                if (kOutputs) {
-                    if (!landed(m) || !wait(s_ready, x) || (x > 0 && !wait(o_free, x - 1))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (uint32_t kk = 0; kk < kD / 16; ++kk) {
-                        const uint32_t a = q_low + qs * (kTile >> 4) + ((kk / 4 * kHalfTile + kk % 4 * 32) >> 4), b = state_low + kk * (2048 >> 4);
-                        if (kk == 0)
-                            tc_mma_low<false>(o2_tmem, a, b, kIdesc2);
-                        else
-                            tc_mma_low<true>(o2_tmem, a, b, kIdesc2);
-                    }
-                    tc_commit(o2_full);
-                    tc_commit(empty0 + 8 * qs);
-                }
+                const uint32_t m = x * kTiles, ks = (m + kTiles - 2) % kStages, vs = (m + kTiles - 1) % kStages;
                 if (!landed(m + kTiles - 1) || !wait(k_ready, x) || (x > 0 && !wait(ds_free, x - 1))) break;
                 // a short chunk among rows of other sequences: the rows behind it are cleared with P
                 if (kOutputs && p.starts && chunk_len(chunk_at(x)) < kChunk && !wait(p_ready, x)) break;
@@ -279,44 +288,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 tc_commit(empty0 + 8 * ks);
                 tc_commit(empty0 + 8 * vs);
             }
-            tc_commit(done_b);
-            drain_phase(done_b, 0);
-        } else if (kFp16 && warp == 23) {
-            // ---------------- the largest values of a chunk's keys and queries, and the scales that follow
-            for (uint32_t x = 0; x < visits; ++x) {
-                const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles;
-                uint32_t found[2] = {0, 0};  // two fp16 numbers without their signs: those order as integers
-                bool ok = true;
-#pragma unroll
-                for (int y = 0; y < (kOutputs ? 2 : 1); ++y) {  // Q, K; or K
-                    if (!(ok = __all_sync(0xffffffffu, landed(m + y)))) break;
-                    const uint8_t* tile = smem + ((m + y) % kStages) * size_t(kTile);
-                    for (uint32_t r = lane; r < len; r += 32)
-#pragma unroll 4
-                        for (int z = 0; z < kD / 8; ++z) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(tile + z / 8 * kHalfTile + r * kSwizzleRow + ((uint32_t(z) % 8) ^ (r & 7u)) * 16);
-                            found[y] = __vmaxu2(__vmaxu2(found[y], w.x & 0x7fff7fffu), __vmaxu2(w.y & 0x7fff7fffu, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-                        }
-                    found[y] = __reduce_max_sync(0xffffffffu, max(found[y] & 0xffffu, found[y] >> 16));
-                }
-                // nobody that waits for `sizes` is a phase behind
-                if (!ok || (x > 0 && (!all_wait(k_ready, x - 1) || (kOutputs && !all_wait(p_ready, x - 1))))) break;
-                if (lane == 0) {
-                    const float key = __half2float(__ushort_as_half(uint16_t(found[kOutputs ? 1 : 0]))), query = __half2float(__ushort_as_half(uint16_t(found[0])));
-                    key_scale[x & 3u] = up_scale(key * (p.reverse ? expf(-decay) : 1.f));  // the largest weight
-                    // |q . k| <= D times both; typical scores are some 2^10 below that and stay normal numbers
-                    p_scale[x & 3u] = up_scale(query * key * float(kD) * fabsf(p.out_scale * p.kv_scale));
-                }
-                arrive(sizes);
-            }
+            tc_commit(done_c);
+            drain_phase(done_c, 0);
         }
     } else if (group == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (kOutputs) {
             // ---------------- P: a thread a row
             const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
             const float c = decay * kLog2e, both_scales = p.out_scale * p.kv_scale;
-            if (warp == 0) decays[lane] = ex2(-c * float(p.reverse ? lane : 31 - lane));
+            if (warp < 2) {
+                const uint32_t r = warp * 32 + lane;
+                decays[r] = p.reverse ? (r < 32 ? 0.f : ex2(-c * float(r - 32))) : r < 32 ? ex2(-c * float(31 - r)) : 0.f;
+            }
             asm volatile("bar.sync 1, 128;" ::: "memory");  // these four warps, before any wait
+            const float* own_decays = decays + (p.reverse ? 32 - lane : 31 - lane);  // of columns in the row's own block
+            const float* far_decays = decays + (p.reverse ? 32 : 0);                 // of others, up to a factor
+            const uint32_t own_columns = p.reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
             // scores of 32 columns times their decays, from column 32 j of the row on
             auto weighted = [&](uint32_t j, uint64_t (&w)[16], const float scales) {
                 uint32_t r[32];
@@ -324,11 +312,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 tc_wait_ld();
                 tc_landed(r);
                 if (j == quarter) {
-                    #pragma unroll
+#pragma unroll
                     for (int y = 0; y < 16; ++y) {
-                        const int gone0 = p.reverse ? 2 * y - int(lane) : int(lane) - 2 * y, gone1 = p.reverse ? gone0 + 1 : gone0 - 1;
-                        const float w0 = ex2(-c * float(max(gone0, 0))) * scales, w1 = ex2(-c * float(max(gone1, 0))) * scales;
-                        w[y] = f2_pack(gone0 >= 0 ? __uint_as_float(r[2 * y]) * w0 : 0.f, gone1 >= 0 ? __uint_as_float(r[2 * y + 1]) * w1 : 0.f);
+                        // selected: a masked key may be anything
+                        const float w0 = own_decays[2 * y] * scales, w1 = own_decays[2 * y + 1] * scales;
+                        w[y] = f2_pack((own_columns >> (2 * y)) & 1u ? __uint_as_float(r[2 * y]) * w0 : 0.f,
+                                       (own_columns >> (2 * y + 1)) & 1u ? __uint_as_float(r[2 * y + 1]) * w1 : 0.f);
                     }
                 } else {
                     const int gone = p.reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
@@ -336,7 +325,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     const uint64_t f2 = f2_pack(f, f);
 #pragma unroll
                     for (int y = 0; y < 16; y += 2) {
-                        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(decays + 2 * y);
+                        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(far_decays + 2 * y);
                         w[y] = f2_mul(f2_pack(__uint_as_float(r[2 * y]), __uint_as_float(r[2 * y + 1])), f2_mul(t.x, f2));
                         w[y + 1] = f2_mul(f2_pack(__uint_as_float(r[2 * y + 2]), __uint_as_float(r[2 * y + 3])), f2_mul(t.y, f2));
                     }
@@ -349,8 +338,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 tc_fence_after();
                 float f = both_scales;
                 if (kFp16) {
-                    if (!all_wait(sizes, x)) break;
-                    f *= p_scale[x & 3u];
+                    // the row's power of two, from its scores as they are: decays are at most 1, and 2^-28 of the largest
+                    // is still a normal number
+                    float most = 0.f;
+#pragma unroll 1
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        if (!seen(j)) continue;
+                        uint32_t r[32];
+                        tc_ld32(tmem + lane_base + j * 32, r);
+                        tc_wait_ld();
+                        tc_landed(r);
+                        const uint32_t columns = j == quarter ? own_columns : 0xffffffffu;
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) most = (columns >> y) & 1u ? fmaxf(most, fabsf(__uint_as_float(r[y]))) : most;
+                    }
+                    const float to_half = up_scale(most * fabsf(both_scales));
+                    row_factor[(x & 1u) * kChunk + a] = inverse(to_half);
+                    f *= to_half;
                 }
 #pragma unroll 1
                 for (uint32_t j = 0; j < 4; ++j) {
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 if (p.reverse) age = p.out_scale * expf(-decay * float(int(len) - 1 - int(a)));
                 if (!all_wait(o1_full, x) || !all_wait(o2_full, x)) break;
                 tc_fence_after();
-                const float f1 = kFp16 ? inverse(p_scale[x & 3u]) : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
+                const float f1 = kFp16 ? row_factor[(x & 1u) * kChunk + a] : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
                 const uint64_t f1_2 = f2_pack(f1, f1), f2_2 = f2_pack(f2, f2);
                 uint8_t* dst = p.out.base[g] + int64_t(seq.b) * p.out.b + (seq.first + at + (valid ? a : 0)) * p.out.t + int64_t(h) * p.out.h;
 #pragma unroll 1
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         constexpr int kCols = kD == 128 ? 128 : 32;
         const uint32_t t = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
         const uint32_t row = t % kD, col = kD == 128 ? 0 : t / 64 * 32;
-        Largest most{largest, state_largest, 0};
+        Largest<4> most{largest, state_largest, 0};
         uint64_t s[kCols / 2];
         const int64_t own = (int64_t(seq.slot) * heads + head) * (kD * kD);
         // in front of a segment; the state itself only where there is one segment: another one's CTA may write it
@@ -462,7 +466,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         for (uint32_t x = 0; x < visits; ++x) {
             const uint32_t len = chunk_len(chunk_at(x));
             if (kOutputs) {
-                // the product with the tile's last contents has completed: ds_full of the chunk before
                 float to_half = 1.f;
                 if (kFp16) {
                     float v = 0.f;
@@ -476,6 +479,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     to_half = up_scale(v);
                     if (t == 0) state_factor[x & 1u] = inverse(to_half);
                 }
+                if (x > 0 && !(ok = all_wait(o2_full, x - 1))) break;  // the product with the tile's last contents
                 uint8_t* dst = state_tile + row * kSwizzleRow;
 #pragma unroll
                 for (int y = 0; y < kCols; y += 8) {
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const Fade fade(decay * float(len));
             if (!(ok = all_wait(ds_full, x))) break;
             tc_fence_after();
-            const float back = kFp16 ? p.kv_scale * inverse(key_scale[x & 3u]) : p.kv_scale;
+            const float back = kFp16 ? p.kv_scale * key_factor[x & 1u] : p.kv_scale;
             const uint64_t back2 = f2_pack(back, back), factor2 = f2_pack(fade.factor, fade.factor), whole2 = f2_pack(fade.whole, fade.whole);
 #pragma unroll
             for (int z = 0; z < kCols; z += 32) {
@@ -535,9 +539,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         // ---------------- the keys times their decay: a thread half a row of the chunk
         const uint32_t t = quarter * 32 + lane, half = group - 3;
+        Largest<8> most{largest + 8, key_largest, 0};
         for (uint32_t x = 0; x < visits; ++x) {
             const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2;
             // the scores no longer need K as it came; the products with the rest tiles' last contents have completed
@@ -550,14 +555,26 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             auto vec = [&](int y) {
                 return kD == 128 ? half * kHalfTile + ((uint32_t(y) ^ (t & 7u)) * 16) : ((half * 4 + uint32_t(y)) ^ (t & 7u)) * 16;
             };
+            constexpr int kVecs = kD / 16, kHeld = kFp16 ? kVecs : 1;
+            uint4 held[kHeld];
             if (kFp16) {
-                if (!all_wait(sizes, x)) break;
-                w *= key_scale[x & 3u];
+                uint32_t found = 0;  // fp16 numbers without their signs order as integers
+#pragma unroll
+                for (int y = 0; y < kHeld; ++y) {
+                    const uint4 k = held[y] = *reinterpret_cast<const uint4*>(key + vec(y));
+                    found = __vmaxu2(__vmaxu2(found, k.x & 0x7fff7fffu), __vmaxu2(k.y & 0x7fff7fffu, __vmaxu2(k.z & 0x7fff7fffu, k.w & 0x7fff7fffu)));
+                }
+                found = max(found & 0xffffu, found >> 16);
+                float v = valid ? w * __half2float(__ushort_as_half(uint16_t(found))) : 0.f;
+                if (!most.of(v, warp - 12, lane, abort_flag)) break;
+                const float to_half = up_scale(v);
+                w *= to_half;
+                if (t == 0 && half == 0) key_factor[x & 1u] = inverse(to_half);
             }
             const uint64_t w2 = f2_pack(w, w);
-#pragma unroll 2
-            for (int y = 0; y < kD / 16; ++y) {
-                const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
+#pragma unroll
+            for (int y = 0; y < kVecs; ++y) {
+                const uint4 k = kFp16 ? held[kFp16 ? y : 0] : *reinterpret_cast<const uint4*>(key + vec(y));
                 const uint32_t kw[4] = {valid ? k.x : 0u, valid ? k.y : 0u, valid ? k.z : 0u, valid ? k.w : 0u};
                 uint32_t part[1 + kRests][4];
 #pragma unroll
@@ -630,30 +647,37 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     }
 }
 
-template <Fused kF, int kD, bool kOutputs>
+template <Fused kF, int kD, bool kOutputs, int kRests>
 cudaError_t launch(const LinearChunkParams& p, uint32_t grid, cudaStream_t stream) {
-    const size_t smem = Shape<kF, kD, kOutputs>::kSmem;
-    auto kernel = linear_chunks_kernel<kF, kD, kOutputs>;
+    const size_t smem = Shape<kD, kOutputs, kRests>::kSmem;
+    auto kernel = linear_chunks_kernel<kF, kD, kOutputs, kRests>;
     // setting it twice is harmless; the cost is a fraction of a microsecond
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     return launch_overlapped(kernel, grid, kThreadsC, smem, stream, p);
 }
 
-template <Fused kF, int kD>
+template <Fused kF, int kD, int kRests>
 cudaError_t launch_all(const LinearChunkParams& p, cudaStream_t stream, int* launches) {
     const uint32_t units = p.p.N * p.p.P * p.p.Hl;
     cudaError_t e;
     if (p.segments > 1) {
-        if ((e = launch<kF, kD, false>(p, units * (p.segments - 1), stream)) != cudaSuccess) return e;
+        if ((e = launch<kF, kD, false, kRests>(p, units * (p.segments - 1), stream)) != cudaSuccess) return e;
         if ((e = launch_overlapped(linear_join_kernel, units * (kD * kD / 1024), 256, 0, stream, p.p, p.parts, p.segments, p.seg_chunks)) !=
             cudaSuccess)
             return e;
         *launches += 2;
     }
-    if ((e = launch<kF, kD, true>(p, units * p.segments, stream)) != cudaSuccess) return e;
+    if ((e = launch<kF, kD, true, kRests>(p, units * p.segments, stream)) != cudaSuccess) return e;
     *launches += 1;
     return cudaSuccess;
+}
+
+// Three bf16 parts of a weighted key where a state is handed out, two where it stays inside the call.
+template <int kD>
+cudaError_t launch_typed(const LinearChunkParams& p, bool bf16, cudaStream_t stream, int* launches) {
+    if (!bf16) return launch_all<Fused::kFP16, kD, 1>(p, stream, launches);
+    return p.p.final_state ? launch_all<Fused::kBF16, kD, 2>(p, stream, launches) : launch_all<Fused::kBF16, kD, 1>(p, stream, launches);
 }
 
 cudaError_t read_word(const unsigned& symbol, unsigned* out, bool clear) {
@@ -667,8 +691,7 @@ cudaError_t read_word(const unsigned& symbol, unsigned* out, bool clear) {
 
 cudaError_t launch_linear_chunks(const LinearChunkParams& p, bool bf16, cudaStream_t stream, int* launches) {
     *launches = 0;
-    if (p.p.D == 64) return bf16 ? launch_all<Fused::kBF16, 64>(p, stream, launches) : launch_all<Fused::kFP16, 64>(p, stream, launches);
-    return bf16 ? launch_all<Fused::kBF16, 128>(p, stream, launches) : launch_all<Fused::kFP16, 128>(p, stream, launches);
+    return p.p.D == 64 ? launch_typed<64>(p, bf16, stream, launches) : launch_typed<128>(p, bf16, stream, launches);
 }
 
 cudaError_t read_linear_chunks_status(unsigned* out, unsigned* waits, bool clear) {
