@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                             for (int y = 0; y < 8; ++y) v[z * (kHalfTile / 16) + y] = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_shared();
+                    __syncwarp();  // tcgen05.wait is for a warp that has come together
                 }
                 tc_wait_st();
                 tc_fence_before();
@@ -477,9 +478,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     }
                     if (!(ok = most.of(v, quarter, lane, abort_flag))) break;
                     to_half = up_scale(v);
-                    if (t == 0) state_factor[x & 1u] = inverse(to_half);
                 }
-                if (x > 0 && !(ok = all_wait(o2_full, x - 1))) break;  // the product with the tile's last contents
+                // the product with the tile's last contents; it followed the output of the chunk before that one, which was the
+                // last reader of the factor that is overwritten here
+                if (x > 0 && !(ok = all_wait(o2_full, x - 1))) break;
+                if (kFp16 && t == 0) state_factor[x & 1u] = inverse(to_half);
                 uint8_t* dst = state_tile + row * kSwizzleRow;
 #pragma unroll
                 for (int y = 0; y < kCols; y += 8) {
