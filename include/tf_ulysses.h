@@ -694,7 +694,7 @@ TF_API tf_status tf_ulysses_linear_attention(const tf_linear *a, const void *con
  *  dfinal_state the gradient of the final state, or NULL: zeros.
  *  dq, dk, dv   host arrays of P device pointers, [B, S, H/P, D] through grad_strides (3
  *               tf_strides: dq, dk, dv; NULL = contiguous); every element is written.
- *  dstate       the gradient of `state`, or NULL.  May be dfinal_state itself.
+ *  dstate       the gradient of `state`, or NULL.  Must not overlap dfinal_state.
  *  workspace    as above, tf_ulysses_linear_attention_workspace(a, 1) bytes.
  * States are computed again; nothing of the forward pass but its inputs is needed.  There is
  * no gradient of the decay.

@@ -22,7 +22,7 @@ namespace tfu {
 struct LinearPass {
     GroupView q, k, v, out;    // [B, S, Hl, D] of each head group (rows: B = 1)
     const float* state;        // where S starts: [N or slots][H][D][D], or null: 0
-    float* final_state;        // where it ends, or null.  May be `state`
+    float* final_state;        // where it ends, or null.  May be this pass's `state`
     const float* decay;        // [H]
     const int32_t* starts;     // rows: [N + 1], first row of each sequence; null: N batch rows of S tokens
     const int32_t* slots;      // rows: [N], states of the sequences
@@ -63,13 +63,16 @@ __device__ __forceinline__ LinearSequence linear_sequence(const LinearPass& p, u
 
 constexpr uint32_t kLinearChunk = 128;  // tokens: TMEM lanes
 
-// The chunk kernels' launches: every sequence cut into `segments` of seg_chunks chunks (1: not cut).
+// The chunk kernels' launches: up to three passes over the same sequences at once, every sequence cut into `segments` of
+// seg_chunks chunks (1: not cut).
+constexpr uint32_t kLinearPasses = 3;
 struct LinearChunkParams {
-    GroupMaps q, k, v;  // boxes of 128 tokens
-    LinearPass p;
-    uint32_t segments, seg_chunks;
-    uint32_t wide_out;  // rows of out are 32-byte aligned
-    float* parts;       // workspace [N * H][segments][D][D], used where there are several
+    GroupMaps maps[4];                    // of the tensors, boxes of 128 tokens
+    LinearPass pass[kLinearPasses];
+    uint32_t tensor[kLinearPasses][3];    // a pass's q, k, v among the maps
+    uint32_t wide_out[kLinearPasses];     // rows of out are 32-byte aligned
+    uint32_t passes, segments, seg_chunks;
+    float* parts;                         // workspace [passes][N * H][segments][D][D], used where there are several segments
 };
 cudaError_t launch_linear_chunks(const LinearChunkParams& p, bool bf16, cudaStream_t stream, int* launches);
 

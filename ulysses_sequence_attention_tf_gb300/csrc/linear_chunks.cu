@@ -106,13 +106,15 @@ __device__ __forceinline__ uint32_t take_part(uint64_t& v) {
     return part;
 }
 
-template <Fused kF, int kD, bool kOutputs, int kRests>
+// kOne: a single pass, whose parameters lie at constant addresses (an index there cost 5 %)
+template <Fused kF, int kD, bool kOutputs, int kRests, bool kOne>
 __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
     using Sh = Shape<kD, kOutputs, kRests>;
     constexpr uint32_t kTile = Sh::kTile;
     constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles;
     constexpr bool kFp16 = kF == Fused::kFP16;
-    const LinearPass& p = cp.p;
+    const uint32_t which = kOne ? 0 : blockIdx.x % cp.passes, block = kOne ? blockIdx.x : blockIdx.x / cp.passes;
+    const LinearPass& p = cp.pass[which];
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* rest_tiles = smem + kStages * size_t(kTile);  // of K_w
@@ -167,9 +169,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     grid_dependency_wait();
     const uint32_t tmem = *tmem_slot, o1_tmem = tmem + kChunk, o2_tmem = o1_tmem + kD, ds_tmem = o2_tmem + kD;
 
-    // the unit: sequence, head, segment.  Segments of one head lie beside one another in the grid's order
+    // the unit: sequence, head, segment.  In the grid's order the passes of a unit lie beside one another, then the
+    // segments of a head, a reverse pass's from its last on: what runs together reads the same tokens
     const uint32_t heads = p.P * p.Hl, here = kOutputs ? cp.segments : cp.segments - 1;
-    const uint32_t seg = blockIdx.x % here, unit = blockIdx.x / here, head = unit % heads, n = unit / heads;
+    const uint32_t seg = p.reverse ? here - 1 - block % here : block % here, unit = block / here, head = unit % heads, n = unit / heads;
     const uint32_t g = head / p.Hl, h = head % p.Hl;
     const LinearSequence seq = linear_sequence(p, n, &g_linear_chunks_status);
     const uint32_t chunks = (seq.len + kChunk - 1) / kChunk, first = seg * cp.seg_chunks;
@@ -199,7 +202,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 20 && elect_one()) {
             // ---------------- TMA producer
-            const CUtensorMap* maps[3] = {&cp.q.m[g], &cp.k.m[g], &cp.v.m[g]};
+            const uint32_t* tensor = cp.tensor[which];
+            const CUtensorMap* maps[3] = {&cp.maps[tensor[0]].m[g], &cp.maps[tensor[1]].m[g], &cp.maps[tensor[2]].m[g]};
             uint32_t m = 0;  // tiles loaded
             bool ok = true;
             for (uint32_t x = 0; ok && x < visits; ++x) {
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                         w.w[i] = pack2<kF>(lo, hi);
                     }
                     if (!valid) continue;
-                    if (cp.wide_out) {
+                    if (cp.wide_out[which]) {
                         st_stream<32>(dst + z * 2, w);
                     } else {
                         *reinterpret_cast<uint4*>(dst + z * 2) = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         uint64_t s[kCols / 2];
         const int64_t own = (int64_t(seq.slot) * heads + head) * (kD * kD);
         // in front of a segment; the state itself only where there is one segment: another one's CTA may write it
-        float* const parts = cp.parts + (int64_t(unit) * cp.segments + seg) * (kD * kD);
+        float* const parts = cp.parts + ((int64_t(which) * p.N * heads + unit) * cp.segments + seg) * (kD * kD);
         const bool joined = kOutputs && chunks > cp.seg_chunks;
         const float* from = joined ? (seg > 0 || p.state ? parts : nullptr) : kOutputs && p.state ? p.state + own : nullptr;
         if (!from) {
@@ -558,13 +562,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             auto vec = [&](int y) {
                 return kD == 128 ? half * kHalfTile + ((uint32_t(y) ^ (t & 7u)) * 16) : ((half * 4 + uint32_t(y)) ^ (t & 7u)) * 16;
             };
-            constexpr int kVecs = kD / 16, kHeld = kFp16 ? kVecs : 1;
-            uint4 held[kHeld];
+            constexpr int kVecs = kD / 16;
             if (kFp16) {
                 uint32_t found = 0;  // fp16 numbers without their signs order as integers
 #pragma unroll
-                for (int y = 0; y < kHeld; ++y) {
-                    const uint4 k = held[y] = *reinterpret_cast<const uint4*>(key + vec(y));
+                for (int y = 0; y < kVecs; ++y) {
+                    const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
                     found = __vmaxu2(__vmaxu2(found, k.x & 0x7fff7fffu), __vmaxu2(k.y & 0x7fff7fffu, __vmaxu2(k.z & 0x7fff7fffu, k.w & 0x7fff7fffu)));
                 }
                 found = max(found & 0xffffu, found >> 16);
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const uint64_t w2 = f2_pack(w, w);
 #pragma unroll
             for (int y = 0; y < kVecs; ++y) {
-                const uint4 k = kFp16 ? held[kFp16 ? y : 0] : *reinterpret_cast<const uint4*>(key + vec(y));
+                const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
                 const uint32_t kw[4] = {valid ? k.x : 0u, valid ? k.y : 0u, valid ? k.z : 0u, valid ? k.w : 0u};
                 uint32_t part[1 + kRests][4];
 #pragma unroll
@@ -613,10 +616,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
 // The sums of the segments, run up to the states in front of them: parts[0] of a head becomes the state that the sequence
 // starts from (where there is one), parts[1], what segment 0 adds, the state in front of segment 1, and so on.  Four
 // elements a thread.
-__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearPass p, float* parts, uint32_t segments, uint32_t seg_chunks) {
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearChunkParams cp) {
     grid_dependency_wait();
+    const uint32_t which = blockIdx.x % cp.passes, block = blockIdx.x / cp.passes, segments = cp.segments, seg_chunks = cp.seg_chunks;
+    const LinearPass& p = cp.pass[which];
     const uint32_t size = p.D * p.D, blocks = size / 1024, heads = p.P * p.Hl;
-    const uint32_t unit = blockIdx.x / blocks, e = (blockIdx.x % blocks * 256 + threadIdx.x) * 4, head = unit % heads, n = unit / heads;
+    const uint32_t unit = block / blocks, e = (block % blocks * 256 + threadIdx.x) * 4, head = unit % heads, n = unit / heads;
     unsigned unused = 0;
     const LinearSequence seq = linear_sequence(p, n, p.starts ? &g_linear_chunks_status : &unused);
     if (!seq.ok) return;
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
                          : *reinterpret_cast<const float4*>(from + e);
     }
     const float decay = p.decay[head];
-    float4* at = reinterpret_cast<float4*>(parts + int64_t(unit) * segments * size + e);
+    float4* at = reinterpret_cast<float4*>(cp.parts + (int64_t(which) * p.N * heads + unit) * segments * size + e);
     if (p.state) *at = s;
     const uint32_t whole = seg_chunks * kChunk, short_by = chunks * kChunk - seq.len;
     const Fade fade(decay * float(whole)), begin(decay * float(p.reverse ? whole - short_by : whole));
@@ -653,7 +658,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
 template <Fused kF, int kD, bool kOutputs, int kRests>
 cudaError_t launch(const LinearChunkParams& p, uint32_t grid, cudaStream_t stream) {
     const size_t smem = Shape<kD, kOutputs, kRests>::kSmem;
-    auto kernel = linear_chunks_kernel<kF, kD, kOutputs, kRests>;
+    auto kernel = p.passes == 1 ? linear_chunks_kernel<kF, kD, kOutputs, kRests, true> : linear_chunks_kernel<kF, kD, kOutputs, kRests, false>;
     // setting it twice is harmless; the cost is a fraction of a microsecond
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
@@ -662,11 +667,11 @@ cudaError_t launch(const LinearChunkParams& p, uint32_t grid, cudaStream_t strea
 
 template <Fused kF, int kD, int kRests>
 cudaError_t launch_all(const LinearChunkParams& p, cudaStream_t stream, int* launches) {
-    const uint32_t units = p.p.N * p.p.P * p.p.Hl;
+    const uint32_t units = p.passes * p.pass[0].N * p.pass[0].P * p.pass[0].Hl;
     cudaError_t e;
     if (p.segments > 1) {
         if ((e = launch<kF, kD, false, kRests>(p, units * (p.segments - 1), stream)) != cudaSuccess) return e;
-        if ((e = launch_overlapped(linear_join_kernel, units * (kD * kD / 1024), 256, 0, stream, p.p, p.parts, p.segments, p.seg_chunks)) !=
+        if ((e = launch_overlapped(linear_join_kernel, units * (kD * kD / 1024), 256, 0, stream, p)) !=
             cudaSuccess)
             return e;
         *launches += 2;
@@ -680,7 +685,9 @@ cudaError_t launch_all(const LinearChunkParams& p, cudaStream_t stream, int* lau
 template <int kD>
 cudaError_t launch_typed(const LinearChunkParams& p, bool bf16, cudaStream_t stream, int* launches) {
     if (!bf16) return launch_all<Fused::kFP16, kD, 1>(p, stream, launches);
-    return p.p.final_state ? launch_all<Fused::kBF16, kD, 2>(p, stream, launches) : launch_all<Fused::kBF16, kD, 1>(p, stream, launches);
+    bool out = false;
+    for (uint32_t i = 0; i < p.passes; ++i) out |= p.pass[i].final_state != nullptr;
+    return out ? launch_all<Fused::kBF16, kD, 2>(p, stream, launches) : launch_all<Fused::kBF16, kD, 1>(p, stream, launches);
 }
 
 cudaError_t read_word(const unsigned& symbol, unsigned* out, bool clear) {
@@ -694,7 +701,7 @@ cudaError_t read_word(const unsigned& symbol, unsigned* out, bool clear) {
 
 cudaError_t launch_linear_chunks(const LinearChunkParams& p, bool bf16, cudaStream_t stream, int* launches) {
     *launches = 0;
-    return p.p.D == 64 ? launch_typed<64>(p, bf16, stream, launches) : launch_typed<128>(p, bf16, stream, launches);
+    return p.pass[0].D == 64 ? launch_typed<64>(p, bf16, stream, launches) : launch_typed<128>(p, bf16, stream, launches);
 }
 
 cudaError_t read_linear_chunks_status(unsigned* out, unsigned* waits, bool clear) {

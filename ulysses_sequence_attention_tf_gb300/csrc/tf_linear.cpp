@@ -95,42 +95,48 @@ Cut plan_cut(uint64_t units, uint32_t chunks) {
     }
     return best;
 }
-Cut cut_of(const tfu::LinearPass& p) {
+Cut cut_of(const tfu::LinearPass& p, uint32_t passes) {
     if (p.most <= kStepsMost) return {};
-    return plan_cut(uint64_t(p.N) * p.P * p.Hl, (p.most + tfu::kLinearChunk - 1) / tfu::kLinearChunk);
+    return plan_cut(uint64_t(passes) * p.N * p.P * p.Hl, (p.most + tfu::kLinearChunk - 1) / tfu::kLinearChunk);
 }
 
-size_t workspace_of(const tfu::LinearPass& p) {
-    const uint32_t segments = cut_of(p).segments;
-    return segments > 1 ? size_t(segments) * p.N * p.P * p.Hl * p.D * p.D * sizeof(float) : 0;
+size_t workspace_of(const tfu::LinearPass& p, uint32_t passes) {
+    const uint32_t segments = cut_of(p, passes).segments;
+    return segments > 1 ? size_t(passes) * segments * p.N * p.P * p.Hl * p.D * p.D * sizeof(float) : 0;
 }
 
-tf_status run(const tfu::LinearPass& p, bool bf16, void* workspace, cudaStream_t stream) {
-    int launches = 1;
-    cudaError_t e;
-    if (p.most <= kStepsMost) {
-        e = tfu::launch_linear_steps(p, bf16, stream);
+// Passes over the same sequences that depend on one another in nothing: tensor[i] are pass i's q, k, v among `views`.
+tf_status run(const tfu::LinearPass* p, uint32_t passes, const tfu::GroupView* views, uint32_t tensors,
+              const uint32_t (*tensor)[3], bool bf16, void* workspace, cudaStream_t stream) {
+    int launches = 0;
+    cudaError_t e = cudaSuccess;
+    if (p->most <= kStepsMost) {
+        for (uint32_t i = 0; i < passes && e == cudaSuccess; ++i, ++launches) e = tfu::launch_linear_steps(p[i], bf16, stream);
     } else {
         tfu::LinearChunkParams c{};
-        const uint32_t B = p.starts ? 1 : p.N;
-        if (!tfu::encode_group_maps(&c.q, p.q, p.P, B, p.S, p.Hl, p.D, tfu::kLinearChunk, bf16) ||
-            !tfu::encode_group_maps(&c.k, p.k, p.P, B, p.S, p.Hl, p.D, tfu::kLinearChunk, bf16) ||
-            !tfu::encode_group_maps(&c.v, p.v, p.P, B, p.S, p.Hl, p.D, tfu::kLinearChunk, bf16))
-            return fail(TF_ERR_UNSUPPORTED, "the driver refuses a tensor map of these views");
-        c.p = p;
-        const Cut cut = cut_of(p);
+        const uint32_t B = p->starts ? 1 : p->N;
+        for (uint32_t i = 0; i < tensors; ++i)
+            if (!tfu::encode_group_maps(&c.maps[i], views[i], p->P, B, p->S, p->Hl, p->D, tfu::kLinearChunk, bf16))
+                return fail(TF_ERR_UNSUPPORTED, "the driver refuses a tensor map of these views");
+        const Cut cut = cut_of(*p, passes);
+        c.passes = passes;
         c.segments = cut.segments;
         c.seg_chunks = cut.seg_chunks;
-        uintptr_t bits = uintptr_t(p.out.b | p.out.t | p.out.h);
-        for (uint32_t g = 0; g < p.P; ++g) bits |= reinterpret_cast<uintptr_t>(p.out.base[g]);
-        c.wide_out = bits % 32 == 0;
         c.parts = static_cast<float*>(workspace);
+        for (uint32_t i = 0; i < passes; ++i) {
+            c.pass[i] = p[i];
+            for (int x = 0; x < 3; ++x) c.tensor[i][x] = tensor[i][x];
+            uintptr_t bits = uintptr_t(p[i].out.b | p[i].out.t | p[i].out.h);
+            for (uint32_t g = 0; g < p->P; ++g) bits |= reinterpret_cast<uintptr_t>(p[i].out.base[g]);
+            c.wide_out[i] = bits % 32 == 0;
+        }
         e = tfu::launch_linear_chunks(c, bf16, stream, &launches);
     }
     if (e != cudaSuccess) return cuda_fail(e, "launching linear attention");
     count_launches(launches);
     return TF_OK;
 }
+constexpr uint32_t kInOrder[1][3] = {{0, 1, 2}};
 
 tf_status check_pool(const tf_linear* a, const tf_linear_pool* pool, tfu::LinearPass* p) {
     tf_status s = check_linear(a);
@@ -163,11 +169,10 @@ tf_status check_pool(const tf_linear* a, const tf_linear_pool* pool, tfu::Linear
 extern "C" {
 
 TF_API tf_status tf_ulysses_linear_attention_workspace(const tf_linear* a, int backward, size_t* bytes) {
-    (void)backward;  // its passes run one after another in the same place
     if (!bytes) return fail(TF_ERR_INVALID, "bytes is NULL");
     const tf_status s = check_linear(a);
     if (s != TF_OK) return s;
-    *bytes = workspace_of(pass_of(*a));
+    *bytes = workspace_of(pass_of(*a), backward ? 3 : 1);
     return TF_OK;
 }
 
@@ -184,13 +189,14 @@ TF_API tf_status tf_ulysses_linear_attention(const tf_linear* a, const void* con
         (s = view("v", v, &strides[2], *a, false, &p.v)) != TF_OK || (s = view("out", out, out_strides, *a, true, &p.out)) != TF_OK)
         return s;
     if ((s = check_state("state", state)) != TF_OK || (s = check_state("final_state", final_state)) != TF_OK) return s;
-    if ((s = check_workspace(workspace_of(p), workspace, workspace_bytes)) != TF_OK) return s;
+    if ((s = check_workspace(workspace_of(p, 1), workspace, workspace_bytes)) != TF_OK) return s;
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;
     if (a->B == 0 || (a->S == 0 && !final_state)) return TF_OK;
     p.state = state;
     p.final_state = final_state;
-    return run(p, a->dtype == TF_BF16, workspace, static_cast<cudaStream_t>(stream));
+    const tfu::GroupView views[3] = {p.q, p.k, p.v};
+    return run(&p, 1, views, 3, kInOrder, a->dtype == TF_BF16, workspace, static_cast<cudaStream_t>(stream));
 }
 
 TF_API tf_status tf_ulysses_linear_attention_backward(const tf_linear* a, const void* const* dout, const void* const* q,
@@ -214,33 +220,31 @@ TF_API tf_status tf_ulysses_linear_attention_backward(const tf_linear* a, const 
     if ((s = check_state("state", state)) != TF_OK || (s = check_state("dfinal_state", dfinal_state)) != TF_OK ||
         (s = check_state("dstate", dstate)) != TF_OK)
         return s;
+    if (dstate && dfinal_state) {
+        const int64_t n = int64_t(a->B) * a->H * a->D * a->D;
+        if (dstate < dfinal_state + n && dfinal_state < dstate + n) return fail(TF_ERR_INVALID, "dstate overlaps dfinal_state");
+    }
     const tfu::LinearPass all = pass_of(*a);
-    if ((s = check_workspace(workspace_of(all), workspace, workspace_bytes)) != TF_OK) return s;
+    if ((s = check_workspace(workspace_of(all, 3), workspace, workspace_bytes)) != TF_OK) return s;
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;
     if (a->B == 0 || (a->S == 0 && !dstate)) return TF_OK;
+    const tfu::GroupView views[4] = {vdout, vq, vk, vv};
+    constexpr uint32_t kRoles[3][3] = {{0, 3, 2}, {3, 0, 1}, {2, 1, 0}};  // dq: (dout, v, k), dk: (v, dout, q), dv: (k, q, dout)
+    tfu::LinearPass p[3] = {all, all, all};
+    for (int i = 0; i < 3; ++i) {
+        p[i].q = views[kRoles[i][0]], p[i].k = views[kRoles[i][1]], p[i].v = views[kRoles[i][2]];
+        p[i].state = i == 0 ? state : dfinal_state;
+        p[i].transposed = i < 2;
+        p[i].reverse = i > 0;
+        if (i > 0) p[i].kv_scale = a->scale, p[i].out_scale = 1.f;
+    }
+    p[0].out = vdq, p[1].out = vdk, p[2].out = vdv;
+    p[2].final_state = dstate;
     const bool bf16 = a->dtype == TF_BF16;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (a->S > 0) {
-        tfu::LinearPass p = all;  // dq
-        p.q = vdout, p.k = vv, p.v = vk, p.out = vdq;
-        p.state = state;
-        p.transposed = 1;
-        if ((s = run(p, bf16, workspace, st)) != TF_OK) return s;
-        p = all;  // dk: in front of the pass that may write dstate over dfinal_state
-        p.q = vv, p.k = vdout, p.v = vq, p.out = vdk;
-        p.state = dfinal_state;
-        p.transposed = p.reverse = 1;
-        p.kv_scale = a->scale, p.out_scale = 1.f;
-        if ((s = run(p, bf16, workspace, st)) != TF_OK) return s;
-    }
-    tfu::LinearPass p = all;  // dv
-    p.q = vk, p.k = vq, p.v = vdout, p.out = vdv;
-    p.state = dfinal_state;
-    p.final_state = dstate;
-    p.reverse = 1;
-    p.kv_scale = a->scale, p.out_scale = 1.f;
-    return run(p, bf16, workspace, st);
+    if (a->S == 0) return run(&p[2], 1, views, 4, kRoles + 2, bf16, workspace, st);
+    return run(p, 3, views, 4, kRoles, bf16, workspace, st);
 }
 
 TF_API tf_status tf_ulysses_linear_attend_workspace(const tf_linear* a, const tf_linear_pool* pool, size_t* bytes) {
@@ -248,7 +252,7 @@ TF_API tf_status tf_ulysses_linear_attend_workspace(const tf_linear* a, const tf
     tfu::LinearPass p{};
     const tf_status s = check_pool(a, pool, &p);
     if (s != TF_OK) return s;
-    *bytes = workspace_of(p);
+    *bytes = workspace_of(p, 1);
     return TF_OK;
 }
 
@@ -264,11 +268,12 @@ TF_API tf_status tf_ulysses_linear_attend(const tf_linear* a, const tf_linear_po
     if ((s = view("q", q, &strides[0], *a, false, &p.q)) != TF_OK || (s = view("k", k, &strides[1], *a, false, &p.k)) != TF_OK ||
         (s = view("v", v, &strides[2], *a, false, &p.v)) != TF_OK || (s = view("out", out, out_strides, *a, true, &p.out)) != TF_OK)
         return s;
-    if ((s = check_workspace(workspace_of(p), workspace, workspace_bytes)) != TF_OK) return s;
+    if ((s = check_workspace(workspace_of(p, 1), workspace, workspace_bytes)) != TF_OK) return s;
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;
     if (a->S == 0 || pool->N == 0) return TF_OK;
-    return run(p, a->dtype == TF_BF16, workspace, static_cast<cudaStream_t>(stream));
+    const tfu::GroupView views[3] = {p.q, p.k, p.v};
+    return run(&p, 1, views, 3, kInOrder, a->dtype == TF_BF16, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
