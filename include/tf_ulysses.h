@@ -671,13 +671,13 @@ typedef struct tf_linear {
  * tf_ulysses_linear_attention -- the forward pass.
  *  q, k, v      host arrays of P device pointers: group g's views [B, S, H/P, D].
  *  strides      host array of 3 tf_strides: q, k, v.
- *  state        device fp32 [B][H][D][D] contiguous, 16-byte aligned, the state in front of the first
+ *  state        device fp32 [B][H][D][D] contiguous, 32-byte aligned, the state in front of the first
  *               token (rows belong to k, columns to v), or NULL: zeros.
  *  out          host array of P device pointers, [B, S, H/P, D] through out_strides
  *               (NULL = contiguous); must not overlap the inputs.
  *  final_state  as state, the one behind the last token, or NULL.  May be `state` itself.
  *  workspace    device memory of at least tf_ulysses_linear_attention_workspace(a, 0)
- *               bytes, 16-byte aligned (NULL where that is 0), one for each call that may run
+ *               bytes, 32-byte aligned (NULL where that is 0), one for each call that may run
  *               at the same time (replays of graphs among them); its contents need not be kept.
  * Nothing is allocated and nothing is kept between calls; the call may be captured.  The same
  * inputs give the same bits.
@@ -721,7 +721,7 @@ TF_API tf_status tf_ulysses_linear_attention_workspace(const tf_linear *a, int b
  * tf_ulysses_device_status.  Sequences with new rows name different slots.
  */
 typedef struct tf_linear_pool {
-    float *states;           /* device, fp32 [num_slots][H][D][D] contiguous, 16-byte aligned */
+    float *states;           /* device, fp32 [num_slots][H][D][D] contiguous, 32-byte aligned */
     int num_slots, N;        /* slots of the pool, sequences of the call */
     const int32_t *slots;    /* device, [N] */
     const int32_t *starts;   /* device, [N + 1] */
@@ -733,7 +733,7 @@ typedef struct tf_linear_pool {
  *  q, k, v      host arrays of P device pointers to row views [T, H/P, D]; strides: host array
  *               of 3 tf_strides (t and h used).
  *  out          the same through out_strides (NULL = contiguous); must not overlap the inputs.
- *  workspace    tf_ulysses_linear_attend_workspace bytes, 16-byte aligned, one for each call
+ *  workspace    tf_ulysses_linear_attend_workspace bytes, 32-byte aligned, one for each call
  *               that may run at the same time.
  */
 TF_API tf_status tf_ulysses_linear_attend(const tf_linear *a, const tf_linear_pool *pool, const void *const *q,

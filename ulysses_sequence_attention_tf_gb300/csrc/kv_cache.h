@@ -69,9 +69,9 @@ struct KvPlanParams {
     const int32_t *lens, *new_tokens, *free_span;
     int32_t *table, *free_pages, *lens_out, *starts, *positions, *slots, *span_out;
     int64_t table_stride;
-    uint32_t N, max_pages, page, num_pages, T;
+    uint32_t N, max_pages, page, page_bits, num_pages, T;  // page: 2^page_bits
 };
-constexpr int kMostRequests = 8192;  // three sums of each in shared memory: 96 KiB
+constexpr int kMostRequests = 8192;  // three sums and a length of each in shared memory: 128 KiB
 
 constexpr uint32_t kTileRows = 256;  // rows of a CTA of the tile kernel
 

@@ -52,6 +52,7 @@ __device__ __forceinline__ uint32_t owner(const uint32_t* first, uint32_t count,
 }
 
 struct Request {
+    int32_t len;
     uint32_t had;  // pages
     Sums asks;     // what it asks for, or gives back
     bool serve;    // may get tokens
@@ -59,12 +60,12 @@ struct Request {
 };
 __device__ __forceinline__ Request request(const KvPlanParams& p, uint32_t n) {
     const int64_t len = p.lens[n], more = p.new_tokens[n], room = int64_t(p.max_pages) * p.page;
-    Request r{0, {0, 0, 0}, false, len < 0 || len > room || (more > 0 && len + more > room)};
+    Request r{int32_t(len), 0, {0, 0, 0}, false, len < 0 || len > room || (more > 0 && len + more > room)};
     if (r.bad) return r;
-    r.had = (uint32_t(len) + p.page - 1) / p.page;
+    r.had = (uint32_t(len) + p.page - 1) >> p.page_bits;
     r.serve = more >= 0;
     if (r.serve)
-        r.asks = {uint32_t(more), (uint32_t(len + more) + p.page - 1) / p.page - r.had, 0};
+        r.asks = {uint32_t(more), ((uint32_t(len + more) + p.page - 1) >> p.page_bits) - r.had, 0};
     else
         r.asks.back = r.had;
     return r;
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(kThreadsP) kv_plan_kernel(const __grid_constan
     extern __shared__ uint32_t first[];  // [3][N + 1]: of tokens, pages taken, pages given back
     uint32_t* first_page = first + p.N + 1;
     uint32_t* first_back = first_page + p.N + 1;
+    uint32_t* lens = first_back + p.N + 1;  // [N]; of no use where a length is out of range
     __shared__ Sums warp_sums[kWarpsP];
     __shared__ uint32_t total_tokens, total_pages;
     grid_dependency_wait();
@@ -87,7 +89,12 @@ __global__ void __launch_bounds__(kThreadsP) kv_plan_kernel(const __grid_constan
     // each thread sums a run of requests, then the block
     const uint32_t each = (p.N + kThreadsP - 1) / kThreadsP, from = min(threadIdx.x * each, p.N), to = min(from + each, p.N);
     Sums own{0, 0, 0};
-    for (uint32_t n = from; n < to; ++n) own = own + request(p, n).asks;
+    Request held{};  // the run's first: up to 1024 requests, all there is
+    for (uint32_t n = from; n < to; ++n) {
+        const Request r = request(p, n);
+        if (n == from) held = r;
+        own = own + r.asks;
+    }
     const Sums upto = scanned(own);
     if (lane == 31) warp_sums[warp] = upto;
     __syncthreads();
@@ -102,8 +109,9 @@ __global__ void __launch_bounds__(kThreadsP) kv_plan_kernel(const __grid_constan
     const uint32_t room = span ? p.num_pages - count : 0;
     uint32_t most_tokens = 0, most_pages = 0;
     for (uint32_t n = from; n < to; ++n) {
-        const Request r = request(p, n);
+        const Request r = n == from ? held : request(p, n);
         bad |= r.bad;
+        lens[n] = uint32_t(r.len);
         first[n] = at.tokens;
         first_page[n] = at.pages;
         first_back[n] = at.back;
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(kThreadsP) kv_plan_kernel(const __grid_constan
             most_pages = next.pages;
         }
         if (blockIdx.x == 0)
-            p.lens_out[n] = r.bad ? p.lens[n] : !r.serve ? 0 : served ? p.lens[n] + p.new_tokens[n] : p.lens[n];
+            p.lens_out[n] = r.bad ? r.len : !r.serve ? 0 : served ? r.len + int32_t(r.asks.tokens) : r.len;
         at = next;
     }
     if (to == p.N && from < to) first_back[p.N] = at.back;
@@ -128,27 +136,30 @@ __global__ void __launch_bounds__(kThreadsP) kv_plan_kernel(const __grid_constan
     const uint32_t stride = gridDim.x * kThreadsP, me = blockIdx.x * kThreadsP + threadIdx.x;
     for (uint32_t n = me; n <= p.N; n += stride) p.starts[n] = int32_t(n < p.N ? min(first[n], tokens) : tokens);
     if (me == 0) {
-        p.span_out[0] = int32_t((uint64_t(head) + taken) % p.num_pages);
+        p.span_out[0] = int32_t(head + taken < p.num_pages ? head + taken : head + taken - p.num_pages);
         p.span_out[1] = int32_t(count - taken + back);
     }
-    auto ring = [&](uint64_t rank) { return uint32_t((head + rank) % p.num_pages); };
-    auto pages_of = [&](uint32_t n) { return (uint32_t(p.lens[n]) + p.page - 1) / p.page; };
+    auto ring = [&](uint32_t rank) {  // rank <= num_pages
+        const uint32_t x = head + rank;
+        return x < p.num_pages ? x : x - p.num_pages;
+    };
+    auto pages_of = [&](uint32_t n) { return (lens[n] + p.page - 1) >> p.page_bits; };
     for (uint32_t r = me; r < taken; r += stride) {
         const uint32_t n = owner(first_page, p.N, r);
         p.table[int64_t(n) * p.table_stride + pages_of(n) + (r - first_page[n])] = p.free_pages[ring(r)];
     }
     for (uint32_t r = me; r < back; r += stride) {
         const uint32_t n = owner(first_back, p.N, r);
-        p.free_pages[ring(uint64_t(count) + r)] = p.table[int64_t(n) * p.table_stride + (r - first_back[n])];
+        p.free_pages[ring(count + r)] = p.table[int64_t(n) * p.table_stride + (r - first_back[n])];
     }
     for (uint32_t t = me; t < p.T; t += stride) {
         int32_t position = 0, slot = -1;
         if (t < tokens) {
             const uint32_t n = owner(first, p.N, t);
-            position = p.lens[n] + int32_t(t - first[n]);
-            const uint32_t page = uint32_t(position) / p.page, had = pages_of(n);
-            const int32_t id = page < had ? p.table[int64_t(n) * p.table_stride + page] : p.free_pages[ring(uint64_t(first_page[n]) + page - had)];
-            slot = int32_t(uint32_t(id) * p.page + uint32_t(position) % p.page);
+            position = int32_t(lens[n] + (t - first[n]));
+            const uint32_t page = uint32_t(position) >> p.page_bits, had = pages_of(n);
+            const int32_t id = page < had ? p.table[int64_t(n) * p.table_stride + page] : p.free_pages[ring(first_page[n] + page - had)];
+            slot = int32_t(uint32_t(id) * p.page + (uint32_t(position) & (p.page - 1)));
         }
         p.positions[t] = position;
         p.slots[t] = slot;
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(kThreadsP) kv_plan_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream) {
-    const size_t smem = 3 * (size_t(p.N) + 1) * sizeof(uint32_t);
+    const size_t smem = (4 * size_t(p.N) + 3) * sizeof(uint32_t);
     const cudaError_t e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     const uint32_t most = 152, want = (p.T + kThreadsP - 1) / kThreadsP;

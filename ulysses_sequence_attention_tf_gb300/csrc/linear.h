@@ -29,7 +29,7 @@ struct LinearPass {
     uint32_t num_slots;
     uint32_t P, N, S, Hl, D;   // S: tokens of a batch row, or rows of the row tensors
     uint32_t most;             // bound of the tokens of one sequence
-    uint32_t reverse, transposed;  // transposed: S lies as its transpose in state and final_state
+    uint32_t reverse, transposed;  // transposed: S lies as its transpose in state (such a pass has no final_state)
     float kv_scale, out_scale;
 };
 

@@ -106,6 +106,16 @@ __device__ __forceinline__ uint32_t take_part(uint64_t& v) {
     return part;
 }
 
+// Eight floats of a state's row, a sector of memory: a thread's rows lie 4 D bytes apart, and with 16 bytes at a time the
+// L1, small beside the shared memory taken, would read every sector twice.  Not the read-only path: the state may be written
+// where it was read.
+__device__ __forceinline__ void load_sector(const float* p, uint64_t* s) {
+    asm volatile("ld.global.L1::no_allocate.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(s[0]), "=l"(s[1]), "=l"(s[2]), "=l"(s[3]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void store_sector(float* p, const uint64_t* s) {
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(s[0]), "l"(s[1]), "l"(s[2]), "l"(s[3]) : "memory");
+}
+
 // kOne: a single pass, whose parameters lie at constant addresses (an index there cost 5 %)
 template <Fused kF, int kD, bool kOutputs, int kRests, bool kOne>
 __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
@@ -462,10 +472,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             for (int y = 0; y < kCols / 2; ++y) s[y] = f2_pack(from[(col + 2 * y) * kD + row], from[(col + 2 * y + 1) * kD + row]);
         } else {
 #pragma unroll
-            for (int y = 0; y < kCols / 2; y += 2) {
-                const float4 v = *reinterpret_cast<const float4*>(from + row * kD + col + 2 * y);
-                s[y] = f2_pack(v.x, v.y), s[y + 1] = f2_pack(v.z, v.w);
-            }
+            for (int y = 0; y < kCols / 2; y += 4) load_sector(from + row * kD + col + 2 * y, &s[y]);
         }
         bool ok = true;
         for (uint32_t x = 0; x < visits; ++x) {
@@ -530,19 +537,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                         : last && p.final_state ? p.final_state + own : nullptr;
             if (to) {
 #pragma unroll
-                for (int y = 0; y < kCols / 2; y += 2) {
-                    float4 v;
-                    f2_unpack(s[y], v.x, v.y);
-                    f2_unpack(s[y + 1], v.z, v.w);
-                    if (kOutputs && p.transposed) {
-                        to[(col + 2 * y) * kD + row] = v.x;
-                        to[(col + 2 * y + 1) * kD + row] = v.y;
-                        to[(col + 2 * y + 2) * kD + row] = v.z;
-                        to[(col + 2 * y + 3) * kD + row] = v.w;
-                    } else {
-                        *reinterpret_cast<float4*>(to + row * kD + col + 2 * y) = v;
-                    }
-                }
+                for (int y = 0; y < kCols / 2; y += 4) store_sector(to + row * kD + col + 2 * y, &s[y]);
             }
         }
     } else {

@@ -107,15 +107,7 @@ __global__ void __launch_bounds__(kThreadsL) linear_steps_kernel(const __grid_co
 #pragma unroll
     for (int x = 0; x < kRows; ++x) {
         const uint32_t i = group + x * kGroups;
-        const float4 z = s[x];
-        if (p.transposed) {
-            p.final_state[at + col * kD + i] = z.x;
-            p.final_state[at + (col + 1) * kD + i] = z.y;
-            p.final_state[at + (col + 2) * kD + i] = z.z;
-            p.final_state[at + (col + 3) * kD + i] = z.w;
-        } else {
-            *reinterpret_cast<float4*>(p.final_state + at + i * kD + col) = z;
-        }
+        *reinterpret_cast<float4*>(p.final_state + at + i * kD + col) = s[x];
     }
 }
 

@@ -311,6 +311,7 @@ TF_API tf_status tf_ulysses_kv_plan(const tf_kv_plan* p, void* stream) {
     k.N = uint32_t(p->N);
     k.max_pages = uint32_t(p->max_pages);
     k.page = uint32_t(p->page_size);
+    while ((1u << k.page_bits) < k.page) ++k.page_bits;
     k.num_pages = uint32_t(p->num_pages);
     k.T = uint32_t(p->T);
     const cudaError_t e = tfu::launch_kv_plan(k, static_cast<cudaStream_t>(stream));

@@ -46,14 +46,14 @@ tf_status view(const char* name, const void* const* base, const tf_strides* give
 }
 
 tf_status check_state(const char* name, const float* s) {
-    return aligned16(s) ? TF_OK : fail(TF_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
+    return reinterpret_cast<uintptr_t>(s) % 32 == 0 ? TF_OK : fail(TF_ERR_ALIGNMENT, "%s is not 32-byte aligned", name);
 }
 
 tf_status check_workspace(size_t need, const void* workspace, size_t bytes) {
     if (need == 0) return TF_OK;
     if (!workspace || bytes < need)
         return fail(TF_ERR_INVALID, "the workspace holds %zu bytes of the %zu needed", workspace ? bytes : size_t(0), need);
-    if (!aligned16(workspace)) return fail(TF_ERR_ALIGNMENT, "the workspace is not 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(workspace) % 32) return fail(TF_ERR_ALIGNMENT, "the workspace is not 32-byte aligned");
     return TF_OK;
 }
 
@@ -70,8 +70,11 @@ tfu::LinearPass pass_of(const tf_linear& a) {
     return p;
 }
 
-// Up to this many tokens of a sequence go token by token; more in chunks.
-constexpr uint32_t kStepsMost = 8;
+// Up to this many tokens of a sequence go token by token; more in chunks.  A chunk costs the same for one token and 128, about 12
+// us of a CTA with its state's way in and out at D = 128, a token 0.5 us.  One round of CTAs: 8 tokens 14 against 13 us, 16
+// tokens 22 against 13 (8 sequences, 16 heads).  Many, at D = 128 and 64: 8 tokens 99 against 163 us, 26 against 97, 16
+// tokens 162 against 163, 44 against 96 (64 sequences, 32 heads), because the steps' CTAs share an SM.
+uint32_t steps_most(const tfu::LinearPass& p) { return uint64_t(p.N) * p.P * p.Hl > 2 * tfu::kAttnSms ? 16 : 8; }
 
 // How the sequences are cut.  A CTA runs alone on its SM; `units` sequences and heads of `chunks` chunks each.  In chunks of
 // time, a CTA's start costs kStart, the sums of a segment kSums of a chunk each (K and V only), their join kJoin.
@@ -96,7 +99,7 @@ Cut plan_cut(uint64_t units, uint32_t chunks) {
     return best;
 }
 Cut cut_of(const tfu::LinearPass& p, uint32_t passes) {
-    if (p.most <= kStepsMost) return {};
+    if (p.most <= steps_most(p)) return {};
     return plan_cut(uint64_t(passes) * p.N * p.P * p.Hl, (p.most + tfu::kLinearChunk - 1) / tfu::kLinearChunk);
 }
 
@@ -110,7 +113,7 @@ tf_status run(const tfu::LinearPass* p, uint32_t passes, const tfu::GroupView* v
               const uint32_t (*tensor)[3], bool bf16, void* workspace, cudaStream_t stream) {
     int launches = 0;
     cudaError_t e = cudaSuccess;
-    if (p->most <= kStepsMost) {
+    if (p->most <= steps_most(*p)) {
         for (uint32_t i = 0; i < passes && e == cudaSuccess; ++i, ++launches) e = tfu::launch_linear_steps(p[i], bf16, stream);
     } else {
         tfu::LinearChunkParams c{};
