@@ -63,8 +63,8 @@ __device__ __forceinline__ LinearSequence linear_sequence(const LinearPass& p, u
 
 constexpr uint32_t kLinearChunk = 128;  // tokens: TMEM lanes
 
-// The chunk kernels' launches: up to three passes over the same sequences at once, every sequence cut into `segments` of
-// seg_chunks chunks (1: not cut).
+// The chunk kernels' launches: one pass forward, or the three of the gradients over the same batch rows at once;
+// every sequence cut into `segments` of seg_chunks chunks (1: not cut).
 constexpr uint32_t kLinearPasses = 3;
 struct LinearChunkParams {
     GroupMaps maps[4];                    // of the tensors, boxes of 128 tokens

@@ -116,7 +116,7 @@ __device__ __forceinline__ void store_sector(float* p, const uint64_t* s) {
     asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(s[0]), "l"(s[1]), "l"(s[2]), "l"(s[3]) : "memory");
 }
 
-// kOne: a single pass, whose parameters lie at constant addresses (an index there cost 5 %)
+// kOne: a single pass, whose parameters lie at constant addresses (an index there cost 5 %), forward
 template <Fused kF, int kD, bool kOutputs, int kRests, bool kOne>
 __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
     using Sh = Shape<kD, kOutputs, kRests>;
@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     constexpr bool kFp16 = kF == Fused::kFP16;
     const uint32_t which = kOne ? 0 : blockIdx.x % cp.passes, block = kOne ? blockIdx.x : blockIdx.x / cp.passes;
     const LinearPass& p = cp.pass[which];
+    // several passes are the gradients' (of batch rows), a single one goes forward
+    const bool reverse = !kOne && p.reverse, rows_of_sequences = kOne && p.starts;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* rest_tiles = smem + kStages * size_t(kTile);  // of K_w
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     // the unit: sequence, head, segment.  In the grid's order the passes of a unit lie beside one another, then the
     // segments of a head, a reverse pass's from its last on: what runs together reads the same tokens
     const uint32_t heads = p.P * p.Hl, here = kOutputs ? cp.segments : cp.segments - 1;
-    const uint32_t seg = p.reverse ? here - 1 - block % here : block % here, unit = block / here, head = unit % heads, n = unit / heads;
+    const uint32_t seg = reverse ? here - 1 - block % here : block % here, unit = block / here, head = unit % heads, n = unit / heads;
     const uint32_t g = head / p.Hl, h = head % p.Hl;
     const LinearSequence seq = linear_sequence(p, n, &g_linear_chunks_status);
     const uint32_t chunks = (seq.len + kChunk - 1) / kChunk, first = seg * cp.seg_chunks;
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     const uint32_t skipped = !kOutputs && reach < float(count) ? count - uint32_t(reach) - 1 : 0;
     const uint32_t visits = count - skipped;
     // chunk x of those visited: its first token and how many it has
-    auto chunk_at = [&](uint32_t x) { return (p.reverse ? chunks - 1 - first - skipped - x : first + skipped + x) * kChunk; };
+    auto chunk_at = [&](uint32_t x) { return (reverse ? chunks - 1 - first - skipped - x : first + skipped + x) * kChunk; };
     auto chunk_len = [&](uint32_t at) { return min(seq.len - at, kChunk); };
     auto wait = [&](uint32_t bar, uint32_t x) { return bounded_wait(bar, x & 1u, abort_flag, &g_linear_chunks_waits); };
     auto all_wait = [&](uint32_t bar, uint32_t x) { return bool(__all_sync(0xffffffffu, wait(bar, x))); };
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 const uint32_t m = x * kTiles, ks = (m + kTiles - 2) % kStages, vs = (m + kTiles - 1) % kStages;
                 if (!landed(m + kTiles - 1) || !wait(k_ready, x) || (x > 0 && !wait(ds_free, x - 1))) break;
                 // a short chunk among rows of other sequences: the rows behind it are cleared with P
-                if (kOutputs && p.starts && chunk_len(chunk_at(x)) < kChunk && !wait(p_ready, x)) break;
+                if (kOutputs && rows_of_sequences && chunk_len(chunk_at(x)) < kChunk && !wait(p_ready, x)) break;
                 tc_fence_after();
                 const uint32_t b = v_low + vs * (kTile >> 4), a = k_low + ks * (kTile >> 4);
                 tc_mma_low<false>(ds_tmem, a, b, kIdescS);
@@ -313,12 +315,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const float c = decay * kLog2e, both_scales = p.out_scale * p.kv_scale;
             if (warp < 2) {
                 const uint32_t r = warp * 32 + lane;
-                decays[r] = p.reverse ? (r < 32 ? 0.f : ex2(-c * float(r - 32))) : r < 32 ? ex2(-c * float(31 - r)) : 0.f;
+                decays[r] = reverse ? (r < 32 ? 0.f : ex2(-c * float(r - 32))) : r < 32 ? ex2(-c * float(31 - r)) : 0.f;
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");  // these four warps, before any wait
-            const float* own_decays = decays + (p.reverse ? 32 - lane : 31 - lane);  // of columns in the row's own block
-            const float* far_decays = decays + (p.reverse ? 32 : 0);                 // of others, up to a factor
-            const uint32_t own_columns = p.reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+            const float* own_decays = decays + (reverse ? 32 - lane : 31 - lane);  // of columns in the row's own block
+            const float* far_decays = decays + (reverse ? 32 : 0);                 // of others, up to a factor
+            const uint32_t own_columns = reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
             // scores of 32 columns times their decays, from column 32 j of the row on
             auto weighted = [&](uint32_t j, uint64_t (&w)[16], const float scales) {
                 uint32_t r[32];
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                                        (own_columns >> (2 * y + 1)) & 1u ? __uint_as_float(r[2 * y + 1]) * w1 : 0.f);
                     }
                 } else {
-                    const int gone = p.reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
+                    const int gone = reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
                     const float f = ex2(-c * float(gone)) * scales;
                     const uint64_t f2 = f2_pack(f, f);
 #pragma unroll
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     }
                 }
             };
-            auto seen = [&](uint32_t j) { return p.reverse ? j >= quarter : j <= quarter; };
+            auto seen = [&](uint32_t j) { return reverse ? j >= quarter : j <= quarter; };
             for (uint32_t x = 0; x < visits; ++x) {
                 const uint32_t len = chunk_len(chunk_at(x));
                 if (!all_wait(x_full, x)) break;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     }
                     tc_st16(tmem + lane_base + j * 16, o);
                 }
-                if (p.starts && len < kChunk) {  // rows of other sequences, whose V may be anything
+                if (rows_of_sequences && len < kChunk) {  // rows of other sequences, whose V may be anything
                     const uint32_t m = x * kTiles + 2;
                     if (!__all_sync(0xffffffffu, landed(m))) break;
                     if (a >= len) {
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             for (uint32_t x = 0; x < visits; ++x) {
                 const uint32_t at = chunk_at(x), len = chunk_len(at);
                 const bool valid = a < len;
-                if (p.reverse) age = p.out_scale * expf(-decay * float(int(len) - 1 - int(a)));
+                if (reverse) age = p.out_scale * expf(-decay * float(int(len) - 1 - int(a)));
                 if (!all_wait(o1_full, x) || !all_wait(o2_full, x)) break;
                 tc_fence_after();
                 const float f1 = kFp16 ? row_factor[(x & 1u) * kChunk + a] : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         if (!from) {
 #pragma unroll
             for (int y = 0; y < kCols / 2; ++y) s[y] = 0;
-        } else if (!joined && p.transposed) {
+        } else if (!kOne && !joined && p.transposed) {
 #pragma unroll
             for (int y = 0; y < kCols / 2; ++y) s[y] = f2_pack(from[(col + 2 * y) * kD + row], from[(col + 2 * y + 1) * kD + row]);
         } else {
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             // the scores no longer need K as it came; the products with the rest tiles' last contents have completed
             if ((kOutputs && !all_wait(x_full, x)) || !__all_sync(0xffffffffu, landed(m)) || (x > 0 && !all_wait(ds_full, x - 1))) break;
             const bool valid = t < len;
-            float w = valid ? expf(-decay * float(p.reverse ? t + 1 : len - 1 - t)) : 0.f;
+            float w = valid ? expf(-decay * float(reverse ? t + 1 : len - 1 - t)) : 0.f;
             // D = 128: 64 elements are a half of the tile; D = 64: 32 of the row
             uint8_t* key = smem + (m % kStages) * size_t(kTile) + t * kSwizzleRow;
             uint8_t* rest = rest_tiles + t * kSwizzleRow;
@@ -617,8 +619,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     const LinearPass& p = cp.pass[which];
     const uint32_t size = p.D * p.D, blocks = size / 1024, heads = p.P * p.Hl;
     const uint32_t unit = block / blocks, e = (block % blocks * 256 + threadIdx.x) * 4, head = unit % heads, n = unit / heads;
-    unsigned unused = 0;
-    const LinearSequence seq = linear_sequence(p, n, p.starts ? &g_linear_chunks_status : &unused);
+    const LinearSequence seq = linear_sequence(p, n, &g_linear_chunks_status);
     if (!seq.ok) return;
     const uint32_t chunks = (seq.len + kChunk - 1) / kChunk, used = (chunks + seg_chunks - 1) / seg_chunks;
     if (used < 2) return;
