@@ -116,6 +116,21 @@ __device__ __forceinline__ void store_sector(float* p, const uint64_t* s) {
     asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(s[0]), "l"(s[1]), "l"(s[2]), "l"(s[3]) : "memory");
 }
 
+// This warpgroup's registers a thread, of the kLaunched that the CTA was launched with.
+constexpr int kLaunched = 80;  // 65536 / kThreadsC, in eights
+template <int kRegisters>
+__device__ __forceinline__ void registers() {
+    if constexpr (kRegisters < kLaunched) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegisters));
+    if constexpr (kRegisters > kLaunched) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegisters));
+}
+// S is 128 registers of a thread at D = 128 and 32 at D = 64.
+template <int kD>
+struct Registers {
+    static constexpr int kP = kD == 128 ? 72 : 112, kO = kD == 128 ? 64 : 80, kS = kD == 128 ? 192 : 96, kK = kD == 128 ? 56 : 72,
+                         kIssue = kD == 128 ? 40 : 48;
+    static_assert(kP + kO + kS + 2 * kK + kIssue == 6 * kLaunched, "what some take, others give");
+};
+
 // kOne: a single pass, whose parameters lie at constant addresses (an index there cost 5 %), forward
 template <Fused kF, int kD, bool kOutputs, int kRests, bool kOne>
 __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
@@ -208,10 +223,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         if (lane == 0) mbar_arrive(bar);
     };
 
-    // 768 * 80 registers at launch = 128 * (72 + 64 + 192 + 56 + 56 + 40)
     if (!work) {
     } else if (group == 5) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        registers<Registers<kD>::kIssue>();
         if (warp == 20 && elect_one()) {
             // ---------------- TMA producer
             const uint32_t* tensor = cp.tensor[which];
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             drain_phase(done_c, 0);
         }
     } else if (group == 0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        registers<Registers<kD>::kP>();
         if (kOutputs) {
             // ---------------- P: a thread a row
             const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
@@ -407,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
         }
     } else if (group == 1) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        registers<Registers<kD>::kO>();
         if (kOutputs) {
             // ---------------- the output: a thread a row
             const uint32_t a = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
@@ -454,7 +468,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
         }
     } else if (group == 2) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        registers<Registers<kD>::kS>();
         // ---------------- the state: a thread a row of it (D = 64: half a row)
         constexpr int kCols = kD == 128 ? 128 : 32;
         const uint32_t t = quarter * 32 + lane, lane_base = (quarter * 32u) << 16;
@@ -543,7 +557,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        registers<Registers<kD>::kK>();
         // ---------------- the keys times their decay: a thread half a row of the chunk
         const uint32_t t = quarter * 32 + lane, half = group - 3;
         Largest<8> most{largest + 8, key_largest, 0};
