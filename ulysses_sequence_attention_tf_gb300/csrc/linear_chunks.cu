@@ -48,7 +48,7 @@ struct Shape {
     static constexpr uint32_t kStateTile = kD * kSwizzleRow * (kD / 64);
     static constexpr int kTiles = kOutputs ? 3 : 2;                      // a chunk's
     static constexpr int kStages = kD == 128 ? (kOutputs ? 6 : 7) - kRests : 9;
-    static constexpr size_t kBars = 2048;
+    static constexpr size_t kBars = kD == 64 ? 3072 : 2048;
     static constexpr size_t kSmem = (kStages + kRests) * size_t(kTile) + (kOutputs ? kStateTile : 0) + kBars + 1024;  // and alignment
 };
 
@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     using Sh = Shape<kD, kOutputs, kRests>;
     constexpr uint32_t kTile = Sh::kTile;
     constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles;
+    constexpr uint32_t kScores = kD == 64 ? 2 : 1;  // chunks whose scores TMEM holds: D = 128 fills its 512 columns with one
+    constexpr uint32_t kFactors = 2 * kScores;      // P is up to kScores chunks ahead of the output
     constexpr bool kFp16 = kF == Fused::kFP16;
     const uint32_t which = kOne ? 0 : blockIdx.x % cp.passes, block = kOne ? blockIdx.x : blockIdx.x / cp.passes;
     const LinearPass& p = cp.pass[which];
@@ -149,18 +151,18 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     uint64_t* bars = reinterpret_cast<uint64_t*>(state_tile + (kOutputs ? Sh::kStateTile : 0));
     const uint32_t ring = smem_u32(smem);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
-    const uint32_t x_full = empty0 + 8 * kStages, p_ready = x_full + 8, o1_full = p_ready + 8, o2_full = o1_full + 8,
-                   o_free = o2_full + 8, s_ready = o_free + 8, k_ready = s_ready + 8, ds_full = k_ready + 8, ds_free = ds_full + 8,
+    const uint32_t x_full0 = empty0 + 8 * kStages, p_ready0 = x_full0 + 16, o1_full = p_ready0 + 16, o2_full = o1_full + 8,
+                   o_free = o2_full + 8, s_ready = o_free + 8, k_ready0 = s_ready + 8, ds_full = k_ready0 + 16, ds_free = ds_full + 8,
                    done_a = ds_free + 8, done_b = done_a + 8, done_c = done_b + 8, state_largest = done_c + 8, key_largest = state_largest + 8;
-    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 16);
+    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 18);
     float* decays = floats;             // [64]: lambda^(31 - r), reverse: lambda^(r - 32), 0 where that is no decay
     float* state_factor = floats + 64;  // fp16: what O2 is to be multiplied by, [2] by parity of the chunk
     float* key_factor = floats + 66;    // dS, [2]
     float* largest = floats + 68;       // [2][4], [2][8]
-    float* row_factor = floats + 92;    // O1's rows, [2][128]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 348);
+    float* row_factor = floats + 92;    // O1's rows, [kFactors][128]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 92 + kFactors * kChunk);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 16) * 8 + 350 * 4 <= int(Sh::kBars), "barriers and factors");
+    static_assert((2 * kStages + 18) * 8 + (94 + kFactors * kChunk) * 4 <= int(Sh::kBars), "barriers and factors");
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4, group = warp / 4;
 
     if (threadIdx.x == 0) {
@@ -168,13 +170,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, kOutputs ? 2 : 1);
         }
-        mbar_init(x_full, 1);
-        mbar_init(p_ready, 4);  // a warp each
+        for (uint32_t s = 0; s < kScores; ++s) {  // by the chunk
+            mbar_init(x_full0 + 8 * s, 1);
+            mbar_init(p_ready0 + 8 * s, 4);  // a warp each
+            mbar_init(k_ready0 + 8 * s, 8);
+        }
         mbar_init(o1_full, 1);
         mbar_init(o2_full, 1);
         mbar_init(o_free, 4);
         mbar_init(s_ready, 4);
-        mbar_init(k_ready, 8);
         mbar_init(ds_full, 1);
         mbar_init(ds_free, 4);
         mbar_init(done_a, 1);
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     __syncthreads();
     tc_fence_after();
     grid_dependency_wait();
-    const uint32_t tmem = *tmem_slot, o1_tmem = tmem + kChunk, o2_tmem = o1_tmem + kD, ds_tmem = o2_tmem + kD;
+    const uint32_t tmem = *tmem_slot, o1_tmem = tmem + kScores * kChunk, o2_tmem = o1_tmem + kD, ds_tmem = o2_tmem + kD;
 
     // the unit: sequence, head, segment.  In the grid's order the passes of a unit lie beside one another, then the
     // segments of a head, a reverse pass's from its last on: what runs together reads the same tokens
@@ -217,6 +221,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     auto chunk_len = [&](uint32_t at) { return min(seq.len - at, kChunk); };
     auto wait = [&](uint32_t bar, uint32_t x) { return bounded_wait(bar, x & 1u, abort_flag, &g_linear_chunks_waits); };
     auto all_wait = [&](uint32_t bar, uint32_t x) { return bool(__all_sync(0xffffffffu, wait(bar, x))); };
+    auto wait2 = [&](uint32_t bar0, uint32_t x) { return wait(bar0 + 8 * (x % kScores), x / kScores); };
+    auto all_wait2 = [&](uint32_t bar0, uint32_t x) { return all_wait(bar0 + 8 * (x % kScores), x / kScores); };
+    auto scores_of = [&](uint32_t x) { return tmem + x % kScores * kChunk; };
     auto landed = [&](uint32_t m) { return wait(full0 + 8 * (m % kStages), m / kStages); };  // the ring's tile m
     auto arrive = [&](uint32_t bar) {
         __syncwarp();
@@ -253,22 +260,28 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             constexpr uint32_t kIdescX = f16_idesc(!kFp16, kChunk, kChunk, false);
             constexpr uint32_t kIdescO = f16_idesc(!kFp16, kChunk, kD, true);
             const uint32_t low = desc_low(ring), v_low = desc_low(ring, kHalfTile);
-            for (uint32_t x = 0; x < visits; ++x) {
-                const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + 1) % kStages, vs = (m + 2) % kStages;
-                if (!landed(m) || !landed(m + 1)) break;
-                // the keys of the chunk before are weighted: no arrival on x_full can run two phases ahead of the warps that
-                // wait for it to do so
-                if (x > 0 && !wait(k_ready, x - 1)) break;
+            auto scores = [&](uint32_t x) {
+                const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + 1) % kStages;
+                if (!landed(m) || !landed(m + 1)) return false;
+                // no arrival on x_full runs two phases ahead of the warps that wait for it to weight the keys
+                if (x >= kScores && !wait2(k_ready0, x - kScores)) return false;
                 tc_fence_after();
-                tc_product<kD, kHalfTile, kHalfTile>(tmem, low + qs * (kTile >> 4), low + ks * (kTile >> 4), kIdescX);
-                tc_commit(x_full);
+                tc_product<kD, kHalfTile, kHalfTile>(scores_of(x), low + qs * (kTile >> 4), low + ks * (kTile >> 4), kIdescX);
+                tc_commit(x_full0 + 8 * (x % kScores));
                 tc_commit(empty0 + 8 * qs);
                 tc_commit(empty0 + 8 * ks);
-                if (!wait(p_ready, x) || !landed(m + 2) || (x > 0 && !wait(o_free, x - 1))) break;
+                return true;
+            };
+            bool ok = true;
+            for (uint32_t x = 0; ok && x < kScores && x < visits; ++x) ok = scores(x);
+            for (uint32_t x = 0; ok && x < visits; ++x) {
+                const uint32_t m = x * kTiles, vs = (m + 2) % kStages;
+                if (!wait2(p_ready0, x) || !landed(m + 2) || (x > 0 && !wait(o_free, x - 1))) break;
                 tc_fence_after();
-                tc_product_ts<kChunk>(o1_tmem, tmem, v_low + vs * (kTile >> 4), kIdescO, 0u);
+                tc_product_ts<kChunk>(o1_tmem, scores_of(x), v_low + vs * (kTile >> 4), kIdescO, 0u);
                 tc_commit(o1_full);
                 tc_commit(empty0 + 8 * vs);
+                if (x + kScores < visits) ok = scores(x + kScores);  // over the weights that this product reads first
             }
             tc_commit(done_a);
             drain_phase(done_a, 0);  // every product of this thread has completed
@@ -301,9 +314,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const uint32_t k_low = desc_low(ring, kD == 128 ? kHalfTile : 0), rest_low = desc_low(smem_u32(rest_tiles), kD == 128 ? kHalfTile : 0);
             for (uint32_t x = 0; x < visits; ++x) {
                 const uint32_t m = x * kTiles, ks = (m + kTiles - 2) % kStages, vs = (m + kTiles - 1) % kStages;
-                if (!landed(m + kTiles - 1) || !wait(k_ready, x) || (x > 0 && !wait(ds_free, x - 1))) break;
+                if (!landed(m + kTiles - 1) || !wait2(k_ready0, x) || (x > 0 && !wait(ds_free, x - 1))) break;
                 // a short chunk among rows of other sequences: the rows behind it are cleared with P
-                if (kOutputs && rows_of_sequences && chunk_len(chunk_at(x)) < kChunk && !wait(p_ready, x)) break;
+                if (kOutputs && rows_of_sequences && chunk_len(chunk_at(x)) < kChunk && !wait2(p_ready0, x)) break;
                 tc_fence_after();
                 const uint32_t b = v_low + vs * (kTile >> 4), a = k_low + ks * (kTile >> 4);
                 tc_mma_low<false>(ds_tmem, a, b, kIdescS);
@@ -336,9 +349,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const float* far_decays = decays + (reverse ? 32 : 0);                 // of others, up to a factor
             const uint32_t own_columns = reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
             // scores of 32 columns times their decays, from column 32 j of the row on
-            auto weighted = [&](uint32_t j, uint64_t (&w)[16], const float scales) {
+            auto weighted = [&](uint32_t at, uint32_t j, uint64_t (&w)[16], const float scales) {
                 uint32_t r[32];
-                tc_ld32(tmem + lane_base + j * 32, r);
+                tc_ld32(at + j * 32, r);
                 tc_wait_ld();
                 tc_landed(r);
                 if (j == quarter) {
@@ -364,8 +377,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             auto seen = [&](uint32_t j) { return reverse ? j >= quarter : j <= quarter; };
             for (uint32_t x = 0; x < visits; ++x) {
                 const uint32_t len = chunk_len(chunk_at(x));
-                if (!all_wait(x_full, x)) break;
+                if (!all_wait2(x_full0, x)) break;
                 tc_fence_after();
+                const uint32_t at = scores_of(x) + lane_base;
                 float f = both_scales;
                 if (kFp16) {
                     // the row's power of two, from its scores as they are: decays are at most 1, and 2^-28 of the largest
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     for (uint32_t j = 0; j < 4; ++j) {
                         if (!seen(j)) continue;
                         uint32_t r[32];
-                        tc_ld32(tmem + lane_base + j * 32, r);
+                        tc_ld32(at + j * 32, r);
                         tc_wait_ld();
                         tc_landed(r);
                         const uint32_t columns = j == quarter ? own_columns : 0xffffffffu;
@@ -383,7 +397,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                         for (int y = 0; y < 32; ++y) most = (columns >> y) & 1u ? fmaxf(most, fabsf(__uint_as_float(r[y]))) : most;
                     }
                     const float to_half = up_scale(most * fabsf(both_scales));
-                    row_factor[(x & 1u) * kChunk + a] = inverse(to_half);
+                    row_factor[x % kFactors * kChunk + a] = inverse(to_half);
                     f *= to_half;
                 }
 #pragma unroll 1
@@ -391,7 +405,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     uint32_t o[16];
                     if (seen(j)) {
                         uint64_t w[16];
-                        weighted(j, w, f);
+                        weighted(at, j, w, f);
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
                             float lo, hi;
@@ -402,7 +416,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
 #pragma unroll
                         for (int y = 0; y < 16; ++y) o[y] = 0u;
                     }
-                    tc_st16(tmem + lane_base + j * 16, o);
+                    tc_st16(at + j * 16, o);
                 }
                 if (rows_of_sequences && len < kChunk) {  // rows of other sequences, whose V may be anything
                     const uint32_t m = x * kTiles + 2;
@@ -417,7 +431,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 }
                 tc_wait_st();
                 tc_fence_before();
-                arrive(p_ready);
+                arrive(p_ready0 + 8 * (x % kScores));
             }
         }
     } else if (group == 1) {
@@ -432,7 +446,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 if (reverse) age = p.out_scale * expf(-decay * float(int(len) - 1 - int(a)));
                 if (!all_wait(o1_full, x) || !all_wait(o2_full, x)) break;
                 tc_fence_after();
-                const float f1 = kFp16 ? row_factor[(x & 1u) * kChunk + a] : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
+                const float f1 = kFp16 ? row_factor[x % kFactors * kChunk + a] : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
                 const uint64_t f1_2 = f2_pack(f1, f1), f2_2 = f2_pack(f2, f2);
                 uint8_t* dst = p.out.base[g] + int64_t(seq.b) * p.out.b + (seq.first + at + (valid ? a : 0)) * p.out.t + int64_t(h) * p.out.h;
 #pragma unroll 1
@@ -564,7 +578,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         for (uint32_t x = 0; x < visits; ++x) {
             const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2;
             // the scores no longer need K as it came; the products with the rest tiles' last contents have completed
-            if ((kOutputs && !all_wait(x_full, x)) || !__all_sync(0xffffffffu, landed(m)) || (x > 0 && !all_wait(ds_full, x - 1))) break;
+            if ((kOutputs && !all_wait2(x_full0, x)) || !__all_sync(0xffffffffu, landed(m)) || (x > 0 && !all_wait(ds_full, x - 1))) break;
             const bool valid = t < len;
             float w = valid ? expf(-decay * float(reverse ? t + 1 : len - 1 - t)) : 0.f;
             // D = 128: 64 elements are a half of the tile; D = 64: 32 of the row
@@ -610,7 +624,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     *reinterpret_cast<uint4*>(rest + r * kTile + vec(y)) = make_uint4(part[r + 1][0], part[r + 1][1], part[r + 1][2], part[r + 1][3]);
             }
             fence_async_shared();
-            arrive(k_ready);
+            arrive(k_ready0 + 8 * (x % kScores));
         }
     }
     // teardown: every product has completed (their threads drained them) and every TMEM access has finished before
