@@ -655,9 +655,12 @@ TF_API tf_status tf_ulysses_rope_frequencies(int rotary_dim, double theta, tf_ro
  *         = scale * ( sum_(j <= t) e^(-decay (t - j)) (q_t . k_j) v_j + e^(-decay (t + 1)) q_t state )
  * States, sums and decays are fp32.  Chunks of tokens go through the tensor cores: the
  * weights e^(-decay (t - j)) (q_t . k_j) and the states are rounded to the I/O type for the products
- * with V and q (in fp16 times powers of two that keep them in its normal range); keys
- * times their decay enter a state as two numbers of the I/O type, 2^-17 (fp16: 2^-22) of the key apart.
- * Inputs should be finite: a token's infinity or NaN reaches every later output of its head.
+ * with V and q (in fp16 times powers of two that keep them in its normal range); keys times
+ * their decay enter a state as a sum of numbers of the I/O type, within 2^-24 of the key in bf16
+ * and 2^-22 in fp16 where a state is handed out, 2^-16 in bf16 where it stays inside the call.
+ * Inputs should be finite: a token's infinity or NaN reaches every later output of its head,
+ * and in V also earlier ones among the same 128 tokens.  A negative decay is not refused (it
+ * lies on the device) but grows without bound.
  */
 typedef struct tf_linear {
     int P, B, S;             /* head groups (1..8), batch rows, tokens of each (0 is valid) */
@@ -675,7 +678,8 @@ typedef struct tf_linear {
  *               token (rows belong to k, columns to v), or NULL: zeros.
  *  out          host array of P device pointers, [B, S, H/P, D] through out_strides
  *               (NULL = contiguous); must not overlap the inputs.
- *  final_state  as state, the one behind the last token, or NULL.  May be `state` itself.
+ *  final_state  as state, the one behind the last token, or NULL.  May be `state` itself; else they
+ *               must not overlap.
  *  workspace    device memory of at least tf_ulysses_linear_attention_workspace(a, 0)
  *               bytes, 32-byte aligned (NULL where that is 0), one for each call that may run
  *               at the same time (replays of graphs among them); its contents need not be kept.
@@ -694,7 +698,7 @@ TF_API tf_status tf_ulysses_linear_attention(const tf_linear *a, const void *con
  *  dfinal_state the gradient of the final state, or NULL: zeros.
  *  dq, dk, dv   host arrays of P device pointers, [B, S, H/P, D] through grad_strides (3
  *               tf_strides: dq, dk, dv; NULL = contiguous); every element is written.
- *  dstate       the gradient of `state`, or NULL.  Must not overlap dfinal_state.
+ *  dstate       the gradient of `state`, or NULL.  Must not overlap state or dfinal_state.
  *  workspace    as above, tf_ulysses_linear_attention_workspace(a, 1) bytes.
  * States are computed again; nothing of the forward pass but its inputs is needed.  There is
  * no gradient of the decay.
@@ -777,9 +781,10 @@ TF_API void tf_ulysses_set_allocator(tf_alloc_fn alloc, tf_free_fn release, void
  * that kernel then stopped early and its outputs are incomplete.  Bit 2 exists
  * in checked builds of the library (compiled with TFU_CHECKED=1) only: a block
  * kernel access fell outside the buffer the plan allows and was skipped.  Bit 3:
- * a key-value cache call left out a sequence or a page whose length, starts or
- * page number (device data) were out of range.  Bit 4: a bounded wait of an
- * attention kernel gave up; its outputs are incomplete.
+ * a key-value cache or linear attention call left out a sequence, a page or a request
+ * whose length, starts, page number, slot or span (device data) were out of range.
+ * Bit 4: a bounded wait of an attention or linear attention kernel gave up; its outputs
+ * are incomplete.
  * Synchronises with the device.  clear != 0 resets the words after reading them.
  */
 TF_API tf_status tf_ulysses_device_status(int clear, unsigned *status);

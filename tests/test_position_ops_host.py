@@ -142,6 +142,12 @@ def test_linear_attention_refused(tf, kw, status, asked, backward):
     assert linear(tf, backward, **kw) == (asked, status) and tf.lib().tf_ulysses_last_error()
 
 
+def test_states_that_overlap_are_refused(tf):
+    """A final state shifted against the state by less than its size (2 * 8 * 64 * 64 floats)."""
+    assert linear(tf, state=FAKE, last=FAKE + 0x10000) == (0, 1)
+    assert b"overlaps" in tf.lib().tf_ulysses_last_error()
+
+
 def attend(tf, q=FAKE, workspace=None, nbytes=0, **kw):
     a = dict(P=2, B=1, S=16, H=8, D=64, dtype=1, scale=0.125, decay=FAKE)
     p = dict(states=FAKE, num_slots=4, N=3, slots=FAKE, starts=FAKE, max_tokens=8)

@@ -49,6 +49,13 @@ tf_status check_state(const char* name, const float* s) {
     return reinterpret_cast<uintptr_t>(s) % 32 == 0 ? TF_OK : fail(TF_ERR_ALIGNMENT, "%s is not 32-byte aligned", name);
 }
 
+// Two states over the same memory, `same` excepted where it is the very same.
+tf_status check_apart(const char* written, const float* to, const char* read, const float* from, const tf_linear& a, bool same) {
+    const int64_t n = int64_t(a.B) * a.H * a.D * a.D;
+    if (!to || !from || (same && to == from)) return TF_OK;
+    return to < from + n && from < to + n ? fail(TF_ERR_INVALID, "%s overlaps %s", written, read) : TF_OK;
+}
+
 tf_status check_workspace(size_t need, const void* workspace, size_t bytes) {
     if (need == 0) return TF_OK;
     if (!workspace || bytes < need)
@@ -192,6 +199,7 @@ TF_API tf_status tf_ulysses_linear_attention(const tf_linear* a, const void* con
         (s = view("v", v, &strides[2], *a, false, &p.v)) != TF_OK || (s = view("out", out, out_strides, *a, true, &p.out)) != TF_OK)
         return s;
     if ((s = check_state("state", state)) != TF_OK || (s = check_state("final_state", final_state)) != TF_OK) return s;
+    if ((s = check_apart("final_state", final_state, "state", state, *a, true)) != TF_OK) return s;
     if ((s = check_workspace(workspace_of(p, 1), workspace, workspace_bytes)) != TF_OK) return s;
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;
@@ -223,10 +231,10 @@ TF_API tf_status tf_ulysses_linear_attention_backward(const tf_linear* a, const 
     if ((s = check_state("state", state)) != TF_OK || (s = check_state("dfinal_state", dfinal_state)) != TF_OK ||
         (s = check_state("dstate", dstate)) != TF_OK)
         return s;
-    if (dstate && dfinal_state) {
-        const int64_t n = int64_t(a->B) * a->H * a->D * a->D;
-        if (dstate < dfinal_state + n && dfinal_state < dstate + n) return fail(TF_ERR_INVALID, "dstate overlaps dfinal_state");
-    }
+    // the passes run together: one reads what another would write
+    if ((s = check_apart("dstate", dstate, "dfinal_state", dfinal_state, *a, false)) != TF_OK ||
+        (s = check_apart("dstate", dstate, "state", state, *a, false)) != TF_OK)
+        return s;
     const tfu::LinearPass all = pass_of(*a);
     if ((s = check_workspace(workspace_of(all, 3), workspace, workspace_bytes)) != TF_OK) return s;
     int device = 0;

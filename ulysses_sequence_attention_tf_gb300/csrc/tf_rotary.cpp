@@ -11,9 +11,10 @@ namespace {
 
 constexpr double kTurn = 6.283185307179586476925286766559;  // 2 pi
 
-// Heads that one thread takes: as many as leave kRotaryThreads threads, at most kRotaryMost -- then the sines and
-// cosines no longer show.
-constexpr uint64_t kRotaryThreads = 4 * 152 * 2048;
+// Heads that one thread takes: as many as leave kRotaryThreads threads, an SM's worth of resident ones twice over (four times
+// as many: 24 heads of 12002 tokens, half of D = 64, 14 -> 26 us, for the sines and cosines are computed again), at most
+// kRotaryMost -- then these no longer show (8: 80 heads of 32760 tokens 197 -> 217 us).
+constexpr uint64_t kRotaryThreads = 2 * 152 * 1024;
 constexpr uint32_t kRotaryMost = 16;
 
 tf_status tensor(const char* name, const void* const* in, void* const* out, const tf_strides* in_st, const tf_strides* out_st,

@@ -11,6 +11,11 @@
   python -m ulysses_sequence_attention_tf_gb300.profile_cases attention_backward --P 1 --H 5 [--S 8192] [--alibi]
   python -m ulysses_sequence_attention_tf_gb300.profile_cases kv_append [--S 32760] [--tokens 4680] [--page 64]
   python -m ulysses_sequence_attention_tf_gb300.profile_cases kv_attend --B 24 --P 1 --H 16 --Hkv 4 --page 128
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases kv_plan --B 64 [--tokens 1] [--S 8192] [--page 64]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases rotary [--S 32760] [--rope neox]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases linear --P 1 --H 152 [--S 8192]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases linear_backward --P 1 --H 5 [--S 8192]
+  python -m ulysses_sequence_attention_tf_gb300.profile_cases linear_attend --B 64 --P 1 --H 32 [--tokens 1]
 
 ``--layout``: v_strided (Q/K contiguous, V a view into a fused projection; the
 default), fused (Q/K/V all views of one fused projection), contiguous, pad16
@@ -18,7 +23,8 @@ default), fused (Q/K/V all views of one fused projection), contiguous, pad16
 which sends fused scatters to the register kernel).  ``rope_table`` builds the
 resident cos/sin table of (theta, S, D) once per iteration, each time for
 another theta.  ``attention`` and ``attention_backward`` see every key (``--alibi``: causal, with
-distances as a bias; ``--docs``: within documents); the ``kv`` cases have --B sequences of --S tokens, the last --tokens of them new.
+distances as a bias; ``--docs``: within documents); the ``kv`` cases have --B sequences of --S tokens, the last --tokens of them
+new, ``linear_attend`` --B sequences with --tokens new ones each.
 
 Inputs are the seeded synthetic ones of ``synth``; shapes default to the
 video-DiT workload's head geometry (P=4, H=40, D=128, bf16) with a smaller
@@ -36,7 +42,8 @@ from . import binding, build, synth
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("case", choices=["projection", "scatter", "scatter_fused", "scatter_fused_qk", "gather",
-                                     "rope_table", "attention", "attention_backward", "kv_append", "kv_attend"])
+                                     "rope_table", "attention", "attention_backward", "kv_append", "kv_attend", "kv_plan",
+                                     "rotary", "linear", "linear_backward", "linear_attend"])
     ap.add_argument("--P", type=int, default=4)
     ap.add_argument("--B", type=int, default=1)
     ap.add_argument("--D", type=int, default=128)
@@ -54,7 +61,8 @@ def main(argv=None):
     ap.add_argument("--page", type=int, default=64)
     args = ap.parse_args(argv)
     P, H, D, B = args.P, args.H, args.D, args.B
-    S = args.S or (8192 if args.case in ("projection", "attention", "attention_backward") else 32760)
+    short = ("projection", "attention", "attention_backward", "kv_plan", "linear", "linear_backward")
+    S = args.S or (8192 if args.case in short else 32760)
     Hkv = args.Hkv or H
     Sl, Hl = S // P, H // P
     build.build()
@@ -114,6 +122,36 @@ def main(argv=None):
                 binding.kv_append(cache, *where, k, v, q, q_out, q_weight=wq, k_weight=wk, rope=args.rope)
             else:
                 binding.kv_attend(cache, *where, q, q_out, max_tokens=n, max_len=S, softcap=args.softcap, causal=n == 1)
+    elif args.case == "kv_plan":
+        n = args.tokens or 1
+        had, used = -(-S // args.page), -(-(S + n) // args.page)
+        ids = torch.randperm(B * used, generator=torch.Generator(device=dev).manual_seed(0), device=dev).to(torch.int32)
+        table = torch.zeros((B, used), dtype=torch.int32, device=dev)
+        table[:, :had] = ids[:B * had].view(B, had)
+        lens, new = (torch.full((B,), x, dtype=torch.int32, device=dev) for x in (S, n))
+        span = torch.tensor([B * had % (B * used), B * (used - had)], dtype=torch.int32, device=dev)
+
+        def call():
+            binding.kv_plan(table, lens, new, ids, span, page_size=args.page, rows=B * n)
+    elif args.case in ("rotary", "linear", "linear_backward", "linear_attend"):
+        gen = torch.Generator(device=dev).manual_seed(0)
+        n = args.tokens or 1
+        lead = (B * n,) if args.case == "linear_attend" else (B, S)
+        q, k, v, dout = ([torch.randn((*lead, Hl, D), generator=gen, device=dev).to(dt) for _ in range(P)] for _ in range(4))
+        out = [torch.empty_like(t) for t in q]
+        decay = torch.exp2(-8.0 * torch.arange(1, H + 1, device=dev) / H)
+        states = torch.randn((B, H, D, D), generator=gen, device=dev) if args.case == "linear_attend" else None
+        slots, starts = torch.arange(B, dtype=torch.int32, device=dev), torch.arange(0, B * n + 1, n, dtype=torch.int32, device=dev)
+
+        def call():
+            if args.case == "rotary":
+                binding.rope(q, k, out, v, rope=args.rope)
+            elif args.case == "linear":
+                binding.linear_attention(q, k, v, out, decay=decay)
+            elif args.case == "linear_backward":
+                binding.linear_attention_backward(dout, q, k, v, out, decay=decay)
+            else:
+                binding.linear_attend(states, slots, starts, q, k, v, out, decay=decay, max_tokens=n)
     elif args.case in ("scatter", "scatter_fused", "scatter_fused_qk"):
         if args.layout == "pad16":
             pad = 16 // 2
