@@ -679,6 +679,8 @@ PyObject* linear_attend(PyObject* const* x, Py_ssize_t n) {
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* x, Py_ssize_t n) {
     HANDLE_TH_ERRORS
+    // results and workspaces are made below autograd, which records none of these calls (2 us of host time a call)
+    at::AutoDispatchBelowADInplaceOrView below;
     try {
         return F(x, n);
     } catch (const PythonError&) {
