@@ -2,7 +2,7 @@
 
 The translation units (kernels, host ABI) compile in parallel into
 ``_build/`` and link into ``ulysses_sequence_attention_tf_gb300/libtf_ulysses.so``;
-``_torch_calls.so`` beside it marshals the attention and cache calls.
+``_torch_calls.so`` beside it marshals the attention, rotation and cache calls.
 cudart is linked statically, so the library depends only on the driver.
 """
 from __future__ import annotations

@@ -5,7 +5,9 @@
 // A CTA of 256 threads takes columns of one head's state, all rows of them: a thread four columns of
 // every R-th row, in registers for all tokens, so a state is read and written once a call.  lambda S as Fade takes it.
 // Rows that the threads of a column hold are summed by shuffles and through shared memory.
-// Bound: DRAM, 8 D^2 bytes of state a head and call.
+// Bound: DRAM, 8 D^2 bytes of state a head and call.  One token of 64 sequences, 32 heads, D = 128: 44 us, 6.0 TB/s (0.89 of
+// the copy bandwidth); of one sequence, 8 heads, D = 64: 4.4 us of the GPU, 6 a call.  With few heads a CTA takes 32 columns, so that
+// more of them share a state.
 #include "device_common.cuh"
 #include "linear.h"
 

@@ -1,4 +1,4 @@
-// torch_calls.cpp -- the attention, rotation and key-value cache calls of the binding, marshalled in C++.
+// torch_calls.cpp -- the attention, linear attention, rotation and key-value cache calls of the binding, marshalled in C++.
 //
 // These calls are short on the GPU, and checking and unpacking a dozen tensors in Python
 // takes longer than the kernels of a small call (35 us of host time for two head groups of
