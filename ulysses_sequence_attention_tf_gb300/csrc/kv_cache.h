@@ -64,21 +64,10 @@ struct KvAttendParams {
     uint32_t causal;
 };
 
-// Pages, starts, positions and slots of a step's requests.
-struct KvPlanParams {
-    const int32_t *lens, *new_tokens, *free_span;
-    int32_t *table, *free_pages, *lens_out, *starts, *positions, *slots, *span_out;
-    int64_t table_stride;
-    uint32_t N, max_pages, page, page_bits, num_pages, T;  // page: 2^page_bits
-};
-constexpr int kMostRequests = 8192;  // three sums and a length of each in shared memory: 128 KiB
-
 constexpr uint32_t kTileRows = 256;  // rows of a CTA of the tile kernel
 
 cudaError_t launch_kv_append(const KvAppendParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_kv_attend(const KvAttendParams& p, bool bf16, cudaStream_t stream, int* launches);
-
-cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream);
 
 // the tile kernel alone (kv_attend_tiles.cu)
 cudaError_t launch_kv_tiles(const KvAttendParams& p, bool bf16, cudaStream_t stream);
@@ -87,7 +76,6 @@ cudaError_t launch_kv_tiles(const KvAttendParams& p, bool bf16, cudaStream_t str
 // of some sequence was out of range and the sequence (or the page) was left out.
 cudaError_t read_kv_append_status(unsigned* out, bool clear);
 cudaError_t read_kv_attend_status(unsigned* out, bool clear);
-cudaError_t read_kv_plan_status(unsigned* out, bool clear);
 cudaError_t read_kv_tiles_status(unsigned* out, unsigned* waits, bool clear);  // *waits: 1 when a bounded wait gave up
 
 }  // namespace tfu

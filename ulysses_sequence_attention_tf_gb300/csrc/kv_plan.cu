@@ -8,7 +8,7 @@
 // takes the page from the ring by its rank.  Bound: latency -- the launch, loads of the lengths, three block-wide steps
 // and a page's load: 64 requests 5.4 us, 512 with prompts of 22 thousand rows 7.3.
 #include "device_common.cuh"
-#include "kv_cache.h"
+#include "kv_plan.h"
 
 namespace tfu {
 

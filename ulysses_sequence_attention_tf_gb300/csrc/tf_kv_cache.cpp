@@ -4,6 +4,7 @@
 
 #include "host.h"
 #include "kv_cache.h"
+#include "kv_plan.h"
 
 using namespace tfu::host;
 

@@ -25,6 +25,7 @@
 #include "gemm.h"
 #include "host.h"
 #include "kv_cache.h"
+#include "kv_plan.h"
 #include "linear.h"
 #include "noalloc.h"
 #include "relayout.h"
