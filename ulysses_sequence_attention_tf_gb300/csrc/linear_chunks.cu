@@ -60,7 +60,7 @@ struct Shape {
     static constexpr uint32_t kStateTile = kD * kSwizzleRow * (kD / 64);
     static constexpr int kTiles = kOutputs ? 3 : 2;                      // a chunk's
     static constexpr int kStages = kD == 128 ? (kOutputs ? 6 : 7) - kRests : 9;
-    static constexpr size_t kBars = kD == 64 ? 3072 : 2048;
+    static constexpr size_t kBars = kD == 64 ? 2816 : 2048;
     static constexpr size_t kSmem = (kStages + kRests) * size_t(kTile) + (kOutputs ? kStateTile : 0) + kBars + 1024;  // and alignment
 };
 
