@@ -1,4 +1,5 @@
 """The plan of a step's requests -- pages, starts, positions, slots -- against a loop over the requests."""
+import concurrent.futures
 import random
 
 import pytest
@@ -185,6 +186,26 @@ def test_given_outputs_strides_streams_and_graphs(tf):
         t[4].copy_(outs["span_out"])
         t[2].copy_(torch.where(t[1] > 60, -1, 1))
         assert rows >= 40
+
+
+def test_calls_of_several_threads(tf):
+    """Large and small calls at once, each on its own stream: one's shared memory is not what the other asked for."""
+    cases = [case(random.Random(7), 8000, 16, 3), case(random.Random(8), 3, 16, 3)] * 2
+    wants = [by_hand(*c)[0] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    inputs = [[i32(x) for x in c[:5]] for c in cases]
+    torch.cuda.synchronize()
+
+    def calls(i):
+        for _ in range(200):
+            p = tf.kv_plan(*inputs[i], page_size=cases[i][5], rows=cases[i][6], stream=streams[i])
+        streams[i].synchronize()
+        return p
+
+    with concurrent.futures.ThreadPoolExecutor(len(cases)) as pool:
+        got = list(pool.map(calls, range(len(cases))))
+    for p, want in zip(got, wants):
+        assert p.slots.tolist() == want["slots"] and p.lens.tolist() == want["lens"]
 
 
 def test_refusals(tf):

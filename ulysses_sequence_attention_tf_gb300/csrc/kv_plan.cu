@@ -171,7 +171,9 @@ __global__ void __launch_bounds__(kThreadsP) kv_plan_kernel(const __grid_constan
 
 cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream) {
     const size_t smem = (4 * size_t(p.N) + 3) * sizeof(uint32_t);
-    const cudaError_t e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // always the largest: with this call's own size, a smaller call of another thread could set it back before the launch
+    constexpr int kMostSmem = (4 * kMostRequests + 3) * int(sizeof(uint32_t));
+    const cudaError_t e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
     const uint32_t most = 152, want = (p.T + kThreadsP - 1) / kThreadsP;
     return launch_overlapped(kv_plan_kernel, want < 1 ? 1 : want > most ? most : want, kThreadsP, smem, stream, p);
