@@ -558,8 +558,9 @@ TF_API tf_status tf_ulysses_kv_attend_workspace(const tf_kv_cache *c, const tf_k
  * A request whose length is out of range (0 <= lens[n], lens[n] + new_tokens[n] <=
  * max_pages * page_size) gets and gives nothing, and a span that does not describe the
  * ring (0 <= head < num_pages, 0 <= count <= num_pages) stands for one without free pages
- * that takes none back; pages given back beyond the ring's capacity are dropped.  All
- * three set bit 3 of tf_ulysses_device_status.
+ * that takes none back; pages given back beyond the ring's capacity are dropped; a row
+ * on a page whose number is negative or has slots above 2^31 - 1 gets slot -1.  All four
+ * set bit 3 of tf_ulysses_device_status.
  * The inputs are left as they were but for the table's new entries and the ring's, so the
  * same call again gives the same results.
  */

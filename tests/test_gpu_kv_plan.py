@@ -157,6 +157,21 @@ def test_more_pages_given_back_than_fit(tf):
     run(tf, [[1, 2, 3], [4, 5, 6]], [40, 40], [-1, -1], list(range(6)), [4, 2], 16, 4)
 
 
+@pytest.mark.parametrize("page,bad", [(16, -1), (16, 2 ** 27), (128, 2 ** 31 - 1), (64, -2 ** 31)])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_rows_on_pages_out_of_range_have_no_slot(tf, page, bad, fresh):
+    """The page that a request has, or the one that it takes; the largest that has slots beside it."""
+    largest = 2 ** 31 // page - 1
+    lens = [0, 0] if fresh else [2, 2]
+    table, free = ([[-7], [-7]], [bad, largest]) if fresh else ([[bad], [largest]], [3, 4])
+    t = [i32(table), i32(lens), i32([3, 3]), i32(free), i32([0, 2])]
+    p = tf.kv_plan(*t, page_size=page, rows=8)
+    at = lens[0]
+    assert p.slots.tolist() == [-1] * 3 + [largest * page + at + x for x in range(3)] + [-1] * 2
+    assert p.starts.tolist() == [0, 3, 6] and p.lens.tolist() == [at + 3] * 2
+    assert tf.device_status(clear=True) == 8
+
+
 def test_given_outputs_strides_streams_and_graphs(tf):
     args = case(random.Random(5), 40, 16, 6)
     table, lens, new, free, span, page, rows = args

@@ -160,7 +160,11 @@ __global__ void __launch_bounds__(kThreadsP) kv_plan_kernel(const __grid_constan
             position = int32_t(lens[n] + (t - first[n]));
             const uint32_t page = uint32_t(position) >> p.page_bits, had = pages_of(n);
             const int32_t id = page < had ? p.table[int64_t(n) * p.table_stride + page] : p.free_pages[ring(first_page[n] + page - had)];
-            slot = int32_t(uint32_t(id) * p.page + (uint32_t(position) & (p.page - 1)));
+            // a page whose slots no 32-bit number holds (-1 of an entry never filled among them) has none
+            if (uint32_t(id) < (1u << 31) >> p.page_bits)
+                slot = int32_t(uint32_t(id) * p.page + (uint32_t(position) & (p.page - 1)));
+            else
+                atomicOr(&g_kv_plan_status, 1u);
         }
         p.positions[t] = position;
         p.slots[t] = slot;

@@ -18,7 +18,7 @@ constexpr int kMostRequests = 8192;  // three sums and a length of each in share
 
 cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream);
 
-// Status word: 0, or 1 when a length, the span or what was given back was out of range.
+// Status word: 0, or 1 when a length, the span, what was given back or a new row's page was out of range.
 cudaError_t read_kv_plan_status(unsigned* out, bool clear);
 
 }  // namespace tfu
