@@ -133,7 +133,7 @@ def linear(tf, backward=False, q=FAKE, out=FAKE, state=None, last=None, workspac
 @pytest.mark.parametrize("kw,status,asked", [
     (dict(P=0), 1, 1), (dict(P=9), 1, 1), (dict(B=-1), 1, 1), (dict(S=-1), 1, 1), (dict(H=0), 1, 1), (dict(H=7), 2, 2), (dict(D=96), 4, 4),
     (dict(D=256), 4, 4), (dict(dtype=2), 4, 4), (dict(scale=math.nan), 1, 1), (dict(scale=math.inf), 1, 1), (dict(decay=None), 1, 1),
-    (dict(decay=FAKE + 2), 3, 3), (dict(S=2 ** 30 + 1), 4, 4), (dict(B=2 ** 20, S=2 ** 20), 4, 4),
+    (dict(decay=FAKE + 2), 3, 3), (dict(S=2 ** 30 + 1), 4, 4), (dict(B=2 ** 20, S=2 ** 20), 4, 4), (dict(B=2 ** 25, S=0, last=FAKE), 4, 4),
     (dict(q=None), 1, 0), (dict(out=None), 1, 0), (dict(q=FAKE + 8), 3, 0), (dict(out=FAKE + 4), 3, 0), (dict(state=FAKE + 4), 3, 0),
     (dict(last=FAKE + 8), 3, 0), (dict(st=(4096, 252, 64)), 3, 0), (dict(st=(4096, 256, -64)), 4, 0), (dict(st=(4096, 0, 64)), 4, 0),
     (dict(out_st=(4096, 256, 0)), 1, 0),

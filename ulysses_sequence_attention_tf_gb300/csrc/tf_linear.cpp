@@ -23,7 +23,8 @@ tf_status check_linear(const tf_linear* a) {
     if (!a->decay) return fail(TF_ERR_INVALID, "decay is NULL");
     if (reinterpret_cast<uintptr_t>(a->decay) % 4) return fail(TF_ERR_ALIGNMENT, "decay must be 4-byte aligned");
     if (a->S > 1 << 30) return fail(TF_ERR_UNSUPPORTED, "S exceeds 2^30 tokens");
-    if (int64_t(a->B) * a->H * ((int64_t(a->S) + 127) / 128) >= (int64_t(1) << 28))
+    // without tokens a state is still copied
+    if (int64_t(a->B) * a->H >= (int64_t(1) << 28) || int64_t(a->B) * a->H * ((int64_t(a->S) + 127) / 128) >= (int64_t(1) << 28))
         return fail(TF_ERR_UNSUPPORTED, "problem exceeds 2^28 work units");
     return TF_OK;
 }
@@ -162,7 +163,8 @@ tf_status check_pool(const tf_linear* a, const tf_linear_pool* pool, tfu::Linear
         return fail(TF_ERR_ALIGNMENT, "slots and starts must be 4-byte aligned");
     if (a->S > 0 && (pool->max_tokens < 1 || pool->max_tokens > a->S))
         return fail(TF_ERR_INVALID, "max_tokens=%d outside [1, T=%d]", pool->max_tokens, a->S);
-    if (int64_t(pool->N) * a->H * ((int64_t(pool->max_tokens) + 127) / 128) >= (int64_t(1) << 28))
+    if (int64_t(pool->N) * a->H >= (int64_t(1) << 28) ||
+        int64_t(pool->N) * a->H * ((int64_t(pool->max_tokens) + 127) / 128) >= (int64_t(1) << 28))
         return fail(TF_ERR_UNSUPPORTED, "problem exceeds 2^28 work units");
     *p = pass_of(*a);
     p->N = uint32_t(pool->N);
