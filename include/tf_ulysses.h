@@ -616,7 +616,7 @@ typedef struct tf_rotary {
  *  strides      host array of 2 tf_strides: q, k.
  *  q_out, k_out host arrays of P device pointers through out_strides (2 tf_strides, NULL =
  *               contiguous).  q_out may be q itself, with its strides, and k_out k (elements R..D-1
- *               are then not touched); they overlap nothing else.  k_out is NULL without k.
+ *               then keep their bits); they overlap nothing else.  k_out is NULL without k.
  * One launch, nothing is allocated; the call may be captured (positions are read on the device).
  */
 TF_API tf_status tf_ulysses_rope(const tf_rotary *r, const void *const *q, const void *const *k, const tf_strides *strides,
@@ -698,7 +698,8 @@ TF_API tf_status tf_ulysses_linear_attention(const tf_linear *a, const void *con
  *  q, k, v, state   the forward pass's inputs.  strides: host array of 4 tf_strides: dout, q, k, v.
  *  dfinal_state the gradient of the final state, or NULL: zeros.
  *  dq, dk, dv   host arrays of P device pointers, [B, S, H/P, D] through grad_strides (3
- *               tf_strides: dq, dk, dv; NULL = contiguous); every element is written.
+ *               tf_strides: dq, dk, dv; NULL = contiguous); every element is written.  They
+ *               overlap neither one another nor anything that is read.
  *  dstate       the gradient of `state`, or NULL.  Must not overlap state or dfinal_state.
  *  workspace    as above, tf_ulysses_linear_attention_workspace(a, 1) bytes.
  * States are computed again; nothing of the forward pass but its inputs is needed.  There is

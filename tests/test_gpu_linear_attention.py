@@ -24,7 +24,8 @@ def tf():
 
 def decays(kind, H):
     h = torch.arange(H, device="cuda", dtype=torch.float32)
-    return {"slopes": torch.exp2(-8 * (h + 1) / H), "none": 0 * h, "slow": 1e-4 * (h + 1), "fast": 3.0 + h, "mixed": (h % 2) * 100.0}[kind]
+    return {"slopes": torch.exp2(-8 * (h + 1) / H), "none": 0 * h, "slow": 1e-4 * (h + 1), "fast": 3.0 + h, "mixed": (h % 2) * 100.0,
+            "huge": (h % 2) * 1e30}[kind]
 
 
 class Case:
@@ -80,6 +81,40 @@ def test_decays(tf, decay, S, B, H, D, dtype):
     c = Case(B, S, H, D, dtype=dtype, decay=decay, state=True, fused=True, seed=S)
     c.forward(tf)
     c.backward(tf)
+
+
+@pytest.mark.parametrize("S", [5, 300, 6000])
+def test_a_decay_that_leaves_a_token_alone(tf, S):
+    """e^-decay is 0 for every second head: the others' rounding and their own state must not show in it."""
+    c = Case(1, S, 2, 64, decay="huge", state=True)
+    c.forward(tf)
+    c.backward(tf)
+
+
+@pytest.mark.parametrize("S", [3, 140])
+def test_offsets_beyond_32_bits(tf, S):
+    """Batch rows 2^31 elements apart, and a state as far into its pool."""
+    c = Case(3, S, 2, 128, state=True, decay="slow")
+    store, n = torch.empty(2 ** 32 + 2 ** 20, dtype=BF16, device="cuda"), S * 2 * 128
+
+    def far(i, x=None):
+        y = store.as_strided((3, S, 2, 128), (2 ** 31, 256, 128, 1), i * n)
+        return [y if x is None else y.copy_(x)]
+
+    c.q, c.k, c.v, c.dout = (far(i, x[0]) for i, x in enumerate((c.q, c.k, c.v, c.dout)))
+    out, _ = c.forward(tf, out=far(4))
+    assert out[0].stride(0) == 2 ** 31
+    c.backward(tf, dq=far(4), dk=far(5), dv=far(6))
+    del store
+    states = torch.empty((70000, 2, 128, 128), dtype=torch.float32, device="cuda")
+    slots = [69999, 0, 65537]
+    for n, slot in enumerate(slots):
+        states[slot] = c.state[n]
+    rows = [[x[0].reshape(3 * S, 2, 128)] for x in (c.q, c.k, c.v)]
+    starts = torch.arange(0, 3 * S + 1, S, dtype=torch.int32, device="cuda")
+    tf.linear_attend(states, torch.tensor(slots, dtype=torch.int32, device="cuda"), starts, *rows, decay=c.decay, max_tokens=S)
+    want = recurrence(wide(c.q), wide(c.k), wide(c.v), c.decay, c.scale, c.state.double())
+    check_state("state", states[slots], *want[2:])
 
 
 @pytest.mark.parametrize("B,S,H,P", [(1, 6001, 1, 1), (5, 333, 64, 8), (300, 40, 2, 1), (1, 130, 200, 1)])

@@ -113,6 +113,19 @@ def test_strided_and_in_place(tf, rope, R):
 
 
 @pytest.mark.parametrize("rope", ["interleaved", "neox"])
+def test_offsets_beyond_32_bits(tf, rope):
+    """Batch rows 2^31 elements apart, into another tensor and in place."""
+    store = torch.empty(2 ** 32 + 2 ** 16, dtype=BF16, device="cuda")
+    far = [store.as_strided((3, 5, 2, 64), (2 ** 31, 128, 64, 1), i * 640) for i in range(2)]
+    x = rows(3, 5, 2, 64)
+    far[0].copy_(x)
+    f, at = tf.rope_frequencies(64), torch.arange(5, device="cuda").expand(3, 5)
+    for out in (far[1], far[0]):
+        tf.rope([far[0]], q_out=[out], rope=rope)
+        check(x, out, at, f, rope=rope)
+
+
+@pytest.mark.parametrize("rope", ["interleaved", "neox"])
 def test_inverse_is_the_gradient(tf, rope):
     x, g = rows(1, 50, 2, 64, dtype=FP16), rows(1, 50, 2, 64, dtype=FP16, seed=1)
     f = tf.rope_frequencies(48)
