@@ -370,6 +370,32 @@ def test_empty(tf):
     tf.linear_attend(r.states, r.slots, r.starts, r.q, r.k, r.v, decay=r.decay)
 
 
+def test_small_results_lie_apart_and_are_ordinary_tensors(tf):
+    """They may share an allocation, but no memory; one outlives the others; large ones share nothing."""
+    c = Case(2, 40, 4, 64, P=2, state=True)
+    out, last = tf.linear_attention(c.q, c.k, c.v, decay=c.decay, state=c.state, final_state=True)
+    grads = tf.linear_attention_backward(c.dout, c.q, c.k, c.v, decay=c.decay, state=c.state, dstate=c.dstate)
+    for results in ([*out, last], [*grads[0], *grads[1], *grads[2], grads[3]]):
+        spans = sorted((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size()) for x in results)
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:])) and all(a[0] % 32 == 0 for a in spans)
+        assert all(x.is_contiguous() and x.is_leaf and not x.requires_grad and not x.is_inference() for x in results)
+    kept, copy = last, last.clone()
+    x = out[1].requires_grad_()
+    (x.float() * 2).sum().backward()
+    assert bool((x.grad == 2).all()) and x._version == 0
+    out[0].add_(1)
+    assert x._version == 0 and out[0]._version == 1
+    del out, x, grads
+    torch.full((1 << 20,), float("nan"), device="cuda")
+    assert torch.equal(kept, copy)
+    with torch.inference_mode():
+        out, last = tf.linear_attention(c.q, c.k, c.v, decay=c.decay, state=c.state, final_state=True)
+        assert out[0].is_inference() and torch.equal(last, kept)
+    c = Case(1, 2100, 4, 128, P=2)
+    out, last = tf.linear_attention(c.q, c.k, c.v, decay=c.decay, final_state=True)
+    assert len({x.untyped_storage().data_ptr() for x in (*out, last)}) == 3
+
+
 def test_what_is_not_asked_for(tf):
     c = Case(1, 300, 2, 64)
     out, last = tf.linear_attention(c.q, c.k, c.v, decay=c.decay)

@@ -91,6 +91,40 @@ tf_dtype dtype_code(ScalarType t) {
     }
 }
 
+// New contiguous results of one call.  An allocation takes 1.6 us of host time, as much as two kernels' launches, so small results
+// -- up to kSmall bytes altogether -- share one (five of the plan: 12 -> 8 us a call); each of large ones gives its memory back
+// by itself.
+class Results {
+    static constexpr int64_t kSmall = 1 << 20, kAlign = 512;
+    at::TensorOptions like;
+    Tensor all;
+    int64_t room = 0, used = 0, number = 0;
+    static int64_t bytes(IntArrayRef shape, ScalarType type) {
+        int64_t n = int64_t(c10::elementSize(type));
+        for (const int64_t d : shape) n = d > 0 && n > kSmall / d ? kSmall + 1 : n * d;
+        return n;
+    }
+    static int64_t up(int64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+
+public:
+    explicit Results(const at::TensorOptions& options) : like(options) {}
+    // announces what make() is then asked for
+    void plan(IntArrayRef shape, ScalarType type, int64_t times = 1) {
+        room += times * up(bytes(shape, type));
+        number += times;
+    }
+    Tensor make(IntArrayRef shape, ScalarType type) {
+        const int64_t n = up(bytes(shape, type));
+        if (number < 2 || room > kSmall || used + n > room) return at::empty(shape, like.dtype(type));
+        if (!all.defined()) all = at::empty({room}, like.dtype(ScalarType::Byte));
+        Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
+        t.unsafeGetTensorImpl()->set_storage_offset(used / int64_t(c10::elementSize(type)));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+        used += n;
+        return t;
+    }
+};
+
 // P tensors of a list or tuple.
 struct List {
     Tensor t[TF_ULYSSES_MAX_SHARDS];
@@ -107,6 +141,9 @@ struct List {
     // new contiguous tensors
     List(int groups, IntArrayRef shape, const at::TensorOptions& options) : P(groups) {
         for (int i = 0; i < P; ++i) t[i] = at::empty(shape, options);
+    }
+    List(int groups, IntArrayRef shape, ScalarType type, Results& results) : P(groups) {
+        for (int i = 0; i < P; ++i) t[i] = results.make(shape, type);
     }
     PyObject* wrap() const {
         PyObject* list = PyList_New(P);
@@ -459,11 +496,14 @@ PyObject* kv_plan(PyObject* const* x, Py_ssize_t n) {
     p.free_span = ints("span", x[4], 2);
     const char* names[5] = {"lens_out", "starts", "positions", "slots", "span_out"};
     const int64_t sizes[5] = {N, N + 1, p.T, p.T, 2};
+    Results results(table.options());
+    for (int i = 0; i < 5; ++i)
+        if (x[9 + i] == Py_None) results.plan({sizes[i]}, ScalarType::Int);
     Tensor made[5];
     int32_t* at[5];
     for (int i = 0; i < 5; ++i) {
         if (x[9 + i] == Py_None) {
-            made[i] = at::empty({sizes[i]}, table.options());
+            made[i] = results.make({sizes[i]}, ScalarType::Int);
             at[i] = static_cast<int32_t*>(made[i].data_ptr());
         } else {
             at[i] = ints(names[i], x[9 + i], sizes[i]);
@@ -526,10 +566,12 @@ PyObject* rope(PyObject* const* x, Py_ssize_t n) {
             refuse("rotary_dim does not go with " + std::to_string(f.size(0)) + " frequencies");
         r.frequencies = static_cast<const double*>(f.data_ptr());
     }
-    const List qo = x[4] == Py_None ? List(q.P, shape, q.t[0].options()) : List("q_out", x[4], q.P);
-    const Views qov("q_out", qo, shape, type, device);
+    Results results(q.t[0].options());
+    if (x[4] == Py_None) results.plan(shape, type, q.P);
     if (x[1] == Py_None) {
         if (x[5] != Py_None) refuse("k_out is given without k");
+        const List qo = x[4] == Py_None ? List(q.P, shape, type, results) : List("q_out", x[4], q.P);
+        const Views qov("q_out", qo, shape, type, device);
         const tf_strides st[2] = {qv.st, qv.st}, os[2] = {qov.st, qov.st};
         call([&] { return g_abi.rope(&r, qv.ptr, nullptr, st, qov.ptr, nullptr, os, stream); });
         return pair(x[4] == Py_None ? qo.wrap() : same(x[4]), same(Py_None));
@@ -540,7 +582,10 @@ PyObject* rope(PyObject* const* x, Py_ssize_t n) {
     k_shape[dims - 2] = k.t[0].size(dims - 2);
     const Views kv("k", k, k_shape, type, device);
     r.Hk = extent(q.P * k_shape[dims - 2]);
-    const List ko = x[5] == Py_None ? List(q.P, k_shape, k.t[0].options()) : List("k_out", x[5], q.P);
+    if (x[5] == Py_None) results.plan(k_shape, type, q.P);
+    const List qo = x[4] == Py_None ? List(q.P, shape, type, results) : List("q_out", x[4], q.P);
+    const List ko = x[5] == Py_None ? List(q.P, k_shape, type, results) : List("k_out", x[5], q.P);
+    const Views qov("q_out", qo, shape, type, device);
     const Views kov("k_out", ko, k_shape, type, device);
     const tf_strides st[2] = {qv.st, kv.st}, os[2] = {qov.st, kov.st};
     call([&] { return g_abi.rope(&r, qv.ptr, kv.ptr, st, qov.ptr, kov.ptr, os, stream); });
@@ -585,10 +630,10 @@ struct State {
     Tensor t;
     PyObject* given = nullptr;
     float* at = nullptr;
-    State(const char* name, PyObject* o, const Linear& c, int device) {
+    State(const char* name, PyObject* o, const Linear& c, int device, Results& results) {
         if (o == Py_None || o == Py_False) return;
         if (o == Py_True) {
-            t = at::empty(c.states(), c.options().dtype(ScalarType::Float));
+            t = results.make(c.states(), ScalarType::Float);
             at = static_cast<float*>(t.data_ptr());
         } else {
             given = o;
@@ -605,9 +650,12 @@ PyObject* linear_attention(PyObject* const* x, Py_ssize_t n) {
     void* stream = address(x[7]);
     const Linear c(x, device, 4);
     const float* state = static_cast<float*>(plain("state", x[5], ScalarType::Float, c.states(), device));
-    const List out = x[8] == Py_None ? List(c.a.P, c.shape, c.options()) : List("out", x[8], c.a.P);
+    Results results(c.options());
+    if (x[8] == Py_None) results.plan(c.shape, c.type, c.a.P);
+    if (x[9] == Py_True) results.plan(c.states(), ScalarType::Float);
+    const List out = x[8] == Py_None ? List(c.a.P, c.shape, c.type, results) : List("out", x[8], c.a.P);
     const Views ov("out", out, c.shape, c.type, device);
-    const State last("final_state", x[9], c, device);
+    const State last("final_state", x[9], c, device, results);
     const Workspace ws(c.workspace(false), c.options());
     const tf_strides st[3] = {c.qv.st, c.kv.st, c.vv.st};
     call([&] {
@@ -627,10 +675,15 @@ PyObject* linear_attention_backward(PyObject* const* x, Py_ssize_t n) {
     const Views dv("dout", dout, c.shape, c.type, device);
     const float* dfinal = static_cast<float*>(plain("dstate", x[9], ScalarType::Float, c.states(), device));
     const char* names[3] = {"dq", "dk", "dv"};
-    auto made = [&](int i) { return x[10 + i] == Py_None ? List(c.a.P, c.shape, c.options()) : List(names[i], x[10 + i], c.a.P); };
+    PyObject* const asked = x[13] == Py_None && state ? Py_True : x[13];
+    Results results(c.options());
+    for (int i = 0; i < 3; ++i)
+        if (x[10 + i] == Py_None) results.plan(c.shape, c.type, c.a.P);
+    if (asked == Py_True) results.plan(c.states(), ScalarType::Float);
+    auto made = [&](int i) { return x[10 + i] == Py_None ? List(c.a.P, c.shape, c.type, results) : List(names[i], x[10 + i], c.a.P); };
     const List gq = made(0), gk = made(1), gv = made(2);
     const Views gqv("dq", gq, c.shape, c.type, device), gkv("dk", gk, c.shape, c.type, device), gvv("dv", gv, c.shape, c.type, device);
-    const State first("dstate_out", x[13] == Py_None && state ? Py_True : x[13], c, device);
+    const State first("dstate_out", asked, c, device, results);
     const Workspace ws(c.workspace(true), c.options());
     const tf_strides st[4] = {dv.st, c.qv.st, c.kv.st, c.vv.st}, gs[3] = {gqv.st, gkv.st, gvv.st};
     call([&] {
@@ -664,7 +717,9 @@ PyObject* linear_attend(PyObject* const* x, Py_ssize_t n) {
     p.slots = static_cast<int32_t*>(plain("slots", x[6], ScalarType::Int, {p.N}, device));
     p.starts = static_cast<int32_t*>(plain("starts", x[7], ScalarType::Int, {int64_t(p.N) + 1}, device));
     p.max_tokens = x[11] == Py_None ? c.a.S : small("max_tokens", x[11]);
-    const List out = x[10] == Py_None ? List(c.a.P, c.shape, c.options()) : List("out", x[10], c.a.P);
+    Results results(c.options());
+    if (x[10] == Py_None) results.plan(c.shape, c.type, c.a.P);
+    const List out = x[10] == Py_None ? List(c.a.P, c.shape, c.type, results) : List("out", x[10], c.a.P);
     const Views ov("out", out, c.shape, c.type, device);
     size_t need = 0;
     check(g_abi.linear_attend_workspace(&c.a, &p, &need));
