@@ -28,14 +28,15 @@
 // segments, and the segments then go on their own.
 //
 // Bound: DRAM, q, k, v and out once -- 4 KB a chunk row pair of D = 128 in bf16, 2.9 us of an SM's share a chunk.  152 heads of
-// 8192 tokens, D = 128: bf16 232 us (5.5 TB/s, 0.81 of the copy bandwidth), fp16 290; D = 64: 140 and 188 us.  A chunk
+// 8192 tokens, D = 128: bf16 232 us (5.5 TB/s, 0.81 of the copy bandwidth), fp16 290; D = 64: 129 and 187 us.  A chunk
 // takes 3.5 us: its groups take 1.5 to 1.9 us each for their part, and the scores, P and the product with P follow one
 // another.  The matrix pipe is busy 32 % of the cycles, issue slots 35 %; what stalls a group is its own latency (TMEM and shared memory,
 // whose bandwidth the products with both operands there take half of) and instruction fetches of six different codes.  40
 // heads of 32760 tokens: 374 us, 94 of them the segments' sums, 8 their join.
 // Measured on the way to this split (152 heads of 8192 tokens, bf16, D = 128): keys weighted by the state's warps 598 us at
 // the video shape, by four warps of their own 559, by eight 477; the parts rounded one from another instead of cut 281 us
-// here, cut 236; P and output shared by both groups, half of the columns each, 254; D = 64 with scores of one chunk in TMEM 152, of two 140.
+// here, cut 236; P and output shared by both groups, half of the columns each, 254; D = 64 with scores of one chunk in TMEM 152, of two
+// 140, with two chunks' rest tiles 130.
 // Registers: the groups' shares are what they hold; 8 to 60 bytes a thread are spilled (0.1 % of the instructions at D = 128,
 // 0.8 % at D = 64).
 #include "attention_common.cuh"
@@ -61,7 +62,9 @@ struct Shape {
     static constexpr int kTiles = kOutputs ? 3 : 2;                      // a chunk's
     static constexpr int kStages = kD == 128 ? (kOutputs ? 6 : 7) - kRests : 9;
     static constexpr size_t kBars = kD == 64 ? 2816 : 2048;
-    static constexpr size_t kSmem = (kStages + kRests) * size_t(kTile) + (kOutputs ? kStateTile : 0) + kBars + 1024;  // and alignment
+    // D = 64 has room for two chunks' rest tiles, so that the keys of a chunk are weighted beside the product before it
+    static constexpr int kSets = kD == 64 ? 2 : 1;
+    static constexpr size_t kSmem = (kStages + kSets * kRests) * size_t(kTile) + (kOutputs ? kStateTile : 0) + kBars + 1024;  // and alignment
 };
 
 constexpr uint32_t kRowsTransposed = 1u << 15;  // of f16_idesc: A MN-major
@@ -157,7 +160,7 @@ template <Fused kF, int kD, bool kOutputs, int kRests, bool kOne>
 __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __grid_constant__ LinearChunkParams cp) {
     using Sh = Shape<kD, kOutputs, kRests>;
     constexpr uint32_t kTile = Sh::kTile;
-    constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles;
+    constexpr int kStages = Sh::kStages, kTiles = Sh::kTiles, kSets = Sh::kSets;
     constexpr uint32_t kScores = kD == 64 ? 2 : 1;  // chunks whose scores TMEM holds: D = 128 fills its 512 columns with one
     constexpr uint32_t kFactors = 2 * kScores;      // P is up to kScores chunks ahead of the output
     constexpr bool kFp16 = kF == Fused::kFP16;
@@ -168,22 +171,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* rest_tiles = smem + kStages * size_t(kTile);  // of K_w
-    uint8_t* state_tile = rest_tiles + kRests * kTile;
+    uint8_t* state_tile = rest_tiles + kSets * kRests * kTile;
     uint64_t* bars = reinterpret_cast<uint64_t*>(state_tile + (kOutputs ? Sh::kStateTile : 0));
     const uint32_t ring = smem_u32(smem);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
     const uint32_t x_full0 = empty0 + 8 * kStages, p_ready0 = x_full0 + 16, o1_full = p_ready0 + 16, o2_full = o1_full + 8,
-                   o_free = o2_full + 8, s_ready = o_free + 8, k_ready0 = s_ready + 8, ds_full = k_ready0 + 16, ds_free = ds_full + 8,
+                   o_free = o2_full + 8, s_ready = o_free + 8, k_ready0 = s_ready + 8, ds_full0 = k_ready0 + 16, ds_free = ds_full0 + 16,
                    done_a = ds_free + 8, done_b = done_a + 8, done_c = done_b + 8, state_largest = done_c + 8, key_largest = state_largest + 8;
-    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 18);
+    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 18);  // 16-byte aligned
     float* decays = floats;             // [64]: lambda^(31 - r), reverse: lambda^(r - 32), 0 where that is no decay
     float* state_factor = floats + 64;  // fp16: what O2 is to be multiplied by, [2] by parity of the chunk
-    float* key_factor = floats + 66;    // dS, [2]
-    float* largest = floats + 68;       // [2][4], [2][8]
-    float* row_factor = floats + 92;    // O1's rows, [kFactors][128]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 92 + kFactors * kChunk);
+    // dS, [4] by chunk: the keys of chunk x + 4 wait for the product of x + 2 at the least, which waits for the state to have taken x + 1
+    float* key_factor = floats + 66;
+    float* largest = floats + 70;       // [2][4], [2][8]
+    float* row_factor = floats + 94;    // O1's rows, [kFactors][128]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 94 + kFactors * kChunk);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 18) * 8 + (94 + kFactors * kChunk) * 4 <= int(Sh::kBars), "barriers and factors");
+    static_assert((2 * kStages + 18) * 8 + (96 + kFactors * kChunk) * 4 <= int(Sh::kBars), "barriers and factors");
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4, group = warp / 4;
 
     if (threadIdx.x == 0) {
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         mbar_init(o2_full, 1);
         mbar_init(o_free, 4);
         mbar_init(s_ready, 4);
-        mbar_init(ds_full, 1);
+        for (uint32_t s = 0; s < uint32_t(kSets); ++s) mbar_init(ds_full0 + 8 * s, 1);
         mbar_init(ds_free, 4);
         mbar_init(done_a, 1);
         mbar_init(done_b, 1);
@@ -244,6 +248,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     auto all_wait = [&](uint32_t bar, uint32_t x) { return bool(__all_sync(0xffffffffu, wait(bar, x))); };
     auto wait2 = [&](uint32_t bar0, uint32_t x) { return wait(bar0 + 8 * (x % kScores), x / kScores); };
     auto all_wait2 = [&](uint32_t bar0, uint32_t x) { return all_wait(bar0 + 8 * (x % kScores), x / kScores); };
+    auto ds_full = [&](uint32_t x) { return ds_full0 + 8 * (x % kSets); };
+    auto all_wait_ds = [&](uint32_t x) { return all_wait(ds_full(x), x / kSets); };
     auto scores_of = [&](uint32_t x) { return tmem + x % kScores * kChunk; };
     auto landed = [&](uint32_t m) { return wait(full0 + 8 * (m % kStages), m / kStages); };  // the ring's tile m
     auto arrive = [&](uint32_t bar) {
@@ -339,7 +345,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 // a short chunk among rows of other sequences: the rows behind it are cleared with P
                 if (kOutputs && rows_of_sequences && chunk_len(chunk_at(x)) < kChunk && !wait2(p_ready0, x)) break;
                 tc_fence_after();
-                const uint32_t b = v_low + vs * (kTile >> 4), a = k_low + ks * (kTile >> 4);
+                const uint32_t b = v_low + vs * (kTile >> 4), a = k_low + ks * (kTile >> 4), rests = rest_low + x % kSets * (kRests * kTile >> 4);
                 tc_mma_low<false>(ds_tmem, a, b, kIdescS);
 #pragma unroll
                 for (uint32_t kk = 1; kk < kChunk / 16; ++kk) tc_mma_low<true>(ds_tmem, a + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescS);
@@ -347,8 +353,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 for (int r = 0; r < kRests; ++r)
 #pragma unroll
                     for (uint32_t kk = 0; kk < kChunk / 16; ++kk)
-                        tc_mma_low<true>(ds_tmem, rest_low + r * (kTile >> 4) + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescS);
-                tc_commit(ds_full);
+                        tc_mma_low<true>(ds_tmem, rests + r * (kTile >> 4) + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescS);
+                tc_commit(ds_full(x));
                 tc_commit(empty0 + 8 * ks);
                 tc_commit(empty0 + 8 * vs);
             }
@@ -562,9 +568,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 arrive(s_ready);
             }
             const Fade fade(decay * float(len));
-            if (!(ok = all_wait(ds_full, x))) break;
+            if (!(ok = all_wait_ds(x))) break;
             tc_fence_after();
-            const float back = kFp16 ? p.kv_scale * key_factor[x & 1u] : p.kv_scale;
+            const float back = kFp16 ? p.kv_scale * key_factor[x & 3u] : p.kv_scale;
             const uint64_t back2 = f2_pack(back, back), factor2 = f2_pack(fade.factor, fade.factor), whole2 = f2_pack(fade.whole, fade.whole);
 #pragma unroll
             for (int z = 0; z < kCols; z += 32) {
@@ -599,12 +605,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         for (uint32_t x = 0; x < visits; ++x) {
             const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2;
             // the scores no longer need K as it came; the products with the rest tiles' last contents have completed
-            if ((kOutputs && !all_wait2(x_full0, x)) || !__all_sync(0xffffffffu, landed(m)) || (x > 0 && !all_wait(ds_full, x - 1))) break;
+            if ((kOutputs && !all_wait2(x_full0, x)) || !__all_sync(0xffffffffu, landed(m)) || (x >= kSets && !all_wait_ds(x - kSets))) break;
             const bool valid = t < len;
             float w = valid ? expf(-decay * float(reverse ? t + 1 : len - 1 - t)) : 0.f;
             // D = 128: 64 elements are a half of the tile; D = 64: 32 of the row
             uint8_t* key = smem + (m % kStages) * size_t(kTile) + t * kSwizzleRow;
-            uint8_t* rest = rest_tiles + t * kSwizzleRow;
+            uint8_t* rest = rest_tiles + x % kSets * (kRests * kTile) + t * kSwizzleRow;
             auto vec = [&](int y) {
                 return kD == 128 ? half * kHalfTile + ((uint32_t(y) ^ (t & 7u)) * 16) : ((half * 4 + uint32_t(y)) ^ (t & 7u)) * 16;
             };
@@ -621,7 +627,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 if (!most.of(v, warp - 12, lane, abort_flag)) break;
                 const float to_half = up_scale(v);
                 w *= to_half;
-                if (t == 0 && half == 0) key_factor[x & 1u] = inverse(to_half);
+                if (t == 0 && half == 0) key_factor[x & 3u] = inverse(to_half);
             }
             const uint64_t w2 = f2_pack(w, w);
 #pragma unroll
