@@ -32,7 +32,7 @@
 // takes 3.5 us: its groups take 1.5 to 1.9 us each for their part, and the scores, P and the product with P follow one
 // another.  The matrix pipe is busy 32 % of the cycles, issue slots 35 %; what stalls a group is its own latency (TMEM and shared memory,
 // whose bandwidth the products with both operands there take half of) and instruction fetches of six different codes.  40
-// heads of 32760 tokens: 374 us, 94 of them the segments' sums, 8 their join.
+// heads of 32760 tokens: 372 us, 94 of them the segments' sums, 8 their join.
 // Measured on the way to this split (152 heads of 8192 tokens, bf16, D = 128): keys weighted by the state's warps 598 us at
 // the video shape, by four warps of their own 559, by eight 477; the parts rounded one from another instead of cut 281 us
 // here, cut 236; P and output shared by both groups, half of the columns each, 254; D = 64 with scores of one chunk in TMEM 152, of two
@@ -190,6 +190,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     static_assert((2 * kStages + 18) * 8 + (96 + kFactors * kChunk) * 4 <= int(Sh::kBars), "barriers and factors");
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4, group = warp / 4;
 
+    // the unit: sequence, head, segment.  In the grid's order the passes of a unit lie beside one another, then the
+    // segments of a head, a reverse pass's from its last on: what runs together reads the same tokens
+    const uint32_t heads = p.P * p.Hl, here = kOutputs ? cp.segments : cp.segments - 1;
+    const uint32_t seg = reverse ? here - 1 - block % here : block % here, unit = block / here, head = unit % heads, n = unit / heads;
+    const uint32_t g = head / p.Hl, h = head % p.Hl;
+
+    if (threadIdx.x == 640)  // the producer's thread
+        for (int y = 3 - kTiles; y < 3; ++y)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&cp.maps[cp.tensor[which][y]].m[g])) : "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -225,11 +234,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     grid_dependency_wait();
     const uint32_t tmem = *tmem_slot, o1_tmem = tmem + kScores * kChunk, o2_tmem = o1_tmem + kD, ds_tmem = o2_tmem + kD;
 
-    // the unit: sequence, head, segment.  In the grid's order the passes of a unit lie beside one another, then the
-    // segments of a head, a reverse pass's from its last on: what runs together reads the same tokens
-    const uint32_t heads = p.P * p.Hl, here = kOutputs ? cp.segments : cp.segments - 1;
-    const uint32_t seg = reverse ? here - 1 - block % here : block % here, unit = block / here, head = unit % heads, n = unit / heads;
-    const uint32_t g = head / p.Hl, h = head % p.Hl;
     const LinearSequence seq = linear_sequence(p, n, &g_linear_chunks_status);
     const uint32_t chunks = (seq.len + kChunk - 1) / kChunk, first = seg * cp.seg_chunks;
     const uint32_t count = seq.ok && chunks > first ? min(chunks - first, cp.seg_chunks) : 0;
