@@ -240,7 +240,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     const uint32_t count = seq.ok && chunks > first ? min(chunks - first, cp.seg_chunks) : 0;
     const bool last = first + count == chunks;  // of this sequence's segments
     const bool work = count > 0 && (kOutputs || !last);
-    const float decay = p.decay[head];
+    // a decay that leaves nothing of the token before is as good as any larger one, and times log2 e it stays finite: 0 times it is 0
+    constexpr float kMostDecay = 256.f;
+    const float decay = p.decay[head] > kMostDecay ? kMostDecay : p.decay[head];
     // a segment's sum: what is more than kGone / decay tokens in front of its end weighs less than fp32's least number (e^-104 < 2^-149)
     constexpr float kGone = 104.f;
     const float reach = kGone / (decay * float(kChunk)) + 1.f;  // chunks
