@@ -656,9 +656,10 @@ TF_API tf_status tf_ulysses_rope_frequencies(int rotary_dim, double theta, tf_ro
  *         = scale * ( sum_(j <= t) e^(-decay (t - j)) (q_t . k_j) v_j + e^(-decay (t + 1)) q_t state )
  * States, sums and decays are fp32.  Chunks of tokens go through the tensor cores: the
  * weights e^(-decay (t - j)) (q_t . k_j) and the states are rounded to the I/O type for the products
- * with V and q (in fp16 times powers of two that keep them in its normal range); keys times
- * their decay enter a state as a sum of numbers of the I/O type, within 2^-24 of the key in bf16
- * and 2^-22 in fp16 where a state is handed out, 2^-16 in bf16 where it stays inside the call.
+ * with V and q (in fp16 times powers of two: entries of a state below 2^-27 of its largest lose bits); keys times
+ * their decay enter a state as a sum of numbers of the I/O type: in bf16 within 2^-24 of the key where a state is
+ * handed out, 2^-16 where it stays inside the call; in fp16 within 2^-22 of the key or 2^-27 of the largest weighted
+ * key of its channel among the chunk's tokens, whichever is more.
  * Inputs should be finite: a token's infinity or NaN reaches every later output of its head,
  * and in V also earlier ones among the same 128 tokens.  A negative decay is not refused (it
  * lies on the device) but grows without bound.

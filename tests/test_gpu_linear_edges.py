@@ -51,3 +51,41 @@ def test_decays_up_to_the_largest_number(tf, S, D, dtype):
     q, k, v, dout = (rows(1, S, 6, D, dtype, i) for i in range(4))
     state, dstate = (torch.randn((1, 6, D, D), generator=torch.Generator(device="cuda").manual_seed(i), device="cuda") for i in (5, 6))
     check_all(tf, q, k, v, dout, decay, state, dstate, dtype)
+
+
+def channels(D, *sizes):
+    """[D]: sizes in turn."""
+    return torch.tensor(sizes, device="cuda").repeat(D // len(sizes))
+
+
+@pytest.mark.parametrize("S", [3, 8, 9, 16, 17, 100, 128, 300, 1100])
+@pytest.mark.parametrize("D,H", [(64, 2), (128, 2), (64, 400)])
+@pytest.mark.parametrize("large,small", [(100.0, 1e-3), (100.0, 1e-5)])
+def test_channels_of_unlike_size(tf, S, D, H, large, small):
+    """fp16: a key channel far smaller than another keeps its bits in the state, token by token and in chunks.  The state's
+    columns are as unlike for dQ."""
+    if H > 2 and S > 128:
+        return
+    size = channels(D, large, small)
+    decay = torch.tensor([0.05, 0.4], device="cuda").repeat(H // 2)
+    q, k, v, dout = (rows(1, S, H, D, FP16, i) for i in range(4))
+    k = [(k[0].float() * size).to(FP16)]
+    state, dstate = (torch.randn((1, H, D, D), generator=torch.Generator(device="cuda").manual_seed(i), device="cuda") for i in (5, 6))
+    check_all(tf, q, k, v, dout, decay, state * size[:, None], dstate, FP16)
+
+
+@pytest.mark.parametrize("S", [5, 16, 17, 128, 300, 3000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_channels_over_the_whole_range_of_fp16(tf, S, D):
+    size = channels(D, 8192.0, 1e-6, 1.0, 1e-3)
+    decay = torch.tensor([0.0, 0.01, 0.3, 3.0], device="cuda")
+    q, k, v = (rows(2, S, 4, D, FP16, i) for i in range(3))
+    k = [(k[0].float().clamp(-4, 4) * size).to(FP16)]
+    out, last = tf.linear_attention(q, k, v, decay=decay, final_state=True, scale=1e-4)
+    want = recurrence(wide(q), wide(k), wide(v), decay, 1e-4)
+    check_rows("out", out, *want[:2], FP16)
+    check_state("state", last, *want[2:])
+    starts, slots = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, S, 2 * S], [1, 0]))
+    states = torch.zeros((2, 4, D, D), device="cuda")
+    tf.linear_attend(states, slots, starts, *[[x[0].reshape(2 * S, 4, D)] for x in (q, k, v)], decay=decay, max_tokens=S)
+    check_state("states", states.flip(0), *want[2:])

@@ -20,8 +20,9 @@
 // add up over the chunks.  K_w is a sum of several 16-bit numbers, because S is fp32 and outlives the chunk: two fp16 ones, two
 // bf16 ones (2^-16 of a key: S is 2.4e-6 off) for states that only enter outputs, three (S 3e-7 off) for those handed
 // out.  P and S only enter the chunk's own output, in 16 bits like it.
-// fp16: P is scaled by a power of two by its row, S and K_w by that of their largest value, so that none of them
-// leaves fp16's normal range.
+// fp16: powers of two bring the largest value of each row of P, of S and of each channel (column) of K_w into [2^13, 2^14), so that
+// what is smaller keeps its 11 bits down to 2^-27 of it, K_w its 22 down to 2^-16 of it, and below is off by 2^-38 of it at
+// most.  A channel's factor comes out as that of a row of dS, where S takes it in.
 //
 // Segments: where there are fewer heads than SMs, each sequence is cut.  A first launch finds what every segment but the
 // last adds to the state (K and V only), a second one runs these sums up to the states in front of the
@@ -62,7 +63,7 @@ struct Shape {
     static constexpr uint32_t kStateTile = kD * kSwizzleRow * (kD / 64);
     static constexpr int kTiles = kOutputs ? 3 : 2;                      // a chunk's
     static constexpr int kStages = kD == 128 ? (kOutputs ? 6 : 7) - kRests : 9;
-    static constexpr size_t kBars = kD == 64 ? 2816 : 2048;
+    static constexpr size_t kBars = 2048;
     // D = 64 has room for two chunks' rest tiles, so that the keys of a chunk are weighted beside the product before it
     static constexpr int kSets = kD == 64 ? 2 : 1;
     static constexpr size_t kSmem = (kStages + kSets * kRests) * size_t(kTile) + (kOutputs ? kStateTile : 0) + kBars + 1024;  // and alignment
@@ -97,6 +98,7 @@ __device__ __forceinline__ float up_scale(float v) {
     const int to = 127 + 13 - (e - 127);
     return __uint_as_float(uint32_t(min(to, 253)) << 23);
 }
+__device__ __forceinline__ float power_of(uint8_t exponent) { return __uint_as_float(uint32_t(exponent) << 23); }
 __device__ __forceinline__ float inverse(float power_of_two) { return __uint_as_float((254u << 23) - __float_as_uint(power_of_two)); }
 
 // 16 consecutive 32-bit columns of this thread's TMEM lane
@@ -178,17 +180,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
     const uint32_t x_full0 = empty0 + 8 * kStages, p_ready0 = x_full0 + 16, o1_full = p_ready0 + 16, o2_full = o1_full + 8,
                    o_free = o2_full + 8, s_ready = o_free + 8, k_ready0 = s_ready + 8, ds_full0 = k_ready0 + 16, ds_free = ds_full0 + 16,
-                   done_a = ds_free + 8, done_b = done_a + 8, done_c = done_b + 8, state_largest = done_c + 8, key_largest = state_largest + 8;
-    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + 18);  // 16-byte aligned
+                   done_a = ds_free + 8, done_b = done_a + 8, done_c = done_b + 8, state_largest = done_c + 8, keys_met = state_largest + 8,
+                   k_begun0 = keys_met + 8;
+    constexpr int kFixedBars = 20;  // an even number
+    float* floats = reinterpret_cast<float*>(bars + 2 * kStages + kFixedBars);  // 16-byte aligned
     float* decays = floats;             // [64]: lambda^(31 - r), reverse: lambda^(r - 32), 0 where that is no decay
     float* state_factor = floats + 64;  // fp16: what O2 is to be multiplied by, [2] by parity of the chunk
-    // dS, [4] by chunk: the keys of chunk x + 4 wait for the product of x + 2 at the least, which waits for the state to have taken x + 1
-    float* key_factor = floats + 66;
-    float* largest = floats + 70;       // [2][4], [2][8]
-    float* row_factor = floats + 94;    // O1's rows, [kFactors][128]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(floats + 94 + kFactors * kChunk);
+    float* largest = floats + 66;       // [2][4]
+    // fp16: biased exponents of the channels' powers of two, [kExponents][D] by chunk: the keys of chunk x + kExponents wait for the
+    // product of x + kExponents - kSets, which waits for the state to have taken the chunk before that one, x at the least
+    constexpr uint32_t kExponents = 256 / kD;
+    static_assert(kExponents > kSets, "a factor is overwritten behind its reader");
+    uint8_t* key_exponents = reinterpret_cast<uint8_t*>(floats + 74);
+    uint8_t* row_exponents = key_exponents + 256;  // of the powers of two of P's rows, [kFactors][128]
+    float* key_scale = floats + 140 + kFactors * kChunk / 4;  // this chunk's powers of two by channel, [D]; 16-byte aligned
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(key_scale + kD);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 18) * 8 + (96 + kFactors * kChunk) * 4 <= int(Sh::kBars), "barriers and factors");
+    static_assert((2 * kStages + kFixedBars) * 8 + (142 + kFactors * kChunk / 4 + kD) * 4 <= int(Sh::kBars), "barriers and factors");
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, quarter = warp % 4, group = warp / 4;
 
     // the unit: sequence, head, segment.  In the grid's order the passes of a unit lie beside one another, then the
@@ -209,6 +217,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             mbar_init(x_full0 + 8 * s, 1);
             mbar_init(p_ready0 + 8 * s, 4);  // a warp each
             mbar_init(k_ready0 + 8 * s, 8);
+            mbar_init(k_begun0 + 8 * s, 8);
         }
         mbar_init(o1_full, 1);
         mbar_init(o2_full, 1);
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         mbar_init(done_b, 1);
         mbar_init(done_c, 1);
         mbar_init(state_largest, 4);
-        mbar_init(key_largest, 8);
+        mbar_init(keys_met, 8);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 const uint32_t m = x * kTiles, qs = m % kStages, ks = (m + 1) % kStages;
                 if (!landed(m) || !landed(m + 1)) return false;
                 // no arrival on x_full runs two phases ahead of the warps that wait for it to weight the keys
-                if (x >= kScores && !wait2(k_ready0, x - kScores)) return false;
+                if (x >= kScores && !wait2(k_begun0, x - kScores)) return false;
                 tc_fence_after();
                 tc_product<kD, kHalfTile, kHalfTile>(scores_of(x), low + qs * (kTile >> 4), low + ks * (kTile >> 4), kIdescX);
                 tc_commit(x_full0 + 8 * (x % kScores));
@@ -431,7 +440,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                         for (int y = 0; y < 32; ++y) most = (columns >> y) & 1u ? fmaxf(most, fabsf(__uint_as_float(r[y]))) : most;
                     }
                     const float to_half = up_scale(most * fabsf(both_scales));
-                    row_factor[x % kFactors * kChunk + a] = inverse(to_half);
+                    row_exponents[x % kFactors * kChunk + a] = uint8_t(__float_as_uint(to_half) >> 23);
                     f *= to_half;
                 }
 #pragma unroll 1
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 if (reverse) age = p.out_scale * expf(-decay * float(int(len) - 1 - int(a)));
                 if (!all_wait(o1_full, x) || !all_wait(o2_full, x)) break;
                 tc_fence_after();
-                const float f1 = kFp16 ? row_factor[x % kFactors * kChunk + a] : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
+                const float f1 = kFp16 ? inverse(power_of(row_exponents[x % kFactors * kChunk + a])) : 1.f, f2 = kFp16 ? age * state_factor[x & 1u] : age;
                 const uint64_t f1_2 = f2_pack(f1, f1), f2_2 = f2_pack(f2, f2);
                 uint8_t* dst = p.out.base[g] + int64_t(seq.b) * p.out.b + (seq.first + at + (valid ? a : 0)) * p.out.t + int64_t(h) * p.out.h;
 #pragma unroll 1
@@ -577,7 +586,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const Fade fade(decay * float(len));
             if (!(ok = all_wait_ds(x))) break;
             tc_fence_after();
-            const float back = kFp16 ? p.kv_scale * key_factor[x & 3u] : p.kv_scale;
+            const float back =
+                kFp16 ? p.kv_scale * inverse(power_of(key_exponents[x % kExponents * kD + row])) : p.kv_scale;
             const uint64_t back2 = f2_pack(back, back), factor2 = f2_pack(fade.factor, fade.factor), whole2 = f2_pack(fade.whole, fade.whole);
 #pragma unroll
             for (int z = 0; z < kCols; z += 32) {
@@ -608,13 +618,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
         registers<Registers<kD>::kK>();
         // ---------------- the keys times their decay: a thread half a row of the chunk
         const uint32_t t = quarter * 32 + lane, half = group - 3;
-        Largest<8> most{largest + 8, key_largest, 0};
         for (uint32_t x = 0; x < visits; ++x) {
             const uint32_t len = chunk_len(chunk_at(x)), m = x * kTiles + kTiles - 2;
             // the scores no longer need K as it came; the products with the rest tiles' last contents have completed
             if ((kOutputs && !all_wait2(x_full0, x)) || !__all_sync(0xffffffffu, landed(m)) || (x >= kSets && !all_wait_ds(x - kSets))) break;
+            if (kOutputs) arrive(k_begun0 + 8 * (x % kScores));
             const bool valid = t < len;
-            float w = valid ? expf(-decay * float(reverse ? t + 1 : len - 1 - t)) : 0.f;
+            const float w = valid ? expf(-decay * float(reverse ? t + 1 : len - 1 - t)) : 0.f;
             // D = 128: 64 elements are a half of the tile; D = 64: 32 of the row
             uint8_t* key = smem + (m % kStages) * size_t(kTile) + t * kSwizzleRow;
             uint8_t* rest = rest_tiles + x % kSets * (kRests * kTile) + t * kSwizzleRow;
@@ -622,22 +632,55 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 return kD == 128 ? half * kHalfTile + ((uint32_t(y) ^ (t & 7u)) * 16) : ((half * 4 + uint32_t(y)) ^ (t & 7u)) * 16;
             };
             constexpr int kVecs = kD / 16;
+            // the groups' codes share the instruction cache: fp16 by half of the vectors 329 -> 299 us (D = 64 216 -> 204), all rolled up 302
+            constexpr int kAtOnce = kFp16 ? kVecs / 2 : kVecs;
             if (kFp16) {
-                uint32_t found = 0;  // fp16 numbers without their signs order as integers
+                // every channel's largest weighted key: a lane takes two channels, a warp a part of the tokens; the parts meet where
+                // the rests are written afterwards
+                constexpr uint32_t kParts = kD == 128 ? 4 : 8, kEach = kChunk / kParts;
+                const uint32_t part = kD == 128 ? quarter : quarter * 2 + half, channel = kD == 128 ? half * 64 : 0;
+                float* const found = reinterpret_cast<float*>(rest_tiles + x % kSets * (kRests * kTile));  // [kParts][D]
+                const uint8_t* from = smem + (m % kStages) * size_t(kTile) + channel / 64 * kHalfTile + part * kEach * kSwizzleRow + lane % 4 * 4;
+                auto word = [&](uint32_t i) { return *reinterpret_cast<const __half2*>(from + i * kSwizzleRow + ((lane / 4) ^ (i & 7u)) * 16); };
+                float most0 = 0.f, most1 = 0.f;  // fmaxf passes over NaN: rows of no token, times 0
+                auto take = [&](__half2 two, uint32_t token) {
+                    const float weight = __shfl_sync(0xffffffffu, w, token % 32);
+                    const float2 k = __half22float2(two);
+                    most0 = fmaxf(most0, fabsf(k.x) * weight);
+                    most1 = fmaxf(most1, fabsf(k.y) * weight);
+                };
+                // Eight tokens may share the weight of the one that has faded least, e^7 too large at most (2^-27 and 2^-6 in place of 2^-38
+                // and 2^-16 of a channel's largest): 152 heads of 8192 tokens 299 us, every token by its own 317.
+                if (decay >= 0.f && decay <= 1.f && len == kChunk) {
+                    const uint32_t nearest = reverse ? 0 : 7;
 #pragma unroll
-                for (int y = 0; y < kVecs; ++y) {
-                    const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
-                    found = __vmaxu2(__vmaxu2(found, k.x & 0x7fff7fffu), __vmaxu2(k.y & 0x7fff7fffu, __vmaxu2(k.z & 0x7fff7fffu, k.w & 0x7fff7fffu)));
+                    for (uint32_t i = 0; i < kEach; i += 8) {
+                        __half2 eight = __habs2(word(i));
+#pragma unroll
+                        for (uint32_t z = 1; z < 8; ++z) eight = __hmax2(eight, __habs2(word(i + z)));
+                        take(eight, part * kEach + i + nearest);
+                    }
+                } else {
+#pragma unroll 8
+                    for (uint32_t i = 0; i < kEach; ++i) take(word(i), part * kEach + i);
                 }
-                found = max(found & 0xffffu, found >> 16);
-                float v = valid ? w * __half2float(__ushort_as_half(uint16_t(found))) : 0.f;
-                if (!most.of(v, warp - 12, lane, abort_flag)) break;
-                const float to_half = up_scale(v);
-                w *= to_half;
-                if (t == 0 && half == 0) key_factor[x & 3u] = inverse(to_half);
+                *reinterpret_cast<float2*>(found + part * kD + channel + lane * 2) = make_float2(most0, most1);
+                arrive(keys_met);
+                if (!all_wait(keys_met, 0)) break;
+                const uint32_t c = half * 128 + t;
+                if (c < kD) {
+                    float v = found[c];
+#pragma unroll
+                    for (uint32_t y = 1; y < kParts; ++y) v = fmaxf(v, found[y * kD + c]);
+                    const float to_half = up_scale(v);
+                    key_scale[c] = to_half;
+                    key_exponents[x % kExponents * kD + c] = uint8_t(__float_as_uint(to_half) >> 23);
+                }
+                arrive(keys_met);
+                if (!all_wait(keys_met, 1)) break;
             }
             const uint64_t w2 = f2_pack(w, w);
-#pragma unroll
+#pragma unroll kAtOnce
             for (int y = 0; y < kVecs; ++y) {
                 const uint4 k = *reinterpret_cast<const uint4*>(key + vec(y));
                 const uint32_t kw[4] = {valid ? k.x : 0u, valid ? k.y : 0u, valid ? k.z : 0u, valid ? k.w : 0u};
@@ -647,6 +690,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                     float lo, hi;
                     unpack2<kF>(kw[i], lo, hi);
                     uint64_t v = f2_mul(f2_pack(lo, hi), w2);
+                    if (kFp16) v = f2_mul(v, *reinterpret_cast<const uint64_t*>(key_scale + half * (kD / 2) + y * 8 + i * 2));
 #pragma unroll
                     for (int r = 0; r < kRests; ++r) part[r][i] = take_part<kF>(v);
                     f2_unpack(v, lo, hi);
