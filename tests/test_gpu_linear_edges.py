@@ -89,3 +89,23 @@ def test_channels_over_the_whole_range_of_fp16(tf, S, D):
     states = torch.zeros((2, 4, D, D), device="cuda")
     tf.linear_attend(states, slots, starts, *[[x[0].reshape(2 * S, 4, D)] for x in (q, k, v)], decay=decay, max_tokens=S)
     check_state("states", states.flip(0), *want[2:])
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_tokens_that_have_faded(tf, reverse, D):
+    """fp16: keys 2^29 times as large as a row's own, 10 tokens and more away at a decay of 3, weigh nothing in that row -- also
+    not by taking its power of two.  Outputs beyond fp16 are infinite."""
+    S, H, scale = 260, 2, 2.0 ** 12
+    decay = torch.full((H,), 3.0, device="cuda")
+    q, k, v = (rows(1, S, H, D, FP16, i) for i in range(3))
+    token = torch.arange(S, device="cuda") % 128
+    size = torch.where((token >= 64) == reverse, 2.0 ** 13, 2.0 ** -16)[:, None, None]
+    k = [(k[0].float().clamp(-4, 4) * size).to(FP16)]
+    if reverse:  # of the gradients: dV_j sums k_j . q_i over later rows i
+        got = tf.linear_attention_backward(v, k, q, v, decay=decay, scale=scale)[2]
+        want = recurrence(wide(q), wide(k), wide(v), decay, scale, None, 1.0, reverse=True)
+    else:
+        got, _ = tf.linear_attention(q, k, v, decay=decay, scale=scale)
+        want = recurrence(wide(q), wide(k), wide(v), decay, scale)
+    check_rows("rows", got, *want[:2], FP16, norm=False)

@@ -391,6 +391,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
             const float* own_decays = decays + (reverse ? 32 - lane : 31 - lane);  // of columns in the row's own block
             const float* far_decays = decays + (reverse ? 32 : 0);                 // of others, up to a factor
             const uint32_t own_columns = reverse ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+            // of block j's columns, what far_decays leaves out
+            auto far_factor = [&](uint32_t j) {
+                const int gone = reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
+                return ex2(-c * float(gone));
+            };
             // scores of 32 columns times their decays, from column 32 j of the row on
             auto weighted = [&](uint32_t at, uint32_t j, uint64_t (&w)[16], const float scales) {
                 uint32_t r[32];
@@ -406,8 +411,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                                        (own_columns >> (2 * y + 1)) & 1u ? __uint_as_float(r[2 * y + 1]) * w1 : 0.f);
                     }
                 } else {
-                    const int gone = reverse ? int(32 * (j - quarter)) - int(lane) : int(32 * (quarter - j)) + int(lane) - 31;
-                    const float f = ex2(-c * float(gone)) * scales;
+                    const float f = far_factor(j) * scales;
                     const uint64_t f2 = f2_pack(f, f);
 #pragma unroll
                     for (int y = 0; y < 16; y += 2) {
@@ -425,8 +429,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                 const uint32_t at = scores_of(x) + lane_base;
                 float f = both_scales;
                 if (kFp16) {
-                    // the row's power of two, from its scores as they are: decays are at most 1, and 2^-28 of the largest
-                    // is still a normal number
+                    // the row's power of two, from its weighted scores: one that has faded says nothing about the others
                     float most = 0.f;
 #pragma unroll 1
                     for (uint32_t j = 0; j < 4; ++j) {
@@ -435,9 +438,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
                         tc_ld32(at + j * 32, r);
                         tc_wait_ld();
                         tc_landed(r);
-                        const uint32_t columns = j == quarter ? own_columns : 0xffffffffu;
+                        // own_decays are 0 behind the row; fmaxf passes over NaN: a masked key that is not finite, times 0
+                        const float* t = j == quarter ? own_decays : far_decays;
+                        float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) most = (columns >> y) & 1u ? fmaxf(most, fabsf(__uint_as_float(r[y]))) : most;
+                        for (int y = 0; y < 32; ++y) m[y % 4] = fmaxf(m[y % 4], fabsf(__uint_as_float(r[y]) * t[y]));
+                        most = fmaxf(most, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * (j == quarter ? 1.f : far_factor(j)));
                     }
                     const float to_half = up_scale(most * fabsf(both_scales));
                     row_exponents[x % kFactors * kChunk + a] = uint8_t(__float_as_uint(to_half) >> 23);
