@@ -594,8 +594,8 @@ TF_API tf_status tf_ulysses_kv_plan(const tf_kv_plan *p, void *stream);
  *     x0' = m (x0 cos - x1 sin)      x1' = m (x0 sin + x1 cos)        m = magnitude
  * and elements R..D-1 are copied.  inverse != 0 takes the negative angle: applied to the
  * gradient of x' it gives the gradient of x.
- * Angles are held as 64-bit fractions of a turn, so a position of any size gives its
- * sine and cosine within 3e-7; the rest is fp32 with one rounding to the I/O type.
+ * Angles are held as 64-bit fractions of a turn, exact for the frequencies as they are given, so a position
+ * of any size gives its sine and cosine within 3e-7; the rest is fp32 with one rounding to the I/O type.
  */
 typedef struct tf_rotary {
     int P, B, T;                 /* head groups (1..8), batch rows, tokens of each */
@@ -606,7 +606,7 @@ typedef struct tf_rotary {
     tf_rope rope;                /* TF_ROPE_INTERLEAVED or TF_ROPE_HALF_SPLIT */
     int inverse;                 /* 0 or 1 */
     float magnitude;             /* finite; 1 as a rule */
-    const double *frequencies;   /* host, [R/2], finite, read before the call returns: radians a position */
+    const double *frequencies;   /* host, [R/2], at most 2^60 in magnitude, read before the call returns: radians a position */
     const int32_t *positions;    /* device, [B][T] contiguous, or NULL: token t stands at first + t */
     int first;
 } tf_rotary;

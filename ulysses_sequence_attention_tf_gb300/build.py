@@ -27,7 +27,7 @@ SOURCES = ["block_kernels.cu", "block_kernels_v16.cu", "gemm_kernels.cu", "relay
            "tf_kv_cache.cpp", "kv_plan.cu", "rotary.cu", "tf_rotary.cpp", "linear_steps.cu", "linear_chunks.cu", "tf_linear.cpp"]
 DEPS = SOURCES + ["relayout.h", "noalloc.h", "device_common.cuh", "block_kernel.cuh", "tma_plan.h", "gemm.h", "host.h",
                   "attention.h", "attention_common.cuh", "attention_order.h", "attention_plan.h",
-                  "tcgen05.cuh", "kv_cache.h", "kv_common.cuh", "rotary.h", "linear.h", "kv_plan.h"]
+                  "tcgen05.cuh", "kv_cache.h", "kv_common.cuh", "rotary.h", "rotary_turns.h", "linear.h", "kv_plan.h"]
 
 
 # The Python module that marshals the attention and cache calls: C++ against the installed torch.

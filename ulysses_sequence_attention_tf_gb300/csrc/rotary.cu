@@ -3,8 +3,8 @@
 //   x0' = m (x0 cos a - x1 sin a)     x1' = m (x0 sin a + x1 cos a)     a = position * frequency
 //
 // The angle is kept in turns as a 64-bit fraction: position times the frequency's fraction, modulo
-// 2^64, is the angle modulo one turn with nothing lost, whatever the position (the fraction itself is off by at most
-// 2^-53 of the frequency, as in fp64).  Its upper 32 bits give the sine and cosine.  So no table is read and no 64-bit
+// 2^64, is the angle modulo one turn, whatever the position; the fraction itself is the nearest of 64 bits (rotary_turns.h), so
+// position 2^31 is 2^-34 of a turn off.  Its upper 32 bits give the sine and cosine.  So no table is read and no 64-bit
 // float is computed, and the positions may come from the device.
 //
 // A thread takes one item of a row -- one vector of 8 elements (4 pairs) with interleaved pairs, two

@@ -4,6 +4,7 @@
 
 #include "host.h"
 #include "rotary.h"
+#include "rotary_turns.h"
 
 using namespace tfu::host;
 
@@ -45,16 +46,6 @@ tf_status tensor(const char* name, const void* const* in, void* const* out, cons
     x->Hl = uint32_t(hl);
     x->in_place = in_place != 0;
     return TF_OK;
-}
-
-// frequency / 2 pi modulo 1 as a 64-bit fraction
-uint64_t fraction(double frequency) {
-    const double turns = frequency / kTurn;
-    const double part = turns - std::floor(turns);  // [0, 1]
-    // 53 bits at most: exact in two steps of 32 bits
-    const double high = std::floor(part * 0x1p32);
-    const double low = (part * 0x1p32 - high) * 0x1p32;
-    return (uint64_t(high) << 32) + uint64_t(low);
 }
 
 }  // namespace
@@ -115,7 +106,9 @@ TF_API tf_status tf_ulysses_rope(const tf_rotary* r, const void* const* q, const
     tfu::RotaryParams p{};
     for (int i = 0; i < r->rotary_dim / 2; ++i) {
         if (!std::isfinite(r->frequencies[i])) return fail(TF_ERR_INVALID, "frequencies[%d] is not finite", i);
-        p.turn[i] = fraction(r->frequencies[i]);
+        if (std::fabs(r->frequencies[i]) > tfu::kMostFrequency)
+            return fail(TF_ERR_UNSUPPORTED, "frequencies[%d] exceeds 2^60 radians a position", i);
+        p.turn[i] = tfu::turn_fraction(r->frequencies[i]);
     }
     if (reinterpret_cast<uintptr_t>(r->positions) % 4) return fail(TF_ERR_ALIGNMENT, "positions must be 4-byte aligned");
     tf_status s = tensor("q", q, q_out, &strides[0], out_strides ? &out_strides[0] : nullptr, *r, r->H, &p.x[0]);
