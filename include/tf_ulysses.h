@@ -616,7 +616,8 @@ typedef struct tf_rotary {
  *  strides      host array of 2 tf_strides: q, k.
  *  q_out, k_out host arrays of P device pointers through out_strides (2 tf_strides, NULL =
  *               contiguous).  q_out may be q itself, with its strides, and k_out k (elements R..D-1
- *               then keep their bits); they overlap nothing else.  k_out is NULL without k.
+ *               then keep their bits); they overlap nothing else (refused where two start together).  k_out is
+ *               NULL without k.
  * One launch, nothing is allocated; the call may be captured (positions are read on the device).
  */
 TF_API tf_status tf_ulysses_rope(const tf_rotary *r, const void *const *q, const void *const *k, const tf_strides *strides,
@@ -679,7 +680,7 @@ typedef struct tf_linear {
  *  state        device fp32 [B][H][D][D] contiguous, 32-byte aligned, the state in front of the first
  *               token (rows belong to k, columns to v), or NULL: zeros.
  *  out          host array of P device pointers, [B, S, H/P, D] through out_strides
- *               (NULL = contiguous); must not overlap the inputs.
+ *               (NULL = contiguous); must not overlap the inputs or itself (refused where two start together).
  *  final_state  as state, the one behind the last token, or NULL.  May be `state` itself; else they
  *               must not overlap.
  *  workspace    device memory of at least tf_ulysses_linear_attention_workspace(a, 0)
@@ -700,7 +701,7 @@ TF_API tf_status tf_ulysses_linear_attention(const tf_linear *a, const void *con
  *  dfinal_state the gradient of the final state, or NULL: zeros.
  *  dq, dk, dv   host arrays of P device pointers, [B, S, H/P, D] through grad_strides (3
  *               tf_strides: dq, dk, dv; NULL = contiguous); every element is written.  They
- *               overlap neither one another nor anything that is read.
+ *               overlap neither one another nor anything that is read (refused where two start together).
  *  dstate       the gradient of `state`, or NULL.  Must not overlap state or dfinal_state.
  *  workspace    as above, tf_ulysses_linear_attention_workspace(a, 1) bytes.
  * States are computed again; nothing of the forward pass but its inputs is needed.  There is
@@ -739,7 +740,8 @@ typedef struct tf_linear_pool {
  *  a            as above with B = 1 and S = T, the rows of the row tensors.
  *  q, k, v      host arrays of P device pointers to row views [T, H/P, D]; strides: host array
  *               of 3 tf_strides (t and h used).
- *  out          the same through out_strides (NULL = contiguous); must not overlap the inputs.
+ *  out          the same through out_strides (NULL = contiguous); must not overlap the inputs or itself (refused
+ *               where two start together).
  *  workspace    tf_ulysses_linear_attend_workspace bytes, 32-byte aligned, one for each call
  *               that may run at the same time.
  */

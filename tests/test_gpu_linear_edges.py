@@ -109,3 +109,22 @@ def test_large_tokens_that_have_faded(tf, reverse, D):
         got, _ = tf.linear_attention(q, k, v, decay=decay, scale=scale)
         want = recurrence(wide(q), wide(k), wide(v), decay, scale)
     check_rows("rows", got, *want[:2], FP16, norm=False)
+
+
+def test_outputs_over_inputs_are_refused(tf):
+    """The passes run together and read ahead; slices of one payload lie apart and are fine."""
+    q, k, v, dout = (rows(1, 300, 2, 64, BF16, i) for i in range(4))
+    decay = torch.tensor([0.1, 0.2], device="cuda")
+    for out in (q, k, v):
+        with pytest.raises(tf.TfUlyssesError):
+            tf.linear_attention(q, k, v, out, decay=decay)
+    for grads in (dict(dq=dout), dict(dq=q), dict(dk=k), dict(dv=v), dict(dk=dout, dv=dout)):
+        with pytest.raises(tf.TfUlyssesError):
+            tf.linear_attention_backward(dout, q, k, v, decay=decay, **grads)
+    with pytest.raises(tf.TfUlyssesError):
+        tf.rope(q, k, k, None)
+    payload = torch.empty((1, 300, 2, 3 * 64), dtype=BF16, device="cuda")
+    into = [[payload[..., i * 64:(i + 1) * 64]] for i in range(3)]
+    got = tf.linear_attention_backward(dout, q, k, v, *into, decay=decay)
+    for x, y in zip(got, tf.linear_attention_backward(dout, q, k, v, decay=decay)[:3]):
+        assert torch.equal(x[0], y[0])

@@ -39,6 +39,15 @@ tf_status check_ptrs(const char* what, const void* const* a, int P);
 // strides of a [nb, nt, nh, D] view; a stride of an extent-1 dimension is never used
 tf_status check_strides(const char* what, const tf_strides& s, int esize, int64_t nb, int64_t nt, int64_t nh);
 
+// P pointers under a name
+struct Named {
+    const char* name;
+    const void* const* at;
+};
+// Refuses written tensors that start where one that is read, or another written one, does.  in_place: written tensor x may be
+// tensor x of those read, group by group.
+tf_status check_starts(const Named* written, int n_written, const Named* read, int n_read, int P, bool in_place);
+
 // scale and cap of attention scores
 tf_status check_scores(float scale, float softcap);
 

@@ -46,6 +46,8 @@ tf_status view(const char* name, const void* const* base, const tf_strides* give
     return TF_OK;
 }
 
+const void* const* starts(void* const* p) { return const_cast<const void* const*>(p); }
+
 tf_status check_state(const char* name, const float* s) {
     return reinterpret_cast<uintptr_t>(s) % 32 == 0 ? TF_OK : fail(TF_ERR_ALIGNMENT, "%s is not 32-byte aligned", name);
 }
@@ -202,6 +204,8 @@ TF_API tf_status tf_ulysses_linear_attention(const tf_linear* a, const void* con
         return s;
     if ((s = check_state("state", state)) != TF_OK || (s = check_state("final_state", final_state)) != TF_OK) return s;
     if ((s = check_apart("final_state", final_state, "state", state, *a, true)) != TF_OK) return s;
+    const Named in[3] = {{"q", q}, {"k", k}, {"v", v}}, written{"out", starts(out)};
+    if (a->B > 0 && a->S > 0 && (s = check_starts(&written, 1, in, 3, a->P, false)) != TF_OK) return s;
     if ((s = check_workspace(workspace_of(p, 1), workspace, workspace_bytes)) != TF_OK) return s;
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;
@@ -237,6 +241,8 @@ TF_API tf_status tf_ulysses_linear_attention_backward(const tf_linear* a, const 
     if ((s = check_apart("dstate", dstate, "dfinal_state", dfinal_state, *a, false)) != TF_OK ||
         (s = check_apart("dstate", dstate, "state", state, *a, false)) != TF_OK)
         return s;
+    const Named in[4] = {{"dout", dout}, {"q", q}, {"k", k}, {"v", v}}, written[3] = {{"dq", starts(dq)}, {"dk", starts(dk)}, {"dv", starts(dv)}};
+    if (a->B > 0 && a->S > 0 && (s = check_starts(written, 3, in, 4, a->P, false)) != TF_OK) return s;
     const tfu::LinearPass all = pass_of(*a);
     if ((s = check_workspace(workspace_of(all, 3), workspace, workspace_bytes)) != TF_OK) return s;
     int device = 0;
@@ -281,6 +287,8 @@ TF_API tf_status tf_ulysses_linear_attend(const tf_linear* a, const tf_linear_po
     if ((s = view("q", q, &strides[0], *a, false, &p.q)) != TF_OK || (s = view("k", k, &strides[1], *a, false, &p.k)) != TF_OK ||
         (s = view("v", v, &strides[2], *a, false, &p.v)) != TF_OK || (s = view("out", out, out_strides, *a, true, &p.out)) != TF_OK)
         return s;
+    const Named in[3] = {{"q", q}, {"k", k}, {"v", v}}, written{"out", starts(out)};
+    if (a->S > 0 && (s = check_starts(&written, 1, in, 3, a->P, false)) != TF_OK) return s;
     if ((s = check_workspace(workspace_of(p, 1), workspace, workspace_bytes)) != TF_OK) return s;
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;

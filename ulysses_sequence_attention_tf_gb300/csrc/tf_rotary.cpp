@@ -116,6 +116,8 @@ TF_API tf_status tf_ulysses_rope(const tf_rotary* r, const void* const* q, const
     if (k && (s = tensor("k", k, k_out, &strides[1], out_strides ? &out_strides[1] : nullptr, *r, r->Hk, &p.x[1])) != TF_OK) return s;
     const int64_t heads = int64_t(r->H) + (k ? r->Hk : 0), rows = int64_t(r->B) * r->T;
     if (rows * heads >= (int64_t(1) << 31)) return fail(TF_ERR_UNSUPPORTED, "problem exceeds 2^31 head rows");
+    const Named in[2] = {{"q", q}, {"k", k}}, out[2] = {{"q_out", const_cast<const void* const*>(q_out)}, {"k_out", const_cast<const void* const*>(k_out)}};
+    if (rows > 0 && (s = check_starts(out, k ? 2 : 1, in, k ? 2 : 1, r->P, true)) != TF_OK) return s;
     int device = 0;
     if ((s = current_device(&device)) != TF_OK) return s;
     if (rows == 0) return TF_OK;

@@ -100,6 +100,21 @@ tf_status check_strides(const char* what, const tf_strides& s, int esize, int64_
     return TF_OK;
 }
 
+tf_status check_starts(const Named* written, int n_written, const Named* read, int n_read, int P, bool in_place) {
+    for (int x = 0; x < n_written; ++x)
+        for (int g = 0; g < P; ++g) {
+            const void* at = written[x].at[g];
+            for (int y = 0; y < n_read; ++y)
+                for (int h = 0; h < P; ++h)
+                    if (at == read[y].at[h] && !(in_place && x == y && g == h))
+                        return fail(TF_ERR_INVALID, "%s[%d] overlaps %s[%d]", written[x].name, g, read[y].name, h);
+            for (int y = x; y < n_written; ++y)
+                for (int h = y == x ? g + 1 : 0; h < P; ++h)
+                    if (at == written[y].at[h]) return fail(TF_ERR_INVALID, "%s[%d] overlaps %s[%d]", written[x].name, g, written[y].name, h);
+        }
+    return TF_OK;
+}
+
 void count_launches(int n) { g_launches.fetch_add(uint64_t(n)); }
 
 uint64_t launch_count() { return g_launches.load(); }
