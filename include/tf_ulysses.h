@@ -661,8 +661,9 @@ TF_API tf_status tf_ulysses_rope_frequencies(int rotary_dim, double theta, tf_ro
  * their decay enter a state as a sum of numbers of the I/O type: in bf16 within 2^-24 of the key where a state is
  * handed out, 2^-16 where it stays inside the call; in fp16 within 2^-22 of the key or 2^-27 of the largest weighted
  * key of its channel among the chunk's tokens, whichever is more.
- * Inputs should be finite: a token's infinity or NaN reaches every later output of its head,
- * and in V also earlier ones among the same 128 tokens.  A negative decay is not refused (it
+ * Inputs should be finite: how far a token's infinity or NaN reaches among the later outputs of its head is not defined
+ * (tokens that weigh nothing may be left out), and in V it also reaches earlier ones among the same 128 tokens; other
+ * heads, batch rows and sequences never see it.  A negative decay is not refused (it
  * lies on the device) but grows without bound.
  */
 typedef struct tf_linear {
