@@ -128,3 +128,31 @@ def test_outputs_over_inputs_are_refused(tf):
     got = tf.linear_attention_backward(dout, q, k, v, *into, decay=decay)
     for x, y in zip(got, tf.linear_attention_backward(dout, q, k, v, decay=decay)[:3]):
         assert torch.equal(x[0], y[0])
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_large_numbers_far_in_front_of_a_segment(tf, reverse):
+    """40 heads of 256 chunks are cut into segments of 37.  The first (reverse: the last) token's key and value of 2^60
+    still count behind its segment, at e^-142 and less, where every other number in front is 0."""
+    S, H, D, far, scale = 32768, 40, 64, 2.0 ** 40, 2.0 ** 10
+    decay = torch.full((H,), 0.03, device="cuda")
+    t = torch.arange(S, device="cuda", dtype=torch.float64)
+    q, k, v = (torch.zeros((1, S, H, D), dtype=BF16, device="cuda") for _ in range(3))
+    first = S - 1 if reverse else 0
+    size = rows(1, 1, H, D, BF16, 1)[0][0, 0].float().sign()
+    k[0, first, :, 3], v[0, first] = 2.0 ** 60, (size * 2.0 ** 60).to(BF16)
+    gone = (t - first).abs()
+    q[0, :, :, 3] = torch.where(gone >= 4000, far, 0.0).to(BF16)[:, None]
+    if reverse:  # dV_j = scale sum_(i >= j) e^(-decay (i - j)) (k_j . q_i) dout_i
+        got = tf.linear_attention_backward([v], [k], [q], [v], decay=decay, scale=scale)[2][0]
+    else:
+        got = tf.linear_attention([q], [k], [v], decay=decay, scale=scale)[0][0]
+    seen = (gone >= 4000) & (gone <= 6500)
+    want = scale * far * 2.0 ** 120 * torch.exp(-decay.double()[0] * gone[seen])[:, None, None] * size.double()
+    # two roundings to bf16's 8 bits, the result's and the state's or the weight's, half a step of 2^-7 each; the exponents' 2^-24 of
+    # 200 and the keys' 2^-16.  A number below 2^-126, bf16's least normal one, need not count in the state: from 246 log 2 / 0.03 =
+    # 5684 tokens on 2^120 has faded below it, so 2^-126 far scale = 2^-76 may be missing, where 2^-35 are at stake at the first
+    # segment's end
+    room = (2 * 2.0 ** -8 + 2.0 ** -14) * want.abs() + 2.0 ** -126 * far * scale
+    off = (got[0, seen].double() - want).abs()
+    assert bool((off <= room).all()), [(int(i), float(off[i].max()), float(room[i].max())) for i in (off > room).any(-1).any(-1).nonzero()[:3, 0]]

@@ -252,10 +252,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) linear_chunks_kernel(const __gri
     // a decay that leaves nothing of the token before is as good as any larger one, and times log2 e it stays finite: 0 times it is 0
     constexpr float kMostDecay = 256.f;
     const float decay = p.decay[head] > kMostDecay ? kMostDecay : p.decay[head];
-    // a segment's sum: what is more than kGone / decay tokens in front of its end weighs less than fp32's least number (e^-104 < 2^-149)
-    constexpr float kGone = 104.f;
-    const float reach = kGone / (decay * float(kChunk)) + 1.f;  // chunks
-    const uint32_t skipped = !kOutputs && decay > 0.f && reach < float(count) ? count - uint32_t(reach) - 1 : 0;
+    // a segment's sum: what is more than kGone / decay tokens in front of its end counts for less than fp32's least number, whatever
+    // its key and value are (2^128 e^-193 < 2^-149)
+    constexpr float kGone = 193.f;
+    const float reach = kGone / (decay * float(kChunk));  // chunks; the last ones of a segment are whole
+    const uint32_t skipped = !kOutputs && decay > 0.f && reach + 1.f < float(count) ? count - uint32_t(reach) - 1 : 0;
     const uint32_t visits = count - skipped;
     // chunk x of those visited: its first token and how many it has
     auto chunk_at = [&](uint32_t x) { return (reverse ? chunks - 1 - first - skipped - x : first + skipped + x) * kChunk; };
