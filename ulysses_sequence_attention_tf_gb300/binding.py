@@ -485,7 +485,9 @@ def gather_out(tag, attn, out=None, *, stream=None):
 
 
 # ---------------------------------------------------------------- attention and key-value cache
-# These calls are short on the GPU: their checks and marshalling are in csrc/torch_calls.cpp.
+# These calls are short on the GPU: their checks and marshalling are in csrc/torch_calls.cpp.  Results of a call of the rotation,
+# linear attention and the plan that are made there share one allocation up to 1 MiB altogether: one that is kept keeps the others'
+# memory, and torch.save writes all of it.  clone() what is kept for long, or give the result.
 _calls = None
 
 
@@ -605,7 +607,7 @@ def kv_plan(page_table, lens, new, free, span, *, page_size, rows, lens_out=None
     lengths, the first row of each request among ``rows`` (the ``lens`` and ``starts`` of ``kv_append``), each row's position
     (that of ``rope``) and its slot ``page * page_size + position % page_size``, 0 and -1 behind the last, and the ring's new
     span.  They are made here unless given.  Requests are served in order: where pages or rows run out, the first one
-    that does not fit and all behind it get nothing, which their ``starts`` tell.
+    that does not fit and all behind it get nothing, which their ``starts`` tell.  The results made here share one allocation.
     """
     return KvPlan(*_run("kv_plan", stream, (page_table, lens, new, free, span),
                         (page_size, rows, lens_out, starts, positions, slots, span_out)))
@@ -637,7 +639,7 @@ def rope(q, k=None, q_out=None, k_out=None, *, positions=None, first=0, frequenc
     ``rotary_dim``, which is D unless given) and are multiplied by ``magnitude``; the other elements are copied.
     ``inverse=True`` turns the other way: the gradient of the inputs from that of the outputs.  Returns
     ``(q_out, k_out)``, lists of P tensors made here unless given (``q`` and ``k`` themselves are fine); k_out is None
-    without k.
+    without k.  The call is not recorded by autograd, also where a tensor requires a gradient.
     """
     if rope not in ("interleaved", "neox"):
         raise ValueError(f"rope must be 'interleaved' or 'neox', not {rope!r}")
@@ -651,8 +653,9 @@ def linear_attention(q, k, v, out=None, *, decay, scale=None, state=None, final_
 
     ``decay``: fp32 ``[H]``, >= 0.  ``state``: fp32 ``[B, H, D, D]``, what the sequence starts from (default: zeros);
     ``final_state=True`` (or a tensor, ``state`` itself too) asks for the one behind the last token.  Returns
-    ``(out, final_state)``, the latter None unless asked for.  Not recorded by autograd: ``linear_attention_backward``
-    gives the gradients.
+    ``(out, final_state)``, the latter None unless asked for; made here, small ones (up to 1 MiB altogether) share an
+    allocation, so ``clone()`` a state that is kept for long or saved, or give its tensor.  Not recorded by autograd:
+    ``linear_attention_backward`` gives the gradients.
     """
     return _run("linear_attention", stream, (q, k, v, decay, scale, state), (out, final_state))
 
@@ -661,8 +664,8 @@ def linear_attention_backward(dout, q, k, v, dq=None, dk=None, dv=None, *, decay
                               dstate_out=None, stream=None):
     """Gradients ``(dq, dk, dv, dstate_out)`` of ``linear_attention`` for the gradients ``dout`` of its output and ``dstate`` of
     its final state (fp32 ``[B, H, D, D]`` or None), from the same inputs: lists of P tensors shaped like q, k and v, and
-    the gradient of ``state`` (None without state, unless a tensor or True is given).  Not recorded by autograd.
-    There is no gradient of the decay."""
+    the gradient of ``state`` (None without state, unless a tensor or True is given).  Small ones made here (up to 1 MiB
+    altogether) share an allocation.  Not recorded by autograd.  There is no gradient of the decay."""
     return _run("linear_attention_backward", stream, (q, k, v, decay, scale, state), (dout, dstate, dq, dk, dv, dstate_out))
 
 
