@@ -94,3 +94,14 @@ def test_frequencies_beyond_that_are_refused(f):
     st = (binding.Strides * 2)(*[binding.Strides(512, 128, 64)] * 2)
     assert binding.lib().tf_ulysses_rope(ctypes.byref(r), fake, None, st, fake, None, None, None) == 4
     assert b"2^60" in binding.lib().tf_ulysses_last_error()
+
+
+def test_frequencies_out_of_range():
+    """A rotary_dim that 32 bits do not hold, and a factor whose base they do not."""
+    from ulysses_sequence_attention_tf_gb300 import binding, build
+    build.build()
+    with pytest.raises(ValueError):
+        binding.rope_frequencies(2 ** 32 + 64)
+    for factor in (1e300, 1e-300):
+        with pytest.raises(binding.TfUlyssesError):
+            binding.rope_frequencies(4, 1e10 if factor > 1 else 1e-10, scaling="base", factor=factor)

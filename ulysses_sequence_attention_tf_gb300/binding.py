@@ -623,6 +623,8 @@ def rope_frequencies(rotary_dim, theta=10000.0, *, scaling=None, factor=1.0, ori
     which goes with a magnitude of ``0.1 * log(factor) + 1`` as a rule)."""
     if scaling not in _ROPE_SCALE:
         raise ValueError(f"scaling must be 'linear', 'base', 'parts' or None, not {scaling!r}")
+    if not -2 ** 31 <= rotary_dim < 2 ** 31:
+        raise ValueError(f"rotary_dim={rotary_dim} is out of range")
     out = (ctypes.c_double * 128)()
     _check(lib().tf_ulysses_rope_frequencies(int(rotary_dim), float(theta), _ROPE_SCALE[scaling], float(factor), float(original),
                                              float(low), float(high), out))

@@ -65,6 +65,7 @@ TF_API tf_status tf_ulysses_rope_frequencies(int rotary_dim, double theta, tf_ro
     if (scale == TF_ROPE_SCALE_BASE) {
         if (rotary_dim == 2) return fail(TF_ERR_INVALID, "a scaled base needs rotary_dim > 2");
         theta *= std::pow(factor, double(rotary_dim) / (rotary_dim - 2));
+        if (!std::isfinite(theta) || theta <= 0) return fail(TF_ERR_INVALID, "the scaled base is not finite and > 0");
     }
     if (scale == TF_ROPE_SCALE_PARTS &&
         (!std::isfinite(original) || original <= 0 || !std::isfinite(low) || !std::isfinite(high) || !(low < high)))
