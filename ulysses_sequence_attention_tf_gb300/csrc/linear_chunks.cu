@@ -28,19 +28,21 @@
 // last adds to the state (K and V only), a second one runs these sums up to the states in front of the
 // segments, and the segments then go on their own.
 //
-// Bound: DRAM, q, k, v and out once -- 4 KB a chunk row pair of D = 128 in bf16, 2.9 us of an SM's share a chunk.  152 heads of
-// 8192 tokens, D = 128: bf16 232 us (5.5 TB/s, 0.81 of the copy bandwidth), fp16 290; D = 64: 129 and 187 us.  A chunk
-// takes 3.3 us at D = 128, 6650 cycles: 4500 from the scores to P, set by the rows that see four blocks of 32 columns (1100 each), 700
-// to the product with P, 1500 to the next scores; the keys 3400, the output 2700 and dS 1300 go beside that.  The matrix pipe is busy 32 % of the cycles, issue slots 35 %; what stalls a group is its own latency (TMEM and shared memory,
-// whose bandwidth the products with both operands there take half of) and instruction fetches of six different codes.  40
-// heads of 32760 tokens: 372 us, 94 of them the segments' sums, 8 their join.
+// Bound: DRAM, q, k, v and out once -- 1 KB a token of D = 128, 2.9 us of an SM's share a chunk.  152 heads of 8192 tokens,
+// D = 128: bf16 231 us (5.5 TB/s, 0.81 of the copy bandwidth), handing its state on (three parts of the keys, a ring of four
+// stages) 263, fp16 299; D = 64: 129, 140 and 205 us.  A chunk takes 3.3 us at D = 128 in bf16, 6650 cycles: 4500 from the
+// scores to P, set by the rows that see four blocks of 32 columns (1100 each), 700 to the product with P, 1500 to the next
+// scores; the keys 3400, the output 2700 and dS 1300 go beside that.  The matrix pipe is busy 31 % of the cycles, issue
+// slots 35 %; what stalls a group is its own latency (TMEM and shared memory, whose bandwidth the products with both operands
+// there take half of) and instruction fetches of six different codes.  fp16 reads its scores twice, for each row's power of two.
+// 40 heads of 32760 tokens: 384 us, 105 of them the segments' sums, 8 their join; 425 with decays so slow that the sums leave
+// nothing out.
 // Measured on the way to this split (152 heads of 8192 tokens, bf16, D = 128): keys weighted by the state's warps 598 us at
 // the video shape, by four warps of their own 559, by eight 477; the parts rounded one from another instead of cut 281 us
 // here, cut 236; P and output shared by both groups, half of the columns each, 254; a block of P of the rows
 // with the most taken by the output's warps 250; D = 64 with scores of one chunk in TMEM 152, of two
 // 140, with two chunks' rest tiles 130.
-// Registers: the groups' shares are what they hold; 8 to 60 bytes a thread are spilled (0.1 % of the instructions at D = 128,
-// 0.8 % at D = 64).
+// Registers: the groups' shares are what they hold; up to 48 bytes a thread are spilled (0.1 to 0.3 % of the instructions).
 #include "attention_common.cuh"
 #include "linear.h"
 

@@ -11,7 +11,7 @@
 // vectors half of R apart (their pairs) with half-split ones -- and a set of heads, for which the sines and cosines
 // are the same.  Bound: DRAM, each row read and written once.  80 heads of 32760 tokens, D = 128, bf16: 197 us, 6.8 TB/s,
 // the copy bandwidth (217 with sincospif and a division for every head); 24 heads of 12002 tokens, half of D = 64: 14 us,
-// 5.2 TB/s.  With few heads a row's sines and cosines show: 4 heads of 60000 tokens 34 us, 3.7 TB/s.
+// 5.2 TB/s.  With few heads a row's sines and cosines show: 4 heads of 60000 tokens 30 us, 4.1 TB/s.
 #include "device_common.cuh"
 #include "rotary.h"
 
