@@ -657,10 +657,10 @@ TF_API tf_status tf_ulysses_rope_frequencies(int rotary_dim, double theta, tf_ro
  *         = scale * ( sum_(j <= t) e^(-decay (t - j)) (q_t . k_j) v_j + e^(-decay (t + 1)) q_t state )
  * States, sums and decays are fp32.  Chunks of tokens go through the tensor cores: the
  * weights e^(-decay (t - j)) (q_t . k_j) and the states are rounded to the I/O type for the products
- * with V and q (in fp16 times powers of two: entries of a state below 2^-27 of its largest lose bits); keys times
- * their decay enter a state as a sum of numbers of the I/O type: in bf16 within 2^-24 of the key where a state is
- * handed out, 2^-16 where it stays inside the call; in fp16 within 2^-22 of the key or 2^-27 of the largest weighted
- * key of its channel among the chunk's tokens, whichever is more.
+ * with V and q (in fp16 times powers of two: an entry of a state below 2^-27 of its head's largest is off by 2^-38 of
+ * that); keys times their decay enter a state as a sum of numbers of the I/O type: in bf16 within 2^-24 of the key where
+ * a state is handed out, 2^-16 where it stays inside the call; in fp16 within 2^-22 of the key or 2^-27 of the largest
+ * weighted key of its channel among the chunk's tokens, whichever is more.
  * Inputs should be finite: how far a token's infinity or NaN reaches among the later outputs of its head is not defined
  * (tokens that weigh nothing may be left out), and in V it also reaches earlier ones among the same 128 tokens; other
  * heads, batch rows and sequences never see it.  A negative decay is not refused (it

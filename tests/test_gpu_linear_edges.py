@@ -156,3 +156,54 @@ def test_large_numbers_far_in_front_of_a_segment(tf, reverse):
     room = (2 * 2.0 ** -8 + 2.0 ** -14) * want.abs() + 2.0 ** -126 * far * scale
     off = (got[0, seen].double() - want).abs()
     assert bool((off <= room).all()), [(int(i), float(off[i].max()), float(room[i].max())) for i in (off > room).any(-1).any(-1).nonzero()[:3, 0]]
+
+
+@pytest.mark.parametrize("S", [17, 300])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_channels_that_large_queries_bring_up(tf, S, D):
+    """fp16: channels of k 2^24 times as small as others, which queries as much larger bring up again, and channels of v 2^22 times
+    as small.  The state's tile for q keeps 11 bits of what is above 2^-27 of its largest entry; entries of both are 2^-46 of it,
+    and below 2^-27 an entry is off by 2^-38 of the largest (2^-25 of a number in [2^13, 2^14)).  So beside the usual bound an
+    output may be off by scale sum_c |q_c| 2^-38 max |S|, S in front of its chunk."""
+    decay = torch.tensor([0.01, 0.0], device="cuda")
+    q, k, v = (rows(1, S, 2, D, FP16, i) for i in range(3))
+    size, of_v = channels(D, 2.0 ** 12, 2.0 ** -12), channels(D, 2.0 ** 10, 2.0 ** 10, 2.0 ** -12, 1.0)
+    q, k, v = [(q[0].float() / size).to(FP16)], [(k[0].float() * size).to(FP16)], [(v[0].float() * of_v).to(FP16)]
+    out, last = tf.linear_attention(q, k, v, decay=decay, final_state=True, scale=0.05)
+    Q, K, V = wide(q), wide(k), wide(v)
+    want = recurrence(Q, K, V, decay, 0.05)
+    beside = torch.zeros_like(want[1])
+    for at in range(128, S, 128):
+        front = recurrence(Q[:, :, :at], K[:, :, :at], V[:, :, :at], decay, 0.05)[2]
+        beside[:, :, at:] = 0.05 * 2.0 ** -38 * front.abs().amax((-1, -2))[..., None, None] * Q[:, :, at:].abs().sum(-1, keepdim=True)
+    check_rows("out", out, want[0], want[1] + beside / (2.0 ** -11 + 2.0 ** -15), FP16)
+    check_state("state", last, *want[2:])
+
+
+@pytest.mark.parametrize("S", [8200, 20000])
+def test_one_head_in_many_segments(tf, S):
+    """65 and 157 chunks of one head: as many segments as are looked at, of one, two or three chunks."""
+    decay = torch.tensor([2e-4], device="cuda")
+    q, k, v, dout = (rows(1, S, 1, 64, BF16, i) for i in range(4))
+    state, dstate = (torch.randn((1, 1, 64, 64), generator=torch.Generator(device="cuda").manual_seed(i), device="cuda") for i in (5, 6))
+    check_all(tf, q, k, v, dout, decay, state, dstate, BF16)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, FP16), (128, BF16)])
+def test_calls_at_once(tf, D, dtype):
+    """Calls on streams of their own, beside one another and beside attention, give the bits of the calls alone."""
+    q, k, v, dout = (rows(1, 2000, 8, D, dtype, i) for i in range(4))
+    decay = torch.exp2(-torch.arange(1.0, 9.0, device="cuda"))
+    calls = [lambda: tf.linear_attention(q, k, v, decay=decay)[0], lambda: tf.linear_attention_backward(dout, q, k, v, decay=decay)[1],
+             lambda: tf.attention(q, k, v, causal=True)[0], lambda: tf.linear_attention(k, v, q, decay=decay)[0]]
+    want = [f()[0].clone() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(10):
+        for f, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(f()[0])
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % len(calls)])
